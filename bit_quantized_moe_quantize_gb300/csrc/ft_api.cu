@@ -33,6 +33,8 @@ int fail(int status, const char* fmt, ...) {
     return status;
 }
 
+void clear_error() { g_last_error.clear(); }
+
 // ---------------------------------------------------------------- profiling
 struct Prof {
     std::mutex mu;
@@ -790,14 +792,22 @@ int ft_moe_read_device_error(void* stream, uint32_t* flags_out) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+    uint32_t fp8_flags = 0;   // the FP8 operators' own word
+    uint32_t* fp8_word = nullptr;
+    if (int st = fp8_error_word(&fp8_word)) return st;
+    e = cudaMemcpy(&fp8_flags, fp8_word, sizeof(fp8_flags), cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && fp8_flags) e = cudaMemset(fp8_word, 0, sizeof(fp8_flags));
+    if (e != cudaSuccess) return cuda_fail(e, "reading the FP8 operators' error word");
     std::lock_guard<std::mutex> lk(g_ws_mu);
     DeviceWs& w = g_ws[dev];
-    if (!w.base) return FT_OK;
+    *flags_out = fp8_flags;
+    if (!w.base) return fp8_flags ? fail(FT_ERR_DEVICE_FLAG, "device error flags 0x%x", fp8_flags) : FT_OK;
     uint32_t v = 0;
     e = cudaMemcpy(&v, w.base, sizeof(v), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(error word)");
     e = cudaMemset(w.base, 0, sizeof(v));
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(error word)");
+    v |= fp8_flags;
     uint8_t guard[kGuardBytes];
     uint8_t* gdev = static_cast<uint8_t*>(w.base) + w.bytes;
     e = cudaMemcpy(guard, gdev, kGuardBytes, cudaMemcpyDeviceToHost);

@@ -12,6 +12,13 @@ int fail(int status, const char* fmt, ...);
 // Multiprocessor count of the current device (cached per device).
 int sm_count();
 
+// Clears the message of ft_last_error() at the start of an entry point.
+void clear_error();
+
+// Device word that the FP8 operators raise FT_DEVERR_* flags in (one per
+// device, fixed for the life of the process; ft_moe_read_device_error reads it).
+int fp8_error_word(uint32_t** word);
+
 // Sets the dynamic shared-memory limit of a kernel once per device and size.
 int set_smem_limit(const void* kernel, int bytes);
 
@@ -137,5 +144,37 @@ int launch_gemm(const uint8_t* weights, const uint8_t* act, const int32_t* perm,
                 const int32_t* tiles, float* out, int32_t* dots, uint32_t* err, int64_t n_slots, int32_t top_k,
                 int32_t n_experts, int64_t nrows, int64_t ncols, uint16_t* xh, uint16_t* da, int tile_width,
                 cudaStream_t s, const ActFuse* af = nullptr, const float* sa = nullptr);
+
+
+// ------------------------------------------------- FP8 expert-layer operators
+struct GateParams {
+    int64_t tokens;
+    int32_t n_experts, top_k, score, n_groups, topk_groups, group_top, renormalize;
+    float scale;
+    const float* bias;
+};
+// stride: elements between the rows of logits (dtype FT_DTYPE_*)
+int launch_gate(const GateParams& p, const void* logits, int dtype, int64_t stride, int32_t* ids, float* weights,
+                cudaStream_t s);
+
+// gated: x holds rows of 2 ncols values (gate, up), and act(gate) * up is quantized
+int launch_quantize_fp8(const void* x, int dtype, uint8_t* codes, float* scales, int64_t rows, int64_t ncols,
+                        bool gated, int kind, cudaStream_t s);
+
+int launch_combine(const void* rows, int rows_dtype, const float* weights, const void* add, void* y, int y_dtype,
+                   int64_t tokens, int32_t top_k, int64_t ncols, cudaStream_t s);
+
+struct Fp8Product {
+    const uint8_t* weights;     // [n_experts][nrows][ncols] e4m3
+    const float* w_scales;      // [n_experts][ceil(nrows / 128)][ceil(ncols / 128)]
+    const uint8_t* act;         // [rows][ncols] e4m3
+    const float* act_scales;    // [rows][ceil(ncols / 128)]
+    const int32_t* ids;         // [n_slots] expert of each slot, -1: none; nullptr: dense (one matrix)
+    int64_t n_slots, act_rows, nrows, ncols;
+    int32_t act_div;            // activation row of slot s: s / act_div
+    int32_t n_experts;
+};
+size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts);
+int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* workspace, uint32_t* err, cudaStream_t s);
 
 }  // namespace ft

@@ -1,0 +1,215 @@
+// Router of a mixture-of-experts layer: logits -> the top_k experts of each
+// token and their weights.
+//
+//   s   = softmax(l) or sigmoid(l) over the E experts of a token; an expert
+//         whose logit is -inf or NaN is masked: s = 0, and it is never chosen
+//   key = l where there is no bias and one group (the order of l is the order
+//         of s, without its rounding), else s + bias
+//   groups of E / n_groups neighbouring experts: a group's score is the sum of
+//         its group_top largest keys (of those not masked); only experts of
+//         the topk_groups best groups can be chosen
+//   ids = the top_k largest keys, equal keys by lowest index; -1 with weight 0
+//         where no expert is left
+//   w   = s[ids], renormalised by max(sum, 1e-30) if asked, times `scale`
+//
+// One warp per token.  The keys lie in shared memory; each lane keeps the best
+// key of its experts (every 32nd), and one round per chosen expert takes the
+// warp's best of those with two integer warp reductions (largest key, then the
+// lowest index that has it) and lets the lane that held it look again.
+#include "fp8_common.cuh"
+#include "ft_internal.h"
+
+namespace ft {
+
+constexpr int kGateWarps = 4;
+constexpr float kGateTiny = 1e-30f;   // smallest sum that weights are divided by
+
+struct GateArgs {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int64_t tokens, stride;
+    int32_t n_experts, top_k, score, n_groups, topk_groups, group_top, renormalize;
+    float scale;
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// exp(l - top) with the limits top = +inf (those experts share the weight) and
+// a masked l taken as 0.
+__device__ __forceinline__ float gate_exp(float l, float top) {
+    if (!(l > -INFINITY)) return 0.0f;
+    return l == top ? 1.0f : expf(l - top);
+}
+
+__device__ __forceinline__ float gate_score(float l, float top, float sum, int32_t score) {
+    if (!(l > -INFINITY)) return 0.0f;
+    if (score == FT_SCORE_SIGMOID) return __fdiv_rn(1.0f, 1.0f + expf(-l));
+    return __fdiv_rn(gate_exp(l, top), fmaxf(sum, kGateTiny));
+}
+
+// Removes and returns the largest key of keys[0..n) (order integers, 0: none
+// left) as its index, -1 if none is left.  best/at: the lane's own largest key
+// and its index, kept from call to call.
+struct Best {
+    uint32_t key;
+    int32_t at;
+};
+
+__device__ __forceinline__ Best lane_best(const uint32_t* keys, int32_t n) {
+    Best b{0u, -1};
+    for (int32_t e = static_cast<int32_t>(lane_id()); e < n; e += 32)
+        if (keys[e] > b.key) b = Best{keys[e], e};
+    return b;
+}
+
+__device__ __forceinline__ int32_t take_best(uint32_t* keys, int32_t n, Best& b) {
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, b.key);
+    if (top == 0u) return -1;
+    const uint32_t at = __reduce_min_sync(0xFFFFFFFFu, b.key == top ? static_cast<uint32_t>(b.at) : 0xFFFFFFFFu);
+    if (b.at == static_cast<int32_t>(at)) {
+        keys[at] = 0u;
+        b = lane_best(keys, n);
+    }
+    return static_cast<int32_t>(at);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const GateArgs a) {
+    extern __shared__ uint32_t gate_smem[];
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+    if (t >= a.tokens) return;
+    const int32_t E = a.n_experts;
+    uint32_t* keys = gate_smem + static_cast<size_t>(warp) * (E + a.n_groups);
+    const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+
+    float top = -INFINITY, sum = 0.0f;
+    if (a.score == FT_SCORE_SOFTMAX) {
+        for (int32_t e = lane; e < E; e += 32) top = fmaxf(top, to_f32<T>(row[e]));   // fmaxf leaves NaN out
+        top = warp_max(top);
+        for (int32_t e = lane; e < E; e += 32) sum += gate_exp(to_f32<T>(row[e]), top);
+        sum = warp_sum(sum);
+    }
+    const bool by_logit = a.bias == nullptr && a.n_groups == 1;
+    for (int32_t e = lane; e < E; e += 32) {
+        const float l = to_f32<T>(row[e]);
+        float key = l;
+        if (!by_logit) {
+            key = gate_score(l, top, sum, a.score);
+            if (a.bias) key += a.bias[e];
+        }
+        keys[e] = l > -INFINITY && key > -INFINITY ? float_order(key) : 0u;
+    }
+    __syncwarp();
+
+    if (a.n_groups > 1) {
+        const int32_t per = E / a.n_groups;
+        uint32_t* score = keys + E;
+        for (int32_t g = lane; g < a.n_groups; g += 32) {
+            uint32_t k1 = 0u, k2 = 0u;      // the group's two largest keys
+            for (int32_t i = 0; i < per; ++i) {
+                const uint32_t k = keys[g * per + i];
+                k2 = max(k2, min(k, k1));
+                k1 = max(k1, k);
+            }
+            auto value = [](uint32_t k) {   // inverse of float_order
+                return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+            };
+            float v = k1 ? value(k1) : -INFINITY;
+            if (a.group_top == 2 && k2) v += value(k2);
+            score[g] = k1 ? float_order(v) : 0u;
+        }
+        __syncwarp();
+        // each chosen group's score becomes the mark ~0
+        Best b = lane_best(score, a.n_groups);
+        for (int32_t i = 0; i < a.topk_groups; ++i) {
+            const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, b.key);
+            if (best == 0u) break;
+            const uint32_t at =
+                __reduce_min_sync(0xFFFFFFFFu, b.key == best ? static_cast<uint32_t>(b.at) : 0xFFFFFFFFu);
+            if (b.at == static_cast<int32_t>(at)) {
+                score[at] = 0xFFFFFFFFu;
+                b = Best{0u, -1};
+                for (int32_t g = lane; g < a.n_groups; g += 32)
+                    if (score[g] != 0xFFFFFFFFu && score[g] > b.key) b = Best{score[g], g};
+            }
+        }
+        __syncwarp();
+        for (int32_t e = lane; e < E; e += 32)
+            if (score[e / per] != 0xFFFFFFFFu) keys[e] = 0u;
+        __syncwarp();
+    }
+
+    Best b = lane_best(keys, E);
+    int32_t* ids = a.ids + t * a.top_k;
+    float* weights = a.weights + t * a.top_k;
+    float total = 0.0f, mine = 0.0f;      // mine: weight `lane` of the current 32
+    for (int32_t j0 = 0; j0 < a.top_k; j0 += 32) {
+        const int32_t n = min(32, a.top_k - j0);
+        for (int32_t j = 0; j < n; ++j) {
+            const int32_t at = take_best(keys, E, b);
+            const float w = at < 0 ? 0.0f : gate_score(to_f32<T>(row[at]), top, sum, a.score);
+            total += w;
+            if (lane == static_cast<uint32_t>(j)) {
+                mine = w;
+                ids[j0 + j] = at;
+            }
+        }
+        if (static_cast<int32_t>(lane) < n && (!a.renormalize || a.top_k > 32))
+            weights[j0 + lane] = a.renormalize ? mine : mine * a.scale;
+    }
+    if (!a.renormalize) return;
+    total = fmaxf(total, kGateTiny);
+    if (a.top_k <= 32) {
+        if (lane < static_cast<uint32_t>(a.top_k)) weights[lane] = __fdiv_rn(mine, total) * a.scale;
+    } else {      // each lane rereads what it wrote
+        for (int32_t j = lane; j < a.top_k; j += 32) weights[j] = __fdiv_rn(weights[j], total) * a.scale;
+    }
+}
+
+int launch_gate(const GateParams& p, const void* logits, int dtype, int64_t stride, int32_t* ids, float* weights,
+                cudaStream_t s) {
+    if (p.tokens == 0) return FT_OK;
+    GateArgs a{};
+    a.logits = logits;
+    a.bias = p.bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.tokens = p.tokens;
+    a.stride = stride;
+    a.n_experts = p.n_experts;
+    a.top_k = p.top_k;
+    a.score = p.score;
+    a.n_groups = p.n_groups;
+    a.topk_groups = p.topk_groups;
+    a.group_top = p.group_top;
+    a.renormalize = p.renormalize;
+    a.scale = p.scale;
+    const int64_t ctas = (p.tokens + kGateWarps - 1) / kGateWarps;
+    if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "too many tokens for one launch");
+    const dim3 grid(static_cast<unsigned>(ctas)), block(32 * kGateWarps);
+    const size_t sm = static_cast<size_t>(kGateWarps) * (p.n_experts + p.n_groups) * sizeof(uint32_t);
+    const void* k = dtype == FT_DTYPE_F32   ? reinterpret_cast<const void*>(moe_gate_kernel<float>)
+                    : dtype == FT_DTYPE_F16 ? reinterpret_cast<const void*>(moe_gate_kernel<__half>)
+                                            : reinterpret_cast<const void*>(moe_gate_kernel<__nv_bfloat16>);
+    if (sm > 48 * 1024)
+        if (int st = set_smem_limit(k, static_cast<int>(sm))) return st;
+    if (dtype == FT_DTYPE_F32) moe_gate_kernel<float><<<grid, block, sm, s>>>(a);
+    else if (dtype == FT_DTYPE_F16) moe_gate_kernel<__half><<<grid, block, sm, s>>>(a);
+    else moe_gate_kernel<__nv_bfloat16><<<grid, block, sm, s>>>(a);
+    return check_launch("moe_gate_kernel", grid, block, sm);
+}
+
+}  // namespace ft

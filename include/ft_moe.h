@@ -549,6 +549,162 @@ FT_API int ft_profile_enable(int32_t max_calls);
 FT_API int ft_profile_read(double* quantize_ms, double* route_ms, double* matmul_ms, int64_t* n_calls,
                            int64_t* n_launches);
 
+/* ------------------------------------------------ FP8 expert-layer operators
+ *
+ * The pieces of a mixture-of-experts layer whose expert matrices are stored in
+ * 8-bit floating point: the router (ft_moe_gate), the activation quantizer
+ * (ft_quantize_fp8, ft_act_mul_quantize_fp8), the routed products
+ * (ft_moe_fp8_fp8, ft_moe_fp8_fp8_slots, and ft_matmul_fp8_fp8 for one dense
+ * matrix), the weighted sum of a token's expert rows (ft_moe_combine), and all
+ * of them in one call (ft_moe_layer_fp8).
+ *
+ * Format: e4m3 codes (one byte: sign, 4 exponent bits, 3 mantissa bits, no
+ * infinities, largest finite value 448) with one fp32 scale per 128 consecutive
+ * values of an activation row, and one per block of 128 rows x 128 columns of a
+ * weight matrix; the last block of a row or matrix may be short.  A value is
+ * code * scale.
+ *   weights  [n_experts][nrows][ncols] e4m3, 16-byte aligned
+ *   w_scales [n_experts][ceil(nrows/128)][ceil(ncols/128)] fp32
+ *   act      [rows][ncols] e4m3, 16-byte aligned
+ *   act_scales [rows][ceil(ncols/128)] fp32
+ * ncols must be a multiple of 16 everywhere.
+ *
+ * Conventions.  As for the other entry points, except:
+ *   - They keep no state.  Scratch memory is the caller's: `workspace` (256-byte
+ *     aligned, at least the bytes the matching _workspace_bytes function
+ *     returns, any contents) may be reused once the call's work on the stream
+ *     is done, so calls on different streams do not meet when their
+ *     workspaces differ.
+ *   - An expert id of -1 means "no expert": its output row is 0 and no error
+ *     flag is raised.  Other ids outside [0, n_experts) give a zero row and
+ *     raise FT_DEVERR_BAD_EXPERT_ID.
+ *   - Outputs must not overlap inputs.
+ * Errors of all of them: FT_ERR_ARG, FT_ERR_SIZE, FT_ERR_ALIGN,
+ * FT_ERR_WORKSPACE (workspace null or too small), FT_ERR_CUDA, FT_ERR_LAUNCH. */
+
+/* Element types. */
+#define FT_DTYPE_F32 0
+#define FT_DTYPE_F16 1
+#define FT_DTYPE_BF16 2
+
+/* Router scores. */
+#define FT_SCORE_SOFTMAX 0
+#define FT_SCORE_SIGMOID 1
+
+/*
+ * ft_moe_gate - the router: logits -> the top_k experts of every token and
+ * their weights.  Per token, in fp32:
+ *   s   = softmax(logits) or sigmoid(logits); a logit of -inf or NaN masks its
+ *         expert (s = 0, never chosen); experts at +inf share a softmax
+ *   key = the logit where bias is NULL and n_groups is 1, else s + bias
+ *   with n_groups > 1, experts are in n_groups runs of n_experts / n_groups; a
+ *         run's score is the sum of its group_top (1 or 2) largest keys, and
+ *         only the topk_groups best runs' experts can be chosen
+ *   topk_ids = the top_k largest keys in descending order; equal keys (and
+ *         equal runs) by lowest index; -1 where no expert is left
+ *   topk_weights = s of the chosen (0 for -1), divided by max(their sum, 1e-30)
+ *         if renormalize, times scale
+ *
+ *   logits       device, [tokens] rows of n_experts elements of dtype, row_stride
+ *                (>= n_experts) elements apart, element-aligned
+ *   bias         device fp32 [n_experts] or NULL; steers the choice only
+ *   topk_ids     device int32 [tokens][top_k] out
+ *   topk_weights device fp32 [tokens][top_k] out
+ * Needs n_experts <= FT_MAX_EXPERTS, n_groups dividing n_experts, 1 <=
+ * topk_groups <= n_groups, group_top <= n_experts / n_groups, 1 <= top_k <=
+ * topk_groups * n_experts / n_groups, tokens * top_k < 2^31.
+ */
+FT_API int ft_moe_gate(const void* logits, int32_t dtype, int64_t row_stride, const float* bias,
+                       int32_t* topk_ids, float* topk_weights, int64_t tokens, int32_t n_experts, int32_t top_k,
+                       int32_t score, int32_t n_groups, int32_t topk_groups, int32_t group_top,
+                       int32_t renormalize, float scale, void* stream);
+
+/*
+ * ft_quantize_fp8 - rows -> e4m3 codes and scales.  Per 128 columns of a row,
+ * in IEEE fp32: scale = max |x| / 448, code = x / scale rounded to the nearest
+ * e4m3 value (ties to even); scale 0 gives codes 0.  A non-finite x makes its
+ * block's scale non-finite.
+ *   x      device, [rows][ncols] of dtype (FT_DTYPE_*), 16-byte aligned
+ *   codes  device, [rows][ncols] out, 4-byte aligned; scales device fp32
+ *          [rows][ceil(ncols/128)] out
+ */
+FT_API int ft_quantize_fp8(const void* x, int32_t dtype, void* codes, float* scales, int64_t rows,
+                           int64_t ncols, void* stream);
+
+/*
+ * ft_act_mul_quantize_fp8 - the step between the two expert products: rows of
+ * 2 * n_inter values (gate, then up) -> e4m3 codes and scales of
+ * act(gate) * up (FT_ACT_*), evaluated in fp32.  h: [rows][2 * n_inter] of dtype;
+ * the outputs are those of ft_quantize_fp8 for [rows][n_inter].
+ */
+FT_API int ft_act_mul_quantize_fp8(const void* h, int32_t dtype, void* codes, float* scales, int64_t rows,
+                                   int64_t n_inter, int32_t act_kind, void* stream);
+
+/*
+ * ft_moe_fp8_fp8 - the routed expert product.  For slot s = t * top_k + j with
+ * expert e = topk_ids[s], and every weight row r of e:
+ *   out[s][r] = sum_b act_scales[t][b] * w_scales[e][r / 128][b] *
+ *               sum_{i in block b} weights[e][r][i] * act[t][i]
+ * summed in fp32 and rounded once to out_dtype (FT_DTYPE_F32 or FT_DTYPE_BF16).
+ * ft_moe_fp8_fp8_slots takes one activation row per slot (act [tokens*top_k])
+ * instead of one per token.  ft_matmul_fp8_fp8 is the product with one dense
+ * matrix: act [rows], weights [nrows][ncols], out [rows][nrows].
+ *
+ *   out  device, [tokens][top_k][nrows] of out_dtype, element-aligned; every
+ *        element is written
+ * Needs 0 < ncols <= FT_MAX_NCOLS, n_experts * nrows < 2^31, top_k <= n_experts
+ * <= FT_MAX_EXPERTS, tokens * top_k < 2^31.
+ * ft_moe_fp8_workspace_bytes: bytes for tokens, top_k, n_experts (the dense
+ * product: rows, 1, 1); 0 for invalid arguments.
+ */
+FT_API size_t ft_moe_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_experts);
+FT_API int ft_moe_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales,
+                          const int32_t* topk_ids, void* out, int32_t out_dtype, int64_t tokens, int32_t top_k,
+                          int32_t n_experts, int64_t nrows, int64_t ncols, void* workspace,
+                          size_t workspace_bytes, void* stream);
+FT_API int ft_moe_fp8_fp8_slots(const void* weights, const float* w_scales, const void* act_slots,
+                                const float* act_scales, const int32_t* topk_ids, void* out, int32_t out_dtype,
+                                int64_t tokens, int32_t top_k, int32_t n_experts, int64_t nrows, int64_t ncols,
+                                void* workspace, size_t workspace_bytes, void* stream);
+FT_API int ft_matmul_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales,
+                             void* out, int32_t out_dtype, int64_t rows, int64_t nrows, int64_t ncols,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ft_moe_combine - the weighted sum of a token's expert rows:
+ *   y[t][c] = sum_j topk_weights[t][j] * rows[t][j][c] (+ add[t][c])
+ * in fp32, j ascending, rounded once.  A row whose weight is 0 is not read.
+ *   rows  device, [tokens][top_k][ncols] of rows_dtype (FT_DTYPE_F32 or
+ *         FT_DTYPE_BF16), element-aligned; add (or NULL) and y [tokens][ncols]
+ *         of y_dtype, element-aligned
+ */
+FT_API int ft_moe_combine(const void* rows, int32_t rows_dtype, const float* topk_weights, const void* add,
+                          void* y, int32_t y_dtype, int64_t tokens, int32_t top_k, int64_t ncols, void* stream);
+
+/*
+ * ft_moe_layer_fp8 - a whole expert layer: ft_moe_gate on the logits,
+ * ft_quantize_fp8 of x, the routed product with w13 (gate rows, then up rows),
+ * act(gate) * up quantized, the routed product with w2 and ft_moe_combine.
+ * The gated values are fp32 when they are quantized; the rows of the second
+ * product are rounded to bf16 before they are weighted.
+ *   x       device, [tokens][hidden] of x_dtype (FT_DTYPE_F16 or FT_DTYPE_BF16),
+ *           16-byte aligned; y the same shape and type, out
+ *   w13     [n_experts][2 * n_inter][hidden] e4m3, s13 its scales
+ *   w2      [n_experts][hidden][n_inter] e4m3, s2 its scales
+ *   topk_ids, topk_weights  out, as in ft_moe_gate
+ * hidden and n_inter must be multiples of 16.  The other arguments and limits are those of
+ * the operators above.
+ */
+FT_API size_t ft_moe_layer_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_experts, int64_t hidden,
+                                               int64_t n_inter);
+FT_API int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t logits_dtype,
+                            int64_t row_stride, const float* bias, const void* w13, const float* s13,
+                            const void* w2, const float* s2, void* y, int32_t* topk_ids, float* topk_weights,
+                            int64_t tokens, int32_t n_experts, int32_t top_k, int64_t hidden, int64_t n_inter,
+                            int32_t score, int32_t n_groups, int32_t topk_groups, int32_t group_top,
+                            int32_t renormalize, float scale, int32_t act_kind, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* ft_last_error - message of the last failing call on this host thread
  * (empty string if none).  The pointer stays valid until the next call on the
  * same thread. */
