@@ -100,7 +100,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.ft_moe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i64, i32, i64, vp]
         L.ft_moe_layer_fp8.argtypes = [vp, i32, vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64,
                                        i32, i32, i32, i32, i32, f32, i32, vp, sz, vp]
-        L.ft_moe_fp8_workspace_bytes.argtypes = [i64, i32, i32]
+        L.ft_moe_fp8_workspace_bytes.argtypes = [i64, i32, i32, i64]
         L.ft_moe_fp8_workspace_bytes.restype = sz
         L.ft_moe_layer_fp8_workspace_bytes.argtypes = [i64, i32, i32, i64, i64]
         L.ft_moe_layer_fp8_workspace_bytes.restype = sz
@@ -544,7 +544,7 @@ def _moe_fp8(fn, per_slot, weights, w_scales, act, act_scales, topk_ids, out, ou
     code = _dtype_code(out_dtype, "out_dtype", "torch.float32", "torch.bfloat16")
     out = _out(out, "out", (T, k, N), out_dtype, weights)
     L = load()
-    n = L.ft_moe_fp8_workspace_bytes(T, k, E)
+    n = L.ft_moe_fp8_workspace_bytes(T, k, E, K)
     ws = _workspace(n, weights)
     _check(fn(L)(pw, ps, pa, pt, pi, out.data_ptr(), code, T, k, E, N, K, None if ws is None else ws.data_ptr(), n,
                  _raw_stream(weights)))
@@ -583,10 +583,7 @@ def matmul_fp8_fp8(weights, w_scales, act, act_scales, out=None, out_dtype=None)
     code = _dtype_code(out_dtype, "out_dtype", "torch.float32", "torch.bfloat16")
     out = _out(out, "out", (M, N), out_dtype, weights)
     L = load()
-    n = L.ft_moe_fp8_workspace_bytes(M, 1, 1)
-    ws = _workspace(n, weights)
-    _check(L.ft_matmul_fp8_fp8(pw, ps, pa, pt, out.data_ptr(), code, M, N, K, None if ws is None else ws.data_ptr(), n,
-                               _raw_stream(weights)))
+    _check(L.ft_matmul_fp8_fp8(pw, ps, pa, pt, out.data_ptr(), code, M, N, K, None, 0, _raw_stream(weights)))
     return out
 
 

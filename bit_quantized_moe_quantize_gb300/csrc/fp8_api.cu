@@ -1,6 +1,7 @@
 // C entry points of the FP8 expert-layer operators: argument checks, the
 // layout of the caller's workspace, and the order of the kernels.  See
 // include/ft_moe.h for the contract.
+#include <algorithm>
 #include <mutex>
 
 #include <cuda_runtime.h>
@@ -120,7 +121,7 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
     if (!aligned(weights, 16) || !aligned(act, 16)) return fail(FT_ERR_ALIGN, "weights and act must be 16-byte aligned");
     if (!aligned(w_scales, 4) || !aligned(act_scales, 4) || !aligned(ids, 4) || !aligned(out, dtype_bytes(out_dtype)))
         return fail(FT_ERR_ALIGN, "scales, ids and out must be aligned to their elements");
-    if (int st = check_workspace(workspace, workspace_bytes, fp8_product_workspace(n_slots, n_experts))) return st;
+    if (int st = check_workspace(workspace, workspace_bytes, dense ? 0 : fp8_product_workspace(n_slots, n_experts, ncols))) return st;
     uint32_t* err = nullptr;
     if (int st = fp8_error_word(&err)) return st;
     Fp8Product p{};
@@ -157,7 +158,7 @@ LayerWs layer_ws(int64_t tokens, int64_t n_slots, int32_t n_experts, int64_t hid
     L.mq = take(S * n_inter);
     L.ms = take(S * fp8_blocks(n_inter) * 4);
     L.rows = take(S * hidden * 2);
-    L.product = take(fp8_product_workspace(n_slots, n_experts));
+    L.product = take(std::max(fp8_product_workspace(n_slots, n_experts, hidden), fp8_product_workspace(n_slots, n_experts, n_inter)));
     L.total = o;
     return L;
 }
@@ -211,11 +212,12 @@ int ft_act_mul_quantize_fp8(const void* h, int32_t dtype, void* codes, float* sc
     return quantize_entry(h, dtype, codes, scales, rows, n_inter, true, act_kind, stream);
 }
 
-size_t ft_moe_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_experts) {
+size_t ft_moe_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_experts, int64_t ncols) {
     clear_error();
     int64_t n_slots;
-    if (check_slots(tokens, top_k, n_experts, &n_slots)) return 0;
-    return fp8_product_workspace(n_slots, n_experts);
+    int64_t n;
+    if (check_slots(tokens, top_k, n_experts, &n_slots) || check_cols(ncols, "ncols") || !mul_ok(n_slots, ncols, &n)) return 0;
+    return fp8_product_workspace(n_slots, n_experts, ncols);
 }
 
 int ft_moe_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales,

@@ -21,13 +21,22 @@
 // costs more than the MMAs of the block (512 cycles).
 //
 // Per CTA, warp-specialised:
-//   8 drain warps  warp w: TMEM lanes 32 (w % 4) .. + 31 (one slot per thread),
-//                  columns 128 (w / 4) .. + 127
-//   producer       TMA: the weight boxes, and the slots' rows four at a time by
-//                  index (gather), or in boxes of 16 neighbouring rows where
-//                  slots lie in order, both with 128-byte swizzle; columns past
-//                  the row's end arrive as 0
-//   MMA            (leader CTA) four MMAs of 32 columns per block
+//   8 drain warps  in two warpgroups, one per 128 weight rows (half) of the tile; warp w:
+//                  TMEM lanes 32 (w % 4) .. + 31, one slot per thread
+//   producer       TMA: the weight boxes, and the slots' rows in boxes of 32
+//                  neighbouring rows (router order), or four at a time by index
+//                  (gather), with 128-byte swizzle; columns past the row's end
+//                  arrive as 0
+//   MMA            (leader CTA) per block and half four MMAs of 32 columns, into
+//                  one of the half's two accumulators of 128 columns
+//
+// An accumulator goes from the MMA to the drain warps of both CTAs and back, which
+// takes about 1000 cycles on top of the MMAs (637 a block) and the drain: four
+// accumulators of 128 columns in flight hide more of it than two of 256.
+//
+// A gather fetches four 128-byte rows per instruction and the TMA unit takes about
+// 85 cycles for one, so 128 slots a CTA would need 2700 cycles a block: batches
+// with many slots per expert first copy their rows to router order.
 #include "fp8_tc.cuh"
 #include "ft_internal.h"
 #include "gemm_common.cuh"
@@ -37,21 +46,25 @@ namespace ft {
 struct Pair {
     static constexpr int BM = 128;                 // slots per CTA
     static constexpr int BN = 256;                 // weight rows per tile
-    static constexpr int STAGES = 5;
+    static constexpr int STAGES = 4;
     static constexpr int A_BYTES = BM * kFp8Block;
     static constexpr int B_BYTES = BN / 2 * kFp8Block;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int BOX = 64;                 // weight rows per TMA box
+    static constexpr int BOX = 64;                 // weight rows per TMA box (half a half)
+    static constexpr int ROW_BOX = 32;             // slots' rows per TMA box in router order
     static constexpr int N_DRAIN_WARPS = 8;
-    static constexpr int WARP_PRODUCER = 8, WARP_MMA = 9;
-    static constexpr int THREADS = 12 * 32;        // warps 10 and 11 complete the third warpgroup and zero rows
+    static constexpr int WARP_PRODUCER = 8, WARP_MMA = 9, N_MMA_WARPS = 2, WARP_ZERO = 11;
+    static constexpr int THREADS = 12 * 32;
     // registers: 384 threads are launched with LAUNCH_REGS each; the drain warps
     // take DRAIN_REGS, and the others give theirs down to OTHER_REGS
-    static constexpr int LAUNCH_REGS = 168, DRAIN_REGS = 216, OTHER_REGS = 72;
+    static constexpr int LAUNCH_REGS = 168, DRAIN_REGS = 232, OTHER_REGS = 40;
     static_assert(DRAIN_REGS * 256 + OTHER_REGS * 128 <= LAUNCH_REGS * THREADS, "the split must fit the launch's registers");
-    static constexpr int CW = BN / 2;              // columns per drain warp
-    static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
-    static constexpr int N_BARS = 2 * STAGES + 4;
+    static constexpr int CW = BN / 2;              // columns of a half
+    static constexpr int STAGE_ROW = 256 + 16;     // output staging: 256 bytes of a slot's row, and 16 so that
+                                                   // eight lanes' 16-byte words fall in different banks
+    static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
+    static constexpr int OFF_BAR = OFF_OUT + N_DRAIN_WARPS * 32 * STAGE_ROW;
+    static constexpr int N_BARS = 2 * STAGES + 8;
     static constexpr int OFF_TMEM = OFF_BAR + N_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;    // + alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -67,6 +80,7 @@ struct PairArgs {
     uint32_t* err;
     int64_t n_slots, nrows;
     int32_t act_div, n_experts, nb, row_tiles, row_blocks;
+    bool ordered;                // act rows and scales lie in router order
     bool wide;                   // the rows of out are whole 16-byte words
 };
 
@@ -76,6 +90,8 @@ struct PairTile {
     // slots of CTA `rank`, and their first position
     __device__ int32_t mine(uint32_t rank) const { return rank ? n - half : half; }
     __device__ int64_t first(uint32_t rank) const { return p0 + (rank ? half : 0); }
+    // MMA columns of half h (0, or past 0 where the tile has none)
+    __device__ int32_t cols(int32_t h) const { return min(Pair::CW, width - h * Pair::CW); }
 };
 
 // Work item w: row tile w % row_tiles of slot tile w / row_tiles.
@@ -113,6 +129,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return *reinterpret_cast<float2*>(&r);
 }
 
+// Read-only load that stays where it is written (a block before its use).
+__device__ __forceinline__ float load_now(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 // Rows of slots without an expert are 0; ids that are neither -1 nor an expert raise the flag.
 template <typename TO>
 __device__ __forceinline__ void zero_unrouted(const PairArgs& a, TO* out, int64_t warp, int64_t n_warps) {
@@ -140,8 +163,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* empty = full + C::STAGES;
-    uint64_t* acc_full = empty + C::STAGES;
-    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* acc_full = empty + C::STAGES;      // [half][buffer]
+    uint64_t* acc_empty = acc_full + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
 
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id(), rank = cluster_ctarank();
@@ -150,11 +173,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], C::N_MMA_WARPS);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 2 * C::N_DRAIN_WARPS);     // the leader's: drain warps of both CTAs
+            mbar_init(&acc_empty[i], C::N_DRAIN_WARPS);         // the leader's: a warpgroup of both CTAs
         }
         fence_mbar_init();
     }
@@ -181,8 +204,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         for (int64_t w = w0; w < total && ok; w += dw) {
             const PairTile t = pair_tile(a, w);
             const int32_t mine = t.mine(rank), other = t.mine(rank ^ 1u);
-            // lane l copies 4 (gather) or 16 of this CTA's slots
-            constexpr int PER = GATHER ? 4 : 16;
+            // lane l copies 4 (gather) or 32 of this CTA's slots
+            constexpr int PER = GATHER ? 4 : C::ROW_BOX;
             const bool copies = static_cast<int32_t>(lane) * PER < mine;
             int32_t y[4] = {0, 0, 0, 0};
             if (copies) {
@@ -195,10 +218,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                     y[0] = static_cast<int32_t>(p);
                 }
             }
-            // weight rows of this CTA's half of the tile: one box or two
-            const int32_t boxes = t.width > 2 * C::BOX ? 2 : 1;
-            const int32_t wy = static_cast<int32_t>(static_cast<int64_t>(t.e) * a.nrows + t.r0 + rank * (t.width / 2));
-            const uint32_t bytes = 2 * boxes * C::BOX * kFp8Block +
+            // half h of the tile (weight rows 128 h ..): this CTA's part of its MMA's columns
+            const int32_t halves = t.width > C::CW ? 2 : 1;
+            const int64_t row0 = static_cast<int64_t>(t.e) * a.nrows + t.r0;
+            const int32_t wy = static_cast<int32_t>(row0 + lane * C::CW + rank * (t.cols(static_cast<int32_t>(lane)) / 2));
+            const uint32_t bytes = 2 * halves * C::BOX * kFp8Block +
                                    ((mine + PER - 1) / PER + (other + PER - 1) / PER) * PER * kFp8Block;
             for (int32_t b = 0; b < nb; ++b, ++it) {
                 const uint32_t s = it % C::STAGES;
@@ -206,9 +230,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
                 const uint32_t dst = smem_u32(smem + s * C::STAGE_BYTES);
                 if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                if (static_cast<int32_t>(lane) < boxes)
-                    tma_load_2d_pair(dst + C::A_BYTES + lane * (C::BOX * kFp8Block), &wmap, b * kFp8Block,
-                                     wy + static_cast<int32_t>(lane) * C::BOX, bar);
+                if (static_cast<int32_t>(lane) < halves)
+                    tma_load_2d_pair(dst + C::A_BYTES + lane * (C::BOX * kFp8Block), &wmap, b * kFp8Block, wy, bar);
                 if (copies) {
                     const uint32_t d = dst + lane * (PER * kFp8Block);
                     if constexpr (GATHER) tma_gather4_pair(d, &xmap, b * kFp8Block, y, bar);
@@ -217,103 +240,170 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 __syncwarp();
             }
         }
-    } else if (warp == C::WARP_MMA) {
+    } else if (warp < C::WARP_ZERO) {
         // ----------------------------------------------------------------- MMA
-        if (rank == 0 && lane == 0) {
-            uint32_t it = 0;
+        // Warp h issues the MMAs of half h.  The whole warp runs the loop and one elected
+        // lane issues: with the operands in uniform registers four MMAs and a commit take
+        // 180 cycles to issue, from a single-lane branch 295, more than the 256 that they run.
+        if (rank == 0) {
+            const uint32_t h = warp - C::WARP_MMA;
+            const bool elected = elect_one();
+            const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+            const uint64_t bskip = (C::A_BYTES + h * (C::BOX * kFp8Block)) >> 4;
+            uint32_t s = 0, phase = 0, done = 0;      // stage, its phase, blocks of this half
             bool ok = true;
             for (int64_t w = w0; w < total && ok; w += dw) {
                 const PairTile t = pair_tile(a, w);
-                const uint32_t idesc = idesc_e4m3_f32(2 * C::BM, t.width);
-                for (int32_t b = 0; b < nb; ++b, ++it) {
-                    const uint32_t s = it % C::STAGES, d = it & 1u;
-                    if (!mbar_wait(&acc_empty[d], ((it >> 1) & 1u) ^ 1u, a.err)) { ok = false; break; }
-                    if (!mbar_wait(&full[s], (it / C::STAGES) & 1u, a.err)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t abase = smem_u32(smem + s * C::STAGE_BYTES), bbase = abase + C::A_BYTES;
+                const int32_t cols = t.cols(static_cast<int32_t>(h));
+                const uint32_t idesc = idesc_e4m3_f32(2 * C::BM, max(cols, 0));
+                for (int32_t b = 0; b < nb; ++b) {
+                    const uint32_t d = 2 * h + (done & 1u);
+                    if (cols > 0) {
+                        if (!mbar_wait2_warp(&full[s], phase, &acc_empty[d], ((done >> 1) & 1u) ^ 1u, a.err)) { ok = false; break; }
+                        ++done;
+                        tc_fence_after();
+                        if (elected) {
+                            const uint64_t adesc = desc0 + ((s * C::STAGE_BYTES) >> 4), bdesc = adesc + bskip;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_f8_pair(tmem + d * C::BN, smem_desc_sw128(abase + 32 * k),
-                                       smem_desc_sw128(bbase + 32 * k), idesc, k);
-                    tc_commit_pair(&empty[s]);
-                    tc_commit_pair(&acc_full[d]);
+                            for (int k = 0; k < 4; ++k) tc_mma_f8_pair(tmem + d * C::CW, adesc + 2 * k, bdesc + 2 * k, idesc, k);
+                            tc_commit_pair(&acc_full[d]);
+                            tc_commit_pair(&empty[s]);
+                        }
+                    } else {
+                        if (!mbar_wait_warp(&full[s], phase, a.err)) { ok = false; break; }
+                        if (elected) tc_commit_pair(&empty[s]);
+                    }
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
         }
         __syncwarp();
-    } else if (warp > C::WARP_MMA) {
-        if (a.ids) zero_unrouted<TO>(a, out, static_cast<int64_t>(blockIdx.x) * 2 + (warp & 1u),
-                                     static_cast<int64_t>(gridDim.x) * 2);
+    } else if (a.ids) {
+        zero_unrouted<TO>(a, out, blockIdx.x, gridDim.x);
     }
     } else {
         // --------------------------------------------------------------- drain
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::DRAIN_REGS));
-        const uint32_t lane0 = (warp & 3u) * 32u, col0 = (warp >> 2) * static_cast<uint32_t>(C::CW);
+        const uint32_t lane0 = (warp & 3u) * 32u, h = warp >> 2;
         const uint32_t acc_empty0 = map_to_rank(smem_u32(acc_empty), 0);
-        uint32_t it = 0;
+        uint8_t* stage = smem + C::OFF_OUT + warp * (32 * C::STAGE_ROW);
+        uint32_t it = 0;                 // blocks of this half
         bool ok = true;
         for (int64_t w = w0; w < total && ok; w += dw) {
             const PairTile t = pair_tile(a, w);
+            const int64_t r0 = t.r0 + h * C::CW;
+            if (r0 >= a.nrows) continue;
             const int32_t mine = t.mine(rank);
             const int32_t m = static_cast<int32_t>(lane0 + lane);        // this thread's slot of the CTA
-            const bool has = m < mine;
-            // nothing to do for warps without a slot or past the weight rows
-            const bool busy = static_cast<int32_t>(lane0) < mine && static_cast<int32_t>(col0) < t.width;
-            int64_t slot = 0;
+            const bool busy = static_cast<int32_t>(lane0) < mine;        // the warp has a slot at all
+            int32_t slot = 0;
             const float* sa = a.act_scales;
-            if (has) {
-                slot = t.first(rank) + m;
-                if (a.perm) slot = a.perm[slot];
-                sa += slot / a.act_div * nb;
+            if (m < mine) {
+                const int64_t p = t.first(rank) + m;
+                slot = a.perm ? a.perm[p] : static_cast<int32_t>(p);
+                sa += (a.ordered ? p : static_cast<int64_t>(slot / a.act_div)) * nb;
             }
-            const int64_t rb = min((t.r0 + col0) / kFp8Block, static_cast<int64_t>(a.row_blocks - 1));
-            const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + rb) * nb;
+            const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + r0 / kFp8Block) * nb;
             float2 acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            float next = __ldg(sa) * __ldg(sw);
-            for (int32_t b = 0; b < nb; ++b, ++it) {
-                const uint32_t d = it & 1u;
-                const float2 sc = make_float2(next, next);
-                if (b + 1 < nb) next = __ldg(sa + b + 1) * __ldg(sw + b + 1);
-                if (!mbar_wait_warp(&acc_full[d], (it >> 1) & 1u, a.err)) { ok = false; break; }
-                tc_fence_after();
-                if (busy) {
+            // scales of the current four blocks (multiplied) and of the next four (in flight:
+            // a load takes longer than a block)
+            float sc[4], na[4], nw[4];
 #pragma unroll
-                    for (int j = 0; j < C::CW / 32; ++j) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(tmem + d * C::BN + (lane0 << 16) + col0 + 32 * j, v);
-                        tmem_wait_ld();
+            for (int i = 0; i < 4; ++i) {
+                na[i] = load_now(sa + min(i, nb - 1));
+                nw[i] = load_now(sw + min(i, nb - 1));
+            }
+            const uint32_t tm = tmem + h * (2 * C::CW) + (lane0 << 16);     // buffer d of this half: + 128 d
+            if (!busy) {
+                for (int32_t b = 0; b < nb; ++b, ++it) {
+                    if (!mbar_wait_warp(&acc_full[2 * h + (it & 1u)], (it >> 1) & 1u, a.err)) { ok = false; break; }
+                    if (lane == 0) mbar_arrive_remote(acc_empty0 + (2 * h + (it & 1u)) * 8);
+                }
+                if (!ok) break;
+                continue;
+            }
+            // 32 columns are on their way from tensor memory while the 32 before them are added
+            uint32_t v[2][32];
+            if (!mbar_wait_warp(&acc_full[2 * h + (it & 1u)], (it >> 1) & 1u, a.err)) { ok = false; break; }
+            tc_fence_after();
+            tmem_ld_32x32b_x32(tm + (it & 1u) * C::CW, v[0]);
+            for (int32_t b = 0; b < nb; ++b) {
+                if ((b & 3) == 0) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[16 * j + i] = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc,
-                                                   acc[16 * j + i]);
+                    for (int i = 0; i < 4; ++i) sc[i] = na[i] * nw[i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        na[i] = load_now(sa + min(b + 4 + i, nb - 1));
+                        nw[i] = load_now(sw + min(b + 4 + i, nb - 1));
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(acc_empty0 + d * 8);
-            }
-            if (!ok) break;
-            if (busy && has) {
-                TO* o = out + slot * a.nrows + t.r0 + col0;
-                const int32_t left = static_cast<int32_t>(min(static_cast<int64_t>(C::CW), a.nrows - t.r0 - col0));
-                constexpr int PER = 16 / static_cast<int>(sizeof(TO));
-                const float* f = reinterpret_cast<const float*>(acc);
-                if (a.wide) {
+                const float2 s2 = make_float2(sc[0], sc[0]);
+                sc[0] = sc[1];
+                sc[1] = sc[2];
+                sc[2] = sc[3];
 #pragma unroll
-                    for (int i = 0; i < C::CW / PER; ++i) {
-                        if (PER * i < left) {
-                            __align__(16) TO v[PER];
-#pragma unroll
-                            for (int k = 0; k < PER; ++k) v[k] = from_f32<TO>(f[PER * i + k]);
-                            *reinterpret_cast<uint4*>(o + PER * i) = *reinterpret_cast<const uint4*>(v);
+                for (int j = 0; j < C::CW / 32; ++j) {
+                    tmem_wait_ld_regs(v[j & 1]);
+                    if (j < C::CW / 32 - 1) {
+                        tmem_ld_32x32b_x32(tm + (it & 1u) * C::CW + 32 * (j + 1), v[(j + 1) & 1]);
+                    } else {      // the block is in registers: its accumulator goes back, the next one's first columns come
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(acc_empty0 + (2 * h + (it & 1u)) * 8);
+                        ++it;
+                        if (b + 1 < nb) {
+                            if (!mbar_wait_warp(&acc_full[2 * h + (it & 1u)], (it >> 1) & 1u, a.err)) { ok = false; break; }
+                            tc_fence_after();
+                            tmem_ld_32x32b_x32(tm + (it & 1u) * C::CW, v[0]);
                         }
                     }
-                } else {
 #pragma unroll
-                    for (int i = 0; i < C::CW; ++i)
-                        if (i < left) o[i] = from_f32<TO>(f[i]);
+                    for (int i = 0; i < 16; ++i)
+                        acc[16 * j + i] = fma2(make_float2(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])),
+                                               s2, acc[16 * j + i]);
+                }
+                if (!ok) break;
+            }
+            if (!ok) break;
+            // out: 256 bytes of each of the warp's rows at a time go through shared memory,
+            // so that a row leaves in whole lines
+            constexpr int PER = 16 / static_cast<int>(sizeof(TO)), PASS = 256 / static_cast<int>(sizeof(TO));
+            const float* f = reinterpret_cast<const float*>(acc);
+            const int32_t rows_here = min(32, mine - static_cast<int32_t>(lane0));
+#pragma unroll
+            for (int ps = 0; ps < C::CW / PASS; ++ps) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    __align__(16) TO v[PER];
+#pragma unroll
+                    for (int k = 0; k < PER; ++k) v[k] = from_f32<TO>(f[ps * PASS + PER * i + k]);
+                    *reinterpret_cast<uint4*>(stage + lane * C::STAGE_ROW + 16 * i) = *reinterpret_cast<const uint4*>(v);
+                }
+                __syncwarp();
+                const int64_t c0 = r0 + ps * PASS;
+                const int32_t left = static_cast<int32_t>(min(static_cast<int64_t>(PASS), a.nrows - c0));
+                if (a.wide) {
+#pragma unroll 4
+                    for (int k = 0; k < 16; ++k) {       // two rows at a time, 16 bytes a lane
+                        const int32_t r = 2 * k + static_cast<int32_t>(lane >> 4), c = static_cast<int32_t>(lane & 15u) * PER;
+                        const int32_t to = __shfl_sync(0xFFFFFFFFu, slot, r);
+                        if (r < rows_here && c < left)
+                            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(to) * a.nrows + c0 + c) =
+                                *reinterpret_cast<const uint4*>(stage + r * C::STAGE_ROW + (lane & 15u) * 16);
+                    }
+                } else {
+                    for (int r = 0; r < rows_here; ++r) {
+                        const int32_t to = __shfl_sync(0xFFFFFFFFu, slot, r);
+                        const TO* src = reinterpret_cast<const TO*>(stage + r * C::STAGE_ROW);
+                        for (int32_t c = static_cast<int32_t>(lane); c < left; c += 32)
+                            out[static_cast<int64_t>(to) * a.nrows + c0 + c] = src[c];
+                    }
                 }
             }
         }
@@ -324,14 +414,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     if (warp == C::WARP_MMA) tmem_dealloc_pair(tmem, 512);
 }
 
+// Activation rows and scales in router order: a warp per position.
+__global__ void __launch_bounds__(256)
+    gather_rows_kernel(const uint8_t* __restrict__ act, const float* __restrict__ scales, const int32_t* __restrict__ perm,
+                       const int32_t* __restrict__ n_routed, int32_t act_div, int32_t row_words, int32_t nb,
+                       uint4* __restrict__ act_out, float* __restrict__ scales_out) {
+    const int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (p >= *n_routed) return;
+    const int64_t row = perm[p] / act_div;
+    const uint4* src = reinterpret_cast<const uint4*>(act) + row * row_words;
+    for (int32_t i = lane_id(); i < row_words; i += 32) act_out[p * row_words + i] = __ldg(src + i);
+    for (int32_t i = lane_id(); i < nb; i += 32) scales_out[p * nb + i] = __ldg(scales + row * nb + i);
+}
+
 // ------------------------------------------------------------------- host
 namespace {
 
+// Routed slots per expert on average from which the rows are copied to router order first.
+constexpr int kGatherMean = 24;
+
+
 struct ProductWs {
-    size_t counts, offsets, perm, tiles, hist, err, total;
+    size_t counts, offsets, perm, tiles, hist, err, rows, scales, total;
 };
 
-ProductWs product_ws(int64_t n_slots, int32_t n_experts) {
+bool copies_rows(int64_t n_slots, int32_t n_experts) { return n_slots > static_cast<int64_t>(kGatherMean) * n_experts; }
+
+ProductWs product_ws(int64_t n_slots, int32_t n_experts, int64_t ncols) {
     ProductWs L{};
     size_t o = 0;
     auto take = [&o](size_t bytes) {
@@ -346,6 +455,9 @@ ProductWs product_ws(int64_t n_slots, int32_t n_experts) {
     L.tiles = take(4 * (E + 1));
     L.hist = take(4 * static_cast<size_t>(route_chunks(n_slots)) * E);
     L.err = take(4);       // the router's own flags: ids of -1 are no error here
+    const size_t copied = copies_rows(n_slots, n_experts) ? S : 0;
+    L.rows = take(copied * static_cast<size_t>(ncols));
+    L.scales = take(copied * static_cast<size_t>(fp8_blocks(ncols)) * 4);
     L.total = o;
     return L;
 }
@@ -370,11 +482,13 @@ int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs
 
 }  // namespace
 
-size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts) { return product_ws(n_slots, n_experts).total; }
+size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts, int64_t ncols) {
+    return product_ws(n_slots, n_experts, ncols).total;
+}
 
 int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* workspace, uint32_t* err, cudaStream_t s) {
     using C = Pair;
-    const ProductWs L = product_ws(p.n_slots, p.n_experts);
+    const ProductWs L = product_ws(p.n_slots, p.n_experts, p.ncols);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PairArgs a{};
     a.act_scales = p.act_scales;
@@ -403,24 +517,38 @@ int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* work
         a.offsets = rb.offsets;
         a.tiles = rb.tiles_gemm;
     }
+    const uint8_t* act = p.act;
+    int64_t act_rows = p.act_rows;
+    const bool copies = p.ids && copies_rows(p.n_slots, p.n_experts);
+    if (copies) {
+        const dim3 grid(static_cast<unsigned>((p.n_slots + 7) / 8));
+        gather_rows_kernel<<<grid, 256, 0, s>>>(p.act, p.act_scales, a.perm, a.offsets + p.n_experts, p.act_div,
+                                                static_cast<int32_t>(p.ncols / 16), a.nb,
+                                                reinterpret_cast<uint4*>(ws + L.rows), reinterpret_cast<float*>(ws + L.scales));
+        if (int st = check_launch("gather_rows_kernel", grid, dim3(256), 0)) return st;
+        act = ws + L.rows;
+        a.act_scales = reinterpret_cast<const float*>(ws + L.scales);
+        act_rows = p.n_slots;
+    }
+    a.ordered = copies || !p.ids;
     CUtensorMap wmap, xmap;
     if (int st = encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weights, p.ncols,
                            static_cast<uint64_t>(p.n_experts) * p.nrows, p.ncols, kFp8Block, C::BOX,
                            CU_TENSOR_MAP_SWIZZLE_128B, "FP8 weights"))
         return st;
-    if (int st = encode_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.act, p.ncols, p.act_rows, p.ncols, kFp8Block,
-                           p.ids ? 1 : 16, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
+    if (int st = encode_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, act, p.ncols, act_rows, p.ncols, kFp8Block,
+                           a.ordered ? C::ROW_BOX : 1, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
         return st;
     const int64_t slot_tiles = (p.n_slots + 2 * C::BM - 1) / (2 * C::BM) + (p.ids ? (p.n_experts < p.n_slots ? p.n_experts : p.n_slots) : 0);
     const int64_t pairs = slot_tiles * a.row_tiles, most = sm_count() / 2;
     const int grid = 2 * static_cast<int>(pairs < most ? pairs : most);
     if (out_dtype == FT_DTYPE_F32) {
         float* o = static_cast<float*>(out);
-        return p.ids ? launch_pair<float, true>(wmap, xmap, a, o, grid, s) : launch_pair<float, false>(wmap, xmap, a, o, grid, s);
+        return a.ordered ? launch_pair<float, false>(wmap, xmap, a, o, grid, s) : launch_pair<float, true>(wmap, xmap, a, o, grid, s);
     }
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-    return p.ids ? launch_pair<__nv_bfloat16, true>(wmap, xmap, a, o, grid, s)
-                 : launch_pair<__nv_bfloat16, false>(wmap, xmap, a, o, grid, s);
+    return a.ordered ? launch_pair<__nv_bfloat16, false>(wmap, xmap, a, o, grid, s)
+                     : launch_pair<__nv_bfloat16, true>(wmap, xmap, a, o, grid, s);
 }
 
 }  // namespace ft

@@ -78,11 +78,11 @@ def test_products_refuse(lib, dense, kw, status):
 def test_routed_products_refuse(lib):
     assert product(lib, E=0) == ARG and product(lib, k=9) == ARG and product(lib, ids=None) == ARG
     assert product(lib, E=4096, N=1 << 20) == SIZE and product(lib, ids=P[4] + 2) == ALIGN
-    need = lib.ft_moe_fp8_workspace_bytes(4, 2, 8)
+    need = lib.ft_moe_fp8_workspace_bytes(4, 2, 8, 256)
     if need:
         assert product(lib, n=need - 1) == WORKSPACE and product(lib, work=None) == WORKSPACE
         assert product(lib, work=P[6] + 16) == ALIGN
-    assert lib.ft_moe_fp8_workspace_bytes(4, 9, 8) == 0
+    assert lib.ft_moe_fp8_workspace_bytes(4, 9, 8, 256) == 0 and lib.ft_moe_fp8_workspace_bytes(4, 2, 8, 100) == 0
 
 
 def test_combine_refuses(lib):
