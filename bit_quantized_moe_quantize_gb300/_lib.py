@@ -96,7 +96,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.ft_act_mul_quantize_fp8.argtypes = [vp, i32, vp, vp, i64, i64, i32, vp]
         L.ft_moe_fp8_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i64, i64, vp, sz, vp]
         L.ft_moe_fp8_fp8_slots.argtypes = L.ft_moe_fp8_fp8.argtypes
-        L.ft_matmul_fp8_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, sz, vp]
+        L.ft_matmul_fp8_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]
         L.ft_moe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i64, i32, i64, vp]
         L.ft_moe_layer_fp8.argtypes = [vp, i32, vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64,
                                        i32, i32, i32, i32, i32, f32, i32, vp, sz, vp]
@@ -582,8 +582,7 @@ def matmul_fp8_fp8(weights, w_scales, act, act_scales, out=None, out_dtype=None)
     out_dtype = (torch.float32 if out_dtype is None else out_dtype) if out is None else out.dtype
     code = _dtype_code(out_dtype, "out_dtype", "torch.float32", "torch.bfloat16")
     out = _out(out, "out", (M, N), out_dtype, weights)
-    L = load()
-    _check(L.ft_matmul_fp8_fp8(pw, ps, pa, pt, out.data_ptr(), code, M, N, K, None, 0, _raw_stream(weights)))
+    _check(load().ft_matmul_fp8_fp8(pw, ps, pa, pt, out.data_ptr(), code, M, N, K, _raw_stream(weights)))
     return out
 
 

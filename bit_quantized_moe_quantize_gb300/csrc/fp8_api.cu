@@ -121,7 +121,8 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
     if (!aligned(weights, 16) || !aligned(act, 16)) return fail(FT_ERR_ALIGN, "weights and act must be 16-byte aligned");
     if (!aligned(w_scales, 4) || !aligned(act_scales, 4) || !aligned(ids, 4) || !aligned(out, dtype_bytes(out_dtype)))
         return fail(FT_ERR_ALIGN, "scales, ids and out must be aligned to their elements");
-    if (int st = check_workspace(workspace, workspace_bytes, dense ? 0 : fp8_product_workspace(n_slots, n_experts, ncols))) return st;
+    if (!dense)
+        if (int st = check_workspace(workspace, workspace_bytes, fp8_product_workspace(n_slots, n_experts, ncols))) return st;
     uint32_t* err = nullptr;
     if (int st = fp8_error_word(&err)) return st;
     Fp8Product p{};
@@ -237,10 +238,9 @@ int ft_moe_fp8_fp8_slots(const void* weights, const float* w_scales, const void*
 }
 
 int ft_matmul_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales, void* out,
-                      int32_t out_dtype, int64_t rows, int64_t nrows, int64_t ncols, void* workspace,
-                      size_t workspace_bytes, void* stream) {
+                      int32_t out_dtype, int64_t rows, int64_t nrows, int64_t ncols, void* stream) {
     return product_entry(weights, w_scales, act, act_scales, nullptr, true, true, out, out_dtype, rows, 1, 1, nrows,
-                         ncols, workspace, workspace_bytes, stream);
+                         ncols, nullptr, 0, stream);
 }
 
 int ft_moe_combine(const void* rows, int32_t rows_dtype, const float* topk_weights, const void* add, void* y,

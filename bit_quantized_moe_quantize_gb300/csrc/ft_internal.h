@@ -174,7 +174,7 @@ struct Fp8Product {
     int32_t act_div;            // activation row of slot s: s / act_div
     int32_t n_experts;
 };
-size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts, int64_t ncols);
+size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts, int64_t ncols);   // routed products
 int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* workspace, uint32_t* err, cudaStream_t s);
 
 }  // namespace ft

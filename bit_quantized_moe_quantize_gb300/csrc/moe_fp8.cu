@@ -57,13 +57,15 @@ struct Pair {
     static constexpr int THREADS = 12 * 32;
     // registers: 384 threads are launched with LAUNCH_REGS each; the drain warps
     // take DRAIN_REGS, and the others give theirs down to OTHER_REGS
-    static constexpr int LAUNCH_REGS = 168, DRAIN_REGS = 232, OTHER_REGS = 40;
+    static constexpr int LAUNCH_REGS = 168, DRAIN_REGS = 216, OTHER_REGS = 72;
     static_assert(DRAIN_REGS * 256 + OTHER_REGS * 128 <= LAUNCH_REGS * THREADS, "the split must fit the launch's registers");
     static constexpr int CW = BN / 2;              // columns of a half
     static constexpr int STAGE_ROW = 256 + 16;     // output staging: 256 bytes of a slot's row, and 16 so that
                                                    // eight lanes' 16-byte words fall in different banks
     static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
-    static constexpr int OFF_BAR = OFF_OUT + N_DRAIN_WARPS * 32 * STAGE_ROW;
+    static constexpr int OFF_SCALE = OFF_OUT + N_DRAIN_WARPS * 32 * STAGE_ROW;
+    static constexpr int SCALE_RING = 4;           // groups of four blocks' scales in flight
+    static constexpr int OFF_BAR = OFF_SCALE + SCALE_RING * (N_DRAIN_WARPS * 32 + N_DRAIN_WARPS) * 16;
     static constexpr int N_BARS = 2 * STAGES + 8;
     static constexpr int OFF_TMEM = OFF_BAR + N_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;    // + alignment slack
@@ -80,16 +82,18 @@ struct PairArgs {
     uint32_t* err;
     int64_t n_slots, nrows;
     int32_t act_div, n_experts, nb, row_tiles, row_blocks;
+    int32_t scale_pitch;         // act_scales: elements between rows
+    bool scale_words;            // four neighbouring activation scales from a multiple of 4 on are a 16-byte word
     bool ordered;                // act rows and scales lie in router order
     bool wide;                   // the rows of out are whole 16-byte words
 };
 
 struct PairTile {
     int32_t e, n, half, width;   // expert, valid slots, slots of CTA 0 (the rest are CTA 1's), MMA width
-    int64_t p0, r0;              // first router position, first weight row
+    int32_t p0, r0;              // first router position, first weight row
     // slots of CTA `rank`, and their first position
     __device__ int32_t mine(uint32_t rank) const { return rank ? n - half : half; }
-    __device__ int64_t first(uint32_t rank) const { return p0 + (rank ? half : 0); }
+    __device__ int32_t first(uint32_t rank) const { return p0 + (rank ? half : 0); }
     // MMA columns of half h (0, or past 0 where the tile has none)
     __device__ int32_t cols(int32_t h) const { return min(Pair::CW, width - h * Pair::CW); }
 };
@@ -97,10 +101,10 @@ struct PairTile {
 // Work item w: row tile w % row_tiles of slot tile w / row_tiles.
 __device__ __forceinline__ PairTile pair_tile(const PairArgs& a, int64_t w) {
     PairTile t;
-    const int64_t st = w / a.row_tiles;
-    t.r0 = (w - st * a.row_tiles) * Pair::BN;
-    t.width = static_cast<int32_t>(min(static_cast<int64_t>(Pair::BN), (a.nrows - t.r0 + 31) / 32 * 32));
-    int64_t first = 0, count = a.n_slots, j = st;
+    const int32_t st = static_cast<int32_t>(w / a.row_tiles), nrows = static_cast<int32_t>(a.nrows);
+    t.r0 = static_cast<int32_t>(w - static_cast<int64_t>(st) * a.row_tiles) * Pair::BN;
+    t.width = (min(Pair::BN, nrows - t.r0) + 31) / 32 * 32;
+    int32_t first = 0, count = static_cast<int32_t>(a.n_slots), j = st;
     t.e = 0;
     if (a.tiles) {
         int32_t lo = 0, hi = a.n_experts - 1;
@@ -115,25 +119,27 @@ __device__ __forceinline__ PairTile pair_tile(const PairArgs& a, int64_t w) {
         j = st - a.tiles[lo];
     }
     t.p0 = first + j * (2 * Pair::BM);
-    t.n = static_cast<int32_t>(min(static_cast<int64_t>(2 * Pair::BM), count - j * (2 * Pair::BM)));
+    t.n = min(2 * Pair::BM, count - j * (2 * Pair::BM));
     t.half = min(t.n, (t.n + 63) / 64 * 32);        // whole warps, nearly even
     return t;
 }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+// Two fp32 values in one 64-bit register, the operand of the packed FMA.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
-          "l"(*reinterpret_cast<uint64_t*>(&c)));
-    return *reinterpret_cast<float2*>(&r);
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
 
-// Read-only load that stays where it is written (a block before its use).
-__device__ __forceinline__ float load_now(const float* p) {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
+// acc += {lo, hi} * s
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
 }
 
 // Rows of slots without an expert are 0; ids that are neither -1 nor an expert raise the flag.
@@ -151,6 +157,37 @@ __device__ __forceinline__ void zero_unrouted(const PairArgs& a, TO* out, int64_
             for (int64_t r = lane_id(); r < a.nrows; r += 32) out[row * a.nrows + r] = from_f32<TO>(0.0f);
         }
     }
+}
+
+// The ring of scales: group g of four blocks lies in slot g % SCALE_RING.  A thread
+// copies (asynchronously) and reads its own activation scales; the weight scales are
+// its warp's.  A register would hold a load that the next block's code waits for
+// even when an older one is wanted: with three blocks in flight in registers the
+// products of a block waited 100 cycles.
+template <int STEP>
+__device__ __forceinline__ float4* ring_at(float4* ring, int32_t g) { return ring + g % Pair::SCALE_RING * STEP; }
+
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src, int32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Starts the copies of group g (blocks past the row's end arrive as 0) and closes
+// their group of asynchronous copies; groups past the last one close empty.
+__device__ __forceinline__ void copy_scales(const PairArgs& a, const float* sa, const float* sw, int32_t g, float4* ring_a,
+                                            float4* ring_w) {
+    const int32_t b = 4 * g;
+    if (b < a.nb) {
+        const uint32_t da = smem_u32(ring_at<256>(ring_a, g)), dw = smem_u32(ring_at<8>(ring_w, g));
+        if (a.scale_words) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(da), "l"(sa + b) : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy_async4(da + 4 * i, sa + min(b + i, a.nb - 1), b + i < a.nb ? 4 : 0);
+        }
+        const int32_t i = static_cast<int32_t>(lane_id());
+        if (i < 4) copy_async4(dw + 4 * i, sw + min(b + i, a.nb - 1), b + i < a.nb ? 4 : 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 template <typename TO, bool GATHER>
@@ -209,13 +246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             const bool copies = static_cast<int32_t>(lane) * PER < mine;
             int32_t y[4] = {0, 0, 0, 0};
             if (copies) {
-                const int64_t p = t.first(rank) + lane * PER;
+                const int32_t p = t.first(rank) + static_cast<int32_t>(lane) * PER;
                 if constexpr (GATHER) {
-                    const int64_t last = t.first(rank) + mine - 1;      // the last rows of a part group repeat it
+                    const int32_t last = t.first(rank) + mine - 1;      // the last rows of a part group repeat it
 #pragma unroll
                     for (int i = 0; i < 4; ++i) y[i] = a.perm[min(p + i, last)] / a.act_div;
                 } else {
-                    y[0] = static_cast<int32_t>(p);
+                    y[0] = p;
                 }
             }
             // half h of the tile (weight rows 128 h ..): this CTA's part of its MMA's columns
@@ -290,11 +327,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         const uint32_t lane0 = (warp & 3u) * 32u, h = warp >> 2;
         const uint32_t acc_empty0 = map_to_rank(smem_u32(acc_empty), 0);
         uint8_t* stage = smem + C::OFF_OUT + warp * (32 * C::STAGE_ROW);
+        // this thread's word of the ring of activation scales, and its warp's of the ring of weight scales
+        float4* ring_a = reinterpret_cast<float4*>(smem + C::OFF_SCALE) + threadIdx.x;
+        float4* ring_w = reinterpret_cast<float4*>(smem + C::OFF_SCALE) + C::SCALE_RING * 256 + warp;
         uint32_t it = 0;                 // blocks of this half
         bool ok = true;
         for (int64_t w = w0; w < total && ok; w += dw) {
             const PairTile t = pair_tile(a, w);
-            const int64_t r0 = t.r0 + h * C::CW;
+            const int32_t r0 = t.r0 + static_cast<int32_t>(h) * C::CW;
             if (r0 >= a.nrows) continue;
             const int32_t mine = t.mine(rank);
             const int32_t m = static_cast<int32_t>(lane0 + lane);        // this thread's slot of the CTA
@@ -302,22 +342,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             int32_t slot = 0;
             const float* sa = a.act_scales;
             if (m < mine) {
-                const int64_t p = t.first(rank) + m;
-                slot = a.perm ? a.perm[p] : static_cast<int32_t>(p);
-                sa += (a.ordered ? p : static_cast<int64_t>(slot / a.act_div)) * nb;
+                const int32_t p = t.first(rank) + m;
+                slot = a.perm ? a.perm[p] : p;
+                sa += static_cast<int64_t>(a.ordered ? p : slot / a.act_div) * a.scale_pitch;
             }
             const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + r0 / kFp8Block) * nb;
-            float2 acc[C::CW / 2];
+            uint64_t acc[C::CW / 2];
 #pragma unroll
-            for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            // scales of the current four blocks (multiplied) and of the next four (in flight:
-            // a load takes longer than a block)
-            float sc[4], na[4], nw[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                na[i] = load_now(sa + min(i, nb - 1));
-                nw[i] = load_now(sw + min(i, nb - 1));
-            }
+            for (int i = 0; i < C::CW / 2; ++i) acc[i] = 0;
             const uint32_t tm = tmem + h * (2 * C::CW) + (lane0 << 16);     // buffer d of this half: + 128 d
             if (!busy) {
                 for (int32_t b = 0; b < nb; ++b, ++it) {
@@ -327,45 +359,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 if (!ok) break;
                 continue;
             }
-            // 32 columns are on their way from tensor memory while the 32 before them are added
-            uint32_t v[2][32];
+            // the scales of the first blocks: four at a time through a ring in shared memory
+#pragma unroll
+            for (int i = 0; i < C::SCALE_RING - 1; ++i) copy_scales(a, sa, sw, i, ring_a, ring_w);
+            float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            // 16 columns are on their way from tensor memory while the 16 before them are added
+            uint32_t v[2][16];
             if (!mbar_wait_warp(&acc_full[2 * h + (it & 1u)], (it >> 1) & 1u, a.err)) { ok = false; break; }
             tc_fence_after();
-            tmem_ld_32x32b_x32(tm + (it & 1u) * C::CW, v[0]);
+            tmem_ld_32x32b_x16(tm + (it & 1u) * C::CW, v[0]);
             for (int32_t b = 0; b < nb; ++b) {
                 if ((b & 3) == 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[i] = na[i] * nw[i];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        na[i] = load_now(sa + min(b + 4 + i, nb - 1));
-                        nw[i] = load_now(sw + min(b + 4 + i, nb - 1));
-                    }
+                    asm volatile("cp.async.wait_group %0;" ::"n"(C::SCALE_RING - 2) : "memory");
+                    __syncwarp();
+                    const float4 x = *ring_at<256>(ring_a, b >> 2), y = *ring_at<8>(ring_w, b >> 2);
+                    sc[0] = x.x * y.x;
+                    sc[1] = x.y * y.y;
+                    sc[2] = x.z * y.z;
+                    sc[3] = x.w * y.w;
+                    __syncwarp();      // before the slot is filled again
+                    copy_scales(a, sa, sw, (b >> 2) + C::SCALE_RING - 1, ring_a, ring_w);
                 }
-                const float2 s2 = make_float2(sc[0], sc[0]);
+                const float scale = sc[0];
                 sc[0] = sc[1];
                 sc[1] = sc[2];
                 sc[2] = sc[3];
+                const uint64_t s2 = pack2(scale, scale);
+                const uint32_t nd = 2 * h + ((it + 1) & 1u), nph = ((it + 1) >> 1) & 1u;      // the next block's accumulator
+                bool ready = false;
 #pragma unroll
-                for (int j = 0; j < C::CW / 32; ++j) {
+                for (int j = 0; j < C::CW / 16; ++j) {
                     tmem_wait_ld_regs(v[j & 1]);
-                    if (j < C::CW / 32 - 1) {
-                        tmem_ld_32x32b_x32(tm + (it & 1u) * C::CW + 32 * (j + 1), v[(j + 1) & 1]);
+                    if (j == C::CW / 16 - 3) ready = mbar_test(&acc_full[nd], nph);      // its latency passes under the sums
+                    if (j < C::CW / 16 - 1) {
+                        tmem_ld_32x32b_x16(tm + (it & 1u) * C::CW + 16 * (j + 1), v[(j + 1) & 1]);
                     } else {      // the block is in registers: its accumulator goes back, the next one's first columns come
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_remote(acc_empty0 + (2 * h + (it & 1u)) * 8);
                         ++it;
                         if (b + 1 < nb) {
-                            if (!mbar_wait_warp(&acc_full[2 * h + (it & 1u)], (it >> 1) & 1u, a.err)) { ok = false; break; }
+                            if (!__all_sync(0xFFFFFFFFu, ready) && !mbar_wait_warp(&acc_full[nd], nph, a.err)) { ok = false; break; }
                             tc_fence_after();
-                            tmem_ld_32x32b_x32(tm + (it & 1u) * C::CW, v[0]);
+                            tmem_ld_32x32b_x16(tm + (it & 1u) * C::CW, v[0]);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[16 * j + i] = fma2(make_float2(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])),
-                                               s2, acc[16 * j + i]);
+                    for (int i = 0; i < 8; ++i) fma2(acc[8 * j + i], v[j & 1][2 * i], v[j & 1][2 * i + 1], s2);
                 }
                 if (!ok) break;
             }
@@ -373,21 +413,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             // out: 256 bytes of each of the warp's rows at a time go through shared memory,
             // so that a row leaves in whole lines
             constexpr int PER = 16 / static_cast<int>(sizeof(TO)), PASS = 256 / static_cast<int>(sizeof(TO));
-            const float* f = reinterpret_cast<const float*>(acc);
             const int32_t rows_here = min(32, mine - static_cast<int32_t>(lane0));
 #pragma unroll
             for (int ps = 0; ps < C::CW / PASS; ++ps) {
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    __align__(16) TO v[PER];
+                    __align__(16) TO o[PER];
 #pragma unroll
-                    for (int k = 0; k < PER; ++k) v[k] = from_f32<TO>(f[ps * PASS + PER * i + k]);
-                    *reinterpret_cast<uint4*>(stage + lane * C::STAGE_ROW + 16 * i) = *reinterpret_cast<const uint4*>(v);
+                    for (int k = 0; k < PER; k += 2) {
+                        const float2 f = unpack2(acc[(ps * PASS + PER * i + k) / 2]);
+                        o[k] = from_f32<TO>(f.x);
+                        o[k + 1] = from_f32<TO>(f.y);
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * C::STAGE_ROW + 16 * i) = *reinterpret_cast<const uint4*>(o);
                 }
                 __syncwarp();
-                const int64_t c0 = r0 + ps * PASS;
-                const int32_t left = static_cast<int32_t>(min(static_cast<int64_t>(PASS), a.nrows - c0));
+                const int32_t c0 = r0 + ps * PASS;
+                const int32_t left = min(PASS, static_cast<int32_t>(a.nrows) - c0);
                 if (a.wide) {
 #pragma unroll 4
                     for (int k = 0; k < 16; ++k) {       // two rows at a time, 16 bytes a lane
@@ -414,17 +457,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     if (warp == C::WARP_MMA) tmem_dealloc_pair(tmem, 512);
 }
 
-// Activation rows and scales in router order: a warp per position.
+// Activation rows and scales in router order: a warp per position.  Rows of scales lie
+// `pitch` apart (a multiple of 4, so that a drain thread takes four with one copy).
 __global__ void __launch_bounds__(256)
-    gather_rows_kernel(const uint8_t* __restrict__ act, const float* __restrict__ scales, const int32_t* __restrict__ perm,
-                       const int32_t* __restrict__ n_routed, int32_t act_div, int32_t row_words, int32_t nb,
-                       uint4* __restrict__ act_out, float* __restrict__ scales_out) {
+    order_rows_kernel(const uint8_t* __restrict__ act, const float* __restrict__ scales, const int32_t* __restrict__ perm,
+                      const int32_t* __restrict__ n_routed, int32_t act_div, int32_t row_words, int32_t nb, int32_t pitch,
+                      uint4* __restrict__ act_out, float* __restrict__ scales_out) {
     const int64_t p = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (p >= *n_routed) return;
     const int64_t row = perm[p] / act_div;
     const uint4* src = reinterpret_cast<const uint4*>(act) + row * row_words;
     for (int32_t i = lane_id(); i < row_words; i += 32) act_out[p * row_words + i] = __ldg(src + i);
-    for (int32_t i = lane_id(); i < nb; i += 32) scales_out[p * nb + i] = __ldg(scales + row * nb + i);
+    for (int32_t i = lane_id(); i < nb; i += 32) scales_out[p * pitch + i] = __ldg(scales + row * nb + i);
 }
 
 // ------------------------------------------------------------------- host
@@ -439,6 +483,8 @@ struct ProductWs {
 };
 
 bool copies_rows(int64_t n_slots, int32_t n_experts) { return n_slots > static_cast<int64_t>(kGatherMean) * n_experts; }
+
+int32_t scale_pitch(int64_t ncols) { return static_cast<int32_t>((fp8_blocks(ncols) + 3) / 4 * 4); }
 
 ProductWs product_ws(int64_t n_slots, int32_t n_experts, int64_t ncols) {
     ProductWs L{};
@@ -457,7 +503,7 @@ ProductWs product_ws(int64_t n_slots, int32_t n_experts, int64_t ncols) {
     L.err = take(4);       // the router's own flags: ids of -1 are no error here
     const size_t copied = copies_rows(n_slots, n_experts) ? S : 0;
     L.rows = take(copied * static_cast<size_t>(ncols));
-    L.scales = take(copied * static_cast<size_t>(fp8_blocks(ncols)) * 4);
+    L.scales = take(copied * static_cast<size_t>(scale_pitch(ncols)) * 4);
     L.total = o;
     return L;
 }
@@ -488,7 +534,6 @@ size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts, int64_t ncols) 
 
 int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* workspace, uint32_t* err, cudaStream_t s) {
     using C = Pair;
-    const ProductWs L = product_ws(p.n_slots, p.n_experts, p.ncols);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PairArgs a{};
     a.act_scales = p.act_scales;
@@ -503,7 +548,9 @@ int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* work
     a.row_tiles = static_cast<int32_t>((p.nrows + C::BN - 1) / C::BN);
     const int out_bytes = out_dtype == FT_DTYPE_F32 ? 4 : 2;
     a.wide = p.nrows * out_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    ProductWs L{};
     if (p.ids) {
+        L = product_ws(p.n_slots, p.n_experts, p.ncols);
         RouteBuffers rb{};
         rb.counts = reinterpret_cast<int32_t*>(ws + L.counts);
         rb.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
@@ -519,17 +566,20 @@ int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* work
     }
     const uint8_t* act = p.act;
     int64_t act_rows = p.act_rows;
+    a.scale_pitch = a.nb;
     const bool copies = p.ids && copies_rows(p.n_slots, p.n_experts);
     if (copies) {
+        a.scale_pitch = scale_pitch(p.ncols);
         const dim3 grid(static_cast<unsigned>((p.n_slots + 7) / 8));
-        gather_rows_kernel<<<grid, 256, 0, s>>>(p.act, p.act_scales, a.perm, a.offsets + p.n_experts, p.act_div,
-                                                static_cast<int32_t>(p.ncols / 16), a.nb,
-                                                reinterpret_cast<uint4*>(ws + L.rows), reinterpret_cast<float*>(ws + L.scales));
-        if (int st = check_launch("gather_rows_kernel", grid, dim3(256), 0)) return st;
+        order_rows_kernel<<<grid, 256, 0, s>>>(p.act, p.act_scales, a.perm, a.offsets + p.n_experts, p.act_div,
+                                               static_cast<int32_t>(p.ncols / 16), a.nb, a.scale_pitch,
+                                               reinterpret_cast<uint4*>(ws + L.rows), reinterpret_cast<float*>(ws + L.scales));
+        if (int st = check_launch("order_rows_kernel", grid, dim3(256), 0)) return st;
         act = ws + L.rows;
         a.act_scales = reinterpret_cast<const float*>(ws + L.scales);
         act_rows = p.n_slots;
     }
+    a.scale_words = a.scale_pitch % 4 == 0 && reinterpret_cast<uintptr_t>(a.act_scales) % 16 == 0;
     a.ordered = copies || !p.ids;
     CUtensorMap wmap, xmap;
     if (int st = encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weights, p.ncols,

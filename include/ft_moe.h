@@ -654,8 +654,8 @@ FT_API int ft_act_mul_quantize_fp8(const void* h, int32_t dtype, void* codes, fl
  *        element is written
  * Needs 0 < ncols <= FT_MAX_NCOLS, n_experts * nrows < 2^31, top_k <= n_experts
  * <= FT_MAX_EXPERTS, tokens * top_k < 2^31.
- * ft_moe_fp8_workspace_bytes: bytes for tokens, top_k, n_experts, ncols (the
- * dense product: rows, 1, 1, ncols); 0 for invalid arguments.
+ * ft_moe_fp8_workspace_bytes returns 0 for invalid arguments; the dense product
+ * needs no workspace.
  */
 FT_API size_t ft_moe_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_experts, int64_t ncols);
 FT_API int ft_moe_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales,
@@ -668,7 +668,7 @@ FT_API int ft_moe_fp8_fp8_slots(const void* weights, const float* w_scales, cons
                                 void* workspace, size_t workspace_bytes, void* stream);
 FT_API int ft_matmul_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales,
                              void* out, int32_t out_dtype, int64_t rows, int64_t nrows, int64_t ncols,
-                             void* workspace, size_t workspace_bytes, void* stream);
+                             void* stream);
 
 /*
  * ft_moe_combine - the weighted sum of a token's expert rows:

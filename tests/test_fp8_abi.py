@@ -56,8 +56,7 @@ def product(lib, dense=False, **kw):
              n=1 << 40)
     a.update(kw)
     if dense:
-        return lib.ft_matmul_fp8_fp8(a["w"], a["ws"], a["a"], a["s"], a["out"], a["dt"], a["T"], a["N"], a["K"],
-                                     a["work"], a["n"], None)
+        return lib.ft_matmul_fp8_fp8(a["w"], a["ws"], a["a"], a["s"], a["out"], a["dt"], a["T"], a["N"], a["K"], None)
     got = {f(a["w"], a["ws"], a["a"], a["s"], a["ids"], a["out"], a["dt"], a["T"], a["k"], a["E"], a["N"], a["K"],
              a["work"], a["n"], None) for f in (lib.ft_moe_fp8_fp8, lib.ft_moe_fp8_fp8_slots)}
     assert len(got) == 1
