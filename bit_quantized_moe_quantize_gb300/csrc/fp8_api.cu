@@ -104,7 +104,29 @@ int check_workspace(const void* workspace, size_t have, size_t need) {
     return FT_OK;
 }
 
-// ids == nullptr: dense (tokens rows, one matrix)
+size_t take_bytes(size_t* at, size_t bytes) {
+    const size_t r = *at;
+    *at = al256(*at + bytes);
+    return r;
+}
+
+// Workspace of a routed product: router order, then (many slots per expert) the
+// activation rows and scales in that order.
+struct ProductWs {
+    Fp8Order order;
+    size_t rows, scales, total;
+};
+
+ProductWs product_ws(uint8_t* base, int64_t n_slots, int32_t n_experts, int64_t ncols) {
+    ProductWs L{};
+    size_t at = al256(fp8_order_layout(base, n_slots, n_experts, false, &L.order));
+    const size_t copied = fp8_copies_rows(n_slots, n_experts) ? static_cast<size_t>(n_slots) : 0;
+    L.rows = take_bytes(&at, copied * static_cast<size_t>(ncols));
+    L.scales = take_bytes(&at, copied * static_cast<size_t>(fp8_scale_pitch(ncols)) * 4);
+    L.total = at;
+    return L;
+}
+
 int product_entry(const void* weights, const float* w_scales, const void* act, const float* act_scales,
                   const int32_t* ids, bool dense, bool per_slot, void* out, int32_t out_dtype, int64_t tokens,
                   int32_t top_k, int32_t n_experts, int64_t nrows, int64_t ncols, void* workspace,
@@ -121,46 +143,64 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
     if (!aligned(weights, 16) || !aligned(act, 16)) return fail(FT_ERR_ALIGN, "weights and act must be 16-byte aligned");
     if (!aligned(w_scales, 4) || !aligned(act_scales, 4) || !aligned(ids, 4) || !aligned(out, dtype_bytes(out_dtype)))
         return fail(FT_ERR_ALIGN, "scales, ids and out must be aligned to their elements");
-    if (!dense)
-        if (int st = check_workspace(workspace, workspace_bytes, fp8_product_workspace(n_slots, n_experts, ncols))) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    ProductWs L{};
+    if (!dense) {
+        L = product_ws(ws, n_slots, n_experts, ncols);
+        if (int st = check_workspace(workspace, workspace_bytes, L.total)) return st;
+    }
     uint32_t* err = nullptr;
     if (int st = fp8_error_word(&err)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     Fp8Product p{};
     p.weights = static_cast<const uint8_t*>(weights);
     p.w_scales = w_scales;
     p.act = static_cast<const uint8_t*>(act);
     p.act_scales = act_scales;
-    p.ids = dense ? nullptr : ids;
+    p.scale_pitch = static_cast<int32_t>(fp8_blocks(ncols));
     p.n_slots = n_slots;
     p.act_div = per_slot ? 1 : top_k;
     p.act_rows = per_slot ? n_slots : tokens;
     p.nrows = nrows;
     p.ncols = ncols;
     p.n_experts = n_experts;
-    return launch_fp8_product(p, out, out_dtype, workspace, err, static_cast<cudaStream_t>(stream));
+    if (!dense) {
+        p.ids = ids;
+        p.order = &L.order;
+        if (int st = launch_fp8_order(ids, n_slots, n_experts, L.order, s)) return st;
+        if (fp8_copies_rows(n_slots, n_experts))
+            if (int st = launch_fp8_order_rows(&p, ws + L.rows, reinterpret_cast<float*>(ws + L.scales), s)) return st;
+    }
+    return launch_fp8_product(p, out, out_dtype, err, s);
 }
 
+// Workspace of a layer: router order; x's codes and scales, in router order where a
+// batch has many slots per expert (`spread`), else by token; the gated values' codes and
+// scales in router order; where the products cannot quantize them themselves
+// (n_inter % 128 != 0) the first product's fp32 rows, codes by slot and (`spread`) copies
+// of them in router order; the second product's bf16 rows.
 struct LayerWs {
-    size_t xq, xs, h, mq, ms, rows, product, total;
+    Fp8Order order;
+    size_t xq, xs, mq, ms, h, oq, os, rows, total;
+    bool spread, gated;
 };
 
-LayerWs layer_ws(int64_t tokens, int64_t n_slots, int32_t n_experts, int64_t hidden, int64_t n_inter) {
+LayerWs layer_ws(uint8_t* base, int64_t tokens, int64_t n_slots, int32_t n_experts, int64_t hidden, int64_t n_inter) {
     LayerWs L{};
-    size_t o = 0;
-    auto take = [&o](size_t bytes) {
-        const size_t at = o;
-        o = al256(o + bytes);
-        return at;
-    };
-    const size_t T = static_cast<size_t>(tokens), S = static_cast<size_t>(n_slots);
-    L.xq = take(T * hidden);
-    L.xs = take(T * fp8_blocks(hidden) * 4);
-    L.h = take(S * 2 * n_inter * 4);
-    L.mq = take(S * n_inter);
-    L.ms = take(S * fp8_blocks(n_inter) * 4);
-    L.rows = take(S * hidden * 2);
-    L.product = take(std::max(fp8_product_workspace(n_slots, n_experts, hidden), fp8_product_workspace(n_slots, n_experts, n_inter)));
-    L.total = o;
+    L.spread = fp8_copies_rows(n_slots, n_experts);
+    L.gated = n_inter % kFp8Block == 0;
+    size_t at = al256(fp8_order_layout(base, n_slots, n_experts, L.spread, &L.order));
+    const size_t S = static_cast<size_t>(n_slots), X = L.spread ? S : static_cast<size_t>(tokens);
+    L.xq = take_bytes(&at, X * hidden);
+    L.xs = take_bytes(&at, X * fp8_scale_pitch(hidden) * 4);
+    L.mq = take_bytes(&at, S * n_inter);
+    L.ms = take_bytes(&at, S * fp8_scale_pitch(n_inter) * 4);
+    L.h = take_bytes(&at, L.gated ? 0 : S * 2 * n_inter * 4);
+    const size_t ordered = L.spread && !L.gated ? S : 0;
+    L.oq = take_bytes(&at, ordered * n_inter);
+    L.os = take_bytes(&at, ordered * fp8_scale_pitch(n_inter) * 4);
+    L.rows = take_bytes(&at, S * hidden * 2);
+    L.total = at;
     return L;
 }
 
@@ -218,7 +258,7 @@ size_t ft_moe_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_exper
     int64_t n_slots;
     int64_t n;
     if (check_slots(tokens, top_k, n_experts, &n_slots) || check_cols(ncols, "ncols") || !mul_ok(n_slots, ncols, &n)) return 0;
-    return fp8_product_workspace(n_slots, n_experts, ncols);
+    return product_ws(nullptr, n_slots, n_experts, ncols).total;
 }
 
 int ft_moe_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales,
@@ -272,7 +312,7 @@ size_t ft_moe_layer_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n
     if (check_matrix(n_experts, hidden, n_inter) || n_inter > FT_MAX_NCOLS || check_matrix(n_experts, 2 * n_inter, hidden))
         return 0;
     if (!mul_ok(n_slots, 8 * (hidden + n_inter), &n)) return 0;
-    return layer_ws(tokens, n_slots, n_experts, hidden, n_inter).total;
+    return layer_ws(nullptr, tokens, n_slots, n_experts, hidden, n_inter).total;
 }
 
 int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t logits_dtype, int64_t row_stride,
@@ -304,32 +344,56 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
     if (!aligned(logits, dtype_bytes(logits_dtype)) || !aligned(bias, 4) || !aligned(s13, 4) || !aligned(s2, 4) ||
         !aligned(y, 2) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
         return fail(FT_ERR_ALIGN, "logits, bias, scales, y, topk_ids and topk_weights must be aligned to their elements");
-    const LayerWs L = layer_ws(tokens, n_slots, n_experts, hidden, n_inter);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const LayerWs L = layer_ws(ws, tokens, n_slots, n_experts, hidden, n_inter);
     if (int st = check_workspace(workspace, workspace_bytes, L.total)) return st;
     uint32_t* err = nullptr;
     if (int st = fp8_error_word(&err)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
 
     const GateParams g{tokens, n_experts, top_k, score, n_groups, topk_groups, group_top, renormalize, scale, bias};
     if (int st = launch_gate(g, logits, logits_dtype, row_stride, topk_ids, topk_weights, s)) return st;
-    float* xs = reinterpret_cast<float*>(ws + L.xs);
-    if (int st = launch_quantize_fp8(x, x_dtype, ws + L.xq, xs, tokens, hidden, false, act_kind, s)) return st;
+    if (int st = launch_fp8_order(topk_ids, n_slots, n_experts, L.order, s)) return st;
+    float *xs = reinterpret_cast<float*>(ws + L.xs), *ms = reinterpret_cast<float*>(ws + L.ms);
     Fp8Product p{};
+    p.ids = topk_ids;
+    p.order = &L.order;
+    p.n_slots = n_slots;
+    p.n_experts = n_experts;
+    // first product: gate and up rows
+    if (L.spread) {
+        p.scale_pitch = fp8_scale_pitch(hidden);
+        if (int st = launch_quantize_fp8_spread(x, x_dtype, ws + L.xq, xs, tokens, hidden, L.order.pos, top_k, p.scale_pitch, s))
+            return st;
+    } else {
+        p.scale_pitch = static_cast<int32_t>(fp8_blocks(hidden));
+        if (int st = launch_quantize_fp8(x, x_dtype, ws + L.xq, xs, tokens, hidden, false, act_kind, s)) return st;
+    }
     p.weights = static_cast<const uint8_t*>(w13);
     p.w_scales = s13;
     p.act = ws + L.xq;
     p.act_scales = xs;
-    p.ids = topk_ids;
-    p.n_slots = n_slots;
+    p.ordered = L.spread;
     p.act_div = top_k;
-    p.act_rows = tokens;
+    p.act_rows = L.spread ? n_slots : tokens;
     p.nrows = 2 * n_inter;
     p.ncols = hidden;
-    p.n_experts = n_experts;
-    if (int st = launch_fp8_product(p, ws + L.h, FT_DTYPE_F32, ws + L.product, err, s)) return st;
-    float* ms = reinterpret_cast<float*>(ws + L.ms);
-    if (int st = launch_quantize_fp8(ws + L.h, FT_DTYPE_F32, ws + L.mq, ms, n_slots, n_inter, true, act_kind, s)) return st;
+    if (L.gated) {
+        p.mid = ws + L.mq;
+        p.mid_scales = ms;
+        p.mid_pitch = fp8_scale_pitch(n_inter);
+        p.act_kind = act_kind;
+        if (int st = launch_fp8_product(p, nullptr, FT_DTYPE_F32, err, s)) return st;
+        p.mid = nullptr;
+        p.ordered = true;
+        p.scale_pitch = fp8_scale_pitch(n_inter);
+    } else {
+        if (int st = launch_fp8_product(p, ws + L.h, FT_DTYPE_F32, err, s)) return st;
+        if (int st = launch_quantize_fp8(ws + L.h, FT_DTYPE_F32, ws + L.mq, ms, n_slots, n_inter, true, act_kind, s)) return st;
+        p.ordered = false;
+        p.scale_pitch = static_cast<int32_t>(fp8_blocks(n_inter));
+    }
+    // second product
     p.weights = static_cast<const uint8_t*>(w2);
     p.w_scales = s2;
     p.act = ws + L.mq;
@@ -338,7 +402,9 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
     p.act_rows = n_slots;
     p.nrows = hidden;
     p.ncols = n_inter;
-    if (int st = launch_fp8_product(p, ws + L.rows, FT_DTYPE_BF16, ws + L.product, err, s)) return st;
+    if (L.spread && !L.gated)
+        if (int st = launch_fp8_order_rows(&p, ws + L.oq, reinterpret_cast<float*>(ws + L.os), s)) return st;
+    if (int st = launch_fp8_product(p, ws + L.rows, FT_DTYPE_BF16, err, s)) return st;
     return launch_combine(ws + L.rows, FT_DTYPE_BF16, topk_weights, nullptr, y, x_dtype, tokens, top_k, hidden, s);
 }
 

@@ -164,17 +164,48 @@ int launch_quantize_fp8(const void* x, int dtype, uint8_t* codes, float* scales,
 int launch_combine(const void* rows, int rows_dtype, const float* weights, const void* add, void* y, int y_dtype,
                    int64_t tokens, int32_t top_k, int64_t ncols, cudaStream_t s);
 
+// The same into router order: row r of x goes to rows pos[r * k .. r * k + k - 1] (-1:
+// none) of codes and scales (rows of scales `pitch` apart).  x fp16 or bf16.
+int launch_quantize_fp8_spread(const void* x, int dtype, uint8_t* codes, float* scales, int64_t tokens, int64_t ncols,
+                               const int32_t* pos, int32_t k, int32_t pitch, cudaStream_t s);
+
+// Router order (fp8_route.cu); fp8_route_ok: sizes that it takes.  pos may be null.
+bool fp8_route_ok(int64_t n_slots, int32_t n_experts);
+size_t fp8_route_scratch(int64_t n_slots, int32_t n_experts);
+int launch_fp8_route(const int32_t* ids, int64_t n_slots, int32_t n_experts, int32_t tile, int32_t* hist, int32_t* offsets,
+                     int32_t* tiles, int32_t* perm, int32_t* pos, cudaStream_t s);
+int launch_fp8_invert(const int32_t* perm, const int32_t* n_routed, int64_t n_slots, int32_t* pos, cudaStream_t s);
+
+// Slots in router order, in the caller's workspace.
+struct Fp8Order {
+    int32_t *offsets, *tiles, *perm, *pos, *hist, *counts;
+    uint32_t* err;        // the general router's own flags: ids of -1 are no error here
+};
+size_t fp8_order_layout(uint8_t* base, int64_t n_slots, int32_t n_experts, bool with_pos, Fp8Order* o);   // bytes
+int launch_fp8_order(const int32_t* ids, int64_t n_slots, int32_t n_experts, const Fp8Order& o, cudaStream_t s);
+
 struct Fp8Product {
     const uint8_t* weights;     // [n_experts][nrows][ncols] e4m3
     const float* w_scales;      // [n_experts][ceil(nrows / 128)][ceil(ncols / 128)]
-    const uint8_t* act;         // [rows][ncols] e4m3
-    const float* act_scales;    // [rows][ceil(ncols / 128)]
+    const uint8_t* act;         // [act_rows][ncols] e4m3
+    const float* act_scales;    // [act_rows], rows scale_pitch apart
     const int32_t* ids;         // [n_slots] expert of each slot, -1: none; nullptr: dense (one matrix)
+    const Fp8Order* order;      // router order of ids (nullptr: dense)
     int64_t n_slots, act_rows, nrows, ncols;
-    int32_t act_div;            // activation row of slot s: s / act_div
-    int32_t n_experts;
+    int32_t act_div;            // activation row of slot s: s / act_div (not `ordered`)
+    int32_t n_experts, scale_pitch;
+    bool ordered;               // act rows and scales lie in router order
+    // gated (nrows = 2 n_inter, n_inter % 128 == 0): instead of out, the e4m3 codes
+    // [routed][n_inter] and scales (rows mid_pitch apart) of act(gate) * up, in router order
+    uint8_t* mid;
+    float* mid_scales;
+    int32_t mid_pitch, act_kind;
 };
-size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts, int64_t ncols);   // routed products
-int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* workspace, uint32_t* err, cudaStream_t s);
+int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
+// Copies the rows of p to router order (codes, scales: room for n_slots rows) and makes p `ordered`.
+int launch_fp8_order_rows(Fp8Product* p, uint8_t* codes, float* scales, cudaStream_t s);
+// Whether a batch's rows should be copied to router order, and the pitch of scales there.
+bool fp8_copies_rows(int64_t n_slots, int32_t n_experts);
+inline int32_t fp8_scale_pitch(int64_t ncols) { return static_cast<int32_t>(((ncols + 127) / 128 + 3) / 4 * 4); }
 
 }  // namespace ft

@@ -65,8 +65,9 @@ struct Pair {
     static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
     static constexpr int OFF_SCALE = OFF_OUT + N_DRAIN_WARPS * 32 * STAGE_ROW;
     static constexpr int SCALE_RING = 4;           // groups of four blocks' scales in flight
-    static constexpr int OFF_BAR = OFF_SCALE + SCALE_RING * (N_DRAIN_WARPS * 32 + N_DRAIN_WARPS) * 16;
-    static constexpr int N_BARS = 2 * STAGES + 8;
+    static constexpr int OFF_BAR = OFF_SCALE + SCALE_RING * (N_DRAIN_WARPS * 32 + 2 * N_DRAIN_WARPS) * 16 + 4 * BM * 4;
+    static constexpr int OFF_AMAX = OFF_BAR - 4 * BM * 4;       // [tile parity][half][slot], gated
+    static constexpr int N_BARS = 2 * STAGES + 8 + 4;
     static constexpr int OFF_TMEM = OFF_BAR + N_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;    // + alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -86,6 +87,11 @@ struct PairArgs {
     bool scale_words;            // four neighbouring activation scales from a multiple of 4 on are a 16-byte word
     bool ordered;                // act rows and scales lie in router order
     bool wide;                   // the rows of out are whole 16-byte words
+    // gated: the weight rows are n_inter gate rows and n_inter up rows; a tile is 128 of
+    // each, and the epilogue writes codes and scales of act(gate) * up in router order
+    uint8_t* mid;
+    float* mid_scales;
+    int32_t n_inter, mid_pitch, act_kind;
 };
 
 struct PairTile {
@@ -165,7 +171,9 @@ __device__ __forceinline__ void zero_unrouted(const PairArgs& a, TO* out, int64_
 // even when an older one is wanted: with three blocks in flight in registers the
 // products of a block waited 100 cycles.
 template <int STEP>
-__device__ __forceinline__ float4* ring_at(float4* ring, int32_t g) { return ring + g % Pair::SCALE_RING * STEP; }
+__device__ __forceinline__ float4* ring_at(float4* ring, int32_t g) {
+    return ring + g % Pair::SCALE_RING * STEP;
+}
 
 __device__ __forceinline__ void copy_async4(uint32_t dst, const float* src, int32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -173,11 +181,12 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const float* src, int3
 
 // Starts the copies of group g (blocks past the row's end arrive as 0) and closes
 // their group of asynchronous copies; groups past the last one close empty.
+template <bool GATED>
 __device__ __forceinline__ void copy_scales(const PairArgs& a, const float* sa, const float* sw, int32_t g, float4* ring_a,
                                             float4* ring_w) {
     const int32_t b = 4 * g;
     if (b < a.nb) {
-        const uint32_t da = smem_u32(ring_at<256>(ring_a, g)), dw = smem_u32(ring_at<8>(ring_w, g));
+        const uint32_t da = smem_u32(ring_at<256>(ring_a, g)), dw = smem_u32(ring_at<16>(ring_w, g));
         if (a.scale_words) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(da), "l"(sa + b) : "memory");
         } else {
@@ -186,11 +195,24 @@ __device__ __forceinline__ void copy_scales(const PairArgs& a, const float* sa, 
         }
         const int32_t i = static_cast<int32_t>(lane_id());
         if (i < 4) copy_async4(dw + 4 * i, sw + min(b + i, a.nb - 1), b + i < a.nb ? 4 : 0);
+        if constexpr (GATED) {      // the up rows' scales lie n_inter / 128 rows of blocks further
+            if (i >= 4 && i < 8)
+                copy_async4(dw + 8 * 16 + 4 * (i - 4), sw + static_cast<int64_t>(a.n_inter / kFp8Block) * a.nb + min(b + i - 4, a.nb - 1),
+                            b + i - 4 < a.nb ? 4 : 0);
+        }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-template <typename TO, bool GATHER>
+// g -> act(g) * up (see act_mul in the quantizer): the fast exponential and quotient are
+// within a few units in the last place, 2^-20 of what a code's rounding (2^-4) moves.
+__device__ __forceinline__ float act_mul_fast(float g, float up, int32_t kind) {
+    const float z = kind == FT_ACT_SILU ? g : 1.5957691216057308f * fmaf(0.044715f * g, g * g, g);
+    return __fdividef(g, 1.0f + __expf(-z)) * up;
+}
+
+// GATED: TO is unused.
+template <typename TO, bool GATHER, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     moe_fp8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const PairArgs a, TO* __restrict__ out) {
@@ -202,6 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     uint64_t* empty = full + C::STAGES;
     uint64_t* acc_full = empty + C::STAGES;      // [half][buffer]
     uint64_t* acc_empty = acc_full + 4;
+    uint64_t* amax_bar = acc_empty + 4;          // gated: the two warps of 32 slots have stored their maxima
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
 
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id(), rank = cluster_ctarank();
@@ -215,6 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         for (int i = 0; i < 4; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], C::N_DRAIN_WARPS);         // the leader's: a warpgroup of both CTAs
+            mbar_init(&amax_bar[i], 2);
         }
         fence_mbar_init();
     }
@@ -258,7 +282,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             // half h of the tile (weight rows 128 h ..): this CTA's part of its MMA's columns
             const int32_t halves = t.width > C::CW ? 2 : 1;
             const int64_t row0 = static_cast<int64_t>(t.e) * a.nrows + t.r0;
-            const int32_t wy = static_cast<int32_t>(row0 + lane * C::CW + rank * (t.cols(static_cast<int32_t>(lane)) / 2));
+            // gated: columns 0 .. 63 of half h are gate rows 64 h .., columns 64 .. 127 the same up rows
+            const int32_t wy = GATED ? static_cast<int32_t>(static_cast<int64_t>(t.e) * a.nrows + t.r0 / 2 + lane * C::BOX + rank * a.n_inter)
+                                     : static_cast<int32_t>(row0 + lane * C::CW + rank * (t.cols(static_cast<int32_t>(lane)) / 2));
             const uint32_t bytes = 2 * halves * C::BOX * kFp8Block +
                                    ((mine + PER - 1) / PER + (other + PER - 1) / PER) * PER * kFp8Block;
             for (int32_t b = 0; b < nb; ++b, ++it) {
@@ -318,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (a.ids) {
+    } else if (!GATED && a.ids) {
         zero_unrouted<TO>(a, out, blockIdx.x, gridDim.x);
     }
     } else {
@@ -329,7 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         uint8_t* stage = smem + C::OFF_OUT + warp * (32 * C::STAGE_ROW);
         // this thread's word of the ring of activation scales, and its warp's of the ring of weight scales
         float4* ring_a = reinterpret_cast<float4*>(smem + C::OFF_SCALE) + threadIdx.x;
-        float4* ring_w = reinterpret_cast<float4*>(smem + C::OFF_SCALE) + C::SCALE_RING * 256 + warp;
+        float4* ring_w = reinterpret_cast<float4*>(smem + C::OFF_SCALE) + C::SCALE_RING * 256 + warp;     // + 8: the up rows'
+        float* amax_of = reinterpret_cast<float*>(smem + C::OFF_AMAX);                                     // [tile parity][half][slot]
+        uint32_t tiles_done = 0;         // gated: tiles that this warp had slots of
         uint32_t it = 0;                 // blocks of this half
         bool ok = true;
         for (int64_t w = w0; w < total && ok; w += dw) {
@@ -346,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 slot = a.perm ? a.perm[p] : p;
                 sa += static_cast<int64_t>(a.ordered ? p : slot / a.act_div) * a.scale_pitch;
             }
-            const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + r0 / kFp8Block) * nb;
+            const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + (GATED ? t.r0 / 2 : r0) / kFp8Block) * nb;
             uint64_t acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = 0;
@@ -361,8 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             }
             // the scales of the first blocks: four at a time through a ring in shared memory
 #pragma unroll
-            for (int i = 0; i < C::SCALE_RING - 1; ++i) copy_scales(a, sa, sw, i, ring_a, ring_w);
-            float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < C::SCALE_RING - 1; ++i) copy_scales<GATED>(a, sa, sw, i, ring_a, ring_w);
+            float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, su[GATED ? 4 : 1] = {};      // gated: the up rows' beside the gate rows'
             // 16 columns are on their way from tensor memory while the 16 before them are added
             uint32_t v[2][16];
             if (!mbar_wait_warp(&acc_full[2 * h + (it & 1u)], (it >> 1) & 1u, a.err)) { ok = false; break; }
@@ -372,19 +400,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 if ((b & 3) == 0) {
                     asm volatile("cp.async.wait_group %0;" ::"n"(C::SCALE_RING - 2) : "memory");
                     __syncwarp();
-                    const float4 x = *ring_at<256>(ring_a, b >> 2), y = *ring_at<8>(ring_w, b >> 2);
+                    const float4 x = *ring_at<256>(ring_a, b >> 2), y = *ring_at<16>(ring_w, b >> 2);
                     sc[0] = x.x * y.x;
                     sc[1] = x.y * y.y;
                     sc[2] = x.z * y.z;
                     sc[3] = x.w * y.w;
+                    if constexpr (GATED) {
+                        const float4 z = *ring_at<16>(ring_w + 8, b >> 2);
+                        su[0] = x.x * z.x;
+                        su[1] = x.y * z.y;
+                        su[2] = x.z * z.z;
+                        su[3] = x.w * z.w;
+                    }
                     __syncwarp();      // before the slot is filled again
-                    copy_scales(a, sa, sw, (b >> 2) + C::SCALE_RING - 1, ring_a, ring_w);
+                    copy_scales<GATED>(a, sa, sw, (b >> 2) + C::SCALE_RING - 1, ring_a, ring_w);
                 }
                 const float scale = sc[0];
                 sc[0] = sc[1];
                 sc[1] = sc[2];
                 sc[2] = sc[3];
-                const uint64_t s2 = pack2(scale, scale);
+                const uint64_t s2 = pack2(scale, scale), u2 = GATED ? pack2(su[0], su[0]) : s2;
+                if constexpr (GATED) {
+                    su[0] = su[1];
+                    su[1] = su[2];
+                    su[2] = su[3];
+                }
                 const uint32_t nd = 2 * h + ((it + 1) & 1u), nph = ((it + 1) >> 1) & 1u;      // the next block's accumulator
                 bool ready = false;
 #pragma unroll
@@ -405,11 +445,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fma2(acc[8 * j + i], v[j & 1][2 * i], v[j & 1][2 * i + 1], s2);
+                    for (int i = 0; i < 8; ++i) fma2(acc[8 * j + i], v[j & 1][2 * i], v[j & 1][2 * i + 1], j < C::CW / 32 ? s2 : u2);
                 }
                 if (!ok) break;
             }
             if (!ok) break;
+            if constexpr (GATED) {
+                // this thread's 64 of the slot's 128 values; the other half's thread has the rest
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < C::CW / 4; ++i) {
+                    const float2 g = unpack2(acc[i]), u = unpack2(acc[C::CW / 4 + i]);
+                    const float x = act_mul_fast(g.x, u.x, a.act_kind), y = act_mul_fast(g.y, u.y, a.act_kind);
+                    amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+                    acc[i] = pack2(x, y);
+                }
+                float* both = amax_of + (tiles_done & 1u) * (2 * C::BM);
+                both[h * C::BM + m] = amax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&amax_bar[warp & 3u]);
+                if (!mbar_wait_warp(&amax_bar[warp & 3u], tiles_done & 1u, a.err)) { ok = false; break; }
+                amax = fmaxf(amax, both[(h ^ 1u) * C::BM + m]);      // written again two tiles on, when the other warp has read it
+                ++tiles_done;
+                // a reciprocal instead of a quotient moves a code only where it lies within 2^-23 of a tie;
+                // below 1e-30 it could overflow, and the block's values count as 0
+                const float scale = amax < 1e-30f ? 0.0f : __fdiv_rn(amax, kFp8Max);
+                const float inv = amax < 1e-30f ? 0.0f : __fdiv_rn(kFp8Max, amax);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t q[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = unpack2(acc[8 * i + 2 * k]), y = unpack2(acc[8 * i + 2 * k + 1]);
+                        q[k] = e4m3x4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * 80 + 16 * i) = make_uint4(q[0], q[1], q[2], q[3]);
+                }
+                const int32_t p0 = t.first(rank) + static_cast<int32_t>(lane0), n = min(32, mine - static_cast<int32_t>(lane0));
+                if (h == 0 && m < mine) a.mid_scales[static_cast<int64_t>(p0 + static_cast<int32_t>(lane)) * a.mid_pitch + t.r0 / 2 / kFp8Block] = scale;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {      // eight rows at a time, 64 bytes of each
+                    const int32_t r = 8 * i + static_cast<int32_t>(lane >> 2);
+                    if (r < n)
+                        *reinterpret_cast<uint4*>(a.mid + static_cast<int64_t>(p0 + r) * a.n_inter + t.r0 / 2 + h * 64 + (lane & 3u) * 16) =
+                            *reinterpret_cast<const uint4*>(stage + r * 80 + (lane & 3u) * 16);
+                }
+                __syncwarp();
+                continue;
+            }
             // out: 256 bytes of each of the warp's rows at a time go through shared memory,
             // so that a row leaves in whole lines
             constexpr int PER = 16 / static_cast<int>(sizeof(TO)), PASS = 256 / static_cast<int>(sizeof(TO));
@@ -477,41 +562,10 @@ namespace {
 // Routed slots per expert on average from which the rows are copied to router order first.
 constexpr int kGatherMean = 24;
 
-
-struct ProductWs {
-    size_t counts, offsets, perm, tiles, hist, err, rows, scales, total;
-};
-
-bool copies_rows(int64_t n_slots, int32_t n_experts) { return n_slots > static_cast<int64_t>(kGatherMean) * n_experts; }
-
-int32_t scale_pitch(int64_t ncols) { return static_cast<int32_t>((fp8_blocks(ncols) + 3) / 4 * 4); }
-
-ProductWs product_ws(int64_t n_slots, int32_t n_experts, int64_t ncols) {
-    ProductWs L{};
-    size_t o = 0;
-    auto take = [&o](size_t bytes) {
-        const size_t at = o;
-        o = (o + bytes + 255) & ~size_t(255);
-        return at;
-    };
-    const size_t E = static_cast<size_t>(n_experts), S = static_cast<size_t>(n_slots);
-    L.counts = take(4 * E);
-    L.offsets = take(4 * (E + 1));
-    L.perm = take(4 * S);
-    L.tiles = take(4 * (E + 1));
-    L.hist = take(4 * static_cast<size_t>(route_chunks(n_slots)) * E);
-    L.err = take(4);       // the router's own flags: ids of -1 are no error here
-    const size_t copied = copies_rows(n_slots, n_experts) ? S : 0;
-    L.rows = take(copied * static_cast<size_t>(ncols));
-    L.scales = take(copied * static_cast<size_t>(scale_pitch(ncols)) * 4);
-    L.total = o;
-    return L;
-}
-
-template <typename TO, bool GATHER>
-int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs& a, TO* out, int grid, cudaStream_t s) {
+template <typename TO, bool GATHER, bool GATED>
+int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs& a, void* out, int grid, cudaStream_t s) {
     using C = Pair;
-    const void* k = reinterpret_cast<const void*>(moe_fp8_pair_kernel<TO, GATHER>);
+    const void* k = reinterpret_cast<const void*>(moe_fp8_pair_kernel<TO, GATHER, GATED>);
     static int regs = 0;     // of this instantiation: with fewer than LAUNCH_REGS the split of registers would never end
     if (regs == 0) {
         cudaFuncAttributes at{};
@@ -522,19 +576,65 @@ int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs
     if (regs * C::THREADS < C::DRAIN_REGS * 256 + C::OTHER_REGS * 128)
         return fail(FT_ERR_LAUNCH, "moe_fp8_pair_kernel was compiled with %d registers, %d are needed", regs, C::LAUNCH_REGS);
     if (int st = set_smem_limit(k, C::SMEM_BYTES)) return st;
-    moe_fp8_pair_kernel<TO, GATHER><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, out);
+    moe_fp8_pair_kernel<TO, GATHER, GATED><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, static_cast<TO*>(out));
     return check_launch("moe_fp8_pair_kernel", dim3(grid), dim3(C::THREADS), C::SMEM_BYTES);
 }
 
 }  // namespace
 
-size_t fp8_product_workspace(int64_t n_slots, int32_t n_experts, int64_t ncols) {
-    return product_ws(n_slots, n_experts, ncols).total;
+bool fp8_copies_rows(int64_t n_slots, int32_t n_experts) { return n_slots > static_cast<int64_t>(kGatherMean) * n_experts; }
+
+size_t fp8_order_layout(uint8_t* base, int64_t n_slots, int32_t n_experts, bool with_pos, Fp8Order* o) {
+    size_t at = 0;
+    auto take = [&at, base](size_t words) {
+        int32_t* p = reinterpret_cast<int32_t*>(base + at);
+        at = (at + 4 * words + 255) & ~size_t(255);
+        return p;
+    };
+    const size_t E = static_cast<size_t>(n_experts), S = static_cast<size_t>(n_slots);
+    const size_t hist = fp8_route_ok(n_slots, n_experts) ? fp8_route_scratch(n_slots, n_experts) / 4
+                                                         : static_cast<size_t>(route_chunks(n_slots)) * E;
+    o->offsets = take(E + 1);
+    o->tiles = take(E + 1);
+    o->perm = take(S);
+    o->pos = with_pos ? take(S) : nullptr;
+    o->hist = take(hist);
+    o->counts = take(E);
+    o->err = reinterpret_cast<uint32_t*>(take(1));
+    return at;
 }
 
-int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* workspace, uint32_t* err, cudaStream_t s) {
+int launch_fp8_order(const int32_t* ids, int64_t n_slots, int32_t n_experts, const Fp8Order& o, cudaStream_t s) {
+    constexpr int tile = 2 * Pair::BM;
+    if (fp8_route_ok(n_slots, n_experts))
+        return launch_fp8_route(ids, n_slots, n_experts, tile, o.hist, o.offsets, o.tiles, o.perm, o.pos, s);
+    RouteBuffers rb{};
+    rb.counts = o.counts;
+    rb.offsets = o.offsets;
+    rb.perm = o.perm;
+    rb.hist = o.hist;
+    rb.tiles_gemm = o.tiles;
+    rb.err = o.err;
+    if (int st = launch_route(ids, n_slots, n_experts, rb, tile, tile, nullptr, 0, s)) return st;
+    return o.pos ? launch_fp8_invert(o.perm, o.offsets + n_experts, n_slots, o.pos, s) : FT_OK;
+}
+
+int launch_fp8_order_rows(Fp8Product* p, uint8_t* codes, float* scales, cudaStream_t s) {
+    const int32_t pitch = fp8_scale_pitch(p->ncols), nb = static_cast<int32_t>(fp8_blocks(p->ncols));
+    const dim3 grid(static_cast<unsigned>((p->n_slots + 7) / 8));
+    order_rows_kernel<<<grid, 256, 0, s>>>(p->act, p->act_scales, p->order->perm, p->order->offsets + p->n_experts, p->act_div,
+                                           static_cast<int32_t>(p->ncols / 16), nb, pitch, reinterpret_cast<uint4*>(codes), scales);
+    p->act = codes;
+    p->act_scales = scales;
+    p->act_rows = p->n_slots;
+    p->scale_pitch = pitch;
+    p->ordered = true;
+    return check_launch("order_rows_kernel", grid, dim3(256), 0);
+}
+
+int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, uint32_t* err, cudaStream_t s) {
     using C = Pair;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const bool gated = p.mid != nullptr, boxes = p.ordered || !p.ids;      // rows that lie in order arrive in boxes
     PairArgs a{};
     a.act_scales = p.act_scales;
     a.w_scales = p.w_scales;
@@ -546,59 +646,37 @@ int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, void* work
     a.nb = static_cast<int32_t>(fp8_blocks(p.ncols));
     a.row_blocks = static_cast<int32_t>(fp8_blocks(p.nrows));
     a.row_tiles = static_cast<int32_t>((p.nrows + C::BN - 1) / C::BN);
-    const int out_bytes = out_dtype == FT_DTYPE_F32 ? 4 : 2;
-    a.wide = p.nrows * out_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    ProductWs L{};
+    a.scale_pitch = p.scale_pitch;
+    a.scale_words = p.scale_pitch % 4 == 0 && reinterpret_cast<uintptr_t>(p.act_scales) % 16 == 0;
+    a.ordered = boxes;
+    a.wide = p.nrows * (out_dtype == FT_DTYPE_F32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    a.mid = p.mid;
+    a.mid_scales = p.mid_scales;
+    a.n_inter = static_cast<int32_t>(p.nrows / 2);
+    a.mid_pitch = p.mid_pitch;
+    a.act_kind = p.act_kind;
     if (p.ids) {
-        L = product_ws(p.n_slots, p.n_experts, p.ncols);
-        RouteBuffers rb{};
-        rb.counts = reinterpret_cast<int32_t*>(ws + L.counts);
-        rb.offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
-        rb.perm = reinterpret_cast<int32_t*>(ws + L.perm);
-        rb.hist = reinterpret_cast<int32_t*>(ws + L.hist);
-        rb.tiles_gemm = reinterpret_cast<int32_t*>(ws + L.tiles);
-        rb.err = reinterpret_cast<uint32_t*>(ws + L.err);
-        if (int st = launch_route(p.ids, p.n_slots, p.n_experts, rb, 2 * C::BM, 2 * C::BM, nullptr, 0, s)) return st;
         a.ids = p.ids;
-        a.perm = rb.perm;
-        a.offsets = rb.offsets;
-        a.tiles = rb.tiles_gemm;
+        a.perm = p.order->perm;
+        a.offsets = p.order->offsets;
+        a.tiles = p.order->tiles;
     }
-    const uint8_t* act = p.act;
-    int64_t act_rows = p.act_rows;
-    a.scale_pitch = a.nb;
-    const bool copies = p.ids && copies_rows(p.n_slots, p.n_experts);
-    if (copies) {
-        a.scale_pitch = scale_pitch(p.ncols);
-        const dim3 grid(static_cast<unsigned>((p.n_slots + 7) / 8));
-        order_rows_kernel<<<grid, 256, 0, s>>>(p.act, p.act_scales, a.perm, a.offsets + p.n_experts, p.act_div,
-                                               static_cast<int32_t>(p.ncols / 16), a.nb, a.scale_pitch,
-                                               reinterpret_cast<uint4*>(ws + L.rows), reinterpret_cast<float*>(ws + L.scales));
-        if (int st = check_launch("order_rows_kernel", grid, dim3(256), 0)) return st;
-        act = ws + L.rows;
-        a.act_scales = reinterpret_cast<const float*>(ws + L.scales);
-        act_rows = p.n_slots;
-    }
-    a.scale_words = a.scale_pitch % 4 == 0 && reinterpret_cast<uintptr_t>(a.act_scales) % 16 == 0;
-    a.ordered = copies || !p.ids;
     CUtensorMap wmap, xmap;
     if (int st = encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weights, p.ncols,
                            static_cast<uint64_t>(p.n_experts) * p.nrows, p.ncols, kFp8Block, C::BOX,
                            CU_TENSOR_MAP_SWIZZLE_128B, "FP8 weights"))
         return st;
-    if (int st = encode_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, act, p.ncols, act_rows, p.ncols, kFp8Block,
-                           a.ordered ? C::ROW_BOX : 1, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
+    if (int st = encode_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.act, p.ncols, p.act_rows, p.ncols, kFp8Block,
+                           boxes ? C::ROW_BOX : 1, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
         return st;
     const int64_t slot_tiles = (p.n_slots + 2 * C::BM - 1) / (2 * C::BM) + (p.ids ? (p.n_experts < p.n_slots ? p.n_experts : p.n_slots) : 0);
     const int64_t pairs = slot_tiles * a.row_tiles, most = sm_count() / 2;
     const int grid = 2 * static_cast<int>(pairs < most ? pairs : most);
-    if (out_dtype == FT_DTYPE_F32) {
-        float* o = static_cast<float*>(out);
-        return a.ordered ? launch_pair<float, false>(wmap, xmap, a, o, grid, s) : launch_pair<float, true>(wmap, xmap, a, o, grid, s);
-    }
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-    return a.ordered ? launch_pair<__nv_bfloat16, false>(wmap, xmap, a, o, grid, s)
-                     : launch_pair<__nv_bfloat16, true>(wmap, xmap, a, o, grid, s);
+    if (gated) return boxes ? launch_pair<float, false, true>(wmap, xmap, a, nullptr, grid, s) : launch_pair<float, true, true>(wmap, xmap, a, nullptr, grid, s);
+    if (out_dtype == FT_DTYPE_F32)
+        return boxes ? launch_pair<float, false, false>(wmap, xmap, a, out, grid, s) : launch_pair<float, true, false>(wmap, xmap, a, out, grid, s);
+    return boxes ? launch_pair<__nv_bfloat16, false, false>(wmap, xmap, a, out, grid, s)
+                 : launch_pair<__nv_bfloat16, true, false>(wmap, xmap, a, out, grid, s);
 }
 
 }  // namespace ft

@@ -25,11 +25,13 @@ __device__ __forceinline__ float act_mul_f32(float g, float up, int kind) {
     return __fdiv_rn(g, 1.0f + expf(-z)) * up;
 }
 
-// GATED: x holds rows of 2 ncols values, gate then up.
-template <typename T, bool GATED>
+// GATED: x holds rows of 2 ncols values, gate then up.  SPREAD: row r is a token's, and
+// its codes and scales go to the rows pos[r * k ..] (-1: none) of the outputs.
+template <typename T, bool GATED, bool SPREAD>
 __global__ void __launch_bounds__(32 * kQuantWarps)
     quantize_fp8_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, float* __restrict__ scales,
-                        int64_t n_blocks, int32_t nb, int64_t ncols, int kind) {
+                        int64_t n_blocks, int32_t nb, int64_t ncols, int kind, const int32_t* __restrict__ pos, int32_t k,
+                        int32_t pitch) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5);
     if (i >= n_blocks) return;
     const int64_t row = i / nb;
@@ -56,24 +58,32 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     if (__any_sync(0xFFFFFFFFu, nan)) amax = NAN;
     const float scale = __fdiv_rn(amax, kFp8Max);
-    if (lane_id() == 0) scales[i] = scale;
-    if (c < ncols) {
-        uint32_t q = 0;
-        if (scale != 0.0f)
-            q = e4m3x4(__fdiv_rn(v[0], scale), __fdiv_rn(v[1], scale), __fdiv_rn(v[2], scale), __fdiv_rn(v[3], scale));
-        *reinterpret_cast<uint32_t*>(codes + row * ncols + c) = q;
+    uint32_t q = 0;
+    if (c < ncols && scale != 0.0f)
+        q = e4m3x4(__fdiv_rn(v[0], scale), __fdiv_rn(v[1], scale), __fdiv_rn(v[2], scale), __fdiv_rn(v[3], scale));
+    if constexpr (SPREAD) {
+        for (int32_t j = 0; j < k; ++j) {
+            const int64_t p = __ldg(pos + row * k + j);
+            if (p >= 0) {
+                if (c < ncols) *reinterpret_cast<uint32_t*>(codes + p * ncols + c) = q;
+                if (lane_id() == 0) scales[p * pitch + (i - row * nb)] = scale;
+            }
+        }
+    } else {
+        if (lane_id() == 0) scales[i] = scale;
+        if (c < ncols) *reinterpret_cast<uint32_t*>(codes + row * ncols + c) = q;
     }
 }
 
-template <typename T, bool GATED>
+template <typename T, bool GATED, bool SPREAD = false>
 static int launch_typed(const void* x, uint8_t* codes, float* scales, int64_t rows, int64_t ncols, int kind,
-                        cudaStream_t s) {
+                        cudaStream_t s, const int32_t* pos = nullptr, int32_t k = 0, int32_t pitch = 0) {
     const int64_t nb = fp8_blocks(ncols), n_blocks = rows * nb;
     const int64_t ctas = (n_blocks + kQuantWarps - 1) / kQuantWarps;
     if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "rows * ncols too large for one launch");
     const dim3 grid(static_cast<unsigned>(ctas)), block(32 * kQuantWarps);
-    quantize_fp8_kernel<T, GATED><<<grid, block, 0, s>>>(static_cast<const T*>(x), codes, scales, n_blocks,
-                                                        static_cast<int32_t>(nb), ncols, kind);
+    quantize_fp8_kernel<T, GATED, SPREAD><<<grid, block, 0, s>>>(static_cast<const T*>(x), codes, scales, n_blocks,
+                                                                static_cast<int32_t>(nb), ncols, kind, pos, k, pitch);
     return check_launch("quantize_fp8_kernel", grid, block, 0);
 }
 
@@ -88,6 +98,13 @@ int launch_quantize_fp8(const void* x, int dtype, uint8_t* codes, float* scales,
                      : launch_typed<__half, false>(x, codes, scales, rows, ncols, kind, s);
     return gated ? launch_typed<__nv_bfloat16, true>(x, codes, scales, rows, ncols, kind, s)
                  : launch_typed<__nv_bfloat16, false>(x, codes, scales, rows, ncols, kind, s);
+}
+
+int launch_quantize_fp8_spread(const void* x, int dtype, uint8_t* codes, float* scales, int64_t tokens, int64_t ncols,
+                               const int32_t* pos, int32_t k, int32_t pitch, cudaStream_t s) {
+    if (dtype == FT_DTYPE_F16)
+        return launch_typed<__half, false, true>(x, codes, scales, tokens, ncols, FT_ACT_SILU, s, pos, k, pitch);
+    return launch_typed<__nv_bfloat16, false, true>(x, codes, scales, tokens, ncols, FT_ACT_SILU, s, pos, k, pitch);
 }
 
 }  // namespace ft
