@@ -164,31 +164,35 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
     p.nrows = nrows;
     p.ncols = ncols;
     p.n_experts = n_experts;
+    const int width = fp8_tile_width(n_slots, n_experts);
     if (!dense) {
         p.ids = ids;
         p.order = &L.order;
-        if (int st = launch_fp8_order(ids, n_slots, n_experts, L.order, s)) return st;
+        if (!fp8_orders_itself(n_slots, n_experts, width))
+            if (int st = launch_fp8_order(ids, n_slots, n_experts, width, L.order, s)) return st;
         if (fp8_copies_rows(n_slots, n_experts))
             if (int st = launch_fp8_order_rows(&p, ws + L.rows, reinterpret_cast<float*>(ws + L.scales), s)) return st;
     }
-    return launch_fp8_product(p, out, out_dtype, err, s);
+    return launch_fp8_product(p, width, out, out_dtype, err, s);
 }
 
 // Workspace of a layer: router order; x's codes and scales, in router order where a
 // batch has many slots per expert (`spread`), else by token; the gated values' codes and
-// scales in router order; where the products cannot quantize them themselves
-// (n_inter % 128 != 0) the first product's fp32 rows, codes by slot and (`spread`) copies
+// scales in router order; where the first product does not quantize them itself
+// (n_inter % 128 != 0, or few slots per expert) its fp32 rows, codes by slot and (`spread`) copies
 // of them in router order; the second product's bf16 rows.
 struct LayerWs {
     Fp8Order order;
     size_t xq, xs, mq, ms, h, oq, os, rows, total;
+    int width;
     bool spread, gated;
 };
 
 LayerWs layer_ws(uint8_t* base, int64_t tokens, int64_t n_slots, int32_t n_experts, int64_t hidden, int64_t n_inter) {
     LayerWs L{};
     L.spread = fp8_copies_rows(n_slots, n_experts);
-    L.gated = n_inter % kFp8Block == 0;
+    L.width = fp8_tile_width(n_slots, n_experts);
+    L.gated = L.width == 256 && n_inter % kFp8Block == 0;
     size_t at = al256(fp8_order_layout(base, n_slots, n_experts, L.spread, &L.order));
     const size_t S = static_cast<size_t>(n_slots), X = L.spread ? S : static_cast<size_t>(tokens);
     L.xq = take_bytes(&at, X * hidden);
@@ -353,7 +357,8 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
 
     const GateParams g{tokens, n_experts, top_k, score, n_groups, topk_groups, group_top, renormalize, scale, bias};
     if (int st = launch_gate(g, logits, logits_dtype, row_stride, topk_ids, topk_weights, s)) return st;
-    if (int st = launch_fp8_order(topk_ids, n_slots, n_experts, L.order, s)) return st;
+    if (!fp8_orders_itself(n_slots, n_experts, L.width))
+        if (int st = launch_fp8_order(topk_ids, n_slots, n_experts, L.width, L.order, s)) return st;
     float *xs = reinterpret_cast<float*>(ws + L.xs), *ms = reinterpret_cast<float*>(ws + L.ms);
     Fp8Product p{};
     p.ids = topk_ids;
@@ -383,12 +388,12 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
         p.mid_scales = ms;
         p.mid_pitch = fp8_scale_pitch(n_inter);
         p.act_kind = act_kind;
-        if (int st = launch_fp8_product(p, nullptr, FT_DTYPE_F32, err, s)) return st;
+        if (int st = launch_fp8_product(p, L.width, nullptr, FT_DTYPE_F32, err, s)) return st;
         p.mid = nullptr;
         p.ordered = true;
         p.scale_pitch = fp8_scale_pitch(n_inter);
     } else {
-        if (int st = launch_fp8_product(p, ws + L.h, FT_DTYPE_F32, err, s)) return st;
+        if (int st = launch_fp8_product(p, L.width, ws + L.h, FT_DTYPE_F32, err, s)) return st;
         if (int st = launch_quantize_fp8(ws + L.h, FT_DTYPE_F32, ws + L.mq, ms, n_slots, n_inter, true, act_kind, s)) return st;
         p.ordered = false;
         p.scale_pitch = static_cast<int32_t>(fp8_blocks(n_inter));
@@ -404,7 +409,7 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
     p.ncols = n_inter;
     if (L.spread && !L.gated)
         if (int st = launch_fp8_order_rows(&p, ws + L.oq, reinterpret_cast<float*>(ws + L.os), s)) return st;
-    if (int st = launch_fp8_product(p, ws + L.rows, FT_DTYPE_BF16, err, s)) return st;
+    if (int st = launch_fp8_product(p, L.width, ws + L.rows, FT_DTYPE_BF16, err, s)) return st;
     return launch_combine(ws + L.rows, FT_DTYPE_BF16, topk_weights, nullptr, y, x_dtype, tokens, top_k, hidden, s);
 }
 

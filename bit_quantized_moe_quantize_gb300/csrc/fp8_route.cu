@@ -12,12 +12,11 @@
 // less work than another launch, and places its slots: each of its eight warps
 // counts 128 of them, and equal ids in a step of 32 rank by lane, so that the
 // order never depends on timing.
-#include "fp8_common.cuh"
+#include "fp8_order.cuh"
 #include "ft_internal.h"
 
 namespace ft {
 
-constexpr int kChunk = 1024, kChunkThreads = 256, kChunkWarps = kChunkThreads / 32;
 constexpr int64_t kMostChunks = 256;
 constexpr int32_t kMostRouteExperts = 1024;
 
@@ -45,36 +44,6 @@ __global__ void __launch_bounds__(kChunkThreads)
         hist[static_cast<int64_t>(blockIdx.x) * n_experts + e] = count[e];
 }
 
-// Exclusive prefix of v[0 .. n) in shared memory by the whole CTA; returns the total.  part: 8 words.
-__device__ int32_t chunk_scan(int32_t* v, int32_t n, int32_t* part) {
-    const int32_t tid = threadIdx.x, per = (n + kChunkThreads - 1) / kChunkThreads;
-    const int32_t lo = min(n, tid * per), hi = min(n, lo + per);
-    const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
-    int32_t sum = 0;
-    for (int32_t i = lo; i < hi; ++i) sum += v[i];
-    int32_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= static_cast<uint32_t>(o)) inc += y;
-    }
-    if (lane == 31) part[warp] = inc;
-    __syncthreads();
-    int32_t before = 0, total = 0;
-    for (int w = 0; w < kChunkWarps; ++w) {
-        if (w < static_cast<int>(warp)) before += part[w];
-        total += part[w];
-    }
-    int32_t run = before + inc - sum;
-    for (int32_t i = lo; i < hi; ++i) {
-        const int32_t x = v[i];
-        v[i] = run;
-        run += x;
-    }
-    __syncthreads();
-    return total;
-}
-
 // hist == nullptr: one chunk, whose counts are the totals.
 __global__ void __launch_bounds__(kChunkThreads)
     fp8_place_kernel(const int32_t* __restrict__ ids, int32_t n_slots, int32_t n_experts, const int32_t* __restrict__ hist,
@@ -86,25 +55,10 @@ __global__ void __launch_bounds__(kChunkThreads)
     int32_t* total = before + n_experts;                 // [E] slots, then offsets
     int32_t* nt = total + n_experts;                     // [E] tiles
     int32_t* part = nt + n_experts;                      // [8]
-    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
     const int32_t E = n_experts, chunk = static_cast<int32_t>(blockIdx.x);
-    for (int32_t i = threadIdx.x; i < kChunkWarps * E; i += kChunkThreads) mine[i] = 0;
-    __syncthreads();
-    int32_t* count = mine + static_cast<int32_t>(warp) * E;
     int32_t id[4], rank[4];
-    const int32_t s0 = chunk * kChunk + static_cast<int32_t>(warp) * 128 + static_cast<int32_t>(lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int32_t s = s0 + 32 * i, e = s < n_slots ? ids[s] : -1;
-        id[i] = e >= 0 && e < E ? e : -1;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[i]);
-        uint32_t below;
-        asm("mov.u32 %0, %%lanemask_lt;" : "=r"(below));
-        rank[i] = id[i] >= 0 ? count[id[i]] + __popc(same & below) : 0;      // among the warp's slots
-        __syncwarp();
-        if (id[i] >= 0 && (same & below) == 0) count[id[i]] += __popc(same);
-        __syncwarp();
-    }
+    const int32_t s0 = chunk_rank(ids, chunk * kChunk, n_slots, E, mine, id, rank);
+    const int32_t* count = mine + static_cast<int32_t>(threadIdx.x >> 5) * E;
     if (hist) {
         for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) {
             int32_t b = 0, t = 0;
@@ -119,13 +73,8 @@ __global__ void __launch_bounds__(kChunkThreads)
         }
         __syncthreads();
     } else {
-        __syncthreads();
-        for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) {
-            int32_t t = 0;
-            for (int w = 0; w < kChunkWarps; ++w) t += mine[w * E + e];
-            before[e] = 0;
-            total[e] = t;
-        }
+        chunk_totals(mine, E, total);
+        for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) before[e] = 0;
         __syncthreads();
     }
     for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) nt[e] = (total[e] + tile - 1) / tile;
@@ -142,15 +91,9 @@ __global__ void __launch_bounds__(kChunkThreads)
             tiles[E] = n_tiles;
         }
     }
-    for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) {
-        int32_t at = total[e] + before[e];
-        for (int w = 0; w < kChunkWarps; ++w) {
-            const int32_t n = mine[w * E + e];
-            mine[w * E + e] = at;
-            at += n;
-        }
-    }
+    for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) total[e] += before[e];
     __syncthreads();
+    chunk_starts(mine, E, total);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int32_t s = s0 + 32 * i;

@@ -133,6 +133,43 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
         : "memory");
 }
 
+// Rows of slots without an expert are 0; ids that are neither -1 nor an expert raise the flag.
+template <typename TO>
+__device__ __forceinline__ void zero_unrouted(const int32_t* ids, int64_t n_slots, int32_t n_experts, int64_t nrows, uint32_t* err,
+                                              TO* out, int64_t warp, int64_t n_warps) {
+    for (int64_t s0 = warp * 32; s0 < n_slots; s0 += n_warps * 32) {
+        const int64_t s = s0 + lane_id();
+        const int32_t id = s < n_slots ? ids[s] : 0;
+        const bool none = id < 0 || id >= n_experts;
+        if (none && id != -1) atomicOr(err, FT_DEVERR_BAD_EXPERT_ID);
+        uint32_t left = __ballot_sync(0xFFFFFFFFu, none);
+        while (left) {
+            const int64_t row = s0 + __ffs(left) - 1;
+            left &= left - 1;
+            for (int64_t r = lane_id(); r < nrows; r += 32) out[row * nrows + r] = from_f32<TO>(0.0f);
+        }
+    }
+}
+
+// Forms within one CTA (cta_group::1).
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int32_t x, const int32_t (&y)[4], uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0), fp32 accumulator, both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);

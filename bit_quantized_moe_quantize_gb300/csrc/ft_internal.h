@@ -182,7 +182,7 @@ struct Fp8Order {
     uint32_t* err;        // the general router's own flags: ids of -1 are no error here
 };
 size_t fp8_order_layout(uint8_t* base, int64_t n_slots, int32_t n_experts, bool with_pos, Fp8Order* o);   // bytes
-int launch_fp8_order(const int32_t* ids, int64_t n_slots, int32_t n_experts, const Fp8Order& o, cudaStream_t s);
+int launch_fp8_order(const int32_t* ids, int64_t n_slots, int32_t n_experts, int width, const Fp8Order& o, cudaStream_t s);
 
 struct Fp8Product {
     const uint8_t* weights;     // [n_experts][nrows][ncols] e4m3
@@ -201,7 +201,12 @@ struct Fp8Product {
     float* mid_scales;
     int32_t mid_pitch, act_kind;
 };
-int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
+// Slots per tile for a batch (16 or 32: moe_fp8_narrow.cu; 256: moe_fp8.cu); the order's
+// tiles must be of that width.  fp8_orders_itself: the product needs no launch_fp8_order before it.
+int fp8_tile_width(int64_t n_slots, int32_t n_experts);
+bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width);
+int launch_fp8_product(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
+int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
 // Copies the rows of p to router order (codes, scales: room for n_slots rows) and makes p `ordered`.
 int launch_fp8_order_rows(Fp8Product* p, uint8_t* codes, float* scales, cudaStream_t s);
 // Whether a batch's rows should be copied to router order, and the pitch of scales there.

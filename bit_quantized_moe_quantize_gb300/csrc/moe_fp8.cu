@@ -37,6 +37,7 @@
 // A gather fetches four 128-byte rows per instruction and the TMA unit takes about
 // 85 cycles for one, so 128 slots a CTA would need 2700 cycles a block: batches
 // with many slots per expert first copy their rows to router order.
+#include "fp8_order.cuh"
 #include "fp8_tc.cuh"
 #include "ft_internal.h"
 #include "gemm_common.cuh"
@@ -69,7 +70,10 @@ struct Pair {
     static constexpr int OFF_AMAX = OFF_BAR - 4 * BM * 4;       // [tile parity][half][slot], gated
     static constexpr int N_BARS = 2 * STAGES + 8 + 4;
     static constexpr int OFF_TMEM = OFF_BAR + N_BARS * 8;
-    static constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;    // + alignment slack
+    // offsets[E + 1] and tiles[E + 1] of up to MAX_E experts (a search in global memory waits for it at every step)
+    static constexpr int MAX_E = 1024;
+    static constexpr int OFF_ORDER = OFF_TMEM + 16;
+    static constexpr int SMEM_BYTES = OFF_ORDER + 2 * (MAX_E + 1) * 4 + 1024;    // + alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
@@ -113,12 +117,7 @@ __device__ __forceinline__ PairTile pair_tile(const PairArgs& a, int64_t w) {
     int32_t first = 0, count = static_cast<int32_t>(a.n_slots), j = st;
     t.e = 0;
     if (a.tiles) {
-        int32_t lo = 0, hi = a.n_experts - 1;
-        while (lo < hi) {
-            const int32_t mid = (lo + hi + 1) >> 1;
-            if (a.tiles[mid] <= st) lo = mid;
-            else hi = mid - 1;
-        }
+        const int32_t lo = last_not_above(a.tiles, a.n_experts, st);
         t.e = lo;
         first = a.offsets[lo];
         count = a.offsets[lo + 1] - first;
@@ -146,23 +145,6 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
 // acc += {lo, hi} * s
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
     asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
-}
-
-// Rows of slots without an expert are 0; ids that are neither -1 nor an expert raise the flag.
-template <typename TO>
-__device__ __forceinline__ void zero_unrouted(const PairArgs& a, TO* out, int64_t warp, int64_t n_warps) {
-    for (int64_t s0 = warp * 32; s0 < a.n_slots; s0 += n_warps * 32) {
-        const int64_t s = s0 + lane_id();
-        const int32_t id = s < a.n_slots ? a.ids[s] : 0;
-        const bool none = id < 0 || id >= a.n_experts;
-        if (none && id != -1) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
-        uint32_t left = __ballot_sync(0xFFFFFFFFu, none);
-        while (left) {
-            const int64_t row = s0 + __ffs(left) - 1;
-            left &= left - 1;
-            for (int64_t r = lane_id(); r < a.nrows; r += 32) out[row * a.nrows + r] = from_f32<TO>(0.0f);
-        }
-    }
 }
 
 // The ring of scales: group g of four blocks lies in slot g % SCALE_RING.  A thread
@@ -215,8 +197,9 @@ __device__ __forceinline__ float act_mul_fast(float g, float up, int32_t kind) {
 template <typename TO, bool GATHER, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     moe_fp8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                        const PairArgs a, TO* __restrict__ out) {
+                        const PairArgs args, TO* __restrict__ out) {
     using C = Pair;
+    PairArgs a = args;
     extern __shared__ uint8_t smem_raw[];
     // both CTAs round up by the same amount: their dynamic shared memory starts at the same offset
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -246,6 +229,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     if (warp == C::WARP_PRODUCER && lane == 0) {
         prefetch_tmap(&wmap);
         prefetch_tmap(&xmap);
+    }
+    if (a.tiles && a.n_experts <= C::MAX_E) {
+        int32_t *offsets = reinterpret_cast<int32_t*>(smem + C::OFF_ORDER), *tiles = offsets + C::MAX_E + 1;
+        for (int32_t e = static_cast<int32_t>(threadIdx.x); e <= a.n_experts; e += C::THREADS) {
+            offsets[e] = a.offsets[e];
+            tiles[e] = a.tiles[e];
+        }
+        a.offsets = offsets;
+        a.tiles = tiles;
     }
     tc_fence_before();
     cluster_sync_all();
@@ -345,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         }
         __syncwarp();
     } else if (!GATED && a.ids) {
-        zero_unrouted<TO>(a, out, blockIdx.x, gridDim.x);
+        zero_unrouted<TO>(a.ids, a.n_slots, a.n_experts, a.nrows, a.err, out, blockIdx.x, gridDim.x);
     }
     } else {
         // --------------------------------------------------------------- drain
@@ -582,6 +574,11 @@ int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs
 
 }  // namespace
 
+int fp8_tile_width(int64_t n_slots, int32_t n_experts) {
+    const double mean = static_cast<double>(n_slots) / n_experts;
+    return mean <= 12 ? 16 : mean <= 24 ? 32 : 2 * Pair::BM;
+}
+
 bool fp8_copies_rows(int64_t n_slots, int32_t n_experts) { return n_slots > static_cast<int64_t>(kGatherMean) * n_experts; }
 
 size_t fp8_order_layout(uint8_t* base, int64_t n_slots, int32_t n_experts, bool with_pos, Fp8Order* o) {
@@ -604,8 +601,7 @@ size_t fp8_order_layout(uint8_t* base, int64_t n_slots, int32_t n_experts, bool 
     return at;
 }
 
-int launch_fp8_order(const int32_t* ids, int64_t n_slots, int32_t n_experts, const Fp8Order& o, cudaStream_t s) {
-    constexpr int tile = 2 * Pair::BM;
+int launch_fp8_order(const int32_t* ids, int64_t n_slots, int32_t n_experts, int tile, const Fp8Order& o, cudaStream_t s) {
     if (fp8_route_ok(n_slots, n_experts))
         return launch_fp8_route(ids, n_slots, n_experts, tile, o.hist, o.offsets, o.tiles, o.perm, o.pos, s);
     RouteBuffers rb{};
@@ -632,8 +628,9 @@ int launch_fp8_order_rows(Fp8Product* p, uint8_t* codes, float* scales, cudaStre
     return check_launch("order_rows_kernel", grid, dim3(256), 0);
 }
 
-int launch_fp8_product(const Fp8Product& p, void* out, int out_dtype, uint32_t* err, cudaStream_t s) {
+int launch_fp8_product(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s) {
     using C = Pair;
+    if (width < 2 * C::BM) return launch_fp8_narrow(p, width, out, out_dtype, err, s);
     const bool gated = p.mid != nullptr, boxes = p.ordered || !p.ids;      // rows that lie in order arrive in boxes
     PairArgs a{};
     a.act_scales = p.act_scales;

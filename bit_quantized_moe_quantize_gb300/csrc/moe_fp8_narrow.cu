@@ -1,0 +1,410 @@
+// The FP8 products for few slots per expert (up to 128 in a tile): what bounds them is
+// reading the experts' matrices once.
+//
+// One tile: up to 128 weight rows of an expert x up to NW of its slots (16 or 32), one CTA, tcgen05 MMAs with M = 128 weight rows and N = the tile's slots rounded
+// up to 16.  Here the weight rows lie along the tensor-memory lanes: with few slots the
+// scales of a block are few, and a warp reads them from shared memory at a broadcast for
+// its 32 rows.  Where a batch has too few tiles of 128 rows to fill the GPU, a tile takes
+// 64 or 32 weight rows; the MMA still runs over 128 lanes, whose other rows are whatever
+// lies behind in shared memory and are not read.
+//
+// Blocks go through tensor memory in units of 64 columns (two blocks of 32 slots or four
+// of 16), so that the drain waits once per unit and the MMAs of eight units run ahead of it.
+//
+// Up to 1024 slots are put in order by every CTA for itself, in shared memory (some 2 us
+// less than a launch and the reads of its results); more come ordered.
+//
+// Per CTA: warps 0-3 drain (32 weight rows each), warp 4 TMA producer, warp 5 MMA, warp 6
+// scales (sa * sw of a unit's blocks and slots to a ring in shared memory), warp 7 zeroes
+// the rows of slots without an expert.
+//
+#include "fp8_order.cuh"
+#include "fp8_tc.cuh"
+#include "ft_internal.h"
+#include "gemm_common.cuh"
+
+namespace ft {
+
+template <int NW_>
+struct Narrow {
+    static constexpr int NW = NW_;
+    static constexpr int BM = 128;                                  // lanes; weight rows of a tile at most
+    static constexpr int G = 64 / NW;                               // blocks per unit
+    static constexpr int UNIT = G * NW;                             // columns of a unit
+    static constexpr int UNITS = 512 / UNIT;
+    static constexpr int NSC = 4;                                   // units in the scale ring
+    static constexpr int MAX_STAGES = 16;
+    static constexpr int RING_BYTES = 160 * 1024;
+    static constexpr int SLACK = BM * kFp8Block;                    // what an MMA reads past the last short tile
+    static constexpr int OFF_SC = RING_BYTES + SLACK;
+    static constexpr int OFF_BAR = OFF_SC + NSC * UNIT * 4;
+    static constexpr int N_BARS = 2 * MAX_STAGES + 2 * UNITS + 2 * NSC;
+    static constexpr int OFF_TMEM = OFF_BAR + N_BARS * 8;
+    // in-CTA order: offsets[E + 1], tiles[E + 1], perm[1024]; the counts [8][E] lie in the ring
+    static constexpr int MAX_E = 1024;
+    static constexpr int OFF_ORDER = OFF_TMEM + 16;
+    static constexpr int SMEM_BYTES = OFF_ORDER + (2 * (MAX_E + 1) + 1024 + 8) * 4 + 1024;
+    static_assert(kChunkWarps * MAX_E * 4 <= RING_BYTES, "counts");
+    static constexpr int WARP_PRODUCER = 4, WARP_MMA = 5, WARP_SCALE = 6;
+    static constexpr int THREADS = 256;
+    static constexpr int ROW_BOX = 16;
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+struct NarrowArgs {
+    const int32_t* ids;
+    const int32_t* perm;
+    const int32_t* offsets;
+    const int32_t* tiles;        // prefix of tiles of NW slots
+    const float* act_scales;
+    const float* w_scales;
+    uint32_t* err;
+    int64_t n_slots, nrows;
+    int32_t act_div, n_experts, nb, row_tiles, row_blocks, scale_pitch;
+    int32_t br;                  // weight rows of a tile: 32, 64 or 128
+    int32_t stages;
+    bool ordered;
+    bool orders;                 // perm, offsets and tiles are worked out by the CTA
+};
+
+struct NarrowTile {
+    int32_t e, p0, n, r0;        // expert, first position, slots, first weight row
+};
+
+template <int NW>
+__device__ __forceinline__ NarrowTile narrow_tile(const NarrowArgs& a, int64_t w) {
+    NarrowTile t;
+    const int32_t st = static_cast<int32_t>(w / a.row_tiles);
+    t.r0 = static_cast<int32_t>(w - static_cast<int64_t>(st) * a.row_tiles) * a.br;
+    int32_t first = 0, count = static_cast<int32_t>(a.n_slots), j = st;
+    t.e = 0;
+    if (a.tiles) {
+        t.e = last_not_above(a.tiles, a.n_experts, st);
+        first = a.offsets[t.e];
+        count = a.offsets[t.e + 1] - first;
+        j = st - a.tiles[t.e];
+    }
+    t.p0 = first + j * NW;
+    t.n = min(NW, count - j * NW);
+    return t;
+}
+
+template <int NW, typename TO, bool GATHER>
+__global__ void __launch_bounds__(Narrow<NW>::THREADS, 1)
+    moe_fp8_narrow_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                          const NarrowArgs args, TO* __restrict__ out) {
+    using C = Narrow<NW>;
+    NarrowArgs a = args;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + C::MAX_STAGES;
+    uint64_t* acc_full = empty + C::MAX_STAGES;
+    uint64_t* acc_empty = acc_full + C::UNITS;
+    uint64_t* sc_full = acc_empty + C::UNITS;
+    uint64_t* sc_empty = sc_full + C::NSC;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_TMEM);
+    float* sc_ring = reinterpret_cast<float*>(smem + C::OFF_SC);
+
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    const int32_t nb = a.nb, stages = a.stages;
+    // a stage: NW slots' rows, then br weight rows (last, so that an MMA over 128 rows stays inside)
+    const uint32_t b_bytes = NW * kFp8Block, stage_bytes = b_bytes + static_cast<uint32_t>(a.br) * kFp8Block;
+    const uint32_t n_drain = static_cast<uint32_t>(a.br) / 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::MAX_STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::UNITS; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], n_drain);
+        }
+        for (int i = 0; i < C::NSC; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_empty[i], n_drain);
+        }
+        fence_mbar_init();
+    }
+    if (warp == C::WARP_MMA) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == C::WARP_PRODUCER && lane == 0) {
+        prefetch_tmap(&wmap);
+        prefetch_tmap(&xmap);
+    }
+    if (a.orders) {
+        int32_t* offsets = reinterpret_cast<int32_t*>(smem + C::OFF_ORDER);
+        int32_t *tiles = offsets + C::MAX_E + 1, *perm = tiles + C::MAX_E + 1, *part = perm + 1024;
+        int32_t* mine = reinterpret_cast<int32_t*>(smem);
+        const int32_t E = a.n_experts, n_slots = static_cast<int32_t>(a.n_slots);
+        int32_t id[4], rank[4];
+        const int32_t s0 = chunk_rank(a.ids, 0, n_slots, E, mine, id, rank);
+        chunk_totals(mine, E, offsets);
+        for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) tiles[e] = (offsets[e] + NW - 1) / NW;
+        __syncthreads();
+        const int32_t routed = chunk_scan(offsets, E, part), n_tiles = chunk_scan(tiles, E, part);
+        if (threadIdx.x == 0) {
+            offsets[E] = routed;
+            tiles[E] = n_tiles;
+        }
+        chunk_starts(mine, E, offsets);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (id[i] >= 0) perm[mine[static_cast<int32_t>(warp) * E + id[i]] + rank[i]] = s0 + 32 * i;
+        fence_proxy_async_smem();      // the copies that follow write where the counts lay
+        a.perm = perm;
+        a.offsets = offsets;
+        a.tiles = tiles;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int64_t slot_tiles = a.tiles ? a.tiles[a.n_experts] : (a.n_slots + NW - 1) / NW;
+    const int64_t total = slot_tiles * a.row_tiles;
+
+    if (warp == C::WARP_PRODUCER) {
+        // ------------------------------------------------------------ producer
+        int32_t s = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const NarrowTile t = narrow_tile<NW>(a, w);
+            constexpr int PER = GATHER ? 4 : C::ROW_BOX;
+            const bool copies = static_cast<int32_t>(lane) * PER < t.n;
+            int32_t y[4] = {0, 0, 0, 0};
+            if (copies) {
+                const int32_t p = t.p0 + static_cast<int32_t>(lane) * PER;
+                if constexpr (GATHER) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = a.perm[min(p + i, t.p0 + t.n - 1)] / a.act_div;
+                } else {
+                    y[0] = p;
+                }
+            }
+            const int32_t wy = static_cast<int32_t>(static_cast<int64_t>(t.e) * a.nrows + t.r0);
+            const uint32_t bytes = static_cast<uint32_t>(a.br + (t.n + PER - 1) / PER * PER) * kFp8Block;
+            for (int32_t b = 0; b < nb; ++b) {
+                if (!mbar_wait_warp(&empty[s], phase, a.err)) { ok = false; break; }
+                uint8_t* dst = smem + static_cast<uint32_t>(s) * stage_bytes;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[s], bytes);
+                    tma_load_2d(dst + b_bytes, &wmap, b * kFp8Block, wy, &full[s]);
+                }
+                __syncwarp();
+                if (copies) {
+                    uint8_t* d = dst + lane * (PER * kFp8Block);
+                    if constexpr (GATHER) tma_gather4(smem_u32(d), &xmap, b * kFp8Block, y, &full[s]);
+                    else tma_load_2d(d, &xmap, b * kFp8Block, y[0], &full[s]);
+                }
+                __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == C::WARP_MMA) {
+        // ----------------------------------------------------------------- MMA
+        const bool elected = elect_one();
+        const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+        int32_t s = 0;
+        uint32_t phase = 0, unit = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const NarrowTile t = narrow_tile<NW>(a, w);
+            const uint32_t idesc = idesc_e4m3_f32(C::BM, (t.n + 15) / 16 * 16);
+            for (int32_t b0 = 0; b0 < nb && ok; b0 += C::G, ++unit) {
+                const uint32_t u = unit % C::UNITS;
+                if (!mbar_wait_warp(&acc_empty[u], ((unit / C::UNITS) & 1u) ^ 1u, a.err)) { ok = false; break; }
+                const int32_t n = min(C::G, nb - b0);
+                for (int32_t g = 0; g < n; ++g) {
+                    if (!mbar_wait_warp(&full[s], phase, a.err)) { ok = false; break; }
+                    tc_fence_after();
+                    if (elected) {
+                        const uint64_t bdesc = desc0 + ((static_cast<uint32_t>(s) * stage_bytes) >> 4), adesc = bdesc + (b_bytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f8(tmem + u * C::UNIT + static_cast<uint32_t>(g) * NW, adesc + 2 * k, bdesc + 2 * k, idesc, k);
+                        tc_commit(&empty[s]);
+                        if (g == n - 1) tc_commit(&acc_full[u]);
+                    }
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == C::WARP_SCALE) {
+        // -------------------------------------------------------------- scales
+                uint32_t unit = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const NarrowTile t = narrow_tile<NW>(a, w);
+            const float* sa = nullptr;                   // of slot `lane`
+            if (static_cast<int32_t>(lane) < t.n) {
+                const int32_t p = t.p0 + static_cast<int32_t>(lane);
+                sa = a.act_scales + static_cast<int64_t>(a.ordered ? p : a.perm[p] / a.act_div) * a.scale_pitch;
+            }
+            const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + t.r0 / kFp8Block) * nb;
+            float v[C::G], x[C::G];                      // of the unit to come
+            auto load = [&](int32_t b0) {
+#pragma unroll
+                for (int g = 0; g < C::G; ++g) {
+                    x[g] = b0 + g < nb ? __ldg(sw + b0 + g) : 0.0f;
+                    v[g] = sa && b0 + g < nb ? __ldg(sa + b0 + g) : 0.0f;
+                }
+            };
+            load(0);
+            for (int32_t b0 = 0; b0 < nb; b0 += C::G, ++unit) {
+                const uint32_t r = unit % C::NSC;
+                if (!mbar_wait_warp(&sc_empty[r], ((unit / C::NSC) & 1u) ^ 1u, a.err)) { ok = false; break; }
+#pragma unroll
+                for (int g = 0; g < C::G; ++g)
+                    if (lane < static_cast<uint32_t>(NW)) sc_ring[r * C::UNIT + g * NW + lane] = v[g] * x[g];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_full[r]);
+                if (b0 + C::G < nb) load(b0 + C::G);
+            }
+        }
+    } else if (warp < n_drain) {
+        // --------------------------------------------------------------- drain
+        uint32_t unit = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const NarrowTile t = narrow_tile<NW>(a, w);
+            float acc[NW];
+#pragma unroll
+            for (int i = 0; i < NW; ++i) acc[i] = 0.0f;
+            for (int32_t b0 = 0; b0 < nb; b0 += C::G, ++unit) {
+                const uint32_t u = unit % C::UNITS, r = unit % C::NSC;
+                if (!mbar_wait2_warp(&sc_full[r], (unit / C::NSC) & 1u, &acc_full[u], (unit / C::UNITS) & 1u, a.err)) { ok = false; break; }
+                tc_fence_after();
+                const float4* sc = reinterpret_cast<const float4*>(sc_ring + r * C::UNIT);
+#pragma unroll
+                for (int j = 0; j < C::UNIT / 16; ++j) {      // 16 columns: slots 16 j % NW .. of block 16 j / NW
+                    if (b0 + 16 * j / NW < nb && 16 * j % NW < t.n) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(tmem + u * C::UNIT + ((warp * 32u) << 16) + 16 * j, v);
+                        float4 c[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c[i] = sc[4 * j + i];
+                        tmem_wait_ld_regs(v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float* o = acc + 16 * j % NW + 4 * i;
+                            o[0] = fmaf(__uint_as_float(v[4 * i]), c[i].x, o[0]);
+                            o[1] = fmaf(__uint_as_float(v[4 * i + 1]), c[i].y, o[1]);
+                            o[2] = fmaf(__uint_as_float(v[4 * i + 2]), c[i].z, o[2]);
+                            o[3] = fmaf(__uint_as_float(v[4 * i + 3]), c[i].w, o[3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&acc_empty[u]);
+                    mbar_arrive(&sc_empty[r]);
+                }
+            }
+            if (!ok) break;
+            const int32_t row = t.r0 + static_cast<int32_t>(threadIdx.x);
+#pragma unroll
+            for (int c = 0; c < NW; ++c) {
+                if (c < t.n) {
+                    const int32_t p = t.p0 + c, slot = a.perm ? a.perm[p] : p;
+                    if (row < a.nrows) out[static_cast<int64_t>(slot) * a.nrows + row] = from_f32<TO>(acc[c]);
+                }
+            }
+        }
+    } else if (warp == 7 && a.ids) {
+        zero_unrouted<TO>(a.ids, a.n_slots, a.n_experts, a.nrows, a.err, out, blockIdx.x, gridDim.x);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::WARP_MMA) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------- host
+namespace {
+
+template <int NW, typename TO, bool GATHER>
+int launch_narrow(const CUtensorMap& wmap, const CUtensorMap& xmap, NarrowArgs& a, void* out, int64_t tiles, cudaStream_t s) {
+    using C = Narrow<NW>;
+    const void* k = reinterpret_cast<const void*>(moe_fp8_narrow_kernel<NW, TO, GATHER>);
+    const int stage = (NW + a.br) * kFp8Block;
+    a.stages = C::RING_BYTES / stage < C::MAX_STAGES ? C::RING_BYTES / stage : C::MAX_STAGES;
+    if (int st = set_smem_limit(k, C::SMEM_BYTES)) return st;
+    const int64_t sms = sm_count();
+    const dim3 grid(static_cast<unsigned>(tiles < sms ? tiles : sms));
+    moe_fp8_narrow_kernel<NW, TO, GATHER><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, static_cast<TO*>(out));
+    return check_launch("moe_fp8_narrow_kernel", grid, dim3(C::THREADS), C::SMEM_BYTES);
+}
+
+template <int NW>
+int launch_narrow_width(const CUtensorMap& wmap, const CUtensorMap& xmap, NarrowArgs& a, void* out, int out_dtype, bool gather,
+                        int64_t tiles, cudaStream_t s) {
+    if (gather)
+        return out_dtype == FT_DTYPE_F32 ? launch_narrow<NW, float, true>(wmap, xmap, a, out, tiles, s)
+                                         : launch_narrow<NW, __nv_bfloat16, true>(wmap, xmap, a, out, tiles, s);
+    return out_dtype == FT_DTYPE_F32 ? launch_narrow<NW, float, false>(wmap, xmap, a, out, tiles, s)
+                                     : launch_narrow<NW, __nv_bfloat16, false>(wmap, xmap, a, out, tiles, s);
+}
+
+}  // namespace
+
+bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width) {
+    return width <= 32 && n_slots <= kChunk && n_experts <= Narrow<16>::MAX_E;
+}
+
+// width: slots per tile (16 or 32), that of p.order's tiles
+int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s) {
+    const bool boxes = p.ordered || !p.ids;
+    NarrowArgs a{};
+    a.act_scales = p.act_scales;
+    a.w_scales = p.w_scales;
+    a.err = err;
+    a.n_slots = p.n_slots;
+    a.nrows = p.nrows;
+    a.act_div = p.act_div;
+    a.n_experts = p.n_experts;
+    a.nb = static_cast<int32_t>(fp8_blocks(p.ncols));
+    a.row_blocks = static_cast<int32_t>(fp8_blocks(p.nrows));
+    a.scale_pitch = p.scale_pitch;
+    a.ordered = boxes;
+    if (p.ids) {
+        a.ids = p.ids;
+        a.orders = fp8_orders_itself(p.n_slots, p.n_experts, width);
+        a.perm = p.order->perm;
+        a.offsets = p.order->offsets;
+        a.tiles = p.order->tiles;
+    }
+    const int64_t some = p.ids ? (p.n_experts < p.n_slots ? p.n_experts : p.n_slots) : 1;
+    const int64_t most_tiles = (p.n_slots + width - 1) / width + (p.ids ? some : 0);
+    // shorter tiles where those of 128 rows, over the experts that a batch is likely to
+    // touch, would leave SMs without one
+    const int64_t likely = p.ids ? (some > (p.n_slots + width - 1) / width ? some : (p.n_slots + width - 1) / width) : most_tiles;
+    a.br = 128;
+    while (a.br > 32 && likely * ((p.nrows + a.br - 1) / a.br) < sm_count()) a.br /= 2;
+    a.row_tiles = static_cast<int32_t>((p.nrows + a.br - 1) / a.br);
+    CUtensorMap wmap, xmap;
+    if (int st = encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weights, p.ncols,
+                           static_cast<uint64_t>(p.n_experts) * p.nrows, p.ncols, kFp8Block, a.br,
+                           CU_TENSOR_MAP_SWIZZLE_128B, "FP8 weights"))
+        return st;
+    if (int st = encode_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.act, p.ncols, p.act_rows, p.ncols, kFp8Block,
+                           boxes ? 16 : 1, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
+        return st;
+    const int64_t tiles = most_tiles * a.row_tiles;
+    if (width == 16) return launch_narrow_width<16>(wmap, xmap, a, out, out_dtype, !boxes, tiles, s);
+    return launch_narrow_width<32>(wmap, xmap, a, out, out_dtype, !boxes, tiles, s);
+}
+
+}  // namespace ft
