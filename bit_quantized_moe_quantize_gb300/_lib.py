@@ -387,167 +387,200 @@ def block_dots(weights, act, topk_ids, out=None):
 
 
 # ------------------------------------------------- FP8 expert-layer operators
+# A decoded token's calls take the GPU a few microseconds: the checks below stay cheap
+# (one attribute at a time, device indices instead of device objects).
 SCORES = {"softmax": 0, "sigmoid": 1}
-_DTYPES: dict = {}
+F32, F16, BF16 = 0, 1, 2
+_DTYPES: dict = {}       # torch dtype -> FT_DTYPE_*
+_CODES: tuple = ()       # torch dtypes that hold e4m3 codes
+_i32 = _f32 = _e4m3 = None
+_Tensor = _empty = _stream_of = None
 
 
-def _dtype_code(t, name, *allowed):
-    """FT_DTYPE_* of a tensor (or dtype), one of the torch type names `allowed`."""
+def _ready():
+    """The library, with the torch names that the checks use."""
+    global _CODES, _i32, _f32, _e4m3, _Tensor, _empty, _stream_of
     torch = _torch()
-    if not _DTYPES:
-        _DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    dt = t.dtype if isinstance(t, torch.Tensor) else t
-    if dt not in _DTYPES or (allowed and str(dt) not in allowed):
-        raise TypeError(f"{name} must be one of {', '.join(allowed) or 'float32, float16, bfloat16'}, got {dt}")
-    return _DTYPES[dt]
+    if not _CODES:
+        _DTYPES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+        _i32, _f32, _e4m3 = torch.int32, torch.float32, torch.float8_e4m3fn
+        _Tensor, _empty = torch.Tensor, torch.empty
+        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _CODES = (torch.float8_e4m3fn, torch.uint8)
+    return load()
 
 
-def _ptr(t, name, ndim, like=None):
-    """Data pointer of a contiguous CUDA tensor with `ndim` dims on the device of `like`."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _lib_ready():
+    return _lib if _CODES and _lib is not None else _ready()
+
+
+def _bad_dtype(name, allowed, dt):
+    names = ", ".join(str(t).replace("torch.", "") for t, c in _DTYPES.items() if c in allowed)
+    raise TypeError(f"{name} must be one of {names}, got {dt}")
+
+
+def _dtype_code(dt, name, allowed=(F32, F16, BF16)):
+    """FT_DTYPE_* of a torch dtype, one of `allowed`."""
+    code = _DTYPES.get(dt)
+    if code is None or code not in allowed:
+        _bad_dtype(name, allowed, dt)
+    return code
+
+
+def _ptr(t, name, ndim, dev=None):
+    """Data pointer of a contiguous CUDA tensor with `ndim` dims on device `dev`."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     return t.data_ptr()
 
 
-def _codes_ptr(t, name, ndim, like=None):
-    torch = _torch()
-    p = _ptr(t, name, ndim, like)
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+def _codes_ptr(t, name, ndim, dev=None):
+    p = _ptr(t, name, ndim, dev)
+    if t.dtype not in _CODES:
         raise TypeError(f"{name} must hold e4m3 codes (torch.float8_e4m3fn or uint8), got {t.dtype}")
     return p
 
 
-def _f32_ptr(t, name, shape, like):
-    torch = _torch()
-    p = _ptr(t, name, len(shape), like)
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _typed_ptr(t, name, dtype, shape, dev):
+    p = _ptr(t, name, len(shape), dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return p
 
 
-def _out(out, name, shape, dtype, like):
-    torch = _torch()
+def _out(out, name, shape, dtype, like, dev):
+    """`out` checked, or a new tensor beside `like`."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _ptr(out, name, len(shape), like)
-    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
+        return _empty(shape, dtype=dtype, device=like.device)
+    _ptr(out, name, len(shape), dev)
+    if out.dtype != dtype or out.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {shape}, got {out.dtype} {tuple(out.shape)}")
     return out
 
 
 def _workspace(n, like):
-    torch = _torch()
-    return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
+    """(tensor, pointer) of n bytes; the caching allocator hands them out in stream order."""
+    if not n:
+        return None, None
+    t = _empty(n, dtype=_CODES[1], device=like.device)
+    return t, t.data_ptr()
 
 
 def _b(n):
     return (n + 127) // 128
 
 
-def _raw_stream(t):
-    return _torch().cuda.current_stream(t.device).cuda_stream
-
-
-def _gate_row_stride(logits):
-    torch = _torch()
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+def _logits_of(logits):
+    """(tokens, experts, row stride, device index) of router logits, whose rows may lie apart."""
+    if not isinstance(logits, _Tensor) or not logits.is_cuda:
         raise TypeError("logits must be a CUDA tensor")
     if logits.dim() != 2:
         raise ValueError(f"logits must have 2 dims, got {tuple(logits.shape)}")
     T, E = logits.shape
-    if E > 1 and logits.stride(1) != 1:
+    stride, step = logits.stride()
+    if E > 1 and step != 1:
         raise ValueError("the elements of a row of logits must be neighbours")
-    stride = logits.stride(0) if T > 1 else E
-    if stride < E:
+    if T <= 1:
+        stride = E
+    elif stride < E:
         raise ValueError("rows of logits must not overlap")
-    return stride
+    return T, E, stride, logits.get_device()
 
 
 def _score_code(score):
-    if score not in SCORES:
+    code = SCORES.get(score)
+    if code is None:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
-    return SCORES[score]
+    return code
 
 
 def moe_gate(logits, top_k, score="softmax", bias=None, n_groups=1, topk_groups=1, group_top=1, renormalize=True,
              scale=1.0, topk_ids=None, topk_weights=None):
     """Router (ft_moe_gate): logits [T, E] fp32 / fp16 / bf16 (rows may lie apart) ->
     (topk_ids int32 [T, k], topk_weights fp32 [T, k]); id -1, weight 0 where no expert is left."""
-    torch = _torch()
-    stride = _gate_row_stride(logits)
-    T, E = logits.shape
-    k = int(top_k)
-    code = _dtype_code(logits, "logits")
-    pb = None if bias is None else _f32_ptr(bias, "bias", (E,), logits)
-    shape = (T, max(k, 0))
-    topk_ids = _out(topk_ids, "topk_ids", shape, torch.int32, logits)
-    topk_weights = _out(topk_weights, "topk_weights", shape, torch.float32, logits)
-    _check(load().ft_moe_gate(logits.data_ptr(), code, stride, pb, topk_ids.data_ptr(), topk_weights.data_ptr(), T, E,
-                              k, _score_code(score), n_groups, topk_groups, group_top, int(renormalize), scale,
-                              _raw_stream(logits)))
+    L = _lib_ready()
+    T, E, stride, dev = _logits_of(logits)
+    code = _dtype_code(logits.dtype, "logits")
+    pb = None if bias is None else _typed_ptr(bias, "bias", _f32, (E,), dev)
+    shape = (T, max(int(top_k), 0))
+    topk_ids = _out(topk_ids, "topk_ids", shape, _i32, logits, dev)
+    topk_weights = _out(topk_weights, "topk_weights", shape, _f32, logits, dev)
+    st = L.ft_moe_gate(logits.data_ptr(), code, stride, pb, topk_ids.data_ptr(), topk_weights.data_ptr(), T, E, top_k,
+                       _score_code(score), n_groups, topk_groups, group_top, 1 if renormalize else 0, scale,
+                       _stream_of(dev))
+    if st:
+        _check(st)
     return topk_ids, topk_weights
 
 
 def quantize_fp8(x, codes=None, scales=None):
     """[R, K] fp32 / fp16 / bf16 -> (e4m3 codes [R, K], fp32 scales [R, ceil(K/128)]) (ft_quantize_fp8)."""
-    torch = _torch()
+    L = _lib_ready()
     px = _ptr(x, "x", 2)
     R, K = x.shape
-    code = _dtype_code(x, "x")
-    codes = _out(codes, "codes", (R, K), torch.float8_e4m3fn, x)
-    scales = _out(scales, "scales", (R, _b(K)), torch.float32, x)
-    _check(load().ft_quantize_fp8(px, code, codes.data_ptr(), scales.data_ptr(), R, K, _raw_stream(x)))
+    dev = x.get_device()
+    code = _dtype_code(x.dtype, "x")
+    codes = _out(codes, "codes", (R, K), _e4m3, x, dev)
+    scales = _out(scales, "scales", (R, _b(K)), _f32, x, dev)
+    st = L.ft_quantize_fp8(px, code, codes.data_ptr(), scales.data_ptr(), R, K, _stream_of(dev))
+    if st:
+        _check(st)
     return codes, scales
 
 
 def act_mul_quantize_fp8(h, act_kind, codes=None, scales=None):
     """[R, 2I] (gate | up) fp32 / fp16 / bf16 -> (e4m3 codes [R, I], fp32 scales [R, ceil(I/128)])
     of act(gate) * up (ft_act_mul_quantize_fp8)."""
-    torch = _torch()
+    L = _lib_ready()
     ph = _ptr(h, "h", 2)
     R, two_i = h.shape
     if two_i % 2:
         raise ValueError(f"h must hold gate and up values, got rows of {two_i}")
     I = two_i // 2
-    code = _dtype_code(h, "h")
-    codes = _out(codes, "codes", (R, I), torch.float8_e4m3fn, h)
-    scales = _out(scales, "scales", (R, _b(I)), torch.float32, h)
-    _check(load().ft_act_mul_quantize_fp8(ph, code, codes.data_ptr(), scales.data_ptr(), R, I, int(act_kind),
-                                          _raw_stream(h)))
+    dev = h.get_device()
+    code = _dtype_code(h.dtype, "h")
+    codes = _out(codes, "codes", (R, I), _e4m3, h, dev)
+    scales = _out(scales, "scales", (R, _b(I)), _f32, h, dev)
+    st = L.ft_act_mul_quantize_fp8(ph, code, codes.data_ptr(), scales.data_ptr(), R, I, int(act_kind), _stream_of(dev))
+    if st:
+        _check(st)
     return codes, scales
 
 
-def _moe_fp8(fn, per_slot, weights, w_scales, act, act_scales, topk_ids, out, out_dtype):
-    torch = _torch()
+def _moe_fp8(per_slot, weights, w_scales, act, act_scales, topk_ids, out, out_dtype):
+    L = _lib_ready()
     pw = _codes_ptr(weights, "weights", 3)
     E, N, K = weights.shape
-    pi = _ptr(topk_ids, "topk_ids", 2, weights)
-    if topk_ids.dtype != torch.int32:
-        raise TypeError(f"topk_ids must be torch.int32, got {topk_ids.dtype}")
+    dev = weights.get_device()
+    pi = _ptr(topk_ids, "topk_ids", 2, dev)
+    if topk_ids.dtype != _i32:
+        raise TypeError(f"topk_ids must be {_i32}, got {topk_ids.dtype}")
     T, k = topk_ids.shape
     rows = T * k if per_slot else T
-    pa = _codes_ptr(act, "act", 2, weights)
-    if act.shape[0] != rows or act.shape[1] != K:
+    pa = _codes_ptr(act, "act", 2, dev)
+    if act.shape != (rows, K):
         raise ValueError(f"act must have shape {(rows, K)}, got {tuple(act.shape)}")
-    ps = _f32_ptr(w_scales, "w_scales", (E, _b(N), _b(K)), weights)
-    pt = _f32_ptr(act_scales, "act_scales", (rows, _b(K)), weights)
-    out_dtype = out_dtype if out is None else out.dtype
-    code = _dtype_code(out_dtype, "out_dtype", "torch.float32", "torch.bfloat16")
-    out = _out(out, "out", (T, k, N), out_dtype, weights)
-    L = load()
+    nb = _b(K)
+    ps = _typed_ptr(w_scales, "w_scales", _f32, (E, _b(N), nb), dev)
+    pt = _typed_ptr(act_scales, "act_scales", _f32, (rows, nb), dev)
+    out_dtype = (out_dtype or _f32) if out is None else out.dtype
+    code = _dtype_code(out_dtype, "out_dtype", (F32, BF16))
+    out = _out(out, "out", (T, k, N), out_dtype, weights, dev)
     n = L.ft_moe_fp8_workspace_bytes(T, k, E, K)
-    ws = _workspace(n, weights)
-    _check(fn(L)(pw, ps, pa, pt, pi, out.data_ptr(), code, T, k, E, N, K, None if ws is None else ws.data_ptr(), n,
-                 _raw_stream(weights)))
+    ws, pws = _workspace(n, weights)
+    st = (L.ft_moe_fp8_fp8_slots if per_slot else L.ft_moe_fp8_fp8)(
+        pw, ps, pa, pt, pi, out.data_ptr(), code, T, k, E, N, K, pws, n, _stream_of(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -555,54 +588,53 @@ def moe_fp8_fp8(weights, w_scales, act, act_scales, topk_ids, out=None, out_dtyp
     """Routed product (ft_moe_fp8_fp8): e4m3 weights [E, N, K] with scales [E, ceil(N/128), ceil(K/128)] x
     e4m3 rows [T, K] with scales [T, ceil(K/128)] -> [T, k, N] fp32 (default) or bf16.
     Slots whose id is -1 have no expert: their rows are 0."""
-    torch = _torch()
-    return _moe_fp8(lambda L: L.ft_moe_fp8_fp8, False, weights, w_scales, act, act_scales, topk_ids, out,
-                    torch.float32 if out_dtype is None else out_dtype)
+    return _moe_fp8(False, weights, w_scales, act, act_scales, topk_ids, out, out_dtype)
 
 
 def moe_fp8_fp8_slots(weights, w_scales, act_slots, act_scales, topk_ids, out=None, out_dtype=None):
     """moe_fp8_fp8 with one activation row per routed slot, act_slots [T*k, K] (ft_moe_fp8_fp8_slots)."""
-    torch = _torch()
-    return _moe_fp8(lambda L: L.ft_moe_fp8_fp8_slots, True, weights, w_scales, act_slots, act_scales, topk_ids, out,
-                    torch.float32 if out_dtype is None else out_dtype)
+    return _moe_fp8(True, weights, w_scales, act_slots, act_scales, topk_ids, out, out_dtype)
 
 
 def matmul_fp8_fp8(weights, w_scales, act, act_scales, out=None, out_dtype=None):
     """Product with one dense matrix (ft_matmul_fp8_fp8): weights [N, K] x rows [M, K] -> [M, N]
     fp32 (default) or bf16."""
-    torch = _torch()
+    L = _lib_ready()
     pw = _codes_ptr(weights, "weights", 2)
     N, K = weights.shape
-    pa = _codes_ptr(act, "act", 2, weights)
+    dev = weights.get_device()
+    pa = _codes_ptr(act, "act", 2, dev)
     M = act.shape[0]
     if act.shape[1] != K:
         raise ValueError(f"act must have {K} columns, got {tuple(act.shape)}")
-    ps = _f32_ptr(w_scales, "w_scales", (_b(N), _b(K)), weights)
-    pt = _f32_ptr(act_scales, "act_scales", (M, _b(K)), weights)
-    out_dtype = (torch.float32 if out_dtype is None else out_dtype) if out is None else out.dtype
-    code = _dtype_code(out_dtype, "out_dtype", "torch.float32", "torch.bfloat16")
-    out = _out(out, "out", (M, N), out_dtype, weights)
-    _check(load().ft_matmul_fp8_fp8(pw, ps, pa, pt, out.data_ptr(), code, M, N, K, _raw_stream(weights)))
+    nb = _b(K)
+    ps = _typed_ptr(w_scales, "w_scales", _f32, (_b(N), nb), dev)
+    pt = _typed_ptr(act_scales, "act_scales", _f32, (M, nb), dev)
+    out_dtype = (out_dtype or _f32) if out is None else out.dtype
+    code = _dtype_code(out_dtype, "out_dtype", (F32, BF16))
+    out = _out(out, "out", (M, N), out_dtype, weights, dev)
+    st = L.ft_matmul_fp8_fp8(pw, ps, pa, pt, out.data_ptr(), code, M, N, K, _stream_of(dev))
+    if st:
+        _check(st)
     return out
 
 
 def moe_combine(rows, topk_weights, add=None, out=None, out_dtype=None):
     """Weighted sum of each token's expert rows (ft_moe_combine): rows [T, k, N] fp32 / bf16, topk_weights
     fp32 [T, k], add [T, N] or None -> [T, N] of out_dtype (default: rows' type).  Rows with weight 0 are not read."""
-    torch = _torch()
+    L = _lib_ready()
     pr = _ptr(rows, "rows", 3)
     T, k, N = rows.shape
-    pw = _f32_ptr(topk_weights, "topk_weights", (T, k), rows)
-    code = _dtype_code(rows, "rows", "torch.float32", "torch.bfloat16")
-    out_dtype = (rows.dtype if out_dtype is None else out_dtype) if out is None else out.dtype
+    dev = rows.get_device()
+    pw = _typed_ptr(topk_weights, "topk_weights", _f32, (T, k), dev)
+    code = _dtype_code(rows.dtype, "rows", (F32, BF16))
+    out_dtype = (out_dtype or rows.dtype) if out is None else out.dtype
     ocode = _dtype_code(out_dtype, "out_dtype")
-    out = _out(out, "out", (T, N), out_dtype, rows)
-    if add is not None:
-        _ptr(add, "add", 2, rows)
-        if add.dtype != out_dtype or tuple(add.shape) != (T, N):
-            raise ValueError(f"add must be {out_dtype} {(T, N)}, got {add.dtype} {tuple(add.shape)}")
-    _check(load().ft_moe_combine(pr, code, pw, None if add is None else add.data_ptr(), out.data_ptr(), ocode, T, k, N,
-                                 _raw_stream(rows)))
+    out = _out(out, "out", (T, N), out_dtype, rows, dev)
+    pa = None if add is None else _typed_ptr(add, "add", out_dtype, (T, N), dev)
+    st = L.ft_moe_combine(pr, code, pw, pa, out.data_ptr(), ocode, T, k, N, _stream_of(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -610,35 +642,36 @@ def moe_layer_fp8(x, logits, w13, s13, w2, s2, top_k, act_kind=0, score="softmax
                   topk_groups=1, group_top=1, renormalize=True, scale=1.0, out=None):
     """A whole expert layer (ft_moe_layer_fp8): x [T, H] fp16 / bf16, router logits [T, E], e4m3 w13 [E, 2I, H]
     (gate rows, then up rows) and w2 [E, H, I] with their scales -> (y [T, H], topk_ids, topk_weights)."""
-    torch = _torch()
+    L = _lib_ready()
     px = _ptr(x, "x", 2)
     T, H = x.shape
-    xcode = _dtype_code(x, "x", "torch.float16", "torch.bfloat16")
-    stride = _gate_row_stride(logits)
-    E = logits.shape[1]
-    if logits.shape[0] != T or logits.device != x.device:
+    xcode = _dtype_code(x.dtype, "x", (F16, BF16))
+    T2, E, stride, dev = _logits_of(logits)
+    if T2 != T or x.get_device() != dev:
         raise ValueError(f"logits must be [{T}, E] on {x.device}, got {tuple(logits.shape)} on {logits.device}")
-    lcode = _dtype_code(logits, "logits")
-    pw13, pw2 = _codes_ptr(w13, "w13", 3, x), _codes_ptr(w2, "w2", 3, x)
+    lcode = _dtype_code(logits.dtype, "logits")
+    pw13, pw2 = _codes_ptr(w13, "w13", 3, dev), _codes_ptr(w2, "w2", 3, dev)
     two_i = w13.shape[1]
-    if tuple(w13.shape) != (E, two_i, H) or two_i % 2 or tuple(w2.shape) != (E, H, two_i // 2):
+    I = two_i // 2
+    if two_i % 2 or w13.shape != (E, two_i, H) or w2.shape != (E, H, I):
         raise ValueError(f"shape mismatch: x {tuple(x.shape)} logits {tuple(logits.shape)} w13 {tuple(w13.shape)} "
                          f"w2 {tuple(w2.shape)}")
-    I = two_i // 2
-    ps13 = _f32_ptr(s13, "s13", (E, _b(two_i), _b(H)), x)
-    ps2 = _f32_ptr(s2, "s2", (E, _b(H), _b(I)), x)
-    pb = None if bias is None else _f32_ptr(bias, "bias", (E,), x)
-    k = int(top_k)
-    out = _out(out, "out", (T, H), x.dtype, x)
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=x.device)
-    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=x.device)
-    L = load()
-    n = L.ft_moe_layer_fp8_workspace_bytes(T, k, E, H, I)
-    ws = _workspace(n, x)
-    _check(L.ft_moe_layer_fp8(px, xcode, logits.data_ptr(), lcode, stride, pb, pw13, ps13, pw2, ps2, out.data_ptr(),
-                              ids.data_ptr(), weights.data_ptr(), T, E, k, H, I, _score_code(score), n_groups,
-                              topk_groups, group_top, int(renormalize), scale, int(act_kind),
-                              None if ws is None else ws.data_ptr(), n, _raw_stream(x)))
+    nbh = _b(H)
+    ps13 = _typed_ptr(s13, "s13", _f32, (E, _b(two_i), nbh), dev)
+    ps2 = _typed_ptr(s2, "s2", _f32, (E, nbh, _b(I)), dev)
+    pb = None if bias is None else _typed_ptr(bias, "bias", _f32, (E,), dev)
+    out = _out(out, "out", (T, H), x.dtype, x, dev)
+    device, shape = x.device, (T, max(int(top_k), 0))
+    ids = _empty(shape, dtype=_i32, device=device)
+    weights = _empty(shape, dtype=_f32, device=device)
+    n = L.ft_moe_layer_fp8_workspace_bytes(T, top_k, E, H, I)
+    ws, pws = _workspace(n, x)
+    st = L.ft_moe_layer_fp8(px, xcode, logits.data_ptr(), lcode, stride, pb, pw13, ps13, pw2, ps2, out.data_ptr(),
+                            ids.data_ptr(), weights.data_ptr(), T, E, top_k, H, I, _score_code(score), n_groups,
+                            topk_groups, group_top, 1 if renormalize else 0, scale, int(act_kind), pws, n,
+                            _stream_of(dev))
+    if st:
+        _check(st)
     return out, ids, weights
 
 

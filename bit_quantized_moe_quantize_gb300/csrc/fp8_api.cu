@@ -110,17 +110,19 @@ size_t take_bytes(size_t* at, size_t bytes) {
     return r;
 }
 
-// Workspace of a routed product: router order, then (many slots per expert) the
-// activation rows and scales in that order.
+// Workspace of a routed product: router order, then (wide tiles) the activation rows and
+// scales in that order.
 struct ProductWs {
     Fp8Order order;
+    int width;
     size_t rows, scales, total;
 };
 
 ProductWs product_ws(uint8_t* base, int64_t n_slots, int32_t n_experts, int64_t ncols) {
     ProductWs L{};
     size_t at = al256(fp8_order_layout(base, n_slots, n_experts, false, &L.order));
-    const size_t copied = fp8_copies_rows(n_slots, n_experts) ? static_cast<size_t>(n_slots) : 0;
+    L.width = fp8_tile_width(n_slots, n_experts);
+    const size_t copied = L.width == kWideTile ? static_cast<size_t>(n_slots) : 0;
     L.rows = take_bytes(&at, copied * static_cast<size_t>(ncols));
     L.scales = take_bytes(&at, copied * static_cast<size_t>(fp8_scale_pitch(ncols)) * 4);
     L.total = at;
@@ -164,20 +166,20 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
     p.nrows = nrows;
     p.ncols = ncols;
     p.n_experts = n_experts;
-    const int width = fp8_tile_width(n_slots, n_experts);
+    const int width = dense ? fp8_tile_width(n_slots, 1) : L.width;
     if (!dense) {
         p.ids = ids;
         p.order = &L.order;
         if (!fp8_orders_itself(n_slots, n_experts, width))
             if (int st = launch_fp8_order(ids, n_slots, n_experts, width, L.order, s)) return st;
-        if (fp8_copies_rows(n_slots, n_experts))
+        if (width == kWideTile)
             if (int st = launch_fp8_order_rows(&p, ws + L.rows, reinterpret_cast<float*>(ws + L.scales), s)) return st;
     }
     return launch_fp8_product(p, width, out, out_dtype, err, s);
 }
 
-// Workspace of a layer: router order; x's codes and scales, in router order where a
-// batch has many slots per expert (`spread`), else by token; the gated values' codes and
+// Workspace of a layer: router order; x's codes and scales, in router order for wide
+// tiles (`spread`), else by token; the gated values' codes and
 // scales in router order; where the first product does not quantize them itself
 // (n_inter % 128 != 0, or few slots per expert) its fp32 rows, codes by slot and (`spread`) copies
 // of them in router order; the second product's bf16 rows.
@@ -190,9 +192,9 @@ struct LayerWs {
 
 LayerWs layer_ws(uint8_t* base, int64_t tokens, int64_t n_slots, int32_t n_experts, int64_t hidden, int64_t n_inter) {
     LayerWs L{};
-    L.spread = fp8_copies_rows(n_slots, n_experts);
     L.width = fp8_tile_width(n_slots, n_experts);
-    L.gated = L.width == 256 && n_inter % kFp8Block == 0;
+    L.spread = L.width == kWideTile;
+    L.gated = L.spread && n_inter % kFp8Block == 0;
     size_t at = al256(fp8_order_layout(base, n_slots, n_experts, L.spread, &L.order));
     const size_t S = static_cast<size_t>(n_slots), X = L.spread ? S : static_cast<size_t>(tokens);
     L.xq = take_bytes(&at, X * hidden);

@@ -201,16 +201,18 @@ struct Fp8Product {
     float* mid_scales;
     int32_t mid_pitch, act_kind;
 };
-// Slots per tile for a batch (16 or 32: moe_fp8_narrow.cu; 256: moe_fp8.cu); the order's
-// tiles must be of that width.  fp8_orders_itself: the product needs no launch_fp8_order before it.
+// Slots per tile for a batch (1: moe_fp8_gemv.cu; 16 or 32: moe_fp8_narrow.cu; 256:
+// moe_fp8.cu); the order's tiles must be of that width.  fp8_orders_itself: the product needs no launch_fp8_order before it.
+// Tiles of 256 take rows in router order only.
+constexpr int kWideTile = 256;
 int fp8_tile_width(int64_t n_slots, int32_t n_experts);
 bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width);
 int launch_fp8_product(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
+int launch_fp8_gemv(const Fp8Product& p, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
 int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
 // Copies the rows of p to router order (codes, scales: room for n_slots rows) and makes p `ordered`.
 int launch_fp8_order_rows(Fp8Product* p, uint8_t* codes, float* scales, cudaStream_t s);
-// Whether a batch's rows should be copied to router order, and the pitch of scales there.
-bool fp8_copies_rows(int64_t n_slots, int32_t n_experts);
+// Pitch of rows of scales in router order.
 inline int32_t fp8_scale_pitch(int64_t ncols) { return static_cast<int32_t>(((ncols + 127) / 128 + 3) / 4 * 4); }
 
 }  // namespace ft

@@ -24,9 +24,8 @@
 //   8 drain warps  in two warpgroups, one per 128 weight rows (half) of the tile; warp w:
 //                  TMEM lanes 32 (w % 4) .. + 31, one slot per thread
 //   producer       TMA: the weight boxes, and the slots' rows in boxes of 32
-//                  neighbouring rows (router order), or four at a time by index
-//                  (gather), with 128-byte swizzle; columns past the row's end
-//                  arrive as 0
+//                  neighbouring rows, with 128-byte swizzle; columns past the
+//                  row's end arrive as 0
 //   MMA            (leader CTA) per block and half four MMAs of 32 columns, into
 //                  one of the half's two accumulators of 128 columns
 //
@@ -34,9 +33,8 @@
 // takes about 1000 cycles on top of the MMAs (637 a block) and the drain: four
 // accumulators of 128 columns in flight hide more of it than two of 256.
 //
-// A gather fetches four 128-byte rows per instruction and the TMA unit takes about
-// 85 cycles for one, so 128 slots a CTA would need 2700 cycles a block: batches
-// with many slots per expert first copy their rows to router order.
+// Rows lie in router order: a TMA gather fetches four 128-byte rows per instruction
+// and takes the unit about 85 cycles, so 128 slots a CTA would need 2700 a block.
 #include "fp8_order.cuh"
 #include "fp8_tc.cuh"
 #include "ft_internal.h"
@@ -75,6 +73,7 @@ struct Pair {
     static constexpr int OFF_ORDER = OFF_TMEM + 16;
     static constexpr int SMEM_BYTES = OFF_ORDER + 2 * (MAX_E + 1) * 4 + 1024;    // + alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(2 * BM == kWideTile, "slots per tile");
 };
 
 struct PairArgs {
@@ -86,10 +85,9 @@ struct PairArgs {
     const float* w_scales;
     uint32_t* err;
     int64_t n_slots, nrows;
-    int32_t act_div, n_experts, nb, row_tiles, row_blocks;
+    int32_t n_experts, nb, row_tiles, row_blocks;
     int32_t scale_pitch;         // act_scales: elements between rows
     bool scale_words;            // four neighbouring activation scales from a multiple of 4 on are a 16-byte word
-    bool ordered;                // act rows and scales lie in router order
     bool wide;                   // the rows of out are whole 16-byte words
     // gated: the weight rows are n_inter gate rows and n_inter up rows; a tile is 128 of
     // each, and the epilogue writes codes and scales of act(gate) * up in router order
@@ -194,7 +192,7 @@ __device__ __forceinline__ float act_mul_fast(float g, float up, int32_t kind) {
 }
 
 // GATED: TO is unused.
-template <typename TO, bool GATHER, bool GATED>
+template <typename TO, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     moe_fp8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         const PairArgs args, TO* __restrict__ out) {
@@ -257,20 +255,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         for (int64_t w = w0; w < total && ok; w += dw) {
             const PairTile t = pair_tile(a, w);
             const int32_t mine = t.mine(rank), other = t.mine(rank ^ 1u);
-            // lane l copies 4 (gather) or 32 of this CTA's slots
-            constexpr int PER = GATHER ? 4 : C::ROW_BOX;
+            constexpr int PER = C::ROW_BOX;      // lane l copies 32 of this CTA's slots
             const bool copies = static_cast<int32_t>(lane) * PER < mine;
-            int32_t y[4] = {0, 0, 0, 0};
-            if (copies) {
-                const int32_t p = t.first(rank) + static_cast<int32_t>(lane) * PER;
-                if constexpr (GATHER) {
-                    const int32_t last = t.first(rank) + mine - 1;      // the last rows of a part group repeat it
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = a.perm[min(p + i, last)] / a.act_div;
-                } else {
-                    y[0] = p;
-                }
-            }
+            const int32_t y = t.first(rank) + static_cast<int32_t>(lane) * PER;
             // half h of the tile (weight rows 128 h ..): this CTA's part of its MMA's columns
             const int32_t halves = t.width > C::CW ? 2 : 1;
             const int64_t row0 = static_cast<int64_t>(t.e) * a.nrows + t.r0;
@@ -287,11 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                 if (static_cast<int32_t>(lane) < halves)
                     tma_load_2d_pair(dst + C::A_BYTES + lane * (C::BOX * kFp8Block), &wmap, b * kFp8Block, wy, bar);
-                if (copies) {
-                    const uint32_t d = dst + lane * (PER * kFp8Block);
-                    if constexpr (GATHER) tma_gather4_pair(d, &xmap, b * kFp8Block, y, bar);
-                    else tma_load_2d_pair(d, &xmap, b * kFp8Block, y[0], bar);
-                }
+                if (copies) tma_load_2d_pair(dst + lane * (PER * kFp8Block), &xmap, b * kFp8Block, y, bar);
                 __syncwarp();
             }
         }
@@ -364,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             if (m < mine) {
                 const int32_t p = t.first(rank) + m;
                 slot = a.perm ? a.perm[p] : p;
-                sa += static_cast<int64_t>(a.ordered ? p : slot / a.act_div) * a.scale_pitch;
+                sa += static_cast<int64_t>(p) * a.scale_pitch;
             }
             const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + (GATED ? t.r0 / 2 : r0) / kFp8Block) * nb;
             uint64_t acc[C::CW / 2];
@@ -551,13 +534,21 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------- host
 namespace {
 
-// Routed slots per expert on average from which the rows are copied to router order first.
-constexpr int kGatherMean = 24;
+// Slots per expert on average up to which a batch's slots are matrix-vector products of
+// their own, go by tiles of 16 and of 32.  Measured (us, experts' matrices 768 x 2048 of 128,
+// and 14336 x 4096 of 8): one slot each / 16 / 32 / 256 at
+//   0.25: 8.1 / 15.5 / 17.2 / 26.4    25.5 / 28.1 / 29.9 / 40.5
+//   0.5:  16.9 / 16.2 / 17.7 / 35.7   41.4 / 41.6 / 42.3 / 62.6
+//   1:    32 / 27 / 28 / 48           78 / 60 / 61 / 92
+//   8:    - / 38.4 / 39.0 / 61.9      - / 74.3 / 75.0 / 104.8
+//   16:   - / 45.7 / 45.8 / 66.6      - / 90.9 / 77.4 / 103.5
+//   32:   - / 60.0 / 53.7 / 70.2      (768 x 2048)
+constexpr double kGemvMean = 0.5, kMean16 = 12, kMean32 = 36;
 
-template <typename TO, bool GATHER, bool GATED>
+template <typename TO, bool GATED>
 int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs& a, void* out, int grid, cudaStream_t s) {
     using C = Pair;
-    const void* k = reinterpret_cast<const void*>(moe_fp8_pair_kernel<TO, GATHER, GATED>);
+    const void* k = reinterpret_cast<const void*>(moe_fp8_pair_kernel<TO, GATED>);
     static int regs = 0;     // of this instantiation: with fewer than LAUNCH_REGS the split of registers would never end
     if (regs == 0) {
         cudaFuncAttributes at{};
@@ -568,7 +559,7 @@ int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs
     if (regs * C::THREADS < C::DRAIN_REGS * 256 + C::OTHER_REGS * 128)
         return fail(FT_ERR_LAUNCH, "moe_fp8_pair_kernel was compiled with %d registers, %d are needed", regs, C::LAUNCH_REGS);
     if (int st = set_smem_limit(k, C::SMEM_BYTES)) return st;
-    moe_fp8_pair_kernel<TO, GATHER, GATED><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, static_cast<TO*>(out));
+    moe_fp8_pair_kernel<TO, GATED><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, static_cast<TO*>(out));
     return check_launch("moe_fp8_pair_kernel", dim3(grid), dim3(C::THREADS), C::SMEM_BYTES);
 }
 
@@ -576,10 +567,9 @@ int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs
 
 int fp8_tile_width(int64_t n_slots, int32_t n_experts) {
     const double mean = static_cast<double>(n_slots) / n_experts;
-    return mean <= 12 ? 16 : mean <= 24 ? 32 : 2 * Pair::BM;
+    if (n_slots == 1 || mean <= kGemvMean) return 1;
+    return mean <= kMean16 ? 16 : mean <= kMean32 ? 32 : kWideTile;
 }
-
-bool fp8_copies_rows(int64_t n_slots, int32_t n_experts) { return n_slots > static_cast<int64_t>(kGatherMean) * n_experts; }
 
 size_t fp8_order_layout(uint8_t* base, int64_t n_slots, int32_t n_experts, bool with_pos, Fp8Order* o) {
     size_t at = 0;
@@ -630,22 +620,20 @@ int launch_fp8_order_rows(Fp8Product* p, uint8_t* codes, float* scales, cudaStre
 
 int launch_fp8_product(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s) {
     using C = Pair;
+    if (width == 1) return launch_fp8_gemv(p, out, out_dtype, err, s);
     if (width < 2 * C::BM) return launch_fp8_narrow(p, width, out, out_dtype, err, s);
-    const bool gated = p.mid != nullptr, boxes = p.ordered || !p.ids;      // rows that lie in order arrive in boxes
     PairArgs a{};
     a.act_scales = p.act_scales;
     a.w_scales = p.w_scales;
     a.err = err;
     a.n_slots = p.n_slots;
     a.nrows = p.nrows;
-    a.act_div = p.act_div;
     a.n_experts = p.n_experts;
     a.nb = static_cast<int32_t>(fp8_blocks(p.ncols));
     a.row_blocks = static_cast<int32_t>(fp8_blocks(p.nrows));
     a.row_tiles = static_cast<int32_t>((p.nrows + C::BN - 1) / C::BN);
     a.scale_pitch = p.scale_pitch;
     a.scale_words = p.scale_pitch % 4 == 0 && reinterpret_cast<uintptr_t>(p.act_scales) % 16 == 0;
-    a.ordered = boxes;
     a.wide = p.nrows * (out_dtype == FT_DTYPE_F32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
     a.mid = p.mid;
     a.mid_scales = p.mid_scales;
@@ -664,16 +652,14 @@ int launch_fp8_product(const Fp8Product& p, int width, void* out, int out_dtype,
                            CU_TENSOR_MAP_SWIZZLE_128B, "FP8 weights"))
         return st;
     if (int st = encode_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.act, p.ncols, p.act_rows, p.ncols, kFp8Block,
-                           boxes ? C::ROW_BOX : 1, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
+                           C::ROW_BOX, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
         return st;
     const int64_t slot_tiles = (p.n_slots + 2 * C::BM - 1) / (2 * C::BM) + (p.ids ? (p.n_experts < p.n_slots ? p.n_experts : p.n_slots) : 0);
     const int64_t pairs = slot_tiles * a.row_tiles, most = sm_count() / 2;
     const int grid = 2 * static_cast<int>(pairs < most ? pairs : most);
-    if (gated) return boxes ? launch_pair<float, false, true>(wmap, xmap, a, nullptr, grid, s) : launch_pair<float, true, true>(wmap, xmap, a, nullptr, grid, s);
-    if (out_dtype == FT_DTYPE_F32)
-        return boxes ? launch_pair<float, false, false>(wmap, xmap, a, out, grid, s) : launch_pair<float, true, false>(wmap, xmap, a, out, grid, s);
-    return boxes ? launch_pair<__nv_bfloat16, false, false>(wmap, xmap, a, out, grid, s)
-                 : launch_pair<__nv_bfloat16, true, false>(wmap, xmap, a, out, grid, s);
+    if (p.mid) return launch_pair<float, true>(wmap, xmap, a, nullptr, grid, s);
+    return out_dtype == FT_DTYPE_F32 ? launch_pair<float, false>(wmap, xmap, a, out, grid, s)
+                                     : launch_pair<__nv_bfloat16, false>(wmap, xmap, a, out, grid, s);
 }
 
 }  // namespace ft

@@ -9,7 +9,8 @@
 // lies behind in shared memory and are not read.
 //
 // Blocks go through tensor memory in units of 64 columns (two blocks of 32 slots or four
-// of 16), so that the drain waits once per unit and the MMAs of eight units run ahead of it.
+// of 16), so that the drain waits once per unit and the MMAs of four units run ahead of it.  Two CTAs
+// share an SM, so that one streams while the other starts or ends.
 //
 // Up to 1024 slots are put in order by every CTA for itself, in shared memory (some 2 us
 // less than a launch and the reads of its results); more come ordered.
@@ -31,10 +32,11 @@ struct Narrow {
     static constexpr int BM = 128;                                  // lanes; weight rows of a tile at most
     static constexpr int G = 64 / NW;                               // blocks per unit
     static constexpr int UNIT = G * NW;                             // columns of a unit
-    static constexpr int UNITS = 512 / UNIT;
+    static constexpr int TMEM_COLS = 256;                           // two CTAs per SM
+    static constexpr int UNITS = TMEM_COLS / UNIT;
     static constexpr int NSC = 4;                                   // units in the scale ring
     static constexpr int MAX_STAGES = 16;
-    static constexpr int RING_BYTES = 160 * 1024;
+    static constexpr int RING_BYTES = 80 * 1024;
     static constexpr int SLACK = BM * kFp8Block;                    // what an MMA reads past the last short tile
     static constexpr int OFF_SC = RING_BYTES + SLACK;
     static constexpr int OFF_BAR = OFF_SC + NSC * UNIT * 4;
@@ -48,7 +50,7 @@ struct Narrow {
     static constexpr int WARP_PRODUCER = 4, WARP_MMA = 5, WARP_SCALE = 6;
     static constexpr int THREADS = 256;
     static constexpr int ROW_BOX = 16;
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "shared memory budget of two CTAs");
 };
 
 struct NarrowArgs {
@@ -90,7 +92,7 @@ __device__ __forceinline__ NarrowTile narrow_tile(const NarrowArgs& a, int64_t w
 }
 
 template <int NW, typename TO, bool GATHER>
-__global__ void __launch_bounds__(Narrow<NW>::THREADS, 1)
+__global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
     moe_fp8_narrow_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                           const NarrowArgs args, TO* __restrict__ out) {
     using C = Narrow<NW>;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 1)
         fence_mbar_init();
     }
     if (warp == C::WARP_MMA) {
-        tmem_alloc(tmem_slot, 512);
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
     if (warp == C::WARP_PRODUCER && lane == 0) {
@@ -253,24 +255,36 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 1)
                 sa = a.act_scales + static_cast<int64_t>(a.ordered ? p : a.perm[p] / a.act_div) * a.scale_pitch;
             }
             const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + t.r0 / kFp8Block) * nb;
-            float v[C::G], x[C::G];                      // of the unit to come
-            auto load = [&](int32_t b0) {
+            // a load takes longer than a unit: those of four units are in flight
+            constexpr int AHEAD = 4;
+            float v[AHEAD][C::G], x[AHEAD][C::G];
+            auto load = [&](int q, int32_t b0) {
 #pragma unroll
                 for (int g = 0; g < C::G; ++g) {
-                    x[g] = b0 + g < nb ? __ldg(sw + b0 + g) : 0.0f;
-                    v[g] = sa && b0 + g < nb ? __ldg(sa + b0 + g) : 0.0f;
+                    x[q][g] = b0 + g < nb ? __ldg(sw + b0 + g) : 0.0f;
+                    v[q][g] = sa && b0 + g < nb ? __ldg(sa + b0 + g) : 0.0f;
                 }
             };
-            load(0);
-            for (int32_t b0 = 0; b0 < nb; b0 += C::G, ++unit) {
-                const uint32_t r = unit % C::NSC;
-                if (!mbar_wait_warp(&sc_empty[r], ((unit / C::NSC) & 1u) ^ 1u, a.err)) { ok = false; break; }
 #pragma unroll
-                for (int g = 0; g < C::G; ++g)
-                    if (lane < static_cast<uint32_t>(NW)) sc_ring[r * C::UNIT + g * NW + lane] = v[g] * x[g];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sc_full[r]);
-                if (b0 + C::G < nb) load(b0 + C::G);
+            for (int q = 0; q < AHEAD; ++q) load(q, q * C::G);
+            for (int32_t b0 = 0; b0 < nb && ok; b0 += AHEAD * C::G) {
+#pragma unroll
+                for (int q = 0; q < AHEAD; ++q) {
+                    if (b0 + q * C::G < nb && ok) {
+                        const uint32_t r = unit % C::NSC;
+                        if (!mbar_wait_warp(&sc_empty[r], ((unit / C::NSC) & 1u) ^ 1u, a.err)) {
+                            ok = false;
+                        } else {
+#pragma unroll
+                            for (int g = 0; g < C::G; ++g)
+                                if (lane < static_cast<uint32_t>(NW)) sc_ring[r * C::UNIT + g * NW + lane] = v[q][g] * x[q][g];
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sc_full[r]);
+                            ++unit;
+                            load(q, b0 + (q + AHEAD) * C::G);
+                        }
+                    }
+                }
             }
         }
     } else if (warp < n_drain) {
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == C::WARP_MMA) tmem_dealloc(tmem, 512);
+    if (warp == C::WARP_MMA) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 // ------------------------------------------------------------------- host
@@ -342,8 +356,8 @@ int launch_narrow(const CUtensorMap& wmap, const CUtensorMap& xmap, NarrowArgs& 
     const int stage = (NW + a.br) * kFp8Block;
     a.stages = C::RING_BYTES / stage < C::MAX_STAGES ? C::RING_BYTES / stage : C::MAX_STAGES;
     if (int st = set_smem_limit(k, C::SMEM_BYTES)) return st;
-    const int64_t sms = sm_count();
-    const dim3 grid(static_cast<unsigned>(tiles < sms ? tiles : sms));
+    const int64_t ctas = 2 * sm_count();
+    const dim3 grid(static_cast<unsigned>(tiles < ctas ? tiles : ctas));
     moe_fp8_narrow_kernel<NW, TO, GATHER><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, static_cast<TO*>(out));
     return check_launch("moe_fp8_narrow_kernel", grid, dim3(C::THREADS), C::SMEM_BYTES);
 }
@@ -361,7 +375,7 @@ int launch_narrow_width(const CUtensorMap& wmap, const CUtensorMap& xmap, Narrow
 }  // namespace
 
 bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width) {
-    return width <= 32 && n_slots <= kChunk && n_experts <= Narrow<16>::MAX_E;
+    return width == 1 || (width <= 32 && n_slots <= kChunk && n_experts <= Narrow<16>::MAX_E);
 }
 
 // width: slots per tile (16 or 32), that of p.order's tiles
@@ -389,10 +403,10 @@ int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, 
     const int64_t some = p.ids ? (p.n_experts < p.n_slots ? p.n_experts : p.n_slots) : 1;
     const int64_t most_tiles = (p.n_slots + width - 1) / width + (p.ids ? some : 0);
     // shorter tiles where those of 128 rows, over the experts that a batch is likely to
-    // touch, would leave SMs without one
+    // touch, would leave SMs without two
     const int64_t likely = p.ids ? (some > (p.n_slots + width - 1) / width ? some : (p.n_slots + width - 1) / width) : most_tiles;
     a.br = 128;
-    while (a.br > 32 && likely * ((p.nrows + a.br - 1) / a.br) < sm_count()) a.br /= 2;
+    while (a.br > 32 && likely * ((p.nrows + a.br - 1) / a.br) < 2 * sm_count()) a.br /= 2;
     a.row_tiles = static_cast<int32_t>((p.nrows + a.br - 1) / a.br);
     CUtensorMap wmap, xmap;
     if (int st = encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weights, p.ncols,
