@@ -244,8 +244,8 @@ static int quantize_entry(const void* x, int32_t dtype, void* codes, float* scal
     if (!mul_ok(rows, ncols, &n) || ncols / kFp8Block >= INT32_MAX) return fail(FT_ERR_SIZE, "rows * ncols overflows");
     if (rows == 0) return FT_OK;
     if (!x || !codes || !scales) return fail(FT_ERR_ARG, "null pointer");
-    if (!aligned(x, 16) || !aligned(codes, 4) || !aligned(scales, 4))
-        return fail(FT_ERR_ALIGN, "x must be 16-byte, codes and scales 4-byte aligned");
+    if (!aligned(x, 16) || !aligned(codes, 8) || !aligned(scales, 4))
+        return fail(FT_ERR_ALIGN, "x must be 16-byte, codes 8-byte and scales 4-byte aligned");
     return launch_quantize_fp8(x, dtype, static_cast<uint8_t*>(codes), scales, rows, ncols, gated, act_kind,
                                static_cast<cudaStream_t>(stream));
 }

@@ -12,7 +12,12 @@
 //         where no expert is left
 //   w   = s[ids], renormalised by max(sum, 1e-30) if asked, times `scale`
 //
-// One warp per token.  The keys lie in shared memory; each lane keeps the best
+// Up to 512 experts in one group: 2, 8, 16 or 32 lanes per token, 16 neighbouring experts
+// each, in registers.  A key and the complement of its expert make one integer (32 bits where
+// 16-bit logits are the keys, else 64), whose maximum over the lanes is the choice with its
+// tie rule: a round is a few shuffles, and the lane that held the maximum looks again.
+//
+// Otherwise one warp per token.  The keys lie in shared memory; each lane keeps the best
 // key of its experts (every 32nd), and one round per chosen expert takes the
 // warp's best of those with two integer warp reductions (largest key, then the
 // lowest index that has it) and lets the lane that held it look again.
@@ -179,6 +184,155 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const GateArg
     }
 }
 
+// ------------------------------------------------------------ few experts
+constexpr int kGateThreads = 128, kGatePer = 16;      // experts per lane
+
+// 16-bit float bits -> order-preserving 16-bit integer, zeros of both signs alike.
+__device__ __forceinline__ uint32_t order16(uint32_t b) {
+    b = b == 0x8000u ? 0u : b;
+    return (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
+}
+
+template <typename T>
+__device__ __forceinline__ float order16_value(uint32_t o) {
+    const uint16_t b = static_cast<uint16_t>((o & 0x8000u) ? (o ^ 0x8000u) : (~o & 0xFFFFu));
+    return to_f32<T>(*reinterpret_cast<const T*>(&b));
+}
+
+__device__ __forceinline__ float order32_value(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
+}
+
+// K: uint32_t (T is 16-bit and the keys are logits) or uint64_t.  WIDE: rows start at whole
+// 16-byte words.
+template <typename T, int LANES, typename K, bool WIDE>
+__global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateArgs a) {
+    constexpr bool PACKED = sizeof(K) == 4;
+    const uint32_t sub = threadIdx.x & (LANES - 1);
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * (kGateThreads / LANES) + threadIdx.x / LANES;
+    const bool there = t0 < a.tokens;
+    const int64_t t = there ? t0 : a.tokens - 1;
+    const int32_t E = a.n_experts, e0 = static_cast<int32_t>(sub) * kGatePer;
+    const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+    const bool by_logit = PACKED || a.bias == nullptr;
+    T raw[kGatePer];
+    if (WIDE && e0 + kGatePer <= E) {
+        constexpr int WORDS = kGatePer * static_cast<int>(sizeof(T)) / 16;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            reinterpret_cast<uint4*>(raw)[i] = __ldg(reinterpret_cast<const uint4*>(row + e0) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kGatePer; ++i) raw[i] = e0 + i < E ? row[e0 + i] : from_f32<T>(-INFINITY);
+    }
+    float top = -INFINITY, sum = 0.0f;
+    if (a.score == FT_SCORE_SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < kGatePer; ++i) top = fmaxf(top, to_f32<T>(raw[i]));
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        // renormalised weights of the largest logits need no sum over all: it cancels
+        if (!(by_logit && a.renormalize)) {
+#pragma unroll
+            for (int i = 0; i < kGatePer; ++i) sum += gate_exp(to_f32<T>(raw[i]), top);
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        }
+    }
+    K key[kGatePer], best = 0;
+#pragma unroll
+    for (int i = 0; i < kGatePer; ++i) {
+        const float l = to_f32<T>(raw[i]);
+        bool ok = l > -INFINITY;
+        if constexpr (PACKED) {
+            key[i] = (order16(*reinterpret_cast<const uint16_t*>(&raw[i])) << 16) | (0xFFFFu - static_cast<uint32_t>(e0 + i));
+        } else {
+            float x = l;
+            if (!by_logit) {
+                x = e0 + i < E ? gate_score(l, top, sum, a.score) + __ldg(a.bias + e0 + i) : -INFINITY;
+                ok = ok && x > -INFINITY;
+            }
+            key[i] = (static_cast<uint64_t>(float_order(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e0 + i));
+        }
+        if (!ok) key[i] = 0;
+        best = key[i] > best ? key[i] : best;
+    }
+    int32_t* ids = a.ids + t * a.top_k;
+    float* weights = a.weights + t * a.top_k;
+    float total = 0.0f, mine = 0.0f;      // mine: weight `sub` (of the first LANES)
+    const bool few = a.top_k <= LANES, cancel = by_logit && a.renormalize && a.score == FT_SCORE_SOFTMAX;
+    for (int32_t j = 0; j < a.top_k; ++j) {
+        K m = best;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            const K other = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+            m = other > m ? other : m;
+        }
+        if (m != 0 && best == m) {
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < kGatePer; ++i) {
+                key[i] = key[i] == m ? 0 : key[i];
+                best = key[i] > best ? key[i] : best;
+            }
+        }
+        int32_t at = -1;
+        float w = 0.0f;
+        if (m != 0) {
+            float l;
+            if constexpr (PACKED) {
+                at = static_cast<int32_t>(0xFFFFu - (m & 0xFFFFu));
+                l = order16_value<T>(static_cast<uint32_t>(m) >> 16);
+            } else {
+                at = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(m));
+                l = by_logit ? order32_value(static_cast<uint32_t>(m >> 32)) : to_f32<T>(row[at]);
+            }
+            w = cancel ? gate_exp(l, top) : gate_score(l, top, sum, a.score);
+        }
+        total += w;
+        if (there && sub == static_cast<uint32_t>(j & (LANES - 1))) {
+            mine = w;
+            ids[j] = at;
+            if (!few) weights[j] = a.renormalize ? w : w * a.scale;
+        }
+    }
+    if (!there) return;
+    total = fmaxf(total, kGateTiny);
+    if (few) {
+        if (sub < static_cast<uint32_t>(a.top_k)) weights[sub] = (a.renormalize ? __fdiv_rn(mine, total) : mine) * a.scale;
+    } else if (a.renormalize) {
+        for (int32_t j = static_cast<int32_t>(sub); j < a.top_k; j += LANES)      // each lane rereads what it wrote
+            weights[j] = __fdiv_rn(weights[j], total) * a.scale;
+    }
+}
+
+template <typename T, int LANES, typename K>
+static int launch_few(const GateArgs& a, cudaStream_t s) {
+    const int64_t per = kGateThreads / LANES, ctas = (a.tokens + per - 1) / per;
+    if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "too many tokens for one launch");
+    const dim3 grid(static_cast<unsigned>(ctas)), block(kGateThreads);
+    const bool wide = a.stride * static_cast<int64_t>(sizeof(T)) % 16 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+    if (wide) moe_gate_few_kernel<T, LANES, K, true><<<grid, block, 0, s>>>(a);
+    else moe_gate_few_kernel<T, LANES, K, false><<<grid, block, 0, s>>>(a);
+    return check_launch("moe_gate_few_kernel", grid, block, 0);
+}
+
+template <typename T>
+static int launch_few_typed(const GateArgs& a, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (a.bias == nullptr) {
+            if (a.n_experts <= 2 * kGatePer) return launch_few<T, 2, uint32_t>(a, s);
+            if (a.n_experts <= 8 * kGatePer) return launch_few<T, 8, uint32_t>(a, s);
+            if (a.n_experts <= 16 * kGatePer) return launch_few<T, 16, uint32_t>(a, s);
+            return launch_few<T, 32, uint32_t>(a, s);
+        }
+    }
+    if (a.n_experts <= 2 * kGatePer) return launch_few<T, 2, uint64_t>(a, s);
+    if (a.n_experts <= 8 * kGatePer) return launch_few<T, 8, uint64_t>(a, s);
+    if (a.n_experts <= 16 * kGatePer) return launch_few<T, 16, uint64_t>(a, s);
+    return launch_few<T, 32, uint64_t>(a, s);
+}
+
 int launch_gate(const GateParams& p, const void* logits, int dtype, int64_t stride, int32_t* ids, float* weights,
                 cudaStream_t s) {
     if (p.tokens == 0) return FT_OK;
@@ -197,6 +351,10 @@ int launch_gate(const GateParams& p, const void* logits, int dtype, int64_t stri
     a.group_top = p.group_top;
     a.renormalize = p.renormalize;
     a.scale = p.scale;
+    if (p.n_groups == 1 && p.n_experts <= 32 * kGatePer)
+        return dtype == FT_DTYPE_F32   ? launch_few_typed<float>(a, s)
+               : dtype == FT_DTYPE_F16 ? launch_few_typed<__half>(a, s)
+                                       : launch_few_typed<__nv_bfloat16>(a, s);
     const int64_t ctas = (p.tokens + kGateWarps - 1) / kGateWarps;
     if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "too many tokens for one launch");
     const dim3 grid(static_cast<unsigned>(ctas)), block(32 * kGateWarps);

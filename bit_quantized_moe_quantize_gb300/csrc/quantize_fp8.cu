@@ -5,11 +5,11 @@
 //   code  = e4m3(v / scale), round to nearest even; a block whose scale is 0
 //           gets codes 0
 //
-// A warp takes one block of a row: lane i its values 4 i .. 4 i + 3 (columns
-// past the row's end count as 0 and are not stored), five shuffles find the
-// largest magnitude.  Both quotients are IEEE divisions, so the codes are those
-// of any IEEE evaluation of the formula.  A non-finite value makes its block's
-// scale infinite or NaN, and what is divided by it 0 or NaN.
+// Half a warp takes one block of a row: lane i its values 8 i .. 8 i + 7 (columns past the
+// row's end count as 0 and are not stored), four shuffles find the largest magnitude.  The
+// codes are those of the IEEE quotients; see fp8_codes for how most of them come without a
+// division.  A non-finite value makes its block's scale infinite or NaN, and what is
+// divided by it 0 or NaN.
 #include "fp8_common.cuh"
 #include "ft_internal.h"
 
@@ -17,12 +17,39 @@ namespace ft {
 
 constexpr int kQuantWarps = 8;
 
-// The gated activation of one value: act(g) * up with act(g) = g / (1 + exp(-z)),
-// z = g for SiLU and 2 sqrt(2/pi) (g + 0.044715 g^3) for the tanh form of GELU.
+// The gated activation of one value: act(g) * up with act(g) = g / (1 + exp(-z)), z = g for
+// SiLU and 2 sqrt(2/pi) (g + 0.044715 g^3) for the tanh form of GELU.  The quotient is
+// within two units in the last place.
 __device__ __forceinline__ float act_mul_f32(float g, float up, int kind) {
     const float cube = __fmul_rn(__fmul_rn(__fmul_rn(0.044715f, g), g), g);
     const float z = kind == FT_ACT_SILU ? g : __fmul_rn(1.5957691216057308f, __fadd_rn(g, cube));
-    return __fdiv_rn(g, 1.0f + expf(-z)) * up;
+    return __fdividef(g, 1.0f + expf(-z)) * up;
+}
+
+// Codes of v / scale for eight values.  y = v * (1 / scale) lies within 2^-22 |v / scale| of
+// the IEEE quotient (two roundings of half a unit against one), so both round to the same
+// code unless y (1 - 2^-21) and y (1 + 2^-21) do not; only then, or where 1 / scale could
+// overflow, are the quotients formed.
+__device__ __forceinline__ uint2 fp8_codes(const float (&v)[8], float scale) {
+    const float inv = __frcp_rn(scale);
+    uint32_t lo[2], hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(v[4 * h + j], inv);
+        constexpr float D = 1.0f - 0x1p-21f, U = 1.0f + 0x1p-21f;
+        lo[h] = e4m3x4(y[0] * D, y[1] * D, y[2] * D, y[3] * D);
+        hi[h] = e4m3x4(y[0] * U, y[1] * U, y[2] * U, y[3] * U);
+    }
+    if (lo[0] != hi[0] || lo[1] != hi[1] || !(scale > 1.0e-36f)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            lo[h] = scale == 0.0f ? 0u
+                                  : e4m3x4(__fdiv_rn(v[4 * h], scale), __fdiv_rn(v[4 * h + 1], scale),
+                                           __fdiv_rn(v[4 * h + 2], scale), __fdiv_rn(v[4 * h + 3], scale));
+    }
+    return make_uint2(lo[0], lo[1]);
 }
 
 // GATED: x holds rows of 2 ncols values, gate then up.  SPREAD: row r is a token's, and
@@ -32,46 +59,44 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
     quantize_fp8_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, float* __restrict__ scales,
                         int64_t n_blocks, int32_t nb, int64_t ncols, int kind, const int32_t* __restrict__ pos, int32_t k,
                         int32_t pitch) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5);
-    if (i >= n_blocks) return;
-    const int64_t row = i / nb;
-    const int64_t c = (i - row * nb) * kFp8Block + 4 * static_cast<int64_t>(lane_id());
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < ncols) {      // ncols % 16 == 0: a lane's four values are all inside or all outside
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5)) * 2 + (lane_id() >> 4);
+    const uint32_t sub = lane_id() & 15u;
+    const bool there = i < n_blocks;
+    const int64_t row = there ? i / nb : 0;
+    const int64_t c = (there ? i - row * nb : 0) * kFp8Block + 8 * static_cast<int64_t>(sub);
+    const bool in = there && c < ncols;      // ncols % 16 == 0: a lane's eight values are all inside or all outside
+    float v[8] = {};
+    if (in) {
         if constexpr (GATED) {
-            float g[4], u[4];
-            load_vec<T, 4>(x + row * 2 * ncols + c, g);
-            load_vec<T, 4>(x + row * 2 * ncols + ncols + c, u);
+            float g[8], u[8];
+            load_vec<T, 8>(x + row * 2 * ncols + c, g);
+            load_vec<T, 8>(x + row * 2 * ncols + ncols + c, u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = act_mul_f32(g[j], u[j], kind);
+            for (int j = 0; j < 8; ++j) v[j] = act_mul_f32(g[j], u[j], kind);
         } else {
-            load_vec<T, 4>(x + row * ncols + c, v);
+            load_vec<T, 8>(x + row * ncols + c, v);
         }
     }
-    float amax = 0.0f;
+    // magnitudes order like their bits, and NaN's lie above all others'
+    uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    bool nan = false;
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) nan |= v[j] != v[j];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if (__any_sync(0xFFFFFFFFu, nan)) amax = NAN;
-    const float scale = __fdiv_rn(amax, kFp8Max);
-    uint32_t q = 0;
-    if (c < ncols && scale != 0.0f)
-        q = e4m3x4(__fdiv_rn(v[0], scale), __fdiv_rn(v[1], scale), __fdiv_rn(v[2], scale), __fdiv_rn(v[3], scale));
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float scale = __fdiv_rn(__uint_as_float(top), kFp8Max);
+    if (!in) return;
+    const uint2 q = fp8_codes(v, scale);
     if constexpr (SPREAD) {
         for (int32_t j = 0; j < k; ++j) {
             const int64_t p = __ldg(pos + row * k + j);
             if (p >= 0) {
-                if (c < ncols) *reinterpret_cast<uint32_t*>(codes + p * ncols + c) = q;
-                if (lane_id() == 0) scales[p * pitch + (i - row * nb)] = scale;
+                *reinterpret_cast<uint2*>(codes + p * ncols + c) = q;
+                if (sub == 0) scales[p * pitch + (i - row * nb)] = scale;
             }
         }
     } else {
-        if (lane_id() == 0) scales[i] = scale;
-        if (c < ncols) *reinterpret_cast<uint32_t*>(codes + row * ncols + c) = q;
+        if (sub == 0) scales[i] = scale;
+        *reinterpret_cast<uint2*>(codes + row * ncols + c) = q;
     }
 }
 
@@ -79,7 +104,7 @@ template <typename T, bool GATED, bool SPREAD = false>
 static int launch_typed(const void* x, uint8_t* codes, float* scales, int64_t rows, int64_t ncols, int kind,
                         cudaStream_t s, const int32_t* pos = nullptr, int32_t k = 0, int32_t pitch = 0) {
     const int64_t nb = fp8_blocks(ncols), n_blocks = rows * nb;
-    const int64_t ctas = (n_blocks + kQuantWarps - 1) / kQuantWarps;
+    const int64_t ctas = (n_blocks + 2 * kQuantWarps - 1) / (2 * kQuantWarps);
     if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "rows * ncols too large for one launch");
     const dim3 grid(static_cast<unsigned>(ctas)), block(32 * kQuantWarps);
     quantize_fp8_kernel<T, GATED, SPREAD><<<grid, block, 0, s>>>(static_cast<const T*>(x), codes, scales, n_blocks,

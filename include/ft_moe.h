@@ -625,7 +625,7 @@ FT_API int ft_moe_gate(const void* logits, int32_t dtype, int64_t row_stride, co
  * e4m3 value (ties to even); scale 0 gives codes 0.  A non-finite x makes its
  * block's scale non-finite.
  *   x      device, [rows][ncols] of dtype (FT_DTYPE_*), 16-byte aligned
- *   codes  device, [rows][ncols] out, 4-byte aligned; scales device fp32
+ *   codes  device, [rows][ncols] out, 8-byte aligned; scales device fp32
  *          [rows][ceil(ncols/128)] out
  */
 FT_API int ft_quantize_fp8(const void* x, int32_t dtype, void* codes, float* scales, int64_t rows,
