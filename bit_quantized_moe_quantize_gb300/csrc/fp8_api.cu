@@ -359,6 +359,10 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
 
     const GateParams g{tokens, n_experts, top_k, score, n_groups, topk_groups, group_top, renormalize, scale, bias};
     if (int st = launch_gate(g, logits, logits_dtype, row_stride, topk_ids, topk_weights, s)) return st;
+    if (L.width == 1 && fp8_token_ok(n_slots, tokens, top_k, hidden, n_inter))
+        return launch_fp8_token_layer(x, x_dtype, static_cast<const uint8_t*>(w13), s13, static_cast<const uint8_t*>(w2), s2, topk_ids,
+                                      topk_weights, reinterpret_cast<float*>(ws + L.h), y, tokens, top_k, n_experts, hidden, n_inter,
+                                      act_kind, s);
     if (!fp8_orders_itself(n_slots, n_experts, L.width))
         if (int st = launch_fp8_order(topk_ids, n_slots, n_experts, L.width, L.order, s)) return st;
     float *xs = reinterpret_cast<float*>(ws + L.xs), *ms = reinterpret_cast<float*>(ws + L.ms);

@@ -74,6 +74,20 @@ __device__ __forceinline__ void load_vec(const T* p, float (&v)[N]) {
     }
 }
 
+// The same by ordinary loads, for data that another kernel may have written while this one
+// was already running.
+template <int N>
+__device__ __forceinline__ void load_vec_plain(const float* p, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const float4 w = reinterpret_cast<const float4*>(p)[i];
+        v[4 * i] = w.x;
+        v[4 * i + 1] = w.y;
+        v[4 * i + 2] = w.z;
+        v[4 * i + 3] = w.w;
+    }
+}
+
 // Unsigned integer that orders like the float (-0 and +0 stay equal: the sum
 // with +0 turns -0 into +0); larger is larger, -inf maps above 0.
 __device__ __forceinline__ uint32_t float_order(float v) {

@@ -51,9 +51,12 @@ __device__ __forceinline__ int32_t chunk_rank(const int32_t* __restrict__ ids, i
     uint32_t below;
     asm("mov.u32 %0, %%lanemask_lt;" : "=r"(below));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {      // all four on their way before the first is used
         const int32_t s = s0 + 32 * i, e = s < n_slots ? ids[s] : -1;
         id[i] = e >= 0 && e < E ? e : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[i]);
         rank[i] = id[i] >= 0 ? count[id[i]] + __popc(same & below) : 0;
         __syncwarp();

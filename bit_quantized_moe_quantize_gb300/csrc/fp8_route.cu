@@ -60,16 +60,21 @@ __global__ void __launch_bounds__(kChunkThreads)
     const int32_t s0 = chunk_rank(ids, chunk * kChunk, n_slots, E, mine, id, rank);
     const int32_t* count = mine + static_cast<int32_t>(threadIdx.x >> 5) * E;
     if (hist) {
-        for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) {
+        // the chunks are shared out between the threads that E experts leave
+        const int32_t parts = E < kChunkThreads ? kChunkThreads / E : 1;
+        for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) before[e] = total[e] = 0;
+        __syncthreads();
+        for (int32_t i = threadIdx.x; i < parts * E; i += kChunkThreads) {
+            const int32_t e = i % E, part = i / E;
             int32_t b = 0, t = 0;
-#pragma unroll 8
-            for (int32_t c = 0; c < n_chunks; ++c) {
+#pragma unroll 16
+            for (int32_t c = part; c < n_chunks; c += parts) {
                 const int32_t x = __ldg(hist + static_cast<int64_t>(c) * E + e);
                 t += x;
                 b += c < chunk ? x : 0;
             }
-            before[e] = b;
-            total[e] = t;
+            atomicAdd(&before[e], b);      // whole numbers: the order of the additions does not show
+            atomicAdd(&total[e], t);
         }
         __syncthreads();
     } else {

@@ -212,6 +212,11 @@ int launch_fp8_gemv(const Fp8Product& p, void* out, int out_dtype, uint32_t* err
 int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s);
 // Copies the rows of p to router order (codes, scales: room for n_slots rows) and makes p `ordered`.
 int launch_fp8_order_rows(Fp8Product* p, uint8_t* codes, float* scales, cudaStream_t s);
+// A layer of few tokens after its router (moe_fp8_token.cu); mid: room for n_slots * n_inter floats.
+bool fp8_token_ok(int64_t n_slots, int64_t tokens, int32_t top_k, int64_t hidden, int64_t n_inter);
+int launch_fp8_token_layer(const void* x, int x_dtype, const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2,
+                           const int32_t* ids, const float* weights, float* mid, void* y, int64_t tokens, int32_t top_k,
+                           int32_t n_experts, int64_t hidden, int64_t n_inter, int kind, cudaStream_t s);
 // Pitch of rows of scales in router order.
 inline int32_t fp8_scale_pitch(int64_t ncols) { return static_cast<int32_t>(((ncols + 127) / 128 + 3) / 4 * 4); }
 

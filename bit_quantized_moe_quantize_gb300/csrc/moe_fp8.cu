@@ -55,9 +55,12 @@ struct Pair {
     static constexpr int WARP_PRODUCER = 8, WARP_MMA = 9, N_MMA_WARPS = 2, WARP_ZERO = 11;
     static constexpr int THREADS = 12 * 32;
     // registers: 384 threads are launched with LAUNCH_REGS each; the drain warps
-    // take DRAIN_REGS, and the others give theirs down to OTHER_REGS
-    static constexpr int LAUNCH_REGS = 168, DRAIN_REGS = 216, OTHER_REGS = 72;
-    static_assert(DRAIN_REGS * 256 + OTHER_REGS * 128 <= LAUNCH_REGS * THREADS, "the split must fit the launch's registers");
+    // take drain_regs, and the others give theirs down to other_regs
+    static constexpr int LAUNCH_REGS = 168;
+    static constexpr int drain_regs(bool gated) { return gated ? 216 : 200; }
+    static constexpr int other_regs(bool gated) { return gated ? 72 : 104; }
+    static_assert(216 * 256 + 72 * 128 <= LAUNCH_REGS * THREADS && 200 * 256 + 104 * 128 <= LAUNCH_REGS * THREADS,
+                  "the split must fit the launch's registers");
     static constexpr int CW = BN / 2;              // columns of a half
     static constexpr int STAGE_ROW = 256 + 16;     // output staging: 256 bytes of a slot's row, and 16 so that
                                                    // eight lanes' 16-byte words fall in different banks
@@ -71,7 +74,8 @@ struct Pair {
     // offsets[E + 1] and tiles[E + 1] of up to MAX_E experts (a search in global memory waits for it at every step)
     static constexpr int MAX_E = 1024;
     static constexpr int OFF_ORDER = OFF_TMEM + 16;
-    static constexpr int SMEM_BYTES = OFF_ORDER + 2 * (MAX_E + 1) * 4 + 1024;    // + alignment slack
+    static constexpr int OFF_SLOT = OFF_ORDER + 2 * (MAX_E + 1) * 4;     // [tile parity][drain thread]
+    static constexpr int SMEM_BYTES = OFF_SLOT + 2 * N_DRAIN_WARPS * 32 * 4 + 1024;    // + alignment slack
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
     static_assert(2 * BM == kWideTile, "slots per tile");
 };
@@ -106,26 +110,49 @@ struct PairTile {
     __device__ int32_t cols(int32_t h) const { return min(Pair::CW, width - h * Pair::CW); }
 };
 
-// Work item w: row tile w % row_tiles of slot tile w / row_tiles.
-__device__ __forceinline__ PairTile pair_tile(const PairArgs& a, int64_t w) {
-    PairTile t;
-    const int32_t st = static_cast<int32_t>(w / a.row_tiles), nrows = static_cast<int32_t>(a.nrows);
-    t.r0 = static_cast<int32_t>(w - static_cast<int64_t>(st) * a.row_tiles) * Pair::BN;
-    t.width = (min(Pair::BN, nrows - t.r0) + 31) / 32 * 32;
-    int32_t first = 0, count = static_cast<int32_t>(a.n_slots), j = st;
-    t.e = 0;
-    if (a.tiles) {
-        const int32_t lo = last_not_above(a.tiles, a.n_experts, st);
-        t.e = lo;
-        first = a.offsets[lo];
-        count = a.offsets[lo + 1] - first;
-        j = st - a.tiles[lo];
+// A CTA pair's way through the tiles, `step` apart: row tile rt of slot tile st, of expert
+// e.  The next one costs a few additions and a short walk over the experts; a division and a
+// search per tile took the drain some 600 cycles.
+struct PairWalk {
+    int32_t st, rt, e, step_st, step_rt, row_tiles, slot_tiles;
+
+    __device__ PairWalk(const PairArgs& a, const int32_t* tiles, int32_t first, int32_t step) {
+        row_tiles = a.row_tiles;
+        slot_tiles = tiles ? tiles[a.n_experts] : static_cast<int32_t>((a.n_slots + 2 * Pair::BM - 1) / (2 * Pair::BM));
+        st = first / row_tiles;
+        rt = first - st * row_tiles;
+        step_st = step / row_tiles;
+        step_rt = step - step_st * row_tiles;
+        e = tiles && st < slot_tiles ? last_not_above(tiles, a.n_experts, st) : 0;
     }
-    t.p0 = first + j * (2 * Pair::BM);
-    t.n = min(2 * Pair::BM, count - j * (2 * Pair::BM));
-    t.half = min(t.n, (t.n + 63) / 64 * 32);        // whole warps, nearly even
-    return t;
-}
+    __device__ bool there() const { return st < slot_tiles; }
+    __device__ void next(const int32_t* tiles) {
+        st += step_st;
+        rt += step_rt;
+        if (rt >= row_tiles) {
+            rt -= row_tiles;
+            ++st;
+        }
+        if (tiles && st < slot_tiles)
+            while (tiles[e + 1] <= st) ++e;      // tiles[n_experts] = slot_tiles > st ends it
+    }
+    __device__ PairTile tile(const PairArgs& a, const int32_t* tiles, const int32_t* offsets) const {
+        PairTile t;
+        t.e = e;
+        t.r0 = rt * Pair::BN;
+        t.width = (min(Pair::BN, static_cast<int32_t>(a.nrows) - t.r0) + 31) / 32 * 32;
+        int32_t first = 0, count = static_cast<int32_t>(a.n_slots), j = st;
+        if (tiles) {
+            first = offsets[e];
+            count = offsets[e + 1] - first;
+            j = st - tiles[e];
+        }
+        t.p0 = first + j * (2 * Pair::BM);
+        t.n = min(2 * Pair::BM, count - j * (2 * Pair::BM));
+        t.half = min(t.n, (t.n + 63) / 64 * 32);        // whole warps, nearly even
+        return t;
+    }
+};
 
 // Two fp32 values in one 64-bit register, the operand of the packed FMA.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -137,6 +164,14 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack2(uint64_t v) {
     float2 r;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
+// The two as bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16x2(uint64_t v) {
+    const float2 f = unpack2(v);
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
     return r;
 }
 
@@ -155,7 +190,7 @@ __device__ __forceinline__ float4* ring_at(float4* ring, int32_t g) {
     return ring + g % Pair::SCALE_RING * STEP;
 }
 
-__device__ __forceinline__ void copy_async4(uint32_t dst, const float* src, int32_t bytes) {
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
@@ -195,9 +230,8 @@ __device__ __forceinline__ float act_mul_fast(float g, float up, int32_t kind) {
 template <typename TO, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     moe_fp8_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                        const PairArgs args, TO* __restrict__ out) {
+                        const __grid_constant__ PairArgs a, TO* __restrict__ out) {
     using C = Pair;
-    PairArgs a = args;
     extern __shared__ uint8_t smem_raw[];
     // both CTAs round up by the same amount: their dynamic shared memory starts at the same offset
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -228,32 +262,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         prefetch_tmap(&wmap);
         prefetch_tmap(&xmap);
     }
-    if (a.tiles && a.n_experts <= C::MAX_E) {
-        int32_t *offsets = reinterpret_cast<int32_t*>(smem + C::OFF_ORDER), *tiles = offsets + C::MAX_E + 1;
+    const int32_t *offsets = a.offsets, *tiles = a.tiles;
+    if (tiles && a.n_experts <= C::MAX_E) {
+        int32_t *o = reinterpret_cast<int32_t*>(smem + C::OFF_ORDER), *n = o + C::MAX_E + 1;
         for (int32_t e = static_cast<int32_t>(threadIdx.x); e <= a.n_experts; e += C::THREADS) {
-            offsets[e] = a.offsets[e];
-            tiles[e] = a.tiles[e];
+            o[e] = offsets[e];
+            n[e] = tiles[e];
         }
-        a.offsets = offsets;
-        a.tiles = tiles;
+        offsets = o;
+        tiles = n;
     }
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    const int64_t slot_tiles = a.tiles ? a.tiles[a.n_experts] : (a.n_slots + 2 * C::BM - 1) / (2 * C::BM);
-    const int64_t total = slot_tiles * a.row_tiles;
-    const int64_t w0 = blockIdx.x / 2, dw = gridDim.x / 2;
+    PairWalk walk(a, tiles, static_cast<int32_t>(blockIdx.x / 2), static_cast<int32_t>(gridDim.x / 2));
 
     if (warp >= C::N_DRAIN_WARPS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs(GATED)));
     if (warp == C::WARP_PRODUCER) {
         // ------------------------------------------------------------ producer
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t w = w0; w < total && ok; w += dw) {
-            const PairTile t = pair_tile(a, w);
+        for (; walk.there() && ok; walk.next(tiles)) {
+            const PairTile t = walk.tile(a, tiles, offsets);
             const int32_t mine = t.mine(rank), other = t.mine(rank ^ 1u);
             constexpr int PER = C::ROW_BOX;      // lane l copies 32 of this CTA's slots
             const bool copies = static_cast<int32_t>(lane) * PER < mine;
@@ -290,8 +323,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             const uint64_t bskip = (C::A_BYTES + h * (C::BOX * kFp8Block)) >> 4;
             uint32_t s = 0, phase = 0, done = 0;      // stage, its phase, blocks of this half
             bool ok = true;
-            for (int64_t w = w0; w < total && ok; w += dw) {
-                const PairTile t = pair_tile(a, w);
+            for (; walk.there() && ok; walk.next(tiles)) {
+                const PairTile t = walk.tile(a, tiles, offsets);
                 const int32_t cols = t.cols(static_cast<int32_t>(h));
                 const uint32_t idesc = idesc_e4m3_f32(2 * C::BM, max(cols, 0));
                 for (int32_t b = 0; b < nb; ++b) {
@@ -324,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     }
     } else {
         // --------------------------------------------------------------- drain
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::DRAIN_REGS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::drain_regs(GATED)));
         const uint32_t lane0 = (warp & 3u) * 32u, h = warp >> 2;
         const uint32_t acc_empty0 = map_to_rank(smem_u32(acc_empty), 0);
         uint8_t* stage = smem + C::OFF_OUT + warp * (32 * C::STAGE_ROW);
@@ -335,21 +368,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         uint32_t tiles_done = 0;         // gated: tiles that this warp had slots of
         uint32_t it = 0;                 // blocks of this half
         bool ok = true;
-        for (int64_t w = w0; w < total && ok; w += dw) {
-            const PairTile t = pair_tile(a, w);
-            const int32_t r0 = t.r0 + static_cast<int32_t>(h) * C::CW;
-            if (r0 >= a.nrows) continue;
-            const int32_t mine = t.mine(rank);
-            const int32_t m = static_cast<int32_t>(lane0 + lane);        // this thread's slot of the CTA
-            const bool busy = static_cast<int32_t>(lane0) < mine;        // the warp has a slot at all
-            int32_t slot = 0;
-            const float* sa = a.act_scales;
-            if (m < mine) {
+        // The tile to come: its place, this thread's slot in it and where its scales lie, looked
+        // up after the last one's epilogue (before it, the lookup delays the rows that are
+        // waiting: 207 us against 199 for 65536 slots x 2048 x 768).
+        struct Next {
+            int32_t r0, mine;
+            const float *sa, *sw;
+        } next;
+        // this warp's rows of `out` (gated: of mid), of the current and the coming tile
+        int32_t* rows_of = reinterpret_cast<int32_t*>(smem + C::OFF_SLOT) + warp * 32;
+        uint32_t parity = 0;             // of the coming tile
+        const int32_t m = static_cast<int32_t>(lane0 + lane);            // this thread's slot of the CTA
+        auto look = [&]() {
+            const PairTile t = walk.tile(a, tiles, offsets);
+            next.r0 = GATED ? t.r0 / 2 : t.r0 + static_cast<int32_t>(h) * C::CW;      // first weight row of this half's scales
+            next.mine = t.mine(rank);
+            next.sa = a.act_scales;
+            next.sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + min(next.r0 / kFp8Block, a.row_blocks - 1)) * nb;
+            if (m < next.mine) {
                 const int32_t p = t.first(rank) + m;
-                slot = a.perm ? a.perm[p] : p;
-                sa += static_cast<int64_t>(p) * a.scale_pitch;
+                int32_t* row = rows_of + parity * (C::N_DRAIN_WARPS * 32) + lane;
+                // (a copy: a load would be waited for here, to be stored)
+                if (GATED || !a.perm) *row = p;
+                else copy_async4(smem_u32(row), a.perm + p, 4);
+                next.sa += static_cast<int64_t>(p) * a.scale_pitch;
             }
-            const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + (GATED ? t.r0 / 2 : r0) / kFp8Block) * nb;
+            parity ^= 1u;
+            // four blocks' scales at a time, through a ring in shared memory
+            if (static_cast<int32_t>(lane0) < next.mine && (GATED || next.r0 < a.nrows)) {
+#pragma unroll
+                for (int i = 0; i < C::SCALE_RING - 1; ++i) copy_scales<GATED>(a, next.sa, next.sw, i, ring_a, ring_w);
+            }
+        };
+        bool more = walk.there();
+        if (more) look();
+        while (more && ok) {
+            const int32_t r0 = next.r0, mine = next.mine;
+            const float *sa = next.sa, *sw = next.sw;
+            if (!GATED && r0 >= a.nrows) {
+                walk.next(tiles);
+                more = walk.there();
+                if (more) look();
+                continue;
+            }
+            const bool busy = static_cast<int32_t>(lane0) < mine;        // the warp has a slot at all
             uint64_t acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = 0;
@@ -360,11 +422,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                     if (lane == 0) mbar_arrive_remote(acc_empty0 + (2 * h + (it & 1u)) * 8);
                 }
                 if (!ok) break;
+                walk.next(tiles);
+                more = walk.there();
+                if (more) look();
                 continue;
             }
-            // the scales of the first blocks: four at a time through a ring in shared memory
-#pragma unroll
-            for (int i = 0; i < C::SCALE_RING - 1; ++i) copy_scales<GATED>(a, sa, sw, i, ring_a, ring_w);
             float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, su[GATED ? 4 : 1] = {};      // gated: the up rows' beside the gate rows'
             // 16 columns are on their way from tensor memory while the 16 before them are added
             uint32_t v[2][16];
@@ -425,6 +487,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 if (!ok) break;
             }
             if (!ok) break;
+            walk.next(tiles);
+            more = walk.there();
+            __syncwarp();      // every lane has read the last of this tile's scales
+
+            // `parity` has moved on since this tile's rows were written
+            const int32_t* rows = rows_of + (parity ^ 1u) * (C::N_DRAIN_WARPS * 32);
             if constexpr (GATED) {
                 // this thread's 64 of the slot's 128 values; the other half's thread has the rest
                 float amax = 0.0f;
@@ -457,17 +525,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                     }
                     *reinterpret_cast<uint4*>(stage + lane * 80 + 16 * i) = make_uint4(q[0], q[1], q[2], q[3]);
                 }
-                const int32_t p0 = t.first(rank) + static_cast<int32_t>(lane0), n = min(32, mine - static_cast<int32_t>(lane0));
-                if (h == 0 && m < mine) a.mid_scales[static_cast<int64_t>(p0 + static_cast<int32_t>(lane)) * a.mid_pitch + t.r0 / 2 / kFp8Block] = scale;
+                const int32_t p0 = rows[0], n = min(32, mine - static_cast<int32_t>(lane0));
+                if (h == 0 && m < mine) a.mid_scales[static_cast<int64_t>(p0 + static_cast<int32_t>(lane)) * a.mid_pitch + r0 / kFp8Block] = scale;
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {      // eight rows at a time, 64 bytes of each
                     const int32_t r = 8 * i + static_cast<int32_t>(lane >> 2);
                     if (r < n)
-                        *reinterpret_cast<uint4*>(a.mid + static_cast<int64_t>(p0 + r) * a.n_inter + t.r0 / 2 + h * 64 + (lane & 3u) * 16) =
+                        *reinterpret_cast<uint4*>(a.mid + static_cast<int64_t>(p0 + r) * a.n_inter + r0 + h * 64 + (lane & 3u) * 16) =
                             *reinterpret_cast<const uint4*>(stage + r * 80 + (lane & 3u) * 16);
                 }
                 __syncwarp();
+                if (more) look();
                 continue;
             }
             // out: 256 bytes of each of the warp's rows at a time go through shared memory,
@@ -479,14 +548,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    __align__(16) TO o[PER];
-#pragma unroll
-                    for (int k = 0; k < PER; k += 2) {
-                        const float2 f = unpack2(acc[(ps * PASS + PER * i + k) / 2]);
-                        o[k] = from_f32<TO>(f.x);
-                        o[k + 1] = from_f32<TO>(f.y);
+                    uint4 o;
+                    if constexpr (sizeof(TO) == 2) {
+                        o = make_uint4(bf16x2(acc[4 * i]), bf16x2(acc[4 * i + 1]), bf16x2(acc[4 * i + 2]), bf16x2(acc[4 * i + 3]));
+                    } else {
+                        const float2 f = unpack2(acc[ps * (PASS / 2) + 2 * i]), g = unpack2(acc[ps * (PASS / 2) + 2 * i + 1]);
+                        o = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(g.x), __float_as_uint(g.y));
                     }
-                    *reinterpret_cast<uint4*>(stage + lane * C::STAGE_ROW + 16 * i) = *reinterpret_cast<const uint4*>(o);
+                    *reinterpret_cast<uint4*>(stage + lane * C::STAGE_ROW + 16 * i) = o;
                 }
                 __syncwarp();
                 const int32_t c0 = r0 + ps * PASS;
@@ -495,20 +564,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
 #pragma unroll 4
                     for (int k = 0; k < 16; ++k) {       // two rows at a time, 16 bytes a lane
                         const int32_t r = 2 * k + static_cast<int32_t>(lane >> 4), c = static_cast<int32_t>(lane & 15u) * PER;
-                        const int32_t to = __shfl_sync(0xFFFFFFFFu, slot, r);
                         if (r < rows_here && c < left)
-                            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(to) * a.nrows + c0 + c) =
+                            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(rows[r]) * a.nrows + c0 + c) =
                                 *reinterpret_cast<const uint4*>(stage + r * C::STAGE_ROW + (lane & 15u) * 16);
                     }
                 } else {
                     for (int r = 0; r < rows_here; ++r) {
-                        const int32_t to = __shfl_sync(0xFFFFFFFFu, slot, r);
                         const TO* src = reinterpret_cast<const TO*>(stage + r * C::STAGE_ROW);
                         for (int32_t c = static_cast<int32_t>(lane); c < left; c += 32)
-                            out[static_cast<int64_t>(to) * a.nrows + c0 + c] = src[c];
+                            out[static_cast<int64_t>(rows[r]) * a.nrows + c0 + c] = src[c];
                     }
                 }
             }
+            if (more) look();
         }
     }
     __syncwarp();
@@ -556,7 +624,7 @@ int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs
         if (e != cudaSuccess) return fail(FT_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
         regs = at.numRegs;
     }
-    if (regs * C::THREADS < C::DRAIN_REGS * 256 + C::OTHER_REGS * 128)
+    if (regs * C::THREADS < C::drain_regs(GATED) * 256 + C::other_regs(GATED) * 128)
         return fail(FT_ERR_LAUNCH, "moe_fp8_pair_kernel was compiled with %d registers, %d are needed", regs, C::LAUNCH_REGS);
     if (int st = set_smem_limit(k, C::SMEM_BYTES)) return st;
     moe_fp8_pair_kernel<TO, GATED><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, static_cast<TO*>(out));

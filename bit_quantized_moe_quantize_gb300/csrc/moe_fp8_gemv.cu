@@ -2,32 +2,16 @@
 // CUDA cores, without ordering, barriers or a pipeline to fill.
 //
 // A warp takes four weight rows of one slot's expert; a step covers 512 columns, 16 of each
-// row per lane in one 16-byte load, so that a lane's 16 lie within one scale block.  e4m3
-// codes become fp16 pairs (exact); the activations' also times 2^-4 (exact), which keeps
-// every product inside fp16's range of exact ones (|448 * 448 / 16| < 65504, the smallest
-// 2^-22): products are added in fp32 by mixed FMAs, a lane's 16 at a time, and the
-// partial sums times 16 sa sw to the row's.
+// row per lane in one 16-byte load, so that a lane's 16 lie within one scale block: their
+// dot product times 16 sa sw (fp8_dot.cuh) goes to the row's sum.
 //
 // Bound by latency and by reading the matrices once.
-#include "fp8_common.cuh"
+#include "fp8_dot.cuh"
 #include "ft_internal.h"
 
 namespace ft {
 
 constexpr int kGemvWarps = 4, kGemvRows = 4;
-constexpr float kActDown = 0.0625f;      // 2^-4
-
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t q, uint32_t (&h)[2]) {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"(static_cast<uint16_t>(q & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"(static_cast<uint16_t>(q >> 16)));
-}
-
-// acc += a * b, fp16 operands, fp32 sum.
-__device__ __forceinline__ float fma_f16(uint16_t a, uint16_t b, float acc) {
-    float r;
-    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(r) : "h"(a), "h"(b), "f"(acc));
-    return r;
-}
 
 template <typename TO>
 __global__ void __launch_bounds__(32 * kGemvWarps) moe_fp8_gemv_kernel(const Fp8Product p, TO* __restrict__ out, uint32_t* err) {
@@ -64,35 +48,11 @@ __global__ void __launch_bounds__(32 * kGemvWarps) moe_fp8_gemv_kernel(const Fp8
 #pragma unroll
             for (int i = 0; i < kGemvRows; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(w[i] + c));
             const int32_t b = (c + 16 * static_cast<int32_t>(lane)) / kFp8Block;
-            const float scale = __ldg(sa + b) * (1.0f / kActDown);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            const float scale = __ldg(sa + b) * kActUp;
             uint32_t a[8];
+            act_to_f16(x, a);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t h[2];
-                e4m3x4_to_f16(xs[j], h);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const __half2 d = __hmul2(*reinterpret_cast<__half2*>(&h[k]), __floats2half2_rn(kActDown, kActDown));
-                    a[2 * j + k] = *reinterpret_cast<const uint32_t*>(&d);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kGemvRows; ++i) {
-                const uint32_t ws[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-                float even = 0.0f, odd = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t h[2];
-                    e4m3x4_to_f16(ws[j], h);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        even = fma_f16(static_cast<uint16_t>(h[k] & 0xFFFFu), static_cast<uint16_t>(a[2 * j + k] & 0xFFFFu), even);
-                        odd = fma_f16(static_cast<uint16_t>(h[k] >> 16), static_cast<uint16_t>(a[2 * j + k] >> 16), odd);
-                    }
-                }
-                acc[i] = fmaf(even + odd, scale * __ldg(sw[i] + b), acc[i]);
-            }
+            for (int i = 0; i < kGemvRows; ++i) acc[i] = fmaf(dot16(q[i], a), scale * __ldg(sw[i] + b), acc[i]);
         }
     }
 #pragma unroll

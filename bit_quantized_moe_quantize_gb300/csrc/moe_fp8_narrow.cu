@@ -74,17 +74,17 @@ struct NarrowTile {
 };
 
 template <int NW>
-__device__ __forceinline__ NarrowTile narrow_tile(const NarrowArgs& a, int64_t w) {
+__device__ __forceinline__ NarrowTile narrow_tile(const NarrowArgs& a, const int32_t* tiles, const int32_t* offsets, int64_t w) {
     NarrowTile t;
     const int32_t st = static_cast<int32_t>(w / a.row_tiles);
     t.r0 = static_cast<int32_t>(w - static_cast<int64_t>(st) * a.row_tiles) * a.br;
     int32_t first = 0, count = static_cast<int32_t>(a.n_slots), j = st;
     t.e = 0;
-    if (a.tiles) {
-        t.e = last_not_above(a.tiles, a.n_experts, st);
-        first = a.offsets[t.e];
-        count = a.offsets[t.e + 1] - first;
-        j = st - a.tiles[t.e];
+    if (tiles) {
+        t.e = last_not_above(tiles, a.n_experts, st);
+        first = offsets[t.e];
+        count = offsets[t.e + 1] - first;
+        j = st - tiles[t.e];
     }
     t.p0 = first + j * NW;
     t.n = min(NW, count - j * NW);
@@ -94,9 +94,8 @@ __device__ __forceinline__ NarrowTile narrow_tile(const NarrowArgs& a, int64_t w
 template <int NW, typename TO, bool GATHER>
 __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
     moe_fp8_narrow_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                          const NarrowArgs args, TO* __restrict__ out) {
+                          const __grid_constant__ NarrowArgs a, TO* __restrict__ out) {
     using C = Narrow<NW>;
-    NarrowArgs a = args;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -137,36 +136,37 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         prefetch_tmap(&wmap);
         prefetch_tmap(&xmap);
     }
+    const int32_t *offsets = a.offsets, *tiles = a.tiles, *perm = a.perm;
     if (a.orders) {
-        int32_t* offsets = reinterpret_cast<int32_t*>(smem + C::OFF_ORDER);
-        int32_t *tiles = offsets + C::MAX_E + 1, *perm = tiles + C::MAX_E + 1, *part = perm + 1024;
+        int32_t* o = reinterpret_cast<int32_t*>(smem + C::OFF_ORDER);
+        int32_t *nt = o + C::MAX_E + 1, *pm = nt + C::MAX_E + 1, *part = pm + 1024;
         int32_t* mine = reinterpret_cast<int32_t*>(smem);
         const int32_t E = a.n_experts, n_slots = static_cast<int32_t>(a.n_slots);
         int32_t id[4], rank[4];
         const int32_t s0 = chunk_rank(a.ids, 0, n_slots, E, mine, id, rank);
-        chunk_totals(mine, E, offsets);
-        for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) tiles[e] = (offsets[e] + NW - 1) / NW;
+        chunk_totals(mine, E, o);
+        for (int32_t e = threadIdx.x; e < E; e += kChunkThreads) nt[e] = (o[e] + NW - 1) / NW;
         __syncthreads();
-        const int32_t routed = chunk_scan(offsets, E, part), n_tiles = chunk_scan(tiles, E, part);
+        const int32_t routed = chunk_scan(o, E, part), n_tiles = chunk_scan(nt, E, part);
         if (threadIdx.x == 0) {
-            offsets[E] = routed;
-            tiles[E] = n_tiles;
+            o[E] = routed;
+            nt[E] = n_tiles;
         }
-        chunk_starts(mine, E, offsets);
+        chunk_starts(mine, E, o);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (id[i] >= 0) perm[mine[static_cast<int32_t>(warp) * E + id[i]] + rank[i]] = s0 + 32 * i;
+            if (id[i] >= 0) pm[mine[static_cast<int32_t>(warp) * E + id[i]] + rank[i]] = s0 + 32 * i;
         fence_proxy_async_smem();      // the copies that follow write where the counts lay
-        a.perm = perm;
-        a.offsets = offsets;
-        a.tiles = tiles;
+        perm = pm;
+        offsets = o;
+        tiles = nt;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    const int64_t slot_tiles = a.tiles ? a.tiles[a.n_experts] : (a.n_slots + NW - 1) / NW;
+    const int64_t slot_tiles = tiles ? tiles[a.n_experts] : (a.n_slots + NW - 1) / NW;
     const int64_t total = slot_tiles * a.row_tiles;
 
     if (warp == C::WARP_PRODUCER) {
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         uint32_t phase = 1;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const NarrowTile t = narrow_tile<NW>(a, w);
+            const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
             constexpr int PER = GATHER ? 4 : C::ROW_BOX;
             const bool copies = static_cast<int32_t>(lane) * PER < t.n;
             int32_t y[4] = {0, 0, 0, 0};
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
                 const int32_t p = t.p0 + static_cast<int32_t>(lane) * PER;
                 if constexpr (GATHER) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = a.perm[min(p + i, t.p0 + t.n - 1)] / a.act_div;
+                    for (int i = 0; i < 4; ++i) y[i] = perm[min(p + i, t.p0 + t.n - 1)] / a.act_div;
                 } else {
                     y[0] = p;
                 }
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         uint32_t phase = 0, unit = 0;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const NarrowTile t = narrow_tile<NW>(a, w);
+            const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
             const uint32_t idesc = idesc_e4m3_f32(C::BM, (t.n + 15) / 16 * 16);
             for (int32_t b0 = 0; b0 < nb && ok; b0 += C::G, ++unit) {
                 const uint32_t u = unit % C::UNITS;
@@ -248,11 +248,11 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
                 uint32_t unit = 0;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const NarrowTile t = narrow_tile<NW>(a, w);
+            const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
             const float* sa = nullptr;                   // of slot `lane`
             if (static_cast<int32_t>(lane) < t.n) {
                 const int32_t p = t.p0 + static_cast<int32_t>(lane);
-                sa = a.act_scales + static_cast<int64_t>(a.ordered ? p : a.perm[p] / a.act_div) * a.scale_pitch;
+                sa = a.act_scales + static_cast<int64_t>(a.ordered ? p : perm[p] / a.act_div) * a.scale_pitch;
             }
             const float* sw = a.w_scales + (static_cast<int64_t>(t.e) * a.row_blocks + t.r0 / kFp8Block) * nb;
             // a load takes longer than a unit: those of four units are in flight
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         uint32_t unit = 0;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const NarrowTile t = narrow_tile<NW>(a, w);
+            const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
             float acc[NW];
 #pragma unroll
             for (int i = 0; i < NW; ++i) acc[i] = 0.0f;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
 #pragma unroll
             for (int c = 0; c < NW; ++c) {
                 if (c < t.n) {
-                    const int32_t p = t.p0 + c, slot = a.perm ? a.perm[p] : p;
+                    const int32_t p = t.p0 + c, slot = perm ? perm[p] : p;
                     if (row < a.nrows) out[static_cast<int64_t>(slot) * a.nrows + row] = from_f32<TO>(acc[c]);
                 }
             }

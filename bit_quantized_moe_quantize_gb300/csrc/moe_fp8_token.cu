@@ -1,0 +1,215 @@
+// An expert layer for a few decoded tokens, after the router, in two launches.
+//
+//   token_gated: quantizes the token's row of x (in every CTA, into shared memory), takes its
+//     dot products with gate and up rows of one slot's expert, and writes act(gate) * up in fp32
+//   token_down: quantizes each slot's activated row (a warp per slot, into shared memory),
+//     takes its dot products with eight rows of w2, and adds the slots' sums with their
+//     weights, in the order of the slots
+//
+// Reading the experts' matrices once is what is left to wait for, beside the launches: the
+// same pieces as separate launches (quantizer, product, quantizer, product, weighted sum)
+// take six.  Every value is rounded as those do, except that the second product's rows are
+// added up in fp32 as they come.  Each launch may start before the one before it has ended
+// (programmatic dependent launch): what it reads of that one's results comes after
+// griddepcontrol.wait, and nothing is written before it.
+#include "fp8_dot.cuh"
+#include "fp8_quant.cuh"
+#include "ft_internal.h"
+
+namespace ft {
+
+constexpr int kTokenWarps = 8, kPairs = 2, kDownRows = 8;
+
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Quantizes n values (a multiple of 16) by `warps` warps into codes and scales in shared memory.
+// fp32 rows are the launch before's results.
+template <typename T>
+__device__ __forceinline__ void quantize_row(const T* x, int32_t n, uint8_t* codes, float* scales, uint32_t warp,
+                                             uint32_t warps) {
+    const uint32_t sub = lane_id() & 15u;
+    const int32_t nb = (n + kFp8Block - 1) / kFp8Block;
+    for (int32_t b0 = 2 * static_cast<int32_t>(warp); b0 < nb; b0 += 2 * static_cast<int32_t>(warps)) {
+        const int32_t b = b0 + static_cast<int32_t>(lane_id() >> 4), c = b * kFp8Block + 8 * static_cast<int32_t>(sub);
+        float v[8] = {};
+        if (c < n) {
+            if constexpr (sizeof(T) == 4) load_vec_plain<8>(x + c, v);
+            else load_vec<T, 8>(x + c, v);
+        }
+        const float scale = fp8_block_scale(v);
+        if (c < n) *reinterpret_cast<uint2*>(codes + c) = fp8_codes(v, scale);
+        if (sub == 0 && b < nb) scales[b] = scale;
+    }
+}
+
+// Dot products of R rows (pointers w, scales sw; lane offsets included in w) with a quantized row in shared memory.
+template <int R>
+__device__ __forceinline__ void dot_rows(const uint8_t* const (&w)[R], const float* const (&sw)[R], int32_t n, const uint8_t* codes,
+                                         const float* scales, float (&acc)[R]) {
+    const int32_t l = 16 * static_cast<int32_t>(lane_id());
+#pragma unroll 2
+    for (int32_t c = 0; c < n; c += 512) {
+        if (c + l < n) {
+            uint4 q[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(w[i] + c));
+            const int32_t b = (c + l) / kFp8Block;
+            const float scale = scales[b] * kActUp;
+            uint32_t a[8];
+            act_to_f16(*reinterpret_cast<const uint4*>(codes + c + l), a);
+#pragma unroll
+            for (int i = 0; i < R; ++i) acc[i] = fmaf(dot16(q[i], a), scale * __ldg(sw[i] + b), acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], k);
+}
+
+// grid: (ceil(n_inter / (kTokenWarps * kPairs)), slots)
+template <typename T>
+__global__ void __launch_bounds__(32 * kTokenWarps)
+    token_gated_kernel(const T* __restrict__ x, const uint8_t* __restrict__ w13, const float* __restrict__ s13,
+                       const int32_t* ids, float* mid, int32_t n_experts, int32_t top_k, int32_t hidden,
+                       int32_t n_inter, int kind) {
+    extern __shared__ __align__(16) uint8_t row_smem[];
+    float* scales = reinterpret_cast<float*>(row_smem + hidden);
+    const uint32_t warp = threadIdx.x >> 5;
+    const int64_t s = blockIdx.y;
+    grid_launch_dependents();
+    quantize_row<T>(x + s / top_k * hidden, hidden, row_smem, scales, warp, kTokenWarps);
+    __syncthreads();
+    grid_dependency_wait();      // the router's choice
+    const int32_t e = ids[s], i0 = (static_cast<int32_t>(blockIdx.x) * kTokenWarps + static_cast<int32_t>(warp)) * kPairs;
+    if (e < 0 || e >= n_experts || i0 >= n_inter) return;
+    const int32_t nb = (hidden + kFp8Block - 1) / kFp8Block, blocks = (2 * n_inter + kFp8Block - 1) / kFp8Block;
+    const uint8_t* w[2 * kPairs];
+    const float* sw[2 * kPairs];
+#pragma unroll
+    for (int i = 0; i < 2 * kPairs; ++i) {      // gate rows, then up rows; past the end the last one again
+        const int32_t r = min(i0 + i % kPairs, n_inter - 1) + (i < kPairs ? 0 : n_inter);
+        w[i] = w13 + (static_cast<int64_t>(e) * 2 * n_inter + r) * hidden + 16 * lane_id();
+        sw[i] = s13 + (static_cast<int64_t>(e) * blocks + r / kFp8Block) * nb;
+    }
+    float acc[2 * kPairs] = {};
+    dot_rows<2 * kPairs>(w, sw, hidden, row_smem, scales, acc);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+        if (lane_id() == static_cast<uint32_t>(i) && i0 + i < n_inter)
+            mid[s * n_inter + i0 + i] = act_mul_f32(acc[i], acc[kPairs + i], kind);
+}
+
+// grid: (ceil(hidden / kDownRows), tokens)
+template <typename TO>
+__global__ void __launch_bounds__(32 * kTokenWarps)
+    token_down_kernel(const float* mid, const uint8_t* __restrict__ w2, const float* __restrict__ s2,
+                      const int32_t* ids, const float* weights, TO* y, int32_t n_experts,
+                      int32_t top_k, int32_t hidden, int32_t n_inter, int32_t warp_bytes) {
+    extern __shared__ __align__(16) uint8_t row_smem[];      // per warp codes[n_inter], scales; then sums[top_k][kDownRows]
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    uint8_t* codes = row_smem + warp * static_cast<uint32_t>(warp_bytes);
+    float* scales = reinterpret_cast<float*>(codes + n_inter);
+    float* sums = reinterpret_cast<float*>(row_smem + kTokenWarps * static_cast<uint32_t>(warp_bytes));
+    const int64_t t = blockIdx.y;
+    const int32_t r0 = static_cast<int32_t>(blockIdx.x) * kDownRows;
+    const int32_t nb = (n_inter + kFp8Block - 1) / kFp8Block, blocks = (hidden + kFp8Block - 1) / kFp8Block;
+    grid_dependency_wait();
+    for (int32_t j = static_cast<int32_t>(warp); j < top_k; j += kTokenWarps) {
+        const int64_t s = t * top_k + j;
+        const int32_t e = ids[s];
+        float acc[kDownRows] = {};
+        if (e >= 0 && e < n_experts) {
+            __syncwarp();
+            quantize_row<float>(mid + s * n_inter, n_inter, codes, scales, 0, 1);
+            __syncwarp();
+            const uint8_t* w[kDownRows];
+            const float* sw[kDownRows];
+#pragma unroll
+            for (int i = 0; i < kDownRows; ++i) {
+                const int32_t r = min(r0 + i, hidden - 1);
+                w[i] = w2 + (static_cast<int64_t>(e) * hidden + r) * n_inter + 16 * lane;
+                sw[i] = s2 + (static_cast<int64_t>(e) * blocks + r / kFp8Block) * nb;
+            }
+            dot_rows<kDownRows>(w, sw, n_inter, codes, scales, acc);
+        }
+#pragma unroll
+        for (int i = 0; i < kDownRows; ++i)
+            if (lane == static_cast<uint32_t>(i)) sums[j * kDownRows + i] = acc[i];
+    }
+    __syncthreads();
+    const int32_t r = r0 + static_cast<int32_t>(threadIdx.x);
+    if (threadIdx.x < kDownRows && r < hidden) {
+        float sum = 0.0f;
+        for (int32_t j = 0; j < top_k; ++j) {
+            const float wj = weights[t * top_k + j];
+            if (wj != 0.0f) sum = fmaf(wj, sums[j * kDownRows + threadIdx.x], sum);
+        }
+        y[t * hidden + r] = from_f32<TO>(sum);
+    }
+}
+
+// ------------------------------------------------------------------- host
+namespace {
+
+int32_t down_warp_bytes(int64_t n_inter) { return static_cast<int32_t>((n_inter + 4 * fp8_blocks(n_inter) + 15) / 16 * 16); }
+
+size_t down_smem(int64_t n_inter, int32_t top_k) {
+    return static_cast<size_t>(kTokenWarps) * down_warp_bytes(n_inter) + static_cast<size_t>(top_k) * kDownRows * 4;
+}
+
+template <typename... A>
+int launch_dependent(void (*kernel)(A...), const char* name, dim3 grid, size_t smem, cudaStream_t s, A... args) {
+    if (smem > 48 * 1024)
+        if (int st = set_smem_limit(reinterpret_cast<const void*>(kernel), static_cast<int>(smem))) return st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(32 * kTokenWarps);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(FT_ERR_LAUNCH, "launch of %s failed: %s", name, cudaGetErrorString(e));
+    }
+    return check_launch(name, grid, c.blockDim, smem);
+}
+
+}  // namespace
+
+bool fp8_token_ok(int64_t n_slots, int64_t tokens, int32_t top_k, int64_t hidden, int64_t n_inter) {
+    return n_slots <= 65535 && tokens <= 65535 && hidden + 4 * fp8_blocks(hidden) <= 200 * 1024 &&
+           down_smem(n_inter, top_k) <= 200 * 1024;
+}
+
+int launch_fp8_token_layer(const void* x, int x_dtype, const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2,
+                           const int32_t* ids, const float* weights, float* mid, void* y, int64_t tokens, int32_t top_k,
+                           int32_t n_experts, int64_t hidden, int64_t n_inter, int kind, cudaStream_t s) {
+    const int32_t H = static_cast<int32_t>(hidden), I = static_cast<int32_t>(n_inter);
+    const dim3 g1(static_cast<unsigned>((n_inter + kTokenWarps * kPairs - 1) / (kTokenWarps * kPairs)), static_cast<unsigned>(tokens * top_k));
+    const dim3 g2(static_cast<unsigned>((hidden + kDownRows - 1) / kDownRows), static_cast<unsigned>(tokens));
+    const size_t sm1 = static_cast<size_t>(hidden + 4 * fp8_blocks(hidden)), sm2 = down_smem(n_inter, top_k);
+    const int32_t wb = down_warp_bytes(n_inter);
+    int st;
+    if (x_dtype == FT_DTYPE_F16)
+        st = launch_dependent(token_gated_kernel<__half>, "token_gated_kernel", g1, sm1, s, static_cast<const __half*>(x), w13, s13, ids,
+                              mid, n_experts, top_k, H, I, kind);
+    else
+        st = launch_dependent(token_gated_kernel<__nv_bfloat16>, "token_gated_kernel", g1, sm1, s, static_cast<const __nv_bfloat16*>(x),
+                              w13, s13, ids, mid, n_experts, top_k, H, I, kind);
+    if (st) return st;
+    const float* m = mid;
+    if (x_dtype == FT_DTYPE_F16)
+        return launch_dependent(token_down_kernel<__half>, "token_down_kernel", g2, sm2, s, m, w2, s2, ids, weights,
+                                static_cast<__half*>(y), n_experts, top_k, H, I, wb);
+    return launch_dependent(token_down_kernel<__nv_bfloat16>, "token_down_kernel", g2, sm2, s, m, w2, s2, ids, weights,
+                            static_cast<__nv_bfloat16*>(y), n_experts, top_k, H, I, wb);
+}
+
+}  // namespace ft

@@ -93,6 +93,7 @@ __device__ __forceinline__ int32_t take_best(uint32_t* keys, int32_t n, Best& b)
 template <typename T>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const GateArgs a) {
     extern __shared__ uint32_t gate_smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // a kernel launched to overlap may come up
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
     if (t >= a.tokens) return;
@@ -203,10 +204,52 @@ __device__ __forceinline__ float order32_value(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
 }
 
+__device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
+    const uint32_t x = max(a, b), y = min(a, b);
+    a = x;
+    b = y;
+}
+
+// Sorts eight keys, largest first (odd-even merges: 19 exchanges).
+__device__ __forceinline__ void sort8(uint32_t (&k)[8]) {
+    order_pair(k[0], k[1]);
+    order_pair(k[2], k[3]);
+    order_pair(k[4], k[5]);
+    order_pair(k[6], k[7]);
+    order_pair(k[0], k[2]);
+    order_pair(k[1], k[3]);
+    order_pair(k[4], k[6]);
+    order_pair(k[5], k[7]);
+    order_pair(k[1], k[2]);
+    order_pair(k[5], k[6]);
+    order_pair(k[0], k[4]);
+    order_pair(k[1], k[5]);
+    order_pair(k[2], k[6]);
+    order_pair(k[3], k[7]);
+    order_pair(k[2], k[4]);
+    order_pair(k[3], k[5]);
+    order_pair(k[1], k[2]);
+    order_pair(k[3], k[4]);
+    order_pair(k[5], k[6]);
+}
+
+// a := the eight largest of two sorted lists of eight, sorted.  Largest of a against smallest
+// of b, and so on, leaves them as a bitonic list; three halvings sort that.
+__device__ __forceinline__ void merge8(uint32_t (&a)[8], const uint32_t (&b)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) order_pair(a[i], a[i + d]);
+}
+
 // K: uint32_t (T is 16-bit and the keys are logits) or uint64_t.  WIDE: rows start at whole
 // 16-byte words.
 template <typename T, int LANES, typename K, bool WIDE>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // a kernel launched to overlap may come up
     constexpr bool PACKED = sizeof(K) == 4;
     const uint32_t sub = threadIdx.x & (LANES - 1);
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * (kGateThreads / LANES) + threadIdx.x / LANES;
@@ -259,6 +302,44 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateAr
     }
     int32_t* ids = a.ids + t * a.top_k;
     float* weights = a.weights + t * a.top_k;
+    if constexpr (PACKED && LANES >= 8) {
+        // up to eight choices of 32-bit keys: every lane's eight largest by sorting networks, then
+        // the lanes' lists merged pairwise; the rounds below take three times the instructions
+        if (a.top_k <= 8) {
+            uint32_t k8[8], l8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                k8[i] = key[i];
+                l8[i] = key[8 + i];
+            }
+            sort8(k8);
+            sort8(l8);
+            merge8(k8, l8);
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) l8[i] = __shfl_xor_sync(0xFFFFFFFFu, k8[i], o);
+                merge8(k8, l8);
+            }
+            uint32_t m = k8[0];      // lane j takes choice j
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = sub == static_cast<uint32_t>(i) ? k8[i] : m;
+            const bool mine = sub < static_cast<uint32_t>(a.top_k);
+            float w = 0.0f;
+            if (mine && m != 0) {
+                const float l = order16_value<T>(m >> 16);
+                w = a.renormalize && a.score == FT_SCORE_SOFTMAX ? gate_exp(l, top) : gate_score(l, top, sum, a.score);
+            }
+            float total = w;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+            if (there && mine) {
+                ids[sub] = m != 0 ? static_cast<int32_t>(0xFFFFu - (m & 0xFFFFu)) : -1;
+                weights[sub] = (a.renormalize ? __fdiv_rn(w, fmaxf(total, kGateTiny)) : w) * a.scale;
+            }
+            return;
+        }
+    }
     float total = 0.0f, mine = 0.0f;      // mine: weight `sub` (of the first LANES)
     const bool few = a.top_k <= LANES, cancel = by_logit && a.renormalize && a.score == FT_SCORE_SOFTMAX;
     for (int32_t j = 0; j < a.top_k; ++j) {

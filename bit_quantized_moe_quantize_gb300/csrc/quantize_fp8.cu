@@ -10,47 +10,12 @@
 // codes are those of the IEEE quotients; see fp8_codes for how most of them come without a
 // division.  A non-finite value makes its block's scale infinite or NaN, and what is
 // divided by it 0 or NaN.
-#include "fp8_common.cuh"
+#include "fp8_quant.cuh"
 #include "ft_internal.h"
 
 namespace ft {
 
 constexpr int kQuantWarps = 8;
-
-// The gated activation of one value: act(g) * up with act(g) = g / (1 + exp(-z)), z = g for
-// SiLU and 2 sqrt(2/pi) (g + 0.044715 g^3) for the tanh form of GELU.  The quotient is
-// within two units in the last place.
-__device__ __forceinline__ float act_mul_f32(float g, float up, int kind) {
-    const float cube = __fmul_rn(__fmul_rn(__fmul_rn(0.044715f, g), g), g);
-    const float z = kind == FT_ACT_SILU ? g : __fmul_rn(1.5957691216057308f, __fadd_rn(g, cube));
-    return __fdividef(g, 1.0f + expf(-z)) * up;
-}
-
-// Codes of v / scale for eight values.  y = v * (1 / scale) lies within 2^-22 |v / scale| of
-// the IEEE quotient (two roundings of half a unit against one), so both round to the same
-// code unless y (1 - 2^-21) and y (1 + 2^-21) do not; only then, or where 1 / scale could
-// overflow, are the quotients formed.
-__device__ __forceinline__ uint2 fp8_codes(const float (&v)[8], float scale) {
-    const float inv = __frcp_rn(scale);
-    uint32_t lo[2], hi[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(v[4 * h + j], inv);
-        constexpr float D = 1.0f - 0x1p-21f, U = 1.0f + 0x1p-21f;
-        lo[h] = e4m3x4(y[0] * D, y[1] * D, y[2] * D, y[3] * D);
-        hi[h] = e4m3x4(y[0] * U, y[1] * U, y[2] * U, y[3] * U);
-    }
-    if (lo[0] != hi[0] || lo[1] != hi[1] || !(scale > 1.0e-36f)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            lo[h] = scale == 0.0f ? 0u
-                                  : e4m3x4(__fdiv_rn(v[4 * h], scale), __fdiv_rn(v[4 * h + 1], scale),
-                                           __fdiv_rn(v[4 * h + 2], scale), __fdiv_rn(v[4 * h + 3], scale));
-    }
-    return make_uint2(lo[0], lo[1]);
-}
 
 // GATED: x holds rows of 2 ncols values, gate then up.  SPREAD: row r is a token's, and
 // its codes and scales go to the rows pos[r * k ..] (-1: none) of the outputs.
@@ -77,13 +42,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
             load_vec<T, 8>(x + row * ncols + c, v);
         }
     }
-    // magnitudes order like their bits, and NaN's lie above all others'
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float scale = __fdiv_rn(__uint_as_float(top), kFp8Max);
+    const float scale = fp8_block_scale(v);
     if (!in) return;
     const uint2 q = fp8_codes(v, scale);
     if constexpr (SPREAD) {
