@@ -8,7 +8,9 @@
 //
 // Memory-bound: each thread owns V neighbouring columns of one token and reads
 // them of all rows; V elements make 16 bytes of the rows' type where the
-// column count and the pointers allow it, else V = 1.
+// column count and the pointers allow it, else V = 1.  A CTA works on one token, with as
+// many threads as share its columns evenly (a 64-bit division per thread to find its token
+// took as long as its loads).
 #include "fp8_common.cuh"
 #include "ft_internal.h"
 
@@ -25,10 +27,11 @@ __device__ __forceinline__ void load_cols(const T* p, float (&v)[V]) {
 template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(kCombineThreads)
     moe_combine_kernel(const TI* __restrict__ rows, const float* __restrict__ weights, const TO* __restrict__ add,
-                       TO* __restrict__ y, int64_t n_vec, int64_t row_vec, int32_t top_k) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kCombineThreads + threadIdx.x;
-    if (i >= n_vec) return;
-    const int64_t t = i / row_vec, c = (i - t * row_vec) * V, ncols = row_vec * V;
+                       TO* __restrict__ y, int64_t row_vec, uint32_t per_row, int32_t top_k) {
+    const uint32_t tb = blockIdx.x / per_row;
+    const int64_t v = static_cast<int64_t>(blockIdx.x - tb * per_row) * blockDim.x + threadIdx.x;
+    if (v >= row_vec) return;
+    const int64_t t = tb, c = v * V, ncols = row_vec * V;
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.0f;
@@ -69,15 +72,15 @@ static int launch_typed(const void* rows, const float* weights, const void* add,
     constexpr int V = 16 / static_cast<int>(sizeof(TI));
     auto ok = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const bool wide = ncols % V == 0 && ncols * static_cast<int64_t>(sizeof(TO)) % 16 == 0 && ok(rows) && ok(y) && ok(add);
-    const int64_t row_vec = wide ? ncols / V : ncols, n_vec = tokens * row_vec;
-    const int64_t ctas = (n_vec + kCombineThreads - 1) / kCombineThreads;
-    if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "tokens * ncols too large for one launch");
-    const dim3 grid(static_cast<unsigned>(ctas)), block(kCombineThreads);
+    const int64_t row_vec = wide ? ncols / V : ncols, per_row = (row_vec + kCombineThreads - 1) / kCombineThreads;
+    const int64_t threads = ((row_vec + per_row - 1) / per_row + 31) / 32 * 32;
+    if (per_row > 0x7FFFFFFF / tokens) return fail(FT_ERR_SIZE, "tokens * ncols too large for one launch");
+    const dim3 grid(static_cast<unsigned>(tokens * per_row)), block(static_cast<unsigned>(threads));
     const TI* r = static_cast<const TI*>(rows);
     const TO* a = static_cast<const TO*>(add);
     TO* o = static_cast<TO*>(y);
-    if (wide) moe_combine_kernel<TI, TO, V><<<grid, block, 0, s>>>(r, weights, a, o, n_vec, row_vec, top_k);
-    else moe_combine_kernel<TI, TO, 1><<<grid, block, 0, s>>>(r, weights, a, o, n_vec, row_vec, top_k);
+    if (wide) moe_combine_kernel<TI, TO, V><<<grid, block, 0, s>>>(r, weights, a, o, row_vec, static_cast<uint32_t>(per_row), top_k);
+    else moe_combine_kernel<TI, TO, 1><<<grid, block, 0, s>>>(r, weights, a, o, row_vec, static_cast<uint32_t>(per_row), top_k);
     return check_launch("moe_combine_kernel", grid, block, 0);
 }
 

@@ -15,47 +15,71 @@
 
 namespace ft {
 
-constexpr int kQuantWarps = 8;
+constexpr int kQuantWarps = 8, kQuantAhead = 2;
+
+// Eight neighbouring elements, 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load_raw(const T* p, T (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(v)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+}
 
 // GATED: x holds rows of 2 ncols values, gate then up.  SPREAD: row r is a token's, and
 // its codes and scales go to the rows pos[r * k ..] (-1: none) of the outputs.
 template <typename T, bool GATED, bool SPREAD>
 __global__ void __launch_bounds__(32 * kQuantWarps)
     quantize_fp8_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, float* __restrict__ scales,
-                        int64_t n_blocks, int32_t nb, int64_t ncols, int kind, const int32_t* __restrict__ pos, int32_t k,
+                        uint32_t n_blocks, uint32_t nb, int64_t ncols, int kind, const int32_t* __restrict__ pos, int32_t k,
                         int32_t pitch) {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5)) * 2 + (lane_id() >> 4);
     const uint32_t sub = lane_id() & 15u;
-    const bool there = i < n_blocks;
-    const int64_t row = there ? i / nb : 0;
-    const int64_t c = (there ? i - row * nb : 0) * kFp8Block + 8 * static_cast<int64_t>(sub);
-    const bool in = there && c < ncols;      // ncols % 16 == 0: a lane's eight values are all inside or all outside
-    float v[8] = {};
-    if (in) {
-        if constexpr (GATED) {
-            float g[8], u[8];
-            load_vec<T, 8>(x + row * 2 * ncols + c, g);
-            load_vec<T, 8>(x + row * 2 * ncols + ncols + c, u);
+    // both of a half warp's blocks are asked for before the first is worked on
+    __align__(16) T raw[kQuantAhead][GATED ? 2 : 1][8];
+    uint32_t at[kQuantAhead];
+    int64_t row[kQuantAhead], col[kQuantAhead];
+    bool in[kQuantAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = act_mul_f32(g[j], u[j], kind);
-        } else {
-            load_vec<T, 8>(x + row * ncols + c, v);
-        }
-    }
-    const float scale = fp8_block_scale(v);
-    if (!in) return;
-    const uint2 q = fp8_codes(v, scale);
-    if constexpr (SPREAD) {
-        for (int32_t j = 0; j < k; ++j) {
-            const int64_t p = __ldg(pos + row * k + j);
-            if (p >= 0) {
-                *reinterpret_cast<uint2*>(codes + p * ncols + c) = q;
-                if (sub == 0) scales[p * pitch + (i - row * nb)] = scale;
+    for (int n = 0; n < kQuantAhead; ++n) {
+        at[n] = ((blockIdx.x * kQuantAhead + n) * kQuantWarps + (threadIdx.x >> 5)) * 2 + (lane_id() >> 4);
+        const bool there = at[n] < n_blocks;
+        const uint32_t r = there ? at[n] / nb : 0u;
+        row[n] = r;
+        col[n] = static_cast<int64_t>(there ? at[n] - r * nb : 0u) * kFp8Block + 8 * sub;
+        in[n] = there && col[n] < ncols;      // ncols % 16 == 0: a lane's eight values are all inside or all outside
+        if (in[n]) {
+            if constexpr (GATED) {
+                load_raw(x + row[n] * 2 * ncols + col[n], raw[n][0]);
+                load_raw(x + row[n] * 2 * ncols + ncols + col[n], raw[n][1]);
+            } else {
+                load_raw(x + row[n] * ncols + col[n], raw[n][0]);
             }
         }
-    } else {
-        if (sub == 0) scales[i] = scale;
-        *reinterpret_cast<uint2*>(codes + row * ncols + c) = q;
+    }
+#pragma unroll
+    for (int n = 0; n < kQuantAhead; ++n) {
+        float v[8] = {};
+        if (in[n]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (GATED) v[j] = act_mul_f32(to_f32<T>(raw[n][0][j]), to_f32<T>(raw[n][1][j]), kind);
+                else v[j] = to_f32<T>(raw[n][0][j]);
+            }
+        }
+        const float scale = fp8_block_scale(v);
+        if (in[n]) {
+            const uint2 q = fp8_codes(v, scale);
+            if constexpr (SPREAD) {
+                for (int32_t j = 0; j < k; ++j) {
+                    const int64_t p = __ldg(pos + row[n] * k + j);
+                    if (p >= 0) {
+                        *reinterpret_cast<uint2*>(codes + p * ncols + col[n]) = q;
+                        if (sub == 0) scales[p * pitch + (at[n] - static_cast<uint32_t>(row[n]) * nb)] = scale;
+                    }
+                }
+            } else {
+                if (sub == 0) scales[at[n]] = scale;
+                *reinterpret_cast<uint2*>(codes + row[n] * ncols + col[n]) = q;
+            }
+        }
     }
 }
 
@@ -63,11 +87,12 @@ template <typename T, bool GATED, bool SPREAD = false>
 static int launch_typed(const void* x, uint8_t* codes, float* scales, int64_t rows, int64_t ncols, int kind,
                         cudaStream_t s, const int32_t* pos = nullptr, int32_t k = 0, int32_t pitch = 0) {
     const int64_t nb = fp8_blocks(ncols), n_blocks = rows * nb;
-    const int64_t ctas = (n_blocks + 2 * kQuantWarps - 1) / (2 * kQuantWarps);
-    if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "rows * ncols too large for one launch");
+    constexpr int64_t per = 2 * kQuantWarps * kQuantAhead;
+    const int64_t ctas = (n_blocks + per - 1) / per;
+    if (n_blocks > 0xFFFF0000LL) return fail(FT_ERR_SIZE, "rows * ceil(ncols / 128) too large for one launch");
     const dim3 grid(static_cast<unsigned>(ctas)), block(32 * kQuantWarps);
-    quantize_fp8_kernel<T, GATED, SPREAD><<<grid, block, 0, s>>>(static_cast<const T*>(x), codes, scales, n_blocks,
-                                                                static_cast<int32_t>(nb), ncols, kind, pos, k, pitch);
+    quantize_fp8_kernel<T, GATED, SPREAD><<<grid, block, 0, s>>>(static_cast<const T*>(x), codes, scales, static_cast<uint32_t>(n_blocks),
+                                                                static_cast<uint32_t>(nb), ncols, kind, pos, k, pitch);
     return check_launch("quantize_fp8_kernel", grid, block, 0);
 }
 
