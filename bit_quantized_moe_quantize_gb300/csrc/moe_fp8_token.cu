@@ -3,8 +3,11 @@
 //   token_gated: quantizes the token's row of x (in every CTA, into shared memory), takes its
 //     dot products with gate and up rows of one slot's expert, and writes act(gate) * up in fp32
 //   token_down: quantizes each slot's activated row (a warp per slot, into shared memory),
-//     takes its dot products with eight rows of w2, and adds the slots' sums with their
-//     weights, in the order of the slots
+//     takes its dot products with rows of w2, four at a time, and adds the slots' sums with
+//     their weights, in the order of the slots
+//
+// The grids hold a few CTAs per SM, and a CTA goes over several groups of rows: with one
+// group each, quantizing the row again and again took eight tokens 130 us.
 //
 // Reading the experts' matrices once is what is left to wait for, beside the launches: the
 // same pieces as separate launches (quantizer, product, quantizer, product, weighted sum)
@@ -18,7 +21,7 @@
 
 namespace ft {
 
-constexpr int kTokenWarps = 8, kPairs = 2, kDownRows = 8;
+constexpr int kTokenWarps = 8, kPairs = 2, kDownRows = 4, kCtasPerSm = 3;
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -30,20 +33,31 @@ __device__ __forceinline__ void quantize_row(const T* x, int32_t n, uint8_t* cod
                                              uint32_t warps) {
     const uint32_t sub = lane_id() & 15u;
     const int32_t nb = (n + kFp8Block - 1) / kFp8Block;
-    for (int32_t b0 = 2 * static_cast<int32_t>(warp); b0 < nb; b0 += 2 * static_cast<int32_t>(warps)) {
-        const int32_t b = b0 + static_cast<int32_t>(lane_id() >> 4), c = b * kFp8Block + 8 * static_cast<int32_t>(sub);
-        float v[8] = {};
-        if (c < n) {
-            if constexpr (sizeof(T) == 4) load_vec_plain<8>(x + c, v);
-            else load_vec<T, 8>(x + c, v);
+    constexpr int AHEAD = 4;      // block pairs whose values are on their way at once
+    for (int32_t b0 = 2 * static_cast<int32_t>(warp); b0 < nb; b0 += 2 * AHEAD * static_cast<int32_t>(warps)) {
+        float v[AHEAD][8] = {};
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int32_t c = (b0 + 2 * i * static_cast<int32_t>(warps) + static_cast<int32_t>(lane_id() >> 4)) * kFp8Block + 8 * static_cast<int32_t>(sub);
+            if (c < n) {
+                if constexpr (sizeof(T) == 4) load_vec_plain<8>(x + c, v[i]);
+                else load_vec<T, 8>(x + c, v[i]);
+            }
         }
-        const float scale = fp8_block_scale(v);
-        if (c < n) *reinterpret_cast<uint2*>(codes + c) = fp8_codes(v, scale);
-        if (sub == 0 && b < nb) scales[b] = scale;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int32_t b = b0 + 2 * i * static_cast<int32_t>(warps) + static_cast<int32_t>(lane_id() >> 4);
+            const int32_t c = b * kFp8Block + 8 * static_cast<int32_t>(sub);
+            if (b0 + 2 * i * static_cast<int32_t>(warps) < nb) {      // the whole warp
+                const float scale = fp8_block_scale(v[i]);
+                if (c < n) *reinterpret_cast<uint2*>(codes + c) = fp8_codes(v[i], scale);
+                if (sub == 0 && b < nb) scales[b] = scale;
+            }
+        }
     }
 }
 
-// Dot products of R rows (pointers w, scales sw; lane offsets included in w) with a quantized row in shared memory.
+// Dot products of R rows (w: with the lane's offset; sw: their scales) with a quantized row in shared memory.
 template <int R>
 __device__ __forceinline__ void dot_rows(const uint8_t* const (&w)[R], const float* const (&sw)[R], int32_t n, const uint8_t* codes,
                                          const float* scales, float (&acc)[R]) {
@@ -68,7 +82,7 @@ __device__ __forceinline__ void dot_rows(const uint8_t* const (&w)[R], const flo
         for (int k = 16; k > 0; k >>= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], k);
 }
 
-// grid: (ceil(n_inter / (kTokenWarps * kPairs)), slots)
+// grid: (CTAs per slot, slots)
 template <typename T>
 __global__ void __launch_bounds__(32 * kTokenWarps)
     token_gated_kernel(const T* __restrict__ x, const uint8_t* __restrict__ w13, const float* __restrict__ s13,
@@ -82,69 +96,80 @@ __global__ void __launch_bounds__(32 * kTokenWarps)
     quantize_row<T>(x + s / top_k * hidden, hidden, row_smem, scales, warp, kTokenWarps);
     __syncthreads();
     grid_dependency_wait();      // the router's choice
-    const int32_t e = ids[s], i0 = (static_cast<int32_t>(blockIdx.x) * kTokenWarps + static_cast<int32_t>(warp)) * kPairs;
-    if (e < 0 || e >= n_experts || i0 >= n_inter) return;
+    const int32_t e = ids[s];
+    if (e < 0 || e >= n_experts) return;
     const int32_t nb = (hidden + kFp8Block - 1) / kFp8Block, blocks = (2 * n_inter + kFp8Block - 1) / kFp8Block;
-    const uint8_t* w[2 * kPairs];
-    const float* sw[2 * kPairs];
+    const int32_t step = static_cast<int32_t>(gridDim.x) * kTokenWarps * kPairs;
+    for (int32_t i0 = (static_cast<int32_t>(blockIdx.x) * kTokenWarps + static_cast<int32_t>(warp)) * kPairs; i0 < n_inter; i0 += step) {
+        const uint8_t* w[2 * kPairs];
+        const float* sw[2 * kPairs];
 #pragma unroll
-    for (int i = 0; i < 2 * kPairs; ++i) {      // gate rows, then up rows; past the end the last one again
-        const int32_t r = min(i0 + i % kPairs, n_inter - 1) + (i < kPairs ? 0 : n_inter);
-        w[i] = w13 + (static_cast<int64_t>(e) * 2 * n_inter + r) * hidden + 16 * lane_id();
-        sw[i] = s13 + (static_cast<int64_t>(e) * blocks + r / kFp8Block) * nb;
+        for (int i = 0; i < 2 * kPairs; ++i) {      // gate rows, then up rows; past the end the last one again
+            const int32_t r = min(i0 + i % kPairs, n_inter - 1) + (i < kPairs ? 0 : n_inter);
+            w[i] = w13 + (static_cast<int64_t>(e) * 2 * n_inter + r) * hidden + 16 * lane_id();
+            sw[i] = s13 + (static_cast<int64_t>(e) * blocks + r / kFp8Block) * nb;
+        }
+        float acc[2 * kPairs] = {};
+        dot_rows<2 * kPairs>(w, sw, hidden, row_smem, scales, acc);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            if (lane_id() == static_cast<uint32_t>(i) && i0 + i < n_inter)
+                mid[s * n_inter + i0 + i] = act_mul_f32(acc[i], acc[kPairs + i], kind);
     }
-    float acc[2 * kPairs] = {};
-    dot_rows<2 * kPairs>(w, sw, hidden, row_smem, scales, acc);
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-        if (lane_id() == static_cast<uint32_t>(i) && i0 + i < n_inter)
-            mid[s * n_inter + i0 + i] = act_mul_f32(acc[i], acc[kPairs + i], kind);
 }
 
-// grid: (ceil(hidden / kDownRows), tokens)
+// grid: (CTAs per token, tokens); a CTA takes `groups` neighbouring groups of rows.
 template <typename TO>
 __global__ void __launch_bounds__(32 * kTokenWarps)
     token_down_kernel(const float* mid, const uint8_t* __restrict__ w2, const float* __restrict__ s2,
                       const int32_t* ids, const float* weights, TO* y, int32_t n_experts,
-                      int32_t top_k, int32_t hidden, int32_t n_inter, int32_t warp_bytes) {
-    extern __shared__ __align__(16) uint8_t row_smem[];      // per warp codes[n_inter], scales; then sums[top_k][kDownRows]
+                      int32_t top_k, int32_t hidden, int32_t n_inter, int32_t warp_bytes, int32_t groups) {
+    extern __shared__ __align__(16) uint8_t row_smem[];      // per warp codes[n_inter], scales; then sums[groups][top_k][kDownRows]
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
     uint8_t* codes = row_smem + warp * static_cast<uint32_t>(warp_bytes);
     float* scales = reinterpret_cast<float*>(codes + n_inter);
     float* sums = reinterpret_cast<float*>(row_smem + kTokenWarps * static_cast<uint32_t>(warp_bytes));
     const int64_t t = blockIdx.y;
-    const int32_t r0 = static_cast<int32_t>(blockIdx.x) * kDownRows;
+    const int32_t r0 = static_cast<int32_t>(blockIdx.x) * groups * kDownRows;
     const int32_t nb = (n_inter + kFp8Block - 1) / kFp8Block, blocks = (hidden + kFp8Block - 1) / kFp8Block;
     grid_dependency_wait();
     for (int32_t j = static_cast<int32_t>(warp); j < top_k; j += kTokenWarps) {
         const int64_t s = t * top_k + j;
         const int32_t e = ids[s];
-        float acc[kDownRows] = {};
-        if (e >= 0 && e < n_experts) {
+        const bool routed = e >= 0 && e < n_experts;
+        if (routed) {
             __syncwarp();
             quantize_row<float>(mid + s * n_inter, n_inter, codes, scales, 0, 1);
             __syncwarp();
-            const uint8_t* w[kDownRows];
-            const float* sw[kDownRows];
-#pragma unroll
-            for (int i = 0; i < kDownRows; ++i) {
-                const int32_t r = min(r0 + i, hidden - 1);
-                w[i] = w2 + (static_cast<int64_t>(e) * hidden + r) * n_inter + 16 * lane;
-                sw[i] = s2 + (static_cast<int64_t>(e) * blocks + r / kFp8Block) * nb;
-            }
-            dot_rows<kDownRows>(w, sw, n_inter, codes, scales, acc);
         }
+        for (int32_t g = 0; g < groups; ++g) {
+            const int32_t rg = r0 + g * kDownRows;
+            if (rg >= hidden) break;
+            float acc[kDownRows] = {};
+            if (routed) {
+                const uint8_t* w[kDownRows];
+                const float* sw[kDownRows];
 #pragma unroll
-        for (int i = 0; i < kDownRows; ++i)
-            if (lane == static_cast<uint32_t>(i)) sums[j * kDownRows + i] = acc[i];
+                for (int i = 0; i < kDownRows; ++i) {
+                    const int32_t r = min(rg + i, hidden - 1);
+                    w[i] = w2 + (static_cast<int64_t>(e) * hidden + r) * n_inter + 16 * lane;
+                    sw[i] = s2 + (static_cast<int64_t>(e) * blocks + r / kFp8Block) * nb;
+                }
+                dot_rows<kDownRows>(w, sw, n_inter, codes, scales, acc);
+            }
+#pragma unroll
+            for (int i = 0; i < kDownRows; ++i)
+                if (lane == static_cast<uint32_t>(i)) sums[(g * top_k + j) * kDownRows + i] = acc[i];
+        }
     }
     __syncthreads();
-    const int32_t r = r0 + static_cast<int32_t>(threadIdx.x);
-    if (threadIdx.x < kDownRows && r < hidden) {
+    for (int32_t i = static_cast<int32_t>(threadIdx.x); i < groups * kDownRows; i += 32 * kTokenWarps) {
+        const int32_t r = r0 + i;
+        if (r >= hidden) break;
         float sum = 0.0f;
         for (int32_t j = 0; j < top_k; ++j) {
             const float wj = weights[t * top_k + j];
-            if (wj != 0.0f) sum = fmaf(wj, sums[j * kDownRows + threadIdx.x], sum);
+            if (wj != 0.0f) sum = fmaf(wj, sums[(i / kDownRows * top_k + j) * kDownRows + i % kDownRows], sum);
         }
         y[t * hidden + r] = from_f32<TO>(sum);
     }
@@ -155,8 +180,16 @@ namespace {
 
 int32_t down_warp_bytes(int64_t n_inter) { return static_cast<int32_t>((n_inter + 4 * fp8_blocks(n_inter) + 15) / 16 * 16); }
 
-size_t down_smem(int64_t n_inter, int32_t top_k) {
-    return static_cast<size_t>(kTokenWarps) * down_warp_bytes(n_inter) + static_cast<size_t>(top_k) * kDownRows * 4;
+// Groups of rows of w2 per CTA: as many as leave a few CTAs per SM.
+int32_t down_groups(int64_t tokens, int64_t hidden) {
+    const int64_t all = (hidden + kDownRows - 1) / kDownRows;
+    int64_t ctas = kCtasPerSm * static_cast<int64_t>(sm_count()) / tokens;
+    ctas = ctas < 1 ? 1 : ctas < all ? ctas : all;
+    return static_cast<int32_t>((all + ctas - 1) / ctas);
+}
+
+size_t down_smem(int64_t n_inter, int32_t top_k, int32_t groups) {
+    return static_cast<size_t>(kTokenWarps) * down_warp_bytes(n_inter) + static_cast<size_t>(groups) * top_k * kDownRows * 4;
 }
 
 template <typename... A>
@@ -184,17 +217,25 @@ int launch_dependent(void (*kernel)(A...), const char* name, dim3 grid, size_t s
 }  // namespace
 
 bool fp8_token_ok(int64_t n_slots, int64_t tokens, int32_t top_k, int64_t hidden, int64_t n_inter) {
+    // Past some 40 MB of matrices the separate launches, whose warps are not tied to slots, read
+    // them faster (us, these kernels / separate): 8 MB 10.5 / 16.7, 38 MB 16.2 / 20.2, 50 MB
+    // 22.9 / 21.3, 75 MB 28.4 / 28.9, 151 MB 52.5 / 45.4.
+    if (3 * n_slots * hidden * n_inter > 40'000'000) return false;
     return n_slots <= 65535 && tokens <= 65535 && hidden + 4 * fp8_blocks(hidden) <= 200 * 1024 &&
-           down_smem(n_inter, top_k) <= 200 * 1024;
+           down_smem(n_inter, top_k, down_groups(tokens, hidden)) <= 200 * 1024;
 }
 
 int launch_fp8_token_layer(const void* x, int x_dtype, const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2,
                            const int32_t* ids, const float* weights, float* mid, void* y, int64_t tokens, int32_t top_k,
                            int32_t n_experts, int64_t hidden, int64_t n_inter, int kind, cudaStream_t s) {
     const int32_t H = static_cast<int32_t>(hidden), I = static_cast<int32_t>(n_inter);
-    const dim3 g1(static_cast<unsigned>((n_inter + kTokenWarps * kPairs - 1) / (kTokenWarps * kPairs)), static_cast<unsigned>(tokens * top_k));
-    const dim3 g2(static_cast<unsigned>((hidden + kDownRows - 1) / kDownRows), static_cast<unsigned>(tokens));
-    const size_t sm1 = static_cast<size_t>(hidden + 4 * fp8_blocks(hidden)), sm2 = down_smem(n_inter, top_k);
+    const int64_t slots = tokens * top_k, most = (n_inter + kTokenWarps * kPairs - 1) / (kTokenWarps * kPairs);
+    const int64_t fit = kCtasPerSm * static_cast<int64_t>(sm_count()) / slots, ctas = fit > 0 ? fit : 1;
+    const int32_t groups = down_groups(tokens, hidden);
+    const int64_t per = static_cast<int64_t>(groups) * kDownRows;
+    const dim3 g1(static_cast<unsigned>(ctas < most ? ctas : most), static_cast<unsigned>(slots));
+    const dim3 g2(static_cast<unsigned>((hidden + per - 1) / per), static_cast<unsigned>(tokens));
+    const size_t sm1 = static_cast<size_t>(hidden + 4 * fp8_blocks(hidden)), sm2 = down_smem(n_inter, top_k, groups);
     const int32_t wb = down_warp_bytes(n_inter);
     int st;
     if (x_dtype == FT_DTYPE_F16)
@@ -207,9 +248,9 @@ int launch_fp8_token_layer(const void* x, int x_dtype, const uint8_t* w13, const
     const float* m = mid;
     if (x_dtype == FT_DTYPE_F16)
         return launch_dependent(token_down_kernel<__half>, "token_down_kernel", g2, sm2, s, m, w2, s2, ids, weights,
-                                static_cast<__half*>(y), n_experts, top_k, H, I, wb);
+                                static_cast<__half*>(y), n_experts, top_k, H, I, wb, groups);
     return launch_dependent(token_down_kernel<__nv_bfloat16>, "token_down_kernel", g2, sm2, s, m, w2, s2, ids, weights,
-                            static_cast<__nv_bfloat16*>(y), n_experts, top_k, H, I, wb);
+                            static_cast<__nv_bfloat16*>(y), n_experts, top_k, H, I, wb, groups);
 }
 
 }  // namespace ft
