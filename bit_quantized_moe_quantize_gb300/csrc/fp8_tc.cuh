@@ -92,16 +92,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
         : "memory");
 }
 
-// Four rows of a map whose box is one row high, one under the other.
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const void* tmap, int32_t x, const int32_t (&y)[4],
-                                                 uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                  "r"(ncols)
@@ -152,6 +142,7 @@ __device__ __forceinline__ void zero_unrouted(const int32_t* ids, int64_t n_slot
 }
 
 // Forms within one CTA (cta_group::1).
+// The gather takes four rows of a map whose box is one row high, one under the other.
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int32_t x, const int32_t (&y)[4], uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "

@@ -204,14 +204,23 @@ __device__ __forceinline__ float order32_value(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
 }
 
-__device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
-    const uint32_t x = max(a, b), y = min(a, b);
-    a = x;
-    b = y;
+template <typename K>
+__device__ __forceinline__ void order_pair(K& a, K& b) {
+    if constexpr (sizeof(K) == 4) {
+        const uint32_t x = max(a, b), y = min(a, b);
+        a = x;
+        b = y;
+    } else {
+        const bool turn = a < b;
+        const K x = turn ? b : a, y = turn ? a : b;
+        a = x;
+        b = y;
+    }
 }
 
 // Sorts eight keys, largest first (odd-even merges: 19 exchanges).
-__device__ __forceinline__ void sort8(uint32_t (&k)[8]) {
+template <typename K>
+__device__ __forceinline__ void sort8(K (&k)[8]) {
     order_pair(k[0], k[1]);
     order_pair(k[2], k[3]);
     order_pair(k[4], k[5]);
@@ -235,9 +244,10 @@ __device__ __forceinline__ void sort8(uint32_t (&k)[8]) {
 
 // a := the eight largest of two sorted lists of eight, sorted.  Largest of a against smallest
 // of b, and so on, leaves them as a bitonic list; three halvings sort that.
-__device__ __forceinline__ void merge8(uint32_t (&a)[8], const uint32_t (&b)[8]) {
+template <typename K>
+__device__ __forceinline__ void merge8(K (&a)[8], const K (&b)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+    for (int i = 0; i < 8; ++i) a[i] = a[i] > b[7 - i] ? a[i] : b[7 - i];
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
@@ -302,11 +312,22 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateAr
     }
     int32_t* ids = a.ids + t * a.top_k;
     float* weights = a.weights + t * a.top_k;
-    if constexpr (PACKED && LANES >= 8) {
-        // up to eight choices of 32-bit keys: every lane's eight largest by sorting networks, then
-        // the lanes' lists merged pairwise; the rounds below take three times the instructions
+    // softmax weights of the largest logits, renormalised, need no sum over all
+    const bool cancel = by_logit && a.renormalize && a.score == FT_SCORE_SOFTMAX;
+    auto chosen = [&](K m, int32_t& at) {      // a choice's expert and logit
+        if constexpr (PACKED) {
+            at = static_cast<int32_t>(0xFFFFu - (m & 0xFFFFu));
+            return order16_value<T>(static_cast<uint32_t>(m) >> 16);
+        } else {
+            at = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(m));
+            return by_logit ? order32_value(static_cast<uint32_t>(m >> 32)) : to_f32<T>(row[at]);
+        }
+    };
+    if constexpr (LANES >= 8) {
+        // up to eight choices: every lane's eight largest by sorting networks, then the lanes' lists
+        // merged pairwise; the rounds below take three times the instructions
         if (a.top_k <= 8) {
-            uint32_t k8[8], l8[8];
+            K k8[8], l8[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 k8[i] = key[i];
@@ -321,27 +342,28 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateAr
                 for (int i = 0; i < 8; ++i) l8[i] = __shfl_xor_sync(0xFFFFFFFFu, k8[i], o);
                 merge8(k8, l8);
             }
-            uint32_t m = k8[0];      // lane j takes choice j
+            K m = k8[0];      // lane j takes choice j
 #pragma unroll
             for (int i = 1; i < 8; ++i) m = sub == static_cast<uint32_t>(i) ? k8[i] : m;
             const bool mine = sub < static_cast<uint32_t>(a.top_k);
+            int32_t at = -1;
             float w = 0.0f;
             if (mine && m != 0) {
-                const float l = order16_value<T>(m >> 16);
-                w = a.renormalize && a.score == FT_SCORE_SOFTMAX ? gate_exp(l, top) : gate_score(l, top, sum, a.score);
+                const float l = chosen(m, at);
+                w = cancel ? gate_exp(l, top) : gate_score(l, top, sum, a.score);
             }
             float total = w;
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
             if (there && mine) {
-                ids[sub] = m != 0 ? static_cast<int32_t>(0xFFFFu - (m & 0xFFFFu)) : -1;
+                ids[sub] = at;
                 weights[sub] = (a.renormalize ? __fdiv_rn(w, fmaxf(total, kGateTiny)) : w) * a.scale;
             }
             return;
         }
     }
     float total = 0.0f, mine = 0.0f;      // mine: weight `sub` (of the first LANES)
-    const bool few = a.top_k <= LANES, cancel = by_logit && a.renormalize && a.score == FT_SCORE_SOFTMAX;
+    const bool few = a.top_k <= LANES;
     for (int32_t j = 0; j < a.top_k; ++j) {
         K m = best;
 #pragma unroll
@@ -360,14 +382,7 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateAr
         int32_t at = -1;
         float w = 0.0f;
         if (m != 0) {
-            float l;
-            if constexpr (PACKED) {
-                at = static_cast<int32_t>(0xFFFFu - (m & 0xFFFFu));
-                l = order16_value<T>(static_cast<uint32_t>(m) >> 16);
-            } else {
-                at = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(m));
-                l = by_logit ? order32_value(static_cast<uint32_t>(m >> 32)) : to_f32<T>(row[at]);
-            }
+            const float l = chosen(m, at);
             w = cancel ? gate_exp(l, top) : gate_score(l, top, sum, a.score);
         }
         total += w;
