@@ -141,16 +141,7 @@ __device__ __forceinline__ void zero_unrouted(const int32_t* ids, int64_t n_slot
     }
 }
 
-// Forms within one CTA (cta_group::1).
-// The gather takes four rows of a map whose box is one row high, one under the other.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int32_t x, const int32_t (&y)[4], uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(smem_u32(bar))
-        : "memory");
-}
-
+// The form within one CTA (cta_group::1).
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(

@@ -35,6 +35,8 @@
 //
 // Rows lie in router order: a TMA gather fetches four 128-byte rows per instruction
 // and takes the unit about 85 cycles, so 128 slots a CTA would need 2700 a block.
+#include <atomic>
+
 #include "fp8_order.cuh"
 #include "fp8_tc.cuh"
 #include "ft_internal.h"
@@ -617,12 +619,13 @@ template <typename TO, bool GATED>
 int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs& a, void* out, int grid, cudaStream_t s) {
     using C = Pair;
     const void* k = reinterpret_cast<const void*>(moe_fp8_pair_kernel<TO, GATED>);
-    static int regs = 0;     // of this instantiation: with fewer than LAUNCH_REGS the split of registers would never end
+    static std::atomic<int> known{0};     // registers of this instantiation: with fewer than LAUNCH_REGS the split of registers would never end
+    int regs = known.load(std::memory_order_relaxed);
     if (regs == 0) {
         cudaFuncAttributes at{};
         const cudaError_t e = cudaFuncGetAttributes(&at, k);
         if (e != cudaSuccess) return fail(FT_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
-        regs = at.numRegs;
+        known.store(regs = at.numRegs, std::memory_order_relaxed);
     }
     if (regs * C::THREADS < C::drain_regs(GATED) * 256 + C::other_regs(GATED) * 128)
         return fail(FT_ERR_LAUNCH, "moe_fp8_pair_kernel was compiled with %d registers, %d are needed", regs, C::LAUNCH_REGS);

@@ -1,8 +1,8 @@
 // The FP8 products for few slots per expert (up to 128 in a tile): what bounds them is
 // reading the experts' matrices once.
 //
-// One tile: up to 128 weight rows of an expert x up to NW of its slots (16 or 32), one CTA, tcgen05 MMAs with M = 128 weight rows and N = the tile's slots rounded
-// up to 16.  Here the weight rows lie along the tensor-memory lanes: with few slots the
+// One tile: up to 128 weight rows of an expert x up to NW of its slots (16 or 32), one CTA,
+// tcgen05 MMAs with M = 128 weight rows and N = the tile's slots rounded up to 16.  Here the weight rows lie along the tensor-memory lanes: with few slots the
 // scales of a block are few, and a warp reads them from shared memory at a broadcast for
 // its 32 rows.  Where a batch has too few tiles of 128 rows to fill the GPU, a tile takes
 // 64 or 32 weight rows; the MMA still runs over 128 lanes, whose other rows are whatever
@@ -15,10 +15,13 @@
 // Up to 1024 slots are put in order by every CTA for itself, in shared memory (some 2 us
 // less than a launch and the reads of its results); more come ordered.
 //
-// Per CTA: warps 0-3 drain (32 weight rows each), warp 4 TMA producer, warp 5 MMA, warp 6
-// scales (sa * sw of a unit's blocks and slots to a ring in shared memory), warp 7 zeroes
-// the rows of slots without an expert.
+// Per CTA: warps 0-3 drain (32 weight rows each), warp 4 TMA producer of the weight rows,
+// warp 5 MMA, warp 6 scales (sa * sw of a unit's blocks and slots to a ring in shared memory),
+// warp 7 copies the slots' rows and zeroes the rows of slots without an expert.
 //
+// The slots' rows lie anywhere, and are copied by cp.async, 16 bytes a lane, into the place that
+// the 128-byte swizzle gives them.  A TMA gather fetches four rows and takes the unit about 85
+// cycles: 32 slots in each of two CTAs kept it busy for most of a block's time.
 #include "fp8_order.cuh"
 #include "fp8_tc.cuh"
 #include "ft_internal.h"
@@ -47,9 +50,8 @@ struct Narrow {
     static constexpr int OFF_ORDER = OFF_TMEM + 16;
     static constexpr int SMEM_BYTES = OFF_ORDER + (2 * (MAX_E + 1) + 1024 + 8) * 4 + 1024;
     static_assert(kChunkWarps * MAX_E * 4 <= RING_BYTES, "counts");
-    static constexpr int WARP_PRODUCER = 4, WARP_MMA = 5, WARP_SCALE = 6;
+    static constexpr int WARP_PRODUCER = 4, WARP_MMA = 5, WARP_SCALE = 6, WARP_ROWS = 7;
     static constexpr int THREADS = 256;
-    static constexpr int ROW_BOX = 16;
     static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "shared memory budget of two CTAs");
 };
 
@@ -58,14 +60,15 @@ struct NarrowArgs {
     const int32_t* perm;
     const int32_t* offsets;
     const int32_t* tiles;        // prefix of tiles of NW slots
+    const uint8_t* act;
     const float* act_scales;
     const float* w_scales;
     uint32_t* err;
-    int64_t n_slots, nrows;
+    int64_t n_slots, nrows, ncols;
     int32_t act_div, n_experts, nb, row_tiles, row_blocks, scale_pitch;
     int32_t br;                  // weight rows of a tile: 32, 64 or 128
     int32_t stages;
-    bool ordered;
+    bool ordered;                // activation rows lie in router order
     bool orders;                 // perm, offsets and tiles are worked out by the CTA
 };
 
@@ -91,10 +94,9 @@ __device__ __forceinline__ NarrowTile narrow_tile(const NarrowArgs& a, const int
     return t;
 }
 
-template <int NW, typename TO, bool GATHER>
+template <int NW, typename TO>
 __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
-    moe_fp8_narrow_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                          const __grid_constant__ NarrowArgs a, TO* __restrict__ out) {
+    moe_fp8_narrow_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ NarrowArgs a, TO* __restrict__ out) {
     using C = Narrow<NW>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::MAX_STAGES; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 1 + 32);      // the producer and the lanes that copy rows
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < C::UNITS; ++i) {
@@ -132,10 +134,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
-    if (warp == C::WARP_PRODUCER && lane == 0) {
-        prefetch_tmap(&wmap);
-        prefetch_tmap(&xmap);
-    }
+    if (warp == C::WARP_PRODUCER && lane == 0) prefetch_tmap(&wmap);
     const int32_t *offsets = a.offsets, *tiles = a.tiles, *perm = a.perm;
     if (a.orders) {
         int32_t* o = reinterpret_cast<int32_t*>(smem + C::OFF_ORDER);
@@ -176,32 +175,12 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
             const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
-            constexpr int PER = GATHER ? 4 : C::ROW_BOX;
-            const bool copies = static_cast<int32_t>(lane) * PER < t.n;
-            int32_t y[4] = {0, 0, 0, 0};
-            if (copies) {
-                const int32_t p = t.p0 + static_cast<int32_t>(lane) * PER;
-                if constexpr (GATHER) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = perm[min(p + i, t.p0 + t.n - 1)] / a.act_div;
-                } else {
-                    y[0] = p;
-                }
-            }
             const int32_t wy = static_cast<int32_t>(static_cast<int64_t>(t.e) * a.nrows + t.r0);
-            const uint32_t bytes = static_cast<uint32_t>(a.br + (t.n + PER - 1) / PER * PER) * kFp8Block;
             for (int32_t b = 0; b < nb; ++b) {
                 if (!mbar_wait_warp(&empty[s], phase, a.err)) { ok = false; break; }
-                uint8_t* dst = smem + static_cast<uint32_t>(s) * stage_bytes;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[s], bytes);
-                    tma_load_2d(dst + b_bytes, &wmap, b * kFp8Block, wy, &full[s]);
-                }
-                __syncwarp();
-                if (copies) {
-                    uint8_t* d = dst + lane * (PER * kFp8Block);
-                    if constexpr (GATHER) tma_gather4(smem_u32(d), &xmap, b * kFp8Block, y, &full[s]);
-                    else tma_load_2d(d, &xmap, b * kFp8Block, y[0], &full[s]);
+                    mbar_arrive_expect_tx(&full[s], stage_bytes - b_bytes);
+                    tma_load_2d(smem + static_cast<uint32_t>(s) * stage_bytes + b_bytes, &wmap, b * kFp8Block, wy, &full[s]);
                 }
                 __syncwarp();
                 if (++s == stages) {
@@ -226,6 +205,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
                 const int32_t n = min(C::G, nb - b0);
                 for (int32_t g = 0; g < n; ++g) {
                     if (!mbar_wait_warp(&full[s], phase, a.err)) { ok = false; break; }
+                    fence_proxy_async_smem();      // the copied rows are ordinary writes
                     tc_fence_after();
                     if (elected) {
                         const uint64_t bdesc = desc0 + ((static_cast<uint32_t>(s) * stage_bytes) >> 4), adesc = bdesc + (b_bytes >> 4);
@@ -296,6 +276,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
             float acc[NW];
 #pragma unroll
             for (int i = 0; i < NW; ++i) acc[i] = 0.0f;
+            const int32_t pl = t.p0 + min(static_cast<int32_t>(lane), t.n - 1), slot_of = perm ? perm[pl] : pl;      // of slot `lane`
             for (int32_t b0 = 0; b0 < nb; b0 += C::G, ++unit) {
                 const uint32_t u = unit % C::UNITS, r = unit % C::NSC;
                 if (!mbar_wait2_warp(&sc_full[r], (unit / C::NSC) & 1u, &acc_full[u], (unit / C::UNITS) & 1u, a.err)) { ok = false; break; }
@@ -332,13 +313,49 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
 #pragma unroll
             for (int c = 0; c < NW; ++c) {
                 if (c < t.n) {
-                    const int32_t p = t.p0 + c, slot = perm ? perm[p] : p;
+                    const int32_t slot = __shfl_sync(0xFFFFFFFFu, slot_of, c);
                     if (row < a.nrows) out[static_cast<int64_t>(slot) * a.nrows + row] = from_f32<TO>(acc[c]);
                 }
             }
         }
-    } else if (warp == 7 && a.ids) {
-        zero_unrouted<TO>(a.ids, a.n_slots, a.n_experts, a.nrows, a.err, out, blockIdx.x, gridDim.x);
+    } else if (warp == C::WARP_ROWS) {
+        // ---------------------------------------------------------------- rows
+        // lane: 16-byte word `word` of rows first, first + 4, ..
+        const uint32_t word = lane & 7u, first = lane >> 3;
+        int32_t s = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
+            const uint8_t* src[NW / 4];
+#pragma unroll
+            for (int i = 0; i < NW / 4; ++i) {
+                const int32_t p = t.p0 + min(static_cast<int32_t>(first) + 4 * i, t.n - 1);
+                src[i] = a.act + static_cast<int64_t>(a.ordered ? p : perm[p] / a.act_div) * a.ncols + 16 * word;
+            }
+            int64_t left = a.ncols - 16 * word;      // columns from this lane's word to the rows' end
+            for (int32_t b = 0; b < nb; ++b, left -= kFp8Block) {
+                if (!mbar_wait_warp(&empty[s], phase, a.err)) { ok = false; break; }
+                const uint32_t dst = smem_u32(smem + static_cast<uint32_t>(s) * stage_bytes);
+#pragma unroll
+                for (int i = 0; i < NW / 4; ++i) {
+                    const uint32_t r = first + 4 * i;
+                    if (static_cast<int32_t>(r) < t.n)      // (words past the rows' end arrive as 0)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * kFp8Block + ((word ^ (r & 7u)) << 4)),
+                                     "l"(left > 0 ? src[i] : a.act), "r"(left > 0 ? 16 : 0)
+                                     : "memory");
+                    src[i] += kFp8Block;
+                }
+                // arrives when this lane's copies have
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[s])) : "memory");
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (a.ids) zero_unrouted<TO>(a.ids, a.n_slots, a.n_experts, a.nrows, a.err, out, blockIdx.x, gridDim.x);
     }
     __syncwarp();
     tc_fence_before();
@@ -349,27 +366,17 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
 // ------------------------------------------------------------------- host
 namespace {
 
-template <int NW, typename TO, bool GATHER>
-int launch_narrow(const CUtensorMap& wmap, const CUtensorMap& xmap, NarrowArgs& a, void* out, int64_t tiles, cudaStream_t s) {
+template <int NW, typename TO>
+int launch_narrow(const CUtensorMap& wmap, NarrowArgs& a, void* out, int64_t tiles, cudaStream_t s) {
     using C = Narrow<NW>;
-    const void* k = reinterpret_cast<const void*>(moe_fp8_narrow_kernel<NW, TO, GATHER>);
+    const void* k = reinterpret_cast<const void*>(moe_fp8_narrow_kernel<NW, TO>);
     const int stage = (NW + a.br) * kFp8Block;
     a.stages = C::RING_BYTES / stage < C::MAX_STAGES ? C::RING_BYTES / stage : C::MAX_STAGES;
     if (int st = set_smem_limit(k, C::SMEM_BYTES)) return st;
     const int64_t ctas = 2 * sm_count();
     const dim3 grid(static_cast<unsigned>(tiles < ctas ? tiles : ctas));
-    moe_fp8_narrow_kernel<NW, TO, GATHER><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, xmap, a, static_cast<TO*>(out));
+    moe_fp8_narrow_kernel<NW, TO><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(wmap, a, static_cast<TO*>(out));
     return check_launch("moe_fp8_narrow_kernel", grid, dim3(C::THREADS), C::SMEM_BYTES);
-}
-
-template <int NW>
-int launch_narrow_width(const CUtensorMap& wmap, const CUtensorMap& xmap, NarrowArgs& a, void* out, int out_dtype, bool gather,
-                        int64_t tiles, cudaStream_t s) {
-    if (gather)
-        return out_dtype == FT_DTYPE_F32 ? launch_narrow<NW, float, true>(wmap, xmap, a, out, tiles, s)
-                                         : launch_narrow<NW, __nv_bfloat16, true>(wmap, xmap, a, out, tiles, s);
-    return out_dtype == FT_DTYPE_F32 ? launch_narrow<NW, float, false>(wmap, xmap, a, out, tiles, s)
-                                     : launch_narrow<NW, __nv_bfloat16, false>(wmap, xmap, a, out, tiles, s);
 }
 
 }  // namespace
@@ -380,19 +387,20 @@ bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width) {
 
 // width: slots per tile (16 or 32), that of p.order's tiles
 int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s) {
-    const bool boxes = p.ordered || !p.ids;
     NarrowArgs a{};
+    a.act = p.act;
     a.act_scales = p.act_scales;
     a.w_scales = p.w_scales;
     a.err = err;
     a.n_slots = p.n_slots;
     a.nrows = p.nrows;
+    a.ncols = p.ncols;
     a.act_div = p.act_div;
     a.n_experts = p.n_experts;
     a.nb = static_cast<int32_t>(fp8_blocks(p.ncols));
     a.row_blocks = static_cast<int32_t>(fp8_blocks(p.nrows));
     a.scale_pitch = p.scale_pitch;
-    a.ordered = boxes;
+    a.ordered = p.ordered || !p.ids;
     if (p.ids) {
         a.ids = p.ids;
         a.orders = fp8_orders_itself(p.n_slots, p.n_experts, width);
@@ -408,17 +416,16 @@ int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, 
     a.br = 128;
     while (a.br > 32 && likely * ((p.nrows + a.br - 1) / a.br) < 2 * sm_count()) a.br /= 2;
     a.row_tiles = static_cast<int32_t>((p.nrows + a.br - 1) / a.br);
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap;
     if (int st = encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weights, p.ncols,
                            static_cast<uint64_t>(p.n_experts) * p.nrows, p.ncols, kFp8Block, a.br,
                            CU_TENSOR_MAP_SWIZZLE_128B, "FP8 weights"))
         return st;
-    if (int st = encode_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.act, p.ncols, p.act_rows, p.ncols, kFp8Block,
-                           boxes ? 16 : 1, CU_TENSOR_MAP_SWIZZLE_128B, "FP8 activations"))
-        return st;
     const int64_t tiles = most_tiles * a.row_tiles;
-    if (width == 16) return launch_narrow_width<16>(wmap, xmap, a, out, out_dtype, !boxes, tiles, s);
-    return launch_narrow_width<32>(wmap, xmap, a, out, out_dtype, !boxes, tiles, s);
+    const bool f32 = out_dtype == FT_DTYPE_F32;
+    if (width == 16)
+        return f32 ? launch_narrow<16, float>(wmap, a, out, tiles, s) : launch_narrow<16, __nv_bfloat16>(wmap, a, out, tiles, s);
+    return f32 ? launch_narrow<32, float>(wmap, a, out, tiles, s) : launch_narrow<32, __nv_bfloat16>(wmap, a, out, tiles, s);
 }
 
 }  // namespace ft
