@@ -182,7 +182,8 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
 // tiles (`spread`), else by token; the gated values' codes and
 // scales in router order; where the first product does not quantize them itself
 // (n_inter % 128 != 0, or few slots per expert) its fp32 rows, codes by slot and (`spread`) copies
-// of them in router order; the second product's bf16 rows.
+// of them in router order; the second product's bf16 rows (half the bytes of fp32; their
+// rounding, at most 2^-8, is far below that of the codes, 2^-4, which both products start from).
 struct LayerWs {
     Fp8Order order;
     size_t xq, xs, mq, ms, h, oq, os, rows, total;

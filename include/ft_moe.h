@@ -686,8 +686,8 @@ FT_API int ft_moe_combine(const void* rows, int32_t rows_dtype, const float* top
  * ft_quantize_fp8 of x, the routed product with w13 (gate rows, then up rows),
  * act(gate) * up quantized, the routed product with w2 and ft_moe_combine.
  * The gated values are fp32 when they are quantized; the rows of the second
- * product are rounded to bf16 before they are weighted (not where a batch has at
- * most half a slot per expert: there they are added up in fp32).
+ * product are rounded to bf16 before they are weighted (a few tokens with small
+ * matrices have them added up in fp32 instead).
  *   x       device, [tokens][hidden] of x_dtype (FT_DTYPE_F16 or FT_DTYPE_BF16),
  *           16-byte aligned; y the same shape and type, out
  *   w13     [n_experts][2 * n_inter][hidden] e4m3, s13 its scales

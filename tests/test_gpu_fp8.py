@@ -452,3 +452,165 @@ def test_binding_refuses(ft):
         ft.moe_gate(torch.zeros(2, 8, device="cuda"), 3, n_groups=4, topk_groups=1)
     with pytest.raises(ValueError):
         ft.moe_combine(torch.zeros(2, 3, 8, device="cuda"), torch.zeros(2, 2, device="cuda"))
+
+
+# ------------------------------------------------------- between the variants
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("E", [7, 16, 17, 32, 33, 128, 129, 256, 257, 511, 512, 513])
+@pytest.mark.parametrize("k", [1, 7, 8, 9])
+def test_gate_many_ties(ft, E, k, dtype):
+    """Logits of a few values, masked ones among them: the choice and its order are exact."""
+    if k > E:
+        return
+    T = 211
+    g = R.gen(E * 16 + k)
+    logits = torch.randint(-3, 4, (T, E), generator=g, device="cuda").to(dtype) / 2
+    logits = torch.where(torch.rand(T, E, generator=g, device="cuda") < 0.1, -math.inf, logits)
+    logits[3, 1:] = -math.inf
+    for score in ("softmax", "sigmoid"):
+        ids, w = ft.moe_gate(logits, k, score=score)
+        want, ww, _ = R.gate(logits, k, score, None, 1, 1, 1, True, 1.0)
+        assert torch.equal(ids.long(), want)
+        inside(w, ww, 64 * R.U32 * ww + 1e-30, "weights")
+
+
+@pytest.mark.parametrize("off", [8, 16, 24])
+def test_quantize_unaligned(ft, off):
+    """Codes at any 8 bytes, scales at any 4, rows at any 16."""
+    x = R.rows(R.gen(off), 9, 272, torch.bfloat16)
+    q, s = ft.quantize_fp8(x)
+    xs = torch.empty(9 * 272 + 8, dtype=torch.bfloat16, device="cuda")[8:].view(9, 272).copy_(x)
+    qo = torch.empty(9 * 272 + off, dtype=torch.uint8, device="cuda")[off:].view(torch.float8_e4m3fn).view(9, 272)
+    so = torch.empty(9 * 3 + 1, device="cuda")[1:].view(9, 3)
+    ft.quantize_fp8(xs, qo, so)
+    assert torch.equal(qo.view(torch.uint8), q.view(torch.uint8)) and torch.equal(so, s)
+
+
+def routed(ft, E, k, N, K, T, dt, none=0.0, pop=None, per_slot=False):
+    g = R.gen(E + 3 * N + 5 * K + 7 * T)
+    w, ws = R.weights(g, E, N, K)
+    q, s = R.codes(g, T * k if per_slot else T, K)
+    ids = R.ids(g, T, E, k, none, pop)
+    out = (ft.moe_fp8_fp8_slots if per_slot else ft.moe_fp8_fp8)(w, ws, q, s, ids, out_dtype=dt)
+    want, bound = R.product(w, ws, q, s, ids, per_slot, dt)
+    inside(out, want, bound)
+    assert (out[ids < 0] == 0).all()
+
+
+@pytest.mark.parametrize("per_slot", [False, True])
+@pytest.mark.parametrize("T", [5, 6, 120, 121, 520, 521])
+def test_product_around_the_tile_widths(ft, T, per_slot):
+    """40 experts, 4 slots a token: 0.5, 12 and 52 slots per expert, and one token more."""
+    routed(ft, 40, 4, 144, 272, T, torch.float32, 0.0, per_slot=per_slot)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("c", [
+    # E, k, N, K, T, unrouted, popularity of the last expert over the first
+    (128, 8, 130, 144, 150, 0.1, 0.0),      # over 1024 slots, tiles of 16
+    (128, 8, 65, 400, 129, 0.0, 9.0),       # the same, most slots on some experts
+    (60, 4, 130, 2000, 509, 0.02, 4.0),     # tiles of 32, short last block
+    (100, 5, 32, 16, 205, 0.3, 2.0), (1024, 8, 48, 128, 100, 0.1, 1.0), (1023, 3, 33, 144, 900, 0.0, 3.0),
+    (1100, 2, 40, 144, 12, 0.0, 0.0),       # more experts than the fast order takes: slots by themselves,
+    (1100, 8, 40, 144, 700, 0.1, 2.0),      # tiles of 16
+    (1100, 8, 40, 48, 8300, 0.05, 1.0),     # and of 256
+    (5, 4, 32, 16, 66000, 0.1, 1.0),        # more slots than it takes
+    (3, 3, 33, 32, 20000, 0.0, 0.0),
+])
+def test_product_orders(ft, c, dt):
+    E, k, N, K, T, none, pop = c
+    routed(ft, E, k, N, K, T, dt, none, torch.linspace(0, pop, E, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [3, 60, 700, 2500])
+def test_bad_ids_in_every_tile_width(ft, T):
+    """Ids that are no expert raise the flag and give zero rows; -1 gives zero rows only."""
+    E, k, N, K = 24, 4, 72, 144
+    g = R.gen(T)
+    w, ws = R.weights(g, E, N, K)
+    q, s = R.codes(g, T, K)
+    ids = R.ids(g, T, E, k, 0.1)
+    ft.moe_fp8_fp8(w, ws, q, s, ids)
+    assert ft.read_device_error() == 0
+    ids[0, 1], ids[T // 2, 0], ids[T - 1, 3] = E, -2 ** 31, 2 ** 31 - 1
+    out = ft.moe_fp8_fp8(w, ws, q, s, ids)
+    assert ft.read_device_error() == ft.FT_DEVERR_BAD_EXPERT_ID
+    want, bound = R.product(w, ws, q, s, ids, False, torch.float32)
+    inside(out, want, bound)
+    assert (out[(ids < 0) | (ids >= E)] == 0).all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 12, 13, 52, 53, 128, 257])
+def test_dense_unaligned(ft, M):
+    """Scales and outputs that start at any element, around the tile widths."""
+    N, K = 130, 400
+    g = R.gen(M)
+    w, ws = R.weights(g, 1, N, K)
+    q, s = R.codes(g, M, K)
+    ws1 = torch.empty(ws.numel() + 1, device="cuda")[1:].view(ws.shape[1:]).copy_(ws[0])
+    s1 = torch.empty(s.numel() + 3, device="cuda")[3:].view(s.shape).copy_(s)
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.empty(M * N + 1, dtype=dt, device="cuda")[1:].view(M, N)
+        ft.matmul_fp8_fp8(w[0], ws1, q, s1, out=out)
+        want, bound = R.product(w, ws, q, s, torch.zeros(M, 1, dtype=torch.int32, device="cuda"), False, dt)
+        inside(out, want[:, 0], bound[:, 0])
+
+
+MORE_LAYERS = [
+    # few tokens: all in three launches; 9 slots a token for 8 warps; short last blocks; masked experts
+    dict(T=2, E=64, k=9, H=272, I=144, dt=torch.bfloat16), dict(T=8, E=128, k=8, H=272, I=400, dt=torch.float16, kind=1),
+    dict(T=3, E=40, k=4, H=1040, I=16, dt=torch.bfloat16, score="sigmoid", mask=0.9, renorm=False),
+    dict(T=1, E=1, k=1, H=16, I=16, dt=torch.bfloat16), dict(T=700, E=2048, k=1, H=48, I=32, dt=torch.bfloat16),
+    # the same with larger matrices: separate launches
+    dict(T=2, E=8, k=2, H=4096, I=2048, dt=torch.bfloat16),
+    # tiles of 16 and 32, over and under 1024 slots
+    dict(T=150, E=128, k=8, H=272, I=144, dt=torch.bfloat16, mask=0.3), dict(T=100, E=20, k=4, H=400, I=272, dt=torch.float16, kind=1),
+    # tiles of 256: the activation with the first product, and after it
+    dict(T=300, E=6, k=3, H=272, I=384, dt=torch.bfloat16, kind=1, mask=0.3),
+    dict(T=300, E=6, k=3, H=272, I=208, dt=torch.float16, kind=1, mask=0.3),
+    dict(T=8300, E=1100, k=8, H=48, I=128, dt=torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("c", MORE_LAYERS)
+def test_layer_variants(ft, c):
+    test_layer(ft, c)
+
+
+@pytest.mark.parametrize("c", [dict(T=1, E=128, k=8, H=512, I=256, dt=torch.bfloat16),
+                               dict(T=600, E=8, k=2, H=640, I=384, dt=torch.bfloat16),
+                               dict(T=150, E=128, k=8, H=272, I=144, dt=torch.bfloat16)])
+def test_layer_streams_and_graph_of_every_width(ft, c):
+    """The same bits from two streams at once, behind other work, and from a captured call."""
+    x, logits, w13, s13, w2, s2, opt = layer_inputs(c)
+    k = c["k"]
+    x2 = (x.float() * 0.5).to(x.dtype)
+    lg2 = logits.flip(1).contiguous()
+    want = [ft.moe_layer_fp8(a, l, w13, s13, w2, s2, k, **opt)[0].clone() for a, l in ((x, logits), (x2, lg2))]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(20):
+        for i, (a, l) in enumerate(((x, logits), (x2, lg2))):
+            with torch.cuda.stream(streams[i]):
+                y = ft.moe_layer_fp8(a * 1, l + 0, w13, s13, w2, s2, k, **opt)[0]
+                got.append((y * 1, want[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+    sx, sl = x.clone(), logits.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ft.moe_layer_fp8(sx, sl, w13, s13, w2, s2, k, **opt)[0] * 1
+    for i, (a, l) in enumerate(((x2, lg2), (x, logits))):
+        sx.copy_(a)
+        sl.copy_(l)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[1 - i])
+
+
+def test_layer_of_no_tokens(ft):
+    c = dict(T=0, E=4, k=2, H=256, I=128, dt=torch.bfloat16)
+    x, logits, w13, s13, w2, s2, opt = layer_inputs(c)
+    y, ids, w = ft.moe_layer_fp8(x, logits, w13, s13, w2, s2, 2, **opt)
+    assert y.shape == (0, 256) and ids.shape == (0, 2) and w.shape == (0, 2)
