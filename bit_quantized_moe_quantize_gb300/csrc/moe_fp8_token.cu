@@ -35,13 +35,13 @@ __device__ __forceinline__ void quantize_row(const T* x, int32_t n, uint8_t* cod
     const int32_t nb = (n + kFp8Block - 1) / kFp8Block;
     constexpr int AHEAD = 4;      // block pairs whose values are on their way at once
     for (int32_t b0 = 2 * static_cast<int32_t>(warp); b0 < nb; b0 += 2 * AHEAD * static_cast<int32_t>(warps)) {
-        float v[AHEAD][8] = {};
+        float v[AHEAD][1][8] = {};
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int32_t c = (b0 + 2 * i * static_cast<int32_t>(warps) + static_cast<int32_t>(lane_id() >> 4)) * kFp8Block + 8 * static_cast<int32_t>(sub);
             if (c < n) {
-                if constexpr (sizeof(T) == 4) load_vec_plain<8>(x + c, v[i]);
-                else load_vec<T, 8>(x + c, v[i]);
+                if constexpr (sizeof(T) == 4) load_vec_plain<8>(x + c, v[i][0]);
+                else load_vec<T, 8>(x + c, v[i][0]);
             }
         }
 #pragma unroll
@@ -50,7 +50,7 @@ __device__ __forceinline__ void quantize_row(const T* x, int32_t n, uint8_t* cod
             const int32_t c = b * kFp8Block + 8 * static_cast<int32_t>(sub);
             if (b0 + 2 * i * static_cast<int32_t>(warps) < nb) {      // the whole warp
                 const float scale = fp8_block_scale(v[i]);
-                if (c < n) *reinterpret_cast<uint2*>(codes + c) = fp8_codes(v[i], scale);
+                if (c < n) *reinterpret_cast<uint2*>(codes + c) = fp8_codes(v[i][0], scale, rcp_approx(scale));
                 if (sub == 0 && b < nb) scales[b] = scale;
             }
         }
