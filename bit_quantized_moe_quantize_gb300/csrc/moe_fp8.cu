@@ -574,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                     // single elements, four rows' at a time: one after the other waits for shared memory
                     // at each (8191 tokens, 1407 x 2816 of 128 experts: 459 us instead of 375)
                     constexpr int ROWS = 4;
-                    for (int r0 = 0; r0 < rows_here; r0 += ROWS) {
+                    for (int q = 0; q < rows_here; q += ROWS) {
                         TO x[ROWS][PASS / 32];
                         int32_t slot[ROWS];
 #pragma unroll
