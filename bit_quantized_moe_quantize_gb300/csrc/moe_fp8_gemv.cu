@@ -5,7 +5,8 @@
 // row per lane in one 16-byte load, so that a lane's 16 lie within one scale block: their
 // dot product times 16 sa sw (fp8_dot.cuh) goes to the row's sum.
 //
-// Bound by latency and by reading the matrices once.
+// Bound by latency and by reading the matrices once: 8 slots, 768 x 2048 of 128 experts: 3.8 us
+// in a graph, 8.1 with cold caches (12.6 MB: 1.9 us at the copy's rate).
 #include "fp8_dot.cuh"
 #include "ft_internal.h"
 

@@ -12,6 +12,11 @@
 // of 16), so that the drain waits once per unit and the MMAs of four units run ahead of it.  Two CTAs
 // share an SM, so that one streams while the other starts or ends.
 //
+// Measured, 1536 x 2048 of 128 experts with cold caches: 64 tokens of 8 slots 85 us, 512 tokens 99 us
+// (403 MB: 59 us at the copy's rate).  Where experts have more than 32 slots, what is left over
+// the matrices' one reading is their next ones, from L2: 509 uneven tokens, 4 slots each, 1414 x 2000
+// of 60 experts: 56 us with the order, 48 without, for 170 MB (25 us).
+//
 // Up to 1024 slots are put in order by every CTA for itself, in shared memory (some 2 us
 // less than a launch and the reads of its results); more come ordered.
 //

@@ -12,9 +12,12 @@
 // Reading the experts' matrices once is what is left to wait for, beside the launches: the
 // same pieces as separate launches (quantizer, product, quantizer, product, weighted sum)
 // take six.  Every value is rounded as those do, except that the second product's rows are
-// added up in fp32 as they come.  Each launch may start before the one before it has ended
-// (programmatic dependent launch): what it reads of that one's results comes after
-// griddepcontrol.wait, and nothing is written before it.
+// added up in fp32 as they come.  One token, 8 of 128 experts, 2048 and 768 wide: 16 us with the
+// router in a graph (38 MB: 5.6 us at the copy's rate).
+//
+// Each launch may start before the one before it has ended (programmatic dependent launch):
+// what it reads of that one's results comes after griddepcontrol.wait, and nothing is
+// written before it.
 #include "fp8_dot.cuh"
 #include "fp8_quant.cuh"
 #include "ft_internal.h"
