@@ -63,6 +63,9 @@ __device__ __forceinline__ bool mbar_wait2_warp(uint64_t* bar0, uint32_t parity0
     return mbar_wait_warp(bar0, parity0, err) && mbar_wait_warp(bar1, parity1, err);
 }
 
+// Limit of the waits that a role makes for its own copies before it ends, once a wait has run out.
+constexpr uint64_t kLastWaitNs = 100'000'000;
+
 // 16 consecutive fp32 columns of the warp's 32 lanes (thread i: lane taddr.lane + i).
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"

@@ -318,6 +318,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 __syncwarp();
             }
         }
+        // the last fills: read by their MMAs, or at least arrived, before the CTA's memory goes
+        for (uint32_t f = it - min(it, static_cast<uint32_t>(C::STAGES)); f != it; ++f) {
+            const uint32_t s = f % C::STAGES, parity = (f / C::STAGES) & 1u;
+            if (mbar_wait_warp(&empty[s], parity, a.err, ok ? kWaitLimitNs : kLastWaitNs)) continue;
+            ok = false;
+            if (rank == 0) mbar_wait_warp(&full[s], parity, a.err, kLastWaitNs);
+        }
     } else if (warp < C::WARP_ZERO) {
         // ----------------------------------------------------------------- MMA
         // Warp h issues the MMAs of half h.  The whole warp runs the loop and one elected
@@ -601,6 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             }
             if (more) look();
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();

@@ -176,12 +176,12 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
     if (warp == C::WARP_PRODUCER) {
         // ------------------------------------------------------------ producer
         int32_t s = 0;
-        uint32_t phase = 1;
+        uint32_t phase = 1, it = 0;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
             const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
             const int32_t wy = static_cast<int32_t>(static_cast<int64_t>(t.e) * a.nrows + t.r0);
-            for (int32_t b = 0; b < nb; ++b) {
+            for (int32_t b = 0; b < nb; ++b, ++it) {
                 if (!mbar_wait_warp(&empty[s], phase, a.err)) { ok = false; break; }
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&full[s], stage_bytes - b_bytes);
@@ -193,6 +193,14 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
                     phase ^= 1u;
                 }
             }
+        }
+        // the last fills: read by their MMAs, or at least arrived, before the CTA's memory goes
+        const uint32_t n_stages = static_cast<uint32_t>(stages);
+        for (uint32_t f = it - min(it, n_stages); f != it; ++f) {
+            const uint32_t last = f % n_stages, parity = (f / n_stages) & 1u;
+            if (mbar_wait_warp(&empty[last], parity, a.err, ok ? kWaitLimitNs : kLastWaitNs)) continue;
+            ok = false;
+            mbar_wait_warp(&full[last], parity, a.err, kLastWaitNs);
         }
     } else if (warp == C::WARP_MMA) {
         // ----------------------------------------------------------------- MMA
