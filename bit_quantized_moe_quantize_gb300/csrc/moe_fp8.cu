@@ -43,6 +43,7 @@
 #include <atomic>
 
 #include "fp8_order.cuh"
+#include "fp8_quant.cuh"
 #include "fp8_tc.cuh"
 #include "ft_internal.h"
 #include "gemm_common.cuh"
@@ -224,13 +225,6 @@ __device__ __forceinline__ void copy_scales(const PairArgs& a, const float* sa, 
         }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-// g -> act(g) * up (see act_mul in the quantizer): the fast exponential and quotient are
-// within a few units in the last place, 2^-20 of what a code's rounding (2^-4) moves.
-__device__ __forceinline__ float act_mul_fast(float g, float up, int32_t kind) {
-    const float z = kind == FT_ACT_SILU ? g : 1.5957691216057308f * fmaf(0.044715f * g, g * g, g);
-    return __fdividef(g, 1.0f + __expf(-z)) * up;
 }
 
 // GATED: TO is unused.
@@ -513,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < C::CW / 4; ++i) {
                     const float2 g = unpack2(acc[i]), u = unpack2(acc[C::CW / 4 + i]);
-                    const float x = act_mul_fast(g.x, u.x, a.act_kind), y = act_mul_fast(g.y, u.y, a.act_kind);
+                    const float x = act_mul_f32(g.x, u.x, a.act_kind), y = act_mul_f32(g.y, u.y, a.act_kind);
                     amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
                     acc[i] = pack2(x, y);
                 }
@@ -524,7 +518,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 if (!mbar_wait_warp(&amax_bar[warp & 3u], tiles_done & 1u, a.err)) { ok = false; break; }
                 amax = fmaxf(amax, both[(h ^ 1u) * C::BM + m]);      // written again two tiles on, when the other warp has read it
                 ++tiles_done;
-                // a reciprocal instead of a quotient moves a code only where it lies within 2^-23 of a tie;
+                // a reciprocal instead of a quotient moves a code only where it lies within 2^-23 of a tie
+                // (fp8_codes would sort those out, for values that are themselves off by 2^-20);
                 // below 1e-30 it could overflow, and the block's values count as 0
                 const float scale = amax < 1e-30f ? 0.0f : __fdiv_rn(amax, kFp8Max);
                 const float inv = amax < 1e-30f ? 0.0f : __fdiv_rn(kFp8Max, amax);
