@@ -178,15 +178,14 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
     return launch_fp8_product(p, width, out, out_dtype, err, s);
 }
 
-// Workspace of a layer: router order; x's codes and scales, in router order for wide
-// tiles (`spread`), else by token; the gated values' codes and
-// scales in router order; where the first product does not quantize them itself
-// (n_inter % 128 != 0, or few slots per expert) its fp32 rows, codes by slot and (`spread`) copies
-// of them in router order; the second product's bf16 rows (half the bytes of fp32; their
-// rounding, at most 2^-8, is far below that of the codes, 2^-4, which both products start from).
+// Workspace of a layer: router order; x's codes and scales and the gated values', in router
+// order for wide tiles (`spread`), else by token and by slot; where the first product does not
+// quantize the gated values itself (n_inter % 128 != 0, or few slots per expert) its fp32 rows;
+// the second product's bf16 rows (half the bytes of fp32; their rounding, at most 2^-8, is far
+// below that of the codes, 2^-4, which both products start from).
 struct LayerWs {
     Fp8Order order;
-    size_t xq, xs, mq, ms, h, oq, os, rows, total;
+    size_t xq, xs, mq, ms, h, rows, total;
     int width;
     bool spread, gated;
 };
@@ -203,9 +202,6 @@ LayerWs layer_ws(uint8_t* base, int64_t tokens, int64_t n_slots, int32_t n_exper
     L.mq = take_bytes(&at, S * n_inter);
     L.ms = take_bytes(&at, S * fp8_scale_pitch(n_inter) * 4);
     L.h = take_bytes(&at, L.gated ? 0 : S * 2 * n_inter * 4);
-    const size_t ordered = L.spread && !L.gated ? S : 0;
-    L.oq = take_bytes(&at, ordered * n_inter);
-    L.os = take_bytes(&at, ordered * fp8_scale_pitch(n_inter) * 4);
     L.rows = take_bytes(&at, S * hidden * 2);
     L.total = at;
     return L;
@@ -375,7 +371,8 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
     // first product: gate and up rows
     if (L.spread) {
         p.scale_pitch = fp8_scale_pitch(hidden);
-        if (int st = launch_quantize_fp8_spread(x, x_dtype, ws + L.xq, xs, tokens, hidden, L.order.pos, top_k, p.scale_pitch, s))
+        if (int st = launch_quantize_fp8_spread(x, x_dtype, ws + L.xq, xs, tokens, hidden, false, act_kind, L.order.pos, top_k,
+                                                p.scale_pitch, s))
             return st;
     } else {
         p.scale_pitch = static_cast<int32_t>(fp8_blocks(hidden));
@@ -401,9 +398,11 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
         p.scale_pitch = fp8_scale_pitch(n_inter);
     } else {
         if (int st = launch_fp8_product(p, L.width, ws + L.h, FT_DTYPE_F32, err, s)) return st;
-        if (int st = launch_quantize_fp8(ws + L.h, FT_DTYPE_F32, ws + L.mq, ms, n_slots, n_inter, true, act_kind, s)) return st;
-        p.ordered = false;
-        p.scale_pitch = static_cast<int32_t>(fp8_blocks(n_inter));
+        p.scale_pitch = L.spread ? fp8_scale_pitch(n_inter) : static_cast<int32_t>(fp8_blocks(n_inter));
+        const int st = L.spread ? launch_quantize_fp8_spread(ws + L.h, FT_DTYPE_F32, ws + L.mq, ms, n_slots, n_inter, true, act_kind,
+                                                             L.order.pos, 1, p.scale_pitch, s)
+                                : launch_quantize_fp8(ws + L.h, FT_DTYPE_F32, ws + L.mq, ms, n_slots, n_inter, true, act_kind, s);
+        if (st) return st;
     }
     // second product
     p.weights = static_cast<const uint8_t*>(w2);
@@ -414,8 +413,6 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
     p.act_rows = n_slots;
     p.nrows = hidden;
     p.ncols = n_inter;
-    if (L.spread && !L.gated)
-        if (int st = launch_fp8_order_rows(&p, ws + L.oq, reinterpret_cast<float*>(ws + L.os), s)) return st;
     if (int st = launch_fp8_product(p, L.width, ws + L.rows, FT_DTYPE_BF16, err, s)) return st;
     return launch_combine(ws + L.rows, FT_DTYPE_BF16, topk_weights, nullptr, y, x_dtype, tokens, top_k, hidden, s);
 }

@@ -165,9 +165,9 @@ int launch_combine(const void* rows, int rows_dtype, const float* weights, const
                    int64_t tokens, int32_t top_k, int64_t ncols, cudaStream_t s);
 
 // The same into router order: row r of x goes to rows pos[r * k .. r * k + k - 1] (-1:
-// none) of codes and scales (rows of scales `pitch` apart).  x fp16 or bf16.
-int launch_quantize_fp8_spread(const void* x, int dtype, uint8_t* codes, float* scales, int64_t tokens, int64_t ncols,
-                               const int32_t* pos, int32_t k, int32_t pitch, cudaStream_t s);
+// none) of codes and scales (rows of scales `pitch` apart).  x fp16 or bf16, or gated fp32.
+int launch_quantize_fp8_spread(const void* x, int dtype, uint8_t* codes, float* scales, int64_t rows, int64_t ncols,
+                               bool gated, int kind, const int32_t* pos, int32_t k, int32_t pitch, cudaStream_t s);
 
 // Router order (fp8_route.cu); fp8_route_ok: sizes that it takes.  pos may be null.
 bool fp8_route_ok(int64_t n_slots, int32_t n_experts);

@@ -47,8 +47,8 @@ struct Divider {
 };
 
 // ACT: kNoAct, or FT_ACT_*: x holds rows of 2 ncols values, gate then up (a template: both
-// activations and a choice took a fifth of the instructions).  SPREAD: row r is a token's, and
-// its codes and scales go to the rows pos[r * k ..] (-1: none) of the outputs.
+// activations and a choice took a fifth of the instructions).  SPREAD: the codes and scales of
+// row r, a token's (or, k = 1, a slot's), go to the rows pos[r * k ..] (-1: none) of the outputs.
 template <typename T, int ACT, bool SPREAD>
 __global__ void __launch_bounds__(32 * kQuantWarps)
     quantize_fp8_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, float* __restrict__ scales,
@@ -131,10 +131,16 @@ int launch_quantize_fp8(const void* x, int dtype, uint8_t* codes, float* scales,
     return launch_act<__nv_bfloat16>(x, codes, scales, rows, ncols, gated, kind, s);
 }
 
-int launch_quantize_fp8_spread(const void* x, int dtype, uint8_t* codes, float* scales, int64_t tokens, int64_t ncols,
-                               const int32_t* pos, int32_t k, int32_t pitch, cudaStream_t s) {
-    if (dtype == FT_DTYPE_F16) return launch_typed<__half, kNoAct, true>(x, codes, scales, tokens, ncols, s, pos, k, pitch);
-    return launch_typed<__nv_bfloat16, kNoAct, true>(x, codes, scales, tokens, ncols, s, pos, k, pitch);
+int launch_quantize_fp8_spread(const void* x, int dtype, uint8_t* codes, float* scales, int64_t rows, int64_t ncols,
+                               bool gated, int kind, const int32_t* pos, int32_t k, int32_t pitch, cudaStream_t s) {
+    if (dtype == FT_DTYPE_F32) {      // the gated rows between the products; x itself is 16-bit
+        if (!gated) return fail(FT_ERR_ARG, "rows spread to router order are 16-bit, or gated fp32");
+        return kind == FT_ACT_SILU ? launch_typed<float, FT_ACT_SILU, true>(x, codes, scales, rows, ncols, s, pos, k, pitch)
+                                   : launch_typed<float, FT_ACT_GELU_TANH, true>(x, codes, scales, rows, ncols, s, pos, k, pitch);
+    }
+    if (gated) return fail(FT_ERR_ARG, "gated rows spread to router order are fp32");
+    if (dtype == FT_DTYPE_F16) return launch_typed<__half, kNoAct, true>(x, codes, scales, rows, ncols, s, pos, k, pitch);
+    return launch_typed<__nv_bfloat16, kNoAct, true>(x, codes, scales, rows, ncols, s, pos, k, pitch);
 }
 
 }  // namespace ft
