@@ -12,7 +12,7 @@
 //         where no expert is left
 //   w   = s[ids], renormalised by max(sum, 1e-30) if asked, times `scale`
 //
-// Up to 512 experts in one group: 2, 8, 16 or 32 lanes per token, 16 neighbouring experts
+// Up to 512 experts in one group, or in groups of 16, 32, 64, ..: 2, 8, 16 or 32 lanes per token, 16 neighbouring experts
 // each, in registers.  A key and the complement of its expert make one integer (32 bits where
 // 16-bit logits are the keys, else 64), whose maximum over the lanes is the choice with its
 // tie rule: a round is a few shuffles, and the lane that held the maximum looks again.
@@ -20,9 +20,9 @@
 // Up to eight choices come from sorting networks instead.  Bound by instructions: 65536 tokens of 128
 // bf16 logits, 8 choices: 16 us (21 MB: 3 us at the copy's rate); fp32 34 us, by rounds 48.
 //
-// Otherwise one warp per token (65535 tokens of 256 experts in 8 groups: 144 us).  The keys lie in shared memory; each lane keeps the best
-// key of its experts (every 32nd), and one round per chosen expert takes the
-// warp's best of those with two integer warp reductions (largest key, then the
+// Otherwise one warp per token (65535 tokens of 1024 experts: 191 us).  The keys lie in shared
+// memory; each lane keeps the best key of its experts (every 32nd), and one round
+// per chosen expert takes the warp's best of those with two integer warp reductions (largest key, then the
 // lowest index that has it) and lets the lane that held it look again.
 #include "fp8_common.cuh"
 #include "ft_internal.h"
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateAr
     const int64_t t = there ? t0 : a.tokens - 1;
     const int32_t E = a.n_experts, e0 = static_cast<int32_t>(sub) * kGatePer;
     const T* row = static_cast<const T*>(a.logits) + t * a.stride;
-    const bool by_logit = PACKED || a.bias == nullptr;
+    const bool by_logit = PACKED || (a.bias == nullptr && a.n_groups == 1);
     T raw[kGatePer];
     if (WIDE && e0 + kGatePer <= E) {
         constexpr int WORDS = kGatePer * static_cast<int>(sizeof(T)) / 16;
@@ -305,13 +305,44 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_few_kernel(const GateAr
         } else {
             float x = l;
             if (!by_logit) {
-                x = e0 + i < E ? gate_score(l, top, sum, a.score) + __ldg(a.bias + e0 + i) : -INFINITY;
+                if (e0 + i < E) x = gate_score(l, top, sum, a.score) + (a.bias ? __ldg(a.bias + e0 + i) : 0.0f);
+                else x = -INFINITY;
                 ok = ok && x > -INFINITY;
             }
             key[i] = (static_cast<uint64_t>(float_order(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e0 + i));
         }
         if (!ok) key[i] = 0;
         best = key[i] > best ? key[i] : best;
+    }
+    if constexpr (!PACKED) {
+        if (a.n_groups > 1) {      // a group's experts are those of 1, 2, 4, .. whole lanes
+            const int32_t per = E / a.n_groups / kGatePer, mine = static_cast<int32_t>(sub) / per;
+            uint32_t k1 = 0u, k2 = 0u;      // the group's two largest keys
+#pragma unroll
+            for (int i = 0; i < kGatePer; ++i) {
+                const uint32_t k = static_cast<uint32_t>(key[i] >> 32);
+                k2 = max(k2, min(k, k1));
+                k1 = max(k1, k);
+            }
+            for (int o = 1; o < per; o <<= 1) {
+                const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, k1, o), o2 = __shfl_xor_sync(0xFFFFFFFFu, k2, o);
+                k2 = max(max(k2, o2), min(k1, o1));
+                k1 = max(k1, o1);
+            }
+            float v = order32_value(k1);
+            if (a.group_top == 2 && k2) v += order32_value(k2);
+            const uint32_t score = k1 ? float_order(v) : 0u;
+            int32_t better = 0;
+            for (int32_t g = 0; g < a.n_groups; ++g) {
+                const uint32_t other = __shfl_sync(0xFFFFFFFFu, score, g * per, LANES);
+                better += other > score || (other == score && g < mine) ? 1 : 0;
+            }
+            if (better >= a.topk_groups) {
+                best = 0;
+#pragma unroll
+                for (int i = 0; i < kGatePer; ++i) key[i] = 0;
+            }
+        }
     }
     int32_t* ids = a.ids + t * a.top_k;
     float* weights = a.weights + t * a.top_k;
@@ -419,7 +450,7 @@ static int launch_few(const GateArgs& a, cudaStream_t s) {
 template <typename T>
 static int launch_few_typed(const GateArgs& a, cudaStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (a.bias == nullptr) {
+        if (a.bias == nullptr && a.n_groups == 1) {
             if (a.n_experts <= 2 * kGatePer) return launch_few<T, 2, uint32_t>(a, s);
             if (a.n_experts <= 8 * kGatePer) return launch_few<T, 8, uint32_t>(a, s);
             if (a.n_experts <= 16 * kGatePer) return launch_few<T, 16, uint32_t>(a, s);
@@ -450,7 +481,11 @@ int launch_gate(const GateParams& p, const void* logits, int dtype, int64_t stri
     a.group_top = p.group_top;
     a.renormalize = p.renormalize;
     a.scale = p.scale;
-    if (p.n_groups == 1 && p.n_experts <= 32 * kGatePer)
+    // groups of experts that are 1, 2, 4, .. whole lanes stay in registers too (65535 tokens of 256
+    // in 8 groups: 103 us, by shared memory 144)
+    const int32_t lanes = p.n_experts / p.n_groups / kGatePer;
+    const bool whole = p.n_groups == 1 || (lanes > 0 && p.n_experts == lanes * kGatePer * p.n_groups && (lanes & (lanes - 1)) == 0);
+    if (whole && p.n_experts <= 32 * kGatePer)
         return dtype == FT_DTYPE_F32   ? launch_few_typed<float>(a, s)
                : dtype == FT_DTYPE_F16 ? launch_few_typed<__half>(a, s)
                                        : launch_few_typed<__nv_bfloat16>(a, s);

@@ -614,3 +614,25 @@ def test_layer_of_no_tokens(ft):
     x, logits, w13, s13, w2, s2, opt = layer_inputs(c)
     y, ids, w = ft.moe_layer_fp8(x, logits, w13, s13, w2, s2, 2, **opt)
     assert y.shape == (0, 256) and ids.shape == (0, 2) and w.shape == (0, 2)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("c", [(64, 4, 2, 1, 8), (64, 2, 1, 2, 9), (128, 8, 3, 2, 8), (256, 8, 4, 2, 8), (256, 16, 5, 1, 6), (256, 2, 2, 2, 12),
+                               (512, 4, 2, 2, 8), (512, 32, 7, 2, 8), (32, 2, 1, 1, 4), (160, 2, 1, 2, 6), (384, 8, 3, 2, 8), (1024, 16, 4, 2, 8)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_gate_groups(ft, c, dtype, bias):
+    """Groups of whole lanes and others; masked experts, groups and rows; ties between groups by the lowest."""
+    E, G, TG, GT, k = c
+    T = 97
+    g = R.gen(E + 31 * G + k)
+    logits = torch.randint(-4, 5, (T, E), generator=g, device="cuda").to(dtype) / 2
+    logits = torch.where(torch.rand(T, E, generator=g, device="cuda") < 0.2, -math.inf, logits)
+    logits.view(T, G, -1)[torch.rand(T, G, generator=g, device="cuda") < 0.3] = -math.inf
+    logits[5] = -math.inf
+    b = torch.randint(0, 3, (E,), generator=g, device="cuda").float() / 4 if bias else None
+    ids, w = ft.moe_gate(logits, k, score="sigmoid", bias=b, n_groups=G, topk_groups=TG, group_top=GT, scale=2.5)
+    want, ww, sure = R.gate(logits, k, "sigmoid", b, G, TG, GT, True, 2.5)
+    assert sure.float().mean() > 0.5
+    assert torch.equal(ids[sure].long(), want[sure])
+    inside(w[sure], ww[sure], 64 * R.U32 * ww[sure].abs() + 1e-30, "weights")
+    assert (ids[5] == -1).all()
