@@ -13,8 +13,8 @@
 //   w   = s[ids], renormalised by max(sum, 1e-30) if asked, times `scale`
 //
 // Up to 512 experts in one group, or in groups of 16, 32, 64, ..: 2, 8, 16 or 32 lanes per token,
-// 16 neighbouring experts each, in registers.  A key and the complement of its expert make one integer (32 bits where
-// 16-bit logits are the keys, else 64), whose maximum over the lanes is the choice with its
+// 16 neighbouring experts each, in registers.  A key and the complement of its expert make one
+// integer (32 bits where 16-bit logits are the keys, else 64), whose maximum over the lanes is the choice with its
 // tie rule: a round is a few shuffles, and the lane that held the maximum looks again.
 //
 // Up to eight choices come from sorting networks instead.  Bound by instructions: 65536 tokens of 128
