@@ -2,20 +2,20 @@
 // reading the experts' matrices once.
 //
 // One tile: up to 128 weight rows of an expert x up to NW of its slots (16 or 32), one CTA,
-// tcgen05 MMAs with M = 128 weight rows and N = the tile's slots rounded up to 16.  Here the weight rows lie along the tensor-memory lanes: with few slots the
-// scales of a block are few, and a warp reads them from shared memory at a broadcast for
-// its 32 rows.  Where a batch has too few tiles of 128 rows to fill the GPU, a tile takes
-// 64 or 32 weight rows; the MMA still runs over 128 lanes, whose other rows are whatever
-// lies behind in shared memory and are not read.
+// tcgen05 MMAs with M = 128 weight rows and N = the tile's slots rounded up to 16.  Here the
+// weight rows lie along the tensor-memory lanes: with few slots the scales of a block are few,
+// and a warp reads them from shared memory at a broadcast for its 32 rows.  Where a batch has too
+// few tiles of 128 rows to fill the GPU, a tile takes 64 or 32 weight rows; the MMA still runs
+// over 128 lanes, whose other rows are whatever lies behind in shared memory and are not read.
 //
-// Blocks go through tensor memory in units of 64 columns (two blocks of 32 slots or four
-// of 16), so that the drain waits once per unit and the MMAs of four units run ahead of it.  Two CTAs
+// Blocks go through tensor memory in units of 64 columns (two blocks of 32 slots or four of 16),
+// so that the drain waits once per unit and the MMAs of four units run ahead of it.  Two CTAs
 // share an SM, so that one streams while the other starts or ends.
 //
-// Measured, 1536 x 2048 of 128 experts with cold caches: 64 tokens of 8 slots 85 us, 512 tokens 99 us
-// (403 MB: 59 us at the copy's rate).  Where experts have more than 32 slots, what is left over
-// the matrices' one reading is their next ones, from L2: 509 uneven tokens, 4 slots each, 1414 x 2000
-// of 60 experts: 56 us with the order, 48 without, for 170 MB (25 us).
+// Measured, 1536 x 2048 of 128 experts with cold caches: 64 tokens of 8 slots 85 us, 512 tokens
+// 99 us (403 MB: 59 us at the copy's rate).  Where experts have more than 32 slots, what is left
+// over the matrices' one reading is their next ones, from L2: 509 uneven tokens, 4 slots each,
+// 1414 x 2000 of 60 experts: 56 us with the order, 48 without, for 170 MB (25 us).
 //
 // Up to 1024 slots are put in order by every CTA for itself, in shared memory (some 2 us
 // less than a launch and the reads of its results); more come ordered.

@@ -14,15 +14,16 @@
 //
 // Up to 512 experts in one group, or in groups of 16, 32, 64, ..: 2, 8, 16 or 32 lanes per token,
 // 16 neighbouring experts each, in registers.  A key and the complement of its expert make one
-// integer (32 bits where 16-bit logits are the keys, else 64), whose maximum over the lanes is the choice with its
-// tie rule: a round is a few shuffles, and the lane that held the maximum looks again.
+// integer (32 bits where 16-bit logits are the keys, else 64), whose maximum over the lanes is
+// the choice with its tie rule: a round is a few shuffles, and the lane that held the maximum
+// looks again.
 //
-// Up to eight choices come from sorting networks instead.  Bound by instructions: 65536 tokens of 128
-// bf16 logits, 8 choices: 16 us (21 MB: 3 us at the copy's rate); fp32 34 us, by rounds 48.
+// Up to eight choices come from sorting networks instead.  Bound by instructions: 65536 tokens of
+// 128 bf16 logits, 8 choices: 16 us (21 MB: 3 us at the copy's rate); fp32 34 us, by rounds 48.
 //
 // Otherwise one warp per token (65535 tokens of 1024 experts: 191 us).  The keys lie in shared
-// memory; each lane keeps the best key of its experts (every 32nd), and one round
-// per chosen expert takes the warp's best of those with two integer warp reductions (largest key, then the
+// memory; each lane keeps the best key of its experts (every 32nd), and one round per chosen
+// expert takes the warp's best of those with two integer warp reductions (largest key, then the
 // lowest index that has it) and lets the lane that held it look again.
 #include "fp8_common.cuh"
 #include "ft_internal.h"
