@@ -1,4 +1,4 @@
-// The FP8 products for few slots per expert (up to 128 in a tile): what bounds them is
+// The FP8 products for few slots per expert: what bounds them is
 // reading the experts' matrices once.
 //
 // One tile: up to 128 weight rows of an expert x up to NW of its slots (16 or 32), one CTA,
@@ -15,7 +15,7 @@
 // Measured, 1536 x 2048 of 128 experts with cold caches: 64 tokens of 8 slots 85 us, 512 tokens
 // 99 us (403 MB: 59 us at the copy's rate).  Where experts have more than 32 slots, what is left
 // over the matrices' one reading is their next ones, from L2: 509 uneven tokens, 4 slots each,
-// 1414 x 2000 of 60 experts: 56 us with the order, 48 without, for 170 MB (25 us).
+// 1414 x 2000 of 60 experts: 56 us with the order, 45 without, for 170 MB (25 us).
 //
 // Up to 1024 slots are put in order by every CTA for itself, in shared memory (some 2 us
 // less than a launch and the reads of its results); more come ordered.
