@@ -13,23 +13,16 @@ __device__ __forceinline__ float rcp_approx(float x) {      // within one unit i
     return r;
 }
 
-// The gated activation of one value: act(g) * up with act(g) = g / (1 + exp(-z)), z = g for
-// SiLU and 2 sqrt(2/pi) (g + 0.044715 g^3) for the tanh form of GELU.  exp(-z) = 2^(-z log2 e)
-// is off by the rounding of its argument, 2^-24 |z| of itself, and two units in the last place:
-// some 2^-20 where act(g) has a size to speak of, beside the 2^-4 that a code rounds off
-// (expf's exact reduction of the argument takes four more instructions of some twenty).
-__device__ __forceinline__ float act_mul_f32(float g, float up, int kind) {
-    const float cube = __fmul_rn(__fmul_rn(__fmul_rn(0.044715f, g), g), g);
-    const float z = kind == FT_ACT_SILU ? g : __fmul_rn(1.5957691216057308f, __fadd_rn(g, cube));
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-    return g * rcp_approx(1.0f + e) * up;
-}
-
-// Two fp32 values in a 64-bit register, and their packed product.
+// Two fp32 values in a 64-bit register, and packed operations on them.
 __device__ __forceinline__ uint64_t pair2(float x, float y) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+__device__ __forceinline__ float2 split2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
     return r;
 }
 
@@ -39,10 +32,82 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mad2(uint64_t a, uint64_t b, uint64_t c) {      // a * b + c, rounded once
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t same2(float x) { return pair2(x, x); }
+
+__device__ __forceinline__ float ex2_approx(float x) {      // within 2^-22 of 2^x; 0 below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The largest of two or three values, NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The gated activation of 2 N values: act(g) * up with act(g) = g / (1 + exp(-z)), z = g for
+// SiLU and 2 sqrt(2/pi) (g + 0.044715 g^3) for the tanh form of GELU.
+//
+// exp(-z) = 2^-t exp(-c) with t the rounded z log2(e) and c = z - t ln 2 what that rounding left
+// out (ln 2 in two parts), at most 2^-17 while 2^-t is finite, so that 1 - c stands for exp(-c).
+// Without c the exponential is off by 2^-24 |z| of itself.  A quarter of 1 + exp(-z) keeps
+// its reciprocal a normal number as long as exp(-z) is finite.  In all some 10 * 2^-24 of
+// the value, wherever exp(-z) is finite in fp32; past that act(g) is 0.
+template <int N>
+__device__ __forceinline__ void act_mul_pairs(const uint64_t (&g)[N], const uint64_t (&up)[N], int kind, uint64_t (&out)[N]) {
+    uint64_t z[N];
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        z[i] = g[i];
+        if (kind != FT_ACT_SILU) {
+            const uint64_t cube = mul2(mul2(mul2(same2(0.044715f), g[i]), g[i]), g[i]);
+            z[i] = mul2(same2(1.5957691216057308f), add2(g[i], cube));
+        }
+        const float2 a = split2(z[i]);
+        far = max_nan(far, fabsf(a.x), fabsf(a.y));
+    }
+    if (!(far < 0x1p20f)) {      // (as far out nothing changes any more, but products overflow)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 a = split2(z[i]);
+            z[i] = pair2(fminf(fmaxf(a.x, -128.0f), 128.0f), fminf(fmaxf(a.y, -128.0f), 128.0f));
+        }
+    }
+    constexpr float kLn2Hi = 0.693147182f, kLn2Lo = -1.90465421e-9f;      // ln 2 = kLn2Hi + kLn2Lo
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint64_t t = mul2(z[i], same2(1.4426950408889634f));
+        const uint64_t c = mad2(t, same2(-kLn2Lo), mad2(t, same2(-kLn2Hi), z[i]));
+        const float2 ts = split2(t);
+        const uint64_t e = pair2(ex2_approx(-ts.x), ex2_approx(-ts.y));
+        const float2 d = split2(mad2(e, mad2(c, same2(-0.25f), same2(0.25f)), same2(0.25f)));
+        out[i] = mul2(mul2(mul2(g[i], same2(0.25f)), pair2(rcp_approx(d.x), rcp_approx(d.y))), up[i]);
+    }
+}
+
 __device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b) {
-    float2 x, y;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(a));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(b));
+    const float2 x = split2(a), y = split2(b);
     return e4m3x4(x.x, x.y, y.x, y.y);
 }
 
@@ -67,19 +132,6 @@ __device__ __forceinline__ uint2 fp8_codes(const float (&v)[8], float scale, flo
                                            __fdiv_rn(v[4 * h + 2], scale), __fdiv_rn(v[4 * h + 3], scale));
     }
     return make_uint2(lo[0], lo[1]);
-}
-
-// The largest of two or three values, NaN if one of them is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b, float c) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // Scale of a block of 128 values, eight in each of 16 neighbouring lanes or 16 in each of 8.

@@ -505,11 +505,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 // this thread's 64 of the slot's 128 values; the other half's thread has the rest
                 float amax = 0.0f;
 #pragma unroll
-                for (int i = 0; i < C::CW / 4; ++i) {
-                    const float2 g = unpack2(acc[i]), u = unpack2(acc[C::CW / 4 + i]);
-                    const float x = act_mul_f32(g.x, u.x, a.act_kind), y = act_mul_f32(g.y, u.y, a.act_kind);
-                    amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
-                    acc[i] = pack2(x, y);
+                for (int i = 0; i < C::CW / 4; i += 4) {
+                    uint64_t g[4], up[4], v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        g[j] = acc[i + j];
+                        up[j] = acc[C::CW / 4 + i + j];
+                    }
+                    act_mul_pairs<4>(g, up, a.act_kind, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 x = split2(v[j]);
+                        amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+                        acc[i + j] = v[j];
+                    }
                 }
                 float* both = amax_of + (tiles_done & 1u) * (2 * C::BM);
                 both[h * C::BM + m] = amax;

@@ -11,9 +11,9 @@
 // division.  A non-finite value makes its block's scale infinite or NaN, and what is
 // divided by it 0 or NaN.
 //
-// Bound by instructions as much as by memory (65528 rows x 1408 gated bf16: 79 us, 5.9 TB/s;
+// Bound by instructions as much as by memory (65528 rows x 1408 gated bf16: 84 us, 5.5 TB/s;
 // rows of 2816 bf16 alone 124 us, 4.5 TB/s; fp32 6.3 and 6.6 TB/s).  CTAs that stay and fetch
-// ahead were slower for all but the last but one (gated 85 us): small ones that come and go
+// ahead were slower for all but the last but one: small ones that come and go
 // hide the loads as well, with half the registers.
 #include "fp8_quant.cuh"
 #include "ft_internal.h"
@@ -74,10 +74,23 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
 #pragma unroll
     for (int n = 0; n < kQuantHalves; ++n) {
         if (in[n]) {
+            if constexpr (GATED) {
+                uint64_t g[4], up[4], a[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (GATED) v[n][j] = act_mul_f32(to_f32<T>(raw[n][0][j]), to_f32<T>(raw[n][1][j]), ACT);
-                else v[n][j] = to_f32<T>(raw[n][0][j]);
+                for (int j = 0; j < 4; ++j) {
+                    g[j] = pair2(to_f32<T>(raw[n][0][2 * j]), to_f32<T>(raw[n][0][2 * j + 1]));
+                    up[j] = pair2(to_f32<T>(raw[n][1][2 * j]), to_f32<T>(raw[n][1][2 * j + 1]));
+                }
+                act_mul_pairs<4>(g, up, ACT, a);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = split2(a[j]);
+                    v[n][2 * j] = x.x;
+                    v[n][2 * j + 1] = x.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[n][j] = to_f32<T>(raw[n][0][j]);
             }
         }
     }
