@@ -115,23 +115,29 @@ __device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b) {
 // 2^-22 |v / scale| of the IEEE quotient (2^-23 of the reciprocal, 2^-24 of the product and of
 // the quotient), so both round to the same code unless y (1 - 2^-21) and y (1 + 2^-21) do not;
 // only then, or where 1 / scale could overflow, are the quotients formed.
-__device__ __forceinline__ uint2 fp8_codes(const float (&v)[8], float scale, float inv) {
-    const uint64_t inv2 = pair2(inv, inv), down = pair2(1.0f - 0x1p-21f, 1.0f - 0x1p-21f), up = pair2(1.0f + 0x1p-21f, 1.0f + 0x1p-21f);
+__device__ __forceinline__ uint2 fp8_codes(const uint64_t (&v)[4], float scale, float inv) {
+    const uint64_t inv2 = same2(inv), down = same2(1.0f - 0x1p-21f), up = same2(1.0f + 0x1p-21f);
     uint32_t lo[2], hi[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const uint64_t a = mul2(pair2(v[4 * h], v[4 * h + 1]), inv2), b = mul2(pair2(v[4 * h + 2], v[4 * h + 3]), inv2);
+        const uint64_t a = mul2(v[2 * h], inv2), b = mul2(v[2 * h + 1], inv2);
         lo[h] = e4m3x4(mul2(a, down), mul2(b, down));
         hi[h] = e4m3x4(mul2(a, up), mul2(b, up));
     }
     if (lo[0] != hi[0] || lo[1] != hi[1] || !(scale > 1.0e-36f)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            const float2 x = split2(v[2 * h]), y = split2(v[2 * h + 1]);
             lo[h] = scale == 0.0f ? 0u
-                                  : e4m3x4(__fdiv_rn(v[4 * h], scale), __fdiv_rn(v[4 * h + 1], scale),
-                                           __fdiv_rn(v[4 * h + 2], scale), __fdiv_rn(v[4 * h + 3], scale));
+                                  : e4m3x4(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale), __fdiv_rn(y.x, scale), __fdiv_rn(y.y, scale));
+        }
     }
     return make_uint2(lo[0], lo[1]);
+}
+
+__device__ __forceinline__ uint2 fp8_codes(const float (&v)[8], float scale, float inv) {
+    const uint64_t p[4] = {pair2(v[0], v[1]), pair2(v[2], v[3]), pair2(v[4], v[5]), pair2(v[6], v[7])};
+    return fp8_codes(p, scale, inv);
 }
 
 // Scale of a block of 128 values, eight in each of 16 neighbouring lanes or 16 in each of 8.

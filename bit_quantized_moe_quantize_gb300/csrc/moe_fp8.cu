@@ -516,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 x = split2(v[j]);
-                        amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+                        amax = max_nan(amax, fabsf(x.x), fabsf(x.y));
                         acc[i + j] = v[j];
                     }
                 }
@@ -525,23 +525,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&amax_bar[warp & 3u]);
                 if (!mbar_wait_warp(&amax_bar[warp & 3u], tiles_done & 1u, a.err)) { ok = false; break; }
-                amax = fmaxf(amax, both[(h ^ 1u) * C::BM + m]);      // written again two tiles on, when the other warp has read it
+                amax = max_nan(amax, both[(h ^ 1u) * C::BM + m]);      // written again two tiles on, when the other warp has read it
                 ++tiles_done;
-                // a reciprocal instead of a quotient moves a code only where it lies within 2^-23 of a tie
-                // (fp8_codes would sort those out, for values that are themselves off by 2^-20);
-                // below 1e-30 it could overflow, and the block's values count as 0
-                const float scale = amax < 1e-30f ? 0.0f : __fdiv_rn(amax, kFp8Max);
-                const float inv = amax < 1e-30f ? 0.0f : __fdiv_rn(kFp8Max, amax);
+                const float scale = __fdiv_rn(amax, kFp8Max), inv = rcp_approx(scale);      // as the quantizer's
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t q[4];
+                    uint2 q[2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 x = unpack2(acc[8 * i + 2 * k]), y = unpack2(acc[8 * i + 2 * k + 1]);
-                        q[k] = e4m3x4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+                    for (int k = 0; k < 2; ++k) {
+                        const uint64_t x[4] = {acc[8 * i + 4 * k], acc[8 * i + 4 * k + 1], acc[8 * i + 4 * k + 2], acc[8 * i + 4 * k + 3]};
+                        q[k] = fp8_codes(x, scale, inv);
                     }
-                    *reinterpret_cast<uint4*>(stage + lane * 80 + 16 * i) = make_uint4(q[0], q[1], q[2], q[3]);
+                    *reinterpret_cast<uint4*>(stage + lane * 80 + 16 * i) = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
                 }
                 const int32_t p0 = rows[0], n = min(32, mine - static_cast<int32_t>(lane0));
                 if (h == 0 && m < mine) a.mid_scales[static_cast<int64_t>(p0 + static_cast<int32_t>(lane)) * a.mid_pitch + r0 / kFp8Block] = scale;
