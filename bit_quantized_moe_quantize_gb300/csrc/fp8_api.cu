@@ -178,14 +178,19 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
     return launch_fp8_product(p, width, out, out_dtype, err, s);
 }
 
-// Workspace of a layer: router order; x's codes and scales and the gated values', in router
-// order for wide tiles (`spread`), else by token and by slot; where the first product does not
-// quantize the gated values itself (n_inter % 128 != 0, or few slots per expert) its fp32 rows;
-// the second product's bf16 rows (half the bytes of fp32; their rounding, at most 2^-8, is far
-// below that of the codes, 2^-4, which both products start from).
+// Workspace of a layer: router order; the gated values' codes and scales; and one place for
+// what the second product does not read any more, x's codes and scales and (where the first product
+// does not quantize the gated values itself: n_inter % 128 != 0, or few slots per expert) that one's
+// fp32 rows, and for the rows that the second product writes.  Codes lie in router order for wide tiles
+// (`spread`), else by token and by slot.
+//
+// The second product's rows are fp32 where y is fp16 and bf16 where y is bf16: they have no
+// fewer bits than y, and for bf16 half the bytes (8192 tokens of 8 slots, 2048 wide: 535 us, with fp32
+// rows 614).  Their rounding, at most 2^-8 of a row, is far below that of the codes, 2^-4, which both
+// products start from.
 struct LayerWs {
     Fp8Order order;
-    size_t xq, xs, mq, ms, h, rows, total;
+    size_t mq, ms, xq, xs, h, rows, total;
     int width;
     bool spread, gated;
 };
@@ -197,13 +202,13 @@ LayerWs layer_ws(uint8_t* base, int64_t tokens, int64_t n_slots, int32_t n_exper
     L.gated = L.spread && n_inter % kFp8Block == 0;
     size_t at = al256(fp8_order_layout(base, n_slots, n_experts, L.spread, &L.order));
     const size_t S = static_cast<size_t>(n_slots), X = L.spread ? S : static_cast<size_t>(tokens);
-    L.xq = take_bytes(&at, X * hidden);
-    L.xs = take_bytes(&at, X * fp8_scale_pitch(hidden) * 4);
     L.mq = take_bytes(&at, S * n_inter);
     L.ms = take_bytes(&at, S * fp8_scale_pitch(n_inter) * 4);
+    L.rows = at;
+    L.xq = take_bytes(&at, X * hidden);
+    L.xs = take_bytes(&at, X * fp8_scale_pitch(hidden) * 4);
     L.h = take_bytes(&at, L.gated ? 0 : S * 2 * n_inter * 4);
-    L.rows = take_bytes(&at, S * hidden * 2);
-    L.total = at;
+    L.total = std::max(at, al256(L.rows + S * hidden * 4));
     return L;
 }
 
@@ -413,8 +418,9 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
     p.act_rows = n_slots;
     p.nrows = hidden;
     p.ncols = n_inter;
-    if (int st = launch_fp8_product(p, L.width, ws + L.rows, FT_DTYPE_BF16, err, s)) return st;
-    return launch_combine(ws + L.rows, FT_DTYPE_BF16, topk_weights, nullptr, y, x_dtype, tokens, top_k, hidden, s);
+    const int rows_dtype = x_dtype == FT_DTYPE_F16 ? FT_DTYPE_F32 : FT_DTYPE_BF16;
+    if (int st = launch_fp8_product(p, L.width, ws + L.rows, rows_dtype, err, s)) return st;
+    return launch_combine(ws + L.rows, rows_dtype, topk_weights, nullptr, y, x_dtype, tokens, top_k, hidden, s);
 }
 
 }  // extern "C"

@@ -685,9 +685,11 @@ FT_API int ft_moe_combine(const void* rows, int32_t rows_dtype, const float* top
  * ft_moe_layer_fp8 - a whole expert layer: ft_moe_gate on the logits,
  * ft_quantize_fp8 of x, the routed product with w13 (gate rows, then up rows),
  * act(gate) * up quantized, the routed product with w2 and ft_moe_combine.
- * The gated values are fp32 when they are quantized; the rows of the second
- * product are rounded to bf16 before they are weighted (a few tokens with small
- * matrices have them added up in fp32 instead).
+ * The gated values are fp32 when they are quantized.  The rows of the second
+ * product stay fp32 until they are weighted where x is fp16; where it is bf16
+ * they are rounded to bf16 first (not for a few tokens with small matrices).  Where
+ * rows of a token nearly cancel and their sum needs more, ft_moe_fp8_fp8_slots with
+ * fp32 rows and ft_moe_combine give it; the layer's results are theirs bit for bit.
  *   x       device, [tokens][hidden] of x_dtype (FT_DTYPE_F16 or FT_DTYPE_BF16),
  *           16-byte aligned; y the same shape and type, out
  *   w13     [n_experts][2 * n_inter][hidden] e4m3, s13 its scales

@@ -145,3 +145,10 @@ def test_layer_is_its_operators(ft, c, kind):
     few tokens with small matrices) in fp32."""
     few = c[0] * c[2] <= c[1] / 2
     assert apart_from_operators(ft, c, torch.bfloat16, kind, torch.float32 if few else torch.bfloat16) == 0
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("c", BATCHES)
+def test_fp16_layer_is_its_operators(ft, c, kind):
+    """The same of fp16 layers, whose rows stay fp32: bf16 ones would have fewer bits than y."""
+    assert apart_from_operators(ft, c, torch.float16, kind, torch.float32) == 0
