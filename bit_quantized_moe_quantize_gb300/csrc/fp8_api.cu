@@ -212,6 +212,21 @@ LayerWs layer_ws(uint8_t* base, int64_t tokens, int64_t n_slots, int32_t n_exper
     return L;
 }
 
+// The most that `total` (tokens, slots) gives for up to `tokens` tokens.  It rises with them but where the
+// products' tiles or the order of the slots change, so what counts is the last token of each of those forms.
+template <typename F>
+size_t most_bytes(int64_t tokens, int32_t top_k, int32_t n_experts, const F& total) {
+    size_t most = total(tokens, tokens * top_k);
+    auto last = [&](int64_t slots) {      // of a form that holds up to so many slots
+        const int64_t t = std::min(tokens, slots / top_k);
+        if (t > 0) most = std::max(most, total(t, t * top_k));
+    };
+    last(top_k);      // (one slot is a form of its own)
+    for (const double mean : {kGemvMean, kMean16, kMean32}) last(static_cast<int64_t>(mean * n_experts));
+    last(kFastRouteSlots);
+    return most;
+}
+
 }  // namespace
 }  // namespace ft
 
@@ -266,7 +281,7 @@ size_t ft_moe_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_exper
     int64_t n_slots;
     int64_t n;
     if (check_slots(tokens, top_k, n_experts, &n_slots) || check_cols(ncols, "ncols") || !mul_ok(n_slots, ncols, &n)) return 0;
-    return product_ws(nullptr, n_slots, n_experts, ncols).total;
+    return most_bytes(tokens, top_k, n_experts, [=](int64_t, int64_t slots) { return product_ws(nullptr, slots, n_experts, ncols).total; });
 }
 
 int ft_moe_fp8_fp8(const void* weights, const float* w_scales, const void* act, const float* act_scales,
@@ -320,7 +335,8 @@ size_t ft_moe_layer_fp8_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n
     if (check_matrix(n_experts, hidden, n_inter) || n_inter > FT_MAX_NCOLS || check_matrix(n_experts, 2 * n_inter, hidden))
         return 0;
     if (!mul_ok(n_slots, 8 * (hidden + n_inter), &n)) return 0;
-    return layer_ws(nullptr, tokens, n_slots, n_experts, hidden, n_inter).total;
+    return most_bytes(tokens, top_k, n_experts,
+                      [=](int64_t t, int64_t slots) { return layer_ws(nullptr, t, slots, n_experts, hidden, n_inter).total; });
 }
 
 int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t logits_dtype, int64_t row_stride,

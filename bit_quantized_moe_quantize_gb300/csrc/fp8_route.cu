@@ -19,11 +19,10 @@
 
 namespace ft {
 
-constexpr int64_t kMostChunks = 256;
 constexpr int32_t kMostRouteExperts = 1024;
 
 bool fp8_route_ok(int64_t n_slots, int32_t n_experts) {
-    return n_slots <= kChunk * kMostChunks && n_experts <= kMostRouteExperts;
+    return n_slots <= kFastRouteSlots && n_experts <= kMostRouteExperts;
 }
 
 size_t fp8_route_scratch(int64_t n_slots, int32_t n_experts) {

@@ -170,6 +170,7 @@ int launch_quantize_fp8_spread(const void* x, int dtype, uint8_t* codes, float* 
                                bool gated, int kind, const int32_t* pos, int32_t k, int32_t pitch, cudaStream_t s);
 
 // Router order (fp8_route.cu); fp8_route_ok: sizes that it takes.  pos may be null.
+constexpr int64_t kFastRouteSlots = 256 * 1024;
 bool fp8_route_ok(int64_t n_slots, int32_t n_experts);
 size_t fp8_route_scratch(int64_t n_slots, int32_t n_experts);
 int launch_fp8_route(const int32_t* ids, int64_t n_slots, int32_t n_experts, int32_t tile, int32_t* hist, int32_t* offsets,
@@ -205,6 +206,21 @@ struct Fp8Product {
 // moe_fp8.cu); the order's tiles must be of that width.  fp8_orders_itself: the product needs no launch_fp8_order before it.
 // Tiles of 256 take rows in router order only.
 constexpr int kWideTile = 256;
+// Slots per expert on average up to which a batch's slots are matrix-vector products of
+// their own, go by tiles of 16 and of 32.  Measured (us, experts' matrices 768 x 2048 of 128,
+// and 14336 x 4096 of 8): one slot each / 16 / 32 / 256 at
+//   0.25: 8.1 / 15.5 / 17.2 / 26.4    25.5 / 28.1 / 29.9 / 40.5
+//   0.5:  16.9 / 16.2 / 17.7 / 35.7   41.4 / 41.6 / 42.3 / 62.6
+//   1:    32 / 27 / 28 / 48           78 / 60 / 61 / 92
+//   8:    - / 38.4 / 39.0 / 61.9      - / 74.3 / 75.0 / 104.8
+//   16:   - / 45.7 / 45.8 / 66.6      - / 90.9 / 77.4 / 103.5
+//   32:   - / 60.0 / 53.7 / 70.2      (768 x 2048)
+// and tiles of 32 / 256, one product (1536 x 2048 of 128, 1312 x 1040 of 60, 7168 x 4096 of 8) and
+// the whole layer around it:
+//   40: 101 / 131, 47 / 56, 67 / 79;    185 / 209, 85 / 96, 112 / 117
+//   48: 107 / 134, 50 / 57, 69 / 78;    192 / 210, 87 / 97, 114 / 116
+//   64: 122 / 134, 53 / 58, 77 / 78;    233 / 213, 97 / 97, 131 / 115
+constexpr double kGemvMean = 0.5, kMean16 = 12, kMean32 = 52;
 int fp8_tile_width(int64_t n_slots, int32_t n_experts);
 bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width);
 int launch_fp8_product(const Fp8Product& p, int width, void* out, int out_dtype, uint32_t* err, cudaStream_t s);

@@ -633,22 +633,6 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------- host
 namespace {
 
-// Slots per expert on average up to which a batch's slots are matrix-vector products of
-// their own, go by tiles of 16 and of 32.  Measured (us, experts' matrices 768 x 2048 of 128,
-// and 14336 x 4096 of 8): one slot each / 16 / 32 / 256 at
-//   0.25: 8.1 / 15.5 / 17.2 / 26.4    25.5 / 28.1 / 29.9 / 40.5
-//   0.5:  16.9 / 16.2 / 17.7 / 35.7   41.4 / 41.6 / 42.3 / 62.6
-//   1:    32 / 27 / 28 / 48           78 / 60 / 61 / 92
-//   8:    - / 38.4 / 39.0 / 61.9      - / 74.3 / 75.0 / 104.8
-//   16:   - / 45.7 / 45.8 / 66.6      - / 90.9 / 77.4 / 103.5
-//   32:   - / 60.0 / 53.7 / 70.2      (768 x 2048)
-// and tiles of 32 / 256, one product (1536 x 2048 of 128, 1312 x 1040 of 60, 7168 x 4096 of 8) and
-// the whole layer around it:
-//   40: 101 / 131, 47 / 56, 67 / 79;    185 / 209, 85 / 96, 112 / 117
-//   48: 107 / 134, 50 / 57, 69 / 78;    192 / 210, 87 / 97, 114 / 116
-//   64: 122 / 134, 53 / 58, 77 / 78;    233 / 213, 97 / 97, 131 / 115
-constexpr double kGemvMean = 0.5, kMean16 = 12, kMean32 = 52;
-
 template <typename TO, bool GATED>
 int launch_pair(const CUtensorMap& wmap, const CUtensorMap& xmap, const PairArgs& a, void* out, int grid, cudaStream_t s) {
     using C = Pair;

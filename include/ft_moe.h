@@ -574,7 +574,8 @@ FT_API int ft_profile_read(double* quantize_ms, double* route_ms, double* matmul
  *     aligned, at least the bytes the matching _workspace_bytes function
  *     returns, any contents) may be reused once the call's work on the stream
  *     is done, so calls on different streams do not meet when their
- *     workspaces differ.
+ *     workspaces differ.  What these functions return never falls as tokens
+ *     rise: a workspace for a batch serves every smaller one.
  *   - An expert id of -1 means "no expert": its output row is 0 and no error
  *     flag is raised.  Other ids outside [0, n_experts) give a zero row and
  *     raise FT_DEVERR_BAD_EXPERT_ID.
