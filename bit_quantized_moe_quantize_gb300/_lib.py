@@ -127,7 +127,18 @@ def _torch():
     return torch
 
 
+def _current_device():
+    return _torch().cuda.current_device()
+
+
+def _refuse_device(index):
+    """The library works on the current device: tensors of another one would be read and written from there."""
+    raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{_current_device()}")
+
+
 def _stream(t):
+    if t.get_device() != _current_device():
+        _refuse_device(t.get_device())
     torch = _torch()
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
@@ -394,21 +405,29 @@ F32, F16, BF16 = 0, 1, 2
 _DTYPES: dict = {}       # torch dtype -> FT_DTYPE_*
 _CODES: tuple = ()       # torch dtypes that hold e4m3 codes
 _i32 = _f32 = _e4m3 = None
-_Tensor = _empty = _stream_of = None
+_Tensor = _empty = _raw_stream = None
 
 
 def _ready():
     """The library, with the torch names that the checks use."""
-    global _CODES, _i32, _f32, _e4m3, _Tensor, _empty, _stream_of
+    global _CODES, _i32, _f32, _e4m3, _Tensor, _empty, _raw_stream, _current_device
     torch = _torch()
     if not _CODES:
         _DTYPES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         _i32, _f32, _e4m3 = torch.int32, torch.float32, torch.float8_e4m3fn
         _Tensor, _empty = torch.Tensor, torch.empty
-        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", _current_device)      # without a check for a first use
         _CODES = (torch.float8_e4m3fn, torch.uint8)
     return load()
+
+
+def _stream_of(index):
+    """The current stream of device `index`, which has to be the current device."""
+    if index != _current_device():
+        _refuse_device(index)
+    return _raw_stream(index)
 
 
 def _lib_ready():
