@@ -15,8 +15,8 @@ namespace ft {
 static __device__ uint32_t g_fp8_error;
 
 // The word's address is looked up once per device; host code cannot use the
-// symbol's name as a pointer.
-int fp8_error_word(uint32_t** word) {
+// symbol's name as a pointer.  Every call that can raise a flag looks it up.
+int fp8_error_word(uint32_t** word, bool only_if_used) {
     constexpr int kMaxDevices = 64;
     static std::mutex mu;
     static uint32_t* at[kMaxDevices] = {};
@@ -25,7 +25,7 @@ int fp8_error_word(uint32_t** word) {
     if (e != cudaSuccess) return fail(FT_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
     if (dev < 0 || dev >= kMaxDevices) return fail(FT_ERR_CUDA, "device ordinal %d out of range", dev);
     std::lock_guard<std::mutex> lk(mu);
-    if (!at[dev]) {
+    if (!at[dev] && !only_if_used) {
         void* p = nullptr;
         e = cudaGetSymbolAddress(&p, g_fp8_error);
         if (e != cudaSuccess || !p) return fail(FT_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));

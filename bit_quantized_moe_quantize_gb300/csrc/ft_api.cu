@@ -792,12 +792,14 @@ int ft_moe_read_device_error(void* stream, uint32_t* flags_out) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    uint32_t fp8_flags = 0;   // the FP8 operators' own word
+    uint32_t fp8_flags = 0;   // the FP8 operators' own word; cudaMemcpy waits for other streams, too
     uint32_t* fp8_word = nullptr;
-    if (int st = fp8_error_word(&fp8_word)) return st;
-    e = cudaMemcpy(&fp8_flags, fp8_word, sizeof(fp8_flags), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && fp8_flags) e = cudaMemset(fp8_word, 0, sizeof(fp8_flags));
-    if (e != cudaSuccess) return cuda_fail(e, "reading the FP8 operators' error word");
+    if (int st = fp8_error_word(&fp8_word, true)) return st;
+    if (fp8_word) {
+        e = cudaMemcpy(&fp8_flags, fp8_word, sizeof(fp8_flags), cudaMemcpyDeviceToHost);
+        if (e == cudaSuccess && fp8_flags) e = cudaMemset(fp8_word, 0, sizeof(fp8_flags));
+        if (e != cudaSuccess) return cuda_fail(e, "reading the FP8 operators' error word");
+    }
     std::lock_guard<std::mutex> lk(g_ws_mu);
     DeviceWs& w = g_ws[dev];
     *flags_out = fp8_flags;

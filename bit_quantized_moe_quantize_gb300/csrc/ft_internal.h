@@ -17,7 +17,8 @@ void clear_error();
 
 // Device word that the FP8 operators raise FT_DEVERR_* flags in (one per
 // device, fixed for the life of the process; ft_moe_read_device_error reads it).
-int fp8_error_word(uint32_t** word);
+// only_if_used: null where no call of this process has asked for it before.
+int fp8_error_word(uint32_t** word, bool only_if_used = false);
 
 // Sets the dynamic shared-memory limit of a kernel once per device and size.
 int set_smem_limit(const void* kernel, int bytes);
