@@ -4,9 +4,10 @@
 // One tile: up to 128 weight rows of an expert x up to NW of its slots (16 or 32), one CTA,
 // tcgen05 MMAs with M = 128 weight rows and N = the tile's slots rounded up to 16.  Here the
 // weight rows lie along the tensor-memory lanes: with few slots the scales of a block are few,
-// and a warp reads them from shared memory at a broadcast for its 32 rows.  Where a batch has too
-// few tiles of 128 rows to fill the GPU, a tile takes 64 or 32 weight rows; the MMA still runs
-// over 128 lanes, whose other rows are whatever lies behind in shared memory and are not read.
+// and a warp reads them from shared memory at a broadcast for its 32 rows.  Tiles of 128 rows also
+// where a batch has too few of them to fill the GPU: of 64 or 32 rows, which it has more of, 21
+// batches of 1 to 128 experts and 2 to 300 slots took up to 1.5 times as long (300 slots, 1024 x
+// 4096 of 8: 39 us against 27; 16 slots, 1408 x 2816 of 8: 27.6 / 21.5) and none took less by more than 3 %.
 //
 // Blocks go through tensor memory in units of 64 columns (two blocks of 32 slots or four of 16),
 // so that the drain waits once per unit and the MMAs of four units run ahead of it.  Two CTAs
@@ -37,26 +38,26 @@ namespace ft {
 template <int NW_>
 struct Narrow {
     static constexpr int NW = NW_;
-    static constexpr int BM = 128;                                  // lanes; weight rows of a tile at most
+    static constexpr int BM = 128;                                  // lanes: weight rows of a tile
     static constexpr int G = 64 / NW;                               // blocks per unit
     static constexpr int UNIT = G * NW;                             // columns of a unit
     static constexpr int TMEM_COLS = 256;                           // two CTAs per SM
     static constexpr int UNITS = TMEM_COLS / UNIT;
     static constexpr int NSC = 4;                                   // units in the scale ring
-    static constexpr int MAX_STAGES = 16;
-    static constexpr int RING_BYTES = 80 * 1024;
-    static constexpr int SLACK = BM * kFp8Block;                    // what an MMA reads past the last short tile
-    static constexpr int OFF_SC = RING_BYTES + SLACK;
+    // a stage: NW slots' rows, then the weight rows
+    static constexpr int STAGES = 4;
+    static constexpr int ROW_BYTES = NW * kFp8Block, STAGE_BYTES = ROW_BYTES + BM * kFp8Block;
+    static constexpr int OFF_SC = STAGES * STAGE_BYTES;
     static constexpr int OFF_BAR = OFF_SC + NSC * UNIT * 4;
-    static constexpr int N_BARS = 2 * MAX_STAGES + 2 * UNITS + 2 * NSC;
+    static constexpr int N_BARS = 2 * STAGES + 2 * UNITS + 2 * NSC;
     static constexpr int OFF_TMEM = OFF_BAR + N_BARS * 8;
     // in-CTA order: offsets[E + 1], tiles[E + 1], perm[1024]; the counts [8][E] lie in the ring
     static constexpr int MAX_E = 1024;
     static constexpr int OFF_ORDER = OFF_TMEM + 16;
     static constexpr int SMEM_BYTES = OFF_ORDER + (2 * (MAX_E + 1) + 1024 + 8) * 4 + 1024;
-    static_assert(kChunkWarps * MAX_E * 4 <= RING_BYTES, "counts");
+    static_assert(kChunkWarps * MAX_E * 4 <= OFF_SC, "counts");
     static constexpr int WARP_PRODUCER = 4, WARP_MMA = 5, WARP_SCALE = 6, WARP_ROWS = 7;
-    static constexpr int THREADS = 256;
+    static constexpr int THREADS = 256, N_DRAIN_WARPS = BM / 32;
     static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "shared memory budget of two CTAs");
 };
 
@@ -71,8 +72,6 @@ struct NarrowArgs {
     uint32_t* err;
     int64_t n_slots, nrows, ncols;
     int32_t act_div, n_experts, nb, row_tiles, row_blocks, scale_pitch;
-    int32_t br;                  // weight rows of a tile: 32, 64 or 128
-    int32_t stages;
     bool ordered;                // activation rows lie in router order
     bool orders;                 // perm, offsets and tiles are worked out by the CTA
 };
@@ -85,7 +84,7 @@ template <int NW>
 __device__ __forceinline__ NarrowTile narrow_tile(const NarrowArgs& a, const int32_t* tiles, const int32_t* offsets, int64_t w) {
     NarrowTile t;
     const int32_t st = static_cast<int32_t>(w / a.row_tiles);
-    t.r0 = static_cast<int32_t>(w - static_cast<int64_t>(st) * a.row_tiles) * a.br;
+    t.r0 = static_cast<int32_t>(w - static_cast<int64_t>(st) * a.row_tiles) * Narrow<NW>::BM;
     int32_t first = 0, count = static_cast<int32_t>(a.n_slots), j = st;
     t.e = 0;
     if (tiles) {
@@ -106,8 +105,8 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* empty = full + C::MAX_STAGES;
-    uint64_t* acc_full = empty + C::MAX_STAGES;
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* acc_full = empty + C::STAGES;
     uint64_t* acc_empty = acc_full + C::UNITS;
     uint64_t* sc_full = acc_empty + C::UNITS;
     uint64_t* sc_empty = sc_full + C::NSC;
@@ -115,23 +114,20 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
     float* sc_ring = reinterpret_cast<float*>(smem + C::OFF_SC);
 
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
-    const int32_t nb = a.nb, stages = a.stages;
-    // a stage: NW slots' rows, then br weight rows (last, so that an MMA over 128 rows stays inside)
-    const uint32_t b_bytes = NW * kFp8Block, stage_bytes = b_bytes + static_cast<uint32_t>(a.br) * kFp8Block;
-    const uint32_t n_drain = static_cast<uint32_t>(a.br) / 32;
+    const int32_t nb = a.nb;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::MAX_STAGES; ++i) {
+        for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1 + 32);      // the producer and the lanes that copy rows
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < C::UNITS; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], n_drain);
+            mbar_init(&acc_empty[i], C::N_DRAIN_WARPS);
         }
         for (int i = 0; i < C::NSC; ++i) {
             mbar_init(&sc_full[i], 1);
-            mbar_init(&sc_empty[i], n_drain);
+            mbar_init(&sc_empty[i], C::N_DRAIN_WARPS);
         }
         fence_mbar_init();
     }
@@ -175,8 +171,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
 
     if (warp == C::WARP_PRODUCER) {
         // ------------------------------------------------------------ producer
-        int32_t s = 0;
-        uint32_t phase = 1, it = 0;
+        uint32_t s = 0, phase = 1, it = 0;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
             const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
@@ -184,20 +179,19 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
             for (int32_t b = 0; b < nb; ++b, ++it) {
                 if (!mbar_wait_warp(&empty[s], phase, a.err)) { ok = false; break; }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[s], stage_bytes - b_bytes);
-                    tma_load_2d(smem + static_cast<uint32_t>(s) * stage_bytes + b_bytes, &wmap, b * kFp8Block, wy, &full[s]);
+                    mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES - C::ROW_BYTES);
+                    tma_load_2d(smem + s * C::STAGE_BYTES + C::ROW_BYTES, &wmap, b * kFp8Block, wy, &full[s]);
                 }
                 __syncwarp();
-                if (++s == stages) {
+                if (++s == C::STAGES) {
                     s = 0;
                     phase ^= 1u;
                 }
             }
         }
         // the last fills: read by their MMAs, or at least arrived, before the CTA's memory goes
-        const uint32_t n_stages = static_cast<uint32_t>(stages);
-        for (uint32_t f = it - min(it, n_stages); f != it; ++f) {
-            const uint32_t last = f % n_stages, parity = (f / n_stages) & 1u;
+        for (uint32_t f = it - min(it, static_cast<uint32_t>(C::STAGES)); f != it; ++f) {
+            const uint32_t last = f % C::STAGES, parity = (f / C::STAGES) & 1u;
             if (mbar_wait_warp(&empty[last], parity, a.err, ok ? kWaitLimitNs : kLastWaitNs)) continue;
             ok = false;
             mbar_wait_warp(&full[last], parity, a.err, kLastWaitNs);
@@ -206,8 +200,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         // ----------------------------------------------------------------- MMA
         const bool elected = elect_one();
         const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
-        int32_t s = 0;
-        uint32_t phase = 0, unit = 0;
+        uint32_t s = 0, phase = 0, unit = 0;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
             const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
@@ -221,14 +214,14 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
                     fence_proxy_async_smem();      // the copied rows are ordinary writes
                     tc_fence_after();
                     if (elected) {
-                        const uint64_t bdesc = desc0 + ((static_cast<uint32_t>(s) * stage_bytes) >> 4), adesc = bdesc + (b_bytes >> 4);
+                        const uint64_t bdesc = desc0 + ((s * C::STAGE_BYTES) >> 4), adesc = bdesc + (C::ROW_BYTES >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             tc_mma_f8(tmem + u * C::UNIT + static_cast<uint32_t>(g) * NW, adesc + 2 * k, bdesc + 2 * k, idesc, k);
                         tc_commit(&empty[s]);
                         if (g == n - 1) tc_commit(&acc_full[u]);
                     }
-                    if (++s == stages) {
+                    if (++s == C::STAGES) {
                         s = 0;
                         phase ^= 1u;
                     }
@@ -238,7 +231,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         __syncwarp();
     } else if (warp == C::WARP_SCALE) {
         // -------------------------------------------------------------- scales
-                uint32_t unit = 0;
+        uint32_t unit = 0;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
             const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
@@ -280,7 +273,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
                 }
             }
         }
-    } else if (warp < n_drain) {
+    } else if (warp < C::N_DRAIN_WARPS) {
         // --------------------------------------------------------------- drain
         uint32_t unit = 0;
         bool ok = true;
@@ -335,8 +328,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
         // ---------------------------------------------------------------- rows
         // lane: 16-byte word `word` of rows first, first + 4, ..
         const uint32_t word = lane & 7u, first = lane >> 3;
-        int32_t s = 0;
-        uint32_t phase = 1;
+        uint32_t s = 0, phase = 1;
         bool ok = true;
         for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
             const NarrowTile t = narrow_tile<NW>(a, tiles, offsets, w);
@@ -349,7 +341,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
             int64_t left = a.ncols - 16 * word;      // columns from this lane's word to the rows' end
             for (int32_t b = 0; b < nb; ++b, left -= kFp8Block) {
                 if (!mbar_wait_warp(&empty[s], phase, a.err)) { ok = false; break; }
-                const uint32_t dst = smem_u32(smem + static_cast<uint32_t>(s) * stage_bytes);
+                const uint32_t dst = smem_u32(smem + s * C::STAGE_BYTES);
 #pragma unroll
                 for (int i = 0; i < NW / 4; ++i) {
                     const uint32_t r = first + 4 * i;
@@ -361,7 +353,7 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
                 }
                 // arrives when this lane's copies have
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[s])) : "memory");
-                if (++s == stages) {
+                if (++s == C::STAGES) {
                     s = 0;
                     phase ^= 1u;
                 }
@@ -380,11 +372,9 @@ __global__ void __launch_bounds__(Narrow<NW>::THREADS, 2)
 namespace {
 
 template <int NW, typename TO>
-int launch_narrow(const CUtensorMap& wmap, NarrowArgs& a, void* out, int64_t tiles, cudaStream_t s) {
+int launch_narrow(const CUtensorMap& wmap, const NarrowArgs& a, void* out, int64_t tiles, cudaStream_t s) {
     using C = Narrow<NW>;
     const void* k = reinterpret_cast<const void*>(moe_fp8_narrow_kernel<NW, TO>);
-    const int stage = (NW + a.br) * kFp8Block;
-    a.stages = C::RING_BYTES / stage < C::MAX_STAGES ? C::RING_BYTES / stage : C::MAX_STAGES;
     if (int st = set_smem_limit(k, C::SMEM_BYTES)) return st;
     const int64_t ctas = 2 * sm_count();
     const dim3 grid(static_cast<unsigned>(tiles < ctas ? tiles : ctas));
@@ -421,17 +411,11 @@ int launch_fp8_narrow(const Fp8Product& p, int width, void* out, int out_dtype, 
         a.offsets = p.order->offsets;
         a.tiles = p.order->tiles;
     }
-    const int64_t some = p.ids ? (p.n_experts < p.n_slots ? p.n_experts : p.n_slots) : 1;
-    const int64_t most_tiles = (p.n_slots + width - 1) / width + (p.ids ? some : 0);
-    // shorter tiles where those of 128 rows, over the experts that a batch is likely to
-    // touch, would leave SMs without two
-    const int64_t likely = p.ids ? (some > (p.n_slots + width - 1) / width ? some : (p.n_slots + width - 1) / width) : most_tiles;
-    a.br = 128;
-    while (a.br > 32 && likely * ((p.nrows + a.br - 1) / a.br) < 2 * sm_count()) a.br /= 2;
-    a.row_tiles = static_cast<int32_t>((p.nrows + a.br - 1) / a.br);
+    const int64_t most_tiles = (p.n_slots + width - 1) / width + (p.ids ? (p.n_experts < p.n_slots ? p.n_experts : p.n_slots) : 0);
+    a.row_tiles = static_cast<int32_t>((p.nrows + Narrow<16>::BM - 1) / Narrow<16>::BM);
     CUtensorMap wmap;
     if (int st = encode_2d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.weights, p.ncols,
-                           static_cast<uint64_t>(p.n_experts) * p.nrows, p.ncols, kFp8Block, a.br,
+                           static_cast<uint64_t>(p.n_experts) * p.nrows, p.ncols, kFp8Block, Narrow<16>::BM,
                            CU_TENSOR_MAP_SWIZZLE_128B, "FP8 weights"))
         return st;
     const int64_t tiles = most_tiles * a.row_tiles;
