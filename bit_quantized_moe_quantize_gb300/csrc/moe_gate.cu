@@ -13,13 +13,11 @@
 //   w   = s[ids], renormalised by max(sum, 1e-30) if asked, times `scale`
 //
 // Up to 512 experts in one group, or in groups of 16, 32, 64, ..: 2, 8, 16 or 32 lanes per token,
-// 16 neighbouring experts each, in registers.  A key and the complement of its expert make one
-// integer (32 bits where 16-bit logits are the keys, else 64), whose maximum over the lanes is
-// the choice with its tie rule: a round is a few shuffles, and the lane that held the maximum
-// looks again.
-//
-// Up to eight choices come from sorting networks instead.  Bound by instructions: 65536 tokens of
-// 128 bf16 logits, 8 choices: 16 us (21 MB: 3 us at the copy's rate); fp32 34 us, by rounds 48.
+// 16 neighbouring experts each, in registers (few_experts has when).  A key and the complement of its
+// expert make one integer (32 bits where 16-bit logits are the keys, else 64), whose maximum over the
+// lanes is the choice with its tie rule: a round is a few shuffles, and the lane that held the
+// maximum looks again.  Up to eight choices come from sorting networks instead.  65536 tokens of 128 bf16
+// logits, 8 choices: 16 us (21 MB: 3 us at the copy's rate); fp32 34 us, by rounds 48.
 //
 // Otherwise one warp per token (65535 tokens of 1024 experts: 191 us).  The keys lie in shared
 // memory; each lane keeps the best key of its experts (every 32nd), and one round per chosen
@@ -68,9 +66,7 @@ __device__ __forceinline__ float gate_score(float l, float top, float sum, int32
     return __fdiv_rn(gate_exp(l, top), fmaxf(sum, kGateTiny));
 }
 
-// Removes and returns the largest key of keys[0..n) (order integers, 0: none
-// left) as its index, -1 if none is left.  best/at: the lane's own largest key
-// and its index, kept from call to call.
+// A lane's own largest key (an order integer, 0: none left) and its index.
 struct Best {
     uint32_t key;
     int32_t at;
@@ -83,6 +79,7 @@ __device__ __forceinline__ Best lane_best(const uint32_t* keys, int32_t n) {
     return b;
 }
 
+// Removes the largest key of keys[0..n) and returns its index, -1 if none is left.  b: kept from call to call.
 __device__ __forceinline__ int32_t take_best(uint32_t* keys, int32_t n, Best& b) {
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, b.key);
     if (top == 0u) return -1;
@@ -464,6 +461,31 @@ static int launch_few_typed(const GateArgs& a, cudaStream_t s) {
     return launch_few<T, 32, uint64_t>(a, s);
 }
 
+// Whether a batch goes to moe_gate_few_kernel.  It takes up to 512 experts, and groups that are 1, 2,
+// 4, .. whole lanes; where it takes a batch, both kernels' times decide (us with cold caches, registers /
+// shared memory):
+//   16-bit logits as keys: 65535 tokens of 512, 8 choices 63 / 126, 32 choices 281 / 331
+//   64-bit keys, 65535 tokens by 2, 8, 16 choices
+//     128 experts       fp32 logits 39/46, 39/82, 87/132     sigmoid with a bias 51/47, 51/81, 97/131
+//     256               75/54, 75/93, 169/147                97/64, 97/100, 185/150
+//     512               151/74, 151/125, 331/192             198/101, 199/145, 364/206
+//     256 in 8 groups   -                                    106/112, 106/146, 196/194, and 339/299 by 32
+//     512 in 8 groups   -                                    216/189, 216/227, 389/285
+//   8192 tokens of 512  29/20, 29/27, 53/36                  34/29, 33/35, 58/43
+//   777 tokens of 512   12/11, 12/14, 19/17                  15/18, 16/19, 21/23
+// so 64-bit keys of many tokens stay in registers up to 128 experts, up to 256 where the sorting
+// networks' time, the same for one choice as for eight, is made use of, and in groups while there are
+// networks for them.
+static bool few_experts(const GateParams& p, int dtype) {
+    const int32_t lanes = p.n_experts / p.n_groups / kGatePer;
+    const bool whole = p.n_groups == 1 || (lanes > 0 && p.n_experts == lanes * kGatePer * p.n_groups && (lanes & (lanes - 1)) == 0);
+    if (!whole || p.n_experts > 32 * kGatePer) return false;
+    const bool packed = dtype != FT_DTYPE_F32 && p.bias == nullptr && p.n_groups == 1;
+    if (packed || p.tokens < 8192 || p.n_experts <= 8 * kGatePer) return true;
+    if (p.n_groups > 1) return p.top_k <= 8 || p.n_experts <= 16 * kGatePer;
+    return p.n_experts <= 16 * kGatePer && p.top_k > 5 && p.top_k <= 8;
+}
+
 int launch_gate(const GateParams& p, const void* logits, int dtype, int64_t stride, int32_t* ids, float* weights,
                 cudaStream_t s) {
     if (p.tokens == 0) return FT_OK;
@@ -482,11 +504,7 @@ int launch_gate(const GateParams& p, const void* logits, int dtype, int64_t stri
     a.group_top = p.group_top;
     a.renormalize = p.renormalize;
     a.scale = p.scale;
-    // groups of experts that are 1, 2, 4, .. whole lanes stay in registers too (65535 tokens of 256
-    // in 8 groups: 103 us, by shared memory 144)
-    const int32_t lanes = p.n_experts / p.n_groups / kGatePer;
-    const bool whole = p.n_groups == 1 || (lanes > 0 && p.n_experts == lanes * kGatePer * p.n_groups && (lanes & (lanes - 1)) == 0);
-    if (whole && p.n_experts <= 32 * kGatePer)
+    if (few_experts(p, dtype))
         return dtype == FT_DTYPE_F32   ? launch_few_typed<float>(a, s)
                : dtype == FT_DTYPE_F16 ? launch_few_typed<__half>(a, s)
                                        : launch_few_typed<__nv_bfloat16>(a, s);
