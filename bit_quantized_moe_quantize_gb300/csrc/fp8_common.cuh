@@ -51,26 +51,17 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N consecutive elements (16-byte loads where sizeof(T) * N allows) as fp32;
-// p must be aligned to min(16, sizeof(T) * N) bytes.
+// N consecutive elements, whole 16-byte words of them, as fp32; p must be 16-byte aligned.
 template <typename T, int N>
 __device__ __forceinline__ void load_vec(const T* p, float (&v)[N]) {
-    constexpr int BYTES = static_cast<int>(sizeof(T)) * N;
-    if constexpr (BYTES >= 16) {
-        constexpr int PER = 16 / static_cast<int>(sizeof(T));
+    constexpr int PER = 16 / static_cast<int>(sizeof(T));
+    static_assert(N % PER == 0, "whole words");
 #pragma unroll
-        for (int i = 0; i < N / PER; ++i) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + i);
-            const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-            for (int j = 0; j < PER; ++j) v[i * PER + j] = to_f32<T>(e[j]);
-        }
-    } else {
-        static_assert(BYTES == 8, "8- or 16-byte vectors");
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    for (int i = 0; i < N / PER; ++i) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + i);
         const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = to_f32<T>(e[j]);
+        for (int j = 0; j < PER; ++j) v[i * PER + j] = to_f32<T>(e[j]);
     }
 }
 

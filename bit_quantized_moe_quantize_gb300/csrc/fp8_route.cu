@@ -14,6 +14,12 @@
 // order never depends on timing.
 //
 // 65536 slots, 128 experts: 5 us and 17 us; bound by the place kernel's chain of barriers.
+//
+// Past kFastRouteSlots or kMostRouteExperts the GGUF path's router: the prefixes over chunks take
+// chunks^2 times experts reads in all, and somewhere past both bounds that is the longer way.
+// A product of short rows on this router / on that one (us): 262152 slots of 128 experts 119 / 127,
+// 524288 212 / 221, 2 million 1085 / 778; 8192 slots of 1100 experts 39 / 48, 65536 of 2048 166 / 180,
+// 262144 of 4096 1862 / 1231.
 #include "fp8_order.cuh"
 #include "ft_internal.h"
 

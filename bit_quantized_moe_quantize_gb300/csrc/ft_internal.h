@@ -221,6 +221,13 @@ constexpr int kWideTile = 256;
 //   40: 101 / 131, 47 / 56, 67 / 79;    185 / 209, 85 / 96, 112 / 117
 //   48: 107 / 134, 50 / 57, 69 / 78;    192 / 210, 87 / 97, 114 / 116
 //   64: 122 / 134, 53 / 58, 77 / 78;    233 / 213, 97 / 97, 131 / 115
+// One expert (a dense matrix) of 2048 x 7168, 4096 x 4096, 7168 x 2048, 14336 x 4096:
+//   64:  28.4 / 32.1, 22.4 / 24.4, 18.0 / 18.7, 30.0 / 29.0
+//   128: 28.9 / 33.0, 22.7 / 24.3, 19.0 / 19.2, 40.4 / 29.2
+//   512: 33.0 / 34.4, 37.1 / 24.8, 32.4 / 20.0, 94.9 / 45.7
+// and 16 experts of 768 x 2048, 4 of 1024 x 2048 (up to 1024 slots order themselves with the narrow tiles):
+//   56: 21.5 / 29.0, 19.4 / 26.7    96: 33.1 / 32.1, 20.9 / 27.5    256: 42.4 / 34.8, 22.1 / 27.4    400: 55.1 / 44.6, 32.6 / 30.7
+// so few experts of few rows would stay with 32 slots for longer; by slots per expert alone, 52 is between.
 constexpr double kGemvMean = 0.5, kMean16 = 12, kMean32 = 52;
 int fp8_tile_width(int64_t n_slots, int32_t n_experts);
 bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width);

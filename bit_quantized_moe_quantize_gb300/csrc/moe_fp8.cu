@@ -11,7 +11,7 @@
 // tile's weight rows rounded up to 32).  Each CTA loads its 128 slots' rows and
 // half of the weight rows per block of 128 columns, so an operand byte in shared
 // memory is read once for 256 x 256 products.  A block's products are summed by the tensor
-// core in fp32 in a tensor-memory accumulator (two of them, 256 columns each, in
+// core in fp32 in tensor-memory accumulators (of 128 columns, two for each half of the tile, in
 // turn); the scales change with the next block, so the drain takes each block's
 // sums out of tensor memory and adds them, times sa * sw, to fp32 registers.
 // Slots lie along the lanes, so that product is one number per thread: with the
@@ -38,8 +38,8 @@
 //
 // Bound by the drain beside the MMAs: a block takes some 920 cycles (dense 8192^3, all tiles
 // full: 415 to 436 us, 2.5 to 2.65 PFLOP/s), where the MMAs alone take 512.  Routed, the tiles of 256 slots
-// are not full: 8191 tokens, 8 of 128 experts, 1408 x 2816: 354 us with the order and the copies of
-// the rows, 1.47 PFLOP/s.
+// are not full: 8191 tokens, 8 of 128 experts, 1408 x 2816: 343 us with the order and the copies of
+// the rows, 1.51 PFLOP/s.
 #include <atomic>
 
 #include "fp8_order.cuh"
@@ -281,88 +281,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     PairWalk walk(a, tiles, static_cast<int32_t>(blockIdx.x / 2), static_cast<int32_t>(gridDim.x / 2));
 
     if (warp >= C::N_DRAIN_WARPS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs(GATED)));
-    if (warp == C::WARP_PRODUCER) {
-        // ------------------------------------------------------------ producer
-        uint32_t it = 0;
-        bool ok = true;
-        for (; walk.there() && ok; walk.next(tiles)) {
-            const PairTile t = walk.tile(a, tiles, offsets);
-            const int32_t mine = t.mine(rank), other = t.mine(rank ^ 1u);
-            constexpr int PER = C::ROW_BOX;      // lane l copies 32 of this CTA's slots
-            const bool copies = static_cast<int32_t>(lane) * PER < mine;
-            const int32_t y = t.first(rank) + static_cast<int32_t>(lane) * PER;
-            // half h of the tile (weight rows 128 h ..): this CTA's part of its MMA's columns
-            const int32_t halves = t.width > C::CW ? 2 : 1;
-            const int64_t row0 = static_cast<int64_t>(t.e) * a.nrows + t.r0;
-            // gated: columns 0 .. 63 of half h are gate rows 64 h .., columns 64 .. 127 the same up rows
-            const int32_t wy = GATED ? static_cast<int32_t>(static_cast<int64_t>(t.e) * a.nrows + t.r0 / 2 + lane * C::BOX + rank * a.n_inter)
-                                     : static_cast<int32_t>(row0 + lane * C::CW + rank * (t.cols(static_cast<int32_t>(lane)) / 2));
-            const uint32_t bytes = 2 * halves * C::BOX * kFp8Block +
-                                   ((mine + PER - 1) / PER + (other + PER - 1) / PER) * PER * kFp8Block;
-            for (int32_t b = 0; b < nb; ++b, ++it) {
-                const uint32_t s = it % C::STAGES;
-                if (!mbar_wait_warp(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, a.err)) { ok = false; break; }
-                const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-                const uint32_t dst = smem_u32(smem + s * C::STAGE_BYTES);
-                if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                if (static_cast<int32_t>(lane) < halves)
-                    tma_load_2d_pair(dst + C::A_BYTES + lane * (C::BOX * kFp8Block), &wmap, b * kFp8Block, wy, bar);
-                if (copies) tma_load_2d_pair(dst + lane * (PER * kFp8Block), &xmap, b * kFp8Block, y, bar);
-                __syncwarp();
-            }
-        }
-        // the last fills: read by their MMAs, or at least arrived, before the CTA's memory goes
-        for (uint32_t f = it - min(it, static_cast<uint32_t>(C::STAGES)); f != it; ++f) {
-            const uint32_t s = f % C::STAGES, parity = (f / C::STAGES) & 1u;
-            if (mbar_wait_warp(&empty[s], parity, a.err, ok ? kWaitLimitNs : kLastWaitNs)) continue;
-            ok = false;
-            if (rank == 0) mbar_wait_warp(&full[s], parity, a.err, kLastWaitNs);
-        }
-    } else if (warp < C::WARP_ZERO) {
-        // ----------------------------------------------------------------- MMA
-        // Warp h issues the MMAs of half h.  The whole warp runs the loop and one elected
-        // lane issues: with the operands in uniform registers four MMAs and a commit take
-        // 180 cycles to issue, from a single-lane branch 295, more than the 256 that they run.
-        if (rank == 0) {
-            const uint32_t h = warp - C::WARP_MMA;
-            const bool elected = elect_one();
-            const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
-            const uint64_t bskip = (C::A_BYTES + h * (C::BOX * kFp8Block)) >> 4;
-            uint32_t s = 0, phase = 0, done = 0;      // stage, its phase, blocks of this half
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs(GATED)));
+        if (warp == C::WARP_PRODUCER) {
+            // ------------------------------------------------------------ producer
+            uint32_t it = 0;
             bool ok = true;
             for (; walk.there() && ok; walk.next(tiles)) {
                 const PairTile t = walk.tile(a, tiles, offsets);
-                const int32_t cols = t.cols(static_cast<int32_t>(h));
-                const uint32_t idesc = idesc_e4m3_f32(2 * C::BM, max(cols, 0));
-                for (int32_t b = 0; b < nb; ++b) {
-                    const uint32_t d = 2 * h + (done & 1u);
-                    if (cols > 0) {
-                        if (!mbar_wait2_warp(&full[s], phase, &acc_empty[d], ((done >> 1) & 1u) ^ 1u, a.err)) { ok = false; break; }
-                        ++done;
-                        tc_fence_after();
-                        if (elected) {
-                            const uint64_t adesc = desc0 + ((s * C::STAGE_BYTES) >> 4), bdesc = adesc + bskip;
+                const int32_t mine = t.mine(rank), other = t.mine(rank ^ 1u);
+                constexpr int PER = C::ROW_BOX;      // lane l copies 32 of this CTA's slots
+                const bool copies = static_cast<int32_t>(lane) * PER < mine;
+                const int32_t y = t.first(rank) + static_cast<int32_t>(lane) * PER;
+                // half h of the tile (weight rows 128 h ..): this CTA's part of its MMA's columns
+                const int32_t halves = t.width > C::CW ? 2 : 1;
+                const int64_t row0 = static_cast<int64_t>(t.e) * a.nrows + t.r0;
+                // gated: columns 0 .. 63 of half h are gate rows 64 h .., columns 64 .. 127 the same up rows
+                const int32_t wy = GATED ? static_cast<int32_t>(static_cast<int64_t>(t.e) * a.nrows + t.r0 / 2 + lane * C::BOX + rank * a.n_inter)
+                                         : static_cast<int32_t>(row0 + lane * C::CW + rank * (t.cols(static_cast<int32_t>(lane)) / 2));
+                const uint32_t bytes = 2 * halves * C::BOX * kFp8Block +
+                                       ((mine + PER - 1) / PER + (other + PER - 1) / PER) * PER * kFp8Block;
+                for (int32_t b = 0; b < nb; ++b, ++it) {
+                    const uint32_t s = it % C::STAGES;
+                    if (!mbar_wait_warp(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, a.err)) { ok = false; break; }
+                    const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+                    const uint32_t dst = smem_u32(smem + s * C::STAGE_BYTES);
+                    if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                    if (static_cast<int32_t>(lane) < halves)
+                        tma_load_2d_pair(dst + C::A_BYTES + lane * (C::BOX * kFp8Block), &wmap, b * kFp8Block, wy, bar);
+                    if (copies) tma_load_2d_pair(dst + lane * (PER * kFp8Block), &xmap, b * kFp8Block, y, bar);
+                    __syncwarp();
+                }
+            }
+            // the last fills: read by their MMAs, or at least arrived, before the CTA's memory goes
+            for (uint32_t f = it - min(it, static_cast<uint32_t>(C::STAGES)); f != it; ++f) {
+                const uint32_t s = f % C::STAGES, parity = (f / C::STAGES) & 1u;
+                if (mbar_wait_warp(&empty[s], parity, a.err, ok ? kWaitLimitNs : kLastWaitNs)) continue;
+                ok = false;
+                if (rank == 0) mbar_wait_warp(&full[s], parity, a.err, kLastWaitNs);
+            }
+        } else if (warp < C::WARP_ZERO) {
+            // ----------------------------------------------------------------- MMA
+            // Warp h issues the MMAs of half h.  The whole warp runs the loop and one elected
+            // lane issues: with the operands in uniform registers four MMAs and a commit take
+            // 180 cycles to issue, from a single-lane branch 295, more than the 256 that they run.
+            if (rank == 0) {
+                const uint32_t h = warp - C::WARP_MMA;
+                const bool elected = elect_one();
+                const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+                const uint64_t bskip = (C::A_BYTES + h * (C::BOX * kFp8Block)) >> 4;
+                uint32_t s = 0, phase = 0, done = 0;      // stage, its phase, blocks of this half
+                bool ok = true;
+                for (; walk.there() && ok; walk.next(tiles)) {
+                    const PairTile t = walk.tile(a, tiles, offsets);
+                    const int32_t cols = t.cols(static_cast<int32_t>(h));
+                    const uint32_t idesc = idesc_e4m3_f32(2 * C::BM, max(cols, 0));
+                    for (int32_t b = 0; b < nb; ++b) {
+                        const uint32_t d = 2 * h + (done & 1u);
+                        if (cols > 0) {
+                            if (!mbar_wait2_warp(&full[s], phase, &acc_empty[d], ((done >> 1) & 1u) ^ 1u, a.err)) { ok = false; break; }
+                            ++done;
+                            tc_fence_after();
+                            if (elected) {
+                                const uint64_t adesc = desc0 + ((s * C::STAGE_BYTES) >> 4), bdesc = adesc + bskip;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) tc_mma_f8_pair(tmem + d * C::CW, adesc + 2 * k, bdesc + 2 * k, idesc, k);
-                            tc_commit_pair(&acc_full[d]);
-                            tc_commit_pair(&empty[s]);
+                                for (int k = 0; k < 4; ++k) tc_mma_f8_pair(tmem + d * C::CW, adesc + 2 * k, bdesc + 2 * k, idesc, k);
+                                tc_commit_pair(&acc_full[d]);
+                                tc_commit_pair(&empty[s]);
+                            }
+                        } else {
+                            if (!mbar_wait_warp(&full[s], phase, a.err)) { ok = false; break; }
+                            if (elected) tc_commit_pair(&empty[s]);
                         }
-                    } else {
-                        if (!mbar_wait_warp(&full[s], phase, a.err)) { ok = false; break; }
-                        if (elected) tc_commit_pair(&empty[s]);
-                    }
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        phase ^= 1u;
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
             }
+            __syncwarp();
+        } else if (!GATED && a.ids) {
+            zero_unrouted<TO>(a.ids, a.n_slots, a.n_experts, a.nrows, a.err, out, blockIdx.x, gridDim.x);
         }
-        __syncwarp();
-    } else if (!GATED && a.ids) {
-        zero_unrouted<TO>(a.ids, a.n_slots, a.n_experts, a.nrows, a.err, out, blockIdx.x, gridDim.x);
-    }
     } else {
         // --------------------------------------------------------------- drain
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::drain_regs(GATED)));

@@ -384,6 +384,9 @@ int launch_narrow(const CUtensorMap& wmap, const NarrowArgs& a, void* out, int64
 
 }  // namespace
 
+// (us, ordered by the product's CTAs / by a launch before it: 512 and 1024 slots of 128 experts,
+// 1536 x 2048, 90.1 / 92.3 and 90.6 / 92.5; 1024 of 60, 1414 x 2000, 53.1 / 55.5; 1024 of 512, 512 x 1024,
+// 60.8 / 62.7.  One chunk is what the CTAs' arrays hold.)
 bool fp8_orders_itself(int64_t n_slots, int32_t n_experts, int width) {
     return width == 1 || (width <= 32 && n_slots <= kChunk && n_experts <= Narrow<16>::MAX_E);
 }

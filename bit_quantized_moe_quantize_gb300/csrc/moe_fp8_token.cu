@@ -11,9 +11,9 @@
 //
 // Reading the experts' matrices once is what is left to wait for, beside the launches: the
 // same pieces as separate launches (quantizer, product, quantizer, product, weighted sum)
-// take six.  Every value is rounded as those do, except that the second product's rows are
-// added up in fp32 as they come.  One token, 8 of 128 experts, 2048 and 768 wide: 16 us with the
-// router in a graph (38 MB: 5.6 us at the copy's rate).
+// take six.  Every value is rounded as those do, with the second product's rows in fp32.  One
+// token, 8 of 128 experts, 2048 and 768 wide: 19 us with the router in a graph, 30 with cold caches
+// (38 MB: 5.6 us at the copy's rate).
 //
 // Each launch may start before the one before it has ended (programmatic dependent launch):
 // what it reads of that one's results comes after griddepcontrol.wait, and nothing is
@@ -24,6 +24,8 @@
 
 namespace ft {
 
+// CTAs per SM: 2, 3, 4 take (us) 36.5, 30.5, 31.6 for one token, 8 slots, 2048 and 768 wide; 30.8, 27.6,
+// 29.7 for 4 tokens, 8 slots, 1024 and 384.
 constexpr int kTokenWarps = 8, kPairs = 2, kDownRows = 4, kCtasPerSm = 3;
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -222,9 +224,17 @@ int launch_dependent(void (*kernel)(A...), const char* name, dim3 grid, size_t s
 }  // namespace
 
 bool fp8_token_ok(int64_t n_slots, int64_t tokens, int32_t top_k, int64_t hidden, int64_t n_inter) {
-    // Past some 40 MB of matrices the separate launches, whose warps are not tied to slots, read
-    // them faster (us, these kernels / separate): 8 MB 10.5 / 16.7, 38 MB 16.2 / 20.2, 50 MB
-    // 22.9 / 21.3, 75 MB 28.4 / 28.9, 151 MB 52.5 / 45.4.
+    // The more the matrices' reading takes, the less the launches saved count, and the separate
+    // kernels' warps, which are not tied to slots, read them faster.  Times (us, cold, these kernels /
+    // separate; tokens x slots, hidden, n_inter):
+    //   6 MB   1x1 2048 1024 25/27;   13 MB  4x2 1024 512 20/25, 1x1 4096 1024 35/31;   14 MB 1x8 768 768 22/29
+    //   25 MB  1x8 2048 512 25/29, 8x8 512 256 22/31, 1x2 2048 1792 33/30 (22 MB)
+    //   38 MB  1x8 2048 768 30/32, 1x8 1024 1536 28/33, 2x8 2048 384 28/34, 1x4 2048 1536 32/33, 1x2 4096 1536 41/37
+    //   50 MB  1x8 2048 1024 36/33, 1x8 1024 2048 34/38, 4x8 1024 512 30/36, 1x4 4096 1024 39/38, 1x2 4096 2048 46/40
+    //   75 MB  1x8 4096 768 43/46, 8x8 1024 384 37/43;  65 MB 1x6 2560 1408 43/40, 63 MB 1x10 2048 1024 46/45
+    //   100 MB 4x8 2048 512 47/49;  113 MB 3x8 2048 768 53/51;  142 MB 1x6 5120 1536 71/58
+    // From 25 to 100 MB neither is ahead for all shapes, by 10 % or so either way (with few slots of
+    // large matrices the separate ones); 40 MB lies between.
     if (3 * n_slots * hidden * n_inter > 40'000'000) return false;
     return n_slots <= 65535 && tokens <= 65535 && hidden + 4 * fp8_blocks(hidden) <= 200 * 1024 &&
            down_smem(n_inter, top_k, down_groups(tokens, hidden)) <= 200 * 1024;

@@ -17,7 +17,8 @@
 // expert make one integer (32 bits where 16-bit logits are the keys, else 64), whose maximum over the
 // lanes is the choice with its tie rule: a round is a few shuffles, and the lane that held the
 // maximum looks again.  Up to eight choices come from sorting networks instead.  65536 tokens of 128 bf16
-// logits, 8 choices: 16 us (21 MB: 3 us at the copy's rate); fp32 34 us, by rounds 48.
+// logits, 8 choices: 16 us (21 MB: 3 us at the copy's rate); fp32 33 us, by rounds 48.  A warp's four tokens take 604
+// instructions, mostly integer maxima and minima, whose pipe the warps wait for.
 //
 // Otherwise one warp per token (65535 tokens of 1024 experts: 191 us).  The keys lie in shared
 // memory; each lane keeps the best key of its experts (every 32nd), and one round per chosen

@@ -11,10 +11,10 @@
 // division.  A non-finite value makes its block's scale infinite or NaN, and what is
 // divided by it 0 or NaN.
 //
-// Bound by instructions as much as by memory (65528 rows x 1408 gated bf16: 84 us, 5.5 TB/s;
-// rows of 2816 bf16 alone 124 us, 4.5 TB/s; fp32 6.3 and 6.6 TB/s).  CTAs that stay and fetch
-// ahead were slower for all but the last but one: small ones that come and go
-// hide the loads as well, with half the registers.
+// Bound by instructions as much as by memory (65528 rows x 1408 gated bf16: 78 us alone, 86 behind
+// other work, 5.9 and 5.4 TB/s, issue slots 69 % taken; rows of 2816 bf16 120 us, 4.6 TB/s, 71 %; fp32 6.3 and 6.6
+// TB/s).  CTAs that stay and fetch ahead took longer for 16-bit rows: small ones that come and
+// go hide the loads as well, with half the registers.
 #include "fp8_quant.cuh"
 #include "ft_internal.h"
 

@@ -635,8 +635,10 @@ FT_API int ft_quantize_fp8(const void* x, int32_t dtype, void* codes, float* sca
 /*
  * ft_act_mul_quantize_fp8 - the step between the two expert products: rows of
  * 2 * n_inter values (gate, then up) -> e4m3 codes and scales of
- * act(gate) * up (FT_ACT_*), evaluated in fp32.  h: [rows][2 * n_inter] of dtype;
- * the outputs are those of ft_quantize_fp8 for [rows][n_inter].
+ * act(gate) * up (FT_ACT_*).  That is evaluated in fp32, within some 10 * 2^-24 of
+ * its size (act(gate) is 0 where exp(-gate) overflows), so a code next to a tie, or
+ * a scale's last bits, can differ from another fp32 evaluation's.  h: [rows][2 *
+ * n_inter] of dtype; the outputs are those of ft_quantize_fp8 for [rows][n_inter].
  */
 FT_API int ft_act_mul_quantize_fp8(const void* h, int32_t dtype, void* codes, float* scales, int64_t rows,
                                    int64_t n_inter, int32_t act_kind, void* stream);
@@ -685,7 +687,7 @@ FT_API int ft_moe_combine(const void* rows, int32_t rows_dtype, const float* top
 /*
  * ft_moe_layer_fp8 - a whole expert layer: ft_moe_gate on the logits,
  * ft_quantize_fp8 of x, the routed product with w13 (gate rows, then up rows),
- * act(gate) * up quantized, the routed product with w2 and ft_moe_combine.
+ * ft_act_mul_quantize_fp8, the routed product with w2 and ft_moe_combine.
  * The gated values are fp32 when they are quantized.  The rows of the second
  * product stay fp32 until they are weighted where x is fp16; where it is bf16
  * they are rounded to bf16 first (not for a few tokens with small matrices).  Where
