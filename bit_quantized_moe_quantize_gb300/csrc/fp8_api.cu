@@ -184,10 +184,10 @@ int product_entry(const void* weights, const float* w_scales, const void* act, c
 // fp32 rows, and for the rows that the second product writes.  Codes lie in router order for wide tiles
 // (`spread`), else by token and by slot.
 //
-// The second product's rows are fp32 where y is fp16 and bf16 where y is bf16: they have no
-// fewer bits than y, and for bf16 half the bytes (8192 tokens of 8 slots, 2048 wide: 535 us, with fp32
-// rows 614).  Their rounding, at most 2^-8 of a row, is far below that of the codes, 2^-4, which both
-// products start from.
+// The second product's rows are fp32, but bf16 for wide tiles where y is bf16: no fewer bits than y
+// has, and half the bytes (8192 tokens of 8 slots, 2048 wide: 535 us, with fp32 rows 614; with
+// narrower tiles, 8, 64 and 512 tokens, fp32 rows take no longer).  Their rounding, at most 2^-8 of a
+// row, is far below that of the codes, 2^-4, which both products start from.
 struct LayerWs {
     Fp8Order order;
     size_t mq, ms, xq, xs, h, rows, total;
@@ -434,7 +434,7 @@ int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, int32_t
     p.act_rows = n_slots;
     p.nrows = hidden;
     p.ncols = n_inter;
-    const int rows_dtype = x_dtype == FT_DTYPE_F16 ? FT_DTYPE_F32 : FT_DTYPE_BF16;
+    const int rows_dtype = x_dtype == FT_DTYPE_BF16 && L.width == kWideTile ? FT_DTYPE_BF16 : FT_DTYPE_F32;
     if (int st = launch_fp8_product(p, L.width, ws + L.rows, rows_dtype, err, s)) return st;
     return launch_combine(ws + L.rows, rows_dtype, topk_weights, nullptr, y, x_dtype, tokens, top_k, hidden, s);
 }

@@ -688,11 +688,12 @@ FT_API int ft_moe_combine(const void* rows, int32_t rows_dtype, const float* top
  * ft_moe_layer_fp8 - a whole expert layer: ft_moe_gate on the logits,
  * ft_quantize_fp8 of x, the routed product with w13 (gate rows, then up rows),
  * ft_act_mul_quantize_fp8, the routed product with w2 and ft_moe_combine.
- * The gated values are fp32 when they are quantized.  The rows of the second
- * product stay fp32 until they are weighted where x is fp16; where it is bf16
- * they are rounded to bf16 first (not for a few tokens with small matrices).  Where
- * rows of a token nearly cancel and their sum needs more, ft_moe_fp8_fp8_slots with
- * fp32 rows and ft_moe_combine give it; the layer's results are theirs bit for bit.
+ * The gated values are fp32 when they are quantized, and the rows of the second
+ * product when they are weighted; only of bf16 layers with more than 52 slots per
+ * expert on average (tokens * top_k / n_experts) those rows are rounded to bf16
+ * first.  Where rows of a token nearly cancel and their sum needs more,
+ * ft_moe_fp8_fp8_slots with fp32 rows and ft_moe_combine give it; the layer's
+ * results are those of its operators called one by one, bit for bit.
  *   x       device, [tokens][hidden] of x_dtype (FT_DTYPE_F16 or FT_DTYPE_BF16),
  *           16-byte aligned; y the same shape and type, out
  *   w13     [n_experts][2 * n_inter][hidden] e4m3, s13 its scales

@@ -141,10 +141,10 @@ def apart_from_operators(ft, c, dt, kind, rows_dtype):
 @pytest.mark.parametrize("kind", [0, 1])
 @pytest.mark.parametrize("c", BATCHES)
 def test_layer_is_its_operators(ft, c, kind):
-    """The same bits as the operators called one by one, with the second product's rows in bf16, or (a
-    few tokens with small matrices) in fp32."""
-    few = c[0] * c[2] <= c[1] / 2
-    assert apart_from_operators(ft, c, torch.bfloat16, kind, torch.float32 if few else torch.bfloat16) == 0
+    """The same bits as the operators called one by one, with the second product's rows in fp32, or (more than
+    52 slots per expert) in bf16."""
+    many = c[0] * c[2] > 52 * c[1]
+    assert apart_from_operators(ft, c, torch.bfloat16, kind, torch.bfloat16 if many else torch.float32) == 0
 
 
 @pytest.mark.parametrize("kind", [0, 1])
