@@ -116,12 +116,10 @@ __global__ void __launch_bounds__(32 * kTokenWarps)
         }
         float acc[2 * kPairs] = {};
         dot_rows<2 * kPairs>(w, sw, hidden, row_smem, scales, acc);
-        static_assert(kPairs == 2, "a pair of values");
-        uint64_t a[1];
-        act_mul_pairs<1>({pair2(acc[0], acc[1])}, {pair2(acc[2], acc[3])}, kind, a);
-        const float2 v = split2(a[0]);
-        if (lane_id() < kPairs && i0 + static_cast<int32_t>(lane_id()) < n_inter)
-            mid[s * n_inter + i0 + lane_id()] = lane_id() == 0 ? v.x : v.y;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            if (lane_id() == static_cast<uint32_t>(i) && i0 + i < n_inter)
+                mid[s * n_inter + i0 + i] = act_mul_f32(acc[i], acc[kPairs + i], kind);
     }
 }
 

@@ -11,10 +11,10 @@
 // division.  A non-finite value makes its block's scale infinite or NaN, and what is
 // divided by it 0 or NaN.
 //
-// Bound by instructions as much as by memory (65528 rows x 1408 gated bf16: 78 us alone, 86 behind
-// other work, 5.9 and 5.4 TB/s, issue slots 69 % taken; rows of 2816 bf16 120 us, 4.6 TB/s, 71 %; fp32 6.3 and 6.6
-// TB/s).  CTAs that stay and fetch ahead took longer for 16-bit rows: small ones that come and
-// go hide the loads as well, with half the registers.
+// 16-bit rows are bound by instructions (65528 rows x 1408 gated bf16: 100 us, 4.6 TB/s, with an
+// activation within 10 * 2^-24 instead of act_mul_f32 78; rows of 2816 bf16 120 us, 4.6 TB/s, issue slots
+// 71 % taken), fp32 ones by memory (6.3 and 6.6 TB/s).  CTAs that stay and fetch ahead took longer
+// for 16-bit rows: small ones that come and go hide the loads as well, with half the registers.
 #include "fp8_quant.cuh"
 #include "ft_internal.h"
 
@@ -74,23 +74,10 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
 #pragma unroll
     for (int n = 0; n < kQuantHalves; ++n) {
         if (in[n]) {
-            if constexpr (GATED) {
-                uint64_t g[4], up[4], a[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    g[j] = pair2(to_f32<T>(raw[n][0][2 * j]), to_f32<T>(raw[n][0][2 * j + 1]));
-                    up[j] = pair2(to_f32<T>(raw[n][1][2 * j]), to_f32<T>(raw[n][1][2 * j + 1]));
-                }
-                act_mul_pairs<4>(g, up, ACT, a);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 x = split2(a[j]);
-                    v[n][2 * j] = x.x;
-                    v[n][2 * j + 1] = x.y;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[n][j] = to_f32<T>(raw[n][0][j]);
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (GATED) v[n][j] = act_mul_f32(to_f32<T>(raw[n][0][j]), to_f32<T>(raw[n][1][j]), ACT);
+                else v[n][j] = to_f32<T>(raw[n][0][j]);
             }
         }
     }

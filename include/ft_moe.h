@@ -635,10 +635,10 @@ FT_API int ft_quantize_fp8(const void* x, int32_t dtype, void* codes, float* sca
 /*
  * ft_act_mul_quantize_fp8 - the step between the two expert products: rows of
  * 2 * n_inter values (gate, then up) -> e4m3 codes and scales of
- * act(gate) * up (FT_ACT_*).  That is evaluated in fp32, within some 10 * 2^-24 of
- * its size (act(gate) is 0 where exp(-gate) overflows), so a code next to a tie, or
- * a scale's last bits, can differ from another fp32 evaluation's.  h: [rows][2 *
- * n_inter] of dtype; the outputs are those of ft_quantize_fp8 for [rows][n_inter].
+ * act(gate) * up (FT_ACT_*), evaluated in IEEE fp32 with expf: act(gate) = gate / (1 +
+ * exp(-z)), z = gate for SiLU and 2 sqrt(2/pi) (gate + 0.044715 gate^3) for the
+ * tanh form of GELU.  h: [rows][2 * n_inter] of dtype; the outputs are those of
+ * ft_quantize_fp8 for [rows][n_inter].
  */
 FT_API int ft_act_mul_quantize_fp8(const void* h, int32_t dtype, void* codes, float* scales, int64_t rows,
                                    int64_t n_inter, int32_t act_kind, void* stream);
@@ -689,11 +689,13 @@ FT_API int ft_moe_combine(const void* rows, int32_t rows_dtype, const float* top
  * ft_quantize_fp8 of x, the routed product with w13 (gate rows, then up rows),
  * ft_act_mul_quantize_fp8, the routed product with w2 and ft_moe_combine.
  * The gated values are fp32 when they are quantized, and the rows of the second
- * product when they are weighted; only of bf16 layers with more than 52 slots per
- * expert on average (tokens * top_k / n_experts) those rows are rounded to bf16
- * first.  Where rows of a token nearly cancel and their sum needs more,
- * ft_moe_fp8_fp8_slots with fp32 rows and ft_moe_combine give it; the layer's
- * results are those of its operators called one by one, bit for bit.
+ * product when they are weighted.  With more than 52 slots per expert on average
+ * (tokens * top_k / n_experts) two things change for speed: where n_inter % 128 ==
+ * 0, act(gate) * up is off by up to 10 * 2^-24 of its size, so that a code next to a
+ * tie can be its neighbour; and bf16 layers round the second product's rows to
+ * bf16.  But for that the layer's results are those of its operators called one by
+ * one, bit for bit; where a token's rows nearly cancel and their sum needs more,
+ * ft_moe_fp8_fp8_slots with fp32 rows and ft_moe_combine give it.
  *   x       device, [tokens][hidden] of x_dtype (FT_DTYPE_F16 or FT_DTYPE_BF16),
  *           16-byte aligned; y the same shape and type, out
  *   w13     [n_experts][2 * n_inter][hidden] e4m3, s13 its scales

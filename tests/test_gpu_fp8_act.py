@@ -89,6 +89,26 @@ def test_act_quantize(ft, kind, dtype, size):
 
 
 @pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("size", [3.0, 30.0])
+def test_act_quantize_is_the_formula_in_fp32(ft, kind, dtype, size):
+    """Codes and scales are those that elementary fp32 operations give, bit for bit."""
+    rows, I = 700, 400
+    h = (torch.randn(rows, 2 * I, generator=R.gen(rows + kind), device="cuda") * size).to(dtype)
+    q, s = ft.act_mul_quantize_fp8(h, kind)
+    g, u = h.float().chunk(2, 1)
+    z = g if kind == 0 else 1.5957691216057308 * (g + 0.044715 * g * g * g)
+    a = g / (1.0 + torch.exp(-z)) * u
+    nb = R.blocks(I)
+    b = torch.nn.functional.pad(a, (0, nb * 128 - I)).view(rows, nb, 128)
+    amax = b.abs().amax(2)
+    want = amax / torch.full_like(amax, 448.0)
+    assert torch.equal(s, want)
+    t = torch.where(want[:, :, None] > 0, b / want[:, :, None], 0.0)
+    assert torch.equal(R.decode(q), R.nearest_e4m3(t.double())[0].view(rows, -1)[:, :I])
+
+
+@pytest.mark.parametrize("kind", [0, 1])
 def test_act_limits(ft, kind):
     """Gates whose exponential or cube leaves fp32: act(g) is g or 0, and only what is not finite spoils its block."""
     big = 3e38

@@ -125,8 +125,8 @@ def test_product_nan_stays_in_its_row(ft, T):
     assert torch.equal(out, clean)
 
 
-def apart_from_operators(ft, c, dt, kind, rows_dtype):
-    """Elements of y that differ from those of the operators called one by one."""
+def with_operators(ft, c, dt, kind, rows_dtype):
+    """y of the layer, and of the operators called one by one."""
     T, E, k, H, I = c
     x, logits, w13, s13, w2, s2 = inputs(*c, dt)
     y, ids, w = ft.moe_layer_fp8(x, logits, w13, s13, w2, s2, k, kind)
@@ -135,20 +135,26 @@ def apart_from_operators(ft, c, dt, kind, rows_dtype):
     h = ft.moe_fp8_fp8(w13, s13, *ft.quantize_fp8(x), ids)
     mid = ft.act_mul_quantize_fp8(h.view(-1, 2 * I), kind)
     rows = ft.moe_fp8_fp8_slots(w2, s2, *mid, ids, out_dtype=rows_dtype)
-    return int((y != ft.moe_combine(rows, w, out_dtype=dt)).sum())
+    return y, ft.moe_combine(rows, w, out_dtype=dt)
 
 
 @pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("c", BATCHES)
-def test_layer_is_its_operators(ft, c, kind):
-    """The same bits as the operators called one by one, with the second product's rows in fp32, or (more than
-    52 slots per expert) in bf16."""
+def test_layer_is_its_operators(ft, c, dt, kind):
+    """The same bits as the operators called one by one, with the second product's rows in fp32, or (bf16 layers with
+    more than 52 slots per expert) in bf16.
+
+    With more than 52 slots per expert and n_inter % 128 == 0 the first product quantizes act(gate) * up itself, off by
+    up to 10 * 2^-24: of values and scales together at most 2 * 10 * 2^-24 * 16 = 2e-5 lie so near a tie (16 to a
+    factor of 2) that their code turns, one value in 66 tokens of 768, which moves a row by an eighth of one of its
+    768 terms, some 0.004 of it: sqrt(1 / 66) * 0.004 = 5e-4 of the norm; scales that are one bit off turn roundings of
+    rows and y, far less.  2^-10 covers both."""
     many = c[0] * c[2] > 52 * c[1]
-    assert apart_from_operators(ft, c, torch.bfloat16, kind, torch.bfloat16 if many else torch.float32) == 0
-
-
-@pytest.mark.parametrize("kind", [0, 1])
-@pytest.mark.parametrize("c", BATCHES)
-def test_fp16_layer_is_its_operators(ft, c, kind):
-    """The same of fp16 layers, whose rows stay fp32: bf16 ones would have fewer bits than y."""
-    assert apart_from_operators(ft, c, torch.float16, kind, torch.float32) == 0
+    y, want = with_operators(ft, c, dt, kind, torch.bfloat16 if many and dt == torch.bfloat16 else torch.float32)
+    if not (many and c[4] % 128 == 0):
+        assert torch.equal(y, want)
+        return
+    off = (y.double() - want.double()).abs()
+    assert float(off.norm() / want.double().norm()) < 2.0 ** -10
+    assert (off.amax(1) <= 2.0 ** -5 * want.double().abs().amax(1)).all()
