@@ -11,9 +11,9 @@
 // division.  A non-finite value makes its block's scale infinite or NaN, and what is
 // divided by it 0 or NaN.
 //
-// 16-bit rows are bound by instructions (65528 rows x 1408 gated bf16: 100 us, 4.6 TB/s, with an
-// activation within 10 * 2^-24 instead of act_mul_f32 78; rows of 2816 bf16 120 us, 4.6 TB/s, issue slots
-// 71 % taken), fp32 ones by memory (6.3 and 6.6 TB/s).  CTAs that stay and fetch ahead took longer
+// 16-bit rows are bound by instructions (65528 rows x 1408 gated bf16: 100 us, 4.6 TB/s, issue slots
+// 85 % taken, with an activation within 10 * 2^-24 instead of act_mul_f32 78; rows of 2816 bf16 120 us,
+// 4.4 TB/s, 71 %), fp32 ones by memory (6.3 and 6.6 TB/s).  CTAs that stay and fetch ahead took longer
 // for 16-bit rows: small ones that come and go hide the loads as well, with half the registers.
 #include "fp8_quant.cuh"
 #include "ft_internal.h"
