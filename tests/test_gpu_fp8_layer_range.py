@@ -158,3 +158,29 @@ def test_layer_is_its_operators(ft, c, dt, kind):
     off = (y.double() - want.double()).abs()
     assert float(off.norm() / want.double().norm()) < 2.0 ** -10
     assert (off.amax(1) <= 2.0 ** -5 * want.double().abs().amax(1)).all()
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("up", [6, 21, 60, 100])
+@pytest.mark.parametrize("c", BATCHES)
+def test_layer_of_far_gates(ft, c, up, kind):
+    """Gates 2^up of their usual size: act(g) is g or 0, also where g^3 or g log2(e) leaves fp32; the second matrix
+    undoes the size.  As near to the operators as test_layer_is_its_operators says."""
+    T, E, k, H, I = c
+    x, logits, w13, s13, w2, s2 = inputs(*c)
+    far = s13.clone()
+    far[:, :I // 128] *= 2.0 ** up              # (rows of a block that gate and up share stay as they are)
+    s2 = s2 * 2.0 ** -up
+    y, ids, w = ft.moe_layer_fp8(x, logits, w13, far, w2, s2, k, kind)
+    h = ft.moe_fp8_fp8(w13, far, *ft.quantize_fp8(x), ids)
+    mid = ft.act_mul_quantize_fp8(h.view(-1, 2 * I), kind)
+    many = T * k > 52 * E
+    rows = ft.moe_fp8_fp8_slots(w2, s2, *mid, ids, out_dtype=torch.bfloat16 if many else torch.float32)
+    want = ft.moe_combine(rows, w, out_dtype=x.dtype)
+    assert torch.isfinite(y).all() and float(want.abs().max()) > 0
+    if not (many and I % 128 == 0):
+        assert torch.equal(y, want)
+        return
+    off = (y.double() - want.double()).abs()
+    assert float(off.norm() / want.double().norm()) < 2.0 ** -10
+    assert (off.amax(1) <= 2.0 ** -5 * want.double().abs().amax(1)).all()
