@@ -33,7 +33,8 @@ EXPORTS = ("ft_quantize_q8_1", "ft_moe_route_offsets", "ft_moe_q4_0_q8_1", "ft_m
            "ft_repack_q4_0_soa", "ft_debug_wait_timeout", "ft_moe_q4_0_q8_1_act", "ft_moe_ffn_reserve",
            "ft_moe_q4_0_fp16", "ft_debug_stream_read", "ft_moe_gate", "ft_quantize_fp8", "ft_act_mul_quantize_fp8",
            "ft_moe_fp8_workspace_bytes", "ft_moe_fp8_fp8", "ft_moe_fp8_fp8_slots", "ft_matmul_fp8_fp8",
-           "ft_moe_combine", "ft_moe_layer_fp8_workspace_bytes", "ft_moe_layer_fp8")
+           "ft_moe_combine", "ft_moe_layer_fp8_workspace_bytes", "ft_moe_layer_fp8",
+           "ft_moe_balance_workspace_bytes", "ft_moe_balance_loss", "ft_moe_gate_backward", "ft_moe_combine_backward")
 
 
 class FtError(RuntimeError):
@@ -104,6 +105,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.ft_moe_fp8_workspace_bytes.restype = sz
         L.ft_moe_layer_fp8_workspace_bytes.argtypes = [i64, i32, i32, i64, i64]
         L.ft_moe_layer_fp8_workspace_bytes.restype = sz
+        L.ft_moe_balance_workspace_bytes.argtypes = [i64, i32, i32]
+        L.ft_moe_balance_workspace_bytes.restype = sz
+        L.ft_moe_balance_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp]
+        L.ft_moe_gate_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, f32, i32, vp]
+        L.ft_moe_combine_backward.argtypes = [vp, i32, vp, i32, vp, vp, vp, i64, i32, i64, vp]
         for name in EXPORTS:
             getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
         L.ft_moe_workspace_bytes.restype = ctypes.c_size_t
@@ -692,6 +698,106 @@ def moe_layer_fp8(x, logits, w13, s13, w2, s2, top_k, act_kind=0, score="softmax
     if st:
         _check(st)
     return out, ids, weights
+
+
+# ------------------------------------------------- adapting a layer of experts
+def _offsets_of(seq_offsets, dev):
+    """(pointer, number of sequences) of the offsets of packed sequences, None: one sequence of all rows."""
+    if seq_offsets is None:
+        return None, 1
+    p = _ptr(seq_offsets, "seq_offsets", 1, dev)
+    if seq_offsets.dtype != _i32:
+        raise TypeError(f"seq_offsets must be {_i32}, got {seq_offsets.dtype}")
+    n = seq_offsets.shape[0] - 1
+    if n < 1:
+        raise ValueError("seq_offsets must hold the start of every sequence and the end of the last")
+    return p, n
+
+
+def _ids_of(topk_ids, tokens, dev):
+    """(pointer, top_k) of the chosen experts of `tokens` rows."""
+    p = _ptr(topk_ids, "topk_ids", 2, dev)
+    if topk_ids.dtype != _i32:
+        raise TypeError(f"topk_ids must be {_i32}, got {topk_ids.dtype}")
+    if topk_ids.shape[0] != tokens:
+        raise ValueError(f"topk_ids must have {tokens} rows, got {tuple(topk_ids.shape)}")
+    return p, topk_ids.shape[1]
+
+
+def moe_balance_loss(logits, topk_ids, score="softmax", seq_offsets=None):
+    """Load-balance loss of a router (ft_moe_balance_loss): logits [T, E] (rows may lie apart) and the chosen
+    topk_ids [T, k] -> (loss fp32 [], counts int32 [S, E], seq_scale fp32 [S]).  seq_offsets int32 [S + 1]: where
+    each packed sequence starts, and where the last ends; None: one sequence.  counts and seq_scale are what
+    moe_gate_backward needs for the loss' gradient."""
+    L = _lib_ready()
+    T, E, stride, dev = _logits_of(logits)
+    code = _dtype_code(logits.dtype, "logits")
+    pi, k = _ids_of(topk_ids, T, dev)
+    po, S = _offsets_of(seq_offsets, dev)
+    device = logits.device
+    loss = _empty((), dtype=_f32, device=device)
+    counts = _empty((S, E), dtype=_i32, device=device)
+    seq_scale = _empty((S,), dtype=_f32, device=device)
+    n = L.ft_moe_balance_workspace_bytes(T, E, S)
+    ws, pws = _workspace(n, logits)
+    st = L.ft_moe_balance_loss(logits.data_ptr(), code, stride, pi, po, loss.data_ptr(), counts.data_ptr(),
+                               seq_scale.data_ptr(), T, E, k, _score_code(score), S, pws, n, _stream_of(dev))
+    if st:
+        _check(st)
+    return loss, counts, seq_scale
+
+
+def moe_gate_backward(logits, topk_ids, grad_weights=None, score="softmax", renormalize=True, scale=1.0, counts=None,
+                      seq_scale=None, grad_loss=None, seq_offsets=None, grad_logits=None):
+    """Gradient of the router (ft_moe_gate_backward) -> grad_logits [T, E] of the logits' type: of moe_gate's
+    weights (grad_weights fp32 [T, k]), of moe_balance_loss (its counts and seq_scale, and grad_loss fp32 of
+    one element), or of both at once.  score, renormalize, scale: as moe_gate had them."""
+    L = _lib_ready()
+    T, E, stride, dev = _logits_of(logits)
+    code = _dtype_code(logits.dtype, "logits")
+    pi, k = _ids_of(topk_ids, T, dev)
+    pw = None if grad_weights is None else _typed_ptr(grad_weights, "grad_weights", _f32, (T, k), dev)
+    pc = ps = pl = po = None
+    S = 1
+    if counts is not None or seq_scale is not None or grad_loss is not None:
+        if counts is None or seq_scale is None or grad_loss is None:
+            raise ValueError("counts, seq_scale and grad_loss come together")
+        po, S = _offsets_of(seq_offsets, dev)
+        pc = _typed_ptr(counts, "counts", _i32, (S, E), dev)
+        ps = _typed_ptr(seq_scale, "seq_scale", _f32, (S,), dev)
+        pl = _typed_ptr(grad_loss, "grad_loss", _f32, (1,) if getattr(grad_loss, "ndim", 0) else (), dev)
+    grad_logits = _out(grad_logits, "grad_logits", (T, E), logits.dtype, logits, dev)
+    st = L.ft_moe_gate_backward(logits.data_ptr(), code, stride, pi, pw, pc, ps, pl, po, grad_logits.data_ptr(), T, E, k,
+                                _score_code(score), 1 if renormalize else 0, scale, S, _stream_of(dev))
+    if st:
+        _check(st)
+    return grad_logits
+
+
+def moe_combine_backward(grad_out, rows, topk_weights, need_rows=True, need_weights=True, grad_rows=None,
+                         grad_weights=None):
+    """Gradients of moe_combine (ft_moe_combine_backward): grad_out [T, N] fp32 / fp16 / bf16, rows [T, k, N] fp32 /
+    bf16 and topk_weights fp32 [T, k] as it had them -> (grad_rows [T, k, N] of the rows' type, grad_weights fp32
+    [T, k]); None where not needed."""
+    L = _lib_ready()
+    pr = _ptr(rows, "rows", 3)
+    T, k, N = rows.shape
+    dev = rows.get_device()
+    code = _dtype_code(rows.dtype, "rows", (F32, BF16))
+    pw = _typed_ptr(topk_weights, "topk_weights", _f32, (T, k), dev)
+    pg = _ptr(grad_out, "grad_out", 2, dev)
+    gcode = _dtype_code(grad_out.dtype, "grad_out")
+    if grad_out.shape != (T, N):
+        raise ValueError(f"grad_out must have shape {(T, N)}, got {tuple(grad_out.shape)}")
+    if need_rows or grad_rows is not None:
+        grad_rows = _out(grad_rows, "grad_rows", (T, k, N), rows.dtype, rows, dev)
+    if need_weights or grad_weights is not None:
+        grad_weights = _out(grad_weights, "grad_weights", (T, k), _f32, rows, dev)
+    st = L.ft_moe_combine_backward(pg, gcode, pr, code, pw, None if grad_rows is None else grad_rows.data_ptr(),
+                                   None if grad_weights is None else grad_weights.data_ptr(), T, k, N, _stream_of(dev))
+    if st:
+        _check(st)
+    return grad_rows, grad_weights
 
 
 def workspace_bytes(tokens, top_k, n_experts, nrows, ncols) -> int:

@@ -244,4 +244,33 @@ int launch_fp8_token_layer(const void* x, int x_dtype, const uint8_t* w13, const
 // Pitch of rows of scales in router order.
 inline int32_t fp8_scale_pitch(int64_t ncols) { return static_cast<int32_t>(((ncols + 127) / 128 + 3) / 4 * 4); }
 
+
+// ------------------------------------------------- training the router
+struct BalanceParams {
+    int64_t tokens;
+    int32_t n_experts, top_k, score, n_seqs;
+};
+constexpr int64_t kBalanceCtas = 1024;      // CTAs of the loss' first launch at most
+size_t balance_workspace(int64_t tokens, int32_t n_experts, int32_t n_seqs);
+int launch_balance(const BalanceParams& p, const void* logits, int dtype, int64_t stride, const int32_t* ids,
+                   const int32_t* offsets, float* loss, int32_t* counts, float* seq_scale, uint8_t* ws, uint32_t* err,
+                   cudaStream_t s);
+
+struct GateGradParams {
+    int64_t tokens;
+    int32_t n_experts, top_k, score, renormalize, n_seqs;
+    float scale;
+    const int32_t* ids;
+    const float* grad_weights;      // null: none arrives at the weights
+    const int32_t* counts;          // null: none at the loss
+    const float *seq_scale, *grad_loss;
+    const int32_t* offsets;         // null: one sequence
+};
+int launch_gate_grad(const GateGradParams& p, const void* logits, int dtype, int64_t stride, void* out, uint32_t* err,
+                     cudaStream_t s);
+
+// grad_rows or grad_weights may be null
+int launch_combine_grad(const void* dy, int dy_dtype, const void* rows, int rows_dtype, const float* weights, void* grad_rows,
+                        float* grad_weights, int64_t tokens, int32_t top_k, int64_t ncols, cudaStream_t s);
+
 }  // namespace ft

@@ -1,0 +1,221 @@
+// Gradient of the router: of its weights, and of the load-balance loss, to the logits in one pass.
+//
+//   s   scores of a row (softmax or sigmoid; 0 where masked), W = sum_j s[id_j], gw_j the weights' gradients
+//   h_j scale gw_j; with renormalised weights scale / max(W, 1e-30) (gw_j - [W > 1e-30] sum_i gw_i s[id_i] / W)
+//   a_e grad_loss seq_scale c_se, the loss' gradient to p_te
+//   softmax:  d l_e = p_e (H_e + a_e - sum_j h_j s[id_j] - sum_i a_i p_i),  H_e = sum of h_j over id_j = e
+//             (the sum of h_j s[id_j] is 0 where the weights are renormalised)
+//   sigmoid:  d l_e = s_e (1 - s_e) H_e + p_e (1 - s_e) (a_e - sum_i a_i p_i),  p = s / max(sum, 1e-30)
+//
+// Memory-bound: a row is read once, by the lanes that hold its experts, and written once.  The slots' parts
+// lie in a row of shared memory that their lanes add to and the experts' lanes read; ids that repeat in a
+// row are added in the order of the slots.
+#include <type_traits>
+
+#include "router_rows.cuh"
+#include "ft_internal.h"
+#include "launch.cuh"
+
+namespace ft {
+
+namespace {
+
+struct GateGradArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* grad_weights;   // null: no gradient arrives at the weights
+    const int32_t* counts;       // null: none at the loss
+    const float* seq_scale;
+    const float* grad_loss;
+    const int32_t* offsets;
+    void* out;
+    uint32_t* err;
+    int64_t tokens, stride;
+    int32_t n_experts, top_k, score, renormalize, n_seqs;
+    float scale;
+    bool wide, wide_out;
+};
+
+template <typename T, int L, int STEPS>
+__global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradArgs a) {
+    using G = RowGroup<L>;
+    constexpr int WIDTH = 8 * L * STEPS, LANES = L < 32 ? L : 32;      // LANES: lanes that share the slots
+    __shared__ __align__(16) float extra_all[G::kRows * WIDTH];
+    __shared__ float part[kRowThreads / 32];
+    const G g{part};
+    const int32_t E = a.n_experts, k = a.top_k;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * G::kRows + G::row();
+    const bool there = t0 < a.tokens;
+    const int64_t t = there ? t0 : a.tokens - 1;
+    const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+    float* extra = extra_all + G::row() * WIDTH;
+    float p[STEPS][8];
+    load_logits<T, L, STEPS>(row, E, a.wide, p);
+    float rest[STEPS][8];      // sigmoid: 1 - s
+    const bool soft = a.score == FT_SCORE_SOFTMAX;
+    if (!soft) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rest[i][j] = p[i][j] > -INFINITY ? sigmoid_of(-p[i][j]) : 0.0f;
+    }
+    const RowScale sc = row_scores<L, STEPS>(g, a.score, p);
+    float dots = 0.0f;         // softmax: sum over slots of h_j s[id_j]
+
+    if (a.grad_weights) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            float4* z = reinterpret_cast<float4*>(extra + first_expert<L>(i));
+            z[0] = z[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        g.sync();
+        // the first LANES lanes of the group take a slot each (a whole CTA's other warps take none)
+        const bool mine = L <= 32 || threadIdx.x < 32;
+        const int32_t lane = static_cast<int32_t>(G::lane());
+        auto slot = [&](int32_t j, float& s, float& r, float& gw) {      // a slot's expert, score, 1 - score, gradient
+            s = r = gw = 0.0f;
+            int32_t e = mine && there && j < k ? __ldg(a.ids + t * k + j) : -1;
+            if (e < -1 || e >= E) {
+                if (mine && there && j < k) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
+                e = -1;
+            }
+            if (e >= 0) {
+                const float l = to_f32<T>(row[e]);
+                if (!(l > -INFINITY)) return -1;      // masked: no part in anything
+                s = soft ? soft_exp(l, sc.top) * sc.inv : sigmoid_of(l);
+                r = soft ? 1.0f : sigmoid_of(-l);
+                gw = __ldg(a.grad_weights + t * k + j);
+            }
+            return e;
+        };
+        float W = 0.0f, m = 0.0f, s, r, gw;
+        for (int32_t j0 = 0; j0 < k; j0 += LANES) {
+            slot(j0 + lane, s, r, gw);
+            W += s;
+            m = fmaf(gw, s, m);
+        }
+        W = g.sum(W);
+        m = g.sum(m);
+        const bool spread = a.renormalize && W > kScoreTiny;
+        const float c = a.renormalize ? __fdiv_rn(a.scale, fmaxf(W, kScoreTiny)) : a.scale;
+        const float mean = spread ? __fdiv_rn(m, W) : 0.0f;
+        for (int32_t j0 = 0; j0 < k; j0 += LANES) {
+            const int32_t e = slot(j0 + lane, s, r, gw);
+            const float h = c * (gw - mean), d = (soft ? s : s * r) * h;
+            if (e >= 0) dots = fmaf(h, s, dots);
+            if (mine) {
+                // lanes of this row with the same expert add in turn, lowest first
+                const uint32_t same = __match_any_sync(0xFFFFFFFFu, e < 0 ? -1 - static_cast<int32_t>(lane_id())
+                                                                           : e * G::kRows + static_cast<int32_t>(G::row()));
+                const int32_t turn = __popc(same & ((1u << lane_id()) - 1u));
+                const int32_t turns = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(turn));
+                for (int32_t i = 0; i <= turns; ++i) {
+                    if (e >= 0 && turn == i) extra[e] += d;
+                    __syncwarp();
+                }
+            }
+        }
+        dots = g.sum(dots);      // by all lanes: rows of a warp may differ in what follows
+        if (!soft || spread) dots = 0.0f;
+        g.sync();
+    }
+
+    float coef = 0.0f, mean = 0.0f;      // the loss' part
+    const int32_t* count = nullptr;
+    if (a.counts) {
+        int32_t seq = 0;
+        bool inside = true;
+        if (a.offsets) {
+            seq = seq_of(a.offsets, a.n_seqs, t);
+            inside = seq_start(a.offsets, seq, a.tokens) <= t && t < seq_start(a.offsets, seq + 1, a.tokens);
+        }
+        const float inv = soft ? 1.0f : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
+        coef = inside ? __ldg(a.grad_loss) * __ldg(a.seq_scale + seq) * inv : 0.0f;
+        count = a.counts + static_cast<int64_t>(seq) * E;
+    }
+    float c[STEPS][8];
+    if (count) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int32_t e0 = first_expert<L>(i);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                c[i][j] = e0 + j < E ? static_cast<float>(__ldg(count + e0 + j)) : 0.0f;
+                mean = fmaf(c[i][j], p[i][j], mean);
+            }
+        }
+        mean = g.sum(mean);
+        if (!soft) mean = sc.sum > kScoreTiny ? __fdividef(mean, sc.sum) : 0.0f;
+    }
+    if (!there) return;
+    T* out = static_cast<T*>(a.out) + t * E;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int32_t e0 = first_expert<L>(i);
+        if (e0 >= E) break;
+        __align__(16) T o[8];
+        float x[8] = {};      // the slots' part
+        if (a.grad_weights) {
+            const float4 x0 = reinterpret_cast<const float4*>(extra + e0)[0], x1 = reinterpret_cast<const float4*>(extra + e0)[1];
+            x[0] = x0.x, x[1] = x0.y, x[2] = x0.z, x[3] = x0.w;
+            x[4] = x1.x, x[5] = x1.y, x[6] = x1.z, x[7] = x1.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v = count ? coef * (c[i][j] - mean) : 0.0f;
+            if (soft) v -= dots;
+            v = p[i][j] > 0.0f ? v * p[i][j] : 0.0f;      // a masked expert, or one too far away, takes none
+            if (!soft) v *= rest[i][j];
+            v += x[j];
+            o[j] = from_f32<T>(v);
+        }
+        if (a.wide_out && e0 + 8 <= E) {
+#pragma unroll
+            for (int w = 0; w < static_cast<int>(sizeof(o) / 16); ++w)
+                reinterpret_cast<uint4*>(out + e0)[w] = reinterpret_cast<const uint4*>(o)[w];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e0 + j < E) out[e0 + j] = o[j];
+        }
+    }
+}
+
+}  // namespace
+
+int launch_gate_grad(const GateGradParams& p, const void* logits, int dtype, int64_t stride, void* out, uint32_t* err,
+                     cudaStream_t s) {
+    GateGradArgs a{};
+    a.logits = logits;
+    a.ids = p.ids;
+    a.grad_weights = p.grad_weights;
+    a.counts = p.counts;
+    a.seq_scale = p.seq_scale;
+    a.grad_loss = p.grad_loss;
+    a.offsets = p.offsets;
+    a.out = out;
+    a.err = err;
+    a.tokens = p.tokens;
+    a.stride = stride;
+    a.n_experts = p.n_experts;
+    a.top_k = p.top_k;
+    a.score = p.score;
+    a.renormalize = p.renormalize;
+    a.n_seqs = p.n_seqs;
+    a.scale = p.scale;
+    const int size = dtype == FT_DTYPE_F32 ? 4 : 2;
+    a.wide = stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+    a.wide_out = static_cast<int64_t>(p.n_experts) * size % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    return with_row_lanes(p.n_experts, [&](auto lanes, auto steps) {
+        constexpr int L = decltype(lanes)::value, N = decltype(steps)::value, ROWS = kRowThreads / L;
+        const int64_t ctas = (p.tokens + ROWS - 1) / ROWS;
+        if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "too many tokens for one launch");
+        const dim3 grid(static_cast<unsigned>(ctas)), block(kRowThreads);
+        if (dtype == FT_DTYPE_F32) gate_grad_kernel<float, L, N><<<grid, block, 0, s>>>(a);
+        else if (dtype == FT_DTYPE_F16) gate_grad_kernel<__half, L, N><<<grid, block, 0, s>>>(a);
+        else gate_grad_kernel<__nv_bfloat16, L, N><<<grid, block, 0, s>>>(a);
+        return check_launch("gate_grad_kernel", grid, block, 0);
+    });
+}
+
+}  // namespace ft

@@ -1,0 +1,154 @@
+// Rows of router logits in registers, for the kernels that need every expert's score: a group of L lanes
+// holds a row of up to 8 * L * STEPS experts, eight neighbouring ones per lane and step.
+#pragma once
+
+#include "fp8_common.cuh"
+
+namespace ft {
+
+constexpr int kRowThreads = 256;      // of a CTA
+constexpr float kScoreTiny = 1e-30f;  // smallest sum that scores are divided by
+
+// Lanes that share a row: up to 32 neighbouring ones of a warp, or the whole CTA.
+template <int L>
+struct RowGroup {
+    static_assert(L <= 32 || L == kRowThreads, "lanes of a warp, or the CTA");
+    static constexpr int kRows = kRowThreads / L;      // rows of a CTA at once
+    float* part;      // one word per warp in shared memory (used where L is the CTA)
+
+    __device__ __forceinline__ static uint32_t lane() { return threadIdx.x % L; }
+    __device__ __forceinline__ static uint32_t row() { return threadIdx.x / L; }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (L <= 32) __syncwarp();
+        else __syncthreads();
+    }
+    template <typename F>
+    __device__ __forceinline__ float reduce(float v, const F& f) const {
+#pragma unroll
+        for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        if constexpr (L > 32) {
+            __syncthreads();
+            if ((threadIdx.x & 31u) == 0) part[threadIdx.x >> 5] = v;
+            __syncthreads();
+            v = part[0];
+#pragma unroll
+            for (int w = 1; w < L / 32; ++w) v = f(v, part[w]);
+        }
+        return v;
+    }
+    __device__ __forceinline__ float max(float v) const {
+        return reduce(v, [](float a, float b) { return fmaxf(a, b); });
+    }
+    __device__ __forceinline__ float sum(float v) const {
+        return reduce(v, [](float a, float b) { return a + b; });
+    }
+};
+
+// The first expert of a lane's step.
+template <int L>
+__device__ __forceinline__ int32_t first_expert(int step) {
+    return (step * L + static_cast<int32_t>(RowGroup<L>::lane())) * 8;
+}
+
+// A lane's logits of a row; masked experts (-inf, NaN) and those past the last are -inf.
+// wide: rows start at whole 16-byte words.
+template <typename T, int L, int STEPS>
+__device__ __forceinline__ void load_logits(const T* row, int32_t E, bool wide, float (&l)[STEPS][8]) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int32_t e0 = first_expert<L>(s);
+        if (wide && e0 + 8 <= E) {
+            load_vec<T, 8>(row + e0, l[s]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l[s][i] = e0 + i < E ? to_f32<T>(row[e0 + i]) : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[s][i] = l[s][i] > -INFINITY ? l[s][i] : -INFINITY;
+    }
+}
+
+__device__ __forceinline__ float sigmoid_of(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+
+// What a row's scores need beside its logits: for softmax the largest logit and the reciprocal of the
+// sum of exponentials (experts at +inf share the weight); for the sigmoid the sum of the scores.
+struct RowScale {
+    float top, inv;      // softmax
+    float sum;           // sigmoid
+    bool any;            // some expert is there
+};
+
+__device__ __forceinline__ float soft_exp(float l, float top) {
+    if (!(l > -INFINITY)) return 0.0f;
+    return l == top ? 1.0f : expf(l - top);
+}
+
+// In place: logits -> softmax probabilities, or sigmoid scores (0 where masked).
+template <int L, int STEPS>
+__device__ __forceinline__ RowScale row_scores(const RowGroup<L>& g, int32_t score, float (&l)[STEPS][8]) {
+    RowScale r{-INFINITY, 0.0f, 0.0f, false};
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, l[s][i]);
+    r.top = g.max(top);
+    r.any = r.top > -INFINITY;
+    if (score == FT_SCORE_SOFTMAX) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                l[s][i] = soft_exp(l[s][i], r.top);
+                sum += l[s][i];
+            }
+        sum = g.sum(sum);
+        r.inv = r.any ? __frcp_rn(sum) : 0.0f;      // the largest logit alone makes the sum 1 or more
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l[s][i] *= r.inv;
+    } else {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                l[s][i] = l[s][i] > -INFINITY ? sigmoid_of(l[s][i]) : 0.0f;
+                sum += l[s][i];
+            }
+        r.sum = g.sum(sum);
+    }
+    return r;
+}
+
+// Sequences of packed rows: offsets[0 .. n] ascending, or null: one sequence of all rows.  Whatever the
+// offsets hold, what comes back lies in [0, rows].
+__device__ __forceinline__ int64_t seq_start(const int32_t* offsets, int32_t s, int64_t rows) {
+    if (!offsets) return s == 0 ? 0 : rows;
+    const int64_t o = __ldg(offsets + s);
+    return o < 0 ? 0 : o < rows ? o : rows;
+}
+
+// The last sequence that starts at or before row r (0 if none does).
+__device__ __forceinline__ int32_t seq_of(const int32_t* offsets, int32_t n, int64_t r) {
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (__ldg(offsets + mid) <= r) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Calls f.template operator()<L, STEPS>() for the lanes per row that E experts take.
+template <typename F>
+int with_row_lanes(int32_t E, const F& f) {
+    if (E <= 32) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+    if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+    if (E <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+    if (E <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+    if (E <= 512) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, kRowThreads>{}, std::integral_constant<int, 2>{});
+}
+
+}  // namespace ft

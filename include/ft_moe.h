@@ -714,6 +714,70 @@ FT_API int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, 
                             int32_t renormalize, float scale, int32_t act_kind, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------ adapting a layer of experts
+ *
+ * Training of the router beside expert matrices that stay as they are: the load-balance loss
+ * (ft_moe_balance_loss) and the gradients of the router (ft_moe_gate_backward) and of the weighted
+ * sum (ft_moe_combine_backward).  Conventions and errors are those of the FP8 expert-layer operators
+ * above.  No sum depends on the order in which the GPU works: a call repeated gives the same bits. */
+
+/*
+ * ft_moe_balance_loss - how unevenly a router loads its experts, over packed sequences, and the
+ * experts' counts.  Sequence s holds the rows seq_offsets[s] .. seq_offsets[s + 1] - 1.  A row
+ * counts if one of its logits is not masked (-inf or NaN); n_s rows of sequence s do, and S' sequences
+ * have such rows.
+ *   p_te   = softmax(logits)_e, or sigmoid(logits)_e / max(sum over e, 1e-30)
+ *   counts[s][e] = slots of the sequence's rows whose id is e
+ *   seq_scale[s] = n_experts / (top_k n_s^2 S'), 0 where n_s = 0
+ *   loss   = sum_s seq_scale[s] sum_e counts[s][e] sum_t p_te        (1 where the load is even)
+ * Rows before the first and behind the last sequence take no part.  counts are the derivative's
+ * constants: the loss' gradient goes through p (ft_moe_gate_backward).
+ *
+ *   logits      as in ft_moe_gate
+ *   topk_ids    device int32 [tokens][top_k]; -1: no expert.  Ids outside [-1, n_experts) are left out
+ *               and raise FT_DEVERR_BAD_EXPERT_ID
+ *   seq_offsets device int32 [n_seqs + 1], ascending, or NULL: one sequence of all rows (n_seqs 1)
+ *   loss device fp32 [1] out; counts int32 [n_seqs][n_experts] out; seq_scale fp32 [n_seqs] out
+ * ft_moe_balance_workspace_bytes returns 0 for invalid arguments.
+ */
+FT_API size_t ft_moe_balance_workspace_bytes(int64_t tokens, int32_t n_experts, int32_t n_seqs);
+FT_API int ft_moe_balance_loss(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* topk_ids,
+                               const int32_t* seq_offsets, float* loss, int32_t* counts, float* seq_scale,
+                               int64_t tokens, int32_t n_experts, int32_t top_k, int32_t score, int32_t n_seqs,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ft_moe_gate_backward - the gradient of ft_moe_gate's weights, of the load-balance loss, or of both,
+ * with respect to the logits, in fp32, rounded once to the logits' type.  The choice of the experts is a
+ * constant; a bias and groups steer the choice alone, and are not needed here.
+ *
+ *   logits, topk_ids, score, renormalize, scale   as ft_moe_gate had and gave them.  An id of -1, or of
+ *                a masked expert, takes no part (its weight's gradient is not used); other ids outside
+ *                [0, n_experts) neither, and raise FT_DEVERR_BAD_EXPERT_ID; one that repeats counts as often
+ *   grad_weights device fp32 [tokens][top_k], or NULL: nothing arrives at the weights
+ *   counts, seq_scale   what ft_moe_balance_loss gave for these rows, grad_loss device fp32 [1] the
+ *                gradient that arrives at the loss; or all three NULL (seq_offsets is not read then)
+ *   grad_logits  device, [tokens][n_experts] of dtype out; 0 for masked experts
+ */
+FT_API int ft_moe_gate_backward(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* topk_ids,
+                                const float* grad_weights, const int32_t* counts, const float* seq_scale,
+                                const float* grad_loss, const int32_t* seq_offsets, void* grad_logits, int64_t tokens,
+                                int32_t n_experts, int32_t top_k, int32_t score, int32_t renormalize, float scale,
+                                int32_t n_seqs, void* stream);
+
+/*
+ * ft_moe_combine_backward - the gradients of ft_moe_combine:
+ *   grad_rows[t][j][c] = topk_weights[t][j] * grad_y[t][c], rounded once
+ *   grad_weights[t][j] = sum_c grad_y[t][c] * rows[t][j][c], in fp32
+ * Both are 0 for a row whose weight is 0, which is not read.  (grad_y itself is the gradient of `add`.)
+ *   grad_y  device, [tokens][ncols] of y_dtype; rows, topk_weights as ft_moe_combine had them;
+ *   grad_rows  [tokens][top_k][ncols] of rows_dtype out, or NULL; grad_weights fp32 [tokens][top_k] out, or
+ *           NULL; all aligned to their elements
+ */
+FT_API int ft_moe_combine_backward(const void* grad_y, int32_t y_dtype, const void* rows, int32_t rows_dtype,
+                                   const float* topk_weights, void* grad_rows, float* grad_weights, int64_t tokens,
+                                   int32_t top_k, int64_t ncols, void* stream);
+
 /* ft_last_error - message of the last failing call on this host thread
  * (empty string if none).  The pointer stays valid until the next call on the
  * same thread. */
