@@ -34,7 +34,8 @@ EXPORTS = ("ft_quantize_q8_1", "ft_moe_route_offsets", "ft_moe_q4_0_q8_1", "ft_m
            "ft_moe_q4_0_fp16", "ft_debug_stream_read", "ft_moe_gate", "ft_quantize_fp8", "ft_act_mul_quantize_fp8",
            "ft_moe_fp8_workspace_bytes", "ft_moe_fp8_fp8", "ft_moe_fp8_fp8_slots", "ft_matmul_fp8_fp8",
            "ft_moe_combine", "ft_moe_layer_fp8_workspace_bytes", "ft_moe_layer_fp8",
-           "ft_moe_balance_workspace_bytes", "ft_moe_balance_loss", "ft_moe_gate_backward", "ft_moe_combine_backward")
+           "ft_moe_balance_workspace_bytes", "ft_moe_balance_loss", "ft_moe_gate_backward", "ft_moe_combine_backward",
+           "ft_lora_workspace_bytes", "ft_lora_add", "ft_lora_backward")
 
 
 class FtError(RuntimeError):
@@ -110,6 +111,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.ft_moe_balance_loss.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp]
         L.ft_moe_gate_backward.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, f32, i32, vp]
         L.ft_moe_combine_backward.argtypes = [vp, i32, vp, i32, vp, vp, vp, i64, i32, i64, vp]
+        L.ft_lora_workspace_bytes.argtypes = [i64, i32, i32, i32, i64, i64, i32]
+        L.ft_lora_workspace_bytes.restype = sz
+        L.ft_lora_add.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, i64, i64, vp, sz, vp]
+        L.ft_lora_backward.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, i64, i64, vp, sz, vp]
         for name in EXPORTS:
             getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
         L.ft_moe_workspace_bytes.restype = ctypes.c_size_t
@@ -798,6 +803,74 @@ def moe_combine_backward(grad_out, rows, topk_weights, need_rows=True, need_weig
     if st:
         _check(st)
     return grad_rows, grad_weights
+
+
+def _lora_args(x, a, b, ids, scales):
+    """Checked: (pointers of x, a, b, ids, scales, type code, device, T, k, per_slot, L, R, K, N, shape of the slots)."""
+    px = _ptr(x, "x", 2)
+    rows, K = x.shape
+    dev = x.get_device()
+    code = _dtype_code(x.dtype, "x", (F16, BF16))
+    pa, pb = _ptr(a, "a", 3, dev), _ptr(b, "b", 3, dev)
+    L, R, _ = a.shape
+    N = b.shape[1]
+    if a.dtype != x.dtype or b.dtype != x.dtype:
+        raise TypeError(f"x, a and b must have one type, got {x.dtype}, {a.dtype} and {b.dtype}")
+    if a.shape != (L, R, K) or b.shape != (L, N, R):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)} a {tuple(a.shape)} b {tuple(b.shape)}")
+    pi = _ptr(ids, "ids", 1 if ids.dim() == 1 else 2, dev)
+    if ids.dtype != _i32:
+        raise TypeError(f"ids must be {_i32}, got {ids.dtype}")
+    lead = tuple(ids.shape)
+    T, k = lead if len(lead) == 2 else (lead[0], 1)
+    if rows != T and rows != T * k:
+        raise ValueError(f"x must have a row per token ({T}) or per slot ({T * k}), got {rows}")
+    ps = None if scales is None else _typed_ptr(scales, "scales", _f32, (L,), dev)
+    return px, pa, pb, pi, ps, code, dev, T, k, 1 if rows != T or k == 1 else 0, L, R, K, N, lead
+
+
+def lora_add(x, a, b, ids, scales=None, add=None, out=None, out_dtype=None):
+    """Low-rank adapters beside a product (ft_lora_add): rows x [T, K], or [T*k, K] per slot, fp16 / bf16; adapters a
+    [L, R, K] and b [L, N, R]; ids int32 [T] or [T, k], -1: none; scales fp32 [L] or None -> add + scale * b (a x),
+    [T, N] or [T, k, N], of out_dtype (fp32 or x's type; default: add's type, else x's).  out may be add."""
+    lib = _lib_ready()
+    px, pa, pb, pi, ps, code, dev, T, k, per_slot, L, R, K, N, lead = _lora_args(x, a, b, ids, scales)
+    out_dtype = (out_dtype or (x.dtype if add is None else add.dtype)) if out is None else out.dtype
+    ocode = _dtype_code(out_dtype, "out_dtype", (F32, code))
+    padd = None if add is None else _typed_ptr(add, "add", out_dtype, (*lead, N), dev)
+    out = _out(out, "out", (*lead, N), out_dtype, x, dev)
+    n = lib.ft_lora_workspace_bytes(T, k, L, R, K, N, 0)
+    ws, pws = _workspace(n, x)
+    st = lib.ft_lora_add(px, code, pa, pb, ps, pi, padd, out.data_ptr(), ocode, T, k, per_slot, L, R, K, N, pws, n,
+                         _stream_of(dev))
+    if st:
+        _check(st)
+    return out
+
+
+def lora_backward(grad_out, x, a, b, ids, scales=None, add=None, need_x=True, need_a=True, need_b=True, grad_x=None,
+                  grad_a=None, grad_b=None):
+    """Gradients of lora_add (ft_lora_backward): grad_out [T, N] or [T, k, N] of x's type, the other arguments as it
+    had them, add of x's shape or None -> (grad_x = add + the gradient, of x's shape and type, summed over a token's slots where
+    they share a row; grad_a fp32 [L, R, K]; grad_b fp32 [L, N, R]); None where not needed."""
+    lib = _lib_ready()
+    px, pa, pb, pi, ps, code, dev, T, k, per_slot, L, R, K, N, lead = _lora_args(x, a, b, ids, scales)
+    pg = _typed_ptr(grad_out, "grad_out", x.dtype, (*lead, N), dev)
+    padd = None if add is None else _typed_ptr(add, "add", x.dtype, x.shape, dev)
+    if need_x or grad_x is not None:
+        grad_x = _out(grad_x, "grad_x", tuple(x.shape), x.dtype, x, dev)
+    if need_a or grad_a is not None:
+        grad_a = _out(grad_a, "grad_a", (L, R, K), _f32, x, dev)
+    if need_b or grad_b is not None:
+        grad_b = _out(grad_b, "grad_b", (L, N, R), _f32, x, dev)
+    n = lib.ft_lora_workspace_bytes(T, k, L, R, K, N, 1)
+    ws, pws = _workspace(n, x)
+    st = lib.ft_lora_backward(pg, px, code, pa, pb, ps, pi, padd, None if grad_x is None else grad_x.data_ptr(),
+                              None if grad_a is None else grad_a.data_ptr(), None if grad_b is None else grad_b.data_ptr(),
+                              T, k, per_slot, L, R, K, N, pws, n, _stream_of(dev))
+    if st:
+        _check(st)
+    return grad_x, grad_a, grad_b
 
 
 def workspace_bytes(tokens, top_k, n_experts, nrows, ncols) -> int:

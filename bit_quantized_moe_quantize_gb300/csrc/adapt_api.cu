@@ -24,6 +24,129 @@ int check_router(int64_t tokens, int32_t n_experts, int32_t top_k, int32_t dtype
     return FT_OK;
 }
 
+// ------------------------------------------------------- low-rank adapters
+constexpr int32_t kLoraSmallMean = 16;        // slots per adapter on average that go by tiles of 16
+constexpr int64_t kLoraLeaderSlots = 256;     // slots up to which the CTAs find their tiles among the ids
+
+struct LoraShape {
+    int64_t tokens, n_slots, ncols, nrows;
+    int32_t top_k, n_adapters, rank;
+};
+
+int check_lora(int64_t tokens, int32_t top_k, int32_t n_adapters, int32_t rank, int64_t ncols, int64_t nrows, LoraShape* h) {
+    if (tokens < 0) return fail(FT_ERR_ARG, "tokens must be >= 0 (got %lld)", (long long)tokens);
+    if (top_k < 1) return fail(FT_ERR_ARG, "top_k must be >= 1 (got %d)", top_k);
+    if (n_adapters < 1 || n_adapters > FT_MAX_EXPERTS)
+        return fail(FT_ERR_ARG, "n_adapters must be in [1, %d] (got %d)", FT_MAX_EXPERTS, n_adapters);
+    if (rank < 8 || rank > FT_MAX_LORA_RANK || rank % 8 != 0)
+        return fail(FT_ERR_ARG, "rank must be a multiple of 8 in [8, %d] (got %d)", FT_MAX_LORA_RANK, rank);
+    if (ncols <= 0 || ncols % 8 != 0 || nrows <= 0 || nrows % 8 != 0)
+        return fail(FT_ERR_ARG, "ncols and nrows must be positive multiples of 8 (got %lld, %lld)", (long long)ncols, (long long)nrows);
+    if (ncols > FT_MAX_NCOLS || nrows > FT_MAX_NCOLS)
+        return fail(FT_ERR_SIZE, "ncols and nrows must be <= %d (got %lld, %lld)", FT_MAX_NCOLS, (long long)ncols, (long long)nrows);
+    int64_t n;
+    if (!mul_ok(tokens, top_k, &n) || n > INT32_MAX) return fail(FT_ERR_SIZE, "tokens * top_k = %lld * %d must be < 2^31", (long long)tokens, top_k);
+    *h = LoraShape{tokens, n, ncols, nrows, top_k, n_adapters, rank};
+    return FT_OK;
+}
+
+// Slots of a tile: 64, but 16 where adapters have few slots each.
+int lora_width(int64_t n_slots, int32_t n_adapters) { return n_slots <= kLoraSmallMean * n_adapters ? 16 : 64; }
+
+int64_t lora_tiles(int64_t n_slots, int32_t n_adapters, int width) {
+    const int64_t some = n_slots < n_adapters ? n_slots : n_adapters;      // adapters that can have a tile that is not full
+    return (n_slots + some * (width - 1)) / width;
+}
+
+// Chunks of the matrices' gradients at most, before each adapter's last: some three CTAs per SM, and no chunk
+// of less than 256 slots.
+int64_t lora_most_chunks(int64_t n_tiles, int width, int32_t rank, int64_t cols) {
+    const int64_t blocks = (cols + (rank <= 64 ? 255 : 127)) / (rank <= 64 ? 256 : 128);
+    const int64_t chunks = 3 * 152 / blocks > 0 ? 3 * 152 / blocks : 1, all = (n_tiles * width + 255) / 256;
+    return chunks < all ? chunks : all;
+}
+
+struct LoraWs {
+    Fp8Order order;
+    size_t u, v, rows, present, parts_a, parts_b, total;
+    int width;
+    int64_t n_tiles;
+    int32_t chunk_tiles;
+    bool ordered;
+};
+
+// rows: of the gradient of x, where slots share a row of x.
+LoraWs lora_ws(uint8_t* base, const LoraShape& h, bool backward, bool share) {
+    LoraWs L{};
+    const size_t S = static_cast<size_t>(h.n_slots), R = static_cast<size_t>(h.rank);
+    size_t at = 0;
+    L.width = lora_width(h.n_slots, h.n_adapters);
+    L.ordered = backward || h.n_slots > kLoraLeaderSlots;
+    L.n_tiles = L.ordered ? lora_tiles(h.n_slots, h.n_adapters, L.width) : h.n_slots;
+    if (L.ordered) at = al256(fp8_order_layout(base, h.n_slots, h.n_adapters, false, &L.order));
+    L.u = take_bytes(&at, S * R * 4);
+    if (backward) {
+        L.v = take_bytes(&at, S * R * 4);
+        const int64_t most = lora_most_chunks(L.n_tiles, L.width, h.rank, h.ncols + h.nrows);
+        L.chunk_tiles = most > 0 ? static_cast<int32_t>((L.n_tiles + most - 1) / most) : 1;
+        const size_t chunks = static_cast<size_t>(most + h.n_adapters);
+        L.parts_a = take_bytes(&at, chunks * R * h.ncols * 4);
+        L.parts_b = take_bytes(&at, chunks * R * h.nrows * 4);
+        if (share) {
+            L.rows = take_bytes(&at, S * h.ncols * 4);
+            L.present = take_bytes(&at, S * 4);
+        }
+    }
+    L.total = at;
+    return L;
+}
+
+// The most that lora_ws gives for up to h.tokens tokens: what it needs rises with them but where the tiles' width, the
+// order's scratch or the chunks change.
+size_t lora_most(const LoraShape& h, bool backward, bool share) {
+    size_t most = 0;
+    auto take = [&](int64_t tokens) {
+        if (tokens < 0 || tokens > h.tokens) return;
+        LoraShape x = h;
+        x.tokens = tokens;
+        x.n_slots = tokens * h.top_k;
+        const size_t n = lora_ws(nullptr, x, backward, share).total;
+        most = n > most ? n : most;
+    };
+    take(h.tokens);
+    take(static_cast<int64_t>(kLoraSmallMean) * h.n_adapters / h.top_k);
+    take(kFastRouteSlots / h.top_k);
+    take(kLoraLeaderSlots / h.top_k + 1);
+    return most;
+}
+
+LoraPlan lora_plan(const LoraShape& h, const LoraWs& L, const int32_t* ids, const float* scales, uint32_t* err, bool backward) {
+    LoraPlan p{};
+    p.ids = ids;
+    if (L.ordered) {
+        p.offsets = L.order.offsets;
+        p.tiles = L.order.tiles;
+        p.perm = L.order.perm;
+    }
+    p.scales = scales;
+    p.n_slots = static_cast<int32_t>(h.n_slots);
+    p.n_adapters = h.n_adapters;
+    p.rank = h.rank;
+    p.width = L.width;
+    p.n_tiles = L.n_tiles;
+    p.chunk_tiles = L.chunk_tiles;
+    p.err = err;
+    p.down_jobs = backward ? 2 : 1;
+    p.down_cols = static_cast<int32_t>(backward && h.nrows > h.ncols ? h.nrows : h.ncols);
+    return p;
+}
+
+int check_lora_type(int32_t dtype) {
+    if (dtype != FT_DTYPE_F16 && dtype != FT_DTYPE_BF16)
+        return fail(FT_ERR_ARG, "dtype must be FT_DTYPE_F16 or FT_DTYPE_BF16 (got %d)", dtype);
+    return FT_OK;
+}
+
 }  // namespace
 }  // namespace ft
 
@@ -98,6 +221,96 @@ int ft_moe_combine_backward(const void* grad_y, int32_t y_dtype, const void* row
         return fail(FT_ERR_ALIGN, "grad_y, rows, weights and their gradients must be aligned to their elements");
     return launch_combine_grad(grad_y, y_dtype, rows, rows_dtype, topk_weights, grad_rows, grad_weights, tokens, top_k, ncols,
                                static_cast<cudaStream_t>(stream));
+}
+
+size_t ft_lora_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_adapters, int32_t rank, int64_t ncols, int64_t nrows,
+                               int32_t backward) {
+    clear_error();
+    LoraShape h;
+    if (check_lora(tokens, top_k, n_adapters, rank, ncols, nrows, &h)) return 0;
+    return lora_most(h, backward != 0, top_k > 1);
+}
+
+int ft_lora_add(const void* x, int32_t dtype, const void* a, const void* b, const float* scales, const int32_t* ids,
+                const void* add, void* out, int32_t out_dtype, int64_t tokens, int32_t top_k, int32_t x_per_slot,
+                int32_t n_adapters, int32_t rank, int64_t ncols, int64_t nrows, void* workspace, size_t workspace_bytes,
+                void* stream) {
+    clear_error();
+    LoraShape h;
+    if (int st = check_lora(tokens, top_k, n_adapters, rank, ncols, nrows, &h)) return st;
+    if (int st = check_lora_type(dtype)) return st;
+    if (out_dtype != FT_DTYPE_F32 && out_dtype != dtype)
+        return fail(FT_ERR_ARG, "out_dtype must be FT_DTYPE_F32 or the adapters' type (got %d)", out_dtype);
+    if (tokens == 0) return FT_OK;
+    if (!x || !a || !b || !ids || !out) return fail(FT_ERR_ARG, "null pointer");
+    if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(add, 16) || !aligned(out, 16))
+        return fail(FT_ERR_ALIGN, "x, a, b, add and out must be 16-byte aligned");
+    if (!aligned(scales, 4) || !aligned(ids, 4)) return fail(FT_ERR_ALIGN, "scales and ids must be aligned to their elements");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const LoraWs L = lora_ws(ws, h, false, false);
+    if (int st = check_workspace(workspace, workspace_bytes, L.total)) return st;
+    uint32_t* err = nullptr;
+    if (int st = fp8_error_word(&err)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const LoraPlan p = lora_plan(h, L, ids, scales, err, false);
+    if (L.ordered)
+        if (int st = launch_fp8_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
+    float* u = reinterpret_cast<float*>(ws + L.u);
+    const LoraDown down{x, a, u, static_cast<int32_t>(ncols), x_per_slot ? 1 : top_k, false};
+    if (int st = launch_lora_down(&down, 1, p, dtype, s)) return st;
+    const LoraUp up{u, b, add, out, nullptr, static_cast<int32_t>(nrows), false, out_dtype == FT_DTYPE_F32};
+    return launch_lora_up(up, p, dtype, s);
+}
+
+int ft_lora_backward(const void* grad_out, const void* x, int32_t dtype, const void* a, const void* b, const float* scales,
+                     const int32_t* ids, const void* add, void* grad_x, float* grad_a, float* grad_b, int64_t tokens,
+                     int32_t top_k, int32_t x_per_slot, int32_t n_adapters, int32_t rank, int64_t ncols, int64_t nrows,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    clear_error();
+    LoraShape h;
+    if (int st = check_lora(tokens, top_k, n_adapters, rank, ncols, nrows, &h)) return st;
+    if (int st = check_lora_type(dtype)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t size_a = static_cast<int64_t>(n_adapters) * rank * ncols * 4, size_b = static_cast<int64_t>(n_adapters) * rank * nrows * 4;
+    if (!aligned(grad_x, 16) || !aligned(grad_a, 16) || !aligned(grad_b, 16))
+        return fail(FT_ERR_ALIGN, "grad_x, grad_a and grad_b must be 16-byte aligned");
+    if (tokens == 0) {      // sums over nothing
+        cudaError_t e = cudaSuccess;
+        if (grad_a) e = cudaMemsetAsync(grad_a, 0, static_cast<size_t>(size_a), s);
+        if (grad_b && e == cudaSuccess) e = cudaMemsetAsync(grad_b, 0, static_cast<size_t>(size_b), s);
+        return e == cudaSuccess ? FT_OK : fail(FT_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
+    }
+    if (!grad_x && !grad_a && !grad_b) return fail(FT_ERR_ARG, "grad_x, grad_a and grad_b are all null");
+    if (!grad_out || !x || !a || !b || !ids) return fail(FT_ERR_ARG, "null pointer");
+    if (!aligned(grad_out, 16) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(add, 16))
+        return fail(FT_ERR_ALIGN, "grad_out, x, a, b and add must be 16-byte aligned");
+    if (!aligned(scales, 4) || !aligned(ids, 4)) return fail(FT_ERR_ALIGN, "scales and ids must be aligned to their elements");
+    const bool share = top_k > 1 && !x_per_slot;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const LoraWs L = lora_ws(ws, h, true, share);
+    if (int st = check_workspace(workspace, workspace_bytes, L.total)) return st;
+    uint32_t* err = nullptr;
+    if (int st = fp8_error_word(&err)) return st;
+    const LoraPlan p = lora_plan(h, L, ids, scales, err, true);
+    if (int st = launch_fp8_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
+    float *u = reinterpret_cast<float*>(ws + L.u), *v = reinterpret_cast<float*>(ws + L.v);
+    const int32_t K = static_cast<int32_t>(ncols), N = static_cast<int32_t>(nrows), div = x_per_slot ? 1 : top_k;
+    LoraDown down[2];
+    int n = 0;
+    if (grad_b) down[n++] = LoraDown{x, a, u, K, div, false};
+    if (grad_x || grad_a) down[n++] = LoraDown{grad_out, b, v, N, 1, true};
+    if (int st = launch_lora_down(down, n, p, dtype, s)) return st;
+    if (grad_x) {
+        float *rows = reinterpret_cast<float*>(ws + L.rows), *present = reinterpret_cast<float*>(ws + L.present);
+        const LoraUp up = share ? LoraUp{v, a, nullptr, rows, present, K, true, true}
+                                : LoraUp{v, a, add, grad_x, nullptr, K, true, false};
+        if (int st = launch_lora_up(up, p, dtype, s)) return st;
+        if (share)
+            if (int st = launch_combine(rows, FT_DTYPE_F32, present, add, grad_x, dtype, tokens, top_k, ncols, s)) return st;
+    }
+    const LoraGrad grads[2] = {LoraGrad{x, v, grad_a, reinterpret_cast<float*>(ws + L.parts_a), K, div, false},
+                               LoraGrad{grad_out, u, grad_b, reinterpret_cast<float*>(ws + L.parts_b), N, 1, true}};
+    return launch_lora_grad(grads, p, dtype, s);
 }
 
 }  // extern "C"

@@ -273,4 +273,47 @@ int launch_gate_grad(const GateGradParams& p, const void* logits, int dtype, int
 int launch_combine_grad(const void* dy, int dy_dtype, const void* rows, int rows_dtype, const float* weights, void* grad_rows,
                         float* grad_weights, int64_t tokens, int32_t top_k, int64_t ncols, cudaStream_t s);
 
+// ------------------------------------------------- low-rank adapters
+// Slots by adapter, and what the kernels of a call share.
+struct LoraPlan {
+    const int32_t *ids, *offsets, *tiles, *perm;      // perm null: CTAs find their tiles among the ids
+    const float* scales;                              // per adapter, or null: 1
+    int32_t n_slots, n_adapters, rank;
+    int width;               // slots of a tile: 64 or 16
+    int64_t n_tiles;         // tiles at most
+    int32_t chunk_tiles;     // tiles of a chunk of the matrices' gradients
+    uint32_t* err;           // raised by launch_lora_down for ids that are no adapter
+    int32_t down_jobs, down_cols;      // first products that a call of this kind can have, their longest rows
+};
+// Numbers of chunks that lora_grad.cu gives out at most.
+inline int64_t lora_chunks(int64_t n_tiles, int32_t n_adapters, int32_t per) { return n_tiles / per + n_adapters; }
+
+struct LoraDown {      // u[s] = W z[s / div]
+    const void *z, *w;
+    float* u;
+    int32_t cols, div;
+    bool trans;        // W is [cols][rank], else [rank][cols]
+};
+int launch_lora_down(const LoraDown* jobs, int n_jobs, const LoraPlan& p, int dtype, cudaStream_t s);
+
+struct LoraUp {        // out[s] = add[s] + scale W u[s]; launched to overlap launch_lora_down's tail
+    const float* u;
+    const void *w, *add;
+    void* out;         // fp32 (out_f32) or the adapters' type
+    float* present;    // [slots] 1 or 0, instead of passing rows without an adapter on; or null
+    int32_t cols;
+    bool trans, out_f32;      // trans: W is [rank][cols], else [cols][rank]
+};
+int launch_lora_up(const LoraUp& j, const LoraPlan& p, int dtype, cudaStream_t s);
+int launch_lora_up_bf16(const LoraUp& j, const LoraPlan& p, cudaStream_t s);
+
+struct LoraGrad {      // out[e] = sum over its slots of scale w[s] z[s / div]; out null: not wanted
+    const void* z;
+    const float* w;
+    float *out, *parts;
+    int32_t cols, div;
+    bool turned;       // out is [cols][rank], else [rank][cols]
+};
+int launch_lora_grad(const LoraGrad* jobs, const LoraPlan& p, int dtype, cudaStream_t s);
+
 }  // namespace ft

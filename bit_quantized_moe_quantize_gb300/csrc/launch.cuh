@@ -16,7 +16,7 @@ __device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcon
 template <typename... P, typename... A>
 int launch_with(void (*kernel)(P...), const char* name, dim3 grid, dim3 block, size_t smem, bool overlap, unsigned cluster,
                 cudaStream_t s, A... args) {
-    if (smem > 48 * 1024)
+    if (smem > 40 * 1024)      // 48 KB, with room for what a kernel has of fixed size
         if (int st = set_smem_limit(reinterpret_cast<const void*>(kernel), static_cast<int>(smem))) return st;
     cudaLaunchAttribute at[2];
     unsigned n = 0;

@@ -1,0 +1,216 @@
+// Pieces of the low-rank adapters' kernels: tiles of slots that share an adapter, asynchronous copies, and
+// products of fp32 values with 16-bit ones on the tensor cores (mma.sync).
+//
+// The products here have one side of rank 8 to 128 and are bound by memory: reading a row of x of K values and
+// writing one of N takes 2 K + 4 N bytes for 2 R (K + N) operations, R to 2 R operations a byte, where
+// the card has 280 for a byte.  Registers as accumulators, which the next step needs anyway, cost less
+// there than a trip through tensor memory.
+#pragma once
+
+#include "fp8_common.cuh"
+
+namespace ft {
+
+constexpr int kLoraThreads = 128;
+constexpr int kLoraTile = 64, kLoraSmallTile = 16;      // slots of a tile
+
+// Slots by adapter: in order (perm, by fp8_route.cu, whose tiles have the kernel's width), or
+// perm == nullptr: found by each CTA.
+struct LoraSlots {
+    const int32_t *ids, *offsets, *tiles, *perm;
+    int32_t n_slots, n_adapters;
+};
+
+struct LoraTile {
+    int32_t adapter;      // -1: slot `first` has none
+    int32_t n;            // slots, 0: nothing to do
+    int32_t first;
+};
+
+// Tile b of width MT; its slots go to slots[0 .. n).  By all threads of the CTA; ends behind a barrier.
+// Without an order, b is a slot, and stands for itself and those behind it that share its adapter where the number
+// of such slots before it is a multiple of MT.
+template <int MT>
+__device__ __forceinline__ LoraTile find_tile(const LoraSlots& s, int32_t b, int32_t* slots, int32_t threads) {
+    const int32_t tid = static_cast<int32_t>(threadIdx.x), L = s.n_adapters;
+    if (s.perm) {
+        if (b >= __ldg(s.tiles + L)) return LoraTile{0, 0, 0};
+        int32_t c = 0;
+        for (int32_t e0 = 0; e0 < L; e0 += threads) c += __syncthreads_count(e0 + tid < L && __ldg(s.tiles + e0 + tid) <= b);
+        const int32_t a = c - 1, first = __ldg(s.offsets + a) + (b - __ldg(s.tiles + a)) * MT;
+        const int32_t n = min(MT, __ldg(s.offsets + a + 1) - first);
+        if (tid < n) slots[tid] = __ldg(s.perm + first + tid);
+        __syncthreads();
+        return LoraTile{a, n, slots[0]};
+    }
+    const int32_t a = __ldg(s.ids + b);
+    if (a < 0 || a >= L) return LoraTile{-1, 0, b};
+    int32_t before = 0;
+    for (int32_t s0 = 0; s0 < b; s0 += threads) before += __syncthreads_count(s0 + tid < b && __ldg(s.ids + s0 + tid) == a);
+    if (before % MT != 0) return LoraTile{a, 0, b};
+    int32_t n = 0;
+    __shared__ int32_t warp_n[kLoraThreads / 32];
+    for (int32_t s0 = b; s0 < s.n_slots && n < MT; s0 += threads) {
+        const bool mine = s0 + tid < s.n_slots && __ldg(s.ids + s0 + tid) == a;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, mine);
+        if (lane_id() == 0) warp_n[tid >> 5] = __popc(mask);
+        __syncthreads();
+        int32_t at = n + __popc(mask & ((1u << lane_id()) - 1u));
+        for (int32_t w = 0; w < threads / 32; ++w) {
+            if (w < tid >> 5) at += warp_n[w];
+            n += warp_n[w];
+        }
+        if (mine && at < MT) slots[at] = s0 + tid;
+        __syncthreads();
+    }
+    return LoraTile{a, min(n, MT), b};
+}
+
+// ----------------------------------------------------------- asynchronous copies
+// 16 or 4 bytes to shared memory, zeros where not `there` (src is not read then).
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// ------------------------------------------------------------------- matrices
+// Four 8 x 8 matrices of 16-bit values; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void* row, bool trans) {
+    if (trans)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_u32(row)) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_u32(row)) : "memory");
+}
+
+// d += a b over 16 values; a 16 x 16 (rows of the tile), b 16 x 8.
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t tf32_of(float v) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The first TERMS bf16 parts of a pair of fp32 values: 8, 16 or 24 significant bits.
+template <int TERMS>
+__device__ __forceinline__ void split_pair(float lo, float hi, uint32_t (&part)[TERMS]) {
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+        part[t] = bf16_pair(lo, hi);
+        lo -= __uint_as_float(part[t] << 16);
+        hi -= __uint_as_float(part[t] & 0xFFFF0000u);
+    }
+}
+
+// A 16 x 16 operand of fp32 values, to be multiplied with 16-bit ones: v[2 i], v[2 i + 1] are neighbours in the
+// place that mma's 16-bit operand register i has.  With bf16 as sums of TERMS bf16 parts; with fp16, whose values
+// and products have no such range, as two tf32 parts of 11 bits against fp16 turned to tf32, which is exact.
+template <typename T, int TERMS>
+struct Wide16;
+
+template <int TERMS>
+struct Wide16<__nv_bfloat16, TERMS> {
+    uint32_t part[TERMS][4];
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[TERMS];
+            split_pair<TERMS>(v[2 * i], v[2 * i + 1], p);
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) part[t][i] = p[t];
+        }
+    }
+    template <int N>
+    __device__ __forceinline__ void mul(float (&d)[N][4], const uint32_t (&b)[N][2]) const {
+#pragma unroll
+        for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+            for (int j = 0; j < N; ++j) mma16(d[j], part[t], b[j][0], b[j][1], __nv_bfloat16());
+    }
+};
+
+template <int TERMS>
+struct Wide16<__half, TERMS> {
+    float v[8];
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x[i];
+    }
+    template <int N>
+    __device__ __forceinline__ void mul(float (&d)[N][4], const uint32_t (&b)[N][2]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {      // the pairs' first and second eight
+            uint32_t hi[4], lo[4];         // mma's rows and its first and second four: here the pairs' first and second
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = v[2 * ((i & 1) + 2 * h) + (i >> 1)];
+                hi[i] = tf32_of(x);
+                lo[i] = tf32_of(x - __uint_as_float(hi[i]));
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b[j][h]));
+                const uint32_t b0 = __float_as_uint(f.x), b1 = __float_as_uint(f.y);
+                mma8_tf32(d[j], lo[0], lo[1], lo[2], lo[3], b0, b1);
+                mma8_tf32(d[j], hi[0], hi[1], hi[2], hi[3], b0, b1);
+            }
+        }
+    }
+};
+
+// Elements between rows of `n` 16-bit values in shared memory: whole 16-byte words, an odd number of them, so that
+// eight rows' words at one column lie in different banks.
+inline __host__ __device__ int32_t odd_pitch(int32_t n) { return ((n + 7) / 8 | 1) * 8; }
+
+// Neighbouring threads hold columns 2 q and 2 q + 1 of each of four tiles of eight.  Columns are put where that
+// makes eight neighbours for a thread: column 8 q + 2 j + i of 32 goes to place 8 j + 2 q + i.
+__device__ __forceinline__ int32_t spread_col(int32_t c) { return (c & ~31) | (c >> 1 & 3) << 3 | (c >> 3 & 3) << 1 | (c & 1); }
+
+// --------------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A word of shared memory of the cluster's CTA `rank`, at the place that p has in this one.
+__device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+}  // namespace ft

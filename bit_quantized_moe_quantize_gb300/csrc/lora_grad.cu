@@ -1,0 +1,309 @@
+// Gradients of the adapters' matrices, sums over the slots of an adapter:
+//
+//   dA[r][k] = sum_s v[s][r] x[s][k]      v = scale B^T dy
+//   dB[n][r] = sum_s dy[s][n] u[s][r]     u = scale A x
+//
+// Memory-bound on x and dy, which are read once more.  A CTA takes a chunk of an adapter's slots and 256
+// columns (128 for ranks above 64): z's rows come by cp.async, 32 slots a stage; the narrow side's fp32 values
+// are split into parts of 8 bits (lora.cuh) on their way to shared memory, so that the products keep 24.  The sums lie
+// in registers; an adapter with several chunks leaves them in the workspace, where a second launch
+// adds them up in order.  That launch also writes the zeros of adapters without a slot.
+//
+// Chunk j of adapter e has number tiles[e] / per + e + j: chunks of `per` tiles never need more numbers than that leaves.
+#include <algorithm>
+#include <type_traits>
+
+#include "lora.cuh"
+#include "ft_internal.h"
+#include "launch.cuh"
+
+namespace ft {
+
+namespace {
+
+constexpr int kGradThreads = 256, kGradSlots = 32, kGradStages = 3;
+
+template <typename T>
+struct GradJob {
+    const T* z;
+    const float* w;         // [slots][R]
+    float *out, *parts;     // [adapters][size], [chunks][size]
+    int32_t cols, div;      // of z; row of slot s: s / div
+    bool turned;            // out is [cols][R], else [R][cols]
+};
+
+template <typename T>
+struct GradArgs {
+    GradJob<T> job[2];
+    LoraSlots slots;
+    const float* scales;
+    int32_t rank, per, width, blocks0;      // blocks0: blocks of columns of the first job
+};
+
+// Chunk number b: its adapter, whether it has others, its first slot in order and its slots (0: none).
+struct Chunk {
+    int32_t adapter, first, n;
+    bool alone;
+};
+
+__device__ __forceinline__ Chunk find_chunk(const LoraSlots& s, int32_t b, int32_t per, int32_t width) {
+    const int32_t L = s.n_adapters, tid = static_cast<int32_t>(threadIdx.x);
+    int32_t c = 0;
+    for (int32_t e0 = 0; e0 < L; e0 += kGradThreads) {
+        const int32_t e = e0 + tid;
+        c += __syncthreads_count(e < L && __ldg(s.tiles + e) / per + e <= b);
+    }
+    const int32_t a = c - 1, t0 = __ldg(s.tiles + a), n_tiles = __ldg(s.tiles + a + 1) - t0, j = b - (t0 / per + a);
+    if (j * per >= n_tiles) return Chunk{a, 0, 0, true};
+    const int32_t at = __ldg(s.offsets + a) + j * per * width;
+    return Chunk{a, at, min(per * width, __ldg(s.offsets + a + 1) - at), n_tiles <= per};
+}
+
+// MR: tiles of 16 ranks that there is room for; NJ: tiles of eight columns that a warp has.
+template <typename T, int MR, int NJ>
+__global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_constant__ GradArgs<T> a) {
+    constexpr int CC = 8 * NJ * (kGradThreads / 32), ZP = CC + 8;      // columns of the CTA, their pitch
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int PAIRS = MR;      // pairs of ranks that a thread has of a stage
+    extern __shared__ __align__(16) uint8_t grad_smem[];
+    const int32_t tid = static_cast<int32_t>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const bool second = static_cast<int32_t>(blockIdx.y) >= a.blocks0;
+    const GradJob<T>& job = a.job[second ? 1 : 0];
+    const int32_t col0 = (static_cast<int32_t>(blockIdx.y) - (second ? a.blocks0 : 0)) * CC;
+    const Chunk ck = find_chunk(a.slots, static_cast<int32_t>(blockIdx.x), a.per, a.width);
+    if (ck.n == 0) return;
+    const int32_t R = a.rank, r16 = (R + 15) / 16 * 16, mr = r16 / 16, cols = job.cols;
+    const int32_t wp = odd_pitch(r16), wf = r16 + 4;      // pitch of a part's rows; of fp32 rows (fp16)
+    const int32_t w_bytes = BF ? 3 * kGradSlots * wp * 2 : kGradSlots * wf * 4;
+    T* zs_all = reinterpret_cast<T*>(grad_smem);
+    uint8_t* ws_all = grad_smem + kGradStages * kGradSlots * ZP * sizeof(T);
+    const int32_t* perm = a.slots.perm + ck.first;
+    const float scale = a.scales ? __ldg(a.scales + ck.adapter) : 1.0f;
+    const int32_t steps = (ck.n + kGradSlots - 1) / kGradSlots;
+
+    // z: thread by 16-byte words of a row
+    constexpr int ZW = CC / 8, ZROWS = kGradThreads / ZW, ZI = kGradSlots / ZROWS;
+    const int32_t zc = tid % ZW * 8;
+    auto load_z = [&](int32_t i) {
+        T* zs = zs_all + i % kGradStages * kGradSlots * ZP;
+#pragma unroll
+        for (int j = 0; j < ZI; ++j) {
+            const int32_t row = tid / ZW + ZROWS * j, s = i * kGradSlots + row;
+            const bool there = s < ck.n && col0 + zc < cols;
+            const T* src = there ? job.z + static_cast<int64_t>(__ldg(perm + s) / job.div) * cols + col0 + zc : job.z;
+            copy16(zs + row * ZP + zc, src, there);
+        }
+    };
+    // w: pairs of ranks, by slot and then by pair
+    float2 wreg[PAIRS];
+    auto load_w = [&](int32_t i) {
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) {
+            const int32_t at = tid + j * kGradThreads, row = at / (8 * mr), r = (at - row * 8 * mr) * 2, s = i * kGradSlots + row;
+            wreg[j] = make_float2(0.0f, 0.0f);
+            if (j < mr && s < ck.n && r < R) {
+                const float2 v = *reinterpret_cast<const float2*>(job.w + static_cast<int64_t>(__ldg(perm + s)) * R + r);
+                wreg[j] = make_float2(v.x * scale, v.y * scale);
+            }
+        }
+    };
+    auto store_w = [&](int32_t i) {
+        uint8_t* ws = ws_all + i % 2 * w_bytes;
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) {
+            if (j >= mr) break;
+            const int32_t at = tid + j * kGradThreads, row = at / (8 * mr), r = (at - row * 8 * mr) * 2;
+            if constexpr (BF) {
+                uint32_t p[3];
+                split_pair<3>(wreg[j].x, wreg[j].y, p);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(ws) + (t * kGradSlots + row) * wp + r) = p[t];
+            } else {
+                float* f = reinterpret_cast<float*>(ws) + row * wf + r;
+                f[0] = wreg[j].x;
+                f[1] = wreg[j].y;
+            }
+        }
+    };
+
+    float acc[MR][NJ][4];
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[m][j][x] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGradStages - 1; ++i) {
+        if (i < steps) load_z(i);
+        copies_commit();
+    }
+    load_w(0);
+    store_w(0);
+    if (steps > 1) load_w(1);
+    for (int32_t i = 0; i < steps; ++i) {
+        copies_wait<kGradStages - 2>();
+        __syncthreads();
+        if (i + kGradStages - 1 < steps) load_z(i + kGradStages - 1);
+        copies_commit();
+        if (i + 1 < steps) store_w(i + 1);      // the buffer that the step before last read
+        if (i + 2 < steps) load_w(i + 2);
+        const T* zs = zs_all + i % kGradStages * kGradSlots * ZP;
+        const uint8_t* ws = ws_all + i % 2 * w_bytes;
+#pragma unroll
+        for (int k = 0; k < kGradSlots; k += 16) {
+            uint32_t b[NJ][2];
+#pragma unroll
+            for (int j = 0; j < NJ; j += 2) {
+                uint32_t x[4];
+                ldsm4(x, zs + (k + lane % 16) * ZP + warp * 8 * NJ + (j + lane / 16) * 8, true);
+                b[j][0] = x[0];
+                b[j][1] = x[1];
+                b[j + 1][0] = x[2];
+                b[j + 1][1] = x[3];
+            }
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                if (m >= mr) break;
+                if constexpr (BF) {
+#pragma unroll
+                    for (int t = 2; t >= 0; --t) {
+                        uint32_t x[4];
+                        const T* p = reinterpret_cast<const T*>(ws) + t * kGradSlots * wp;
+                        ldsm4(x, p + (k + lane / 16 * 8 + lane % 8) * wp + m * 16 + lane / 8 % 2 * 8, true);
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) mma16(acc[m][j], x, b[j][0], b[j][1], T());
+                    }
+                } else {
+                    const float* f = reinterpret_cast<const float*>(ws) + (k + lane % 4 * 2) * wf + m * 16 + lane / 4;
+                    float v[8];      // ranks by h, slots 2 q (+1) and 2 q + 8 (+1)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            v[2 * (h + 2 * x)] = f[8 * x * wf + 8 * h];
+                            v[2 * (h + 2 * x) + 1] = f[(8 * x + 1) * wf + 8 * h];
+                        }
+                    Wide16<T, 2> wide;
+                    wide.set(v);
+                    wide.mul(acc[m], b);
+                }
+            }
+        }
+    }
+    copies_wait<0>();
+    const int64_t size = static_cast<int64_t>(R) * cols;
+    float* out = ck.alone ? job.out + ck.adapter * size : job.parts + blockIdx.x * size;
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+        if (m >= mr) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int32_t r = m * 16 + lane / 4 + 8 * h;
+            if (r >= R) continue;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int32_t c = col0 + warp * 8 * NJ + j * 8 + lane % 4 * 2;
+                if (c >= cols) continue;
+                if (job.turned) {
+                    out[static_cast<int64_t>(c) * R + r] = acc[m][j][2 * h];
+                    out[static_cast<int64_t>(c + 1) * R + r] = acc[m][j][2 * h + 1];
+                } else {
+                    *reinterpret_cast<float2*>(out + static_cast<int64_t>(r) * cols + c) = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+                }
+            }
+        }
+    }
+}
+
+// Adds up the chunks of adapters that have several, and zeroes those that have none.
+struct JoinArgs {
+    float* out[2];
+    const float* parts[2];
+    int64_t size4[2];      // in words of 16 bytes
+    const int32_t* tiles;
+    int32_t per;
+};
+
+__global__ void __launch_bounds__(kGradThreads) lora_join_kernel(const JoinArgs a) {
+    const int32_t e = static_cast<int32_t>(blockIdx.x);
+    const int32_t t0 = __ldg(a.tiles + e), n_tiles = __ldg(a.tiles + e + 1) - t0;
+    if (n_tiles > 0 && n_tiles <= a.per) return;
+    const int32_t chunks = (n_tiles + a.per - 1) / a.per;
+    const int64_t first = t0 / a.per + e;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (!a.out[j]) continue;
+        const int64_t size = a.size4[j];
+        const float4* parts = reinterpret_cast<const float4*>(a.parts[j]) + first * size;
+        float4* out = reinterpret_cast<float4*>(a.out[j]) + e * size;
+        for (int64_t i = static_cast<int64_t>(blockIdx.y) * kGradThreads + threadIdx.x; i < size; i += static_cast<int64_t>(gridDim.y) * kGradThreads) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int32_t c = 0; c < chunks; ++c) {
+                const float4 x = __ldg(parts + c * size + i);
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+            }
+            out[i] = v;
+        }
+    }
+}
+
+template <typename T>
+int launch_grad(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
+    GradArgs<T> a{};
+    JoinArgs j{};
+    int n = 0;
+    int32_t blocks[2] = {0, 0};
+    const int32_t cc = p.rank <= 64 ? 256 : 128;
+    for (int i = 0; i < 2; ++i) {
+        if (!jobs[i].out) continue;
+        a.job[n] = GradJob<T>{static_cast<const T*>(jobs[i].z), jobs[i].w, jobs[i].out, jobs[i].parts, jobs[i].cols, jobs[i].div,
+                              jobs[i].turned};
+        blocks[n] = (jobs[i].cols + cc - 1) / cc;
+        j.out[n] = jobs[i].out;
+        j.parts[n] = jobs[i].parts;
+        j.size4[n] = static_cast<int64_t>(p.rank) * jobs[i].cols / 4;
+        ++n;
+    }
+    if (n == 0) return FT_OK;
+    a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters};
+    a.scales = p.scales;
+    a.rank = p.rank;
+    a.per = p.chunk_tiles;
+    a.width = p.width;
+    a.blocks0 = blocks[0];
+    const int64_t chunks = lora_chunks(p.n_tiles, p.n_adapters, p.chunk_tiles);
+    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(blocks[0] + blocks[1])), block(kGradThreads);
+    const int32_t r16 = (p.rank + 15) / 16 * 16;
+    const bool bf = std::is_same<T, __nv_bfloat16>::value;
+    const size_t sm = kGradStages * kGradSlots * static_cast<size_t>(cc + 8) * sizeof(T) +
+                      2 * static_cast<size_t>(bf ? 3 * kGradSlots * odd_pitch(r16) * 2 : kGradSlots * (r16 + 4) * 4);
+    auto go = [&](auto k) { return launch_with(k, "lora_grad_kernel", grid, block, sm, false, 1, s, a); };
+    int st;
+    if (p.rank <= 16) st = go(lora_grad_kernel<T, 1, 4>);
+    else if (p.rank <= 32) st = go(lora_grad_kernel<T, 2, 4>);
+    else if (p.rank <= 64) st = go(lora_grad_kernel<T, 4, 4>);
+    else st = go(lora_grad_kernel<T, 8, 2>);
+    if (st) return st;
+    j.tiles = p.tiles;
+    j.per = p.chunk_tiles;
+    int64_t y = 4 * static_cast<int64_t>(sm_count()) / p.n_adapters;
+    const int64_t most = (std::max(j.size4[0], j.size4[1]) + kGradThreads - 1) / kGradThreads;
+    y = y < 1 ? 1 : y < most ? y : most;
+    const dim3 jgrid(static_cast<unsigned>(p.n_adapters), static_cast<unsigned>(y));
+    lora_join_kernel<<<jgrid, block, 0, s>>>(j);
+    return check_launch("lora_join_kernel", jgrid, block, 0);
+}
+
+}  // namespace
+
+int launch_lora_grad(const LoraGrad* jobs, const LoraPlan& p, int dtype, cudaStream_t s) {
+    return dtype == FT_DTYPE_F16 ? launch_grad<__half>(jobs, p, s) : launch_grad<__nv_bfloat16>(jobs, p, s);
+}
+
+}  // namespace ft

@@ -139,6 +139,7 @@ typedef enum {
 /* Documented limits. */
 #define FT_MAX_EXPERTS 4096
 #define FT_MAX_NCOLS   65536
+#define FT_MAX_LORA_RANK 128
 
 /*
  * ft_quantize_q8_1 - fp16 activations -> Q8_1 blocks (quantize_row_q8_1 on
@@ -716,9 +717,9 @@ FT_API int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, 
 
 /* ------------------------------------------------ adapting a layer of experts
  *
- * Training of the router beside expert matrices that stay as they are: the load-balance loss
- * (ft_moe_balance_loss) and the gradients of the router (ft_moe_gate_backward) and of the weighted
- * sum (ft_moe_combine_backward).  Conventions and errors are those of the FP8 expert-layer operators
+ * What is trained and served beside expert matrices that stay as they are: the router, with the
+ * load-balance loss (ft_moe_balance_loss) and the gradients of the router (ft_moe_gate_backward) and of
+ * the weighted sum (ft_moe_combine_backward), and low-rank adapters (ft_lora_add, ft_lora_backward).  Conventions and errors are those of the FP8 expert-layer operators
  * above.  No sum depends on the order in which the GPU works: a call repeated gives the same bits. */
 
 /*
@@ -777,6 +778,52 @@ FT_API int ft_moe_gate_backward(const void* logits, int32_t dtype, int64_t row_s
 FT_API int ft_moe_combine_backward(const void* grad_y, int32_t y_dtype, const void* rows, int32_t rows_dtype,
                                    const float* topk_weights, void* grad_rows, float* grad_weights, int64_t tokens,
                                    int32_t top_k, int64_t ncols, void* stream);
+
+/*
+ * ft_lora_add - low-rank adapters beside a product whose matrix stays as it is: one adapter for all rows,
+ * one for each request of a batch, or one for each expert beside a routed product.  Slot s = t * top_k + j
+ * takes the adapter e = ids[s], a matrix A of rank rows and a matrix B of rank columns:
+ *   out[s] = add[s] + scales[e] * B[e] (A[e] x)        x: row t, or row s with x_per_slot
+ * and out[s] = add[s] for ids[s] = -1.  Products are summed in fp32; A x keeps its 24 bits where out is
+ * fp32, and 16 where out's own rounding is larger; out is rounded once.
+ *
+ *   x       device, [tokens][ncols], or [tokens * top_k][ncols], of dtype (FT_DTYPE_F16 or FT_DTYPE_BF16)
+ *   a       device, [n_adapters][rank][ncols] of dtype; b  [n_adapters][nrows][rank] of dtype.  Adapters of a
+ *           smaller rank are filled up with zeros
+ *   scales  device fp32 [n_adapters], or NULL: 1
+ *   ids     device int32 [tokens][top_k]; ids outside [-1, n_adapters) count as -1 and raise
+ *           FT_DEVERR_BAD_EXPERT_ID
+ *   add     device, [tokens][top_k][nrows] of out_dtype (FT_DTYPE_F32 or dtype), or NULL: 0; may be out
+ *   out     device, the same, out; every element is written
+ * All matrices and rows 16-byte aligned.  rank: a multiple of 8, at most FT_MAX_LORA_RANK; ncols and nrows:
+ * multiples of 8, at most FT_MAX_NCOLS; n_adapters <= FT_MAX_EXPERTS; tokens * top_k < 2^31.
+ * ft_lora_workspace_bytes returns 0 for invalid arguments; backward: for ft_lora_backward.
+ */
+FT_API size_t ft_lora_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_adapters, int32_t rank, int64_t ncols,
+                                      int64_t nrows, int32_t backward);
+FT_API int ft_lora_add(const void* x, int32_t dtype, const void* a, const void* b, const float* scales,
+                       const int32_t* ids, const void* add, void* out, int32_t out_dtype, int64_t tokens, int32_t top_k,
+                       int32_t x_per_slot, int32_t n_adapters, int32_t rank, int64_t ncols, int64_t nrows,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ft_lora_backward - the gradients of ft_lora_add (add's is grad_out itself).  With v[s] = scales[e] B[e]^T
+ * grad_out[s] and u[s] = scales[e] A[e] x, in fp32:
+ *   grad_x    = add + A[e]^T v[s], summed over the slots that share a row of x, rounded once to dtype
+ *   grad_a[e] = sum over the slots of e of v[s] x^T           fp32 [n_adapters][rank][ncols]
+ *   grad_b[e] = sum over the slots of e of grad_out[s] u[s]^T      fp32 [n_adapters][nrows][rank]
+ * 0 for adapters without a slot.  Sums run in a fixed order.
+ *
+ *   grad_out  device, [tokens][top_k][nrows] of dtype; x, a, b, scales, ids as ft_lora_add had them
+ *   add       device, of x's shape and dtype, or NULL: 0; may be grad_x
+ *   grad_x, grad_a, grad_b   each may be NULL: not wanted
+ * Alignment and limits are those of ft_lora_add.
+ */
+FT_API int ft_lora_backward(const void* grad_out, const void* x, int32_t dtype, const void* a, const void* b,
+                            const float* scales, const int32_t* ids, const void* add, void* grad_x, float* grad_a,
+                            float* grad_b, int64_t tokens, int32_t top_k, int32_t x_per_slot, int32_t n_adapters,
+                            int32_t rank, int64_t ncols, int64_t nrows, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /* ft_last_error - message of the last failing call on this host thread
  * (empty string if none).  The pointer stays valid until the next call on the

@@ -115,3 +115,78 @@ def gate_grad(logits, ids, grad_weights, score, renorm, scale, balance_part=None
     grad = torch.where(there, grad, 0.0)
     dt = logits.dtype
     return grad, 256 * U32 * mag + (U[dt] * 1.01 if dt != torch.float32 else 0.0) * grad.abs() + LEAST[dt]
+
+
+# ------------------------------------------------------------- low-rank adapters
+def chain(n):
+    """Roundings of a sum of n products on the tensor cores: a truncating adder (2 U32 a time) for each 8 of them, and 64
+    more for the join of parts and the scale."""
+    return (n / 8 + 64) * 2 * U32
+
+
+def split_error(dtype, out_dtype):
+    """What the narrow side loses as a matrix operand: it has 24 bits, or two bf16 parts beside 16-bit results (each
+    rounded to 8 bits: 2^-18), or two tf32 parts (2^-24) beside fp16."""
+    return 2.0 ** -17 if dtype == torch.bfloat16 and out_dtype != torch.float32 else 2.0 ** -22
+
+
+def lora(x, a, b, ids, scales, add, out_dtype):
+    """(out fp64, bound)."""
+    L, N, R = b.shape
+    K = x.shape[1]
+    lead = tuple(ids.shape)
+    flat = ids.reshape(-1)
+    S = flat.numel()
+    k = S // ids.shape[0] if ids.shape[0] else 1
+    rows = x if x.shape[0] == S else x.repeat_interleave(k, 0)
+    out = torch.zeros(S, N, dtype=torch.float64, device=x.device)
+    bound = torch.zeros_like(out)
+    for e in torch.unique(flat[(flat >= 0) & (flat < L)]).tolist():
+        s = (flat == e).nonzero()[:, 0]
+        c = 1.0 if scales is None else float(scales[e])
+        xe, A, B = rows[s].double(), a[e].double(), b[e].double()
+        u, eu = xe @ A.t(), (xe.abs() @ A.abs().t()) * chain(K)
+        out[s] = c * (u @ B.t())
+        bound[s] = abs(c) * ((eu + (u.abs() + eu) * (split_error(x.dtype, out_dtype) + chain(3 * R))) @ B.abs().t())
+    if add is not None:
+        out = out + add.double().reshape(S, N)
+    u = U[out_dtype] * 1.01
+    bound = (bound + out.abs() * 2 * U32) * (1 + u) + out.abs() * (u if out_dtype != torch.float32 else 0.0) + LEAST[out_dtype]
+    return out.view(*lead, N), bound.view(*lead, N)
+
+
+def lora_grads(dy, x, a, b, ids, scales, add):
+    """((grad_x, bound), (grad_a, bound), (grad_b, bound)) in fp64."""
+    L, N, R = b.shape
+    K = x.shape[1]
+    flat = ids.reshape(-1)
+    S = flat.numel()
+    k = S // ids.shape[0] if ids.shape[0] else 1
+    share = x.shape[0] != S
+    rows = x.repeat_interleave(k, 0) if share else x
+    dy = dy.reshape(S, N).double()
+    zero = lambda *s: torch.zeros(*s, dtype=torch.float64, device=x.device)      # noqa: E731
+    dr, er = zero(S, K), zero(S, K)
+    da, ea, db, eb = zero(L, R, K), zero(L, R, K), zero(L, N, R), zero(L, N, R)
+    for e in torch.unique(flat[(flat >= 0) & (flat < L)]).tolist():
+        s = (flat == e).nonzero()[:, 0]
+        c = 1.0 if scales is None else float(scales[e])
+        xe, A, B, g = rows[s].double(), a[e].double(), b[e].double(), dy[s]
+        n = len(s)
+        u, eu = c * (xe @ A.t()), abs(c) * (xe.abs() @ A.abs().t()) * chain(K)
+        v, ev = c * (g @ B), abs(c) * (g.abs() @ B.abs()) * chain(N)
+        split = 2.0 ** -17 if x.dtype == torch.bfloat16 and not share else 2.0 ** -22
+        dr[s] = v @ A
+        er[s] = (ev + (v.abs() + ev) * (split + chain(3 * R))) @ A.abs()
+        da[e] = v.t() @ xe
+        ea[e] = (ev + (v.abs() + ev) * (2.0 ** -22 + chain(3 * n))).t() @ xe.abs()
+        db[e] = g.t() @ u
+        eb[e] = g.abs().t() @ (eu + (u.abs() + eu) * (2.0 ** -22 + chain(3 * n)))
+    if share:
+        er = (er + dr.abs() * (k + 1) * U32).view(x.shape[0], k, K).sum(1)
+        dr = dr.view(x.shape[0], k, K).sum(1)
+    if add is not None:
+        dr = dr + add.double()
+    u = U[x.dtype] * 1.01
+    return ((dr, (er + dr.abs() * 2 * U32) * (1 + u) + dr.abs() * u + LEAST[x.dtype]),
+            (da, ea + LEAST[torch.float32]), (db, eb + LEAST[torch.float32]))
