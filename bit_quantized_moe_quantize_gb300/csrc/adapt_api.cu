@@ -26,6 +26,7 @@ int check_router(int64_t tokens, int32_t n_experts, int32_t top_k, int32_t dtype
 
 // ------------------------------------------------------- low-rank adapters
 constexpr int32_t kLoraSmallMean = 16;        // slots per adapter on average that go by tiles of 16
+constexpr int64_t kLoraWideMean = 512;        // from how many on by tiles of 128
 constexpr int64_t kLoraLeaderSlots = 256;     // slots up to which the CTAs find their tiles among the ids
 
 struct LoraShape {
@@ -50,20 +51,27 @@ int check_lora(int64_t tokens, int32_t top_k, int32_t n_adapters, int32_t rank, 
     return FT_OK;
 }
 
-// Slots of a tile: 64, but 16 where adapters have few slots each.
-int lora_width(int64_t n_slots, int32_t n_adapters) { return n_slots <= kLoraSmallMean * n_adapters ? 16 : 64; }
+// Slots of a tile.
+int lora_width(int64_t n_slots, int32_t n_adapters, int32_t rank) {
+    if (n_slots <= kLoraSmallMean * n_adapters) return 16;
+    return n_slots < kLoraWideMean * n_adapters || n_slots <= kLoraLeaderSlots || rank > 64 ? 64 : 128;
+}
 
 int64_t lora_tiles(int64_t n_slots, int32_t n_adapters, int width) {
     const int64_t some = n_slots < n_adapters ? n_slots : n_adapters;      // adapters that can have a tile that is not full
     return (n_slots + some * (width - 1)) / width;
 }
 
-// Chunks of the matrices' gradients at most, before each adapter's last: some three CTAs per SM, and no chunk
-// of less than 256 slots.
-int64_t lora_most_chunks(int64_t n_tiles, int width, int32_t rank, int64_t cols) {
-    const int64_t blocks = (cols + (rank <= 64 ? 255 : 127)) / (rank <= 64 ? 256 : 128);
-    const int64_t chunks = 3 * 152 / blocks > 0 ? 3 * 152 / blocks : 1, all = (n_tiles * width + 255) / 256;
-    return chunks < all ? chunks : all;
+// Chunks of the matrices' gradients, beside one more for each adapter: as many CTAs as the GPU holds at once, two per SM.
+int64_t lora_most_chunks(int32_t rank, int64_t cols) {
+    const int64_t wide = rank <= 64 ? 256 : 128, chunks = 2 * 152 / ((cols + wide - 1) / wide);
+    return chunks > 0 ? chunks : 1;
+}
+
+// Slots of a chunk: no less than 256, whole stages of 32.
+int32_t lora_chunk(int64_t n_slots, int64_t most) {
+    const int64_t slots = (n_slots + most - 1) / most;
+    return static_cast<int32_t>(slots < 256 ? 256 : (slots + 31) / 32 * 32);
 }
 
 struct LoraWs {
@@ -71,7 +79,7 @@ struct LoraWs {
     size_t u, v, rows, present, parts_a, parts_b, total;
     int width;
     int64_t n_tiles;
-    int32_t chunk_tiles;
+    int32_t chunk;
     bool ordered;
 };
 
@@ -80,16 +88,16 @@ LoraWs lora_ws(uint8_t* base, const LoraShape& h, bool backward, bool share) {
     LoraWs L{};
     const size_t S = static_cast<size_t>(h.n_slots), R = static_cast<size_t>(h.rank);
     size_t at = 0;
-    L.width = lora_width(h.n_slots, h.n_adapters);
+    L.width = lora_width(h.n_slots, h.n_adapters, h.rank);
     L.ordered = backward || h.n_slots > kLoraLeaderSlots;
     L.n_tiles = L.ordered ? lora_tiles(h.n_slots, h.n_adapters, L.width) : h.n_slots;
     if (L.ordered) at = al256(fp8_order_layout(base, h.n_slots, h.n_adapters, false, &L.order));
     L.u = take_bytes(&at, S * R * 4);
     if (backward) {
         L.v = take_bytes(&at, S * R * 4);
-        const int64_t most = lora_most_chunks(L.n_tiles, L.width, h.rank, h.ncols + h.nrows);
-        L.chunk_tiles = most > 0 ? static_cast<int32_t>((L.n_tiles + most - 1) / most) : 1;
-        const size_t chunks = static_cast<size_t>(most + h.n_adapters);
+        const int64_t most = lora_most_chunks(h.rank, h.ncols + h.nrows), all = h.n_slots / 256;
+        L.chunk = lora_chunk(h.n_slots, most);
+        const size_t chunks = static_cast<size_t>((all < most ? all : most) + h.n_adapters);      // rises with the slots
         L.parts_a = take_bytes(&at, chunks * R * h.ncols * 4);
         L.parts_b = take_bytes(&at, chunks * R * h.nrows * 4);
         if (share) {
@@ -115,6 +123,7 @@ size_t lora_most(const LoraShape& h, bool backward, bool share) {
     };
     take(h.tokens);
     take(static_cast<int64_t>(kLoraSmallMean) * h.n_adapters / h.top_k);
+    take((kLoraWideMean * h.n_adapters - 1) / h.top_k);
     take(kFastRouteSlots / h.top_k);
     take(kLoraLeaderSlots / h.top_k + 1);
     return most;
@@ -134,7 +143,7 @@ LoraPlan lora_plan(const LoraShape& h, const LoraWs& L, const int32_t* ids, cons
     p.rank = h.rank;
     p.width = L.width;
     p.n_tiles = L.n_tiles;
-    p.chunk_tiles = L.chunk_tiles;
+    p.chunk = L.chunk;
     p.err = err;
     p.down_jobs = backward ? 2 : 1;
     p.down_cols = static_cast<int32_t>(backward && h.nrows > h.ncols ? h.nrows : h.ncols);
@@ -254,7 +263,7 @@ int ft_lora_add(const void* x, int32_t dtype, const void* a, const void* b, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LoraPlan p = lora_plan(h, L, ids, scales, err, false);
     if (L.ordered)
-        if (int st = launch_fp8_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
+        if (int st = launch_lora_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
     float* u = reinterpret_cast<float*>(ws + L.u);
     const LoraDown down{x, a, u, static_cast<int32_t>(ncols), x_per_slot ? 1 : top_k, false};
     if (int st = launch_lora_down(&down, 1, p, dtype, s)) return st;
@@ -292,7 +301,7 @@ int ft_lora_backward(const void* grad_out, const void* x, int32_t dtype, const v
     uint32_t* err = nullptr;
     if (int st = fp8_error_word(&err)) return st;
     const LoraPlan p = lora_plan(h, L, ids, scales, err, true);
-    if (int st = launch_fp8_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
+    if (int st = launch_lora_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
     float *u = reinterpret_cast<float*>(ws + L.u), *v = reinterpret_cast<float*>(ws + L.v);
     const int32_t K = static_cast<int32_t>(ncols), N = static_cast<int32_t>(nrows), div = x_per_slot ? 1 : top_k;
     LoraDown down[2];

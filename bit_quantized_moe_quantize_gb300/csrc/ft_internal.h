@@ -279,14 +279,17 @@ struct LoraPlan {
     const int32_t *ids, *offsets, *tiles, *perm;      // perm null: CTAs find their tiles among the ids
     const float* scales;                              // per adapter, or null: 1
     int32_t n_slots, n_adapters, rank;
-    int width;               // slots of a tile: 64 or 16
+    int width;               // slots of a tile: 128, 64 or 16
     int64_t n_tiles;         // tiles at most
-    int32_t chunk_tiles;     // tiles of a chunk of the matrices' gradients
+    int32_t chunk;           // slots of a chunk of the matrices' gradients
     uint32_t* err;           // raised by launch_lora_down for ids that are no adapter
     int32_t down_jobs, down_cols;      // first products that a call of this kind can have, their longest rows
 };
 // Numbers of chunks that lora_grad.cu gives out at most.
-inline int64_t lora_chunks(int64_t n_tiles, int32_t n_adapters, int32_t per) { return n_tiles / per + n_adapters; }
+inline int64_t lora_chunks(int64_t n_slots, int32_t n_adapters, int32_t chunk) { return n_slots / chunk + n_adapters; }
+
+// Slots by adapter: o's offsets, tiles and perm.
+int launch_lora_order(const int32_t* ids, int64_t n_slots, int32_t n_adapters, int width, const Fp8Order& o, cudaStream_t s);
 
 struct LoraDown {      // u[s] = W z[s / div]
     const void *z, *w;

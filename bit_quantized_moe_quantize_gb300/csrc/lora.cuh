@@ -11,37 +11,45 @@
 
 namespace ft {
 
+constexpr int kLoraSmallTile = 16;      // slots of a tile: 16, 64 or 128
 constexpr int kLoraThreads = 128;
-constexpr int kLoraTile = 64, kLoraSmallTile = 16;      // slots of a tile
 
 // Slots by adapter: in order (perm, by fp8_route.cu, whose tiles have the kernel's width), or
 // perm == nullptr: found by each CTA.
 struct LoraSlots {
     const int32_t *ids, *offsets, *tiles, *perm;
-    int32_t n_slots, n_adapters;
+    int32_t n_slots, n_adapters, width;      // width: of the order's tiles
 };
 
 struct LoraTile {
     int32_t adapter;      // -1: slot `first` has none
     int32_t n;            // slots, 0: nothing to do
-    int32_t first;
+    int32_t first;        // in order; without one the slot itself
 };
 
-// Tile b of width MT; its slots go to slots[0 .. n).  By all threads of the CTA; ends behind a barrier.
+// Tile b of width MT (with an order: part b % (width / MT) of the order's tile b / (width / MT)); its slots go to slots[0 .. n).
+// By all threads of the CTA; ends behind a barrier.
 // Without an order, b is a slot, and stands for itself and those behind it that share its adapter where the number
 // of such slots before it is a multiple of MT.
 template <int MT>
-__device__ __forceinline__ LoraTile find_tile(const LoraSlots& s, int32_t b, int32_t* slots, int32_t threads) {
+__device__ __forceinline__ LoraTile find_tile(const LoraSlots& s, int32_t b, int32_t* slots) {
+    constexpr int32_t threads = kLoraThreads;
     const int32_t tid = static_cast<int32_t>(threadIdx.x), L = s.n_adapters;
     if (s.perm) {
-        if (b >= __ldg(s.tiles + L)) return LoraTile{0, 0, 0};
-        int32_t c = 0;
-        for (int32_t e0 = 0; e0 < L; e0 += threads) c += __syncthreads_count(e0 + tid < L && __ldg(s.tiles + e0 + tid) <= b);
-        const int32_t a = c - 1, first = __ldg(s.offsets + a) + (b - __ldg(s.tiles + a)) * MT;
-        const int32_t n = min(MT, __ldg(s.offsets + a + 1) - first);
-        if (tid < n) slots[tid] = __ldg(s.perm + first + tid);
+        __shared__ LoraTile found;
+        if (tid == 0) found = LoraTile{0, 0, 0};
         __syncthreads();
-        return LoraTile{a, n, slots[0]};
+        const int32_t parts = s.width / MT, tile = b / parts, skip = (b - tile * parts) * MT;
+        for (int32_t e = tid; e < L; e += threads) {      // all that is needed asked for at once
+            const int32_t t0 = __ldg(s.tiles + e), t1 = __ldg(s.tiles + e + 1), o0 = __ldg(s.offsets + e), o1 = __ldg(s.offsets + e + 1);
+            const int32_t first = o0 + (tile - t0) * s.width + skip;
+            if (t0 <= tile && tile < t1) found = LoraTile{e, max(0, min(MT, o1 - first)), first};
+        }
+        __syncthreads();
+        const LoraTile t = found;
+        if (tid < t.n) slots[tid] = __ldg(s.perm + t.first + tid);
+        __syncthreads();
+        return t;
     }
     const int32_t a = __ldg(s.ids + b);
     if (a < 0 || a >= L) return LoraTile{-1, 0, b};
@@ -49,7 +57,7 @@ __device__ __forceinline__ LoraTile find_tile(const LoraSlots& s, int32_t b, int
     for (int32_t s0 = 0; s0 < b; s0 += threads) before += __syncthreads_count(s0 + tid < b && __ldg(s.ids + s0 + tid) == a);
     if (before % MT != 0) return LoraTile{a, 0, b};
     int32_t n = 0;
-    __shared__ int32_t warp_n[kLoraThreads / 32];
+    __shared__ int32_t warp_n[threads / 32];
     for (int32_t s0 = b; s0 < s.n_slots && n < MT; s0 += threads) {
         const bool mine = s0 + tid < s.n_slots && __ldg(s.ids + s0 + tid) == a;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, mine);
@@ -186,9 +194,14 @@ struct Wide16<__half, TERMS> {
 // eight rows' words at one column lie in different banks.
 inline __host__ __device__ int32_t odd_pitch(int32_t n) { return ((n + 7) / 8 | 1) * 8; }
 
-// Neighbouring threads hold columns 2 q and 2 q + 1 of each of four tiles of eight.  Columns are put where that
-// makes eight neighbours for a thread: column 8 q + 2 j + i of 32 goes to place 8 j + 2 q + i.
-__device__ __forceinline__ int32_t spread_col(int32_t c) { return (c & ~31) | (c >> 1 & 3) << 3 | (c >> 3 & 3) << 1 | (c & 1); }
+// Neighbouring threads hold columns 2 q and 2 q + 1 of each of four tiles of eight: of 32 columns, eight a thread.  Columns are
+// put where that makes whole 16-byte words side by side for neighbours: column 8 q + 2 j + i goes to place 8 j + 2 q + i, and with
+// fp32 results, which are two words a thread, column 16 (j / 2) + 4 q + 2 (j % 2) + i does.
+template <bool FP32>
+__device__ __forceinline__ int32_t spread_col(int32_t c) {
+    if (FP32) return (c & ~31) | (c >> 4 & 1) << 4 | (c >> 1 & 1) << 3 | (c >> 2 & 3) << 1 | (c & 1);
+    return (c & ~31) | (c >> 1 & 3) << 3 | (c >> 3 & 3) << 1 | (c & 1);
+}
 
 // --------------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_size() {

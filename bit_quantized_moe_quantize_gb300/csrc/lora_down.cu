@@ -3,10 +3,15 @@
 //   forward   z = x [rows][K], W = A [R][K]                 u = A x
 //   backward  z = dy [slots][N], W = B^T of B [N][R]        B^T dy, beside the forward's u once more
 //
-// Memory-bound on z.  A tile of 64 slots (16 where adapters have few) by all R columns is a cluster's work: its
+// Memory-bound on z.  A tile of 64 or 128 slots (16 where adapters have few) by all R columns is a cluster's work: its
 // CTAs share the inner dimension, and add their sums up through each other's shared memory, in a fixed order.
 // z and W come by cp.async, four stages of 64 values; in tiles of 16 slots the four warps share a
 // stage's values instead of its slots.
+//
+// The tensor cores cut what they add to an accumulator off at its last bit: after n additions a sum is too small
+// by some n 2^-25 of itself.  So a stage's sums start from 0 and are added to the others by the CUDA cores.
+#include <type_traits>
+
 #include "lora.cuh"
 #include "ft_internal.h"
 #include "launch.cuh"
@@ -41,8 +46,9 @@ __host__ __device__ inline int32_t down_w_elems(int32_t rank) {
 // NT: tiles of eight ranks that there is room for.
 template <typename T, int MT, int NT>
 __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_constant__ DownArgs<T> a) {
-    constexpr int PARTS = MT == kLoraTile ? 1 : kLoraThreads / 32;      // warps that share a tile's sums
-    constexpr int ZR = MT / 16;
+    constexpr int THREADS = kLoraThreads, PARTS = MT == kLoraSmallTile ? THREADS / 32 : 1;      // PARTS: warps that share a tile's sums
+    constexpr int MS = MT == 128 ? 2 : 1, WARP_ROWS = 16 * MS;                                      // a warp's runs of 16 slots
+    constexpr int ZS = THREADS / 8, ZR = (MT + ZS - 1) / ZS;                                        // rows that a copy of a word per thread takes
     extern __shared__ __align__(16) uint8_t down_smem[];
     __shared__ int32_t slots[MT];
     let_next_grid_start();
@@ -56,7 +62,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
             if (id < -1 || id >= a.slots.n_adapters) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
         }
     }
-    const LoraTile tile = find_tile<MT>(a.slots, b, slots, kLoraThreads);
+    const LoraTile tile = find_tile<MT>(a.slots, b, slots);
     if (tile.n == 0) return;      // all of the cluster
     const int32_t R = a.rank, nt = R / 8, cols = job.cols, pitch = odd_pitch(R);
     const int32_t stage_elems = MT * kDownPitch + down_w_elems(R);
@@ -69,91 +75,108 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
     const T* z[ZR];
 #pragma unroll
     for (int i = 0; i < ZR; ++i) {
-        const int32_t row = tid / 8 + 16 * i;
+        const int32_t row = tid / 8 + ZS * i;
         z[i] = row < tile.n ? job.z + static_cast<int64_t>(slots[row] / job.div) * cols : nullptr;
     }
-    auto load = [&](int32_t i) {
-        const int32_t col = (c0 + i) * kDownCols;
-        T* zs = smem + i % kDownStages * stage_elems;
-        T* ws = zs + MT * kDownPitch;
-        const bool in = col + part < cols;
+    constexpr int WJ = (NT * 64 + THREADS - 1) / THREADS;      // 16-byte words of W's stage that a thread copies
+    const int32_t nt8 = R * 8;                                 // words of the stage: 64 values of R rows
+    float acc[MS][NT][4] = {};
+    auto product = [&](auto turned) {
+        constexpr bool TRANS = decltype(turned)::value;
+        int32_t from[WJ], to[WJ], edge[WJ];      // where a word comes from and goes; its first value along the inner dimension
 #pragma unroll
-        for (int j = 0; j < ZR; ++j) {
-            const bool there = in && z[j] != nullptr;
-            copy16(zs + (tid / 8 + 16 * j) * kDownPitch + part, there ? z[j] + col + part : job.z, there);
+        for (int j = 0; j < WJ; ++j) {
+            const int32_t at = tid + j * THREADS, words = TRANS ? R / 8 : kDownCols / 8, row = at / words, ch = at - row * words;
+            from[j] = TRANS ? row * R + ch * 8 : row * cols + ch * 8;
+            to[j] = row * (TRANS ? pitch : kDownPitch) + ch * 8;
+            edge[j] = at >= nt8 ? 1 << 30 : TRANS ? row : ch * 8;
         }
-        if (job.trans) {
-            const int32_t words = R / 8;
+        auto load = [&](int32_t i) {
+            const int32_t col = (c0 + i) * kDownCols;
+            T* zs = smem + i % kDownStages * stage_elems;
+            T* ws = zs + MT * kDownPitch;
 #pragma unroll
-            for (int j = 0; j < NT / 2; ++j) {
-                const int32_t at = tid + j * kLoraThreads, row = at / words, ch = at - row * words;
-                if (row < kDownCols) {
-                    const bool there = col + row < cols;
-                    copy16(ws + row * pitch + ch * 8, there ? w + static_cast<int64_t>(col + row) * R + ch * 8 : w, there);
-                }
+            for (int j = 0; j < ZR; ++j) {
+                const bool there = col + part < cols && z[j] != nullptr;
+                copy16(zs + (tid / 8 + ZS * j) * kDownPitch + part, there ? z[j] + col + part : job.z, there);
             }
-        } else {
+            const T* wc = w + static_cast<int64_t>(col) * (TRANS ? R : 1);
+#pragma unroll
+            for (int j = 0; j < WJ; ++j) {
+                const bool there = col + edge[j] < cols;
+                if (edge[j] < kDownCols) copy16(ws + to[j], there ? wc + from[j] : w, there);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kDownStages - 1; ++i) {
+            if (i < n_chunks) load(i);
+            copies_commit();
+        }
+        // what this lane gives the address of: 16 slots by 16 values of z, pairs of W's tiles by 16 values
+        const int32_t row0 = PARTS == 1 ? warp * WARP_ROWS : 0, k0 = PARTS == 1 ? 0 : warp * 16;
+        const int32_t zat = (row0 + lane % 16) * kDownPitch + lane / 16 * 8 + k0, step = TRANS ? 16 * pitch : 16;
+        int32_t wat[NT / 2];
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+            const int32_t n = min(2 * j + lane / 16, nt - 1), k = k0 + lane / 8 % 2 * 8, l = lane % 8;      // an odd last tile stands in for its neighbour
+            wat[j] = TRANS ? (k + l) * pitch + n * 8 : (n * 8 + l) * kDownPitch + k;
+        }
+        for (int32_t c = 0; c < n_chunks; ++c) {
+            copies_wait<kDownStages - 2>();
+            __syncthreads();
+            if (c + kDownStages - 1 < n_chunks) load(c + kDownStages - 1);
+            copies_commit();
+            const T* zs = smem + c % kDownStages * stage_elems;
+            const T* ws = zs + MT * kDownPitch;
+            constexpr int KK = PARTS == 1 ? kDownCols / 16 : 1;
+            uint32_t x[MS][KK][4];
+#pragma unroll
+            for (int m = 0; m < MS; ++m)
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) ldsm4(x[m][kk], zs + zat + m * 16 * kDownPitch + kk * 16, false);
 #pragma unroll
             for (int j = 0; j < NT / 2; ++j) {
-                const int32_t r = tid / 8 + 16 * j;
-                if (r < R) copy16(ws + r * kDownPitch + part, in ? w + static_cast<int64_t>(r) * cols + col + part : w, in);
+                if (2 * j >= nt) break;
+                float sum[MS][2][4] = {};
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    uint32_t b[4];
+                    ldsm4(b, ws + wat[j] + kk * step, TRANS);
+#pragma unroll
+                    for (int m = 0; m < MS; ++m) {
+                        mma16(sum[m][0], x[m][kk], b[0], b[1], T());
+                        mma16(sum[m][1], x[m][kk], b[2], b[3], T());      // behind an odd last tile: not looked at
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < MS; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[m][2 * j][i] += sum[m][0][i];
+                        acc[m][2 * j + 1][i] += sum[m][1][i];
+                    }
             }
         }
     };
-
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kDownStages - 1; ++i) {
-        if (i < n_chunks) load(i);
-        copies_commit();
-    }
-    for (int32_t c = 0; c < n_chunks; ++c) {
-        copies_wait<kDownStages - 2>();
-        __syncthreads();
-        if (c + kDownStages - 1 < n_chunks) load(c + kDownStages - 1);
-        copies_commit();
-        const T* zs = smem + c % kDownStages * stage_elems;
-        const T* ws = zs + MT * kDownPitch;
-        auto step = [&](int32_t k0, int32_t row0) {      // 16 values of 16 slots
-            uint32_t x[4];
-            ldsm4(x, zs + (row0 + lane % 16) * kDownPitch + k0 + lane / 16 * 8, false);
-            const int32_t k = k0 + lane / 8 % 2 * 8, l = lane % 8;
-#pragma unroll
-            for (int j = 0; j < NT; j += 2) {
-                if (j >= nt) break;
-                const int32_t n = min(j + lane / 16, nt - 1);      // an odd last tile stands in for its neighbour
-                uint32_t b[4];
-                if (job.trans) ldsm4(b, ws + (k + l) * pitch + n * 8, true);
-                else ldsm4(b, ws + (n * 8 + l) * kDownPitch + k, false);
-                mma16(acc[j], x, b[0], b[1], T());
-                if (j + 1 < nt) mma16(acc[j + 1], x, b[2], b[3], T());
-            }
-        };
-        if constexpr (PARTS == 1) {
-#pragma unroll
-            for (int k = 0; k < kDownCols; k += 16) step(k, warp * 16);
-        } else {
-            step(warp * 16, 0);
-        }
-    }
+    if (job.trans) product(std::true_type());
+    else product(std::false_type());
     copies_wait<0>();
     __syncthreads();
 
     float* sums = reinterpret_cast<float*>(down_smem);      // [PARTS][MT][R]
-    const int32_t row = (PARTS == 1 ? warp * 16 : warp * MT) + lane / 4;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        if (j >= nt) break;
-        const int32_t col = j * 8 + lane % 4 * 2;
-        *reinterpret_cast<float2*>(sums + row * R + col) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(sums + (row + 8) * R + col) = make_float2(acc[j][2], acc[j][3]);
+    for (int m = 0; m < MS; ++m) {
+        const int32_t row = (PARTS == 1 ? warp * WARP_ROWS + m * 16 : warp * MT) + lane / 4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (j >= nt) break;
+            const int32_t col = j * 8 + lane % 4 * 2;
+            *reinterpret_cast<float2*>(sums + row * R + col) = make_float2(acc[m][j][0], acc[m][j][1]);
+            *reinterpret_cast<float2*>(sums + (row + 8) * R + col) = make_float2(acc[m][j][2], acc[m][j][3]);
+        }
     }
     cluster_sync();
-    for (int32_t i = static_cast<int32_t>(rank) * kLoraThreads + tid; i < tile.n * R; i += static_cast<int32_t>(size) * kLoraThreads) {
+    for (int32_t i = static_cast<int32_t>(rank) * THREADS + tid; i < tile.n * R; i += static_cast<int32_t>(size) * THREADS) {
         float v = 0.0f;
         for (uint32_t q = 0; q < size; ++q)
 #pragma unroll
@@ -165,11 +188,17 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
 }
 
 template <typename T, int MT>
-int launch_down_typed(const DownArgs<T>& a, int64_t n_tiles, int jobs, unsigned cluster, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(n_tiles * cluster), static_cast<unsigned>(jobs)), block(kLoraThreads);
+int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStream_t s) {
     size_t sm = static_cast<size_t>(kDownStages) * (MT * kDownPitch + down_w_elems(a.rank)) * sizeof(T);
-    const size_t sums = static_cast<size_t>(MT == kLoraTile ? MT : 4 * MT) * a.rank * 4;
+    const size_t sums = static_cast<size_t>(MT == kLoraSmallTile ? 4 * MT : MT) * a.rank * 4;
     if (sums > sm) sm = sums;
+    // As many CTAs as the GPU holds at once, with four stages of work or more each.  By what a call can have, not what it has:
+    // leaving out one product changes no bit of the other.
+    const int64_t per_sm = static_cast<int64_t>(220 * 1024 / (sm + 1024)), fit = (per_sm < 8 ? per_sm : 8) * sm_count();
+    unsigned cluster = 1;
+    while (cluster < 8 && p.n_tiles * p.down_jobs * 2 * cluster <= fit && p.down_cols >= static_cast<int32_t>(2 * cluster) * 4 * kDownCols)
+        cluster *= 2;
+    const dim3 grid(static_cast<unsigned>(p.n_tiles * cluster), static_cast<unsigned>(jobs)), block(kLoraThreads);
     auto go = [&](auto k) { return launch_with(k, "lora_down_kernel", grid, block, sm, false, cluster, s, a); };
     if (a.rank <= 16) return go(lora_down_kernel<T, MT, 2>);
     if (a.rank <= 32) return go(lora_down_kernel<T, MT, 4>);
@@ -183,17 +212,12 @@ int launch_down(const LoraDown* jobs, int n_jobs, const LoraPlan& p, cudaStream_
     for (int i = 0; i < n_jobs; ++i)
         a.job[i] = DownJob<T>{static_cast<const T*>(jobs[i].z), static_cast<const T*>(jobs[i].w), jobs[i].u, jobs[i].cols,
                               jobs[i].div, jobs[i].trans};
-    a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters};
+    a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters, p.width};
     a.rank = p.rank;
     a.err = p.err;
-    // as many CTAs as fill the GPU a few times, each with four stages or more; the same for one of a call's
-    // products as for both, so that leaving one out changes no bit of the other
-    unsigned cluster = 1;
-    while (cluster < 8 && p.n_tiles * p.down_jobs * cluster < 3 * static_cast<int64_t>(sm_count()) &&
-           p.down_cols >= static_cast<int32_t>(2 * cluster) * 4 * kDownCols)
-        cluster *= 2;
-    return p.width == kLoraTile ? launch_down_typed<T, kLoraTile>(a, p.n_tiles, n_jobs, cluster, s)
-                                : launch_down_typed<T, kLoraSmallTile>(a, p.n_tiles, n_jobs, cluster, s);
+    if (p.width == 128) return launch_down_typed<T, 128>(a, p, n_jobs, s);
+    if (p.width == 64) return launch_down_typed<T, 64>(a, p, n_jobs, s);
+    return launch_down_typed<T, kLoraSmallTile>(a, p, n_jobs, s);
 }
 
 }  // namespace

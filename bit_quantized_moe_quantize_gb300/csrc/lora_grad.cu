@@ -21,7 +21,7 @@ namespace ft {
 
 namespace {
 
-constexpr int kGradThreads = 256, kGradSlots = 32, kGradStages = 3;
+constexpr int kGradThreads = 256, kGradSlots = 32, kGradStages = 3, kGradRing = 8;
 
 template <typename T>
 struct GradJob {
@@ -37,7 +37,7 @@ struct GradArgs {
     GradJob<T> job[2];
     LoraSlots slots;
     const float* scales;
-    int32_t rank, per, width, blocks0;      // blocks0: blocks of columns of the first job
+    int32_t rank, per, blocks0;      // per: slots of a chunk; blocks0: blocks of columns of the first job
 };
 
 // Chunk number b: its adapter, whether it has others, its first slot in order and its slots (0: none).
@@ -46,23 +46,25 @@ struct Chunk {
     bool alone;
 };
 
-__device__ __forceinline__ Chunk find_chunk(const LoraSlots& s, int32_t b, int32_t per, int32_t width) {
-    const int32_t L = s.n_adapters, tid = static_cast<int32_t>(threadIdx.x);
-    int32_t c = 0;
-    for (int32_t e0 = 0; e0 < L; e0 += kGradThreads) {
-        const int32_t e = e0 + tid;
-        c += __syncthreads_count(e < L && __ldg(s.tiles + e) / per + e <= b);
+__device__ __forceinline__ Chunk find_chunk(const LoraSlots& s, int32_t b, int32_t per) {
+    __shared__ Chunk found;
+    const int32_t tid = static_cast<int32_t>(threadIdx.x);
+    if (tid == 0) found = Chunk{0, 0, 0, true};
+    __syncthreads();
+    for (int32_t e = tid; e < s.n_adapters; e += kGradThreads) {
+        const int32_t o0 = __ldg(s.offsets + e), o1 = __ldg(s.offsets + e + 1), j = b - (o0 / per + e);
+        // j * per stays small where it is looked at: numbers rise with the slots
+        if (j >= 0 && j <= (o1 - o0) / per && j * per < o1 - o0) found = Chunk{e, o0 + j * per, min(per, o1 - o0 - j * per), o1 - o0 <= per};
     }
-    const int32_t a = c - 1, t0 = __ldg(s.tiles + a), n_tiles = __ldg(s.tiles + a + 1) - t0, j = b - (t0 / per + a);
-    if (j * per >= n_tiles) return Chunk{a, 0, 0, true};
-    const int32_t at = __ldg(s.offsets + a) + j * per * width;
-    return Chunk{a, at, min(per * width, __ldg(s.offsets + a + 1) - at), n_tiles <= per};
+    __syncthreads();
+    return found;
 }
 
 // MR: tiles of 16 ranks that there is room for; NJ: tiles of eight columns that a warp has.
 template <typename T, int MR, int NJ>
-__global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_constant__ GradArgs<T> a) {
+__global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid_constant__ GradArgs<T> a) {
     constexpr int CC = 8 * NJ * (kGradThreads / 32), ZP = CC + 8;      // columns of the CTA, their pitch
+    constexpr int TERMS = 3;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     constexpr int PAIRS = MR;      // pairs of ranks that a thread has of a stage
     extern __shared__ __align__(16) uint8_t grad_smem[];
@@ -70,13 +72,14 @@ __global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_co
     const bool second = static_cast<int32_t>(blockIdx.y) >= a.blocks0;
     const GradJob<T>& job = a.job[second ? 1 : 0];
     const int32_t col0 = (static_cast<int32_t>(blockIdx.y) - (second ? a.blocks0 : 0)) * CC;
-    const Chunk ck = find_chunk(a.slots, static_cast<int32_t>(blockIdx.x), a.per, a.width);
+    const Chunk ck = find_chunk(a.slots, static_cast<int32_t>(blockIdx.x), a.per);
     if (ck.n == 0) return;
     const int32_t R = a.rank, r16 = (R + 15) / 16 * 16, mr = r16 / 16, cols = job.cols;
     const int32_t wp = odd_pitch(r16), wf = r16 + 4;      // pitch of a part's rows; of fp32 rows (fp16)
-    const int32_t w_bytes = BF ? 3 * kGradSlots * wp * 2 : kGradSlots * wf * 4;
+    const int32_t w_bytes = BF ? TERMS * kGradSlots * wp * 2 : kGradSlots * wf * 4;
     T* zs_all = reinterpret_cast<T*>(grad_smem);
     uint8_t* ws_all = grad_smem + kGradStages * kGradSlots * ZP * sizeof(T);
+    __shared__ int32_t ring[kGradRing][kGradSlots];      // slots of the stages from the one at work on
     const int32_t* perm = a.slots.perm + ck.first;
     const float scale = a.scales ? __ldg(a.scales + ck.adapter) : 1.0f;
     const int32_t steps = (ck.n + kGradSlots - 1) / kGradSlots;
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_co
         for (int j = 0; j < ZI; ++j) {
             const int32_t row = tid / ZW + ZROWS * j, s = i * kGradSlots + row;
             const bool there = s < ck.n && col0 + zc < cols;
-            const T* src = there ? job.z + static_cast<int64_t>(__ldg(perm + s) / job.div) * cols + col0 + zc : job.z;
+            const T* src = there ? job.z + static_cast<int64_t>(ring[i % kGradRing][row] / job.div) * cols + col0 + zc : job.z;
             copy16(zs + row * ZP + zc, src, there);
         }
     };
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_co
             const int32_t at = tid + j * kGradThreads, row = at / (8 * mr), r = (at - row * 8 * mr) * 2, s = i * kGradSlots + row;
             wreg[j] = make_float2(0.0f, 0.0f);
             if (j < mr && s < ck.n && r < R) {
-                const float2 v = *reinterpret_cast<const float2*>(job.w + static_cast<int64_t>(__ldg(perm + s)) * R + r);
+                const float2 v = *reinterpret_cast<const float2*>(job.w + static_cast<int64_t>(ring[i % kGradRing][row]) * R + r);
                 wreg[j] = make_float2(v.x * scale, v.y * scale);
             }
         }
@@ -114,10 +117,10 @@ __global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_co
             if (j >= mr) break;
             const int32_t at = tid + j * kGradThreads, row = at / (8 * mr), r = (at - row * 8 * mr) * 2;
             if constexpr (BF) {
-                uint32_t p[3];
-                split_pair<3>(wreg[j].x, wreg[j].y, p);
+                uint32_t p[TERMS];
+                split_pair<TERMS>(wreg[j].x, wreg[j].y, p);
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
+                for (int t = 0; t < TERMS; ++t)
                     *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(ws) + (t * kGradSlots + row) * wp + r) = p[t];
             } else {
                 float* f = reinterpret_cast<float*>(ws) + row * wf + r;
@@ -127,13 +130,13 @@ __global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_co
         }
     };
 
-    float acc[MR][NJ][4];
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) acc[m][j][x] = 0.0f;
+    // the slots are asked for four stages ahead of the rows they name
+    constexpr int AHEAD = 4;
+    if (tid < AHEAD * kGradSlots && tid < ck.n) ring[tid / kGradSlots][tid % kGradSlots] = __ldg(perm + tid);
+    auto slot_of = [&](int32_t i) { return tid < kGradSlots && i * kGradSlots + tid < ck.n ? __ldg(perm + i * kGradSlots + tid) : 0; };
+    int32_t next = slot_of(AHEAD);
+    __syncthreads();
+    float acc[MR][NJ][4] = {};
 #pragma unroll
     for (int i = 0; i < kGradStages - 1; ++i) {
         if (i < steps) load_z(i);
@@ -147,36 +150,43 @@ __global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_co
         __syncthreads();
         if (i + kGradStages - 1 < steps) load_z(i + kGradStages - 1);
         copies_commit();
+        if (tid < kGradSlots) ring[(i + AHEAD) % kGradRing][tid] = next;
+        next = slot_of(i + AHEAD + 1);
         if (i + 1 < steps) store_w(i + 1);      // the buffer that the step before last read
         if (i + 2 < steps) load_w(i + 2);
         const T* zs = zs_all + i % kGradStages * kGradSlots * ZP;
         const uint8_t* ws = ws_all + i % 2 * w_bytes;
+        uint32_t b[kGradSlots / 16][NJ][2];
 #pragma unroll
-        for (int k = 0; k < kGradSlots; k += 16) {
-            uint32_t b[NJ][2];
+        for (int k = 0; k < kGradSlots / 16; ++k)
 #pragma unroll
             for (int j = 0; j < NJ; j += 2) {
                 uint32_t x[4];
-                ldsm4(x, zs + (k + lane % 16) * ZP + warp * 8 * NJ + (j + lane / 16) * 8, true);
-                b[j][0] = x[0];
-                b[j][1] = x[1];
-                b[j + 1][0] = x[2];
-                b[j + 1][1] = x[3];
+                ldsm4(x, zs + (k * 16 + lane % 16) * ZP + warp * 8 * NJ + (j + lane / 16) * 8, true);
+                b[k][j][0] = x[0];
+                b[k][j][1] = x[1];
+                b[k][j + 1][0] = x[2];
+                b[k][j + 1][1] = x[3];
             }
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                if (m >= mr) break;
-                if constexpr (BF) {
+        for (int m = 0; m < MR; ++m) {
+            if (m >= mr) break;
+            float sum[NJ][4] = {};      // of the stage: a chain of few additions that cut off (lora_down.cu)
+            if constexpr (BF) {
 #pragma unroll
-                    for (int t = 2; t >= 0; --t) {
+                for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+                    for (int k = 0; k < kGradSlots / 16; ++k) {
                         uint32_t x[4];
                         const T* p = reinterpret_cast<const T*>(ws) + t * kGradSlots * wp;
-                        ldsm4(x, p + (k + lane / 16 * 8 + lane % 8) * wp + m * 16 + lane / 8 % 2 * 8, true);
+                        ldsm4(x, p + (k * 16 + lane / 16 * 8 + lane % 8) * wp + m * 16 + lane / 8 % 2 * 8, true);
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) mma16(acc[m][j], x, b[j][0], b[j][1], T());
+                        for (int j = 0; j < NJ; ++j) mma16(sum[j], x, b[k][j][0], b[k][j][1], T());
                     }
-                } else {
-                    const float* f = reinterpret_cast<const float*>(ws) + (k + lane % 4 * 2) * wf + m * 16 + lane / 4;
+            } else {
+#pragma unroll
+                for (int k = 0; k < kGradSlots / 16; ++k) {
+                    const float* f = reinterpret_cast<const float*>(ws) + (k * 16 + lane % 4 * 2) * wf + m * 16 + lane / 4;
                     float v[8];      // ranks by h, slots 2 q (+1) and 2 q + 8 (+1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -187,9 +197,13 @@ __global__ void __launch_bounds__(kGradThreads) lora_grad_kernel(const __grid_co
                         }
                     Wide16<T, 2> wide;
                     wide.set(v);
-                    wide.mul(acc[m], b);
+                    wide.mul(sum, b[k]);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[m][j][x] += sum[j][x];
         }
     }
     copies_wait<0>();
@@ -222,16 +236,16 @@ struct JoinArgs {
     float* out[2];
     const float* parts[2];
     int64_t size4[2];      // in words of 16 bytes
-    const int32_t* tiles;
+    const int32_t* offsets;
     int32_t per;
 };
 
 __global__ void __launch_bounds__(kGradThreads) lora_join_kernel(const JoinArgs a) {
     const int32_t e = static_cast<int32_t>(blockIdx.x);
-    const int32_t t0 = __ldg(a.tiles + e), n_tiles = __ldg(a.tiles + e + 1) - t0;
-    if (n_tiles > 0 && n_tiles <= a.per) return;
-    const int32_t chunks = (n_tiles + a.per - 1) / a.per;
-    const int64_t first = t0 / a.per + e;
+    const int32_t o0 = __ldg(a.offsets + e), n = __ldg(a.offsets + e + 1) - o0;
+    if (n > 0 && n <= a.per) return;
+    const int32_t chunks = n / a.per + (n % a.per != 0);
+    const int64_t first = o0 / a.per + e;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (!a.out[j]) continue;
@@ -271,13 +285,12 @@ int launch_grad(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
         ++n;
     }
     if (n == 0) return FT_OK;
-    a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters};
+    a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters, p.width};
     a.scales = p.scales;
     a.rank = p.rank;
-    a.per = p.chunk_tiles;
-    a.width = p.width;
+    a.per = p.chunk;
     a.blocks0 = blocks[0];
-    const int64_t chunks = lora_chunks(p.n_tiles, p.n_adapters, p.chunk_tiles);
+    const int64_t chunks = lora_chunks(p.n_slots, p.n_adapters, p.chunk);
     const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(blocks[0] + blocks[1])), block(kGradThreads);
     const int32_t r16 = (p.rank + 15) / 16 * 16;
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
@@ -290,8 +303,8 @@ int launch_grad(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
     else if (p.rank <= 64) st = go(lora_grad_kernel<T, 4, 4>);
     else st = go(lora_grad_kernel<T, 8, 2>);
     if (st) return st;
-    j.tiles = p.tiles;
-    j.per = p.chunk_tiles;
+    j.offsets = p.offsets;
+    j.per = p.chunk;
     int64_t y = 4 * static_cast<int64_t>(sm_count()) / p.n_adapters;
     const int64_t most = (std::max(j.size4[0], j.size4[1]) + kGradThreads - 1) / kGradThreads;
     y = y < 1 ? 1 : y < most ? y : most;

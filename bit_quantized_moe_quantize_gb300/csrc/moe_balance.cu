@@ -25,6 +25,7 @@ namespace {
 
 constexpr int32_t kSingleRounds = 4, kSingleSeqs = 8;      // batches that one CTA works out
 constexpr int32_t kLeastRounds = 2;                         // rounds of rows that a CTA takes at least
+constexpr int kAtOnce = 2;                                  // rows of a lane group under way together
 
 struct Piece {
     float p;
@@ -62,19 +63,31 @@ __device__ __forceinline__ double cta_sum(double v, double* part) {
     return v;
 }
 
+// seq_of for the whole CTA, which looks at 256 offsets at once.
+__device__ __forceinline__ int32_t seq_of_cta(const int32_t* offsets, int32_t n, int64_t r) {
+    if (n > 16 * kRowThreads) return seq_of(offsets, n, r);
+    int32_t c = 0;
+    for (int32_t s0 = 0; s0 < n; s0 += kRowThreads) {
+        const int32_t s = s0 + static_cast<int32_t>(threadIdx.x);
+        c += __syncthreads_count(s < n && __ldg(offsets + s) <= r);
+    }
+    return c > 0 ? c - 1 : 0;
+}
+
 // Loss and scales from the sequences' rows and dots (per_seq of them each), by one CTA.
 __device__ void balance_finish(const BalanceArgs& a, int32_t per_seq, double* part) {
     double full = 0.0, loss = 0.0;
     for (int32_t s = threadIdx.x; s < a.n_seqs; s += kRowThreads) full += __ldcg(a.seq_rows + s) > 0 ? 1.0 : 0.0;
     full = cta_sum(full, part);
-    for (int32_t s = threadIdx.x; s < a.n_seqs; s += kRowThreads) {
-        const double n = __ldcg(a.seq_rows + s);
-        const double scale = n > 0.0 ? a.n_experts / (a.top_k * n * n * full) : 0.0;
-        a.seq_scale[s] = static_cast<float>(scale);
-        double dot = 0.0;
-        for (int32_t b = 0; b < per_seq; ++b) dot += __ldcg(a.dots + static_cast<int64_t>(s) * per_seq + b);
-        if (n > 0.0) loss += scale * dot;
-    }
+    const float some = a.n_experts / (a.top_k * static_cast<float>(full));
+    auto scale_of = [&](int32_t s) {
+        const float n = static_cast<float>(__ldcg(a.seq_rows + s));
+        return n > 0.0f ? some / (n * n) : 0.0f;
+    };
+    for (int32_t s = threadIdx.x; s < a.n_seqs; s += kRowThreads) a.seq_scale[s] = scale_of(s);
+    const int64_t dots = static_cast<int64_t>(a.n_seqs) * per_seq;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < dots; i += kRowThreads) loss += static_cast<double>(scale_of(static_cast<int32_t>(i / per_seq))) * __ldcg(a.dots + i);
     loss = cta_sum(loss, part);
     if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
 }
@@ -99,7 +112,7 @@ __global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const Balance
     __syncthreads();
 
     int64_t r = r0;
-    for (int32_t s = a.single || !a.offsets ? 0 : seq_of(a.offsets, S, r0); s < S && (a.single || r < r1); ++s) {
+    for (int32_t s = a.single || !a.offsets ? 0 : seq_of_cta(a.offsets, S, r0); s < S && (a.single || r < r1); ++s) {
         const int64_t start = seq_start(a.offsets, s, a.tokens), end = seq_start(a.offsets, s + 1, a.tokens);
         const int64_t lo = start > r ? start : r, hi = end < r1 ? end : r1;
         if (lo >= hi && !a.single) continue;
@@ -109,19 +122,31 @@ __global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const Balance
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
         int32_t rows = 0;
-        for (int64_t base = lo; base < hi; base += G::kRows) {      // whole groups: their lanes meet in shuffles
-            const int64_t t = base + G::row();
-            const bool there = t < hi;
-            float p[STEPS][8];
-            load_logits<T, L, STEPS>(static_cast<const T*>(a.logits) + (there ? t : lo) * a.stride, E, a.wide, p);
-            const RowScale sc = row_scores<L, STEPS>(g, a.score, p);
-            const float inv = a.score == FT_SCORE_SOFTMAX ? 1.0f : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
-            if (there) {
-                rows += sc.any ? 1 : 0;
+        for (int64_t base = lo; base < hi; base += kAtOnce * G::kRows) {      // whole groups: their lanes meet in shuffles
+            float p[kAtOnce][STEPS][8];
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i)
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int64_t t = base + u * G::kRows + G::row();
+                load_logits<T, L, STEPS>(static_cast<const T*>(a.logits) + (t < hi ? t : lo) * a.stride, E, a.wide, p[u]);
+            }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(p[i][j], inv, acc[i][j]);
+            for (int u = 0; u < kAtOnce; ++u) {
+                RowScale sc;
+                float inv = 1.0f;
+                if (a.score == FT_SCORE_SOFTMAX) {
+                    sc = row_softmax<L, STEPS>(g, p[u]);
+                } else {
+                    float rest[STEPS][8];
+                    sc = row_sigmoid<L, STEPS>(g, p[u], rest);
+                    inv = __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
+                }
+                if (base + u * G::kRows + G::row() < hi) {
+                    rows += sc.any ? 1 : 0;
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(p[u][i][j], inv, acc[i][j]);
+                }
             }
         }
         for (int64_t i = lo * a.top_k + tid; i < hi * a.top_k; i += kRowThreads) {

@@ -8,8 +8,8 @@
 //   sigmoid:  d l_e = s_e (1 - s_e) H_e + p_e (1 - s_e) (a_e - sum_i a_i p_i),  p = s / max(sum, 1e-30)
 //
 // Memory-bound: a row is read once, by the lanes that hold its experts, and written once.  The slots' parts
-// lie in a row of shared memory that their lanes add to and the experts' lanes read; ids that repeat in a
-// row are added in the order of the slots.
+// lie in a row of shared memory that their lanes write to and the experts' lanes read.  Ids that repeat in a
+// row, found by whose mark stays, are added in the order of the slots.
 #include <type_traits>
 
 #include "router_rows.cuh"
@@ -33,10 +33,11 @@ struct GateGradArgs {
     int64_t tokens, stride;
     int32_t n_experts, top_k, score, renormalize, n_seqs;
     float scale;
-    bool wide, wide_out;
+    bool wide, wide_out, wide_counts;
 };
 
-template <typename T, int L, int STEPS>
+// ONE: no more slots than lanes that share them, so that each has one.
+template <typename T, int L, int STEPS, bool ONE>
 __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradArgs a) {
     using G = RowGroup<L>;
     constexpr int WIDTH = 8 * L * STEPS, LANES = L < 32 ? L : 32;      // LANES: lanes that share the slots
@@ -45,21 +46,35 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
     const G g{part};
     const int32_t E = a.n_experts, k = a.top_k;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * G::kRows + G::row();
-    const bool there = t0 < a.tokens;
+    const bool there = t0 < a.tokens, soft = a.score == FT_SCORE_SOFTMAX;
     const int64_t t = there ? t0 : a.tokens - 1;
     const T* row = static_cast<const T*>(a.logits) + t * a.stride;
     float* extra = extra_all + G::row() * WIDTH;
-    float p[STEPS][8];
+    // the first LANES lanes of the group take a slot each (a whole CTA's other warps take none)
+    const bool mine = L <= 32 || threadIdx.x < 32;
+    const int32_t lane = static_cast<int32_t>(G::lane());
+    struct Slot {
+        int32_t e;        // expert, -1: takes no part
+        float l, gw;      // its logit, the weight's gradient
+    };
+    auto slot = [&](int32_t j) {
+        Slot x{-1, 0.0f, 0.0f};
+        if (!mine || !there || j >= k) return x;
+        const int32_t e = __ldg(a.ids + t * k + j);
+        x.gw = __ldg(a.grad_weights + t * k + j);
+        if (e < -1 || e >= E) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
+        else if (e >= 0) {
+            x.l = to_f32<T>(row[e]);
+            if (x.l > -INFINITY) x.e = e;      // masked: no part in anything
+        }
+        if (x.e < 0) x.gw = 0.0f;
+        return x;
+    };
+    Slot x{-1, 0.0f, 0.0f};
+    if (ONE && a.grad_weights) x = slot(lane);      // on its way while the row is worked on
+    float p[STEPS][8], rest[STEPS][8];              // rest: sigmoid, 1 - score
     load_logits<T, L, STEPS>(row, E, a.wide, p);
-    float rest[STEPS][8];      // sigmoid: 1 - s
-    const bool soft = a.score == FT_SCORE_SOFTMAX;
-    if (!soft) {
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) rest[i][j] = p[i][j] > -INFINITY ? sigmoid_of(-p[i][j]) : 0.0f;
-    }
-    const RowScale sc = row_scores<L, STEPS>(g, a.score, p);
+    const RowScale sc = soft ? row_softmax<L, STEPS>(g, p) : row_sigmoid<L, STEPS>(g, p, rest);
     float dots = 0.0f;         // softmax: sum over slots of h_j s[id_j]
 
     if (a.grad_weights) {
@@ -69,53 +84,72 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
             z[0] = z[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
         g.sync();
-        // the first LANES lanes of the group take a slot each (a whole CTA's other warps take none)
-        const bool mine = L <= 32 || threadIdx.x < 32;
-        const int32_t lane = static_cast<int32_t>(G::lane());
-        auto slot = [&](int32_t j, float& s, float& r, float& gw) {      // a slot's expert, score, 1 - score, gradient
-            s = r = gw = 0.0f;
-            int32_t e = mine && there && j < k ? __ldg(a.ids + t * k + j) : -1;
-            if (e < -1 || e >= E) {
-                if (mine && there && j < k) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
-                e = -1;
+        auto score_of = [&](const Slot& x, float& s, float& r) {      // score and 1 - score (softmax: 1)
+            s = r = 0.0f;
+            if (x.e < 0) return;
+            if (soft) {
+                s = soft_exp(x.l, sc.top) * sc.inv;
+                r = 1.0f;
+            } else {
+                sigmoid_pair(x.l, s, r);
             }
-            if (e >= 0) {
-                const float l = to_f32<T>(row[e]);
-                if (!(l > -INFINITY)) return -1;      // masked: no part in anything
-                s = soft ? soft_exp(l, sc.top) * sc.inv : sigmoid_of(l);
-                r = soft ? 1.0f : sigmoid_of(-l);
-                gw = __ldg(a.grad_weights + t * k + j);
-            }
-            return e;
         };
-        float W = 0.0f, m = 0.0f, s, r, gw;
-        for (int32_t j0 = 0; j0 < k; j0 += LANES) {
-            slot(j0 + lane, s, r, gw);
-            W += s;
-            m = fmaf(gw, s, m);
-        }
-        W = g.sum(W);
-        m = g.sum(m);
-        const bool spread = a.renormalize && W > kScoreTiny;
-        const float c = a.renormalize ? __fdiv_rn(a.scale, fmaxf(W, kScoreTiny)) : a.scale;
-        const float mean = spread ? __fdiv_rn(m, W) : 0.0f;
-        for (int32_t j0 = 0; j0 < k; j0 += LANES) {
-            const int32_t e = slot(j0 + lane, s, r, gw);
-            const float h = c * (gw - mean), d = (soft ? s : s * r) * h;
-            if (e >= 0) dots = fmaf(h, s, dots);
-            if (mine) {
-                // lanes of this row with the same expert add in turn, lowest first
-                const uint32_t same = __match_any_sync(0xFFFFFFFFu, e < 0 ? -1 - static_cast<int32_t>(lane_id())
-                                                                           : e * G::kRows + static_cast<int32_t>(G::row()));
-                const int32_t turn = __popc(same & ((1u << lane_id()) - 1u));
-                const int32_t turns = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(turn));
-                for (int32_t i = 0; i <= turns; ++i) {
-                    if (e >= 0 && turn == i) extra[e] += d;
-                    __syncwarp();
+        float W = 0.0f, m = 0.0f, s = 0.0f, r = 0.0f;
+        if (ONE) score_of(x, s, r);
+        if (a.renormalize) {
+            if (ONE) {
+                W = s;
+                m = x.gw * s;
+            } else {
+                for (int32_t j0 = 0; j0 < k; j0 += LANES) {
+                    x = slot(j0 + lane);
+                    score_of(x, s, r);
+                    W += s;
+                    m = fmaf(x.gw, s, m);
                 }
             }
+            W = g.sum(W);
+            m = g.sum(m);
         }
-        dots = g.sum(dots);      // by all lanes: rows of a warp may differ in what follows
+        const bool spread = a.renormalize && W > kScoreTiny;
+        const float c = a.renormalize ? __fdividef(a.scale, fmaxf(W, kScoreTiny)) : a.scale;
+        const float mean = spread ? __fdividef(m, W) : 0.0f;
+        for (int32_t j0 = 0; j0 < k; j0 += LANES) {
+            if (!ONE) {
+                x = slot(j0 + lane);
+                score_of(x, s, r);
+            }
+            const float h = c * (x.gw - mean), d = s * r * h;
+            if (x.e >= 0) dots = fmaf(h, s, dots);
+            if (mine) {
+                // every lane marks its expert; where all marks stay, no id repeats
+                int32_t* mark = reinterpret_cast<int32_t*>(extra);
+                const float was = !ONE && x.e >= 0 ? extra[x.e] : 0.0f;
+                __syncwarp();
+                if (x.e >= 0) mark[x.e] = static_cast<int32_t>(lane_id());
+                __syncwarp();
+                const bool alone = x.e < 0 || mark[x.e] == static_cast<int32_t>(lane_id());
+                if (__all_sync(0xFFFFFFFFu, alone)) {
+                    if (x.e >= 0) extra[x.e] = was + d;
+                } else {
+                    __syncwarp();
+                    if (x.e >= 0) extra[x.e] = was;
+                    __syncwarp();
+                    // lanes of this row with the same expert add in turn, lowest first
+                    const uint32_t same = __match_any_sync(0xFFFFFFFFu, x.e < 0 ? -1 - static_cast<int32_t>(lane_id())
+                                                                                 : x.e * G::kRows + static_cast<int32_t>(G::row()));
+                    const int32_t turn = __popc(same & ((1u << lane_id()) - 1u));
+                    const int32_t turns = static_cast<int32_t>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(turn)));
+                    for (int32_t i = 0; i <= turns; ++i) {
+                        if (x.e >= 0 && turn == i) extra[x.e] += d;
+                        __syncwarp();
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // by all lanes where it is one row's affair: rows of a warp may differ
+        if (soft && __any_sync(0xFFFFFFFFu, !spread)) dots = g.sum(dots);
         if (!soft || spread) dots = 0.0f;
         g.sync();
     }
@@ -138,11 +172,17 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int32_t e0 = first_expert<L>(i);
+            if (a.wide_counts && e0 + 8 <= E) {
+                const int4 x0 = __ldg(reinterpret_cast<const int4*>(count + e0)), x1 = __ldg(reinterpret_cast<const int4*>(count + e0) + 1);
+                c[i][0] = static_cast<float>(x0.x), c[i][1] = static_cast<float>(x0.y), c[i][2] = static_cast<float>(x0.z);
+                c[i][3] = static_cast<float>(x0.w), c[i][4] = static_cast<float>(x1.x), c[i][5] = static_cast<float>(x1.y);
+                c[i][6] = static_cast<float>(x1.z), c[i][7] = static_cast<float>(x1.w);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                c[i][j] = e0 + j < E ? static_cast<float>(__ldg(count + e0 + j)) : 0.0f;
-                mean = fmaf(c[i][j], p[i][j], mean);
+                for (int j = 0; j < 8; ++j) c[i][j] = e0 + j < E ? static_cast<float>(__ldg(count + e0 + j)) : 0.0f;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mean = fmaf(c[i][j], p[i][j], mean);
         }
         mean = g.sum(mean);
         if (!soft) mean = sc.sum > kScoreTiny ? __fdividef(mean, sc.sum) : 0.0f;
@@ -206,14 +246,20 @@ int launch_gate_grad(const GateGradParams& p, const void* logits, int dtype, int
     const int size = dtype == FT_DTYPE_F32 ? 4 : 2;
     a.wide = stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
     a.wide_out = static_cast<int64_t>(p.n_experts) * size % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    a.wide_counts = p.n_experts % 4 == 0 && reinterpret_cast<uintptr_t>(p.counts) % 16 == 0;
     return with_row_lanes(p.n_experts, [&](auto lanes, auto steps) {
         constexpr int L = decltype(lanes)::value, N = decltype(steps)::value, ROWS = kRowThreads / L;
         const int64_t ctas = (p.tokens + ROWS - 1) / ROWS;
         if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "too many tokens for one launch");
         const dim3 grid(static_cast<unsigned>(ctas)), block(kRowThreads);
-        if (dtype == FT_DTYPE_F32) gate_grad_kernel<float, L, N><<<grid, block, 0, s>>>(a);
-        else if (dtype == FT_DTYPE_F16) gate_grad_kernel<__half, L, N><<<grid, block, 0, s>>>(a);
-        else gate_grad_kernel<__nv_bfloat16, L, N><<<grid, block, 0, s>>>(a);
+        auto go = [&](auto type) {
+            using T = decltype(type);
+            if (p.top_k <= (L < 32 ? L : 32)) gate_grad_kernel<T, L, N, true><<<grid, block, 0, s>>>(a);
+            else gate_grad_kernel<T, L, N, false><<<grid, block, 0, s>>>(a);
+        };
+        if (dtype == FT_DTYPE_F32) go(float());
+        else if (dtype == FT_DTYPE_F16) go(__half());
+        else go(__nv_bfloat16());
         return check_launch("gate_grad_kernel", grid, block, 0);
     });
 }

@@ -68,7 +68,20 @@ __device__ __forceinline__ void load_logits(const T* row, int32_t E, bool wide, 
     }
 }
 
-__device__ __forceinline__ float sigmoid_of(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+// e^x, off by (1.5 |x| + 4) 2^-24 of itself: argument times log2(e) rounded once, two units in ex2.
+__device__ __forceinline__ float row_exp(float x) { return __expf(x); }
+
+// sigmoid(l) and 1 - sigmoid(l), neither by a difference.
+__device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
+    const float e = row_exp(-fabsf(l)), r = __fdividef(1.0f, 1.0f + e), small = e * r;
+    s = l >= 0.0f ? r : small;
+    rest = l >= 0.0f ? small : r;
+}
+
+__device__ __forceinline__ float soft_exp(float l, float top) {
+    if (!(l > -INFINITY)) return 0.0f;
+    return l == top ? 1.0f : row_exp(l - top);
+}
 
 // What a row's scores need beside its logits: for softmax the largest logit and the reciprocal of the
 // sum of exponentials (experts at +inf share the weight); for the sigmoid the sum of the scores.
@@ -78,47 +91,50 @@ struct RowScale {
     bool any;            // some expert is there
 };
 
-__device__ __forceinline__ float soft_exp(float l, float top) {
-    if (!(l > -INFINITY)) return 0.0f;
-    return l == top ? 1.0f : expf(l - top);
-}
-
-// In place: logits -> softmax probabilities, or sigmoid scores (0 where masked).
+// In place: logits -> softmax probabilities.
 template <int L, int STEPS>
-__device__ __forceinline__ RowScale row_scores(const RowGroup<L>& g, int32_t score, float (&l)[STEPS][8]) {
-    RowScale r{-INFINITY, 0.0f, 0.0f, false};
+__device__ __forceinline__ RowScale row_softmax(const RowGroup<L>& g, float (&l)[STEPS][8]) {
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, l[s][i]);
-    r.top = g.max(top);
-    r.any = r.top > -INFINITY;
-    if (score == FT_SCORE_SOFTMAX) {
+    top = g.max(top);
+    const bool any = top > -INFINITY;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                l[s][i] = soft_exp(l[s][i], r.top);
-                sum += l[s][i];
-            }
-        sum = g.sum(sum);
-        r.inv = r.any ? __frcp_rn(sum) : 0.0f;      // the largest logit alone makes the sum 1 or more
+        for (int i = 0; i < 8; ++i) {
+            l[s][i] = soft_exp(l[s][i], top);
+            sum += l[s][i];
+        }
+    sum = g.sum(sum);
+    const float inv = any ? __fdividef(1.0f, sum) : 0.0f;      // the largest logit alone makes the sum 1 or more
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) l[s][i] *= r.inv;
-    } else {
+        for (int i = 0; i < 8; ++i) l[s][i] *= inv;
+    return RowScale{top, inv, 0.0f, any};
+}
+
+// In place: logits -> sigmoid scores, 0 where masked; rest: 1 - score there.
+template <int L, int STEPS>
+__device__ __forceinline__ RowScale row_sigmoid(const RowGroup<L>& g, float (&l)[STEPS][8], float (&rest)[STEPS][8]) {
+    float sum = 0.0f, there = 0.0f;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                l[s][i] = l[s][i] > -INFINITY ? sigmoid_of(l[s][i]) : 0.0f;
-                sum += l[s][i];
-            }
-        r.sum = g.sum(sum);
-    }
-    return r;
+        for (int i = 0; i < 8; ++i) {
+            const bool ok = l[s][i] > -INFINITY;
+            float v;
+            sigmoid_pair(l[s][i], v, rest[s][i]);
+            l[s][i] = ok ? v : 0.0f;
+            rest[s][i] = ok ? rest[s][i] : 0.0f;
+            there = ok ? 1.0f : there;
+            sum += l[s][i];
+        }
+    sum = g.sum(sum);
+    return RowScale{0.0f, 0.0f, sum, g.max(there) > 0.0f};
 }
 
 // Sequences of packed rows: offsets[0 .. n] ascending, or null: one sequence of all rows.  Whatever the

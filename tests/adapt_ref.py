@@ -72,9 +72,10 @@ def weights(x, ids, score, renorm, scale):
 def gate_grad(logits, ids, grad_weights, score, renorm, scale, balance_part=None):
     """(gradient fp64, bound of an fp32 evaluation rounded once).  balance_part: (counts, seq_scale, grad_loss, offsets).
 
-    A score is off by at most (|l - top| + 12) 2^-24 of itself (the exponential's argument and value, the sum of
-    positive terms, reciprocal, product); with |l - top| < 40 that is 52 roundings.  A gradient is a sum of
-    products of at most four such factors: 256 roundings of the magnitudes cover them."""
+    A score is off by at most (1.5 |l - top| + 4) 2^-24 of itself from the exponential (its argument times log2(e) rounded,
+    log2(e) itself, two units in the power), and 8 more from the sum of positive terms, the quotient and the
+    product; with |l - top| < 32 that is 60 roundings.  A gradient is a sum of products of at most four such
+    factors: 256 roundings of the magnitudes cover them."""
     T, E = logits.shape
     x = logits.double()
     there = x > -math.inf

@@ -67,8 +67,8 @@ def check_balance(ft, x, ids, score, off):
     want, wc, ws = A.balance(torch.where(x > -math.inf, x, -math.inf).double(), ids, score, off)
     assert torch.equal(counts.long(), wc)
     inside(scale, ws, 2 * U32 * ws, "seq_scale")
-    # p: 52 roundings (gate_grad's); its sum over at most 128 rows of a lane, 64 lanes' and 608 CTAs' parts by
-    # groups, all positive: under 200 roundings; counts and scales are exact but for one
+    # p: 60 roundings (gate_grad's); its sum over at most 128 rows of a lane, 64 lanes' and 608 CTAs' parts by
+    # groups, all positive: under 190 roundings; counts and scales are exact but for one
     inside(loss, want, 256 * U32 * want, "loss")
     return loss, counts, scale
 
