@@ -11,7 +11,8 @@
 // are added up in order into a piece of the workspace, beside the counts.  A second launch adds the pieces of
 // each sequence and expert up, and its last CTA to finish makes the loss; sums run in a fixed order, and only
 // whole numbers are added by atomics.  CTA c's piece of sequence s is number c + s: both only rise along
-// the rows, so that no two meet.  Batches of a few rows are one CTA's work, in one launch.
+// the rows, so that no two meet.  Batches of some rows and few sequences are one cluster's work, in one launch:
+// its CTAs add up each other's shares through shared memory.
 #include <algorithm>
 #include <type_traits>
 
@@ -23,7 +24,8 @@ namespace ft {
 
 namespace {
 
-constexpr int32_t kSingleRounds = 4, kSingleSeqs = 8;      // batches that one CTA works out
+constexpr int32_t kSingleRounds = 8, kSingleSeqs = 8;      // batches that one cluster works out: rounds of rows of a CTA, sequences
+constexpr unsigned kSingleCtas = 8;
 constexpr int32_t kLeastRounds = 2;                         // rounds of rows that a CTA takes at least
 constexpr int kAtOnce = 2;                                  // rows of a lane group under way together
 
@@ -40,7 +42,7 @@ struct BalanceArgs {
     int32_t n_experts, top_k, score, n_seqs;
     Piece* pieces;        // [ctas + n_seqs][n_experts]
     int32_t* piece_rows;  // [ctas + n_seqs]
-    double* dots;         // [n_seqs][blocks of 8 experts] (single: [n_seqs])
+    float* dots;          // [n_seqs][blocks of 8 experts]
     int32_t* seq_rows;    // [n_seqs]
     uint32_t* ticket;
     uint32_t* err;
@@ -50,14 +52,20 @@ struct BalanceArgs {
     bool wide, single;
 };
 
+// What a sequence of n rows has in the loss, of `full` sequences with rows.
+__device__ __forceinline__ float seq_scale_of(const BalanceArgs& a, int32_t n, int32_t full) {
+    const float rows = static_cast<float>(n);
+    return n > 0 ? __fdiv_rn(static_cast<float>(a.n_experts), a.top_k * static_cast<float>(full) * rows * rows) : 0.0f;
+}
+
 // Sum over the CTA, in a fixed order, for every thread.
-__device__ __forceinline__ double cta_sum(double v, double* part) {
+__device__ __forceinline__ float cta_sum(float v, float* part) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     __syncthreads();
     if ((threadIdx.x & 31u) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
+    v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kRowThreads / 32; ++w) v += part[w];
     return v;
@@ -74,38 +82,23 @@ __device__ __forceinline__ int32_t seq_of_cta(const int32_t* offsets, int32_t n,
     return c > 0 ? c - 1 : 0;
 }
 
-// Loss and scales from the sequences' rows and dots (per_seq of them each), by one CTA.
-__device__ void balance_finish(const BalanceArgs& a, int32_t per_seq, double* part) {
-    double full = 0.0, loss = 0.0;
-    for (int32_t s = threadIdx.x; s < a.n_seqs; s += kRowThreads) full += __ldcg(a.seq_rows + s) > 0 ? 1.0 : 0.0;
-    full = cta_sum(full, part);
-    const float some = a.n_experts / (a.top_k * static_cast<float>(full));
-    auto scale_of = [&](int32_t s) {
-        const float n = static_cast<float>(__ldcg(a.seq_rows + s));
-        return n > 0.0f ? some / (n * n) : 0.0f;
-    };
-    for (int32_t s = threadIdx.x; s < a.n_seqs; s += kRowThreads) a.seq_scale[s] = scale_of(s);
-    const int64_t dots = static_cast<int64_t>(a.n_seqs) * per_seq;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < dots; i += kRowThreads) loss += static_cast<double>(scale_of(static_cast<int32_t>(i / per_seq))) * __ldcg(a.dots + i);
-    loss = cta_sum(loss, part);
-    if (threadIdx.x == 0) *a.loss = static_cast<float>(loss);
-}
-
 template <typename T, int L, int STEPS>
 __global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const BalanceArgs a) {
     using G = RowGroup<L>;
     constexpr int WIDTH = 8 * L * STEPS;      // experts that the lanes have room for
     extern __shared__ __align__(16) uint8_t balance_smem[];
-    double* part64 = reinterpret_cast<double*>(balance_smem);                  // [8]
-    float* part = reinterpret_cast<float*>(part64 + 8);                        // [8]
+    float* part_sum = reinterpret_cast<float*>(balance_smem);                    // [8]
+    float* part = part_sum + 8;                                                  // [8]
     int32_t* group_rows = reinterpret_cast<int32_t*>(part + 8);                // [rows at once]
     float* red = reinterpret_cast<float*>(group_rows + (G::kRows + 3) / 4 * 4);      // [rows at once][WIDTH]
     int32_t* hist = reinterpret_cast<int32_t*>(red + G::kRows * WIDTH);        // [E]
+    float* share = reinterpret_cast<float*>(hist + a.n_experts);               // [E] P of this CTA (single)
+    __shared__ float seq_dot[kSingleSeqs];                                     // of the experts that this CTA adds up
+    __shared__ int32_t seq_n[kSingleSeqs];                                     // rows of this CTA
     let_next_grid_start();
     const G g{part};
     const int32_t E = a.n_experts, S = a.n_seqs, tid = threadIdx.x;
-    const int64_t r0 = blockIdx.x * a.rows_per_cta;
+    const int64_t r0 = min(a.tokens, blockIdx.x * a.rows_per_cta);
     const int64_t r1 = r0 + a.rows_per_cta < a.tokens ? r0 + a.rows_per_cta : a.tokens;
     if (blockIdx.x == 0 && tid == 0 && !a.single) *a.ticket = 0;
     for (int32_t e = tid; e < E; e += kRowThreads) hist[e] = 0;
@@ -132,9 +125,10 @@ __global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const Balance
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
                 RowScale sc;
-                float inv = 1.0f;
+                float inv;
                 if (a.score == FT_SCORE_SOFTMAX) {
                     sc = row_softmax<L, STEPS>(g, p[u]);
+                    inv = sc.inv;
                 } else {
                     float rest[STEPS][8];
                     sc = row_sigmoid<L, STEPS>(g, p[u], rest);
@@ -163,46 +157,71 @@ __global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const Balance
         if (G::lane() == 0) group_rows[G::row()] = rows;
         __syncthreads();
         const int64_t piece = blockIdx.x + static_cast<int64_t>(s);
-        double dot = 0.0;
         for (int32_t e = tid; e < E; e += kRowThreads) {
             float p = 0.0f;
 #pragma unroll 8
             for (int i = 0; i < G::kRows; ++i) p += red[i * WIDTH + e];
-            const int32_t c = hist[e];
-            hist[e] = 0;
             if (a.single) {
-                a.counts[static_cast<int64_t>(s) * E + e] = c;
-                dot += static_cast<double>(c) * p;
+                share[e] = p;
             } else {
-                a.pieces[piece * E + e] = Piece{p, c};
+                a.pieces[piece * E + e] = Piece{p, hist[e]};
+                hist[e] = 0;
             }
         }
-        if (a.single) dot = cta_sum(dot, part64);
         if (tid == 0) {
             int32_t n = 0;
             for (int i = 0; i < G::kRows; ++i) n += group_rows[i];
-            if (a.single) {
-                a.seq_rows[s] = n;
-                a.dots[s] = dot;
-            } else {
-                a.piece_rows[piece] = n;
+            if (a.single) seq_n[s] = n;
+            else a.piece_rows[piece] = n;
+        }
+        if (a.single) {
+            cluster_sync();
+            const uint32_t size = cluster_size(), rank = cluster_rank();
+            float dot = 0.0f;
+            for (int32_t e = tid * static_cast<int32_t>(size) + static_cast<int32_t>(rank); e < E; e += kRowThreads * static_cast<int32_t>(size)) {
+                float p = 0.0f;
+                int32_t c = 0;
+                for (uint32_t q = 0; q < size; ++q) {
+                    p += cluster_load(share + e, q);
+                    c += __float_as_int(cluster_load(hist + e, q));
+                }
+                a.counts[static_cast<int64_t>(s) * E + e] = c;
+                dot = fmaf(static_cast<float>(c), p, dot);
             }
+            dot = cta_sum(dot, part_sum);
+            if (tid == 0) seq_dot[s] = dot;
+            cluster_sync();      // the others have read this CTA's shares
+            for (int32_t e = tid; e < E; e += kRowThreads) hist[e] = 0;
         }
         __syncthreads();
         if (lo < hi) r = hi;
     }
-    if (a.single) {
-        __threadfence();
-        __syncthreads();
-        balance_finish(a, 1, part64);
+    if (!a.single) return;
+    if (cluster_rank() == 0 && tid == 0) {
+        int32_t n[kSingleSeqs], full = 0;
+        for (int32_t s = 0; s < S; ++s) {
+            n[s] = 0;
+            for (uint32_t q = 0; q < cluster_size(); ++q) n[s] += __float_as_int(cluster_load(seq_n + s, q));
+            full += n[s] > 0 ? 1 : 0;
+        }
+        float loss = 0.0f;
+        for (int32_t s = 0; s < S; ++s) {
+            const float scale = seq_scale_of(a, n[s], full);
+            float dot = 0.0f;
+            for (uint32_t q = 0; q < cluster_size(); ++q) dot += cluster_load(seq_dot + s, q);
+            a.seq_scale[s] = scale;
+            loss = fmaf(scale, dot, loss);
+        }
+        *a.loss = loss;
     }
+    cluster_sync();      // no CTA leaves while its sums are read
 }
 
 // Adds the pieces up: TASK threads per sequence and eight experts, a lane per expert in each of TASK / 8
 // groups that share the pieces.
 template <int TASK>
 __global__ void __launch_bounds__(kRowThreads) balance_join_kernel(const BalanceArgs a) {
-    __shared__ double part64[8];
+    __shared__ float part_sum[8];
     __shared__ Piece red[kRowThreads / 32][8];
     __shared__ int32_t red_rows[kRowThreads / 32];
     __shared__ bool last;
@@ -253,7 +272,7 @@ __global__ void __launch_bounds__(kRowThreads) balance_join_kernel(const Balance
             }
         }
     }
-    double dot = static_cast<double>(c) * p;
+    float dot = static_cast<float>(c) * p;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
     if (there && sub < 8) {
@@ -269,7 +288,18 @@ __global__ void __launch_bounds__(kRowThreads) balance_join_kernel(const Balance
     __syncthreads();
     if (!last) return;
     __threadfence();
-    balance_finish(a, blocks, part64);
+    float full = 0.0f, loss = 0.0f;
+    for (int32_t i = threadIdx.x; i < a.n_seqs; i += kRowThreads) full += __ldcg(a.seq_rows + i) > 0 ? 1.0f : 0.0f;
+    const int32_t sequences = static_cast<int32_t>(cta_sum(full, part_sum));
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < tasks; i += kRowThreads) {
+        const int32_t seq = static_cast<int32_t>(i / blocks);
+        const float scale = seq_scale_of(a, __ldcg(a.seq_rows + seq), sequences);
+        if (i % blocks == 0) a.seq_scale[seq] = scale;
+        loss = fmaf(scale, __ldcg(a.dots + i), loss);
+    }
+    loss = cta_sum(loss, part_sum);
+    if (threadIdx.x == 0) *a.loss = loss;
 }
 
 // Rows that a CTA takes at once.
@@ -290,7 +320,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t balance_workspace(int64_t tokens, int32_t n_experts, int32_t n_seqs) {
     const size_t S = static_cast<size_t>(n_seqs);
     const size_t pieces = static_cast<size_t>(balance_ctas(tokens, n_experts, kBalanceCtas)) + S;
-    return 256 + up256(pieces * n_experts * sizeof(Piece)) + up256(pieces * 4) + up256(S * ((n_experts + 7) / 8) * 8) + up256(S * 4);
+    return 256 + up256(pieces * n_experts * sizeof(Piece)) + up256(pieces * 4) + up256(S * ((n_experts + 7) / 8) * 4) + up256(S * 4);
 }
 
 int launch_balance(const BalanceParams& p, const void* logits, int dtype, int64_t stride, const int32_t* ids,
@@ -310,10 +340,13 @@ int launch_balance(const BalanceParams& p, const void* logits, int dtype, int64_
     a.loss = loss;
     a.counts = counts;
     a.seq_scale = seq_scale;
-    a.single = p.tokens == 0 || (p.tokens <= kSingleRounds * rows_at_once(p.n_experts) && p.n_seqs <= kSingleSeqs);
-    int64_t ctas = a.single ? 1 : balance_ctas(p.tokens, p.n_experts, std::min<int64_t>(4 * sm_count(), kBalanceCtas));
+    const int64_t rows = rows_at_once(p.n_experts);
+    a.single = p.n_seqs <= kSingleSeqs && p.tokens <= kSingleCtas * kSingleRounds * rows;
+    unsigned cluster = 1;
+    while (a.single && cluster < kSingleCtas && p.tokens > static_cast<int64_t>(cluster) * kLeastRounds * rows) cluster *= 2;
+    int64_t ctas = a.single ? cluster : balance_ctas(p.tokens, p.n_experts, std::min<int64_t>(4 * sm_count(), kBalanceCtas));
     a.rows_per_cta = p.tokens > 0 ? (p.tokens + ctas - 1) / ctas : 1;
-    ctas = p.tokens > 0 ? (p.tokens + a.rows_per_cta - 1) / a.rows_per_cta : 1;
+    if (!a.single && p.tokens > 0) ctas = (p.tokens + a.rows_per_cta - 1) / a.rows_per_cta;
     const size_t pieces = static_cast<size_t>(ctas) + p.n_seqs, S = static_cast<size_t>(p.n_seqs);
     a.ticket = reinterpret_cast<uint32_t*>(ws);
     ws += 256;
@@ -321,18 +354,18 @@ int launch_balance(const BalanceParams& p, const void* logits, int dtype, int64_
     ws += up256(pieces * p.n_experts * sizeof(Piece));
     a.piece_rows = reinterpret_cast<int32_t*>(ws);
     ws += up256(pieces * 4);
-    a.dots = reinterpret_cast<double*>(ws);
-    ws += up256(S * ((p.n_experts + 7) / 8) * 8);
+    a.dots = reinterpret_cast<float*>(ws);
+    ws += up256(S * ((p.n_experts + 7) / 8) * 4);
     a.seq_rows = reinterpret_cast<int32_t*>(ws);
     const int size = dtype == FT_DTYPE_F32 ? 4 : 2;
     a.wide = stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
     const dim3 block(kRowThreads), grid(static_cast<unsigned>(ctas));
     const int st = with_row_lanes(p.n_experts, [&](auto lanes, auto steps) {
         constexpr int L = decltype(lanes)::value, N = decltype(steps)::value, ROWS = kRowThreads / L;
-        const size_t sm = 64 + 32 + (ROWS + 3) / 4 * 16 + static_cast<size_t>(ROWS) * 8 * L * N * 4 + 4 * static_cast<size_t>(p.n_experts);
-        if (dtype == FT_DTYPE_F32) return launch_with(balance_rows_kernel<float, L, N>, "balance_rows_kernel", grid, block, sm, false, 1, s, a);
-        if (dtype == FT_DTYPE_F16) return launch_with(balance_rows_kernel<__half, L, N>, "balance_rows_kernel", grid, block, sm, false, 1, s, a);
-        return launch_with(balance_rows_kernel<__nv_bfloat16, L, N>, "balance_rows_kernel", grid, block, sm, false, 1, s, a);
+        const size_t sm = 64 + (ROWS + 3) / 4 * 16 + static_cast<size_t>(ROWS) * 8 * L * N * 4 + 8 * static_cast<size_t>(p.n_experts);
+        if (dtype == FT_DTYPE_F32) return launch_with(balance_rows_kernel<float, L, N>, "balance_rows_kernel", grid, block, sm, false, cluster, s, a);
+        if (dtype == FT_DTYPE_F16) return launch_with(balance_rows_kernel<__half, L, N>, "balance_rows_kernel", grid, block, sm, false, cluster, s, a);
+        return launch_with(balance_rows_kernel<__nv_bfloat16, L, N>, "balance_rows_kernel", grid, block, sm, false, cluster, s, a);
     });
     if (st || a.single) return st;
     // a warp per eight experts of a sequence once the sequences are many and their pieces few

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
             s = r = 0.0f;
             if (x.e < 0) return;
             if (soft) {
-                s = soft_exp(x.l, sc.top) * sc.inv;
+                s = soft_exp(x.l, sc.top) * sc.inv;      // +inf at the top: 1, others 0
                 r = 1.0f;
             } else {
                 sigmoid_pair(x.l, s, r);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
             seq = seq_of(a.offsets, a.n_seqs, t);
             inside = seq_start(a.offsets, seq, a.tokens) <= t && t < seq_start(a.offsets, seq + 1, a.tokens);
         }
-        const float inv = soft ? 1.0f : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
+        const float inv = soft ? sc.inv : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
         coef = inside ? __ldg(a.grad_loss) * __ldg(a.seq_scale + seq) * inv : 0.0f;
         count = a.counts + static_cast<int64_t>(seq) * E;
     }
@@ -185,9 +185,11 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
             for (int j = 0; j < 8; ++j) mean = fmaf(c[i][j], p[i][j], mean);
         }
         mean = g.sum(mean);
-        if (!soft) mean = sc.sum > kScoreTiny ? __fdividef(mean, sc.sum) : 0.0f;
+        mean = soft ? mean * sc.inv : sc.sum > kScoreTiny ? __fdividef(mean, sc.sum) : 0.0f;
     }
     if (!there) return;
+    // with softmax, p holds exponentials: what multiplies them carries the reciprocal of their sum
+    if (soft) dots *= sc.inv;
     T* out = static_cast<T*>(a.out) + t * E;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
@@ -203,10 +205,8 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float v = count ? coef * (c[i][j] - mean) : 0.0f;
-            if (soft) v -= dots;
-            v = p[i][j] > 0.0f ? v * p[i][j] : 0.0f;      // a masked expert, or one too far away, takes none
-            if (!soft) v *= rest[i][j];
-            v += x[j];
+            v = soft ? v - dots : v * rest[i][j];
+            v = fmaf(p[i][j], v, x[j]);
             o[j] = from_f32<T>(v);
         }
         if (a.wide_out && e0 + 8 <= E) {

@@ -64,12 +64,17 @@ __device__ __forceinline__ void load_logits(const T* row, int32_t E, bool wide, 
             for (int i = 0; i < 8; ++i) l[s][i] = e0 + i < E ? to_f32<T>(row[e0 + i]) : -INFINITY;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l[s][i] = l[s][i] > -INFINITY ? l[s][i] : -INFINITY;
+        for (int i = 0; i < 8; ++i) l[s][i] = fmaxf(l[s][i], -INFINITY);      // the operand that is no NaN
     }
 }
 
-// e^x, off by (1.5 |x| + 4) 2^-24 of itself: argument times log2(e) rounded once, two units in ex2.
-__device__ __forceinline__ float row_exp(float x) { return __expf(x); }
+// e^x for x <= 0, off by (1.5 |x| + 4) 2^-24 of itself: the argument times log2(e) rounded, log2(e) itself, two units
+// in the power; below 2^-126 it is 0.
+__device__ __forceinline__ float row_exp(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
 
 // sigmoid(l) and 1 - sigmoid(l), neither by a difference.
 __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
@@ -78,20 +83,17 @@ __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
     rest = l >= 0.0f ? small : r;
 }
 
-__device__ __forceinline__ float soft_exp(float l, float top) {
-    if (!(l > -INFINITY)) return 0.0f;
-    return l == top ? 1.0f : row_exp(l - top);
-}
-
-// What a row's scores need beside its logits: for softmax the largest logit and the reciprocal of the
-// sum of exponentials (experts at +inf share the weight); for the sigmoid the sum of the scores.
+// What a row's scores need beside its logits.
 struct RowScale {
-    float top, inv;      // softmax
-    float sum;           // sigmoid
+    float top, inv;      // softmax: the largest logit, the reciprocal of the sum of exponentials (0 where no expert is there)
+    float sum;           // sigmoid: of the scores
     bool any;            // some expert is there
 };
 
-// In place: logits -> softmax probabilities.
+// exp(l - top) of an expert that is there; experts at +inf share the softmax.
+__device__ __forceinline__ float soft_exp(float l, float top) { return l == top ? 1.0f : row_exp(l - top); }
+
+// In place: logits -> exp(l - top), 0 where masked; times RowScale::inv, the softmax.
 template <int L, int STEPS>
 __device__ __forceinline__ RowScale row_softmax(const RowGroup<L>& g, float (&l)[STEPS][8]) {
     float top = -INFINITY, sum = 0.0f;
@@ -101,20 +103,23 @@ __device__ __forceinline__ RowScale row_softmax(const RowGroup<L>& g, float (&l)
         for (int i = 0; i < 8; ++i) top = fmaxf(top, l[s][i]);
     top = g.max(top);
     const bool any = top > -INFINITY;
+    float base = any ? top : 0.0f;
+    if (top == INFINITY) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l[s][i] = l[s][i] == INFINITY ? 0.0f : -INFINITY;
+        base = 0.0f;
+    }
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            l[s][i] = soft_exp(l[s][i], top);
+            l[s][i] = row_exp(l[s][i] - base);
             sum += l[s][i];
         }
     sum = g.sum(sum);
-    const float inv = any ? __fdividef(1.0f, sum) : 0.0f;      // the largest logit alone makes the sum 1 or more
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) l[s][i] *= inv;
-    return RowScale{top, inv, 0.0f, any};
+    return RowScale{top, any ? __fdividef(1.0f, sum) : 0.0f, 0.0f, any};      // the largest logit alone makes the sum 1 or more
 }
 
 // In place: logits -> sigmoid scores, 0 where masked; rest: 1 - score there.
