@@ -197,22 +197,32 @@ __global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const Balance
         if (lo < hi) r = hi;
     }
     if (!a.single) return;
-    if (cluster_rank() == 0 && tid == 0) {
+    if (cluster_rank() == 0 && tid < 32) {
+        // lane q asks CTA q; every lane gets the sums
         int32_t n[kSingleSeqs], full = 0;
-        for (int32_t s = 0; s < S; ++s) {
-            n[s] = 0;
-            for (uint32_t q = 0; q < cluster_size(); ++q) n[s] += __float_as_int(cluster_load(seq_n + s, q));
+        float dot[kSingleSeqs], loss = 0.0f;
+        const bool there = static_cast<uint32_t>(tid) < cluster_size();
+#pragma unroll
+        for (int s = 0; s < kSingleSeqs; ++s) {
+            n[s] = there && s < S ? __float_as_int(cluster_load(seq_n + s, tid)) : 0;
+            dot[s] = there && s < S ? cluster_load(seq_dot + s, tid) : 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < kSingleSeqs; ++s) {
+#pragma unroll
+            for (int o = static_cast<int>(kSingleCtas) / 2; o > 0; o >>= 1) {
+                n[s] += __shfl_xor_sync(0xFFFFFFFFu, n[s], o);
+                dot[s] += __shfl_xor_sync(0xFFFFFFFFu, dot[s], o);
+            }
             full += n[s] > 0 ? 1 : 0;
         }
-        float loss = 0.0f;
-        for (int32_t s = 0; s < S; ++s) {
+#pragma unroll
+        for (int s = 0; s < kSingleSeqs; ++s) {
             const float scale = seq_scale_of(a, n[s], full);
-            float dot = 0.0f;
-            for (uint32_t q = 0; q < cluster_size(); ++q) dot += cluster_load(seq_dot + s, q);
-            a.seq_scale[s] = scale;
-            loss = fmaf(scale, dot, loss);
+            if (tid == 0 && s < S) a.seq_scale[s] = scale;
+            loss = fmaf(scale, dot[s], loss);
         }
-        *a.loss = loss;
+        if (tid == 0) *a.loss = loss;
     }
     cluster_sync();      // no CTA leaves while its sums are read
 }

@@ -37,7 +37,7 @@ struct GateGradArgs {
 };
 
 // ONE: no more slots than lanes that share them, so that each has one.
-template <typename T, int L, int STEPS, bool ONE>
+template <typename T, int L, int STEPS, bool ONE, bool SOFT>
 __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradArgs a) {
     using G = RowGroup<L>;
     constexpr int WIDTH = 8 * L * STEPS, LANES = L < 32 ? L : 32;      // LANES: lanes that share the slots
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
     const G g{part};
     const int32_t E = a.n_experts, k = a.top_k;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * G::kRows + G::row();
-    const bool there = t0 < a.tokens, soft = a.score == FT_SCORE_SOFTMAX;
+    const bool there = t0 < a.tokens;
     const int64_t t = there ? t0 : a.tokens - 1;
     const T* row = static_cast<const T*>(a.logits) + t * a.stride;
     float* extra = extra_all + G::row() * WIDTH;
@@ -72,9 +72,11 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
     };
     Slot x{-1, 0.0f, 0.0f};
     if (ONE && a.grad_weights) x = slot(lane);      // on its way while the row is worked on
-    float p[STEPS][8], rest[STEPS][8];              // rest: sigmoid, 1 - score
+    float p[STEPS][8], rest[SOFT ? 1 : STEPS][8];              // rest: 1 - score
     load_logits<T, L, STEPS>(row, E, a.wide, p);
-    const RowScale sc = soft ? row_softmax<L, STEPS>(g, p) : row_sigmoid<L, STEPS>(g, p, rest);
+    RowScale sc;
+    if constexpr (SOFT) sc = row_softmax<L, STEPS>(g, p);
+    else sc = row_sigmoid<L, STEPS>(g, p, rest);
     float dots = 0.0f;         // softmax: sum over slots of h_j s[id_j]
 
     if (a.grad_weights) {
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
         auto score_of = [&](const Slot& x, float& s, float& r) {      // score and 1 - score (softmax: 1)
             s = r = 0.0f;
             if (x.e < 0) return;
-            if (soft) {
+            if (SOFT) {
                 s = soft_exp(x.l, sc.top) * sc.inv;      // +inf at the top: 1, others 0
                 r = 1.0f;
             } else {
@@ -149,8 +151,8 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
             }
         }
         // by all lanes where it is one row's affair: rows of a warp may differ
-        if (soft && __any_sync(0xFFFFFFFFu, !spread)) dots = g.sum(dots);
-        if (!soft || spread) dots = 0.0f;
+        if (SOFT && __any_sync(0xFFFFFFFFu, !spread)) dots = g.sum(dots);
+        if (!SOFT || spread) dots = 0.0f;
         g.sync();
     }
 
@@ -163,11 +165,11 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
             seq = seq_of(a.offsets, a.n_seqs, t);
             inside = seq_start(a.offsets, seq, a.tokens) <= t && t < seq_start(a.offsets, seq + 1, a.tokens);
         }
-        const float inv = soft ? sc.inv : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
+        const float inv = SOFT ? sc.inv : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
         coef = inside ? __ldg(a.grad_loss) * __ldg(a.seq_scale + seq) * inv : 0.0f;
         count = a.counts + static_cast<int64_t>(seq) * E;
     }
-    float c[STEPS][8];
+    float c[STEPS][8] = {};
     if (count) {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
@@ -185,11 +187,11 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
             for (int j = 0; j < 8; ++j) mean = fmaf(c[i][j], p[i][j], mean);
         }
         mean = g.sum(mean);
-        mean = soft ? mean * sc.inv : sc.sum > kScoreTiny ? __fdividef(mean, sc.sum) : 0.0f;
+        mean = SOFT ? mean * sc.inv : sc.sum > kScoreTiny ? __fdividef(mean, sc.sum) : 0.0f;
     }
     if (!there) return;
     // with softmax, p holds exponentials: what multiplies them carries the reciprocal of their sum
-    if (soft) dots *= sc.inv;
+    if (SOFT) dots *= sc.inv;
     T* out = static_cast<T*>(a.out) + t * E;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
@@ -204,10 +206,10 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float v = count ? coef * (c[i][j] - mean) : 0.0f;
-            v = soft ? v - dots : v * rest[i][j];
-            v = fmaf(p[i][j], v, x[j]);
-            o[j] = from_f32<T>(v);
+            float v;
+            if constexpr (SOFT) v = fmaf(coef, c[i][j] - mean, -dots);
+            else v = coef * (c[i][j] - mean) * rest[i][j];
+            o[j] = from_f32<T>(fmaf(p[i][j], v, x[j]));
         }
         if (a.wide_out && e0 + 8 <= E) {
 #pragma unroll
@@ -254,8 +256,14 @@ int launch_gate_grad(const GateGradParams& p, const void* logits, int dtype, int
         const dim3 grid(static_cast<unsigned>(ctas)), block(kRowThreads);
         auto go = [&](auto type) {
             using T = decltype(type);
-            if (p.top_k <= (L < 32 ? L : 32)) gate_grad_kernel<T, L, N, true><<<grid, block, 0, s>>>(a);
-            else gate_grad_kernel<T, L, N, false><<<grid, block, 0, s>>>(a);
+            const bool one = p.top_k <= (L < 32 ? L : 32);
+            if (p.score == FT_SCORE_SOFTMAX) {
+                if (one) gate_grad_kernel<T, L, N, true, true><<<grid, block, 0, s>>>(a);
+                else gate_grad_kernel<T, L, N, false, true><<<grid, block, 0, s>>>(a);
+            } else {
+                if (one) gate_grad_kernel<T, L, N, true, false><<<grid, block, 0, s>>>(a);
+                else gate_grad_kernel<T, L, N, false, false><<<grid, block, 0, s>>>(a);
+            }
         };
         if (dtype == FT_DTYPE_F32) go(float());
         else if (dtype == FT_DTYPE_F16) go(__half());
