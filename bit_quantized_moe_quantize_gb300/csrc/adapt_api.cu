@@ -62,9 +62,9 @@ int64_t lora_tiles(int64_t n_slots, int32_t n_adapters, int width) {
     return (n_slots + some * (width - 1)) / width;
 }
 
-// Chunks of the matrices' gradients, beside one more for each adapter: as many CTAs as the GPU holds at once, two per SM.
-int64_t lora_most_chunks(int32_t rank, int64_t cols) {
-    const int64_t wide = rank <= 64 ? 256 : 128, chunks = 2 * 152 / ((cols + wide - 1) / wide);
+// Chunks of the matrices' gradients, beside one more for each adapter: a CTA per SM, each with 256 columns.
+int64_t lora_most_chunks(int64_t ncols, int64_t nrows) {
+    const int64_t chunks = 152 / ((ncols + 255) / 256 + (nrows + 255) / 256);
     return chunks > 0 ? chunks : 1;
 }
 
@@ -76,7 +76,7 @@ int32_t lora_chunk(int64_t n_slots, int64_t most) {
 
 struct LoraWs {
     Fp8Order order;
-    size_t u, v, rows, present, parts_a, parts_b, total;
+    size_t u, v, u_parts, v_parts, rows, present, parts_a, parts_b, total;
     int width;
     int64_t n_tiles;
     int32_t chunk;
@@ -95,7 +95,9 @@ LoraWs lora_ws(uint8_t* base, const LoraShape& h, bool backward, bool share) {
     L.u = take_bytes(&at, S * R * 4);
     if (backward) {
         L.v = take_bytes(&at, S * R * 4);
-        const int64_t most = lora_most_chunks(h.rank, h.ncols + h.nrows), all = h.n_slots / 256;
+        L.u_parts = take_bytes(&at, 3 * S * R * 2);
+        L.v_parts = take_bytes(&at, 3 * S * R * 2);
+        const int64_t most = lora_most_chunks(h.ncols, h.nrows), all = h.n_slots / 256;
         L.chunk = lora_chunk(h.n_slots, most);
         const size_t chunks = static_cast<size_t>((all < most ? all : most) + h.n_adapters);      // rises with the slots
         L.parts_a = take_bytes(&at, chunks * R * h.ncols * 4);
@@ -265,7 +267,7 @@ int ft_lora_add(const void* x, int32_t dtype, const void* a, const void* b, cons
     if (L.ordered)
         if (int st = launch_lora_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
     float* u = reinterpret_cast<float*>(ws + L.u);
-    const LoraDown down{x, a, u, static_cast<int32_t>(ncols), x_per_slot ? 1 : top_k, false};
+    const LoraDown down{x, a, u, nullptr, static_cast<int32_t>(ncols), x_per_slot ? 1 : top_k, false};
     if (int st = launch_lora_down(&down, 1, p, dtype, s)) return st;
     const LoraUp up{u, b, add, out, nullptr, static_cast<int32_t>(nrows), false, out_dtype == FT_DTYPE_F32};
     return launch_lora_up(up, p, dtype, s);
@@ -306,8 +308,11 @@ int ft_lora_backward(const void* grad_out, const void* x, int32_t dtype, const v
     const int32_t K = static_cast<int32_t>(ncols), N = static_cast<int32_t>(nrows), div = x_per_slot ? 1 : top_k;
     LoraDown down[2];
     int n = 0;
-    if (grad_b) down[n++] = LoraDown{x, a, u, K, div, false};
-    if (grad_x || grad_a) down[n++] = LoraDown{grad_out, b, v, N, 1, true};
+    // the matrices' gradients take u and v as fp32 (fp16 adapters) or in parts, grad_x takes v as fp32
+    const bool bf = dtype == FT_DTYPE_BF16;
+    void *u_parts = ws + L.u_parts, *v_parts = ws + L.v_parts;
+    if (grad_b) down[n++] = LoraDown{x, a, bf ? nullptr : u, bf ? u_parts : nullptr, K, div, false};
+    if (grad_x || grad_a) down[n++] = LoraDown{grad_out, b, bf && !grad_x ? nullptr : v, bf && grad_a ? v_parts : nullptr, N, 1, true};
     if (int st = launch_lora_down(down, n, p, dtype, s)) return st;
     if (grad_x) {
         float *rows = reinterpret_cast<float*>(ws + L.rows), *present = reinterpret_cast<float*>(ws + L.present);
@@ -317,8 +322,8 @@ int ft_lora_backward(const void* grad_out, const void* x, int32_t dtype, const v
         if (share)
             if (int st = launch_combine(rows, FT_DTYPE_F32, present, add, grad_x, dtype, tokens, top_k, ncols, s)) return st;
     }
-    const LoraGrad grads[2] = {LoraGrad{x, v, grad_a, reinterpret_cast<float*>(ws + L.parts_a), K, div, false},
-                               LoraGrad{grad_out, u, grad_b, reinterpret_cast<float*>(ws + L.parts_b), N, 1, true}};
+    const LoraGrad grads[2] = {LoraGrad{x, v, v_parts, grad_a, reinterpret_cast<float*>(ws + L.parts_a), K, div, false},
+                               LoraGrad{grad_out, u, u_parts, grad_b, reinterpret_cast<float*>(ws + L.parts_b), N, 1, true}};
     return launch_lora_grad(grads, p, dtype, s);
 }
 

@@ -293,7 +293,8 @@ int launch_lora_order(const int32_t* ids, int64_t n_slots, int32_t n_adapters, i
 
 struct LoraDown {      // u[s] = W z[s / div]
     const void *z, *w;
-    float* u;
+    float* u;          // [slots][rank], or null
+    void* parts;       // [3][places][rank] bf16 parts of scale u, in order, whose sum it is; or null
     int32_t cols, div;
     bool trans;        // W is [cols][rank], else [rank][cols]
 };
@@ -312,7 +313,8 @@ int launch_lora_up_bf16(const LoraUp& j, const LoraPlan& p, cudaStream_t s);
 
 struct LoraGrad {      // out[e] = sum over its slots of scale w[s] z[s / div]; out null: not wanted
     const void* z;
-    const float* w;
+    const float* w;       // fp16
+    const void* w_parts;  // bf16: LoraDown's
     float *out, *parts;
     int32_t cols, div;
     bool turned;       // out is [cols][rank], else [rank][cols]

@@ -75,13 +75,11 @@ __device__ __forceinline__ LoraTile find_tile(const LoraSlots& s, int32_t b, int
 }
 
 // ----------------------------------------------------------- asynchronous copies
-// 16 or 4 bytes to shared memory, zeros where not `there` (src is not read then).
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+// 16 bytes to shared memory, zeros where not `there` (src is not read then).
+__device__ __forceinline__ void copy16_at(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy4(void* dst, const void* src, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) { copy16_at(smem_u32(dst), src, there); }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }

@@ -25,7 +25,8 @@ constexpr int kDownCols = 64, kDownPitch = kDownCols + 8, kDownStages = 4;
 template <typename T>
 struct DownJob {
     const T *z, *w;
-    float* u;
+    float* u;               // or null
+    __nv_bfloat16* parts;   // or null
     int32_t cols, div;      // row of slot s: s / div
     bool trans;             // W's values of one column are neighbours ([cols][R])
 };
@@ -34,6 +35,7 @@ template <typename T>
 struct DownArgs {
     DownJob<T> job[2];
     LoraSlots slots;
+    const float* scales;
     uint32_t* err;
     int32_t rank;
 };
@@ -175,14 +177,26 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
             *reinterpret_cast<float2*>(sums + (row + 8) * R + col) = make_float2(acc[m][j][2], acc[m][j][3]);
         }
     }
+    const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.0f;
     cluster_sync();
     for (int32_t i = static_cast<int32_t>(rank) * THREADS + tid; i < tile.n * R; i += static_cast<int32_t>(size) * THREADS) {
         float v = 0.0f;
         for (uint32_t q = 0; q < size; ++q)
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) v += cluster_load(sums + p * MT * R + i, q);
-        const int32_t s = i / R;
-        job.u[static_cast<int64_t>(slots[s]) * R + (i - s * R)] = v;
+        const int32_t s = i / R, r = i - s * R;
+        if (job.u) job.u[static_cast<int64_t>(slots[s]) * R + r] = v;
+        if (job.parts) {
+            v *= scale;
+            __nv_bfloat16* to = job.parts + static_cast<int64_t>(tile.first + s) * R + r;
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const __nv_bfloat16 h = __float2bfloat16_rn(v);
+                *to = h;
+                v -= __bfloat162float(h);
+                to += static_cast<int64_t>(a.slots.n_slots) * R;
+            }
+        }
     }
     cluster_sync();      // no CTA leaves while others read its sums
 }
@@ -210,11 +224,12 @@ template <typename T>
 int launch_down(const LoraDown* jobs, int n_jobs, const LoraPlan& p, cudaStream_t s) {
     DownArgs<T> a{};
     for (int i = 0; i < n_jobs; ++i)
-        a.job[i] = DownJob<T>{static_cast<const T*>(jobs[i].z), static_cast<const T*>(jobs[i].w), jobs[i].u, jobs[i].cols,
+        a.job[i] = DownJob<T>{static_cast<const T*>(jobs[i].z), static_cast<const T*>(jobs[i].w), jobs[i].u, static_cast<__nv_bfloat16*>(jobs[i].parts), jobs[i].cols,
                               jobs[i].div, jobs[i].trans};
     a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters, p.width};
     a.rank = p.rank;
     a.err = p.err;
+    a.scales = p.scales;
     if (p.width == 128) return launch_down_typed<T, 128>(a, p, n_jobs, s);
     if (p.width == 64) return launch_down_typed<T, 64>(a, p, n_jobs, s);
     return launch_down_typed<T, kLoraSmallTile>(a, p, n_jobs, s);

@@ -3,80 +3,39 @@
 //   dA[r][k] = sum_s v[s][r] x[s][k]      v = scale B^T dy
 //   dB[n][r] = sum_s dy[s][n] u[s][r]     u = scale A x
 //
-// Memory-bound on x and dy, which are read once more.  A CTA takes a chunk of an adapter's slots and 256
-// columns (128 for ranks above 64): z's rows come by cp.async, 32 slots a stage; the narrow side's fp32 values
-// are split into parts of 8 bits (lora.cuh) on their way to shared memory, so that the products keep 24.  The sums lie
-// in registers; an adapter with several chunks leaves them in the workspace, where a second launch
-// adds them up in order.  That launch also writes the zeros of adapters without a slot.
+// for fp16 adapters, and what follows for all: lora_grad_tc.cu has the kernel for bf16.
 //
-// Chunk j of adapter e has number tiles[e] / per + e + j: chunks of `per` tiles never need more numbers than that leaves.
+// A CTA takes a chunk of an adapter's slots and 256 columns (128 for ranks above 64).  z's rows come by cp.async, 32 slots a
+// stage; the narrow side's fp32 values go through shared memory as they are and are split into two tf32 parts in
+// registers, beside fp16 turned to tf32, which is exact: the narrow side needs more exponents than fp16 has.  The sums lie in
+// registers; an adapter with several chunks leaves them in the workspace, where a second launch adds them up in order.
+// That launch also writes the zeros of adapters without a slot.
+//
+// Chunk j of adapter e has number offsets[e] / per + e + j: chunks of `per` slots never need more numbers than that leaves.
 #include <algorithm>
-#include <type_traits>
 
-#include "lora.cuh"
-#include "ft_internal.h"
-#include "launch.cuh"
+#include "lora_grad.cuh"
 
 namespace ft {
 
 namespace {
 
-constexpr int kGradThreads = 256, kGradSlots = 32, kGradStages = 3, kGradRing = 8;
-
-template <typename T>
-struct GradJob {
-    const T* z;
-    const float* w;         // [slots][R]
-    float *out, *parts;     // [adapters][size], [chunks][size]
-    int32_t cols, div;      // of z; row of slot s: s / div
-    bool turned;            // out is [cols][R], else [R][cols]
-};
-
-template <typename T>
-struct GradArgs {
-    GradJob<T> job[2];
-    LoraSlots slots;
-    const float* scales;
-    int32_t rank, per, blocks0;      // per: slots of a chunk; blocks0: blocks of columns of the first job
-};
-
-// Chunk number b: its adapter, whether it has others, its first slot in order and its slots (0: none).
-struct Chunk {
-    int32_t adapter, first, n;
-    bool alone;
-};
-
-__device__ __forceinline__ Chunk find_chunk(const LoraSlots& s, int32_t b, int32_t per) {
-    __shared__ Chunk found;
-    const int32_t tid = static_cast<int32_t>(threadIdx.x);
-    if (tid == 0) found = Chunk{0, 0, 0, true};
-    __syncthreads();
-    for (int32_t e = tid; e < s.n_adapters; e += kGradThreads) {
-        const int32_t o0 = __ldg(s.offsets + e), o1 = __ldg(s.offsets + e + 1), j = b - (o0 / per + e);
-        // j * per stays small where it is looked at: numbers rise with the slots
-        if (j >= 0 && j <= (o1 - o0) / per && j * per < o1 - o0) found = Chunk{e, o0 + j * per, min(per, o1 - o0 - j * per), o1 - o0 <= per};
-    }
-    __syncthreads();
-    return found;
-}
+constexpr int kGradSlots = 32, kGradStages = 3, kGradRing = 8;
 
 // MR: tiles of 16 ranks that there is room for; NJ: tiles of eight columns that a warp has.
 template <typename T, int MR, int NJ>
 __global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid_constant__ GradArgs<T> a) {
     constexpr int CC = 8 * NJ * (kGradThreads / 32), ZP = CC + 8;      // columns of the CTA, their pitch
-    constexpr int TERMS = 3;
-    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     constexpr int PAIRS = MR;      // pairs of ranks that a thread has of a stage
     extern __shared__ __align__(16) uint8_t grad_smem[];
     const int32_t tid = static_cast<int32_t>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const bool second = static_cast<int32_t>(blockIdx.y) >= a.blocks0;
     const GradJob<T>& job = a.job[second ? 1 : 0];
     const int32_t col0 = (static_cast<int32_t>(blockIdx.y) - (second ? a.blocks0 : 0)) * CC;
-    const Chunk ck = find_chunk(a.slots, static_cast<int32_t>(blockIdx.x), a.per);
+    const Chunk ck = find_chunk<kGradThreads>(a.slots, static_cast<int32_t>(blockIdx.x), a.per);
     if (ck.n == 0) return;
     const int32_t R = a.rank, r16 = (R + 15) / 16 * 16, mr = r16 / 16, cols = job.cols;
-    const int32_t wp = odd_pitch(r16), wf = r16 + 4;      // pitch of a part's rows; of fp32 rows (fp16)
-    const int32_t w_bytes = BF ? TERMS * kGradSlots * wp * 2 : kGradSlots * wf * 4;
+    const int32_t wf = r16 + 4, w_bytes = kGradSlots * wf * 4;      // pitch of w's rows: lanes' pairs of slots in different banks
     T* zs_all = reinterpret_cast<T*>(grad_smem);
     uint8_t* ws_all = grad_smem + kGradStages * kGradSlots * ZP * sizeof(T);
     __shared__ int32_t ring[kGradRing][kGradSlots];      // slots of the stages from the one at work on
@@ -116,17 +75,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid
         for (int j = 0; j < PAIRS; ++j) {
             if (j >= mr) break;
             const int32_t at = tid + j * kGradThreads, row = at / (8 * mr), r = (at - row * 8 * mr) * 2;
-            if constexpr (BF) {
-                uint32_t p[TERMS];
-                split_pair<TERMS>(wreg[j].x, wreg[j].y, p);
-#pragma unroll
-                for (int t = 0; t < TERMS; ++t)
-                    *reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(ws) + (t * kGradSlots + row) * wp + r) = p[t];
-            } else {
-                float* f = reinterpret_cast<float*>(ws) + row * wf + r;
-                f[0] = wreg[j].x;
-                f[1] = wreg[j].y;
-            }
+            float* f = reinterpret_cast<float*>(ws) + row * wf + r;
+            f[0] = wreg[j].x;
+            f[1] = wreg[j].y;
         }
     };
 
@@ -172,33 +123,20 @@ __global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid
         for (int m = 0; m < MR; ++m) {
             if (m >= mr) break;
             float sum[NJ][4] = {};      // of the stage: a chain of few additions that cut off (lora_down.cu)
-            if constexpr (BF) {
 #pragma unroll
-                for (int t = TERMS - 1; t >= 0; --t)
+            for (int k = 0; k < kGradSlots / 16; ++k) {
+                const float* f = reinterpret_cast<const float*>(ws) + (k * 16 + lane % 4 * 2) * wf + m * 16 + lane / 4;
+                float v[8];      // ranks by h, slots 2 q (+1) and 2 q + 8 (+1)
 #pragma unroll
-                    for (int k = 0; k < kGradSlots / 16; ++k) {
-                        uint32_t x[4];
-                        const T* p = reinterpret_cast<const T*>(ws) + t * kGradSlots * wp;
-                        ldsm4(x, p + (k * 16 + lane / 16 * 8 + lane % 8) * wp + m * 16 + lane / 8 % 2 * 8, true);
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) mma16(sum[j], x, b[k][j][0], b[k][j][1], T());
+                    for (int x = 0; x < 2; ++x) {
+                        v[2 * (h + 2 * x)] = f[8 * x * wf + 8 * h];
+                        v[2 * (h + 2 * x) + 1] = f[(8 * x + 1) * wf + 8 * h];
                     }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kGradSlots / 16; ++k) {
-                    const float* f = reinterpret_cast<const float*>(ws) + (k * 16 + lane % 4 * 2) * wf + m * 16 + lane / 4;
-                    float v[8];      // ranks by h, slots 2 q (+1) and 2 q + 8 (+1)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            v[2 * (h + 2 * x)] = f[8 * x * wf + 8 * h];
-                            v[2 * (h + 2 * x) + 1] = f[(8 * x + 1) * wf + 8 * h];
-                        }
-                    Wide16<T, 2> wide;
-                    wide.set(v);
-                    wide.mul(sum, b[k]);
-                }
+                Wide16<T, 2> wide;
+                wide.set(v);
+                wide.mul(sum, b[k]);
             }
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
@@ -267,56 +205,38 @@ __global__ void __launch_bounds__(kGradThreads) lora_join_kernel(const JoinArgs 
     }
 }
 
-template <typename T>
-int launch_grad(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
-    GradArgs<T> a{};
-    JoinArgs j{};
-    int n = 0;
-    int32_t blocks[2] = {0, 0};
-    const int32_t cc = p.rank <= 64 ? 256 : 128;
-    for (int i = 0; i < 2; ++i) {
-        if (!jobs[i].out) continue;
-        a.job[n] = GradJob<T>{static_cast<const T*>(jobs[i].z), jobs[i].w, jobs[i].out, jobs[i].parts, jobs[i].cols, jobs[i].div,
-                              jobs[i].turned};
-        blocks[n] = (jobs[i].cols + cc - 1) / cc;
-        j.out[n] = jobs[i].out;
-        j.parts[n] = jobs[i].parts;
-        j.size4[n] = static_cast<int64_t>(p.rank) * jobs[i].cols / 4;
-        ++n;
-    }
-    if (n == 0) return FT_OK;
-    a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters, p.width};
-    a.scales = p.scales;
-    a.rank = p.rank;
-    a.per = p.chunk;
-    a.blocks0 = blocks[0];
-    const int64_t chunks = lora_chunks(p.n_slots, p.n_adapters, p.chunk);
-    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(blocks[0] + blocks[1])), block(kGradThreads);
-    const int32_t r16 = (p.rank + 15) / 16 * 16;
-    const bool bf = std::is_same<T, __nv_bfloat16>::value;
-    const size_t sm = kGradStages * kGradSlots * static_cast<size_t>(cc + 8) * sizeof(T) +
-                      2 * static_cast<size_t>(bf ? 3 * kGradSlots * odd_pitch(r16) * 2 : kGradSlots * (r16 + 4) * 4);
+int launch_grad_fp16(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
+    const int32_t cc = p.rank <= 64 ? 256 : 128, r16 = (p.rank + 15) / 16 * 16;
+    int64_t blocks;
+    const GradArgs<__half> a = grad_args<__half>(jobs, p, cc, &blocks);
+    const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kGradThreads);
+    const size_t sm = kGradStages * kGradSlots * static_cast<size_t>(cc + 8) * 2 + 2 * static_cast<size_t>(kGradSlots * (r16 + 4) * 4);
     auto go = [&](auto k) { return launch_with(k, "lora_grad_kernel", grid, block, sm, false, 1, s, a); };
-    int st;
-    if (p.rank <= 16) st = go(lora_grad_kernel<T, 1, 4>);
-    else if (p.rank <= 32) st = go(lora_grad_kernel<T, 2, 4>);
-    else if (p.rank <= 64) st = go(lora_grad_kernel<T, 4, 4>);
-    else st = go(lora_grad_kernel<T, 8, 2>);
-    if (st) return st;
-    j.offsets = p.offsets;
-    j.per = p.chunk;
-    int64_t y = 4 * static_cast<int64_t>(sm_count()) / p.n_adapters;
-    const int64_t most = (std::max(j.size4[0], j.size4[1]) + kGradThreads - 1) / kGradThreads;
-    y = y < 1 ? 1 : y < most ? y : most;
-    const dim3 jgrid(static_cast<unsigned>(p.n_adapters), static_cast<unsigned>(y));
-    lora_join_kernel<<<jgrid, block, 0, s>>>(j);
-    return check_launch("lora_join_kernel", jgrid, block, 0);
+    if (p.rank <= 16) return go(lora_grad_kernel<__half, 1, 4>);
+    if (p.rank <= 32) return go(lora_grad_kernel<__half, 2, 4>);
+    if (p.rank <= 64) return go(lora_grad_kernel<__half, 4, 4>);
+    return go(lora_grad_kernel<__half, 8, 2>);
 }
 
 }  // namespace
 
 int launch_lora_grad(const LoraGrad* jobs, const LoraPlan& p, int dtype, cudaStream_t s) {
-    return dtype == FT_DTYPE_F16 ? launch_grad<__half>(jobs, p, s) : launch_grad<__nv_bfloat16>(jobs, p, s);
+    JoinArgs j{};
+    for (int i = 0; i < 2; ++i) {
+        j.out[i] = jobs[i].out;
+        j.parts[i] = jobs[i].parts;
+        j.size4[i] = jobs[i].out ? static_cast<int64_t>(p.rank) * jobs[i].cols / 4 : 0;
+    }
+    if (!j.out[0] && !j.out[1]) return FT_OK;
+    if (int st = dtype == FT_DTYPE_F16 ? launch_grad_fp16(jobs, p, s) : launch_lora_grad_tc(jobs, p, s)) return st;
+    j.offsets = p.offsets;
+    j.per = p.chunk;
+    int64_t y = 4 * static_cast<int64_t>(sm_count()) / p.n_adapters;
+    const int64_t most = (std::max(j.size4[0], j.size4[1]) + kGradThreads - 1) / kGradThreads;
+    y = y < 1 ? 1 : y < most ? y : most;
+    const dim3 jgrid(static_cast<unsigned>(p.n_adapters), static_cast<unsigned>(y)), block(kGradThreads);
+    lora_join_kernel<<<jgrid, block, 0, s>>>(j);
+    return check_launch("lora_join_kernel", jgrid, block, 0);
 }
 
 }  // namespace ft

@@ -1,0 +1,225 @@
+// Gradients of bf16 adapters' matrices (lora_grad.cu has the formulas) on the tensor cores by tcgen05.
+//
+// D[m][c] = sum over slots of W[m][s] z[s][c]: a CTA takes a chunk of an adapter's slots and 256 columns of z.  The rows m are
+// the narrow side's ranks, each three times: an fp32 value is the sum of three bf16 parts (24 bits), whose products with
+// z's bf16 are exact.  Up to rank 40 all three parts fit the 128 rows of one MMA; up to 64 two, and the third
+// is a second MMA onto the first part's rows; above, each part is an MMA of its own.
+//
+// Both operands lie as they come, a slot's neighbours side by side (M- and N-major), in 8 x 8 blocks of 128 bytes whose
+// strides are odd numbers of 16-byte words, so that copies of rows do not meet in a bank.  z's rows and the parts, which
+// lora_down.cu has left in order, come by cp.async, two to four stages of 64 slots.
+//
+// The tensor cores cut what they add off at the accumulator's last bit, so that a sum of n products is too small by some
+// n 2^-25 of itself.  Every 128 slots the sums move on to the other half of the tensor memory, and the first are added to
+// registers by rounding to nearest: 4096 x 4096, rank 64, 8192 slots: 2e-7 of the gradients' norm off.
+#include "lora_grad.cuh"
+
+namespace ft {
+
+namespace {
+
+constexpr int kTcThreads = 512, kTcSlots = 64, kTcCols = 256, kTcRing = 8, kTcWindow = 2;      // kTcWindow: stages of an accumulator
+constexpr uint32_t kTcBlock = 144;                                           // bytes between blocks of eight columns or ranks
+constexpr uint32_t kTcZGroup = kTcCols / 8 * kTcBlock, kTcZStage = kTcSlots / 8 * kTcZGroup;      // bytes between groups of eight slots
+constexpr uint32_t kTcWGroup = 128 / 8 * kTcBlock, kTcWPass = kTcSlots / 8 * kTcWGroup;
+
+// MMAs that a step of 16 slots takes, and rows of the accumulator that hold sums.
+__host__ __device__ inline int32_t tc_passes(int32_t rank) { return 3 * rank <= 128 ? 1 : 2 * rank <= 128 ? 2 : 3; }
+__host__ __device__ inline int32_t tc_stages(int32_t passes) { return 5 - passes; }
+__host__ __device__ inline uint32_t tc_stage_bytes(int32_t passes) { return kTcZStage + static_cast<uint32_t>(passes) * kTcWPass; }
+
+// Shared-memory descriptor without swizzle: bytes between blocks along K and along M or N.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t at, uint32_t along_k, uint32_t along_mn) {
+    return static_cast<uint64_t>((at & 0x3FFFFu) >> 4) | static_cast<uint64_t>(along_k >> 4) << 16 |
+           static_cast<uint64_t>(along_mn >> 4) << 32 | 1ull << 46;
+}
+
+// WJ: words of a stage's parts that a thread copies.
+template <int WJ>
+__global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __grid_constant__ GradArgs<__nv_bfloat16> a) {
+    using T = __nv_bfloat16;
+    extern __shared__ __align__(128) uint8_t tc_smem[];
+    __shared__ int32_t row_ring[kTcRing][kTcSlots];      // rows of z of the stages ahead
+    __shared__ __align__(8) uint64_t done[4];
+    __shared__ uint32_t tmem_at;
+    const int32_t tid = static_cast<int32_t>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const bool second = static_cast<int32_t>(blockIdx.y) >= a.blocks0;
+    const GradJob<T>& job = a.job[second ? 1 : 0];
+    const int32_t col0 = (static_cast<int32_t>(blockIdx.y) - (second ? a.blocks0 : 0)) * kTcCols, cols = job.cols;
+    const Chunk ck = find_chunk<kTcThreads>(a.slots, static_cast<int32_t>(blockIdx.x), a.per);
+    if (ck.n == 0) return;
+    const int32_t R = a.rank, passes = tc_passes(R), stages = tc_stages(passes), used = passes == 3 ? R : (4 - passes) * R;
+    const uint32_t stage_bytes = tc_stage_bytes(passes);
+    const int32_t* perm = a.slots.perm + ck.first;
+    const int32_t steps = (ck.n + kTcSlots - 1) / kTcSlots;
+
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&done[i], 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_at, 512);
+        tmem_relinquish();
+    }
+    // with two passes, zeros beside the third part: its MMA adds to the second part's rows, too
+    if (passes == 2) {
+        constexpr int32_t WORDS = static_cast<int32_t>(kTcWPass / 16);
+        for (int32_t i = tid; i < stages * WORDS; i += kTcThreads)
+            reinterpret_cast<uint4*>(tc_smem + static_cast<uint32_t>(i / WORDS) * stage_bytes + kTcZStage + kTcWPass)[i % WORDS] = make_uint4(0u, 0u, 0u, 0u);
+    }
+
+    // the slots are asked for stages ahead of the rows they name
+    constexpr int AHEAD = 5;
+    for (int32_t i = tid; i < AHEAD * kTcSlots && i < ck.n; i += kTcThreads) {
+        row_ring[i / kTcSlots][i % kTcSlots] = __ldg(perm + i) / job.div;
+    }
+    auto slot_of = [&](int32_t i) { return tid < kTcSlots && i * kTcSlots + tid < ck.n ? __ldg(perm + i * kTcSlots + tid) : 0; };
+    int32_t next = slot_of(AHEAD);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+
+    // words of z: column block `lane` of slots warp, warp + 16, ..
+    constexpr int WARPS = kTcThreads / 32, ZJ = kTcSlots / WARPS;
+    const bool in = col0 + lane * 8 < cols;
+    const T* z_base = job.z + (in ? col0 + lane * 8 : 0);
+    const uint32_t z_to = smem_u32(tc_smem) + static_cast<uint32_t>(lane) * kTcBlock + static_cast<uint32_t>(warp / 8) * kTcZGroup + warp % 8 * 16;
+    // words of the parts: 64 slots' ranks of one part after the other, each a run of the workspace
+    const int32_t G = R / 8, part_words = kTcSlots * G;
+    const T* w_src[WJ];
+    uint32_t w_to[WJ];
+    int32_t w_slot[WJ];
+#pragma unroll
+    for (int j = 0; j < WJ; ++j) {
+        const int32_t at = tid + j * kTcThreads, t = at / part_words, q = at - t * part_words, s = q / G, g = q - s * G;
+        const int32_t pass = passes == 3 ? t : passes == 2 ? t / 2 : 0, row = passes == 3 || (passes == 2 && t == 2) ? 0 : t * R;
+        w_to[j] = smem_u32(tc_smem) + kTcZStage + static_cast<uint32_t>(pass) * kTcWPass + static_cast<uint32_t>(row / 8 + g) * kTcBlock +
+                  static_cast<uint32_t>(s / 8) * kTcWGroup + static_cast<uint32_t>(s % 8) * 16;
+        w_src[j] = job.w_parts + (static_cast<int64_t>(t) * a.slots.n_slots + ck.first) * R + q * 8;
+        w_slot[j] = t < 3 ? s : 1 << 30;
+    }
+    auto load = [&](int32_t i) {      // stages in turn
+        const uint32_t stage = static_cast<uint32_t>(i % stages) * stage_bytes;
+        const int32_t left = ck.n - i * kTcSlots;
+#pragma unroll
+        for (int j = 0; j < ZJ; ++j) {
+            const int32_t s = warp + j * WARPS;
+            const bool there = in && s < left;
+            const T* src = there ? z_base + static_cast<int64_t>(row_ring[i % kTcRing][s]) * cols : job.z;
+            copy16_at(z_to + stage + j * (WARPS / 8) * kTcZGroup, src, there);
+        }
+#pragma unroll
+        for (int j = 0; j < WJ; ++j) {
+            if (w_slot[j] < kTcSlots) copy16_at(w_to[j] + stage, w_slot[j] < left ? w_src[j] : job.w_parts, w_slot[j] < left);
+            w_src[j] += kTcSlots * R;
+        }
+    };
+
+    constexpr int TC = kTcCols * 128 / kTcThreads;      // sums of a thread: row 32 (warp % 4) + lane, columns TC (warp / 4) ..
+    float total[TC] = {};
+    const uint32_t mine = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + static_cast<uint32_t>(warp / 4 * TC);
+    auto drain = [&](int32_t window) {
+        if (warp % 4 * 32 < used) {
+#pragma unroll
+            for (int q = 0; q < TC / 32; ++q) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(window & 1) * kTcCols + q * 32, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) total[q * 32 + i] += __uint_as_float(v[i]);
+            }
+        }
+        tc_fence_before();      // the accumulator is written again after the next barrier
+    };
+
+    for (int32_t i = 0; i < stages - 1; ++i) {
+        if (i < steps) load(i);
+        copies_commit();
+    }
+    bool ok = true;
+    for (int32_t i = 0; i < steps; ++i) {
+        if (stages == 4) copies_wait<2>();
+        else if (stages == 3) copies_wait<1>();
+        else copies_wait<0>();
+        fence_proxy_async_smem();
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (tid == 0) {
+            tc_fence_after();
+            // bf16 operands, fp32 sums, both M- or N-major, 128 x 256
+            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (kTcCols >> 3) << 17 | (128u >> 4) << 24;
+            const uint32_t zs = smem_u32(tc_smem) + static_cast<uint32_t>(i % stages) * stage_bytes, ws = zs + kTcZStage;
+            const uint32_t d = tmem + static_cast<uint32_t>(i / kTcWindow & 1) * kTcCols;
+            for (int32_t p = 0; p < passes; ++p)
+#pragma unroll
+                for (int k = 0; k < kTcSlots / 16; ++k)
+                    tc_mma_f16(d, tc_desc(ws + static_cast<uint32_t>(p) * kTcWPass + k * 2 * kTcWGroup, kTcWGroup, kTcBlock),
+                               tc_desc(zs + k * 2 * kTcZGroup, kTcZGroup, kTcBlock), idesc, i % kTcWindow || p || k);
+            tc_commit(&done[i % 4]);
+        }
+        if (i > 0) {
+            ok = mbar_wait_warp(&done[(i - 1) % 4], static_cast<uint32_t>((i - 1) / 4 & 1), a.err);
+            if (ok && i % kTcWindow == 0) {
+                tc_fence_after();
+                drain(i / kTcWindow - 1);
+            }
+        }
+        if (i + stages - 1 < steps) load(i + stages - 1);      // where the MMAs just waited for read
+        copies_commit();
+        if (tid < kTcSlots) row_ring[(i + AHEAD) % kTcRing][tid] = next / job.div;
+        next = slot_of(i + AHEAD + 1);
+    }
+    copies_wait<0>();
+    if (ok) ok = mbar_wait_warp(&done[(steps - 1) % 4], static_cast<uint32_t>((steps - 1) / 4 & 1), a.err);
+    ok = __syncthreads_and(ok);
+    if (ok) {
+        tc_fence_after();
+        drain((steps - 1) / kTcWindow);
+        const int64_t size = static_cast<int64_t>(R) * cols;
+        float* out = ck.alone ? job.out + ck.adapter * size : job.parts + blockIdx.x * size;
+        // the parts' rows meet in shared memory
+        constexpr int PITCH = kTcCols + 1;
+        float* tile = reinterpret_cast<float*>(tc_smem);
+        const int32_t m = warp % 4 * 32 + lane;
+        if (m < used) {
+#pragma unroll
+            for (int c = 0; c < TC; ++c) tile[m * PITCH + warp / 4 * TC + c] = total[c];
+        }
+        __syncthreads();
+        auto sum = [&](int32_t r, int32_t c) {
+            float v = tile[r * PITCH + c];
+            if (passes < 3) v += tile[(R + r) * PITCH + c];
+            if (passes < 2) v += tile[(2 * R + r) * PITCH + c];
+            return v;
+        };
+        const int32_t width = min(kTcCols, cols - col0);
+        if (job.turned) {
+            for (int32_t c = warp; c < width; c += WARPS)
+                for (int32_t r = lane; r < R; r += 32) out[static_cast<int64_t>(col0 + c) * R + r] = sum(r, c);
+        } else {
+            for (int32_t r = warp; r < R; r += WARPS)
+                for (int32_t c = lane; c < width; c += 32) out[static_cast<int64_t>(r) * cols + col0 + c] = sum(r, c);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+int launch_lora_grad_tc(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
+    int64_t blocks;
+    const GradArgs<__nv_bfloat16> a = grad_args<__nv_bfloat16>(jobs, p, kTcCols, &blocks);
+    const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kTcThreads);
+    const int32_t passes = tc_passes(p.rank);
+    const size_t sm = static_cast<size_t>(tc_stages(passes)) * tc_stage_bytes(passes);
+    auto go = [&](auto k) { return launch_with(k, "lora_grad_tc_kernel", grid, block, sm, false, 1, s, a); };
+    if (p.rank <= 16) return go(lora_grad_tc_kernel<1>);
+    if (p.rank <= 40) return go(lora_grad_tc_kernel<2>);
+    if (p.rank <= 64) return go(lora_grad_tc_kernel<3>);
+    return go(lora_grad_tc_kernel<6>);
+}
+
+}  // namespace ft

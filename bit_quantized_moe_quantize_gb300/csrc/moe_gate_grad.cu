@@ -249,7 +249,7 @@ int launch_gate_grad(const GateGradParams& p, const void* logits, int dtype, int
     a.wide = stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
     a.wide_out = static_cast<int64_t>(p.n_experts) * size % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
     a.wide_counts = p.n_experts % 4 == 0 && reinterpret_cast<uintptr_t>(p.counts) % 16 == 0;
-    return with_row_lanes(p.n_experts, [&](auto lanes, auto steps) {
+    auto launch = [&](auto lanes, auto steps) {
         constexpr int L = decltype(lanes)::value, N = decltype(steps)::value, ROWS = kRowThreads / L;
         const int64_t ctas = (p.tokens + ROWS - 1) / ROWS;
         if (ctas > 0x7FFFFFFF) return fail(FT_ERR_SIZE, "too many tokens for one launch");
@@ -269,7 +269,10 @@ int launch_gate_grad(const GateGradParams& p, const void* logits, int dtype, int
         else if (dtype == FT_DTYPE_F16) go(__half());
         else go(__nv_bfloat16());
         return check_launch("gate_grad_kernel", grid, block, 0);
-    });
+    };
+    // many rows: half the lanes, with twice the experts each, take fewer instructions (65536 x 128: 19.2 us, 20.1 with
+    // all); few rows: all of them are sooner done (777 x 256: 5.5 us against 6.8)
+    return p.tokens >= 8192 ? with_row_lanes<true>(p.n_experts, launch) : with_row_lanes<false>(p.n_experts, launch);
 }
 
 }  // namespace ft

@@ -161,9 +161,14 @@ __device__ __forceinline__ int32_t seq_of(const int32_t* offsets, int32_t n, int
     return lo;
 }
 
-// Calls f.template operator()<L, STEPS>() for the lanes per row that E experts take.
-template <typename F>
+// Calls f with the lanes per row and the steps that E experts take; FEW: half the lanes where that can be.
+template <bool FEW = false, typename F>
 int with_row_lanes(int32_t E, const F& f) {
+    if constexpr (FEW) {
+        if (E > 32 && E <= 64) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+        if (E > 64 && E <= 128) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+        if (E > 128 && E <= 256) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+    }
     if (E <= 32) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
     if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
     if (E <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
