@@ -294,7 +294,7 @@ int launch_lora_order(const int32_t* ids, int64_t n_slots, int32_t n_adapters, i
 struct LoraDown {      // u[s] = W z[s / div]
     const void *z, *w;
     float* u;          // [slots][rank], or null
-    void* parts;       // [3][places][rank] bf16 parts of scale u, in order, whose sum it is; or null
+    void* parts;       // [places][3][rank] bf16 parts of scale u, in order, whose sum it is; or null
     int32_t cols, div;
     bool trans;        // W is [cols][rank], else [rank][cols]
 };

@@ -6,7 +6,9 @@
 // Memory-bound on z.  A tile of 64 or 128 slots (16 where adapters have few) by all R columns is a cluster's work: its
 // CTAs share the inner dimension, and add their sums up through each other's shared memory, in a fixed order.
 // z and W come by cp.async, four stages of 64 values; in tiles of 16 slots the four warps share a
-// stage's values instead of its slots.
+// stage's values instead of its slots.  A row of a stage is one line of 128 bytes whose 16-byte words are exchanged by
+// word ^ row % 8: the copies fill whole lines (64 MB through shared memory 8.4 us; rows 144 bytes apart 11.8, words by
+// themselves 22), and a column of eight rows lies in all banks.
 //
 // The tensor cores cut what they add to an accumulator off at its last bit: after n additions a sum is too small
 // by some n 2^-25 of itself.  So a stage's sums start from 0 and are added to the others by the CUDA cores.
@@ -20,7 +22,7 @@ namespace ft {
 
 namespace {
 
-constexpr int kDownCols = 64, kDownPitch = kDownCols + 8, kDownStages = 4;
+constexpr int kDownCols = 64, kDownStages = 4;
 
 template <typename T>
 struct DownJob {
@@ -40,10 +42,9 @@ struct DownArgs {
     int32_t rank;
 };
 
-__host__ __device__ inline int32_t down_w_elems(int32_t rank) {
-    const int32_t a = rank * kDownPitch, b = kDownCols * odd_pitch(rank);
-    return a > b ? a : b;
-}
+// Elements between the rows of W's stage where they are the inner dimension's: whole lines at rank 64, else an odd number of words.
+__host__ __device__ inline int32_t down_turned_pitch(int32_t rank) { return rank % 64 == 0 ? rank : odd_pitch(rank); }
+__host__ __device__ inline int32_t down_w_elems(int32_t rank) { return kDownCols * down_turned_pitch(rank) > rank * kDownCols ? kDownCols * down_turned_pitch(rank) : rank * kDownCols; }
 
 // NT: tiles of eight ranks that there is room for.
 template <typename T, int MT, int NT>
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
     constexpr int THREADS = kLoraThreads, PARTS = MT == kLoraSmallTile ? THREADS / 32 : 1;      // PARTS: warps that share a tile's sums
     constexpr int MS = MT == 128 ? 2 : 1, WARP_ROWS = 16 * MS;                                      // a warp's runs of 16 slots
     constexpr int ZS = THREADS / 8, ZR = (MT + ZS - 1) / ZS;                                        // rows that a copy of a word per thread takes
-    extern __shared__ __align__(16) uint8_t down_smem[];
+    extern __shared__ __align__(128) uint8_t down_smem[];
     __shared__ int32_t slots[MT];
     let_next_grid_start();
     const uint32_t size = cluster_size(), rank = cluster_rank();
@@ -66,14 +67,14 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
     }
     const LoraTile tile = find_tile<MT>(a.slots, b, slots);
     if (tile.n == 0) return;      // all of the cluster
-    const int32_t R = a.rank, nt = R / 8, cols = job.cols, pitch = odd_pitch(R);
-    const int32_t stage_elems = MT * kDownPitch + down_w_elems(R);
+    const int32_t R = a.rank, nt = R / 8, cols = job.cols, pitch = down_turned_pitch(R);
+    const int32_t stage_elems = MT * kDownCols + down_w_elems(R);
     T* smem = reinterpret_cast<T*>(down_smem);
     const T* w = job.w + static_cast<int64_t>(tile.adapter) * R * cols;
     const int32_t chunks = (cols + kDownCols - 1) / kDownCols, per = (chunks + static_cast<int32_t>(size) - 1) / static_cast<int32_t>(size);
     const int32_t c0 = static_cast<int32_t>(rank) * per, n_chunks = max(0, min(chunks - c0, per));
 
-    const int32_t part = tid % 8 * 8;      // of a row's 64 values
+    const int32_t part = tid % 8 * 8, z_word = (tid % 8 ^ tid / 8 % 8) * 8;      // of a row's 64 values, where they go
     const T* z[ZR];
 #pragma unroll
     for (int i = 0; i < ZR; ++i) {
@@ -90,17 +91,17 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
         for (int j = 0; j < WJ; ++j) {
             const int32_t at = tid + j * THREADS, words = TRANS ? R / 8 : kDownCols / 8, row = at / words, ch = at - row * words;
             from[j] = TRANS ? row * R + ch * 8 : row * cols + ch * 8;
-            to[j] = row * (TRANS ? pitch : kDownPitch) + ch * 8;
+            to[j] = TRANS ? row * pitch + (R % 64 == 0 ? ch ^ row % 8 : ch) * 8 : row * kDownCols + (ch ^ row % 8) * 8;
             edge[j] = at >= nt8 ? 1 << 30 : TRANS ? row : ch * 8;
         }
         auto load = [&](int32_t i) {
             const int32_t col = (c0 + i) * kDownCols;
             T* zs = smem + i % kDownStages * stage_elems;
-            T* ws = zs + MT * kDownPitch;
+            T* ws = zs + MT * kDownCols;
 #pragma unroll
             for (int j = 0; j < ZR; ++j) {
                 const bool there = col + part < cols && z[j] != nullptr;
-                copy16(zs + (tid / 8 + ZS * j) * kDownPitch + part, there ? z[j] + col + part : job.z, there);
+                copy16(zs + (tid / 8 + ZS * j) * kDownCols + z_word, there ? z[j] + col + part : job.z, there);
             }
             const T* wc = w + static_cast<int64_t>(col) * (TRANS ? R : 1);
 #pragma unroll
@@ -115,13 +116,19 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
             copies_commit();
         }
         // what this lane gives the address of: 16 slots by 16 values of z, pairs of W's tiles by 16 values
-        const int32_t row0 = PARTS == 1 ? warp * WARP_ROWS : 0, k0 = PARTS == 1 ? 0 : warp * 16;
-        const int32_t zat = (row0 + lane % 16) * kDownPitch + lane / 16 * 8 + k0, step = TRANS ? 16 * pitch : 16;
-        int32_t wat[NT / 2];
+        constexpr int KK = PARTS == 1 ? kDownCols / 16 : 1;
+        const int32_t row0 = PARTS == 1 ? warp * WARP_ROWS : 0, first = PARTS == 1 ? 0 : warp, l = lane % 8;      // first: step of 16 values
+        const int32_t zat = (row0 + lane % 16) * kDownCols;
+        int32_t zword[KK], wword[KK], wat[NT / 2];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            zword[kk] = (2 * (first + kk) + lane / 16 ^ l) * 8;
+            wword[kk] = TRANS ? 16 * (first + kk) * pitch : (2 * (first + kk) + lane / 8 % 2 ^ l) * 8;
+        }
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
-            const int32_t n = min(2 * j + lane / 16, nt - 1), k = k0 + lane / 8 % 2 * 8, l = lane % 8;      // an odd last tile stands in for its neighbour
-            wat[j] = TRANS ? (k + l) * pitch + n * 8 : (n * 8 + l) * kDownPitch + k;
+            const int32_t n = min(2 * j + lane / 16, nt - 1);      // an odd last tile stands in for its neighbour
+            wat[j] = TRANS ? (lane / 8 % 2 * 8 + l) * pitch + (R % 64 == 0 ? n ^ l : n) * 8 : (n * 8 + l) * kDownCols;
         }
         for (int32_t c = 0; c < n_chunks; ++c) {
             copies_wait<kDownStages - 2>();
@@ -129,13 +136,12 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
             if (c + kDownStages - 1 < n_chunks) load(c + kDownStages - 1);
             copies_commit();
             const T* zs = smem + c % kDownStages * stage_elems;
-            const T* ws = zs + MT * kDownPitch;
-            constexpr int KK = PARTS == 1 ? kDownCols / 16 : 1;
+            const T* ws = zs + MT * kDownCols;
             uint32_t x[MS][KK][4];
 #pragma unroll
             for (int m = 0; m < MS; ++m)
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) ldsm4(x[m][kk], zs + zat + m * 16 * kDownPitch + kk * 16, false);
+                for (int kk = 0; kk < KK; ++kk) ldsm4(x[m][kk], zs + zat + m * 16 * kDownCols + zword[kk], false);
 #pragma unroll
             for (int j = 0; j < NT / 2; ++j) {
                 if (2 * j >= nt) break;
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     uint32_t b[4];
-                    ldsm4(b, ws + wat[j] + kk * step, TRANS);
+                    ldsm4(b, ws + wat[j] + wword[kk], TRANS);
 #pragma unroll
                     for (int m = 0; m < MS; ++m) {
                         mma16(sum[m][0], x[m][kk], b[0], b[1], T());
@@ -188,13 +194,13 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
         if (job.u) job.u[static_cast<int64_t>(slots[s]) * R + r] = v;
         if (job.parts) {
             v *= scale;
-            __nv_bfloat16* to = job.parts + static_cast<int64_t>(tile.first + s) * R + r;
+            __nv_bfloat16* to = job.parts + static_cast<int64_t>(tile.first + s) * 3 * R + r;
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
                 const __nv_bfloat16 h = __float2bfloat16_rn(v);
                 *to = h;
                 v -= __bfloat162float(h);
-                to += static_cast<int64_t>(a.slots.n_slots) * R;
+                to += R;
             }
         }
     }
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
 
 template <typename T, int MT>
 int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStream_t s) {
-    size_t sm = static_cast<size_t>(kDownStages) * (MT * kDownPitch + down_w_elems(a.rank)) * sizeof(T);
+    size_t sm = static_cast<size_t>(kDownStages) * (MT * kDownCols + down_w_elems(a.rank)) * sizeof(T);
     const size_t sums = static_cast<size_t>(MT == kLoraSmallTile ? 4 * MT : MT) * a.rank * 4;
     if (sums > sm) sm = sums;
     // As many CTAs as the GPU holds at once, with four stages of work or more each.  By what a call can have, not what it has:

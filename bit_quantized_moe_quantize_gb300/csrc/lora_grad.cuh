@@ -13,7 +13,7 @@ template <typename T>
 struct GradJob {
     const T* z;
     const float* w;         // [slots][R] (fp16)
-    const T* w_parts;       // [3][places][R], scaled, in order (bf16)
+    const T* w_parts;       // [places][3][R], scaled, in order (bf16)
     float *out, *parts;     // [adapters][size], [chunks][size]
     int32_t cols, div;      // of z; row of slot s: s / div
     bool turned;            // out is [cols][R], else [R][cols]

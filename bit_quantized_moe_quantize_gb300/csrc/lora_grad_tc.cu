@@ -5,9 +5,10 @@
 // z's bf16 are exact.  Up to rank 40 all three parts fit the 128 rows of one MMA; up to 64 two, and the third
 // is a second MMA onto the first part's rows; above, each part is an MMA of its own.
 //
-// Both operands lie as they come, a slot's neighbours side by side (M- and N-major), in 8 x 8 blocks of 128 bytes whose
-// strides are odd numbers of 16-byte words, so that copies of rows do not meet in a bank.  z's rows and the parts, which
-// lora_down.cu has left in order, come by cp.async, two to four stages of 64 slots.
+// Both operands lie as they come, a slot's neighbours side by side (M- and N-major), in lines of 128 bytes whose 16-byte
+// words are exchanged by word ^ slot % 8 (the 128-byte swizzle).  z's rows and the parts, which lora_down.cu has left in
+// order, come by cp.async, two to four stages of 64 slots; it fills whole lines at 2.3 times the rate at which it fills words
+// that lie apart.
 //
 // The tensor cores cut what they add off at the accumulator's last bit, so that a sum of n products is too small by some
 // n 2^-25 of itself.  Every 128 slots the sums move on to the other half of the tensor memory, and the first are added to
@@ -19,26 +20,26 @@ namespace ft {
 namespace {
 
 constexpr int kTcThreads = 512, kTcSlots = 64, kTcCols = 256, kTcRing = 8, kTcWindow = 2;      // kTcWindow: stages of an accumulator
-constexpr uint32_t kTcBlock = 144;                                           // bytes between blocks of eight columns or ranks
-constexpr uint32_t kTcZGroup = kTcCols / 8 * kTcBlock, kTcZStage = kTcSlots / 8 * kTcZGroup;      // bytes between groups of eight slots
-constexpr uint32_t kTcWGroup = 128 / 8 * kTcBlock, kTcWPass = kTcSlots / 8 * kTcWGroup;
+constexpr uint32_t kTcGroup = 1024, kTcAtom = kTcSlots / 8 * kTcGroup;       // bytes of eight slots' lines, of 64 columns or ranks
+constexpr uint32_t kTcZStage = kTcCols / 64 * kTcAtom, kTcWPass = 128 / 64 * kTcAtom;
 
 // MMAs that a step of 16 slots takes, and rows of the accumulator that hold sums.
 __host__ __device__ inline int32_t tc_passes(int32_t rank) { return 3 * rank <= 128 ? 1 : 2 * rank <= 128 ? 2 : 3; }
 __host__ __device__ inline int32_t tc_stages(int32_t passes) { return 5 - passes; }
 __host__ __device__ inline uint32_t tc_stage_bytes(int32_t passes) { return kTcZStage + static_cast<uint32_t>(passes) * kTcWPass; }
 
-// Shared-memory descriptor without swizzle: bytes between blocks along K and along M or N.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t at, uint32_t along_k, uint32_t along_mn) {
-    return static_cast<uint64_t>((at & 0x3FFFFu) >> 4) | static_cast<uint64_t>(along_k >> 4) << 16 |
-           static_cast<uint64_t>(along_mn >> 4) << 32 | 1ull << 46;
+// Shared-memory descriptor of an M- or N-major operand with the 128-byte swizzle.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t at) {
+    return static_cast<uint64_t>((at & 0x3FFFFu) >> 4) | static_cast<uint64_t>(kTcAtom >> 4) << 16 |
+           static_cast<uint64_t>(kTcGroup >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
 // WJ: words of a stage's parts that a thread copies.
 template <int WJ>
 __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __grid_constant__ GradArgs<__nv_bfloat16> a) {
     using T = __nv_bfloat16;
-    extern __shared__ __align__(128) uint8_t tc_smem[];
+    extern __shared__ uint8_t tc_smem_raw[];
+    uint8_t* tc_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int32_t row_ring[kTcRing][kTcSlots];      // rows of z of the stages ahead
     __shared__ __align__(8) uint64_t done[4];
     __shared__ uint32_t tmem_at;
@@ -84,20 +85,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
     constexpr int WARPS = kTcThreads / 32, ZJ = kTcSlots / WARPS;
     const bool in = col0 + lane * 8 < cols;
     const T* z_base = job.z + (in ? col0 + lane * 8 : 0);
-    const uint32_t z_to = smem_u32(tc_smem) + static_cast<uint32_t>(lane) * kTcBlock + static_cast<uint32_t>(warp / 8) * kTcZGroup + warp % 8 * 16;
-    // words of the parts: 64 slots' ranks of one part after the other, each a run of the workspace
-    const int32_t G = R / 8, part_words = kTcSlots * G;
-    const T* w_src[WJ];
+    const uint32_t z_to = smem_u32(tc_smem) + static_cast<uint32_t>(lane / 8) * kTcAtom + static_cast<uint32_t>(warp) * 128 + (lane % 8 ^ warp % 8) * 16;
+    // words of the parts: a slot's three times R ranks after the other's, a run of the workspace
+    const int32_t G = R / 8;
+    const T* w_src = job.w_parts + static_cast<int64_t>(ck.first) * 3 * R + tid * 8;
     uint32_t w_to[WJ];
     int32_t w_slot[WJ];
 #pragma unroll
     for (int j = 0; j < WJ; ++j) {
-        const int32_t at = tid + j * kTcThreads, t = at / part_words, q = at - t * part_words, s = q / G, g = q - s * G;
-        const int32_t pass = passes == 3 ? t : passes == 2 ? t / 2 : 0, row = passes == 3 || (passes == 2 && t == 2) ? 0 : t * R;
-        w_to[j] = smem_u32(tc_smem) + kTcZStage + static_cast<uint32_t>(pass) * kTcWPass + static_cast<uint32_t>(row / 8 + g) * kTcBlock +
-                  static_cast<uint32_t>(s / 8) * kTcWGroup + static_cast<uint32_t>(s % 8) * 16;
-        w_src[j] = job.w_parts + (static_cast<int64_t>(t) * a.slots.n_slots + ck.first) * R + q * 8;
-        w_slot[j] = t < 3 ? s : 1 << 30;
+        const int32_t at = tid + j * kTcThreads, s = at / (3 * G), q = at - s * 3 * G, t = q / G;
+        const int32_t pass = passes == 3 ? t : passes == 2 ? t / 2 : 0, word = passes == 3 || (passes == 2 && t == 2) ? q - t * G : q;
+        w_to[j] = smem_u32(tc_smem) + kTcZStage + static_cast<uint32_t>(pass) * kTcWPass + static_cast<uint32_t>(word / 8) * kTcAtom +
+                  static_cast<uint32_t>(s) * 128 + static_cast<uint32_t>(word % 8 ^ s % 8) * 16;
+        w_slot[j] = s < kTcSlots ? s : 1 << 30;
     }
     auto load = [&](int32_t i) {      // stages in turn
         const uint32_t stage = static_cast<uint32_t>(i % stages) * stage_bytes;
@@ -107,13 +107,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
             const int32_t s = warp + j * WARPS;
             const bool there = in && s < left;
             const T* src = there ? z_base + static_cast<int64_t>(row_ring[i % kTcRing][s]) * cols : job.z;
-            copy16_at(z_to + stage + j * (WARPS / 8) * kTcZGroup, src, there);
+            copy16_at(z_to + stage + j * WARPS * 128, src, there);
         }
 #pragma unroll
         for (int j = 0; j < WJ; ++j) {
-            if (w_slot[j] < kTcSlots) copy16_at(w_to[j] + stage, w_slot[j] < left ? w_src[j] : job.w_parts, w_slot[j] < left);
-            w_src[j] += kTcSlots * R;
+            if (w_slot[j] < kTcSlots) copy16_at(w_to[j] + stage, w_slot[j] < left ? w_src + j * kTcThreads * 8 : job.w_parts, w_slot[j] < left);
         }
+        w_src += kTcSlots * 3 * R;
     };
 
     constexpr int TC = kTcCols * 128 / kTcThreads;      // sums of a thread: row 32 (warp % 4) + lane, columns TC (warp / 4) ..
@@ -154,19 +154,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
             for (int32_t p = 0; p < passes; ++p)
 #pragma unroll
                 for (int k = 0; k < kTcSlots / 16; ++k)
-                    tc_mma_f16(d, tc_desc(ws + static_cast<uint32_t>(p) * kTcWPass + k * 2 * kTcWGroup, kTcWGroup, kTcBlock),
-                               tc_desc(zs + k * 2 * kTcZGroup, kTcZGroup, kTcBlock), idesc, i % kTcWindow || p || k);
+                    tc_mma_f16(d, tc_desc(ws + static_cast<uint32_t>(p) * kTcWPass + k * 2 * kTcGroup), tc_desc(zs + k * 2 * kTcGroup), idesc,
+                               i % kTcWindow || p || k);
             tc_commit(&done[i % 4]);
         }
-        if (i > 0) {
-            ok = mbar_wait_warp(&done[(i - 1) % 4], static_cast<uint32_t>((i - 1) / 4 & 1), a.err);
-            if (ok && i % kTcWindow == 0) {
-                tc_fence_after();
-                drain(i / kTcWindow - 1);
-            }
-        }
+        if (i > 0) ok = mbar_wait_warp(&done[(i - 1) % 4], static_cast<uint32_t>((i - 1) / 4 & 1), a.err);
         if (i + stages - 1 < steps) load(i + stages - 1);      // where the MMAs just waited for read
         copies_commit();
+        if (ok && i > 0 && i % kTcWindow == 0) {
+            tc_fence_after();
+            drain(i / kTcWindow - 1);
+        }
         if (tid < kTcSlots) row_ring[(i + AHEAD) % kTcRing][tid] = next / job.div;
         next = slot_of(i + AHEAD + 1);
     }
@@ -214,7 +212,7 @@ int launch_lora_grad_tc(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s)
     const GradArgs<__nv_bfloat16> a = grad_args<__nv_bfloat16>(jobs, p, kTcCols, &blocks);
     const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kTcThreads);
     const int32_t passes = tc_passes(p.rank);
-    const size_t sm = static_cast<size_t>(tc_stages(passes)) * tc_stage_bytes(passes);
+    const size_t sm = static_cast<size_t>(tc_stages(passes)) * tc_stage_bytes(passes) + 1024;
     auto go = [&](auto k) { return launch_with(k, "lora_grad_tc_kernel", grid, block, sm, false, 1, s, a); };
     if (p.rank <= 16) return go(lora_grad_tc_kernel<1>);
     if (p.rank <= 40) return go(lora_grad_tc_kernel<2>);
