@@ -27,7 +27,6 @@ int check_router(int64_t tokens, int32_t n_experts, int32_t top_k, int32_t dtype
 // ------------------------------------------------------- low-rank adapters
 constexpr int32_t kLoraSmallMean = 16;        // slots per adapter on average that go by tiles of 16
 constexpr int64_t kLoraWideMean = 512;        // from how many on by tiles of 128
-constexpr int64_t kLoraLeaderSlots = 256;     // slots up to which the CTAs find their tiles among the ids
 
 struct LoraShape {
     int64_t tokens, n_slots, ncols, nrows;
@@ -54,7 +53,7 @@ int check_lora(int64_t tokens, int32_t top_k, int32_t n_adapters, int32_t rank, 
 // Slots of a tile.
 int lora_width(int64_t n_slots, int32_t n_adapters, int32_t rank) {
     if (n_slots <= kLoraSmallMean * n_adapters) return 16;
-    return n_slots < kLoraWideMean * n_adapters || n_slots <= kLoraLeaderSlots || rank > 64 ? 64 : 128;
+    return n_slots < kLoraWideMean * n_adapters || rank > 64 ? 64 : 128;
 }
 
 int64_t lora_tiles(int64_t n_slots, int32_t n_adapters, int width) {
@@ -80,7 +79,6 @@ struct LoraWs {
     int width;
     int64_t n_tiles;
     int32_t chunk;
-    bool ordered;
 };
 
 // rows: of the gradient of x, where slots share a row of x.
@@ -89,9 +87,9 @@ LoraWs lora_ws(uint8_t* base, const LoraShape& h, bool backward, bool share) {
     const size_t S = static_cast<size_t>(h.n_slots), R = static_cast<size_t>(h.rank);
     size_t at = 0;
     L.width = lora_width(h.n_slots, h.n_adapters, h.rank);
-    L.ordered = backward || h.n_slots > kLoraLeaderSlots;
-    L.n_tiles = L.ordered ? lora_tiles(h.n_slots, h.n_adapters, L.width) : h.n_slots;
-    if (L.ordered) at = al256(fp8_order_layout(base, h.n_slots, h.n_adapters, false, &L.order));
+    L.n_tiles = lora_tiles(h.n_slots, h.n_adapters, L.width);
+    if (!backward && h.n_slots <= kLoraFewSlots) return L;      // needs none
+    at = al256(fp8_order_layout(base, h.n_slots, h.n_adapters, false, &L.order));
     L.u = take_bytes(&at, S * R * 4);
     if (backward) {
         L.v = take_bytes(&at, S * R * 4);
@@ -127,18 +125,15 @@ size_t lora_most(const LoraShape& h, bool backward, bool share) {
     take(static_cast<int64_t>(kLoraSmallMean) * h.n_adapters / h.top_k);
     take((kLoraWideMean * h.n_adapters - 1) / h.top_k);
     take(kFastRouteSlots / h.top_k);
-    take(kLoraLeaderSlots / h.top_k + 1);
     return most;
 }
 
 LoraPlan lora_plan(const LoraShape& h, const LoraWs& L, const int32_t* ids, const float* scales, uint32_t* err, bool backward) {
     LoraPlan p{};
     p.ids = ids;
-    if (L.ordered) {
-        p.offsets = L.order.offsets;
-        p.tiles = L.order.tiles;
-        p.perm = L.order.perm;
-    }
+    p.offsets = L.order.offsets;
+    p.tiles = L.order.tiles;
+    p.perm = L.order.perm;
     p.scales = scales;
     p.n_slots = static_cast<int32_t>(h.n_slots);
     p.n_adapters = h.n_adapters;
@@ -264,12 +259,15 @@ int ft_lora_add(const void* x, int32_t dtype, const void* a, const void* b, cons
     if (int st = fp8_error_word(&err)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LoraPlan p = lora_plan(h, L, ids, scales, err, false);
-    if (L.ordered)
-        if (int st = launch_lora_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
+    const bool f32 = out_dtype == FT_DTYPE_F32;
+    if (h.n_slots <= kLoraFewSlots)
+        return launch_lora_few(LoraFew{x, a, b, add, out, static_cast<int32_t>(ncols), static_cast<int32_t>(nrows), x_per_slot ? 1 : top_k, f32},
+                               p, dtype, s);
+    if (int st = launch_lora_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
     float* u = reinterpret_cast<float*>(ws + L.u);
     const LoraDown down{x, a, u, nullptr, static_cast<int32_t>(ncols), x_per_slot ? 1 : top_k, false};
     if (int st = launch_lora_down(&down, 1, p, dtype, s)) return st;
-    const LoraUp up{u, b, add, out, nullptr, static_cast<int32_t>(nrows), false, out_dtype == FT_DTYPE_F32};
+    const LoraUp up{u, b, add, out, nullptr, static_cast<int32_t>(nrows), false, f32};
     return launch_lora_up(up, p, dtype, s);
 }
 

@@ -276,7 +276,7 @@ int launch_combine_grad(const void* dy, int dy_dtype, const void* rows, int rows
 // ------------------------------------------------- low-rank adapters
 // Slots by adapter, and what the kernels of a call share.
 struct LoraPlan {
-    const int32_t *ids, *offsets, *tiles, *perm;      // perm null: CTAs find their tiles among the ids
+    const int32_t *ids, *offsets, *tiles, *perm;
     const float* scales;                              // per adapter, or null: 1
     int32_t n_slots, n_adapters, rank;
     int width;               // slots of a tile: 128, 64 or 16
@@ -310,6 +310,16 @@ struct LoraUp {        // out[s] = add[s] + scale W u[s]; launched to overlap la
 };
 int launch_lora_up(const LoraUp& j, const LoraPlan& p, int dtype, cudaStream_t s);
 int launch_lora_up_bf16(const LoraUp& j, const LoraPlan& p, cudaStream_t s);
+
+struct LoraFew {       // the whole of ft_lora_add for up to kLoraFewSlots slots (plan: ids, scales, sizes)
+    const void *x, *a, *b, *add;
+    void* out;         // fp32 (out_f32) or the adapters' type
+    int32_t ncols, nrows, div;
+    bool out_f32;
+};
+constexpr int64_t kLoraFewSlots = 256;
+int launch_lora_few(const LoraFew& f, const LoraPlan& p, int dtype, cudaStream_t s);
+int launch_lora_few_bf16(const LoraFew& f, const LoraPlan& p, cudaStream_t s);
 
 struct LoraGrad {      // out[e] = sum over its slots of scale w[s] z[s / div]; out null: not wanted
     const void* z;

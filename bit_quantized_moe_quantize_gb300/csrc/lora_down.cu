@@ -58,9 +58,9 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
     const uint32_t size = cluster_size(), rank = cluster_rank();
     const DownJob<T>& job = a.job[blockIdx.y];
     const int32_t tid = static_cast<int32_t>(threadIdx.x), warp = tid >> 5, lane = tid & 31, b = static_cast<int32_t>(blockIdx.x / size);
-    if (blockIdx.y == 0 && rank == 0) {      // the tiles are no fewer than the slots' MTs, or than the slots
-        const int64_t s = a.slots.perm ? static_cast<int64_t>(b) * MT + tid : b;
-        if (tid < (a.slots.perm ? MT : 1) && s < a.slots.n_slots) {
+    if (blockIdx.y == 0 && rank == 0 && tid < MT) {      // the tiles are no fewer than the slots' MTs
+        const int64_t s = static_cast<int64_t>(b) * MT + tid;
+        if (s < a.slots.n_slots) {
             const int32_t id = __ldg(a.slots.ids + s);
             if (id < -1 || id >= a.slots.n_adapters) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
         }

@@ -8,8 +8,7 @@
 // ring of stages in shared memory, add's words at the place of the thread that wants them.  A thread's results are made
 // eight neighbours, by where W's columns are put or by an exchange between four lanes, and written as whole 16-byte words.
 //
-// Rows without an adapter are copied (or zeroed) by CTAs of their own, or, where CTAs find their tiles among
-// the ids, by the slot's own CTA.
+// Rows without an adapter are copied (or zeroed) by CTAs of their own.
 #pragma once
 
 #include <type_traits>
@@ -56,17 +55,17 @@ __device__ __forceinline__ void turn_pairs(float (&v)[8], int32_t lane) {
 }
 
 // out := add or 0, columns [c0, c1) of n slots without an adapter, by the whole CTA.
-template <typename T, typename YT, int THREADS>
-__device__ __forceinline__ void up_pass(const UpArgs<T>& a, const int32_t* slots, int32_t n, int32_t c0, int32_t c1) {
-    if (a.add == a.out) return;
+template <typename YT, int THREADS>
+__device__ __forceinline__ void up_pass(const void* add, void* out, int32_t cols, const int32_t* slots, int32_t n, int32_t c0, int32_t c1) {
+    if (add == out) return;
     constexpr int V = 16 / static_cast<int>(sizeof(YT));
     const uint32_t words = static_cast<uint32_t>(c1 - c0) / V;
 #pragma unroll 8
     for (uint32_t i = threadIdx.x; i < n * words; i += THREADS) {
         const uint32_t row = i / words;
-        const int64_t at = static_cast<int64_t>(slots[row]) * a.cols + c0 + (i - row * words) * V;
-        const uint4 v = a.add ? __ldg(reinterpret_cast<const uint4*>(static_cast<const YT*>(a.add) + at)) : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(static_cast<YT*>(a.out) + at) = v;
+        const int64_t at = static_cast<int64_t>(slots[row]) * cols + c0 + (i - row * words) * V;
+        const uint4 v = add ? __ldg(reinterpret_cast<const uint4*>(static_cast<const YT*>(add) + at)) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(static_cast<YT*>(out) + at) = v;
     }
 }
 
@@ -100,18 +99,11 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
         __syncthreads();
         if (none) slots[atomicAdd(&n_none, 1)] = s;      // rows of their own: the order does not show
         __syncthreads();
-        up_pass<T, YT, THREADS>(a, slots, n_none, c0, c1);
+        up_pass<YT, THREADS>(a.add, a.out, cols, slots, n_none, c0, c1);
         return;
     }
     const LoraTile tile = find_tile<MT>(a.slots, static_cast<int32_t>(blockIdx.x) - a.fills, slots);
-    if (tile.n == 0) {
-        if (tile.adapter < 0) {
-            if (tid == 0) slots[0] = tile.first;
-            __syncthreads();
-            up_pass<T, YT, THREADS>(a, slots, 1, c0, c1);
-        }
-        return;
-    }
+    if (tile.n == 0) return;
     T* smem = reinterpret_cast<T*>(up_smem);
     const T* w = a.w + static_cast<int64_t>(tile.adapter) * R * cols;
     // this thread's two rows, and the first column of its words of a group's 32
@@ -270,15 +262,15 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
 template <typename T, typename YT, int MT>
 int launch_up_typed(UpArgs<T> a, const LoraPlan& p, cudaStream_t s) {
     constexpr int CW = MT == kLoraSmallTile ? 128 : 64;
-    const int64_t blocks = (a.cols + CW - 1) / CW, tiles = p.n_tiles * (p.perm ? p.width / MT : 1);
+    const int64_t blocks = (a.cols + CW - 1) / CW, tiles = p.n_tiles * (p.width / MT);
     // runs of columns: CTAs enough to fill the GPU some times over, each of six stages or more
-    const int64_t some = p.perm ? p.n_slots / MT + 1 : tiles;      // tiles that there are, about
+    const int64_t some = p.n_slots / MT + 1;      // tiles that there are, about
     int64_t parts = 12 * static_cast<int64_t>(sm_count()) / some, most = (blocks + 5) / 6;
     if (tiles * blocks < 8 * static_cast<int64_t>(sm_count())) most = blocks;
     parts = parts < 1 ? 1 : parts < most ? parts : most;
     a.per = static_cast<int32_t>((blocks + parts - 1) / parts * CW);
     parts = (a.cols + a.per - 1) / a.per;
-    a.fills = p.perm ? static_cast<int32_t>((static_cast<int64_t>(p.n_slots) + kUpFill - 1) / kUpFill) : 0;
+    a.fills = static_cast<int32_t>((static_cast<int64_t>(p.n_slots) + kUpFill - 1) / kUpFill);
     const dim3 grid(static_cast<unsigned>(tiles + a.fills), static_cast<unsigned>(parts)), block(kLoraThreads);
     const int32_t r16 = (a.rank + 15) / 16 * 16;
     const size_t adds = a.add ? static_cast<size_t>(kLoraThreads) * (MT == kLoraSmallTile ? 1 : 2) * 2 * sizeof(YT) * 8 : 0;

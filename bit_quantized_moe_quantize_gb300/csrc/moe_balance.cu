@@ -322,12 +322,17 @@ int64_t balance_ctas(int64_t tokens, int32_t n_experts, int64_t most) {
     return ctas < 1 ? 1 : ctas < most ? ctas : most;
 }
 
+bool balance_single(int64_t tokens, int32_t n_experts, int32_t n_seqs) {
+    return n_seqs <= kSingleSeqs && tokens <= static_cast<int64_t>(kSingleCtas) * kSingleRounds * rows_at_once(n_experts);
+}
+
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
 // The CTAs depend on the device; the workspace has room for the most that there can be.
 size_t balance_workspace(int64_t tokens, int32_t n_experts, int32_t n_seqs) {
+    if (balance_single(tokens, n_experts, n_seqs)) return 0;
     const size_t S = static_cast<size_t>(n_seqs);
     const size_t pieces = static_cast<size_t>(balance_ctas(tokens, n_experts, kBalanceCtas)) + S;
     return 256 + up256(pieces * n_experts * sizeof(Piece)) + up256(pieces * 4) + up256(S * ((n_experts + 7) / 8) * 4) + up256(S * 4);
@@ -351,7 +356,7 @@ int launch_balance(const BalanceParams& p, const void* logits, int dtype, int64_
     a.counts = counts;
     a.seq_scale = seq_scale;
     const int64_t rows = rows_at_once(p.n_experts);
-    a.single = p.n_seqs <= kSingleSeqs && p.tokens <= kSingleCtas * kSingleRounds * rows;
+    a.single = balance_single(p.tokens, p.n_experts, p.n_seqs);
     unsigned cluster = 1;
     while (a.single && cluster < kSingleCtas && p.tokens > static_cast<int64_t>(cluster) * kLeastRounds * rows) cluster *= 2;
     int64_t ctas = a.single ? cluster : balance_ctas(p.tokens, p.n_experts, std::min<int64_t>(4 * sm_count(), kBalanceCtas));

@@ -739,7 +739,7 @@ FT_API int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, 
  *               and raise FT_DEVERR_BAD_EXPERT_ID
  *   seq_offsets device int32 [n_seqs + 1], ascending, or NULL: one sequence of all rows (n_seqs 1)
  *   loss device fp32 [1] out; counts int32 [n_seqs][n_experts] out; seq_scale fp32 [n_seqs] out
- * ft_moe_balance_workspace_bytes returns 0 for invalid arguments.
+ * ft_moe_balance_workspace_bytes returns 0 for invalid arguments, and where a call needs none (NULL will do).
  */
 FT_API size_t ft_moe_balance_workspace_bytes(int64_t tokens, int32_t n_experts, int32_t n_seqs);
 FT_API int ft_moe_balance_loss(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* topk_ids,
@@ -797,7 +797,8 @@ FT_API int ft_moe_combine_backward(const void* grad_y, int32_t y_dtype, const vo
  *   out     device, the same, out; every element is written
  * All matrices and rows 16-byte aligned.  rank: a multiple of 8, at most FT_MAX_LORA_RANK; ncols and nrows:
  * multiples of 8, at most FT_MAX_NCOLS; n_adapters <= FT_MAX_EXPERTS; tokens * top_k < 2^31.
- * ft_lora_workspace_bytes returns 0 for invalid arguments; backward: for ft_lora_backward.
+ * ft_lora_workspace_bytes returns 0 for invalid arguments, and where a call needs none (NULL will do: up to 256
+ * slots of ft_lora_add); backward: for ft_lora_backward.
  */
 FT_API size_t ft_lora_workspace_bytes(int64_t tokens, int32_t top_k, int32_t n_adapters, int32_t rank, int64_t ncols,
                                       int64_t nrows, int32_t backward);
