@@ -300,7 +300,7 @@ int ft_lora_backward(const void* grad_out, const void* x, int32_t dtype, const v
     if (int st = check_workspace(workspace, workspace_bytes, L.total)) return st;
     uint32_t* err = nullptr;
     if (int st = fp8_error_word(&err)) return st;
-    const LoraPlan p = lora_plan(h, L, ids, scales, err, true);
+    LoraPlan p = lora_plan(h, L, ids, scales, err, true);
     if (int st = launch_lora_order(ids, h.n_slots, n_adapters, L.width, L.order, s)) return st;
     float *u = reinterpret_cast<float*>(ws + L.u), *v = reinterpret_cast<float*>(ws + L.v);
     const int32_t K = static_cast<int32_t>(ncols), N = static_cast<int32_t>(nrows), div = x_per_slot ? 1 : top_k;
@@ -317,6 +317,7 @@ int ft_lora_backward(const void* grad_out, const void* x, int32_t dtype, const v
         const LoraUp up = share ? LoraUp{v, a, nullptr, rows, present, K, true, true}
                                 : LoraUp{v, a, add, grad_x, nullptr, K, true, false};
         if (int st = launch_lora_up(up, p, dtype, s)) return st;
+        p.overlap_grad = !share;
         if (share)
             if (int st = launch_combine(rows, FT_DTYPE_F32, present, add, grad_x, dtype, tokens, top_k, ncols, s)) return st;
     }

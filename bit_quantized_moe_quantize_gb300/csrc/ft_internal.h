@@ -283,6 +283,7 @@ struct LoraPlan {
     int64_t n_tiles;         // tiles at most
     int32_t chunk;           // slots of a chunk of the matrices' gradients
     uint32_t* err;           // raised by launch_lora_down for ids that are no adapter
+    bool overlap_grad;       // launch_lora_up directly before launch_lora_grad
     int32_t down_jobs, down_cols;      // first products that a call of this kind can have, their longest rows
 };
 // Numbers of chunks that lora_grad.cu gives out at most.

@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
     constexpr int ZS = THREADS / 8, ZR = (MT + ZS - 1) / ZS;                                        // rows that a copy of a word per thread takes
     extern __shared__ __align__(128) uint8_t down_smem[];
     __shared__ int32_t slots[MT];
-    let_next_grid_start();
+    wait_for_prior_grid();
+    let_next_grid_start();      // behind the wait: what comes up early may read the order
     const uint32_t size = cluster_size(), rank = cluster_rank();
     const DownJob<T>& job = a.job[blockIdx.y];
     const int32_t tid = static_cast<int32_t>(threadIdx.x), warp = tid >> 5, lane = tid & 31, b = static_cast<int32_t>(blockIdx.x / size);
@@ -219,7 +220,7 @@ int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStr
     while (cluster < 8 && p.n_tiles * p.down_jobs * 2 * cluster <= fit && p.down_cols >= static_cast<int32_t>(2 * cluster) * 4 * kDownCols)
         cluster *= 2;
     const dim3 grid(static_cast<unsigned>(p.n_tiles * cluster), static_cast<unsigned>(jobs)), block(kLoraThreads);
-    auto go = [&](auto k) { return launch_with(k, "lora_down_kernel", grid, block, sm, false, cluster, s, a); };
+    auto go = [&](auto k) { return launch_with(k, "lora_down_kernel", grid, block, sm, true, cluster, s, a); };
     if (a.rank <= 16) return go(lora_down_kernel<T, MT, 2>);
     if (a.rank <= 32) return go(lora_down_kernel<T, MT, 4>);
     if (a.rank <= 64) return go(lora_down_kernel<T, MT, 8>);

@@ -33,7 +33,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid
     const GradJob<T>& job = a.job[second ? 1 : 0];
     const int32_t col0 = (static_cast<int32_t>(blockIdx.y) - (second ? a.blocks0 : 0)) * CC;
     const Chunk ck = find_chunk<kGradThreads>(a.slots, static_cast<int32_t>(blockIdx.x), a.per);
-    if (ck.n == 0) return;
+    if (ck.n == 0) {
+        wait_for_prior_grid();
+        return;
+    }
     const int32_t R = a.rank, r16 = (R + 15) / 16 * 16, mr = r16 / 16, cols = job.cols;
     const int32_t wf = r16 + 4, w_bytes = kGradSlots * wf * 4;      // pitch of w's rows: lanes' pairs of slots in different banks
     T* zs_all = reinterpret_cast<T*>(grad_smem);
@@ -167,6 +170,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid
             }
         }
     }
+    wait_for_prior_grid();
 }
 
 // Adds up the chunks of adapters that have several, and zeroes those that have none.
@@ -211,7 +215,7 @@ int launch_grad_fp16(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
     const GradArgs<__half> a = grad_args<__half>(jobs, p, cc, &blocks);
     const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kGradThreads);
     const size_t sm = kGradStages * kGradSlots * static_cast<size_t>(cc + 8) * 2 + 2 * static_cast<size_t>(kGradSlots * (r16 + 4) * 4);
-    auto go = [&](auto k) { return launch_with(k, "lora_grad_kernel", grid, block, sm, false, 1, s, a); };
+    auto go = [&](auto k) { return launch_with(k, "lora_grad_kernel", grid, block, sm, p.overlap_grad, 1, s, a); };
     if (p.rank <= 16) return go(lora_grad_kernel<__half, 1, 4>);
     if (p.rank <= 32) return go(lora_grad_kernel<__half, 2, 4>);
     if (p.rank <= 64) return go(lora_grad_kernel<__half, 4, 4>);

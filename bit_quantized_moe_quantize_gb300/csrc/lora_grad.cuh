@@ -1,4 +1,5 @@
-// What the two kernels of the adapters' gradients share: their arguments, and the chunks of slots.
+// What the two kernels of the adapters' gradients share: their arguments, and the chunks of slots.  They may come up under the
+// tail of the second product (lora_up.cuh), whose results they do not read, and end behind it.
 #pragma once
 
 #include "lora.cuh"

@@ -48,7 +48,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
     const GradJob<T>& job = a.job[second ? 1 : 0];
     const int32_t col0 = (static_cast<int32_t>(blockIdx.y) - (second ? a.blocks0 : 0)) * kTcCols, cols = job.cols;
     const Chunk ck = find_chunk<kTcThreads>(a.slots, static_cast<int32_t>(blockIdx.x), a.per);
-    if (ck.n == 0) return;
+    if (ck.n == 0) {
+        wait_for_prior_grid();
+        return;
+    }
     const int32_t R = a.rank, passes = tc_passes(R), stages = tc_stages(passes), used = passes == 3 ? R : (4 - passes) * R;
     const uint32_t stage_bytes = tc_stage_bytes(passes);
     const int32_t* perm = a.slots.perm + ck.first;
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 512);
+    wait_for_prior_grid();
 }
 
 }  // namespace
@@ -213,7 +217,7 @@ int launch_lora_grad_tc(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s)
     const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kTcThreads);
     const int32_t passes = tc_passes(p.rank);
     const size_t sm = static_cast<size_t>(tc_stages(passes)) * tc_stage_bytes(passes) + 1024;
-    auto go = [&](auto k) { return launch_with(k, "lora_grad_tc_kernel", grid, block, sm, false, 1, s, a); };
+    auto go = [&](auto k) { return launch_with(k, "lora_grad_tc_kernel", grid, block, sm, p.overlap_grad, 1, s, a); };
     if (p.rank <= 16) return go(lora_grad_tc_kernel<1>);
     if (p.rank <= 40) return go(lora_grad_tc_kernel<2>);
     if (p.rank <= 64) return go(lora_grad_tc_kernel<3>);

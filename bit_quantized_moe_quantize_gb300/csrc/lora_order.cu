@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(kOrderThreads)
     lora_order_kernel(const int32_t* __restrict__ ids, int32_t n_slots, int32_t L, int32_t bits, int32_t width, int32_t* __restrict__ offsets,
                       int32_t* __restrict__ tiles, int32_t* __restrict__ perm) {
     extern __shared__ int32_t order_smem[];
+    let_next_grid_start();
     __shared__ int2 part[kOrderWarps];
     int32_t* hist = order_smem;                     // [warps][L] counts, then first places
     int32_t* start = hist + kOrderWarps * L;        // [L]

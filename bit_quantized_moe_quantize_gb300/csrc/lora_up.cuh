@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
             copies_commit();
         }
         wait_for_prior_grid();
+        let_next_grid_start();      // behind the wait: what comes up early may read the first products
         Wide16<T, TERMS> u[KS];
         const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.0f;
 #pragma unroll
