@@ -217,7 +217,7 @@ int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStr
     // leaving out one product changes no bit of the other.
     const int64_t per_sm = static_cast<int64_t>(220 * 1024 / (sm + 1024)), fit = (per_sm < 8 ? per_sm : 8) * sm_count();
     unsigned cluster = 1;
-    while (cluster < 8 && p.n_tiles * p.down_jobs * 2 * cluster <= fit && p.down_cols >= static_cast<int32_t>(2 * cluster) * 4 * kDownCols)
+    while (cluster < 8 && p.n_tiles * p.down_jobs * 2 * cluster <= fit * 5 / 4 && p.down_cols >= static_cast<int32_t>(2 * cluster) * 4 * kDownCols)
         cluster *= 2;
     const dim3 grid(static_cast<unsigned>(p.n_tiles * cluster), static_cast<unsigned>(jobs)), block(kLoraThreads);
     auto go = [&](auto k) { return launch_with(k, "lora_down_kernel", grid, block, sm, true, cluster, s, a); };

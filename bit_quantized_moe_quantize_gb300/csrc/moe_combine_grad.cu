@@ -7,7 +7,8 @@
 //
 // Memory-bound: the rows are read once and as much is written.  A slot is one to eight warps', as many as leave
 // work for all of the GPU where slots are few; dy comes from the caches for all of a token's slots but the first.
-// Rows that are no whole 16-byte words go by single elements.
+// Where rows do not start at 16-byte words, the words inside of a row are read and written whole all the same, dy beside
+// them and the elements around them one by one (combine_grad_ragged_kernel).
 #include "fp8_common.cuh"
 #include "ft_internal.h"
 
@@ -90,6 +91,60 @@ __global__ void __launch_bounds__(kGradThreads)
     if (there && lane == 0 && warp % warps == 0) grad_weights[slot] = sum;
 }
 
+// Rows that start anywhere: V elements to a 16-byte word, `rows` and `grad_rows` as far from one as each other.
+template <typename TI, typename TY, int V>
+__global__ void __launch_bounds__(kGradThreads)
+    combine_grad_ragged_kernel(const TY* __restrict__ dy, const TI* __restrict__ rows, const float* __restrict__ weights,
+                               TI* __restrict__ grad_rows, float* __restrict__ grad_weights, int64_t n_slots, int32_t ncols,
+                               uint32_t top_k, int32_t warps) {
+    __shared__ float part[kGradWarps];
+    const int32_t warp = static_cast<int32_t>(threadIdx.x >> 5), lane = static_cast<int32_t>(lane_id());
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * (kGradWarps / warps) + warp / warps;
+    const bool there = slot < n_slots;
+    const float w = there ? __ldg(weights + slot) : 0.0f;
+    float sum = 0.0f;
+    if (there) {
+        const TY* g = dy + static_cast<int64_t>(static_cast<uint32_t>(slot) / top_k) * ncols;
+        const TI* r = rows + slot * ncols;
+        TI* out = grad_rows ? grad_rows + slot * ncols : nullptr;
+        const int32_t before = static_cast<int32_t>(reinterpret_cast<uintptr_t>(r) % 16 / sizeof(TI));      // elements of the first word that are not the row's
+        const int32_t words = (before + ncols + V - 1) / V;
+#pragma unroll 2
+        for (int32_t i = warp % warps * 32 + lane; i < words; i += 32 * warps) {
+            const int32_t c = i * V - before;
+            if (c >= 0 && c + V <= ncols) {
+                float x[V] = {}, y[V];
+                if (w != 0.0f) load_vec<TI, V>(r + c, x);
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] = w != 0.0f ? to_f32<TY>(__ldg(g + c + j)) : 0.0f;
+                __align__(16) TI o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    sum = fmaf(x[j], y[j], sum);
+                    o[j] = from_f32<TI>(w * y[j]);
+                }
+                if (out) *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(o);
+            } else {
+                for (int32_t q = c < 0 ? 0 : c; q < ncols && q < c + V; ++q) {
+                    const float y = w != 0.0f ? to_f32<TY>(g[q]) : 0.0f;
+                    if (w != 0.0f) sum = fmaf(to_f32<TI>(r[q]), y, sum);
+                    if (out) out[q] = from_f32<TI>(w * y);
+                }
+            }
+        }
+    }
+    if (!grad_weights) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (warps > 1) {
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int32_t i = 0; i < warps; ++i) sum += part[warp / warps * warps + i];
+    }
+    if (there && lane == 0 && warp % warps == 0) grad_weights[slot] = sum;
+}
+
 template <typename TI, typename TY>
 int launch_grad_typed(const void* dy, const void* rows, const float* weights, void* grad_rows, float* grad_weights,
                       int64_t tokens, int32_t top_k, int64_t ncols, cudaStream_t s) {
@@ -107,8 +162,10 @@ int launch_grad_typed(const void* dy, const void* rows, const float* weights, vo
     TI* o = static_cast<TI*>(grad_rows);
     const uint32_t k = static_cast<uint32_t>(top_k);
     if (wide) combine_grad_kernel<TI, TY, V><<<grid, block, 0, s>>>(g, r, weights, o, grad_weights, slots, ncols / V, k, warps);
+    else if (ncols < (1 << 30) && (!o || (reinterpret_cast<uintptr_t>(o) - reinterpret_cast<uintptr_t>(r)) % 16 == 0))
+        combine_grad_ragged_kernel<TI, TY, V><<<grid, block, 0, s>>>(g, r, weights, o, grad_weights, slots, static_cast<int32_t>(ncols), k, warps);
     else combine_grad_kernel<TI, TY, 1><<<grid, block, 0, s>>>(g, r, weights, o, grad_weights, slots, ncols, k, warps);
-    return check_launch("combine_grad_kernel", grid, block, 0);
+    return check_launch(wide ? "combine_grad_kernel" : "combine_grad_kernel (ragged)", grid, block, 0);
 }
 
 }  // namespace
