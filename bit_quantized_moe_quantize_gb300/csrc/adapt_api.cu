@@ -93,8 +93,9 @@ LoraWs lora_ws(uint8_t* base, const LoraShape& h, bool backward, bool share) {
     L.u = take_bytes(&at, S * R * 4);
     if (backward) {
         L.v = take_bytes(&at, S * R * 4);
-        L.u_parts = take_bytes(&at, 3 * S * R * 2);
-        L.v_parts = take_bytes(&at, 3 * S * R * 2);
+        const size_t lines = static_cast<size_t>(lora_part_kinds(h.rank)) * S * 128;
+        L.u_parts = take_bytes(&at, lines);
+        L.v_parts = take_bytes(&at, lines);
         const int64_t most = lora_most_chunks(h.ncols, h.nrows), all = h.n_slots / 256;
         L.chunk = lora_chunk(h.n_slots, most);
         const size_t chunks = static_cast<size_t>((all < most ? all : most) + h.n_adapters);      // rises with the slots

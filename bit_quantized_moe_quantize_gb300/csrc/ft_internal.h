@@ -286,6 +286,7 @@ struct LoraPlan {
     bool overlap_grad;       // launch_lora_up directly before launch_lora_grad
     int32_t down_jobs, down_cols;      // first products that a call of this kind can have, their longest rows
 };
+int32_t lora_part_kinds(int32_t rank);      // lines of 128 bytes of a slot's parts (lora.cuh)
 // Numbers of chunks that lora_grad.cu gives out at most.
 inline int64_t lora_chunks(int64_t n_slots, int32_t n_adapters, int32_t chunk) { return n_slots / chunk + n_adapters; }
 
@@ -295,7 +296,7 @@ int launch_lora_order(const int32_t* ids, int64_t n_slots, int32_t n_adapters, i
 struct LoraDown {      // u[s] = W z[s / div]
     const void *z, *w;
     float* u;          // [slots][rank], or null
-    void* parts;       // [places][3][rank] bf16 parts of scale u, in order, whose sum it is; or null
+    void* parts;       // lines of the bf16 parts of scale u, whose sum it is (lora.cuh); or null
     int32_t cols, div;
     bool trans;        // W is [cols][rank], else [rank][cols]
 };

@@ -36,6 +36,14 @@ __device__ __forceinline__ float cluster_load(const void* p, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ float4 cluster_load4(const void* p, uint32_t rank) {      // p at a 16-byte word
+    uint32_t at;
+    float4 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 // cluster: CTAs per cluster along grid.x (1: none).
 template <typename... P, typename... A>
 int launch_with(void (*kernel)(P...), const char* name, dim3 grid, dim3 block, size_t smem, bool overlap, unsigned cluster,

@@ -188,6 +188,25 @@ struct Wide16<__half, TERMS> {
     }
 };
 
+// A slot's fp32 sums as three bf16 parts, as the matrices' gradients take them (lora_grad_tc.cu): rows of an MMA of 128, one for all
+// parts up to rank 40 (parts one after the other), one for the first two and one for the third up to rank 64, one for each
+// above.  64 rows make a line of 128 bytes, whose 16-byte words are exchanged by word ^ slot % 8, slots counted within
+// their adapter; lines of one kind lie in the order of the slots: [kinds][places][128 bytes].
+__host__ __device__ inline int32_t part_passes(int32_t rank) { return 3 * rank <= 128 ? 1 : 2 * rank <= 128 ? 2 : 3; }
+// Lines of a pass's slot; of the passes before.
+__host__ __device__ inline int32_t part_lines(int32_t rank, int32_t pass) {
+    const int32_t passes = part_passes(rank), rows = passes == 1 ? 3 * rank : passes == 2 && pass == 0 ? 2 * rank : rank;
+    return (rows + 63) / 64;
+}
+__host__ __device__ inline int32_t part_kinds(int32_t rank) {
+    int32_t n = 0;
+    for (int32_t p = 0; p < part_passes(rank); ++p) n += part_lines(rank, p);
+    return n;
+}
+// The pass of part t, and its first row there.
+__host__ __device__ inline int32_t part_pass(int32_t passes, int32_t t) { return passes == 3 ? t : passes == 2 ? t / 2 : 0; }
+__host__ __device__ inline int32_t part_row(int32_t passes, int32_t rank, int32_t t) { return passes == 3 || (passes == 2 && t == 2) ? 0 : t * rank; }
+
 // Elements between rows of `n` 16-bit values in shared memory: whole 16-byte words, an odd number of them, so that
 // eight rows' words at one column lie in different banks.
 inline __host__ __device__ int32_t odd_pitch(int32_t n) { return ((n + 7) / 8 | 1) * 8; }

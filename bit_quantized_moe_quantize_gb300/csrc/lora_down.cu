@@ -8,12 +8,14 @@
 // z and W come by cp.async, four stages of 64 values; in tiles of 16 slots the four warps share a
 // stage's values instead of its slots.  A row of a stage is one line of 128 bytes whose 16-byte words are exchanged by
 // word ^ row % 8: the copies fill whole lines (64 MB through shared memory 8.4 us; rows 144 bytes apart 11.8, words by
-// themselves 22), and a column of eight rows lies in all banks.
+// themselves 22), and a column of eight rows lies in all banks.  Where a tile's rows of z are neighbours, as in prompts and in
+// training, and where W's lines are 128 bytes, a fifth warp has them brought by TMA instead.
 //
 // The tensor cores cut what they add to an accumulator off at its last bit: after n additions a sum is too small
 // by some n 2^-25 of itself.  So a stage's sums start from 0 and are added to the others by the CUDA cores.
 #include <type_traits>
 
+#include "gemm_common.cuh"
 #include "lora.cuh"
 #include "ft_internal.h"
 #include "launch.cuh"
@@ -28,13 +30,15 @@ template <typename T>
 struct DownJob {
     const T *z, *w;
     float* u;               // or null
-    __nv_bfloat16* parts;   // or null
+    uint8_t* parts;         // or null
     int32_t cols, div;      // row of slot s: s / div
     bool trans;             // W's values of one column are neighbours ([cols][R])
 };
 
 template <typename T>
 struct DownArgs {
+    CUtensorMap zmap[2], wmap[2];      // boxes of MT rows, of a stage of W
+    bool tma[2], w_tma[2];
     DownJob<T> job[2];
     LoraSlots slots;
     const float* scales;
@@ -48,12 +52,15 @@ __host__ __device__ inline int32_t down_w_elems(int32_t rank) { return kDownCols
 
 // NT: tiles of eight ranks that there is room for.
 template <typename T, int MT, int NT>
-__global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_constant__ DownArgs<T> a) {
+__global__ void __launch_bounds__(MT > kLoraSmallTile ? kLoraThreads + 32 : kLoraThreads, MT == 128 && NT <= 8 ? 2 : 1) lora_down_kernel(const __grid_constant__ DownArgs<T> a) {
     constexpr int THREADS = kLoraThreads, PARTS = MT == kLoraSmallTile ? THREADS / 32 : 1;      // PARTS: warps that share a tile's sums
     constexpr int MS = MT == 128 ? 2 : 1, WARP_ROWS = 16 * MS;                                      // a warp's runs of 16 slots
     constexpr int ZS = THREADS / 8, ZR = (MT + ZS - 1) / ZS;                                        // rows that a copy of a word per thread takes
-    extern __shared__ __align__(128) uint8_t down_smem[];
+    constexpr bool TMA = MT > kLoraSmallTile;
+    extern __shared__ uint8_t down_smem_raw[];
+    uint8_t* down_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(down_smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int32_t slots[MT];
+    __shared__ __align__(8) uint64_t full[kDownStages];
     wait_for_prior_grid();
     let_next_grid_start();      // behind the wait: what comes up early may read the order
     const uint32_t size = cluster_size(), rank = cluster_rank();
@@ -66,8 +73,14 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
             if (id < -1 || id >= a.slots.n_adapters) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
         }
     }
-    const LoraTile tile = find_tile<MT>(a.slots, b, slots);
+    if (TMA && tid == 0) {
+        for (int i = 0; i < kDownStages; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    const LoraTile tile = find_tile<MT>(a.slots, b, slots);      // ends behind a barrier
     if (tile.n == 0) return;      // all of the cluster
+    // whether this tile's rows of z are neighbours
+    const bool run = TMA && a.tma[blockIdx.y] && job.div == 1 && slots[tile.n - 1] - slots[0] == tile.n - 1, w_tma = run && a.w_tma[blockIdx.y];
     const int32_t R = a.rank, nt = R / 8, cols = job.cols, pitch = down_turned_pitch(R);
     const int32_t stage_elems = MT * kDownCols + down_w_elems(R);
     T* smem = reinterpret_cast<T*>(down_smem);
@@ -80,7 +93,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < ZR; ++i) {
         const int32_t row = tid / 8 + ZS * i;
-        z[i] = row < tile.n ? job.z + static_cast<int64_t>(slots[row] / job.div) * cols : nullptr;
+        z[i] = row < tile.n && tid < THREADS ? job.z + static_cast<int64_t>(slots[row] / job.div) * cols : nullptr;
     }
     constexpr int WJ = (NT * 64 + THREADS - 1) / THREADS;      // 16-byte words of W's stage that a thread copies
     const int32_t nt8 = R * 8;                                 // words of the stage: 64 values of R rows
@@ -99,14 +112,23 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
             const int32_t col = (c0 + i) * kDownCols;
             T* zs = smem + i % kDownStages * stage_elems;
             T* ws = zs + MT * kDownCols;
+            if (TMA && tid == THREADS && (run || w_tma)) {
+                uint64_t* bar = &full[i % kDownStages];
+                mbar_arrive_expect_tx(bar, (run ? MT * 128u : 0u) + (w_tma ? static_cast<uint32_t>(R) * 128u : 0u));
+                if (run) tma_load_2d(zs, &a.zmap[blockIdx.y], col, slots[0], bar);
+                if (w_tma) tma_load_2d(ws, &a.wmap[blockIdx.y], TRANS ? 0 : col, tile.adapter * (TRANS ? cols : R) + (TRANS ? col : 0), bar);
+            }
+            if (TMA && tid >= THREADS) return;
 #pragma unroll
             for (int j = 0; j < ZR; ++j) {
+                if (run) break;
                 const bool there = col + part < cols && z[j] != nullptr;
                 copy16(zs + (tid / 8 + ZS * j) * kDownCols + z_word, there ? z[j] + col + part : job.z, there);
             }
             const T* wc = w + static_cast<int64_t>(col) * (TRANS ? R : 1);
 #pragma unroll
             for (int j = 0; j < WJ; ++j) {
+                if (w_tma) break;
                 const bool there = col + edge[j] < cols;
                 if (edge[j] < kDownCols) copy16(ws + to[j], there ? wc + from[j] : w, there);
             }
@@ -131,39 +153,49 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
             const int32_t n = min(2 * j + lane / 16, nt - 1);      // an odd last tile stands in for its neighbour
             wat[j] = TRANS ? (lane / 8 % 2 * 8 + l) * pitch + (R % 64 == 0 ? n ^ l : n) * 8 : (n * 8 + l) * kDownCols;
         }
+        bool ok = true;
         for (int32_t c = 0; c < n_chunks; ++c) {
             copies_wait<kDownStages - 2>();
-            __syncthreads();
+            if (run || w_tma) ok = mbar_wait(&full[c % kDownStages], static_cast<uint32_t>(c / kDownStages & 1), a.err) && ok;
+            ok = __syncthreads_and(ok);
+            if (!ok) break;
             if (c + kDownStages - 1 < n_chunks) load(c + kDownStages - 1);
             copies_commit();
             const T* zs = smem + c % kDownStages * stage_elems;
             const T* ws = zs + MT * kDownCols;
+            if (TMA && tid >= THREADS) continue;
             uint32_t x[MS][KK][4];
 #pragma unroll
             for (int m = 0; m < MS; ++m)
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) ldsm4(x[m][kk], zs + zat + m * 16 * kDownCols + zword[kk], false);
+            constexpr int JU = NT >= 4 && MS == 1 ? 2 : 1;      // pairs of W's tiles at once: enough sums that none waits for itself
 #pragma unroll
-            for (int j = 0; j < NT / 2; ++j) {
-                if (2 * j >= nt) break;
-                float sum[MS][2][4] = {};
+            for (int j0 = 0; j0 < NT / 2; j0 += JU) {
+                if (2 * j0 >= nt) break;
+                float sum[JU][MS][2][4] = {};
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
-                    uint32_t b[4];
-                    ldsm4(b, ws + wat[j] + wword[kk], TRANS);
+                    uint32_t b[JU][4];
 #pragma unroll
-                    for (int m = 0; m < MS; ++m) {
-                        mma16(sum[m][0], x[m][kk], b[0], b[1], T());
-                        mma16(sum[m][1], x[m][kk], b[2], b[3], T());      // behind an odd last tile: not looked at
-                    }
+                    for (int j = 0; j < JU; ++j) ldsm4(b[j], ws + wat[j0 + j] + wword[kk], TRANS);
+#pragma unroll
+                    for (int j = 0; j < JU; ++j)
+#pragma unroll
+                        for (int m = 0; m < MS; ++m) {      // behind the last tile: not looked at
+                            mma16(sum[j][m][0], x[m][kk], b[j][0], b[j][1], T());
+                            mma16(sum[j][m][1], x[m][kk], b[j][2], b[j][3], T());
+                        }
                 }
 #pragma unroll
-                for (int m = 0; m < MS; ++m)
+                for (int j = 0; j < JU; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        acc[m][2 * j][i] += sum[m][0][i];
-                        acc[m][2 * j + 1][i] += sum[m][1][i];
-                    }
+                    for (int m = 0; m < MS; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            acc[m][2 * (j0 + j)][i] += sum[j][m][0][i];
+                            acc[m][2 * (j0 + j) + 1][i] += sum[j][m][1][i];
+                        }
             }
         }
     };
@@ -175,6 +207,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
     float* sums = reinterpret_cast<float*>(down_smem);      // [PARTS][MT][R]
 #pragma unroll
     for (int m = 0; m < MS; ++m) {
+        if (TMA && tid >= THREADS) break;
         const int32_t row = (PARTS == 1 ? warp * WARP_ROWS + m * 16 : warp * MT) + lane / 4;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -185,24 +218,42 @@ __global__ void __launch_bounds__(kLoraThreads) lora_down_kernel(const __grid_co
         }
     }
     const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.0f;
+    const int32_t passes = part_passes(R), q4 = R / 4;
+    const int64_t places = a.slots.n_slots;
     cluster_sync();
-    for (int32_t i = static_cast<int32_t>(rank) * THREADS + tid; i < tile.n * R; i += static_cast<int32_t>(size) * THREADS) {
-        float v = 0.0f;
-        for (uint32_t q = 0; q < size; ++q)
+    for (int32_t i = static_cast<int32_t>(rank) * THREADS + tid; tid < THREADS && i < tile.n * q4; i += static_cast<int32_t>(size) * THREADS) {
+        const int32_t s = i / q4, r = (i - s * q4) * 4;
+        float4 x[8], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) v += cluster_load(sums + p * MT * R + i, q);
-        const int32_t s = i / R, r = i - s * R;
-        if (job.u) job.u[static_cast<int64_t>(slots[s]) * R + r] = v;
+        for (int p = 0; p < PARTS; ++p) {
+#pragma unroll
+            for (uint32_t q = 0; q < 8; ++q)      // all asked for before the first is added
+                if (q < size) x[q] = cluster_load4(sums + p * MT * R + i * 4, q);
+#pragma unroll
+            for (uint32_t q = 0; q < 8; ++q)
+                if (q < size) v = make_float4(v.x + x[q].x, v.y + x[q].y, v.z + x[q].z, v.w + x[q].w);
+        }
+        if (job.u) *reinterpret_cast<float4*>(job.u + static_cast<int64_t>(slots[s]) * R + r) = v;
         if (job.parts) {
-            v *= scale;
-            __nv_bfloat16* to = job.parts + static_cast<int64_t>(tile.first + s) * 3 * R + r;
+            uint32_t lo[3], hi[3];
+            split_pair<3>(v.x * scale, v.y * scale, lo);
+            split_pair<3>(v.z * scale, v.w * scale, hi);
+            int32_t kind = 0;      // lines of the passes before
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                *to = h;
-                v -= __bfloat162float(h);
-                to += R;
+            for (int t = 0; t < 3; ++t) {
+                if (t > 0 && part_pass(passes, t) != part_pass(passes, t - 1)) kind += part_lines(R, part_pass(passes, t - 1));
+                const int32_t m = part_row(passes, R, t) + r;
+                uint8_t* line = job.parts + ((kind + m / 64) * places + tile.first + s) * 128;
+                *reinterpret_cast<uint2*>(line + (m % 64 / 8 ^ s % 8) * 16 + m % 8 * 2) = make_uint2(lo[t], hi[t]);
             }
+        }
+    }
+    if (job.parts && passes == 2) {      // rows behind the third part's add to the second's: zeros
+        const int32_t words = 8 - R / 8;
+        for (int32_t i = static_cast<int32_t>(rank) * THREADS + tid; tid < THREADS && i < tile.n * words; i += static_cast<int32_t>(size) * THREADS) {
+            const int32_t s = i / words, word = R / 8 + i - s * words;
+            uint8_t* line = job.parts + (part_lines(R, 0) * places + tile.first + s) * 128;
+            *reinterpret_cast<uint4*>(line + (word ^ s % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
     cluster_sync();      // no CTA leaves while others read its sums
@@ -213,13 +264,14 @@ int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStr
     size_t sm = static_cast<size_t>(kDownStages) * (MT * kDownCols + down_w_elems(a.rank)) * sizeof(T);
     const size_t sums = static_cast<size_t>(MT == kLoraSmallTile ? 4 * MT : MT) * a.rank * 4;
     if (sums > sm) sm = sums;
+    sm += 1024;
     // As many CTAs as the GPU holds at once, with four stages of work or more each.  By what a call can have, not what it has:
     // leaving out one product changes no bit of the other.
     const int64_t per_sm = static_cast<int64_t>(220 * 1024 / (sm + 1024)), fit = (per_sm < 8 ? per_sm : 8) * sm_count();
     unsigned cluster = 1;
     while (cluster < 8 && p.n_tiles * p.down_jobs * 2 * cluster <= fit * 5 / 4 && p.down_cols >= static_cast<int32_t>(2 * cluster) * 4 * kDownCols)
         cluster *= 2;
-    const dim3 grid(static_cast<unsigned>(p.n_tiles * cluster), static_cast<unsigned>(jobs)), block(kLoraThreads);
+    const dim3 grid(static_cast<unsigned>(p.n_tiles * cluster), static_cast<unsigned>(jobs)), block(MT > kLoraSmallTile ? kLoraThreads + 32 : kLoraThreads);
     auto go = [&](auto k) { return launch_with(k, "lora_down_kernel", grid, block, sm, true, cluster, s, a); };
     if (a.rank <= 16) return go(lora_down_kernel<T, MT, 2>);
     if (a.rank <= 32) return go(lora_down_kernel<T, MT, 4>);
@@ -230,9 +282,25 @@ int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStr
 template <typename T>
 int launch_down(const LoraDown* jobs, int n_jobs, const LoraPlan& p, cudaStream_t s) {
     DownArgs<T> a{};
-    for (int i = 0; i < n_jobs; ++i)
-        a.job[i] = DownJob<T>{static_cast<const T*>(jobs[i].z), static_cast<const T*>(jobs[i].w), jobs[i].u, static_cast<__nv_bfloat16*>(jobs[i].parts), jobs[i].cols,
-                              jobs[i].div, jobs[i].trans};
+    const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    for (int i = 0; i < n_jobs; ++i) {
+        const LoraDown& j = jobs[i];
+        a.job[i] = DownJob<T>{static_cast<const T*>(j.z), static_cast<const T*>(j.w), j.u, static_cast<uint8_t*>(j.parts), j.cols, j.div, j.trans};
+        if (p.width == kLoraSmallTile) continue;
+        const uint64_t cols = static_cast<uint64_t>(j.cols), bytes = cols * 2, rank = static_cast<uint64_t>(p.rank), L = static_cast<uint64_t>(p.n_adapters);
+        a.tma[i] = j.div == 1 && j.cols >= kDownCols;
+        if (a.tma[i])
+            if (int st = encode_2d(&a.zmap[i], type, j.z, cols, static_cast<uint64_t>(p.n_slots), bytes, kDownCols, static_cast<uint32_t>(p.width),
+                                   CU_TENSOR_MAP_SWIZZLE_128B, "rows of an adapter"))
+                return st;
+        // (turned, a box of the last columns would hold another adapter's rows, which may be no numbers)
+        a.w_tma[i] = j.trans ? p.rank == kDownCols && j.cols % kDownCols == 0 : j.cols >= kDownCols;
+        if (a.w_tma[i])
+            if (int st = j.trans ? encode_2d(&a.wmap[i], type, j.w, rank, L * cols, rank * 2, kDownCols, kDownCols, CU_TENSOR_MAP_SWIZZLE_128B, "adapters")
+                                 : encode_2d(&a.wmap[i], type, j.w, cols, L * rank, bytes, kDownCols, static_cast<uint32_t>(p.rank),
+                                             CU_TENSOR_MAP_SWIZZLE_128B, "adapters"))
+                return st;
+    }
     a.slots = LoraSlots{p.ids, p.offsets, p.tiles, p.perm, p.n_slots, p.n_adapters, p.width};
     a.rank = p.rank;
     a.err = p.err;

@@ -2,6 +2,7 @@
 // tail of the second product (lora_up.cuh), whose results they do not read, and end behind it.
 #pragma once
 
+#include "gemm_common.cuh"
 #include "lora.cuh"
 #include "ft_internal.h"
 #include "launch.cuh"
@@ -14,7 +15,7 @@ template <typename T>
 struct GradJob {
     const T* z;
     const float* w;         // [slots][R] (fp16)
-    const T* w_parts;       // [places][3][R], scaled, in order (bf16)
+    const uint8_t* w_parts; // lines of the scaled sums' parts (bf16, lora.cuh)
     float *out, *parts;     // [adapters][size], [chunks][size]
     int32_t cols, div;      // of z; row of slot s: s / div
     bool turned;            // out is [cols][R], else [R][cols]
@@ -22,6 +23,8 @@ struct GradJob {
 
 template <typename T>
 struct GradArgs {
+    CUtensorMap zmap[2];    // boxes of 64 columns of 64 rows (bf16)
+    bool tma[2];
     GradJob<T> job[2];
     LoraSlots slots;
     const float* scales;
@@ -57,7 +60,7 @@ GradArgs<T> grad_args(const LoraGrad* jobs, const LoraPlan& p, int32_t columns, 
     *blocks = 0;
     for (int i = 0; i < 2; ++i) {
         if (!jobs[i].out) continue;
-        a.job[n++] = GradJob<T>{static_cast<const T*>(jobs[i].z), jobs[i].w, static_cast<const T*>(jobs[i].w_parts), jobs[i].out, jobs[i].parts, jobs[i].cols, jobs[i].div,
+        a.job[n++] = GradJob<T>{static_cast<const T*>(jobs[i].z), jobs[i].w, static_cast<const uint8_t*>(jobs[i].w_parts), jobs[i].out, jobs[i].parts, jobs[i].cols, jobs[i].div,
                                 jobs[i].turned};
         if (n == 1) a.blocks0 = (jobs[i].cols + columns - 1) / columns;
         *blocks += (jobs[i].cols + columns - 1) / columns;

@@ -6,9 +6,10 @@
 // is a second MMA onto the first part's rows; above, each part is an MMA of its own.
 //
 // Both operands lie as they come, a slot's neighbours side by side (M- and N-major), in lines of 128 bytes whose 16-byte
-// words are exchanged by word ^ slot % 8 (the 128-byte swizzle).  z's rows and the parts, which lora_down.cu has left in
-// order, come by cp.async, two to four stages of 64 slots; it fills whole lines at 2.3 times the rate at which it fills words
-// that lie apart.
+// words are exchanged by word ^ slot % 8 (the 128-byte swizzle), two to four stages of 64 slots.  lora_down.cu has left the
+// parts as such lines, which bulk copies bring; z's rows come by TMA where a stage's are neighbours, in four boxes of 64
+// columns, else by cp.async.  One warp does nothing but issue MMAs, which holds it for as long as they take; the others have
+// the copies made, one each, and empty the accumulators.
 //
 // The tensor cores cut what they add off at the accumulator's last bit, so that a sum of n products is too small by some
 // n 2^-25 of itself.  Every 128 slots the sums move on to the other half of the tensor memory, and the first are added to
@@ -19,12 +20,10 @@ namespace ft {
 
 namespace {
 
-constexpr int kTcThreads = 512, kTcSlots = 64, kTcCols = 256, kTcRing = 8, kTcWindow = 2;      // kTcWindow: stages of an accumulator
+constexpr int kTcThreads = 512, kTcAll = kTcThreads + 64, kTcSlots = 64, kTcCols = 256, kTcRing = 8, kTcWindow = 2;      // kTcWindow: stages of an accumulator
 constexpr uint32_t kTcGroup = 1024, kTcAtom = kTcSlots / 8 * kTcGroup;       // bytes of eight slots' lines, of 64 columns or ranks
 constexpr uint32_t kTcZStage = kTcCols / 64 * kTcAtom, kTcWPass = 128 / 64 * kTcAtom;
 
-// MMAs that a step of 16 slots takes, and rows of the accumulator that hold sums.
-__host__ __device__ inline int32_t tc_passes(int32_t rank) { return 3 * rank <= 128 ? 1 : 2 * rank <= 128 ? 2 : 3; }
 __host__ __device__ inline int32_t tc_stages(int32_t passes) { return 5 - passes; }
 __host__ __device__ inline uint32_t tc_stage_bytes(int32_t passes) { return kTcZStage + static_cast<uint32_t>(passes) * kTcWPass; }
 
@@ -34,14 +33,21 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t at) {
            static_cast<uint64_t>(kTcGroup >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-// WJ: words of a stage's parts that a thread copies.
-template <int WJ>
-__global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __grid_constant__ GradArgs<__nv_bfloat16> a) {
+// 16 fp32 columns of a warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+                   "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(kTcAll, 1) lora_grad_tc_kernel(const __grid_constant__ GradArgs<__nv_bfloat16> a) {
     using T = __nv_bfloat16;
     extern __shared__ uint8_t tc_smem_raw[];
     uint8_t* tc_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int32_t row_ring[kTcRing][kTcSlots];      // rows of z of the stages ahead
-    __shared__ __align__(8) uint64_t done[4];
+    __shared__ __align__(8) uint64_t done[4], full[4];      // full: a stage's rows by TMA, or nothing to wait for
     __shared__ uint32_t tmem_at;
     const int32_t tid = static_cast<int32_t>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const bool second = static_cast<int32_t>(blockIdx.y) >= a.blocks0;
@@ -52,31 +58,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
         wait_for_prior_grid();
         return;
     }
-    const int32_t R = a.rank, passes = tc_passes(R), stages = tc_stages(passes), used = passes == 3 ? R : (4 - passes) * R;
+    const int32_t R = a.rank, passes = part_passes(R), stages = tc_stages(passes), used = passes == 3 ? R : (4 - passes) * R;
     const uint32_t stage_bytes = tc_stage_bytes(passes);
     const int32_t* perm = a.slots.perm + ck.first;
     const int32_t steps = (ck.n + kTcSlots - 1) / kTcSlots;
 
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&done[i], 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&full[i], 1);
+        }
         fence_mbar_init();
     }
     if (warp == 0) {
         tmem_alloc(&tmem_at, 512);
         tmem_relinquish();
     }
-    // with two passes, zeros beside the third part: its MMA adds to the second part's rows, too
+    // with two passes, zeros in the third part's upper atom: its MMA adds to the second part's rows, too
     if (passes == 2) {
-        constexpr int32_t WORDS = static_cast<int32_t>(kTcWPass / 16);
-        for (int32_t i = tid; i < stages * WORDS; i += kTcThreads)
-            reinterpret_cast<uint4*>(tc_smem + static_cast<uint32_t>(i / WORDS) * stage_bytes + kTcZStage + kTcWPass)[i % WORDS] = make_uint4(0u, 0u, 0u, 0u);
+        constexpr int32_t WORDS = static_cast<int32_t>(kTcAtom / 16);
+        for (int32_t i = tid; i < stages * WORDS; i += kTcAll)
+            reinterpret_cast<uint4*>(tc_smem + static_cast<uint32_t>(i / WORDS) * stage_bytes + kTcZStage + kTcWPass + kTcAtom)[i % WORDS] = make_uint4(0u, 0u, 0u, 0u);
     }
 
     // the slots are asked for stages ahead of the rows they name
     constexpr int AHEAD = 5;
-    for (int32_t i = tid; i < AHEAD * kTcSlots && i < ck.n; i += kTcThreads) {
-        row_ring[i / kTcSlots][i % kTcSlots] = __ldg(perm + i) / job.div;
-    }
+    for (int32_t i = tid; i < AHEAD * kTcSlots && i < ck.n; i += kTcAll) row_ring[i / kTcSlots][i % kTcSlots] = __ldg(perm + i) / job.div;
     auto slot_of = [&](int32_t i) { return tid < kTcSlots && i * kTcSlots + tid < ck.n ? __ldg(perm + i * kTcSlots + tid) : 0; };
     int32_t next = slot_of(AHEAD);
     tc_fence_before();
@@ -86,37 +93,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
 
     // words of z: column block `lane` of slots warp, warp + 16, ..
     constexpr int WARPS = kTcThreads / 32, ZJ = kTcSlots / WARPS;
-    const bool in = col0 + lane * 8 < cols;
+    const bool in = col0 + lane * 8 < cols, tma = a.tma[second ? 1 : 0] && job.div == 1;
     const T* z_base = job.z + (in ? col0 + lane * 8 : 0);
     const uint32_t z_to = smem_u32(tc_smem) + static_cast<uint32_t>(lane / 8) * kTcAtom + static_cast<uint32_t>(warp) * 128 + (lane % 8 ^ warp % 8) * 16;
-    // words of the parts: a slot's three times R ranks after the other's, a run of the workspace
-    const int32_t G = R / 8;
-    const T* w_src = job.w_parts + static_cast<int64_t>(ck.first) * 3 * R + tid * 8;
-    uint32_t w_to[WJ];
-    int32_t w_slot[WJ];
-#pragma unroll
-    for (int j = 0; j < WJ; ++j) {
-        const int32_t at = tid + j * kTcThreads, s = at / (3 * G), q = at - s * 3 * G, t = q / G;
-        const int32_t pass = passes == 3 ? t : passes == 2 ? t / 2 : 0, word = passes == 3 || (passes == 2 && t == 2) ? q - t * G : q;
-        w_to[j] = smem_u32(tc_smem) + kTcZStage + static_cast<uint32_t>(pass) * kTcWPass + static_cast<uint32_t>(word / 8) * kTcAtom +
-                  static_cast<uint32_t>(s) * 128 + static_cast<uint32_t>(word % 8 ^ s % 8) * 16;
-        w_slot[j] = s < kTcSlots ? s : 1 << 30;
-    }
+    // lines of the parts: every kind's run of the workspace goes to the atom of its rows
+    const int32_t kinds = part_kinds(R), first_lines = part_lines(R, 0);
+    const uint8_t* w_src = job.w_parts + static_cast<int64_t>(ck.first) * 128;
+    auto kind_to = [&](int32_t kind) {      // bytes into a stage
+        const int32_t lines = passes == 3 ? first_lines : 1 << 30, pass = passes == 3 ? kind / lines : kind >= first_lines, atom = kind - pass * first_lines;
+        return kTcZStage + static_cast<uint32_t>(pass) * kTcWPass + static_cast<uint32_t>(atom) * kTcAtom;
+    };
+    constexpr int BOXES = kTcCols / 64;
+    const uint32_t my_kind_to = kind_to(warp >= BOXES && warp < BOXES + kinds ? warp - BOXES : 0);
     auto load = [&](int32_t i) {      // stages in turn
         const uint32_t stage = static_cast<uint32_t>(i % stages) * stage_bytes;
         const int32_t left = ck.n - i * kTcSlots;
-#pragma unroll
-        for (int j = 0; j < ZJ; ++j) {
-            const int32_t s = warp + j * WARPS;
-            const bool there = in && s < left;
-            const T* src = there ? z_base + static_cast<int64_t>(row_ring[i % kTcRing][s]) * cols : job.z;
-            copy16_at(z_to + stage + j * WARPS * 128, src, there);
+        const int32_t* rows = row_ring[i % kTcRing];
+        const bool run = tma && left >= kTcSlots && rows[kTcSlots - 1] - rows[0] == kTcSlots - 1;
+        if (lane == 0) {      // a box or a run of lines for each warp, the count for the last
+            uint64_t* bar = &full[i % stages];
+            const uint32_t bytes = static_cast<uint32_t>(min(left, kTcSlots)) * 128;
+            if (warp == kTcAll / 32 - 1) mbar_arrive_expect_tx(bar, (run ? kTcZStage : 0u) + static_cast<uint32_t>(kinds) * bytes);
+            else if (run && warp < BOXES) tma_load_2d(tc_smem + stage + static_cast<uint32_t>(warp) * kTcAtom, &a.zmap[second ? 1 : 0], col0 + warp * 64, rows[0], bar);
+            else if (warp >= BOXES && warp < BOXES + kinds)
+                bulk_g2s(tc_smem + stage + my_kind_to, w_src + (static_cast<int64_t>(warp - BOXES) * a.slots.n_slots + i * kTcSlots) * 128, bytes, bar);
         }
+        __syncwarp();
+        if (warp >= WARPS) return;
+        if (!run) {
 #pragma unroll
-        for (int j = 0; j < WJ; ++j) {
-            if (w_slot[j] < kTcSlots) copy16_at(w_to[j] + stage, w_slot[j] < left ? w_src + j * kTcThreads * 8 : job.w_parts, w_slot[j] < left);
+            for (int j = 0; j < ZJ; ++j) {
+                const int32_t s = warp + j * WARPS;
+                const bool there = in && s < left;
+                const T* src = there ? z_base + static_cast<int64_t>(rows[s]) * cols : job.z;
+                copy16_at(z_to + stage + j * WARPS * 128, src, there);
+            }
         }
-        w_src += kTcSlots * 3 * R;
+        // a last stage's lines that are no slot's: zeros, as z has there
+        for (int32_t x = left * 8 + tid; x < kTcSlots * 8; x += kTcThreads)
+            for (int32_t q = 0; q < kinds; ++q) reinterpret_cast<uint4*>(tc_smem + stage + kind_to(q))[x] = make_uint4(0u, 0u, 0u, 0u);
     };
 
     constexpr int TC = kTcCols * 128 / kTcThreads;      // sums of a thread: row 32 (warp % 4) + lane, columns TC (warp / 4) ..
@@ -125,12 +140,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
     auto drain = [&](int32_t window) {
         if (warp % 4 * 32 < used) {
 #pragma unroll
-            for (int q = 0; q < TC / 32; ++q) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(mine + static_cast<uint32_t>(window & 1) * kTcCols + q * 32, v);
+            for (int q = 0; q < TC / 16; ++q) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(mine + static_cast<uint32_t>(window & 1) * kTcCols + q * 16, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) total[q * 32 + i] += __uint_as_float(v[i]);
+                for (int i = 0; i < 16; ++i) total[q * 16 + i] += __uint_as_float(v[i]);
             }
         }
         tc_fence_before();      // the accumulator is written again after the next barrier
@@ -145,10 +160,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
         if (stages == 4) copies_wait<2>();
         else if (stages == 3) copies_wait<1>();
         else copies_wait<0>();
+        ok = mbar_wait_warp(&full[i % stages], static_cast<uint32_t>(i / stages & 1), a.err) && ok;
         fence_proxy_async_smem();
         ok = __syncthreads_and(ok);
         if (!ok) break;
-        if (tid == 0) {
+        if (tid == kTcThreads) {
             tc_fence_after();
             // bf16 operands, fp32 sums, both M- or N-major, 128 x 256
             constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (kTcCols >> 3) << 17 | (128u >> 4) << 24;
@@ -161,10 +177,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
                                i % kTcWindow || p || k);
             tc_commit(&done[i % 4]);
         }
-        if (i > 0) ok = mbar_wait_warp(&done[(i - 1) % 4], static_cast<uint32_t>((i - 1) / 4 & 1), a.err);
-        if (i + stages - 1 < steps) load(i + stages - 1);      // where the MMAs just waited for read
+        if (i > 0 && warp != WARPS) ok = mbar_wait_warp(&done[(i - 1) % 4], static_cast<uint32_t>((i - 1) / 4 & 1), a.err);
+        if (warp != WARPS && i + stages - 1 < steps) load(i + stages - 1);      // where the MMAs just waited for read
         copies_commit();
-        if (ok && i > 0 && i % kTcWindow == 0) {
+        if (ok && warp < WARPS && i > 0 && i % kTcWindow == 0) {
             tc_fence_after();
             drain(i / kTcWindow - 1);
         }
@@ -176,14 +192,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
     ok = __syncthreads_and(ok);
     if (ok) {
         tc_fence_after();
-        drain((steps - 1) / kTcWindow);
+        if (warp < WARPS) drain((steps - 1) / kTcWindow);
         const int64_t size = static_cast<int64_t>(R) * cols;
         float* out = ck.alone ? job.out + ck.adapter * size : job.parts + blockIdx.x * size;
         // the parts' rows meet in shared memory
         constexpr int PITCH = kTcCols + 1;
         float* tile = reinterpret_cast<float*>(tc_smem);
         const int32_t m = warp % 4 * 32 + lane;
-        if (m < used) {
+        if (warp < WARPS && m < used) {
 #pragma unroll
             for (int c = 0; c < TC; ++c) tile[m * PITCH + warp / 4 * TC + c] = total[c];
         }
@@ -196,10 +212,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
         };
         const int32_t width = min(kTcCols, cols - col0);
         if (job.turned) {
-            for (int32_t c = warp; c < width; c += WARPS)
+            for (int32_t c = warp; c < width; c += kTcAll / 32)
                 for (int32_t r = lane; r < R; r += 32) out[static_cast<int64_t>(col0 + c) * R + r] = sum(r, c);
         } else {
-            for (int32_t r = warp; r < R; r += WARPS)
+            for (int32_t r = warp; r < R; r += kTcAll / 32)
                 for (int32_t c = lane; c < width; c += 32) out[static_cast<int64_t>(r) * cols + col0 + c] = sum(r, c);
         }
     }
@@ -211,17 +227,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) lora_grad_tc_kernel(const __gri
 
 }  // namespace
 
+int32_t lora_part_kinds(int32_t rank) { return part_kinds(rank); }
+
 int launch_lora_grad_tc(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
     int64_t blocks;
-    const GradArgs<__nv_bfloat16> a = grad_args<__nv_bfloat16>(jobs, p, kTcCols, &blocks);
-    const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kTcThreads);
-    const int32_t passes = tc_passes(p.rank);
+    GradArgs<__nv_bfloat16> a = grad_args<__nv_bfloat16>(jobs, p, kTcCols, &blocks);
+    int n = 0;
+    for (int i = 0; i < 2; ++i) {
+        if (!jobs[i].out) continue;
+        a.tma[n] = jobs[i].div == 1 && jobs[i].cols >= 64;
+        if (a.tma[n])
+            if (int st = encode_2d(&a.zmap[n], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, jobs[i].z, static_cast<uint64_t>(jobs[i].cols),
+                                   static_cast<uint64_t>(p.n_slots), static_cast<uint64_t>(jobs[i].cols) * 2, 64, kTcSlots, CU_TENSOR_MAP_SWIZZLE_128B,
+                                   "rows of an adapter"))
+                return st;
+        ++n;
+    }
+    const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kTcAll);
+    const int32_t passes = part_passes(p.rank);
     const size_t sm = static_cast<size_t>(tc_stages(passes)) * tc_stage_bytes(passes) + 1024;
     auto go = [&](auto k) { return launch_with(k, "lora_grad_tc_kernel", grid, block, sm, p.overlap_grad, 1, s, a); };
-    if (p.rank <= 16) return go(lora_grad_tc_kernel<1>);
-    if (p.rank <= 40) return go(lora_grad_tc_kernel<2>);
-    if (p.rank <= 64) return go(lora_grad_tc_kernel<3>);
-    return go(lora_grad_tc_kernel<6>);
+    return go(lora_grad_tc_kernel);
 }
 
 }  // namespace ft

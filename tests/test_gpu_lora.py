@@ -71,6 +71,8 @@ CASES = [
     dict(T=500, k=3, L=9, R=32, K=2000, N=96, slots=True, gap=0.1), dict(T=90, k=8, L=128, R=72, K=64, N=8),
     dict(T=300, k=1, L=2, R=16, K=64, N=128, ids="none", flat=True), dict(T=2049, k=2, L=1, R=8, K=72, N=136, ids="one"),
     dict(T=1100, k=1, L=16, R=48, K=328, N=4104, flat=True), dict(T=5, k=1, L=2, R=16, K=7168, N=64, ids="none"),
+    dict(T=700, k=1, L=1, R=64, K=8, N=64, ids="one", flat=True), dict(T=1500, k=1, L=2, R=64, K=320, N=328, ids="runs", flat=True),
+    dict(T=1300, k=1, L=1, R=128, K=128, N=192, ids="one", flat=True), dict(T=1290, k=1, L=2, R=16, K=4096, N=64, ids="runs", gap=0.01),
     dict(T=271, k=1, L=1030, R=8, K=64, N=64, gap=0.1), dict(T=200, k=1, L=3, R=104, K=4096, N=200, gap=0.1),
 ]
 
@@ -148,6 +150,23 @@ def test_rows_apart(ft, T):
     gx, ga, gb = ft.lora_backward(dy, x, a, b, ids, scales=scales)
     assert torch.isfinite(ga[:2][1]).all() and torch.isfinite(gb[1]).all() and (gx[5] == 0).all()
     assert torch.isfinite(gx[ok]).all()
+
+
+def test_adapters_apart(ft):
+    """An adapter that is no number leaves its neighbours' results alone, at ranks and sizes whose last stage is not full."""
+    for R, N in ((64, 136), (64, 128), (16, 72)):
+        g, x, a, b, ids, scales = make(dict(T=900, k=1, L=3, R=R, K=136, N=N, ids="runs", flat=True), BF)
+        ids.copy_((torch.arange(900, device="cuda") // 300).to(torch.int32))
+        want = ft.lora_add(x, a, b, ids, scales=scales)
+        dy = randn(g, 900, N).to(BF)
+        grads = ft.lora_backward(dy, x, a, b, ids, scales=scales)
+        a[1], b[1], dy[300:600], x[300:600] = math.nan, math.inf, math.nan, math.inf
+        got = ft.lora_add(x, a, b, ids, scales=scales)
+        keep = ids != 1
+        assert torch.equal(got[keep], want[keep])
+        gx, ga, gb = ft.lora_backward(dy, x, a, b, ids, scales=scales)
+        assert torch.equal(gx[keep], grads[0][keep])
+        assert torch.equal(ga[::2], grads[1][::2]) and torch.equal(gb[::2], grads[2][::2])
 
 
 def test_bad_ids(ft):
