@@ -50,13 +50,12 @@ struct DownArgs {
 __host__ __device__ inline int32_t down_turned_pitch(int32_t rank) { return rank % 64 == 0 ? rank : odd_pitch(rank); }
 __host__ __device__ inline int32_t down_w_elems(int32_t rank) { return kDownCols * down_turned_pitch(rank) > rank * kDownCols ? kDownCols * down_turned_pitch(rank) : rank * kDownCols; }
 
-// NT: tiles of eight ranks that there is room for.
-template <typename T, int MT, int NT>
-__global__ void __launch_bounds__(MT > kLoraSmallTile ? kLoraThreads + 32 : kLoraThreads, MT == 128 && NT <= 8 ? 2 : 1) lora_down_kernel(const __grid_constant__ DownArgs<T> a) {
+// NT: tiles of eight ranks that there is room for.  TMA: a fifth warp has neighbouring rows brought.
+template <typename T, int MT, int NT, bool TMA>
+__global__ void __launch_bounds__(TMA ? kLoraThreads + 32 : kLoraThreads, MT == 128 && NT <= 8 ? 2 : 1) lora_down_kernel(const __grid_constant__ DownArgs<T> a) {
     constexpr int THREADS = kLoraThreads, PARTS = MT == kLoraSmallTile ? THREADS / 32 : 1;      // PARTS: warps that share a tile's sums
     constexpr int MS = MT == 128 ? 2 : 1, WARP_ROWS = 16 * MS;                                      // a warp's runs of 16 slots
     constexpr int ZS = THREADS / 8, ZR = (MT + ZS - 1) / ZS;                                        // rows that a copy of a word per thread takes
-    constexpr bool TMA = MT > kLoraSmallTile;
     extern __shared__ uint8_t down_smem_raw[];
     uint8_t* down_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(down_smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int32_t slots[MT];
@@ -157,8 +156,12 @@ __global__ void __launch_bounds__(MT > kLoraSmallTile ? kLoraThreads + 32 : kLor
         for (int32_t c = 0; c < n_chunks; ++c) {
             copies_wait<kDownStages - 2>();
             if (run || w_tma) ok = mbar_wait(&full[c % kDownStages], static_cast<uint32_t>(c / kDownStages & 1), a.err) && ok;
-            ok = __syncthreads_and(ok);
-            if (!ok) break;
+            if constexpr (TMA) {
+                ok = __syncthreads_and(ok);
+                if (!ok) break;
+            } else {
+                __syncthreads();
+            }
             if (c + kDownStages - 1 < n_chunks) load(c + kDownStages - 1);
             copies_commit();
             const T* zs = smem + c % kDownStages * stage_elems;
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(MT > kLoraSmallTile ? kLoraThreads + 32 : kLor
     cluster_sync();      // no CTA leaves while others read its sums
 }
 
-template <typename T, int MT>
+template <typename T, int MT, bool TMA>
 int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStream_t s) {
     size_t sm = static_cast<size_t>(kDownStages) * (MT * kDownCols + down_w_elems(a.rank)) * sizeof(T);
     const size_t sums = static_cast<size_t>(MT == kLoraSmallTile ? 4 * MT : MT) * a.rank * 4;
@@ -271,12 +274,12 @@ int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStr
     unsigned cluster = 1;
     while (cluster < 8 && p.n_tiles * p.down_jobs * 2 * cluster <= fit * 5 / 4 && p.down_cols >= static_cast<int32_t>(2 * cluster) * 4 * kDownCols)
         cluster *= 2;
-    const dim3 grid(static_cast<unsigned>(p.n_tiles * cluster), static_cast<unsigned>(jobs)), block(MT > kLoraSmallTile ? kLoraThreads + 32 : kLoraThreads);
+    const dim3 grid(static_cast<unsigned>(p.n_tiles * cluster), static_cast<unsigned>(jobs)), block(TMA ? kLoraThreads + 32 : kLoraThreads);
     auto go = [&](auto k) { return launch_with(k, "lora_down_kernel", grid, block, sm, true, cluster, s, a); };
-    if (a.rank <= 16) return go(lora_down_kernel<T, MT, 2>);
-    if (a.rank <= 32) return go(lora_down_kernel<T, MT, 4>);
-    if (a.rank <= 64) return go(lora_down_kernel<T, MT, 8>);
-    return go(lora_down_kernel<T, MT, 16>);
+    if (a.rank <= 16) return go(lora_down_kernel<T, MT, 2, TMA>);
+    if (a.rank <= 32) return go(lora_down_kernel<T, MT, 4, TMA>);
+    if (a.rank <= 64) return go(lora_down_kernel<T, MT, 8, TMA>);
+    return go(lora_down_kernel<T, MT, 16, TMA>);
 }
 
 template <typename T>
@@ -305,9 +308,10 @@ int launch_down(const LoraDown* jobs, int n_jobs, const LoraPlan& p, cudaStream_
     a.rank = p.rank;
     a.err = p.err;
     a.scales = p.scales;
-    if (p.width == 128) return launch_down_typed<T, 128>(a, p, n_jobs, s);
-    if (p.width == 64) return launch_down_typed<T, 64>(a, p, n_jobs, s);
-    return launch_down_typed<T, kLoraSmallTile>(a, p, n_jobs, s);
+    const bool tma = a.tma[0] || a.tma[n_jobs - 1];
+    if (p.width == 128) return tma ? launch_down_typed<T, 128, true>(a, p, n_jobs, s) : launch_down_typed<T, 128, false>(a, p, n_jobs, s);
+    if (p.width == 64) return tma ? launch_down_typed<T, 64, true>(a, p, n_jobs, s) : launch_down_typed<T, 64, false>(a, p, n_jobs, s);
+    return launch_down_typed<T, kLoraSmallTile, false>(a, p, n_jobs, s);
 }
 
 }  // namespace
