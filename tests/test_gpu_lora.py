@@ -73,6 +73,7 @@ CASES = [
     dict(T=1100, k=1, L=16, R=48, K=328, N=4104, flat=True), dict(T=5, k=1, L=2, R=16, K=7168, N=64, ids="none"),
     dict(T=700, k=1, L=1, R=64, K=8, N=64, ids="one", flat=True), dict(T=1500, k=1, L=2, R=64, K=320, N=328, ids="runs", flat=True),
     dict(T=1300, k=1, L=1, R=128, K=128, N=192, ids="one", flat=True), dict(T=1290, k=1, L=2, R=16, K=4096, N=64, ids="runs", gap=0.01),
+    dict(T=40000, k=1, L=7, R=8, K=64, N=64, gap=0.1, flat=True), dict(T=3000, k=6, L=300, R=8, K=72, N=64, gap=0.1),
     dict(T=271, k=1, L=1030, R=8, K=64, N=64, gap=0.1), dict(T=200, k=1, L=3, R=104, K=4096, N=200, gap=0.1),
 ]
 
