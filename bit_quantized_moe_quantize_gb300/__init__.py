@@ -17,6 +17,14 @@ and of expert layers whose matrices are e4m3 with a scale per block of 128:
     rows = moe_fp8_fp8(weights, w_scales, q, s, ids)   # [T, k, N]
     y = moe_combine(rows, w)                           # weighted sum of each token's rows
     y, ids, w = moe_layer_fp8(x, logits, w13, s13, w2, s2, top_k)    # the whole layer
+
+and of what adapts a layer whose matrices stay as they are, the router and low-rank adapters:
+
+    rows = lora_add(x, a, b, ids, scales=s, add=rows)              # an adapter per expert, or per request
+    loss, counts, scale = moe_balance_loss(logits, ids)            # how unevenly the experts are loaded
+    d_rows, d_w = moe_combine_backward(dy, rows, w)                # gradients of moe_combine
+    dx, da, db = lora_backward(d_rows, x, a, b, ids, scales=s)     # of lora_add
+    d_logits = moe_gate_backward(logits, ids, d_w, counts=counts, seq_scale=scale, grad_loss=g)   # of router and loss
 """
 
 from ._lib import (ACT_GELU_TANH, ACT_SILU, FT_DEVERR_BAD_EXPERT_ID, FT_DEVERR_WAIT_TIMEOUT,

@@ -25,8 +25,12 @@ int check_router(int64_t tokens, int32_t n_experts, int32_t top_k, int32_t dtype
 }
 
 // ------------------------------------------------------- low-rank adapters
-constexpr int32_t kLoraSmallMean = 16;        // slots per adapter on average that go by tiles of 16
-constexpr int64_t kLoraWideMean = 512;        // from how many on by tiles of 128
+// Slots per adapter on average that go by tiles of 16 slots, and from how many on by tiles of 128; else of 64.  From a
+// graph, 128 adapters of rank 8 with 8, 16, 32 slots each: 30, 30, 38 us by 16, 32, 34, 36 by 64; gradients of 64 of rank
+// 64 with 16, 32 each: 161, 181 against 167, 173.  Gradients, rank 64, 256, 512, 8192 slots each: 202, 181, 149 us by 64,
+// 218, 178, 138 by 128; rank 16 forward has the same times by either.  Above rank 64 the registers hold no 128 slots.
+constexpr int32_t kLoraSmallMean = 16;
+constexpr int64_t kLoraWideMean = 512;
 
 struct LoraShape {
     int64_t tokens, n_slots, ncols, nrows;

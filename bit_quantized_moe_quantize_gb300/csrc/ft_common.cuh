@@ -21,6 +21,8 @@ constexpr int Q8_1_BYTES = 36;    // fp16 d + fp16 s + 32 int8
 // Upper bound of any wait on an mbarrier: 2 s of %globaltimer, orders of
 // magnitude above any legitimate wait in these kernels.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// Limit of the waits that a role makes for its own copies before it ends, once a wait has run out.
+constexpr uint64_t kLastWaitNs = 100'000'000;
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;

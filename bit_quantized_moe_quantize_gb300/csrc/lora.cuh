@@ -14,8 +14,7 @@ namespace ft {
 constexpr int kLoraSmallTile = 16;      // slots of a tile: 16, 64 or 128
 constexpr int kLoraThreads = 128;
 
-// Slots by adapter: in order (perm, by fp8_route.cu, whose tiles have the kernel's width), or
-// perm == nullptr: found by each CTA.
+// Slots by adapter: in order (perm, by lora_order.cu), or perm == nullptr: found by each CTA (lora_few.cuh).
 struct LoraSlots {
     const int32_t *ids, *offsets, *tiles, *perm;
     int32_t n_slots, n_adapters, width;      // width: of the order's tiles

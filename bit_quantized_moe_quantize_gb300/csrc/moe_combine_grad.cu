@@ -5,8 +5,9 @@
 //
 // A row whose weight is 0 took no part: it is not read, and both its gradients are 0.
 //
-// Memory-bound: the rows are read once and as much is written.  A slot is one to eight warps', as many as leave
-// work for all of the GPU where slots are few; dy comes from the caches for all of a token's slots but the first.
+// Memory-bound: the rows are read once and as much is written (8191 x 8 rows of 2816 bf16: 118.5 us, 785 MB at 6.6 TB/s;
+// 8 x 8 of 2048: 4.3 us).  A slot is one to eight warps', as many as leave work for all of the GPU where slots are few;
+// dy comes from the caches for all of a token's slots but the first.
 // Where rows do not start at 16-byte words, the words inside of a row are read and written whole all the same, dy beside
 // them and the elements around them one by one (combine_grad_ragged_kernel).
 #include "fp8_common.cuh"

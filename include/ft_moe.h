@@ -719,8 +719,10 @@ FT_API int ft_moe_layer_fp8(const void* x, int32_t x_dtype, const void* logits, 
  *
  * What is trained and served beside expert matrices that stay as they are: the router, with the
  * load-balance loss (ft_moe_balance_loss) and the gradients of the router (ft_moe_gate_backward) and of
- * the weighted sum (ft_moe_combine_backward), and low-rank adapters (ft_lora_add, ft_lora_backward).  Conventions and errors are those of the FP8 expert-layer operators
- * above.  No sum depends on the order in which the GPU works: a call repeated gives the same bits. */
+ * the weighted sum (ft_moe_combine_backward), and low-rank adapters (ft_lora_add, ft_lora_backward).
+ * Conventions and errors are those of the FP8 expert-layer operators above.  Outputs do not overlap inputs
+ * but where that is said.  No sum depends on the order in which the GPU works: a call repeated gives the
+ * same bits. */
 
 /*
  * ft_moe_balance_loss - how unevenly a router loads its experts, over packed sequences, and the
@@ -785,7 +787,8 @@ FT_API int ft_moe_combine_backward(const void* grad_y, int32_t y_dtype, const vo
  * takes the adapter e = ids[s], a matrix A of rank rows and a matrix B of rank columns:
  *   out[s] = add[s] + scales[e] * B[e] (A[e] x)        x: row t, or row s with x_per_slot
  * and out[s] = add[s] for ids[s] = -1.  Products are summed in fp32; A x keeps its 24 bits where out is
- * fp32, and 16 where out's own rounding is larger; out is rounded once.
+ * fp32, and 16 where out's own rounding is larger; out is rounded once.  Sums that reach an infinity, or
+ * take one in, come out infinite or NaN; they stay in their slot's row.
  *
  *   x       device, [tokens][ncols], or [tokens * top_k][ncols], of dtype (FT_DTYPE_F16 or FT_DTYPE_BF16)
  *   a       device, [n_adapters][rank][ncols] of dtype; b  [n_adapters][nrows][rank] of dtype.  Adapters of a
@@ -813,7 +816,8 @@ FT_API int ft_lora_add(const void* x, int32_t dtype, const void* a, const void* 
  *   grad_x    = add + A[e]^T v[s], summed over the slots that share a row of x, rounded once to dtype
  *   grad_a[e] = sum over the slots of e of v[s] x^T           fp32 [n_adapters][rank][ncols]
  *   grad_b[e] = sum over the slots of e of grad_out[s] u[s]^T      fp32 [n_adapters][nrows][rank]
- * 0 for adapters without a slot.  Sums run in a fixed order.
+ * 0 for adapters without a slot.  Sums run in a fixed order.  What is not finite makes its adapter's sums
+ * infinite or NaN, and no other's.
  *
  *   grad_out  device, [tokens][top_k][nrows] of dtype; x, a, b, scales, ids as ft_lora_add had them
  *   add       device, of x's shape and dtype, or NULL: 0; may be grad_x

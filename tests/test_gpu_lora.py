@@ -256,6 +256,35 @@ def test_two_streams_at_once(ft):
     assert all(torch.equal(p, jobs[i][5]) for i in range(2) for p in got[i])
 
 
+@pytest.mark.parametrize("R", [16, 72])
+def test_gradients_on_two_streams_at_once(ft, R):
+    """Both calls' kernels want tensor memory and most of an SM's shared memory."""
+    jobs = []
+    for seed in range(2):
+        g, x, a, b, ids, scales = make(dict(T=1600 + seed, k=2, L=3, R=R, K=512, N=768, gap=0.1), BF)
+        args = (randn(g, *ids.shape, 768).to(BF), x, a, b, ids, scales)
+        jobs.append((args, ft.lora_backward(*args)))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in jobs], [[], []]
+    for _ in range(6):
+        for i, (st, (args, _)) in enumerate(zip(streams, jobs)):
+            with torch.cuda.stream(st):
+                got[i].append(ft.lora_backward(*args))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for i in range(2) for part in got[i] for p, q in zip(part, jobs[i][1]))
+
+
+def test_nothing_between_two_calls(ft):
+    """Calls one behind the other, the first without a tile of its own, the second in the same memory."""
+    g, x, a, b, ids, scales = make(dict(T=3000, k=1, L=5, R=32, K=512, N=512, flat=True), BF)
+    none = torch.full_like(ids, -1)
+    want = ft.lora_add(x, a, b, ids, scales=scales)
+    for _ in range(20):
+        got = ft.lora_add(x, a, b, none, scales=scales)
+        more = ft.lora_add(x, a, b, ids, scales=scales)
+        assert not got.any() and torch.equal(more, want)
+
+
 def test_gradients_against_differences(ft):
     g, x, a, b, ids, scales = make(dict(T=90, k=3, L=4, R=8, K=64, N=48, gap=0.1), BF)
     dy = randn(g, 90, 3, 48).to(BF)

@@ -139,6 +139,21 @@ def test_gate_backward(ft, c, score, renorm, dtype):
             inside(got, want, bound, f"{'weights ' if w is not None else ''}{'loss' if b else ''}")
 
 
+@pytest.mark.parametrize("E,k", [(24, 3), (64, 12), (128, 8), (200, 4), (512, 40), (600, 6)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_backward_rows_in_turn(ft, E, k, score):
+    """More rows than the lanes have room for at once, the last ones a set that is not full; ids that repeat and leave in between."""
+    T = {24: 60_001, 64: 60_001, 128: 60_001, 200: 29_999, 512: 9_001, 600: 2_003}[E]
+    g, x, ids = router(E, T, E, k, torch.bfloat16, 0.1, 8)
+    ids[::7, 1] = ids[::7, 0]
+    ids[5::11, 2] = -1
+    gw = torch.randn(T, k, generator=g, device="cuda")
+    got = ft.moe_gate_backward(x, ids, gw, score=score)
+    want, bound = A.gate_grad(x, ids, gw, score, True, 1.0, None)
+    inside(got, want, bound)
+    assert torch.equal(got, ft.moe_gate_backward(x, ids, gw, score=score))
+
+
 def test_gate_backward_repeats(ft):
     """One expert in all of a row's 40 slots: added in the slots' order, the same bits every time."""
     g, x, _ = router(2, 33, 64, 40, torch.float32)
