@@ -14,9 +14,10 @@
 // the rows, so that no two meet.  Batches of some rows and few sequences are one cluster's work, in one launch:
 // its CTAs add up each other's shares through shared memory.
 //
-// 65536 rows of 128 fp32 in packed sequences: 15 us for the rows (34 MB, 2.2 TB/s: exponentials and sums, as much as the
-// reads), 9 to join.  512 rows of 128 by one cluster: 10.5 us, a chain of loads, sums and meetings; by two launches
-// that and the join's 9.
+// 65536 rows of 128 fp32 in packed sequences: 12.9 us for the rows (34 MB, 2.6 TB/s: exponentials and sums, as much as the
+// reads), 8.6 to join.  512 rows of 128 by one cluster: 8.8 us, a chain of loads, sums and meetings; by two launches
+// that and the join's 8.  Four CTAs of an SM, one row of a lane group at work and one on its way: with two of each, three
+// CTAs, 18 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -31,7 +32,7 @@ namespace {
 constexpr int32_t kSingleRounds = 8, kSingleSeqs = 8;      // batches that one cluster works out: rounds of rows of a CTA, sequences
 constexpr unsigned kSingleCtas = 8;
 constexpr int32_t kLeastRounds = 2;                         // rounds of rows that a CTA takes at least
-constexpr int kAtOnce = 2;                                  // rows of a lane group under way together
+constexpr int kEarlyIds = 4;                                // ids of a thread asked for before the rows
 
 struct Piece {
     float p;
@@ -87,7 +88,7 @@ __device__ __forceinline__ int32_t seq_of_cta(const int32_t* offsets, int32_t n,
 }
 
 template <typename T, int L, int STEPS>
-__global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kRowThreads, STEPS == 1 ? 4 : 2) balance_rows_kernel(const BalanceArgs a) {
     using G = RowGroup<L>;
     constexpr int WIDTH = 8 * L * STEPS;      // experts that the lanes have room for
     extern __shared__ __align__(16) uint8_t balance_smem[];
@@ -119,39 +120,48 @@ __global__ void __launch_bounds__(kRowThreads) balance_rows_kernel(const Balance
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
         int32_t rows = 0;
-        for (int64_t base = lo; base < hi; base += kAtOnce * G::kRows) {      // whole groups: their lanes meet in shuffles
-            float p[kAtOnce][STEPS][8];
+        // the first ids, and the next row: on their way while a row is worked on
+        const int64_t id_end = hi * a.top_k;
+        int64_t id_at = lo * a.top_k + tid;
+        int32_t early[kEarlyIds];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int64_t t = base + u * G::kRows + G::row();
-                load_logits<T, L, STEPS>(static_cast<const T*>(a.logits) + (t < hi ? t : lo) * a.stride, E, a.wide, p[u]);
+        for (int i = 0; i < kEarlyIds; ++i) early[i] = id_at + i * kRowThreads < id_end ? __ldg(a.ids + id_at + i * kRowThreads) : -1;
+        RowAhead<T, L, STEPS> ahead;
+        auto row_of = [&](int64_t base) {
+            const int64_t t = base + G::row();
+            return static_cast<const T*>(a.logits) + (t < hi ? t : lo) * a.stride;
+        };
+        if (lo < hi) ahead.fetch(row_of(lo), E, a.wide);
+        for (int64_t base = lo; base < hi; base += G::kRows) {      // whole groups: their lanes meet in shuffles
+            float p[STEPS][8];
+            ahead.take(row_of(base), E, a.wide, p);
+            if (base + G::kRows < hi) ahead.fetch(row_of(base + G::kRows), E, a.wide);
+            RowScale sc;
+            float inv;
+            if (a.score == FT_SCORE_SOFTMAX) {
+                sc = row_softmax<L, STEPS>(g, p);
+                inv = sc.inv;
+            } else {
+                float rest[STEPS][8];
+                sc = row_sigmoid<L, STEPS>(g, p, rest);
+                inv = __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
             }
+            if (base + G::row() < hi) {
+                rows += sc.any ? 1 : 0;
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                RowScale sc;
-                float inv;
-                if (a.score == FT_SCORE_SOFTMAX) {
-                    sc = row_softmax<L, STEPS>(g, p[u]);
-                    inv = sc.inv;
-                } else {
-                    float rest[STEPS][8];
-                    sc = row_sigmoid<L, STEPS>(g, p[u], rest);
-                    inv = __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
-                }
-                if (base + u * G::kRows + G::row() < hi) {
-                    rows += sc.any ? 1 : 0;
+                for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-                    for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(p[u][i][j], inv, acc[i][j]);
-                }
+                    for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(p[i][j], inv, acc[i][j]);
             }
         }
-        for (int64_t i = lo * a.top_k + tid; i < hi * a.top_k; i += kRowThreads) {
-            const int32_t e = __ldg(a.ids + i);
+        auto count = [&](int32_t e) {
             if (e >= 0 && e < E) atomicAdd(&hist[e], 1);      // whole numbers: the order does not show
             else if (e != -1) atomicOr(a.err, FT_DEVERR_BAD_EXPERT_ID);
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < kEarlyIds; ++i) count(early[i]);
+#pragma unroll 4
+        for (id_at += kEarlyIds * kRowThreads; id_at < id_end; id_at += kRowThreads) count(__ldg(a.ids + id_at));
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             float4* to = reinterpret_cast<float4*>(red + G::row() * WIDTH + first_expert<L>(i));
@@ -245,14 +255,16 @@ __global__ void __launch_bounds__(kRowThreads) balance_join_kernel(const Balance
     const int64_t task = static_cast<int64_t>(blockIdx.x) * (kRowThreads / TASK) + threadIdx.x / TASK;
     const int32_t sub = threadIdx.x % TASK;
     const bool there = task < tasks;
-    const int32_t s = there ? static_cast<int32_t>(task / blocks) : 0, b = there ? static_cast<int32_t>(task % blocks) : 0;
+    const int32_t s = !there ? 0 : tasks <= INT32_MAX ? static_cast<int32_t>(task) / blocks : static_cast<int32_t>(task / blocks);
+    const int32_t b = there ? static_cast<int32_t>(task - static_cast<int64_t>(s) * blocks) : 0;
     const int32_t e = b * 8 + sub % 8;
     float p = 0.0f;
     int32_t c = 0, n = 0;
     if (there) {
         const int64_t lo = seq_start(a.offsets, s, a.tokens), hi = seq_start(a.offsets, s + 1, a.tokens);
         if (lo < hi) {
-            const int64_t first = lo / a.rows_per_cta, last_cta = (hi - 1) / a.rows_per_cta;
+            const uint32_t per = static_cast<uint32_t>(a.rows_per_cta);      // tokens < 2^31
+            const int64_t first = static_cast<uint32_t>(lo) / per, last_cta = static_cast<uint32_t>(hi - 1) / per;
 #pragma unroll 8
             for (int64_t i = first + sub / 8; i <= last_cta; i += TASK / 8) {
                 if (e < E) {
@@ -305,12 +317,19 @@ __global__ void __launch_bounds__(kRowThreads) balance_join_kernel(const Balance
     float full = 0.0f, loss = 0.0f;
     for (int32_t i = threadIdx.x; i < a.n_seqs; i += kRowThreads) full += __ldcg(a.seq_rows + i) > 0 ? 1.0f : 0.0f;
     const int32_t sequences = static_cast<int32_t>(cta_sum(full, part_sum));
+    int32_t seq = static_cast<int32_t>(threadIdx.x) / blocks, rest = static_cast<int32_t>(threadIdx.x) % blocks;
+    const int32_t seqs = kRowThreads / blocks, more = kRowThreads % blocks;
 #pragma unroll 4
     for (int64_t i = threadIdx.x; i < tasks; i += kRowThreads) {
-        const int32_t seq = static_cast<int32_t>(i / blocks);
         const float scale = seq_scale_of(a, __ldcg(a.seq_rows + seq), sequences);
-        if (i % blocks == 0) a.seq_scale[seq] = scale;
+        if (rest == 0) a.seq_scale[seq] = scale;
         loss = fmaf(scale, __ldcg(a.dots + i), loss);
+        seq += seqs;
+        rest += more;
+        if (rest >= blocks) {
+            rest -= blocks;
+            ++seq;
+        }
     }
     loss = cta_sum(loss, part_sum);
     if (threadIdx.x == 0) *a.loss = loss;

@@ -22,8 +22,9 @@ namespace ft {
 
 namespace {
 
-// CTAs per SM, which take their rows in turn: two or three are resident by their registers, so that six end together
-// (65536 x 128 from a graph: 19.6 us; with four, or a CTA for each set of rows, 21.7).
+// CTAs per SM, which take their rows in turn: three are resident (held to 80 registers: 65536 x 128 fp32 24 us from a graph,
+// 26 with two), so that six end together (bf16: 19.6 us; with four, or a CTA for each set of rows, 21.7; a run of
+// neighbouring rows for each, which would keep their sequence, 21.6).
 constexpr int kGateGradCtas = 6;
 
 struct GateGradArgs {
@@ -44,7 +45,7 @@ struct GateGradArgs {
 
 // ONE: no more slots than lanes that share them, so that each has one.
 template <typename T, int L, int STEPS, bool ONE, bool SOFT>
-__global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 3) gate_grad_kernel(const GateGradArgs a) {
     using G = RowGroup<L>;
     constexpr int WIDTH = 8 * L * STEPS, LANES = L < 32 ? L : 32;      // LANES: lanes that share the slots
     __shared__ __align__(16) float extra_all[G::kRows * WIDTH];
@@ -60,20 +61,12 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
         float l, gw;      // its logit, the weight's gradient
     };
     // A run of rows after another: the next one's logits and slots are on their way while this one's are worked on.
-    constexpr int WORDS = static_cast<int>(sizeof(T)) * 8 / 16;
-    uint4 ahead[STEPS][WORDS];
+    RowAhead<T, L, STEPS> ahead;
     int32_t ahead_e = -1;
     float ahead_gw = 0.0f;
     auto fetch = [&](int64_t first) {
         const int64_t t = first + G::row();
-        const T* row = static_cast<const T*>(a.logits) + (t < a.tokens ? t : a.tokens - 1) * a.stride;
-        if (a.wide) {
-#pragma unroll
-            for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-                for (int w = 0; w < WORDS; ++w)
-                    if (first_expert<L>(i) + 8 <= E) ahead[i][w] = __ldg(reinterpret_cast<const uint4*>(row + first_expert<L>(i)) + w);
-        }
+        ahead.fetch(static_cast<const T*>(a.logits) + (t < a.tokens ? t : a.tokens - 1) * a.stride, E, a.wide);
         if (ONE && a.grad_weights) {
             const bool in = mine && t < a.tokens && lane < k;
             ahead_e = in ? __ldg(a.ids + t * k + lane) : -1;
@@ -105,18 +98,7 @@ __global__ void __launch_bounds__(kRowThreads) gate_grad_kernel(const GateGradAr
         Slot x{-1, 0.0f, 0.0f};
         if (ONE) x = slot_at(ahead_e, ahead_gw);
         float p[STEPS][8], rest[SOFT ? 1 : STEPS][8];              // rest: 1 - score
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int32_t e0 = first_expert<L>(i);
-            const T* l = reinterpret_cast<const T*>(ahead[i]);
-            if (a.wide && e0 + 8 <= E) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[i][j] = fmaxf(to_f32<T>(l[j]), -INFINITY);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[i][j] = e0 + j < E ? fmaxf(to_f32<T>(row[e0 + j]), -INFINITY) : -INFINITY;
-            }
-        }
+        ahead.take(row, E, a.wide, p);
         if (first + static_cast<int64_t>(gridDim.x) * G::kRows < a.tokens) fetch(first + static_cast<int64_t>(gridDim.x) * G::kRows);
         RowScale sc;
         if constexpr (SOFT) sc = row_softmax<L, STEPS>(g, p);

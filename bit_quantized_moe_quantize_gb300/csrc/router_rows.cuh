@@ -50,23 +50,36 @@ __device__ __forceinline__ int32_t first_expert(int step) {
     return (step * L + static_cast<int32_t>(RowGroup<L>::lane())) * 8;
 }
 
-// A lane's logits of a row; masked experts (-inf, NaN) and those past the last are -inf.
+// A lane's logits of a row on their way: words as they come, made logits when they are wanted.
 // wide: rows start at whole 16-byte words.
 template <typename T, int L, int STEPS>
-__device__ __forceinline__ void load_logits(const T* row, int32_t E, bool wide, float (&l)[STEPS][8]) {
+struct RowAhead {
+    static constexpr int WORDS = static_cast<int>(sizeof(T)) * 8 / 16;
+    uint4 word[STEPS][WORDS];
+    __device__ __forceinline__ void fetch(const T* row, int32_t E, bool wide) {
+        if (!wide) return;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        const int32_t e0 = first_expert<L>(s);
-        if (wide && e0 + 8 <= E) {
-            load_vec<T, 8>(row + e0, l[s]);
-        } else {
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) l[s][i] = e0 + i < E ? to_f32<T>(row[e0 + i]) : -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) l[s][i] = fmaxf(l[s][i], -INFINITY);      // the operand that is no NaN
+            for (int w = 0; w < WORDS; ++w)
+                if (first_expert<L>(s) + 8 <= E) word[s][w] = __ldg(reinterpret_cast<const uint4*>(row + first_expert<L>(s)) + w);
     }
-}
+    // Masked experts (-inf, NaN) and those past the last are -inf.
+    __device__ __forceinline__ void take(const T* row, int32_t E, bool wide, float (&l)[STEPS][8]) const {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int32_t e0 = first_expert<L>(s);
+            const T* v = reinterpret_cast<const T*>(word[s]);
+            if (wide && e0 + 8 <= E) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) l[s][i] = fmaxf(to_f32<T>(v[i]), -INFINITY);      // the operand that is no NaN
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) l[s][i] = e0 + i < E ? fmaxf(to_f32<T>(row[e0 + i]), -INFINITY) : -INFINITY;
+            }
+        }
+    }
+};
 
 // e^x for x <= 0, off by (1.5 |x| + 4) 2^-24 of itself: the argument times log2(e) rounded, log2(e) itself, two units
 // in the power; below 2^-126 it is 0.
