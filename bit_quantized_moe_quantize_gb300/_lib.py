@@ -416,17 +416,17 @@ F32, F16, BF16 = 0, 1, 2
 _DTYPES: dict = {}       # torch dtype -> FT_DTYPE_*
 _CODES: tuple = ()       # torch dtypes that hold e4m3 codes
 _i32 = _f32 = _e4m3 = None
-_Tensor = _empty = _raw_stream = None
+_Tensor = _empty_strided = _raw_stream = None
 
 
 def _ready():
     """The library, with the torch names that the checks use."""
-    global _CODES, _i32, _f32, _e4m3, _Tensor, _empty, _raw_stream, _current_device
+    global _CODES, _i32, _f32, _e4m3, _Tensor, _empty_strided, _raw_stream, _current_device
     torch = _torch()
     if not _CODES:
         _DTYPES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         _i32, _f32, _e4m3 = torch.int32, torch.float32, torch.float8_e4m3fn
-        _Tensor, _empty = torch.Tensor, torch.empty
+        _Tensor, _empty_strided = torch.Tensor, torch.empty_strided
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _current_device = getattr(torch._C, "_cuda_getDevice", _current_device)      # without a check for a first use
@@ -487,10 +487,17 @@ def _typed_ptr(t, name, dtype, shape, dev):
     return p
 
 
+def _empty(shape, dtype, device):
+    """A new contiguous tensor of up to three dims; with its strides given torch makes it sooner (1.4 us of a call's 15)."""
+    n = len(shape)
+    stride = (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1) if n == 3 else (1,) * n
+    return _empty_strided(shape, stride, dtype=dtype, device=device)
+
+
 def _out(out, name, shape, dtype, like, dev):
     """`out` checked, or a new tensor beside `like`."""
     if out is None:
-        return _empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype, like.device)
     _ptr(out, name, len(shape), dev)
     if out.dtype != dtype or out.shape != shape:
         raise ValueError(f"{name} must be {dtype} {shape}, got {out.dtype} {tuple(out.shape)}")
@@ -501,7 +508,7 @@ def _workspace(n, like):
     """(tensor, pointer) of n bytes; the caching allocator hands them out in stream order."""
     if not n:
         return None, None
-    t = _empty(n, dtype=_CODES[1], device=like.device)
+    t = _empty((n,), _CODES[1], like.device)
     return t, t.data_ptr()
 
 
@@ -692,8 +699,8 @@ def moe_layer_fp8(x, logits, w13, s13, w2, s2, top_k, act_kind=0, score="softmax
     pb = None if bias is None else _typed_ptr(bias, "bias", _f32, (E,), dev)
     out = _out(out, "out", (T, H), x.dtype, x, dev)
     device, shape = x.device, (T, max(int(top_k), 0))
-    ids = _empty(shape, dtype=_i32, device=device)
-    weights = _empty(shape, dtype=_f32, device=device)
+    ids = _empty(shape, _i32, device)
+    weights = _empty(shape, _f32, device)
     n = L.ft_moe_layer_fp8_workspace_bytes(T, top_k, E, H, I)
     ws, pws = _workspace(n, x)
     st = L.ft_moe_layer_fp8(px, xcode, logits.data_ptr(), lcode, stride, pb, pw13, ps13, pw2, ps2, out.data_ptr(),
@@ -740,9 +747,9 @@ def moe_balance_loss(logits, topk_ids, score="softmax", seq_offsets=None):
     pi, k = _ids_of(topk_ids, T, dev)
     po, S = _offsets_of(seq_offsets, dev)
     device = logits.device
-    loss = _empty((), dtype=_f32, device=device)
-    counts = _empty((S, E), dtype=_i32, device=device)
-    seq_scale = _empty((S,), dtype=_f32, device=device)
+    loss = _empty((), _f32, device)
+    counts = _empty((S, E), _i32, device)
+    seq_scale = _empty((S,), _f32, device)
     n = L.ft_moe_balance_workspace_bytes(T, E, S)
     ws, pws = _workspace(n, logits)
     st = L.ft_moe_balance_loss(logits.data_ptr(), code, stride, pi, po, loss.data_ptr(), counts.data_ptr(),
