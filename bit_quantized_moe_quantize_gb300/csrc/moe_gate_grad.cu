@@ -147,8 +147,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) gate_grad_kernel(const GateGra
                     x = slot(j0 + lane);
                     score_of(x, s, r);
                 }
-                const float h = c * (x.gw - mean), d = s * r * h;
-                if (x.e >= 0) dots = fmaf(h, s, dots);
+                // the score meets the divisor before the gradient: c alone may be 1e30, and 0 times what that makes of a
+                // large gradient would be no number
+                const float q = c * s * (x.gw - mean), d = r * q;
+                if (x.e >= 0) dots += q;
                 if (mine) {
                     // every lane marks its expert; where all marks stay, no id repeats
                     int32_t* mark = reinterpret_cast<int32_t*>(extra);
@@ -191,8 +193,9 @@ __global__ void __launch_bounds__(kRowThreads, 3) gate_grad_kernel(const GateGra
                 seq = seq_of(a.offsets, a.n_seqs, t);
                 inside = seq_start(a.offsets, seq, a.tokens) <= t && t < seq_start(a.offsets, seq + 1, a.tokens);
             }
-            const float inv = SOFT ? sc.inv : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
-            coef = inside ? __ldg(a.grad_loss) * __ldg(a.seq_scale + seq) * inv : 0.0f;
+            // a row of padding has no part, whatever arrives
+            coef = inside && sc.any ? __ldg(a.grad_loss) * __ldg(a.seq_scale + seq) : 0.0f;
+            if constexpr (SOFT) coef *= sc.inv;
             count = a.counts + static_cast<int64_t>(seq) * E;
         }
         float c[STEPS][8] = {};
@@ -216,6 +219,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) gate_grad_kernel(const GateGra
             mean = SOFT ? mean * sc.inv : sc.sum > kScoreTiny ? __fdividef(mean, sc.sum) : 0.0f;
         }
         if (!there) continue;      // (the last run)
+        // sigmoid: scores become p before they meet the loss' gradient, which 1e30 would put out of range
+        const float inv = SOFT || !count ? 1.0f : __fdividef(1.0f, fmaxf(sc.sum, kScoreTiny));
         // with softmax, p holds exponentials: what multiplies them carries the reciprocal of their sum
         if (SOFT) dots *= sc.inv;
         T* out = static_cast<T*>(a.out) + t * E;
@@ -232,10 +237,14 @@ __global__ void __launch_bounds__(kRowThreads, 3) gate_grad_kernel(const GateGra
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float v;
-                if constexpr (SOFT) v = fmaf(coef, c[i][j] - mean, -dots);
-                else v = coef * (c[i][j] - mean) * rest[i][j];
-                o[j] = from_f32<T>(fmaf(p[i][j], v, x[j]));
+                float v, of = p[i][j];
+                if constexpr (SOFT) {
+                    v = fmaf(coef, c[i][j] - mean, -dots);
+                } else {
+                    v = coef * (c[i][j] - mean);
+                    of *= inv * rest[i][j];
+                }
+                o[j] = from_f32<T>(fmaf(of, v, x[j]));
             }
             if (a.wide_out && e0 + 8 <= E) {
 #pragma unroll
