@@ -120,11 +120,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return r;
 }
 
-// The first TERMS bf16 parts of a pair of fp32 values: 8, 16 or 24 significant bits.
-template <int TERMS>
-__device__ __forceinline__ void split_pair(float lo, float hi, uint32_t (&part)[TERMS]) {
+// A pair of fp32 values as the sums of three bf16 parts, which hold their 24 bits.
+__device__ __forceinline__ void split_pair(float lo, float hi, uint32_t (&part)[3]) {
 #pragma unroll
-    for (int t = 0; t < TERMS; ++t) {
+    for (int t = 0; t < 3; ++t) {
         part[t] = bf16_pair(lo, hi);
         lo -= __uint_as_float(part[t] << 16);
         hi -= __uint_as_float(part[t] & 0xFFFF0000u);
@@ -132,34 +131,35 @@ __device__ __forceinline__ void split_pair(float lo, float hi, uint32_t (&part)[
 }
 
 // A 16 x 16 operand of fp32 values, to be multiplied with 16-bit ones: v[2 i], v[2 i + 1] are neighbours in the
-// place that mma's 16-bit operand register i has.  With bf16 as sums of TERMS bf16 parts; with fp16, whose values
-// and products have no such range, as two tf32 parts of 11 bits against fp16 turned to tf32, which is exact.
-template <typename T, int TERMS>
+// place that mma's 16-bit operand register i has.  With bf16 as sums of three bf16 parts; with fp16, whose values
+// and products have no such range, as two tf32 parts of 11 bits against fp16 turned to tf32, which is exact.  Fewer parts would
+// not do where results have 16 bits either: products of ranks that cancel each other leave what the parts dropped.
+template <typename T>
 struct Wide16;
 
-template <int TERMS>
-struct Wide16<__nv_bfloat16, TERMS> {
-    uint32_t part[TERMS][4];
+template <>
+struct Wide16<__nv_bfloat16> {
+    uint32_t part[3][4];
     __device__ __forceinline__ void set(const float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t p[TERMS];
-            split_pair<TERMS>(v[2 * i], v[2 * i + 1], p);
+            uint32_t p[3];
+            split_pair(v[2 * i], v[2 * i + 1], p);
 #pragma unroll
-            for (int t = 0; t < TERMS; ++t) part[t][i] = p[t];
+            for (int t = 0; t < 3; ++t) part[t][i] = p[t];
         }
     }
     template <int N>
     __device__ __forceinline__ void mul(float (&d)[N][4], const uint32_t (&b)[N][2]) const {
 #pragma unroll
-        for (int t = TERMS - 1; t >= 0; --t)
+        for (int t = 2; t >= 0; --t)
 #pragma unroll
             for (int j = 0; j < N; ++j) mma16(d[j], part[t], b[j][0], b[j][1], __nv_bfloat16());
     }
 };
 
-template <int TERMS>
-struct Wide16<__half, TERMS> {
+template <>
+struct Wide16<__half> {
     float v[8];
     __device__ __forceinline__ void set(const float (&x)[8]) {
 #pragma unroll

@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(TMA ? kLoraThreads + 32 : kLoraThreads, MT == 
         if (job.u) *reinterpret_cast<float4*>(job.u + static_cast<int64_t>(slots[s]) * R + r) = v;
         if (job.parts) {
             uint32_t lo[3], hi[3];
-            split_pair<3>(v.x * scale, v.y * scale, lo);
-            split_pair<3>(v.z * scale, v.w * scale, hi);
+            split_pair(v.x * scale, v.y * scale, lo);
+            split_pair(v.z * scale, v.w * scale, hi);
             int32_t kind = 0;      // lines of the passes before
 #pragma unroll
             for (int t = 0; t < 3; ++t) {

@@ -33,7 +33,7 @@ template <typename T, typename YT, int NT>
 __global__ void __launch_bounds__(kLoraThreads) lora_few_kernel(const __grid_constant__ FewArgs<T> a) {
     constexpr int THREADS = kLoraThreads, WARPS = THREADS / 32, KS = NT / 2, UPS = few_up_stages(NT);
     constexpr bool FP32 = sizeof(YT) == 4;
-    constexpr int TERMS = FP32 ? 3 : 2, WORDS = static_cast<int>(sizeof(YT)) * 8 / 16;
+    constexpr int WORDS = static_cast<int>(sizeof(YT)) * 8 / 16;
     extern __shared__ __align__(128) uint8_t few_smem[];
     __shared__ int32_t slots[kFewSlots];
     const uint32_t size = cluster_size(), rank = cluster_rank();
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_few_kernel(const __grid_con
     }
     cluster_sync();      // no CTA leaves while others read its sums
 
-    Wide16<T, TERMS> u[KS];
+    Wide16<T> u[KS];
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
         float v[8];      // rows by h, ranks 2 q (+1) and 2 q + 8 (+1): mma's registers 0, 2 and 1, 3

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid
                         v[2 * (h + 2 * x)] = f[8 * x * wf + 8 * h];
                         v[2 * (h + 2 * x) + 1] = f[(8 * x + 1) * wf + 8 * h];
                     }
-                Wide16<T, 2> wide;
+                Wide16<T> wide;
                 wide.set(v);
                 wide.mul(sum, b[k]);
             }

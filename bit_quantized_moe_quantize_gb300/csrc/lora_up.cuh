@@ -4,7 +4,7 @@
 //   backward  u = B^T dy,       W = A^T of A [R][K]         the gradient of x, per slot
 //
 // Memory-bound on out and add.  A CTA takes 64 slots (16 where adapters have few) and a run of
-// columns; u stays in registers as a matrix operand of 16 or 24 significant bits (lora.cuh).  W and add pass through a
+// columns; u stays in registers as a matrix operand that keeps its 24 bits (lora.cuh).  W and add pass through a
 // ring of stages in shared memory, add's words at the place of the thread that wants them.  A thread's results are made
 // eight neighbours, by where W's columns are put or by an exchange between four lanes, and written as whole 16-byte words.
 //
@@ -81,7 +81,6 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
     constexpr int THREADS = kLoraThreads;
     constexpr int CW = SMALL ? 128 : 64;                // columns of a stage
     constexpr int GROUPS = SMALL ? 1 : 2;               // of 32 columns, that a warp has of a stage
-    constexpr int TERMS = FP32 ? 3 : 2;      // 2^-17 of u's product is far below a 16-bit result's rounding
     constexpr int WORDS = static_cast<int>(sizeof(YT)) * 8 / 16, ADDS = GROUPS * 2 * WORDS;      // 16-byte words of eight results; of a stage's
     extern __shared__ __align__(16) uint8_t up_smem[];
     __shared__ int32_t slots[MT > kUpFill ? MT : kUpFill];
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
         }
         wait_for_prior_grid();
         let_next_grid_start();      // behind the wait: what comes up early may read the first products
-        Wide16<T, TERMS> u[KS];
+        Wide16<T> u[KS];
         const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.0f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {

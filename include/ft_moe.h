@@ -786,9 +786,9 @@ FT_API int ft_moe_combine_backward(const void* grad_y, int32_t y_dtype, const vo
  * one for each request of a batch, or one for each expert beside a routed product.  Slot s = t * top_k + j
  * takes the adapter e = ids[s], a matrix A of rank rows and a matrix B of rank columns:
  *   out[s] = add[s] + scales[e] * B[e] (A[e] x)        x: row t, or row s with x_per_slot
- * and out[s] = add[s] for ids[s] = -1.  Products are summed in fp32; A x keeps its 24 bits where out is
- * fp32, and 16 where out's own rounding is larger; out is rounded once.  Sums that reach an infinity, or
- * take one in, come out infinite or NaN; they stay in their slot's row.
+ * and out[s] = add[s] for ids[s] = -1.  Products are summed in fp32, A x keeps its 24 bits on its way into the
+ * second product, and out is rounded once.  Sums that reach an infinity, or take one in, come out infinite or
+ * NaN; they stay in their slot's row.
  *
  *   x       device, [tokens][ncols], or [tokens * top_k][ncols], of dtype (FT_DTYPE_F16 or FT_DTYPE_BF16)
  *   a       device, [n_adapters][rank][ncols] of dtype; b  [n_adapters][nrows][rank] of dtype.  Adapters of a

@@ -126,8 +126,8 @@ def chain(n):
 
 
 def split_error(dtype, out_dtype):
-    """What the narrow side loses as a matrix operand: it has 24 bits, or two bf16 parts beside 16-bit results (each
-    rounded to 8 bits: 2^-18), or two tf32 parts (2^-24) beside fp16."""
+    """What the narrow side may lose as a matrix operand: three bf16 parts hold 24 bits, two tf32 parts (beside fp16) 22
+    and more.  Beside 16-bit results the bound allows what two bf16 parts lose, 2^-17; test_gpu_adapt_bits.py allows nothing."""
     return 2.0 ** -17 if dtype == torch.bfloat16 and out_dtype != torch.float32 else 2.0 ** -22
 
 
