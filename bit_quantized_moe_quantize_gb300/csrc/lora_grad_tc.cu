@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kTcAll, 1) lora_grad_tc_kernel(const __grid_co
             for (int q = 0; q < TC / 16; ++q) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(mine + static_cast<uint32_t>(window & 1) * kTcCols + q * 16, v);
-                tmem_wait_ld();
+                tmem_wait_ld_regs(v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) total[q * 16 + i] += __uint_as_float(v[i]);
             }

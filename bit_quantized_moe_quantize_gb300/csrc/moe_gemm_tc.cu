@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(FUSE ? Gemm<BN>::THREADS_FUSED : Gemm<BN>::THR
                     for (int hh = 0; hh < NH; ++hh) {
                         uint32_t d[16];
                         tmem_ld_16x256b_x4(tlane + ab * BN + 32 * hh, d);
-                        tmem_wait_ld();
+                        tmem_wait_ld_regs(d);
                         if (h == 1 && hh == NH - 1) {            // the unit's accumulator pair fully read
                             tc_fence_before();
                             __syncwarp();
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(FUSE ? Gemm<BN>::THREADS_FUSED : Gemm<BN>::THR
                     for (int hh = 0; hh < NH; ++hh) {
                         uint32_t d[16];
                         tmem_ld_16x256b_x4(tlane + ab * BN + 32 * hh, d);
-                        tmem_wait_ld();
+                        tmem_wait_ld_regs(d);
                         if (hh == NH - 1) {                      // TMEM buffer ab fully read
                             tc_fence_before();
                             __syncwarp();
