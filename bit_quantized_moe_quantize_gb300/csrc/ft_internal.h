@@ -283,7 +283,7 @@ struct LoraPlan {
     int64_t n_tiles;         // tiles at most
     int32_t chunk;           // slots of a chunk of the matrices' gradients
     uint32_t* err;           // raised by launch_lora_down for ids that are no adapter
-    bool overlap_grad;       // launch_lora_up directly before launch_lora_grad
+    bool overlap_grad;       // launch_lora_up directly before launch_lora_grad, which takes what came before that for done (lora_grad.cuh)
     int32_t down_jobs, down_cols;      // first products that a call of this kind can have, their longest rows
 };
 int32_t lora_part_kinds(int32_t rank);      // lines of 128 bytes of a slot's parts (lora.cuh)

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(TMA ? kLoraThreads + 32 : kLoraThreads, MT == 
     __shared__ int32_t slots[MT];
     __shared__ __align__(8) uint64_t full[kDownStages];
     wait_for_prior_grid();
-    let_next_grid_start();      // behind the wait: what comes up early may read the order
+    let_next_grid_start();      // behind the wait, by every CTA: the second product comes up early and reads the order before its own wait
     const uint32_t size = cluster_size(), rank = cluster_rank();
     const DownJob<T>& job = a.job[blockIdx.y];
     const int32_t tid = static_cast<int32_t>(threadIdx.x), warp = tid >> 5, lane = tid & 31, b = static_cast<int32_t>(blockIdx.x / size);

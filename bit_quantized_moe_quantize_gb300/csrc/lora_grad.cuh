@@ -1,5 +1,8 @@
 // What the two kernels of the adapters' gradients share: their arguments, and the chunks of slots.  They may come up under the
-// tail of the second product (lora_up.cuh), whose results they do not read, and end behind it.
+// tail of the second product (lora_up.cuh), whose results they do not read, and end behind it.  What they do read, the order
+// and the first products, is made by the grids before that one, and they read it without a wait of their own: that is sound
+// because they start only once every CTA of the second product has let them or has ended, and its first CTA, as every one with a
+// tile, waits for all that came before.  A change there that takes this wait out needs one here.
 #pragma once
 
 #include "gemm_common.cuh"

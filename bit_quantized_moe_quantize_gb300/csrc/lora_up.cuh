@@ -102,7 +102,9 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
             __syncthreads();
             up_pass<YT, THREADS>(a.add, a.out, cols, slots, n_none, c0, c1);
         }
-        if (blockIdx.x == 0 && blockIdx.y == 0) wait_for_prior_grid();      // without a tile nothing else would: this grid ends behind it
+        // What starts behind this grid, early or not, takes the first products and the order for made (lora_grad.cuh).  CTAs with a tile wait
+        // for them before they let it start, others end without; where no slot has an adapter this one alone waits.
+        if (blockIdx.x == 0 && blockIdx.y == 0) wait_for_prior_grid();
         return;
     }
     const LoraTile tile = find_tile<MT>(a.slots, static_cast<int32_t>(blockIdx.x) - a.fills, slots);
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_up_kernel(const __grid_cons
             copies_commit();
         }
         wait_for_prior_grid();
-        let_next_grid_start();      // behind the wait: what comes up early may read the first products
+        let_next_grid_start();      // behind the wait: the matrices' gradients come up early and read the first products
         Wide16<T> u[KS];
         const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.0f;
 #pragma unroll
