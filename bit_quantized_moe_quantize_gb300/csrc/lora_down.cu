@@ -56,7 +56,7 @@ __host__ __device__ inline int32_t down_w_elems(int32_t rank) { return kDownCols
 
 // NT: tiles of eight ranks that there is room for.  TMA: a fifth warp has neighbouring rows brought.
 template <typename T, int MT, int NT, bool TMA>
-__global__ void __launch_bounds__(TMA ? kLoraThreads + 32 : kLoraThreads, MT == 128 && NT <= 8 ? 2 : 1) lora_down_kernel(const __grid_constant__ DownArgs<T> a) {
+__global__ void __launch_bounds__(TMA ? kLoraThreads + 32 : kLoraThreads, MT == 128 ? 2 : 1) lora_down_kernel(const __grid_constant__ DownArgs<T> a) {
     constexpr int THREADS = kLoraThreads, PARTS = MT == kLoraSmallTile ? THREADS / 32 : 1;      // PARTS: warps that share a tile's sums
     constexpr int MS = MT == 128 ? 2 : 1, WARP_ROWS = 16 * MS;                                      // a warp's runs of 16 slots
     constexpr int ZS = THREADS / 8, ZR = (MT + ZS - 1) / ZS;                                        // rows that a copy of a word per thread takes
@@ -287,8 +287,12 @@ int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStr
     auto go = [&](auto k) { return launch_with(k, "lora_down_kernel", grid, block, sm, true, cluster, s, a); };
     if (a.rank <= 16) return go(lora_down_kernel<T, MT, 2, TMA>);
     if (a.rank <= 32) return go(lora_down_kernel<T, MT, 4, TMA>);
-    if (a.rank <= 64) return go(lora_down_kernel<T, MT, 8, TMA>);
-    return go(lora_down_kernel<T, MT, 16, TMA>);
+    if constexpr (MT == 128) {      // tiles of 128 slots have a rank of 64 at most
+        return go(lora_down_kernel<T, MT, 8, TMA>);
+    } else {
+        if (a.rank <= 64) return go(lora_down_kernel<T, MT, 8, TMA>);
+        return go(lora_down_kernel<T, MT, 16, TMA>);
+    }
 }
 
 template <typename T>

@@ -26,8 +26,9 @@ namespace {
 constexpr int kGradSlots = 32, kGradStages = 3, kGradRing = 8;
 
 // MR: tiles of 16 ranks that there is room for; NJ: tiles of eight columns that a warp has.
-template <typename T, int MR, int NJ>
-__global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid_constant__ GradArgs<T> a) {
+template <int MR, int NJ>
+__global__ void __launch_bounds__(kGradThreads, 2) lora_grad_kernel(const __grid_constant__ GradArgs<__half> a) {
+    using T = __half;
     constexpr int CC = 8 * NJ * (kGradThreads / 32), ZP = CC + 8;      // columns of the CTA, their pitch
     constexpr int PAIRS = MR;      // pairs of ranks that a thread has of a stage
     extern __shared__ __align__(16) uint8_t grad_smem[];
@@ -219,10 +220,10 @@ int launch_grad_fp16(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(lora_chunks(p.n_slots, p.n_adapters, p.chunk)), static_cast<unsigned>(blocks)), block(kGradThreads);
     const size_t sm = kGradStages * kGradSlots * static_cast<size_t>(cc + 8) * 2 + 2 * static_cast<size_t>(kGradSlots * (r16 + 4) * 4);
     auto go = [&](auto k) { return launch_with(k, "lora_grad_kernel", grid, block, sm, p.overlap_grad, 1, s, a); };
-    if (p.rank <= 16) return go(lora_grad_kernel<__half, 1, 4>);
-    if (p.rank <= 32) return go(lora_grad_kernel<__half, 2, 4>);
-    if (p.rank <= 64) return go(lora_grad_kernel<__half, 4, 4>);
-    return go(lora_grad_kernel<__half, 8, 2>);
+    if (p.rank <= 16) return go(lora_grad_kernel<1, 4>);
+    if (p.rank <= 32) return go(lora_grad_kernel<2, 4>);
+    if (p.rank <= 64) return go(lora_grad_kernel<4, 4>);
+    return go(lora_grad_kernel<8, 2>);
 }
 
 }  // namespace

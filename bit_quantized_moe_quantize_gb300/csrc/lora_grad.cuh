@@ -26,8 +26,6 @@ struct GradJob {
 
 template <typename T>
 struct GradArgs {
-    CUtensorMap zmap[2];    // boxes of 64 columns of 64 rows (bf16)
-    bool tma[2];
     GradJob<T> job[2];
     LoraSlots slots;
     const float* scales;

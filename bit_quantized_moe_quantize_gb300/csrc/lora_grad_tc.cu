@@ -37,8 +37,15 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t at) {
            static_cast<uint64_t>(kTcGroup >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-__global__ void __launch_bounds__(kTcAll, 1) lora_grad_tc_kernel(const __grid_constant__ GradArgs<__nv_bfloat16> a) {
+struct TcArgs {
+    CUtensorMap zmap[2];      // boxes of 64 columns of 64 rows
+    bool tma[2];
+    GradArgs<__nv_bfloat16> grad;
+};
+
+__global__ void __launch_bounds__(kTcAll, 1) lora_grad_tc_kernel(const __grid_constant__ TcArgs t) {
     using T = __nv_bfloat16;
+    const GradArgs<T>& a = t.grad;
     extern __shared__ uint8_t tc_smem_raw[];
     uint8_t* tc_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int32_t row_ring[kTcRing][kTcSlots];      // rows of z of the stages ahead
@@ -88,7 +95,7 @@ __global__ void __launch_bounds__(kTcAll, 1) lora_grad_tc_kernel(const __grid_co
 
     // words of z: column block `lane` of slots warp, warp + 16, ..
     constexpr int WARPS = kTcThreads / 32, ZJ = kTcSlots / WARPS;
-    const bool in = col0 + lane * 8 < cols, tma = a.tma[second ? 1 : 0] && job.div == 1;
+    const bool in = col0 + lane * 8 < cols, tma = t.tma[second ? 1 : 0] && job.div == 1;
     const T* z_base = job.z + (in ? col0 + lane * 8 : 0);
     const uint32_t z_to = smem_u32(tc_smem) + static_cast<uint32_t>(lane / 8) * kTcAtom + static_cast<uint32_t>(warp) * 128 + (lane % 8 ^ warp % 8) * 16;
     // lines of the parts: every kind's run of the workspace goes to the atom of its rows
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(kTcAll, 1) lora_grad_tc_kernel(const __grid_co
             uint64_t* bar = &full[i % stages];
             const uint32_t bytes = static_cast<uint32_t>(min(left, kTcSlots)) * 128;
             if (warp == kTcAll / 32 - 1) mbar_arrive_expect_tx(bar, (run ? kTcZStage : 0u) + static_cast<uint32_t>(kinds) * bytes);
-            else if (run && warp < BOXES) tma_load_2d(tc_smem + stage + static_cast<uint32_t>(warp) * kTcAtom, &a.zmap[second ? 1 : 0], col0 + warp * 64, rows[0], bar);
+            else if (run && warp < BOXES) tma_load_2d(tc_smem + stage + static_cast<uint32_t>(warp) * kTcAtom, &t.zmap[second ? 1 : 0], col0 + warp * 64, rows[0], bar);
             else if (warp >= BOXES && warp < BOXES + kinds)
                 bulk_g2s(tc_smem + stage + my_kind_to, w_src + (static_cast<int64_t>(warp - BOXES) * a.slots.n_slots + i * kTcSlots) * 128, bytes, bar);
         }
@@ -231,7 +238,8 @@ int32_t lora_part_kinds(int32_t rank) { return part_kinds(rank); }
 
 int launch_lora_grad_tc(const LoraGrad* jobs, const LoraPlan& p, cudaStream_t s) {
     int64_t blocks;
-    GradArgs<__nv_bfloat16> a = grad_args<__nv_bfloat16>(jobs, p, kTcCols, &blocks);
+    TcArgs a{};
+    a.grad = grad_args<__nv_bfloat16>(jobs, p, kTcCols, &blocks);
     int n = 0;
     for (int i = 0; i < 2; ++i) {
         if (!jobs[i].out) continue;
