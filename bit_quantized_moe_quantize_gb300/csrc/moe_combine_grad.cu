@@ -33,6 +33,20 @@ __device__ __forceinline__ void load_some(const T* p, float (&v)[V]) {
     }
 }
 
+// A slot's sum over its warps' lanes, in a fixed order, to its weight's gradient.
+__device__ __forceinline__ void store_sum(float sum, float* part, float* grad_weights, int64_t slot, bool there, int32_t warps) {
+    const int32_t warp = static_cast<int32_t>(threadIdx.x >> 5), lane = static_cast<int32_t>(lane_id());
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (warps > 1) {
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int32_t i = 0; i < warps; ++i) sum += part[warp / warps * warps + i];
+    }
+    if (there && lane == 0 && warp % warps == 0) grad_weights[slot] = sum;
+}
+
 // V: elements of a 16-byte word of the rows, or 1.  grad_rows may be null.
 template <typename TI, typename TY, int V>
 __global__ void __launch_bounds__(kGradThreads)
@@ -80,16 +94,7 @@ __global__ void __launch_bounds__(kGradThreads)
             }
         }
     }
-    if (!grad_weights) return;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (warps > 1) {
-        if (lane == 0) part[warp] = sum;
-        __syncthreads();
-        sum = 0.0f;
-        for (int32_t i = 0; i < warps; ++i) sum += part[warp / warps * warps + i];
-    }
-    if (there && lane == 0 && warp % warps == 0) grad_weights[slot] = sum;
+    if (grad_weights) store_sum(sum, part, grad_weights, slot, there, warps);
 }
 
 // Rows that start anywhere: V elements to a 16-byte word, `rows` and `grad_rows` as far from one as each other.
@@ -134,16 +139,7 @@ __global__ void __launch_bounds__(kGradThreads)
             }
         }
     }
-    if (!grad_weights) return;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (warps > 1) {
-        if (lane == 0) part[warp] = sum;
-        __syncthreads();
-        sum = 0.0f;
-        for (int32_t i = 0; i < warps; ++i) sum += part[warp / warps * warps + i];
-    }
-    if (there && lane == 0 && warp % warps == 0) grad_weights[slot] = sum;
+    if (grad_weights) store_sum(sum, part, grad_weights, slot, there, warps);
 }
 
 template <typename TI, typename TY>
