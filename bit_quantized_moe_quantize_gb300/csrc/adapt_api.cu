@@ -65,9 +65,11 @@ int64_t lora_tiles(int64_t n_slots, int32_t n_adapters, int width) {
     return (n_slots + some * (width - 1)) / width;
 }
 
-// Chunks of the matrices' gradients, beside one more for each adapter: a CTA per SM, each with 256 columns.
-int64_t lora_most_chunks(int64_t ncols, int64_t nrows) {
-    const int64_t chunks = 152 / ((ncols + 255) / 256 + (nrows + 255) / 256);
+// Chunks of the matrices' gradients, beside one more for each adapter: a CTA per SM, each with 256 columns.  The workspace, whose
+// size is asked for without a device, has room for those of kLoraGradSms; a call makes them for the SMs that there are.
+constexpr int64_t kLoraGradSms = 152;
+int64_t lora_most_chunks(int64_t ncols, int64_t nrows, int64_t sms) {
+    const int64_t chunks = sms / ((ncols + 255) / 256 + (nrows + 255) / 256);
     return chunks > 0 ? chunks : 1;
 }
 
@@ -85,7 +87,6 @@ struct LoraWs {
     size_t u, v, u_parts, v_parts, rows, present, parts_a, parts_b, total;
     int width;
     int64_t n_tiles;
-    int32_t chunk;
 };
 
 // rows: of the gradient of x, where slots share a row of x.
@@ -103,8 +104,7 @@ LoraWs lora_ws(uint8_t* base, const LoraShape& h, bool backward, bool share) {
         const size_t lines = static_cast<size_t>(lora_part_kinds(h.rank)) * S * 128;
         L.u_parts = take_bytes(&at, lines);
         L.v_parts = take_bytes(&at, lines);
-        const int64_t most = lora_most_chunks(h.ncols, h.nrows), all = h.n_slots / kLoraLeastChunk;
-        L.chunk = lora_chunk(h.n_slots, most);
+        const int64_t most = lora_most_chunks(h.ncols, h.nrows, kLoraGradSms), all = h.n_slots / kLoraLeastChunk;
         const size_t chunks = static_cast<size_t>((all < most ? all : most) + h.n_adapters);      // rises with the slots
         L.parts_a = take_bytes(&at, chunks * R * h.ncols * 4);
         L.parts_b = take_bytes(&at, chunks * R * h.nrows * 4);
@@ -148,7 +148,10 @@ LoraPlan lora_plan(const LoraShape& h, const LoraWs& L, const int32_t* ids, cons
     p.rank = h.rank;
     p.width = L.width;
     p.n_tiles = L.n_tiles;
-    p.chunk = L.chunk;
+    if (backward) {
+        const int64_t sms = sm_count();
+        p.chunk = lora_chunk(h.n_slots, lora_most_chunks(h.ncols, h.nrows, sms < kLoraGradSms ? sms : kLoraGradSms));
+    }
     p.err = err;
     p.down_jobs = backward ? 2 : 1;
     p.down_cols = static_cast<int32_t>(backward && h.nrows > h.ncols ? h.nrows : h.ncols);
