@@ -23,8 +23,10 @@ and of what adapts a layer whose matrices stay as they are, the router and low-r
     rows = lora_add(x, a, b, ids, scales=s, add=rows)              # an adapter per expert, or per request
     loss, counts, scale = moe_balance_loss(logits, ids)            # how unevenly the experts are loaded
     d_rows, d_w = moe_combine_backward(dy, rows, w)                # gradients of moe_combine
-    dx, da, db = lora_backward(d_rows, x, a, b, ids, scales=s)     # of lora_add
+    dx, da, db = lora_backward(d_rows.to(x.dtype), x, a, b, ids, scales=s)     # of lora_add
     d_logits = moe_gate_backward(logits, ids, d_w, counts=counts, seq_scale=scale, grad_loss=g)   # of router and loss
+
+No call is an autograd function: what it returns has no graph, whether an input wants a gradient or not.
 """
 
 from ._lib import (ACT_GELU_TANH, ACT_SILU, FT_DEVERR_BAD_EXPERT_ID, FT_DEVERR_WAIT_TIMEOUT,
