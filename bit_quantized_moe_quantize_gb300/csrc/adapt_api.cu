@@ -26,9 +26,11 @@ int check_router(int64_t tokens, int32_t n_experts, int32_t top_k, int32_t dtype
 
 // ------------------------------------------------------- low-rank adapters
 // Slots per adapter on average that go by tiles of 16 slots, and from how many on by tiles of 128; else of 64.  From a
-// graph, 128 adapters of rank 8 with 8, 16, 32 slots each: 30, 30, 38 us by 16, 32, 34, 36 by 64; gradients of 64 of rank
-// 64 with 16, 32 each: 161, 181 against 167, 173.  Gradients, rank 64, 256, 512, 8192 slots each: 202, 181, 149 us by 64,
-// 218, 178, 138 by 128; rank 16 forward has the same times by either.  Above rank 64 the registers hold no 128 slots.
+// graph, 128 adapters of rank 8 with 8, 16, 32 slots each: 30, 30, 38 us by 16, 32, 33, 36 by 64; gradients of 64 of rank
+// 64 with 16, 32 each: 163, 181 against 171, 177.  Gradients, rank 64, 256, 512, 8192 slots each: 206, 188, 156 us by 64,
+// 236, 181, 144 by 128; rank 16 forward has the same times by either.  Above rank 64 the registers hold no 128 slots.
+// The mean is over all adapters of the call, as the host does not know which have slots: 8191 slots of 12 among 128 or 512 adapters
+// take 67 and 86 us where 12 alone take 58.
 constexpr int32_t kLoraSmallMean = 16;
 constexpr int64_t kLoraWideMean = 512;
 
@@ -74,8 +76,8 @@ int64_t lora_most_chunks(int64_t ncols, int64_t nrows, int64_t sms) {
 }
 
 // Slots of a chunk: whole stages of 32, and no less than 64: what is left to join grows, the chain of stages shrinks.  From a
-// graph, 509 slots of 6 adapters, rank 24, fp16: 32 us, of one adapter 30; with 256 at least 34 and 40, with 32 30 and 30; 512 of 4, rank
-// 128, bf16: 38, 40, 42.
+// graph, 509 slots of 6 adapters, rank 24, fp16: 32 us, of one adapter 32; with 256 at least 34 and 42, with 32 32 and 31; 512 of 4, rank
+// 128, bf16: 39, 40, 42.
 constexpr int64_t kLoraLeastChunk = 64;
 int32_t lora_chunk(int64_t n_slots, int64_t most) {
     const int64_t slots = (n_slots + most - 1) / most;

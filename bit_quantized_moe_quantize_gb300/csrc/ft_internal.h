@@ -320,7 +320,7 @@ struct LoraFew {       // the whole of ft_lora_add for up to kLoraFewSlots slots
     bool out_f32;
 };
 // One launch against order, first and second product, from a graph: 128 slots of 64 adapters 18 against 26 us, 256 22
-// against 26; beyond, the search for a tile's slots among all ids and A read for each 16 of them cost what it saves.
+// against 26, 512 30 against 28: the search for a tile's slots among all ids and A read for each 16 of them cost what it saves.
 constexpr int64_t kLoraFewSlots = 256;
 int launch_lora_few(const LoraFew& f, const LoraPlan& p, int dtype, cudaStream_t s);
 int launch_lora_few_bf16(const LoraFew& f, const LoraPlan& p, cudaStream_t s);

@@ -2,7 +2,7 @@
 // products of fp32 values with 16-bit ones on the tensor cores (mma.sync).
 //
 // The products here have one side of rank 8 to 128 and are bound by memory: reading a row of x of K values and
-// writing one of N takes 2 K + 4 N bytes for 2 R (K + N) operations, R to 2 R operations a byte, where
+// writing one of N takes 2 K + 2 N or 2 K + 4 N bytes for 2 R (K + N) operations, R / 2 to R operations a byte, where
 // the card has 280 for a byte.  Registers as accumulators, which the next step needs anyway, cost less
 // there than a trip through tensor memory.
 #pragma once

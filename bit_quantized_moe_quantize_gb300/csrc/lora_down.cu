@@ -276,8 +276,8 @@ int launch_down_typed(const DownArgs<T>& a, const LoraPlan& p, int jobs, cudaStr
     const size_t sums = static_cast<size_t>(MT == kLoraSmallTile ? 4 * MT : MT) * a.rank * 4;
     if (sums > sm) sm = sums;
     sm += 1024;
-    // As many CTAs as the GPU holds at once, with four stages of work or more each: a call of 8191 slots 56 us from a graph,
-    // with half the cluster 61, with twice 62; 509 slots' gradients 34, 40, 34; 8192's 138, 159, 147.  By what a call can
+    // As many CTAs as the GPU holds at once, with four stages of work or more each: a call of 8191 slots 58 us from a graph,
+    // with half the cluster 60, with twice 63; 509 slots' gradients 32, 34, 32; 8192's 144, 165, 154.  By what a call can
     // have, not what it has: leaving out one product changes no bit of the other.
     const int64_t per_sm = static_cast<int64_t>(220 * 1024 / (sm + 1024)), fit = (per_sm < 8 ? per_sm : 8) * sm_count();
     unsigned cluster = 1;

@@ -6,8 +6,9 @@
 // while A x is summed.  In the first product the four warps share a stage's values, in the second its columns;
 // lora_down.cu and lora_up.cuh have the same steps for many slots, where a launch of its own for each is no loss.
 //
-// 1 slot of 2048 x 2048, rank 16: 7.4 us (the three launches: 19 from a graph against 11); 64 slots of as many adapters,
-// 4096 x 4096: 10.5 us, 17 MB of adapters.
+// 1 slot of 2048 x 2048, rank 16: 7.8 us (the three launches: 19 from a graph against 11); 64 slots of as many adapters,
+// 4096 x 4096: 11.2 us, 17 MB of adapters at 1.5 TB/s: ids, then A and x, two meetings of the cluster, and B's first words behind A's last,
+// each a wait of its own.
 #pragma once
 
 #include "lora_up.cuh"

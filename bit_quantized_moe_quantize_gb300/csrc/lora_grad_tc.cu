@@ -15,7 +15,7 @@
 // n 2^-25 of itself.  Every 128 slots the sums move on to the other half of the tensor memory, and the first are added to
 // registers by rounding to nearest: 4096 x 4096, rank 64, 8192 slots: 2e-7 of the gradients' norm off.
 //
-// Those take 53 us: 134 MB of x and dy at 2.5 TB/s, 17 GFLOP.  A stage of an SM has 32 KB of z and 24 KB of parts to take in, and each of the
+// Those take 51 us: 134 MB of x and dy at 2.5 TB/s, 17 GFLOP.  A stage of an SM has 32 KB of z and 24 KB of parts to take in, and each of the
 // 32 blocks of columns its own copy of the parts: the SMs' intake, 32 bytes a clock, is 40 us of it.
 #include "fp8_tc.cuh"
 #include "lora_grad.cuh"

@@ -10,8 +10,12 @@
 //
 // Rows without an adapter are copied (or zeroed) by CTAs of their own.
 //
-// 8191 slots of 4096 bf16, rank 16, add: 26 us, 134 MB at 5.2 TB/s; 16384 of 1536 fp32, rank 8: 39.5 us, 201 MB at
-// 5.1; 8192 of 4096, rank 64, W turned, no add: 35 us, whose MMAs and the matrices' way to the registers bound it.
+// 8191 slots of 4096 bf16, rank 16, add: 27 us, 134 MB at 4.9 TB/s; 16384 of 1536 fp32, rank 8: 39 us, 201 MB at
+// 5.2; 8192 of 4096, rank 64, W turned, no add: 42.5 us, whose MMAs (three for a product, 47 % of the tensor cores' cycles) and
+// the matrices' way to the registers bound it.  (With two parts of u, 16 bits, the first and last took 26 and 35 us.)
+//
+// All ranks and parts of a result, 24 MMAs at rank 128, go through one accumulator, which cuts off what it adds (lora_down.cu): some
+// 24 2^-25 of the sum, too short a chain for sums that start anew.
 #pragma once
 
 #include <type_traits>
@@ -269,8 +273,8 @@ template <typename T, typename YT, int MT>
 int launch_up_typed(UpArgs<T> a, const LoraPlan& p, cudaStream_t s) {
     constexpr int CW = MT == kLoraSmallTile ? 128 : 64;
     const int64_t blocks = (a.cols + CW - 1) / CW, tiles = p.n_tiles * (p.width / MT);
-    // Runs of columns: CTAs enough to fill the GPU some times over, each of six stages or more (a call of 8191 slots from a
-    // graph: 56 us; with half as many CTAs 61, twice 58; runs of three stages 58, of twelve 61).
+    // Runs of columns: CTAs enough to fill the GPU some times over, each of six stages or more (calls of 8191 slots, bf16, and 16384,
+    // fp32, from a graph: 58 and 65 us; with half as many CTAs 60 and 69, twice 58 and 65; runs of three stages 58 and 67, of twelve 60 and 71).
     const int64_t some = p.n_slots / MT + 1;      // tiles that there are, about
     int64_t parts = 12 * static_cast<int64_t>(sm_count()) / some, most = (blocks + 5) / 6;
     if (tiles * blocks < 8 * static_cast<int64_t>(sm_count())) most = blocks;

@@ -82,7 +82,8 @@ struct RowAhead {
 };
 
 // e^x for x <= 0, off by (1.5 |x| + 4) 2^-24 of itself: the argument times log2(e) rounded, log2(e) itself, two units
-// in the power; below 2^-126 it is 0.
+// in the power; below 2^-126 it is 0.  With the quotients by __fdividef, two units more, fp32 gradients of a sigmoid router are
+// 1.3 10^-7 off (777 x 256), a plain fp32 form 1.0 10^-7.
 __device__ __forceinline__ float row_exp(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));

@@ -760,7 +760,8 @@ FT_API int ft_moe_balance_loss(const void* logits, int32_t dtype, int64_t row_st
  *   grad_weights device fp32 [tokens][top_k], or NULL: nothing arrives at the weights
  *   counts, seq_scale   what ft_moe_balance_loss gave for these rows, grad_loss device fp32 [1] the
  *                gradient that arrives at the loss; or all three NULL (seq_offsets is not read then)
- *   grad_logits  device, [tokens][n_experts] of dtype out; 0 for masked experts
+ *   grad_logits  device, [tokens][n_experts] of dtype out; 0 for masked experts, as long as what arrives is finite, and
+ *                grad_loss times seq_scale and counts too; rows of padding are 0 whatever grad_loss is
  */
 FT_API int ft_moe_gate_backward(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* topk_ids,
                                 const float* grad_weights, const int32_t* counts, const float* seq_scale,
