@@ -53,6 +53,19 @@ def test_padding_beside_a_large_gradient_of_the_loss(ft, score, dtype, E, k, gra
         inside(got, *A.gate_grad(x, ids, w, score, True, 1.0, (counts, scale, gl, off)))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("grad", [math.inf, math.nan])
+def test_padding_beside_a_gradient_that_is_no_number(ft, score, grad):
+    _, x = rows(24, 70)
+    x[::3] = -math.inf
+    ids = torch.tensor([[0, 5]], dtype=torch.int32, device="cuda").repeat(70, 1)
+    ids[::3] = -1
+    _, counts, scale = ft.moe_balance_loss(x, ids, score=score)
+    got = ft.moe_gate_backward(x, ids, torch.ones(70, 2, device="cuda"), score=score, counts=counts, seq_scale=scale,
+                               grad_loss=torch.tensor(grad, device="cuda"))
+    assert not got[::3].any() and not torch.isfinite(got[1::3]).any()
+
+
 @pytest.mark.parametrize("grad", [1.0, 2.0 ** 30])
 def test_loss_of_scores_below_the_smallest_divisor(ft, grad):
     """Sigmoid scores e^-75: their sum is under 1e-30, which divides them, and 1e30 times the loss' gradient is out of range."""
